@@ -24,11 +24,13 @@ import torch
 
 from ._lib import (CAPACITY, ERRF_BAD_EXPERT, ERRF_BAD_SLOT, ERRF_CAPACITY, ERRF_TIMEOUT, EXPORTED, MAX_EXPERTS, MAX_TOPK,
                    PACKED, PAYLOAD_BF16, PAYLOAD_FP8_E4M3, PAYLOAD_FP8_E4M3_UE8M0, EPError, Shape, check, library_path, load)
+from ._tensors import _ptr, _stream
+from .block import BlockNorm, BlockNormGrads
 
 __all__ = ["Plan", "Layout", "Shape", "EPError", "get_layout", "dispatch", "combine", "load", "library_path",
            "PACKED", "CAPACITY", "PAYLOAD_BF16", "PAYLOAD_FP8_E4M3", "PAYLOAD_FP8_E4M3_UE8M0", "ERRF_BAD_EXPERT", "ERRF_CAPACITY",
            "ERRF_TIMEOUT", "ERRF_BAD_SLOT", "MAX_EXPERTS", "MAX_TOPK", "EXPORTED", "make_shape", "recv_rows",
-           "layout_workspace_bytes", "fused_layout_dispatch", "FUSED_MAX_N", "FUSED_MAX_T"]
+           "layout_workspace_bytes", "fused_layout_dispatch", "FUSED_MAX_N", "FUSED_MAX_T", "BlockNorm", "BlockNormGrads"]
 
 
 # Batches the library dispatches with the layout folded into one launch
@@ -59,26 +61,6 @@ def layout_workspace_bytes(shape: Shape) -> int:
     if n == ctypes.c_size_t(-1).value:
         check(1, "ep_layout_workspace_bytes")
     return int(n)
-
-
-def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "tensor",
-         numel: int | None = None) -> int | None:
-    if t is None:
-        return None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() < numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, needs {numel}")
-    return t.data_ptr() or None
-
-
-def _stream(stream: torch.cuda.Stream | None) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream or None
 
 
 @dataclass

@@ -20,6 +20,12 @@ ERRF_CAPACITY = 2
 ERRF_TIMEOUT = 4
 ERRF_BAD_SLOT = 8
 
+TYPE_BF16 = 0
+TYPE_F32 = 1
+GATE_NONE = 0
+GATE_CHANNEL = 1
+GATE_TOKEN = 2
+
 MAX_EXPERTS = 1024
 MAX_TOPK = 32
 
@@ -31,7 +37,7 @@ EP_ERR_CUDA = 3
 # Every symbol include/ep.h declares.
 EXPORTED = ("ep_recv_rows", "ep_layout_workspace_bytes", "ep_get_layout", "ep_get_layout_static",
             "ep_dispatch", "ep_layout_dispatch", "ep_combine", "ep_combine_fp8", "ep_combine_src_workspace_bytes",
-            "ep_combine_src", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
+            "ep_combine_src", "ep_block_norm", "ep_block_norm_workspace_bytes", "ep_block_norm_backward", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
 
 
 class Shape(ctypes.Structure):
@@ -42,6 +48,12 @@ class Shape(ctypes.Structure):
     def __repr__(self) -> str:
         return (f"Shape(T={self.T}, H={self.H}, E={self.E}, k={self.k}, P={self.num_partitions}, "
                 f"mode={self.mode}, capacity={self.capacity})")
+
+
+class Norm(ctypes.Structure):
+    """ep_norm_t."""
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("stream_type", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class EPError(RuntimeError):
@@ -91,6 +103,14 @@ def load() -> ctypes.CDLL:
     lib.ep_combine_src_workspace_bytes.argtypes = [sp]
     lib.ep_combine_src.restype = ctypes.c_int
     lib.ep_combine_src.argtypes = [sp, vp, vp, i32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    npt, i64, size = ctypes.POINTER(Norm), ctypes.c_int64, ctypes.c_size_t
+    lib.ep_block_norm.restype = ctypes.c_int
+    lib.ep_block_norm.argtypes = [npt, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.ep_block_norm_workspace_bytes.restype = size
+    lib.ep_block_norm_workspace_bytes.argtypes = [npt]
+    lib.ep_block_norm_backward.restype = ctypes.c_int
+    lib.ep_block_norm_backward.argtypes = [npt, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                           size, vp]
     lib.ep_status_string.restype = ctypes.c_char_p
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_str.restype = ctypes.c_char_p

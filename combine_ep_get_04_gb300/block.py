@@ -1,0 +1,115 @@
+"""The ends of a mixture-of-experts block, around dispatch and combine.
+
+    norm = BlockNorm(T, H, gate="channel", scaled=True, train=True)
+    h, n = norm.forward(h, y, w_post, w_pre, gate, res_scale)
+
+As elsewhere in this package, objects allocate their outputs and workspace
+once, and calls only launch kernels on the given (or current) stream: a
+second call overwrites what the first returned.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from ._lib import GATE_CHANNEL, GATE_NONE, GATE_TOKEN, TYPE_BF16, TYPE_F32, Norm, check, load
+from ._tensors import _ptr, _rows_ptr, _shaped_ptr, _stream
+
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+_GATES = {None: GATE_NONE, "channel": GATE_CHANNEL, "token": GATE_TOKEN}
+
+
+@dataclass
+class BlockNormGrads:
+    d_h: torch.Tensor                   # stream type [T, H]
+    d_y: torch.Tensor | None            # bf16 [T, H]
+    d_w_post: torch.Tensor | None       # f32 [H]
+    d_w_pre: torch.Tensor | None        # f32 [H]
+    d_gate: torch.Tensor | None         # f32 [H] or [T]
+    d_res_scale: torch.Tensor | None    # f32 [1]
+
+
+class BlockNorm:
+    """The norm after a block, its gate and residual scale, and the norm before
+    the next block (ep_block_norm), with gradients when train is set.
+
+    dtype: type of the residual stream (h, h_out and their gradients), bf16 or
+    f32; the block's output y and the normed n are bf16.  gate: None, "channel"
+    (f32 [H]) or "token" (f32 [T]).  post / pre: whether there is a norm after
+    / before; scaled: whether the residual is scaled by a device scalar;
+    block: False for the first norm of a network (no y).
+    """
+
+    def __init__(self, T: int, H: int, dtype: torch.dtype = torch.bfloat16, gate: str | None = None, post: bool = True,
+                 pre: bool = True, scaled: bool = False, block: bool = True, eps: float = 1e-6, train: bool = False,
+                 device: str | torch.device = "cuda"):
+        lib = load()
+        if dtype not in _TYPES:
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+        if gate not in _GATES:
+            raise ValueError(f"gate must be None, 'channel' or 'token', got {gate!r}")
+        if not block and (post or gate is not None):
+            raise ValueError("post and gate need the block's output: pass post=False and gate=None with block=False")
+        self.norm = Norm(T, H, _TYPES[dtype], _GATES[gate], eps)
+        self._ref = ctypes.byref(self.norm)
+        nbytes = lib.ep_block_norm_workspace_bytes(self._ref)
+        if nbytes == ctypes.c_size_t(-1).value:
+            check(1, "ep_block_norm_workspace_bytes")
+        self.T, self.H, self.dtype, self.gate, self.post, self.pre = T, H, dtype, gate, post, pre
+        self.scaled, self.block, self.train = scaled, block, train
+        dev = torch.device(device)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.h_out = torch.empty((T, H), dtype=dtype, device=dev)
+        self.n = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if pre else None
+        self.rstd = torch.empty((2, T), **f32) if train else None
+        self.grads = None
+        self.workspace = None
+        if train:
+            self.workspace = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
+            self.workspace_bytes = int(nbytes)
+            self.grads = BlockNormGrads(
+                d_h=torch.empty((T, H), dtype=dtype, device=dev),
+                d_y=torch.empty((T, H), dtype=torch.bfloat16, device=dev) if block else None,
+                d_w_post=torch.empty(H, **f32) if post else None, d_w_pre=torch.empty(H, **f32) if pre else None,
+                d_gate=None if gate is None else torch.empty(H if gate == "channel" else T, **f32),
+                d_res_scale=torch.empty(1, **f32) if scaled else None)
+
+    def _inputs(self, h, y, w_post, w_pre, gate, res_scale):
+        for t, wanted, name in ((y, self.block, "y"), (w_post, self.post, "w_post"), (w_pre, self.pre, "w_pre"),
+                                (gate, self.gate is not None, "gate"), (res_scale, self.scaled, "res_scale")):
+            if (t is not None) != wanted:
+                raise ValueError(f"{name} is {'missing' if wanted else 'not part of this norm'}")
+        T, H, f32 = self.T, self.H, torch.float32
+        hp, ldh = _rows_ptr(h, self.dtype, "h", T, H)
+        yp, ldy = _rows_ptr(y, torch.bfloat16, "y", T, H)
+        return (hp, ldh, yp, ldy, _shaped_ptr(w_post, f32, "w_post", (H,)),
+                _shaped_ptr(gate, f32, "gate", (H if self.gate == "channel" else T,)),
+                _shaped_ptr(res_scale, f32, "res_scale", (1,)), _shaped_ptr(w_pre, f32, "w_pre", (H,)))
+
+    def forward(self, h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                w_pre: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                res_scale: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+        """Returns (h_out, n); n is None without a norm before the next block."""
+        st = load().ep_block_norm(self._ref, *self._inputs(h, y, w_post, w_pre, gate, res_scale), _ptr(self.h_out),
+                                  _ptr(self.n), _ptr(self.rstd), _stream(stream))
+        check(st, "ep_block_norm")
+        return self.h_out, self.n
+
+    def backward(self, h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                 w_pre: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                 res_scale: torch.Tensor | None = None, d_h_out: torch.Tensor | None = None,
+                 d_n: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> BlockNormGrads:
+        """Gradients, from the inputs of the last forward() and the gradients
+        of its outputs (d_h_out may be None: zero)."""
+        if not self.train:
+            raise ValueError("this norm was made without train=True")
+        g, T, H = self.grads, self.T, self.H
+        st = load().ep_block_norm_backward(
+            self._ref, *self._inputs(h, y, w_post, w_pre, gate, res_scale), _ptr(self.rstd),
+            _shaped_ptr(d_h_out, self.dtype, "d_h_out", (T, H)), _shaped_ptr(d_n, torch.bfloat16, "d_n", (T, H)), _ptr(g.d_h),
+            _ptr(g.d_y), _ptr(g.d_w_post), _ptr(g.d_gate), _ptr(g.d_res_scale), _ptr(g.d_w_pre), _ptr(self.workspace),
+            self.workspace_bytes, _stream(stream))
+        check(st, "ep_block_norm_backward")
+        return g

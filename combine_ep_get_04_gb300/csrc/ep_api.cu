@@ -73,6 +73,38 @@ ep_status_t launched(cudaError_t e, const char* what) {
     return ok();
 }
 
+// ------------------------------------------------------------- block norm
+
+ep_status_t check_norm(const ep_norm_t* s) {
+    if (s == nullptr) return fail(EP_ERR_INVALID_ARG, "norm is NULL");
+    if (s->T < 0) return fail(EP_ERR_INVALID_ARG, "T = %d < 0", s->T);
+    if (s->H <= 0 || s->H % 8 != 0) return fail(EP_ERR_INVALID_ARG, "H = %d must be a positive multiple of 8", s->H);
+    if (s->H > EP_MAX_NORM_WIDTH) return fail(EP_ERR_UNSUPPORTED, "H = %d > %d", s->H, EP_MAX_NORM_WIDTH);
+    if (s->stream_type != EP_TYPE_BF16 && s->stream_type != EP_TYPE_F32)
+        return fail(EP_ERR_INVALID_ARG, "stream_type = %d is not a type", s->stream_type);
+    if (s->gate_kind != EP_GATE_NONE && s->gate_kind != EP_GATE_CHANNEL && s->gate_kind != EP_GATE_TOKEN)
+        return fail(EP_ERR_INVALID_ARG, "gate_kind = %d is not a gate kind", s->gate_kind);
+    if (!(s->eps > 0.f) || !(s->eps <= 1e30f)) return fail(EP_ERR_INVALID_ARG, "eps = %g must be positive and finite", (double)s->eps);
+    return ok();
+}
+
+// What both directions take in.
+ep_status_t check_norm_inputs(const ep_norm_t* s, const void* h, int64_t ld_h, const void* y, int64_t ld_y,
+                              const float* w_post, const float* gate, const float* w_pre) {
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "h is NULL");
+    if (ld_h < s->H || ld_h % 8 != 0) return fail(EP_ERR_INVALID_ARG, "ld_h = %lld must be a multiple of 8 and at least H = %d", (long long)ld_h, s->H);
+    if (y != nullptr && (ld_y < s->H || ld_y % 8 != 0))
+        return fail(EP_ERR_INVALID_ARG, "ld_y = %lld must be a multiple of 8 and at least H = %d", (long long)ld_y, s->H);
+    if (y == nullptr && (w_post != nullptr || s->gate_kind != EP_GATE_NONE))
+        return fail(EP_ERR_INVALID_ARG, "w_post and gate need y");
+    if ((gate != nullptr) != (s->gate_kind != EP_GATE_NONE))
+        return fail(EP_ERR_INVALID_ARG, "gate and gate_kind = %d do not agree", s->gate_kind);
+    if (!aligned16(h) || !aligned16(y) || !aligned16(w_post) || !aligned16(w_pre) ||
+        (s->gate_kind == EP_GATE_CHANNEL && !aligned16(gate)))
+        return fail(EP_ERR_INVALID_ARG, "h, y, w_post, w_pre and a channel gate must be 16-byte aligned");
+    return ok();
+}
+
 }  // namespace
 
 namespace ep {
@@ -362,6 +394,106 @@ ep_status_t ep_combine_src(const ep_shape_t* shape, const void* y, const void* y
     p.src_k = src_k;
     p.workspace = workspace;
     return launched(ep::launch_combine_src(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "combine_src launch");
+}
+
+ep_status_t ep_block_norm(const ep_norm_t* norm, const void* h, int64_t ld_h, const void* y, int64_t ld_y,
+                          const float* w_post, const float* gate, const float* res_scale, const float* w_pre,
+                          void* h_out, void* n, float* rstd, ep_stream_t stream) {
+    ep_status_t st = check_norm(norm);
+    if (st != EP_OK) return st;
+    if (norm->T == 0) return ok();
+    st = check_norm_inputs(norm, h, ld_h, y, ld_y, w_post, gate, w_pre);
+    if (st != EP_OK) return st;
+    if ((n != nullptr) != (w_pre != nullptr)) return fail(EP_ERR_INVALID_ARG, "n and w_pre go together");
+    if (n == nullptr && h_out == nullptr) return fail(EP_ERR_INVALID_ARG, "h_out and n are both NULL");
+    if (!aligned16(h_out) || !aligned16(n)) return fail(EP_ERR_INVALID_ARG, "h_out and n must be 16-byte aligned");
+    if (h == h_out && ld_h != norm->H) return fail(EP_ERR_INVALID_ARG, "h_out in place of h needs ld_h = H");
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+
+    ep::NormParams p{};
+    p.h = h;
+    p.y = y;
+    p.w_post = w_post;
+    p.gate = gate;
+    p.res_scale = res_scale;
+    p.w_pre = w_pre;
+    p.h_out = h_out;
+    p.n = n;
+    p.rstd = rstd;
+    p.ld_h = ld_h;
+    p.ld_y = ld_y;
+    p.T = norm->T;
+    p.H = norm->H;
+    p.f32 = norm->stream_type == EP_TYPE_F32 ? 1 : 0;
+    p.gate_kind = norm->gate_kind;
+    p.eps = norm->eps;
+    return launched(ep::launch_block_norm(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "block norm launch");
+}
+
+size_t ep_block_norm_workspace_bytes(const ep_norm_t* norm) {
+    if (check_norm(norm) != EP_OK) return (size_t)-1;
+    return ep::norm_workspace_bytes(norm->T, norm->H);
+}
+
+ep_status_t ep_block_norm_backward(const ep_norm_t* norm, const void* h, int64_t ld_h, const void* y, int64_t ld_y,
+                                   const float* w_post, const float* gate, const float* res_scale,
+                                   const float* w_pre, const float* rstd, const void* d_h_out, const void* d_n,
+                                   void* d_h, void* d_y, float* d_w_post, float* d_gate, float* d_res_scale,
+                                   float* d_w_pre, void* workspace, size_t workspace_bytes, ep_stream_t stream) {
+    ep_status_t st = check_norm(norm);
+    if (st != EP_OK) return st;
+    if (norm->T > 0) {
+        st = check_norm_inputs(norm, h, ld_h, y, ld_y, w_post, gate, w_pre);
+        if (st != EP_OK) return st;
+        if ((w_post != nullptr || w_pre != nullptr) && rstd == nullptr) return fail(EP_ERR_INVALID_ARG, "rstd is NULL");
+        if (d_h == nullptr || (d_y != nullptr) != (y != nullptr))
+            return fail(EP_ERR_INVALID_ARG, "d_h is NULL, or d_y does not go with y");
+        if ((d_n != nullptr) != (w_pre != nullptr)) return fail(EP_ERR_INVALID_ARG, "d_n and w_pre go together");
+        if (d_n == nullptr && d_h_out == nullptr) return fail(EP_ERR_INVALID_ARG, "d_h_out and d_n are both NULL");
+        if (!aligned16(d_h_out) || !aligned16(d_n) || !aligned16(d_h) || !aligned16(d_y))
+            return fail(EP_ERR_INVALID_ARG, "d_h_out, d_n, d_h and d_y must be 16-byte aligned");
+        const size_t need = ep::norm_workspace_bytes(norm->T, norm->H);
+        if (workspace == nullptr || workspace_bytes < need)
+            return fail(EP_ERR_INVALID_ARG, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+        if (!aligned16(workspace)) return fail(EP_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    }
+    if ((d_w_post != nullptr) != (w_post != nullptr) || (d_w_pre != nullptr) != (w_pre != nullptr) ||
+        (d_gate != nullptr) != (gate != nullptr) || (d_res_scale != nullptr) != (res_scale != nullptr))
+        return fail(EP_ERR_INVALID_ARG, "each of d_w_post, d_w_pre, d_gate and d_res_scale goes with its input");
+    if ((gate != nullptr) != (norm->gate_kind != EP_GATE_NONE))
+        return fail(EP_ERR_INVALID_ARG, "gate and gate_kind = %d do not agree", norm->gate_kind);
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+
+    ep::NormParams p{};
+    p.h = h;
+    p.y = y;
+    p.w_post = w_post;
+    p.gate = gate;
+    p.res_scale = res_scale;
+    p.w_pre = w_pre;
+    p.rstd = const_cast<float*>(rstd);
+    p.d_h_out = d_h_out;
+    p.d_n = d_n;
+    p.d_h = d_h;
+    p.d_y = d_y;
+    p.d_w_post = d_w_post;
+    p.d_gate = d_gate;
+    p.d_res_scale = d_res_scale;
+    p.d_w_pre = d_w_pre;
+    p.partial = static_cast<float*>(workspace);
+    p.ld_h = ld_h;
+    p.ld_y = ld_y;
+    p.T = norm->T;
+    p.H = norm->H;
+    p.f32 = norm->stream_type == EP_TYPE_F32 ? 1 : 0;
+    p.gate_kind = norm->gate_kind;
+    p.eps = norm->eps;
+    return launched(ep::launch_block_norm_backward(p, num_sms, reinterpret_cast<cudaStream_t>(stream)),
+                    "block norm backward launch");
 }
 
 }  // extern "C"

@@ -141,4 +141,36 @@ inline size_t combine_src_workspace_bytes(int64_t T, int k) { return 2 * combine
 
 cudaError_t launch_combine_src(const CombineSrcParams& p, int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------------------- block norm
+
+struct NormParams {
+    const void* h;             // stream type [T, H], rows ld_h apart
+    const void* y;             // bf16 [T, H], rows ld_y apart, or nullptr
+    const float* w_post;       // [H] or nullptr
+    const float* gate;         // [H] or [T] by gate_kind, or nullptr
+    const float* res_scale;    // [1] or nullptr
+    const float* w_pre;        // [H] or nullptr
+    void* h_out;               // stream type [T, H] or nullptr (forward)
+    void* n;                   // bf16 [T, H] or nullptr (forward)
+    float* rstd;               // [2, T]; written forward (may be nullptr), read backward
+    const void* d_h_out;       // backward from here on
+    const void* d_n;
+    void* d_h;
+    void* d_y;
+    float* d_w_post;
+    float* d_gate;
+    float* d_res_scale;
+    float* d_w_pre;
+    float* partial;            // workspace: column sums of each CTA, then its d_res_scale
+    int64_t ld_h, ld_y;
+    int T, H;
+    int f32;                   // stream type
+    int gate_kind;             // EP_GATE_*
+    float eps;
+};
+
+size_t norm_workspace_bytes(int T, int H);
+cudaError_t launch_block_norm(const NormParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream);
+
 }  // namespace ep

@@ -327,6 +327,107 @@ EP_API ep_status_t ep_combine_src(const ep_shape_t *shape, const void *y,
                        void *workspace, size_t workspace_bytes,
                        uint32_t *err_flags, ep_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The ends of a mixture-of-experts block.  No page of the design describes
+ * these; they are the calls a block needs around dispatch and combine.
+ * Conventions as above (caller-owned buffers, host checks before any launch,
+ * nothing allocated, nothing synchronised).  Exception: inputs marked `ld`
+ * have rows ld elements apart.
+ * ------------------------------------------------------------------------ */
+
+/* Element type of a stream that may be held in either precision. */
+typedef enum {
+    EP_TYPE_BF16 = 0,
+    EP_TYPE_F32 = 1
+} ep_type_t;
+
+/* What the block's gate is held for. */
+typedef enum {
+    EP_GATE_NONE = 0,         /* gate = 1                                     */
+    EP_GATE_CHANNEL = 1,      /* f32 [H]                                      */
+    EP_GATE_TOKEN = 2         /* f32 [T]                                      */
+} ep_gate_kind_t;
+
+#define EP_MAX_NORM_WIDTH 16384
+
+typedef struct {
+    int32_t T;                /* rows, >= 0                                    */
+    int32_t H;                /* channels, > 0, multiple of 8, at most
+                                 EP_MAX_NORM_WIDTH                             */
+    int32_t stream_type;      /* ep_type_t of h, h_out, d_h_out and d_h        */
+    int32_t gate_kind;        /* ep_gate_kind_t                                */
+    float eps;                /* > 0, added to the mean square of both norms   */
+} ep_norm_t;
+
+/*
+ * ep_block_norm -- the end of one block and the start of the next, one pass
+ * over the rows:
+ *   u     = y * r1 * w_post,   r1 = 1 / sqrt(mean(y^2) + eps)
+ *           (u = y without w_post)
+ *   h_out = res_scale * h + gate * u
+ *   n     = h_out * r2 * w_pre,  r2 = 1 / sqrt(mean(h_out^2) + eps)
+ * Everything is computed in fp32; h_out enters the second norm before it is
+ * rounded to the stream's type, and h_out and n are each rounded once.
+ *
+ * In:  h         stream type [T, H], rows ld_h elements apart.
+ *      y         bf16 [T, H], rows ld_y apart (the block's output, e.g. from
+ *                ep_combine); NULL: h_out = res_scale * h (the first norm of
+ *                a network), w_post and gate must then be absent.
+ *      w_post    f32 [H] or NULL;  gate  f32 by gate_kind, NULL for
+ *                EP_GATE_NONE;  res_scale  f32 [1] on the device or NULL (1).
+ *      w_pre     f32 [H], or NULL when n is not wanted.
+ * Out: h_out     stream type [T, H], or NULL when not wanted.
+ *      n         bf16 [T, H] (needs w_pre), NULL exactly when w_pre is.
+ *      rstd      f32 [2, T]: r1 then r2 of every row, for the backward pass
+ *                (entries of a norm that is absent are not written), or NULL.
+ * h and h_out may be the same buffer when ld_h = H.  16-byte alignment of h,
+ * y, w_post, w_pre, h_out, n and a channel gate; ld_h and ld_y multiples of 8
+ * and at least H.
+ */
+EP_API ep_status_t ep_block_norm(const ep_norm_t *norm, const void *h, int64_t ld_h,
+                          const void *y, int64_t ld_y, const float *w_post,
+                          const float *gate, const float *res_scale,
+                          const float *w_pre, void *h_out, void *n, float *rstd,
+                          ep_stream_t stream);
+
+/* Bytes of device workspace ep_block_norm_backward needs (column sums in
+ * progress); (size_t)-1 if the description is invalid. */
+EP_API size_t ep_block_norm_workspace_bytes(const ep_norm_t *norm);
+
+/*
+ * ep_block_norm_backward -- gradients of ep_block_norm.  With
+ * t = d_n * w_pre, hn = h_out * r2, yn = y * r1:
+ *   dH     = d_h_out + r2 * (t - hn * mean(t * hn))
+ *   d_h    = res_scale * dH              d_res_scale = sum(dH * h)
+ *   d_w_pre = sum over rows of d_n * hn
+ *   du     = gate * dH                   d_gate = dH * u summed over what the
+ *                                        gate is shared by
+ *   d_w_post = sum over rows of du * yn
+ *   d_y    = r1 * (du * w_post - yn * mean(du * w_post * yn))
+ *            (du without w_post)
+ * in fp32, h_out recomputed from h and y.  Sums over rows are taken in an
+ * order that depends on the sizes alone: a repeated call gives the same bits.
+ *
+ * In:  the inputs of ep_block_norm and the rstd it wrote; d_h_out stream type
+ *      [T, H] or NULL (zero); d_n bf16 [T, H], NULL exactly when w_pre is; at
+ *      least one of the two.
+ * Out: d_h       stream type [T, H].
+ *      d_y       bf16 [T, H], NULL exactly when y is.
+ *      d_w_post, d_w_pre  f32 [H], NULL exactly when w_post / w_pre is.
+ *      d_gate    f32 [H] or [T], NULL exactly when gate is.
+ *      d_res_scale  f32 [1], NULL exactly when res_scale is.
+ * workspace: ep_block_norm_workspace_bytes(norm) bytes, 16-byte aligned,
+ * contents on entry ignored.  T = 0 sets the sums to zero.
+ */
+EP_API ep_status_t ep_block_norm_backward(const ep_norm_t *norm, const void *h, int64_t ld_h,
+                          const void *y, int64_t ld_y, const float *w_post,
+                          const float *gate, const float *res_scale,
+                          const float *w_pre, const float *rstd,
+                          const void *d_h_out, const void *d_n, void *d_h, void *d_y,
+                          float *d_w_post, float *d_gate, float *d_res_scale,
+                          float *d_w_pre, void *workspace, size_t workspace_bytes,
+                          ep_stream_t stream);
+
 /* Static description of a status code. */
 EP_API const char *ep_status_string(ep_status_t status);
 

@@ -1,0 +1,59 @@
+"""Host-side checks of the block operators' entry points: bad calls return an
+error before any CUDA call, so this runs without a GPU."""
+import ctypes
+
+import pytest
+
+import combine_ep_get_04_gb300 as ep
+from combine_ep_get_04_gb300 import _lib
+from combine_ep_get_04_gb300 import build as epbuild
+
+FAKE = ctypes.c_void_p(0x10000)      # never dereferenced: rejected on the host
+ODD = ctypes.c_void_p(0x10002)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    epbuild.build()
+    return ep.load()
+
+
+@pytest.mark.parametrize("bad,status", [(dict(T=-1), 1), (dict(H=0), 1), (dict(H=12), 1), (dict(H=16392), 2),
+                                        (dict(stream_type=2), 1), (dict(gate_kind=3), 1), (dict(eps=0.0), 1),
+                                        (dict(eps=float("nan")), 1)])
+def test_norm_descriptions(lib, bad, status):
+    f = dict(T=4, H=64, stream_type=0, gate_kind=0, eps=1e-6)
+    f.update(bad)
+    s = _lib.Norm(**f)
+    assert lib.ep_block_norm_workspace_bytes(ctypes.byref(s)) == ctypes.c_size_t(-1).value
+    assert lib.ep_block_norm(ctypes.byref(s), FAKE, 64, FAKE, 64, FAKE, None, None, FAKE, FAKE, FAKE, None, None) == status
+    assert lib.ep_last_error()
+
+
+def test_norm_arguments(lib):
+    s = _lib.Norm(4, 64, 0, 0, 1e-6)
+    gated = _lib.Norm(4, 64, 0, 1, 1e-6)
+
+    def fwd(shape=s, h=FAKE, ld_h=64, y=FAKE, ld_y=64, w_post=FAKE, gate=None, a=None, w_pre=FAKE, h_out=ctypes.c_void_p(0x20000),
+            n=FAKE):
+        return lib.ep_block_norm(ctypes.byref(shape), h, ld_h, y, ld_y, w_post, gate, a, w_pre, h_out, n, None, None)
+
+    for bad in (dict(h=None), dict(h=ODD), dict(y=ODD), dict(w_post=ODD), dict(w_pre=ODD), dict(h_out=ODD), dict(n=ODD),
+                dict(ld_h=63), dict(ld_h=56), dict(ld_h=68), dict(ld_y=56), dict(ld_y=70), dict(y=None), dict(n=None),
+                dict(w_pre=None), dict(gate=FAKE), dict(shape=gated), dict(shape=gated, gate=ODD),
+                dict(w_pre=None, n=None, h_out=None), dict(h_out=FAKE, ld_h=72)):
+        assert fwd(**bad) == _lib.EP_ERR_INVALID_ARG, bad
+    assert lib.ep_block_norm(ctypes.byref(_lib.Norm(0, 64, 0, 0, 1e-6)), *([None, 0] * 2), *([None] * 8)) == 0
+
+    need = lib.ep_block_norm_workspace_bytes(ctypes.byref(s))
+    assert need >= 3 * 64 * 4
+
+    def bwd(shape=s, w_post=FAKE, gate=None, a=None, w_pre=FAKE, rstd=FAKE, dho=FAKE, dn=FAKE, dh=FAKE, dy=FAKE, dwq=FAKE,
+            dg=None, da=None, dwp=FAKE, ws=FAKE, nb=need):
+        return lib.ep_block_norm_backward(ctypes.byref(shape), FAKE, 64, FAKE, 64, w_post, gate, a, w_pre, rstd, dho, dn, dh, dy,
+                                          dwq, dg, da, dwp, ws, nb, None)
+
+    for bad in (dict(rstd=None), dict(dh=None), dict(dy=None), dict(dn=None), dict(dwq=None), dict(dwp=None), dict(dg=FAKE),
+                dict(da=FAKE), dict(a=FAKE), dict(ws=None), dict(nb=need - 1), dict(ws=ODD), dict(dho=ODD), dict(dn=ODD),
+                dict(dh=ODD), dict(dy=ODD), dict(shape=gated, gate=FAKE), dict(w_pre=None, dwp=None, dn=None, dho=None)):
+        assert bwd(**bad) == _lib.EP_ERR_INVALID_ARG, bad
