@@ -19,6 +19,7 @@ ERRF_BAD_EXPERT = 1
 ERRF_CAPACITY = 2
 ERRF_TIMEOUT = 4
 ERRF_BAD_SLOT = 8
+ERRF_BAD_SEQ = 16
 
 TYPE_BF16 = 0
 TYPE_F32 = 1
@@ -37,7 +38,7 @@ EP_ERR_CUDA = 3
 # Every symbol include/ep.h declares.
 EXPORTED = ("ep_recv_rows", "ep_layout_workspace_bytes", "ep_get_layout", "ep_get_layout_static",
             "ep_dispatch", "ep_layout_dispatch", "ep_combine", "ep_combine_fp8", "ep_combine_src_workspace_bytes",
-            "ep_combine_src", "ep_block_norm", "ep_block_norm_workspace_bytes", "ep_block_norm_backward", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
+            "ep_combine_src", "ep_route_workspace_bytes", "ep_route", "ep_route_backward", "ep_block_norm", "ep_block_norm_workspace_bytes", "ep_block_norm_backward", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
 
 
 class Shape(ctypes.Structure):
@@ -48,6 +49,13 @@ class Shape(ctypes.Structure):
     def __repr__(self) -> str:
         return (f"Shape(T={self.T}, H={self.H}, E={self.E}, k={self.k}, P={self.num_partitions}, "
                 f"mode={self.mode}, capacity={self.capacity})")
+
+
+class Route(ctypes.Structure):
+    """ep_route_t."""
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("full_softmax", ctypes.c_int32), ("logits_type", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("balance_coef", ctypes.c_float), ("z_coef", ctypes.c_float)]
 
 
 class Norm(ctypes.Structure):
@@ -104,6 +112,13 @@ def load() -> ctypes.CDLL:
     lib.ep_combine_src.restype = ctypes.c_int
     lib.ep_combine_src.argtypes = [sp, vp, vp, i32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
     npt, i64, size = ctypes.POINTER(Norm), ctypes.c_int64, ctypes.c_size_t
+    rp = ctypes.POINTER(Route)
+    lib.ep_route_workspace_bytes.restype = size
+    lib.ep_route_workspace_bytes.argtypes = [rp]
+    lib.ep_route.restype = ctypes.c_int
+    lib.ep_route.argtypes = [rp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp, vp]
+    lib.ep_route_backward.restype = ctypes.c_int
+    lib.ep_route_backward.argtypes = [rp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.ep_block_norm.restype = ctypes.c_int
     lib.ep_block_norm.argtypes = [npt, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.ep_block_norm_workspace_bytes.restype = size

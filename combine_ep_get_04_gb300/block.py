@@ -1,5 +1,8 @@
 """The ends of a mixture-of-experts block, around dispatch and combine.
 
+    router = Router(T, E, k, balance_coef=0.01, train=True)
+    r = router.route(logits)                       # r.topk_idx, r.topk_w for dispatch and combine
+    d_logits = router.backward(logits, d_topk_w, d_losses)
     norm = BlockNorm(T, H, gate="channel", scaled=True, train=True)
     h, n = norm.forward(h, y, w_post, w_pre, gate, res_scale)
 
@@ -14,11 +17,97 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import GATE_CHANNEL, GATE_NONE, GATE_TOKEN, TYPE_BF16, TYPE_F32, Norm, check, load
+from ._lib import GATE_CHANNEL, GATE_NONE, GATE_TOKEN, TYPE_BF16, TYPE_F32, Norm, Route, check, load
 from ._tensors import _ptr, _rows_ptr, _shaped_ptr, _stream
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
 _GATES = {None: GATE_NONE, "channel": GATE_CHANNEL, "token": GATE_TOKEN}
+
+
+@dataclass
+class Routing:
+    topk_idx: torch.Tensor              # i32 [T, k]
+    topk_w: torch.Tensor                # f32 [T, k]
+    lse: torch.Tensor | None            # f32 [T]; with train=True, as the rest
+    counts: torch.Tensor | None         # i32 [num_seqs, E]
+    prob_sums: torch.Tensor | None      # f32 [num_seqs, E]
+    seq_tokens: torch.Tensor | None     # i32 [num_seqs + 2]
+    losses: torch.Tensor | None         # f32 [2]: balance, z
+    err_flags: torch.Tensor             # u32 word as i32 [1], OR-ed into; the caller clears it
+
+
+class Router:
+    """The choice of each token's experts from router logits (ep_route): top k,
+    limited to the best topk_groups of `groups` groups where given, weighted by
+    the softmax over the chosen logits (or, with full_softmax, over all).  With
+    train=True also per-expert counts, the balance and z losses and backward().
+
+    dtype: type of the logits and their gradient, f32 or bf16.  num_seqs: the
+    balance loss is taken over each of so many sequences (seq_offsets) and
+    averaged.
+    """
+
+    def __init__(self, T: int, E: int, k: int, groups: int = 1, topk_groups: int = 1, full_softmax: bool = False,
+                 dtype: torch.dtype = torch.float32, num_seqs: int = 1, balance_coef: float = 0.0, z_coef: float = 0.0,
+                 train: bool = False, device: str | torch.device = "cuda"):
+        lib = load()
+        if dtype not in _TYPES:
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+        self.desc = Route(T, E, k, groups, topk_groups, int(full_softmax), _TYPES[dtype], num_seqs, balance_coef, z_coef)
+        self._ref = ctypes.byref(self.desc)
+        nbytes = lib.ep_route_workspace_bytes(self._ref)
+        if nbytes == ctypes.c_size_t(-1).value:
+            check(1, "ep_route_workspace_bytes")
+        self.T, self.E, self.k, self.dtype, self.num_seqs, self.train = T, E, k, dtype, num_seqs, train
+        dev = torch.device(device)
+        i32, f32 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.float32, device=dev)
+        self.out = Routing(
+            topk_idx=torch.empty((T, k), **i32), topk_w=torch.empty((T, k), **f32),
+            lse=torch.empty(T, **f32) if train else None, counts=torch.empty((num_seqs, E), **i32) if train else None,
+            prob_sums=torch.empty((num_seqs, E), **f32) if train else None,
+            seq_tokens=torch.empty(num_seqs + 2, **i32) if train else None,
+            losses=torch.empty(2, **f32) if train else None, err_flags=torch.zeros(1, **i32))
+        self.workspace_bytes = int(nbytes) if train else 0
+        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev) if train else None
+        self.d_logits = torch.empty((T, E), dtype=dtype, device=dev) if train else None
+
+    def _seqs(self, seq_offsets):
+        if seq_offsets is None and self.train and self.num_seqs != 1:
+            raise ValueError(f"{self.num_seqs} sequences need seq_offsets")
+        return _shaped_ptr(seq_offsets, torch.int32, "seq_offsets", (self.num_seqs + 1,))
+
+    def route(self, logits: torch.Tensor, select_bias: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
+              seq_offsets: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> Routing:
+        """logits [T, E]; select_bias f32 [E] shifts the choice alone;
+        token_mask u8 or bool [T] leaves tokens out; seq_offsets i32
+        [num_seqs + 1]."""
+        o = self.out
+        lp, ld = _rows_ptr(logits, self.dtype, "logits", self.T, self.E)
+        if token_mask is not None and token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        st = load().ep_route(
+            self._ref, lp, ld, _shaped_ptr(select_bias, torch.float32, "select_bias", (self.E,)),
+            _shaped_ptr(token_mask, torch.uint8, "token_mask", (self.T,)), self._seqs(seq_offsets), _ptr(o.topk_idx),
+            _ptr(o.topk_w), _ptr(o.lse), _ptr(o.counts), _ptr(o.prob_sums), _ptr(o.seq_tokens), _ptr(o.losses),
+            _ptr(self.workspace), self.workspace_bytes, _ptr(o.err_flags), _stream(stream))
+        check(st, "ep_route")
+        return o
+
+    def backward(self, logits: torch.Tensor, d_topk_w: torch.Tensor | None, d_losses: torch.Tensor | None,
+                 seq_offsets: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+        """d_logits, from the logits and outputs of the last route() and the
+        gradients of topk_w f32 [T, k] and of the losses f32 [2] (each None for
+        zero)."""
+        if not self.train:
+            raise ValueError("this router was made without train=True")
+        o = self.out
+        lp, ld = _rows_ptr(logits, self.dtype, "logits", self.T, self.E)
+        st = load().ep_route_backward(
+            self._ref, lp, ld, self._seqs(seq_offsets), _ptr(o.topk_idx), _ptr(o.topk_w), _ptr(o.lse), _ptr(o.counts),
+            _ptr(o.seq_tokens), _shaped_ptr(d_topk_w, torch.float32, "d_topk_w", (self.T, self.k)),
+            _shaped_ptr(d_losses, torch.float32, "d_losses", (2,)), _ptr(self.d_logits), _stream(stream))
+        check(st, "ep_route_backward")
+        return self.d_logits
 
 
 @dataclass

@@ -62,12 +62,6 @@ __device__ __forceinline__ void store_stream(void* base, int64_t at, const Vec8&
 __device__ __forceinline__ Vec8 zeros() { return Vec8{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}}; }
 __device__ __forceinline__ Vec8 ones() { return Vec8{{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}}; }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
-}
-
 // Sum over the `warps` warps of one row.  `red` holds one float for each warp
 // of the CTA; every thread of the CTA takes part.  One barrier: a caller that
 // sums twice uses two arrays in turn.

@@ -73,6 +73,55 @@ ep_status_t launched(cudaError_t e, const char* what) {
     return ok();
 }
 
+// ------------------------------------------------------------------ route
+
+ep_status_t check_route(const ep_route_t* r) {
+    if (r == nullptr) return fail(EP_ERR_INVALID_ARG, "route is NULL");
+    if (r->T < 0) return fail(EP_ERR_INVALID_ARG, "T = %d < 0", r->T);
+    if (r->E < 1) return fail(EP_ERR_INVALID_ARG, "E = %d < 1", r->E);
+    if (r->E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, "E = %d > %d", r->E, EP_MAX_EXPERTS);
+    if (r->k < 1 || r->k > r->E) return fail(EP_ERR_INVALID_ARG, "k = %d must be in [1, E = %d]", r->k, r->E);
+    if (r->k > EP_MAX_TOPK) return fail(EP_ERR_UNSUPPORTED, "k = %d > %d", r->k, EP_MAX_TOPK);
+    if (r->groups < 1 || r->E % r->groups != 0)
+        return fail(EP_ERR_INVALID_ARG, "groups = %d must divide E = %d", r->groups, r->E);
+    if (r->groups > EP_MAX_ROUTE_GROUPS)
+        return fail(EP_ERR_UNSUPPORTED, "groups = %d > %d", r->groups, EP_MAX_ROUTE_GROUPS);
+    if (r->topk_groups < 1 || r->topk_groups > r->groups)
+        return fail(EP_ERR_INVALID_ARG, "topk_groups = %d must be in [1, groups = %d]", r->topk_groups, r->groups);
+    if (r->full_softmax != 0 && r->full_softmax != 1)
+        return fail(EP_ERR_INVALID_ARG, "full_softmax = %d must be 0 or 1", r->full_softmax);
+    if (r->logits_type != EP_TYPE_BF16 && r->logits_type != EP_TYPE_F32)
+        return fail(EP_ERR_INVALID_ARG, "logits_type = %d is not a type", r->logits_type);
+    if (r->num_seqs < 1) return fail(EP_ERR_INVALID_ARG, "num_seqs = %d < 1", r->num_seqs);
+    if (r->num_seqs > 65535) return fail(EP_ERR_UNSUPPORTED, "num_seqs = %d > 65535", r->num_seqs);
+    if ((int64_t)r->T * r->k > INT32_MAX)
+        return fail(EP_ERR_UNSUPPORTED, "T*k = %lld exceeds 2^31-1", (long long)r->T * r->k);
+    return ok();
+}
+
+ep::RouteParams route_params(const ep_route_t* r) {
+    ep::RouteParams p{};
+    p.T = r->T;
+    p.E = r->E;
+    p.k = r->k;
+    p.groups = r->groups;
+    p.topk_groups = r->topk_groups;
+    p.full_softmax = r->full_softmax;
+    p.f32 = r->logits_type == EP_TYPE_F32 ? 1 : 0;
+    p.S = r->num_seqs;
+    p.balance_coef = r->balance_coef;
+    p.z_coef = r->z_coef;
+    return p;
+}
+
+ep_status_t check_logits(const ep_route_t* r, const void* logits, int64_t ld) {
+    const uintptr_t mask = r->logits_type == EP_TYPE_F32 ? 3u : 1u;
+    if (logits == nullptr) return fail(EP_ERR_INVALID_ARG, "logits is NULL");
+    if (reinterpret_cast<uintptr_t>(logits) & mask) return fail(EP_ERR_INVALID_ARG, "logits is not aligned to its elements");
+    if (ld < r->E) return fail(EP_ERR_INVALID_ARG, "ld = %lld < E = %d", (long long)ld, r->E);
+    return ok();
+}
+
 // ------------------------------------------------------------- block norm
 
 ep_status_t check_norm(const ep_norm_t* s) {
@@ -394,6 +443,93 @@ ep_status_t ep_combine_src(const ep_shape_t* shape, const void* y, const void* y
     p.src_k = src_k;
     p.workspace = workspace;
     return launched(ep::launch_combine_src(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "combine_src launch");
+}
+
+size_t ep_route_workspace_bytes(const ep_route_t* route) {
+    if (check_route(route) != EP_OK) return (size_t)-1;
+    ep::RouteParams p = route_params(route);
+    return ep::route_workspace(&p, nullptr);
+}
+
+ep_status_t ep_route(const ep_route_t* route, const void* logits, int64_t ld, const float* select_bias,
+                     const uint8_t* token_mask, const int32_t* seq_offsets, int32_t* topk_idx, float* topk_w,
+                     float* lse, int32_t* counts, float* prob_sums, int32_t* seq_tokens, float* losses,
+                     void* workspace, size_t workspace_bytes, uint32_t* err_flags, ep_stream_t stream) {
+    ep_status_t st = check_route(route);
+    if (st != EP_OK) return st;
+    const bool sums = losses != nullptr;
+    if (route->T > 0) {
+        st = check_logits(route, logits, ld);
+        if (st != EP_OK) return st;
+        if (topk_idx == nullptr || topk_w == nullptr) return fail(EP_ERR_INVALID_ARG, "topk_idx / topk_w is NULL");
+    } else if (!sums) {
+        return ok();
+    }
+    if ((counts != nullptr) != sums || (prob_sums != nullptr) != sums || (seq_tokens != nullptr) != sums)
+        return fail(EP_ERR_INVALID_ARG, "counts, prob_sums, seq_tokens and losses go together");
+    ep::RouteParams p = route_params(route);
+    if (sums) {
+        if (lse == nullptr && route->T > 0) return fail(EP_ERR_INVALID_ARG, "the losses need lse");
+        if (seq_offsets == nullptr && route->num_seqs != 1)
+            return fail(EP_ERR_INVALID_ARG, "num_seqs = %d needs seq_offsets", route->num_seqs);
+        const size_t need = ep::route_workspace(&p, nullptr);
+        if (workspace == nullptr || workspace_bytes < need)
+            return fail(EP_ERR_INVALID_ARG, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+        if (!aligned16(workspace)) return fail(EP_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+        ep::route_workspace(&p, workspace);
+    }
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    p.logits = logits;
+    p.ld = ld;
+    p.select_bias = select_bias;
+    p.token_mask = token_mask;
+    p.seq_offsets = seq_offsets;
+    p.topk_idx = topk_idx;
+    p.topk_w = topk_w;
+    p.lse = lse;
+    p.counts = counts;
+    p.prob_sums = prob_sums;
+    p.seq_tokens = seq_tokens;
+    p.losses = losses;
+    p.err_flags = err_flags;
+    return launched(ep::launch_route(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "route launch");
+}
+
+ep_status_t ep_route_backward(const ep_route_t* route, const void* logits, int64_t ld, const int32_t* seq_offsets,
+                              const int32_t* topk_idx, const float* topk_w, const float* lse, const int32_t* counts,
+                              const int32_t* seq_tokens, const float* d_topk_w, const float* d_losses,
+                              void* d_logits, ep_stream_t stream) {
+    ep_status_t st = check_route(route);
+    if (st != EP_OK) return st;
+    if (route->T == 0) return ok();
+    st = check_logits(route, logits, ld);
+    if (st != EP_OK) return st;
+    if (topk_idx == nullptr || topk_w == nullptr || lse == nullptr || counts == nullptr || seq_tokens == nullptr ||
+        d_logits == nullptr)
+        return fail(EP_ERR_INVALID_ARG, "topk_idx / topk_w / lse / counts / seq_tokens / d_logits is NULL");
+    if (reinterpret_cast<uintptr_t>(d_logits) & (route->logits_type == EP_TYPE_F32 ? 3u : 1u))
+        return fail(EP_ERR_INVALID_ARG, "d_logits is not aligned to its elements");
+    if (seq_offsets == nullptr && route->num_seqs != 1)
+        return fail(EP_ERR_INVALID_ARG, "num_seqs = %d needs seq_offsets", route->num_seqs);
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    ep::RouteParams p = route_params(route);
+    p.logits = logits;
+    p.ld = ld;
+    p.seq_offsets = seq_offsets;
+    p.topk_idx = const_cast<int32_t*>(topk_idx);
+    p.topk_w = const_cast<float*>(topk_w);
+    p.lse = const_cast<float*>(lse);
+    p.counts = const_cast<int32_t*>(counts);
+    p.seq_tokens = const_cast<int32_t*>(seq_tokens);
+    p.d_topk_w = d_topk_w;
+    p.d_losses = d_losses;
+    p.d_logits = d_logits;
+    return launched(ep::launch_route_backward(p, num_sms, reinterpret_cast<cudaStream_t>(stream)),
+                    "route backward launch");
 }
 
 ep_status_t ep_block_norm(const ep_norm_t* norm, const void* h, int64_t ld_h, const void* y, int64_t ld_y,

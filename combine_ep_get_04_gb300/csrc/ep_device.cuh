@@ -13,6 +13,7 @@ constexpr uint32_t kErrBadExpert = 1u;
 constexpr uint32_t kErrCapacity = 2u;
 constexpr uint32_t kErrTimeout = 4u;
 constexpr uint32_t kErrBadSlot = 8u;
+constexpr uint32_t kErrBadSeq = 16u;
 
 // Upper bound on any single wait inside a kernel.  A correct run waits
 // microseconds; reaching this sets kErrTimeout and the kernel returns.
@@ -139,6 +140,14 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // read or write that may touch that grid's data comes after this.
 __device__ __forceinline__ void pdl_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ----------------------------------------------------------------- warps
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
 }
 
 // ------------------------------------------------------------------- bf16

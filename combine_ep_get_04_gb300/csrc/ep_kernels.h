@@ -141,6 +141,43 @@ inline size_t combine_src_workspace_bytes(int64_t T, int k) { return 2 * combine
 
 cudaError_t launch_combine_src(const CombineSrcParams& p, int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------------------------ route
+
+struct RouteParams {
+    const void* logits;          // [T, E], rows ld apart
+    const float* select_bias;    // [E] or nullptr
+    const uint8_t* token_mask;   // [T] or nullptr
+    const int32_t* seq_offsets;  // [S + 1], or nullptr: one sequence
+    int32_t* topk_idx;           // [T, k]; written forward, read backward, as the next five
+    float* topk_w;               // [T, k]
+    float* lse;                  // [T] or nullptr
+    int32_t* counts;             // [S, E]
+    float* prob_sums;            // [S, E]
+    int32_t* seq_tokens;         // [S + 2]
+    float* losses;               // [2], or nullptr: the choice alone
+    const float* d_topk_w;       // backward
+    const float* d_losses;
+    void* d_logits;
+    // workspace, one row for each run of `chunk` tokens of one sequence
+    float* part_prob;            // [runs, E]
+    int32_t* part_count;         // [runs, E]
+    float* part_z;               // [runs]
+    int32_t* part_live;          // [runs]
+    float* part_loss;            // [S, expert blocks]
+    float* seq_z;                // [S]
+    uint32_t* ticket;
+    uint32_t* err_flags;
+    int64_t ld;
+    int T, E, k, groups, topk_groups, full_softmax, f32, S;
+    int chunk;                   // set by the launchers
+    float balance_coef, z_coef;
+};
+
+// Splits the workspace over the part_* members (base may be nullptr); returns its size.
+size_t route_workspace(RouteParams* p, void* base);
+cudaError_t launch_route(const RouteParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteParams& p, int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------------------- block norm
 
 struct NormParams {

@@ -90,8 +90,9 @@ enum {
     EP_ERRF_CAPACITY = 2u,    /* capacity mode dropped at least one copy      */
     EP_ERRF_TIMEOUT = 4u,     /* an internal bounded wait ran out; outputs of
                                  that call are incomplete                     */
-    EP_ERRF_BAD_SLOT = 8u     /* a slot_of entry >= R (or < -1); that copy was
+    EP_ERRF_BAD_SLOT = 8u,    /* a slot_of entry >= R (or < -1); that copy was
                                  skipped                                      */
+    EP_ERRF_BAD_SEQ = 16u     /* ep_route: seq_offsets does not rise from 0 to T */
 };
 
 /* Limits of this library. */
@@ -427,6 +428,95 @@ EP_API ep_status_t ep_block_norm_backward(const ep_norm_t *norm, const void *h, 
                           float *d_w_post, float *d_gate, float *d_res_scale,
                           float *d_w_pre, void *workspace, size_t workspace_bytes,
                           ep_stream_t stream);
+
+#define EP_MAX_ROUTE_GROUPS 32
+
+typedef struct {
+    int32_t T;                /* tokens, >= 0                                  */
+    int32_t E;                /* experts, 1..EP_MAX_EXPERTS                    */
+    int32_t k;                /* experts per token, 1..min(E, EP_MAX_TOPK)     */
+    int32_t groups;           /* expert groups, divides E, at most
+                                 EP_MAX_ROUTE_GROUPS; 1 = no groups            */
+    int32_t topk_groups;      /* groups a token may choose from, 1..groups     */
+    int32_t full_softmax;     /* 0: topk_w is the softmax over the chosen
+                                 logits; 1: the chosen experts' probabilities
+                                 in the softmax over all experts               */
+    int32_t logits_type;      /* ep_type_t of logits and d_logits              */
+    int32_t num_seqs;         /* sequences the batch consists of, >= 1         */
+    float balance_coef;       /* factors of the two losses                     */
+    float z_coef;
+} ep_route_t;
+
+/* Bytes of device workspace ep_route needs when it computes the losses;
+ * (size_t)-1 if the description is invalid. */
+EP_API size_t ep_route_workspace_bytes(const ep_route_t *route);
+
+/*
+ * ep_route -- choose each token's experts from the router's logits and, for
+ * training, count the copies of every expert and compute the balance loss.
+ *
+ * Choice: an expert's rank is decided by logit + select_bias (one fp32
+ * addition).  With groups > 1 only the topk_groups groups with the largest
+ * such value stay; then the k largest, in decreasing order.  Ties go to the
+ * lower index, for groups and experts.  Logits of -inf and NaN are never
+ * chosen.  A token without k experts to choose has topk_idx = -1 and topk_w =
+ * 0 in the remaining places (the masked slot of ep_get_layout).
+ * Live tokens: token_mask (u8 [T], NULL: all ones) is not 0 and some logit is
+ * above -inf.  The logits of other tokens are not used in any way; their
+ * places are -1 and 0.
+ * With p = softmax(logits) over all experts and lse its log normaliser, n_s
+ * the live tokens of sequence s, n their sum, S the sequences that have any:
+ *   losses[0] = balance_coef / S * sum_s E / (k * n_s^2)
+ *                                        * sum_e counts[s,e] * prob_sums[s,e]
+ *   losses[1] = z_coef / n * sum over live tokens of lse^2
+ * (a loss over no tokens is 0).  All sums in fp32 in an order that depends on
+ * the sizes alone; counts are exact.
+ *
+ * In:  logits       [T, E], rows ld elements apart (ld >= E).
+ *      select_bias  f32 [E] or NULL: shifts the choice, not the weights (for
+ *                   balancing without a loss).
+ *      seq_offsets  i32 [num_seqs + 1]: sequence s is the tokens
+ *                   [seq_offsets[s], seq_offsets[s+1]); must rise from 0 to T
+ *                   (else EP_ERRF_BAD_SEQ, and the outputs of that call mean
+ *                   nothing).  NULL for one sequence, or without losses.
+ * Out: topk_idx     i32 [T, k];  topk_w  f32 [T, k].
+ *      lse          f32 [T] (-inf for tokens that are not live), or NULL.
+ *      counts i32 [num_seqs, E], prob_sums f32 [num_seqs, E], seq_tokens i32
+ *      [num_seqs + 2] (live tokens of each sequence, then of all, then the
+ *      number of sequences that have any), losses f32 [2]: all four, with lse,
+ *      or all NULL (the choice alone, as for serving).
+ * workspace: ep_route_workspace_bytes(route) bytes, 16-byte aligned, when the
+ * losses are wanted; contents on entry ignored.
+ * err_flags: EP_ERRF_BAD_SEQ.
+ */
+EP_API ep_status_t ep_route(const ep_route_t *route, const void *logits, int64_t ld,
+                     const float *select_bias, const uint8_t *token_mask,
+                     const int32_t *seq_offsets, int32_t *topk_idx, float *topk_w,
+                     float *lse, int32_t *counts, float *prob_sums,
+                     int32_t *seq_tokens, float *losses, void *workspace,
+                     size_t workspace_bytes, uint32_t *err_flags, ep_stream_t stream);
+
+/*
+ * ep_route_backward -- gradient of topk_w and the losses with respect to the
+ * logits.  The choice and the counts are constants in it:
+ *   g[e]  = d_losses[0] * balance_coef * E / (S * k * n_s^2) * counts[s,e]
+ *           (+ d_topk_w of e if chosen, with full_softmax)
+ *   d_logits[e] = p[e] * (g[e] - sum_e' p[e'] g[e'])
+ *               + d_losses[1] * 2 * z_coef / n * lse * p[e]
+ *               + (softmax over the chosen) w_j * (d_topk_w_j - sum w d_topk_w)
+ *                 for the chosen expert of place j
+ * in fp32, rounded once to the logits' type.  Rows of tokens that are not
+ * live are 0.
+ *
+ * In:  logits, ld, seq_offsets and the outputs of ep_route; d_topk_w f32
+ *      [T, k] and d_losses f32 [2] on the device, each NULL for zero.
+ * Out: d_logits  [T, E], dense, of the logits' type.
+ */
+EP_API ep_status_t ep_route_backward(const ep_route_t *route, const void *logits, int64_t ld,
+                     const int32_t *seq_offsets, const int32_t *topk_idx,
+                     const float *topk_w, const float *lse, const int32_t *counts,
+                     const int32_t *seq_tokens, const float *d_topk_w,
+                     const float *d_losses, void *d_logits, ep_stream_t stream);
 
 /* Static description of a status code. */
 EP_API const char *ep_status_string(ep_status_t status);

@@ -66,3 +66,77 @@ def block_norm(h, y, w_post, w_pre, gate, res_scale, eps, d_h_out=None, d_n=None
         axis = 0 if gate.ndim == 1 else 1
         v["d_gate"], z["d_gate"] = (d * u).sum(axis), (d_size * np.abs(u)).sum(axis)
     return v, z
+
+
+def choose(logits32, select_bias32, mask, k, groups, topk_groups):
+    """topk_idx of ep_route by sorting; the rank of an expert is one fp32 sum."""
+    T, E = logits32.shape
+    pick = logits32 if select_bias32 is None else logits32 + select_bias32
+    live = (logits32 > -np.inf).any(1)
+    if mask is not None:
+        live &= mask != 0
+    pick = np.where(live[:, None] & ~np.isnan(pick), pick, -np.inf).astype(np.float64)
+    if groups > 1:
+        best = pick.reshape(T, groups, -1).max(2)
+        rank = np.argsort(np.argsort(-best, axis=1, kind="stable"), axis=1, kind="stable")
+        pick[np.repeat(rank >= topk_groups, E // groups, axis=1)] = -np.inf
+    idx = np.argsort(-pick, axis=1, kind="stable")[:, :k]
+    return np.where(np.take_along_axis(pick, idx, 1) > -np.inf, idx, -1), live
+
+
+def route(logits, idx, live, bounds, full, balance_coef, z_coef, d_topk_w=None, d_losses=(0.0, 0.0)):
+    """Values and sizes of ep_route and its gradient for the choice `idx`.
+    bounds: the sequences' ends, S + 1 of them."""
+    T, E = logits.shape
+    k, S = idx.shape[1], len(bounds) - 1
+    v, z = {}, {}
+    lv = live[:, None]
+    top = np.where(live, np.max(np.where(lv, logits, 0.0), axis=1, initial=-np.inf), 0.0)
+    ex = np.where(lv, np.exp(np.where(lv, logits, 0.0) - top[:, None]), 0.0)
+    total = np.where(live, ex.sum(1), 1.0)
+    p = ex / total[:, None]
+    lse = np.where(live, top + np.log(total), 0.0)
+    got = idx >= 0
+    at = np.where(got, idx, 0)
+    w = np.where(got, np.take_along_axis(p, at, 1), 0.0)
+    if not full:
+        s = w.sum(1, keepdims=True)
+        # from the chosen logits themselves: probabilities may underflow
+        c = np.where(got, np.take_along_axis(logits, at, 1), -np.inf)
+        c = np.exp(c - np.max(np.where(got, c, -np.inf), axis=1, keepdims=True, initial=-1e300))
+        c = np.where(got, c, 0.0)
+        s = c.sum(1, keepdims=True)
+        w = c / np.where(s > 0, s, 1.0)
+    v["topk_w"], z["topk_w"] = w, w
+    v["lse"], z["lse"] = np.where(live, lse, -np.inf), np.abs(top) + np.abs(lse) + 1
+    counts, sums, tokens = np.zeros((S, E), np.int64), np.zeros((S, E)), np.zeros(S, np.int64)
+    for i in range(S):
+        a, b = bounds[i], bounds[i + 1]
+        counts[i] = np.bincount(idx[a:b][got[a:b]], minlength=E)
+        sums[i] = p[a:b].sum(0)
+        tokens[i] = live[a:b].sum()
+    n, filled = tokens.sum(), (tokens > 0).sum()
+    v["counts"], v["seq_tokens"] = counts, np.concatenate([tokens, [n, filled]])
+    v["prob_sums"], z["prob_sums"] = sums, sums
+    share = np.where(tokens > 0, E / (k * np.maximum(tokens, 1.0) ** 2), 0.0) / max(filled, 1)
+    balance = balance_coef * (share * (counts * sums).sum(1)).sum()
+    zl = z_coef * (lse ** 2).sum() / max(n, 1)
+    v["losses"] = np.array([balance, zl])
+    z["losses"] = np.array([balance, z_coef * ((np.abs(top) + np.abs(lse) + 1) ** 2 * live).sum() / max(n, 1)])
+    dw = np.zeros((T, k)) if d_topk_w is None else np.where(got, d_topk_w, 0.0)
+    seq = np.clip(np.searchsorted(bounds[1:], np.arange(T), side="right"), 0, S - 1)
+    g = d_losses[0] * balance_coef * share[seq][:, None] * counts[seq]
+    extra = np.zeros((T, E))
+    rows = np.broadcast_to(np.arange(T)[:, None], idx.shape)
+    np.add.at(extra, (rows[got], at[got]), (dw if full else w * (dw - (w * dw).sum(1, keepdims=True)))[got])
+    size = np.zeros((T, E))
+    np.add.at(size, (rows[got], at[got]), (np.abs(dw) if full else w * (np.abs(dw) + (w * np.abs(dw)).sum(1, keepdims=True)))[got])
+    if full:
+        g, extra = g + extra, 0.0
+        g_size, size = np.abs(g) + size, 0.0
+    else:
+        g_size = np.abs(g)
+    zg = 2 * d_losses[1] * z_coef / max(n, 1)
+    v["d_logits"] = p * (g - (p * g).sum(1, keepdims=True)) + (zg * lse)[:, None] * p + extra
+    z["d_logits"] = p * (g_size + (p * g_size).sum(1, keepdims=True)) + (abs(zg) * (np.abs(top) + np.abs(lse) + 1))[:, None] * p + size
+    return v, z

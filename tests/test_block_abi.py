@@ -57,3 +57,43 @@ def test_norm_arguments(lib):
                 dict(da=FAKE), dict(a=FAKE), dict(ws=None), dict(nb=need - 1), dict(ws=ODD), dict(dho=ODD), dict(dn=ODD),
                 dict(dh=ODD), dict(dy=ODD), dict(shape=gated, gate=FAKE), dict(w_pre=None, dwp=None, dn=None, dho=None)):
         assert bwd(**bad) == _lib.EP_ERR_INVALID_ARG, bad
+
+
+@pytest.mark.parametrize("bad,status", [(dict(T=-1), 1), (dict(E=0), 1), (dict(E=1025), 2), (dict(k=0), 1), (dict(k=17), 1),
+                                        (dict(E=64, k=33), 2), (dict(groups=3), 1), (dict(E=64, groups=64), 2), (dict(groups=0), 1),
+                                        (dict(topk_groups=0), 1), (dict(topk_groups=2), 1), (dict(full_softmax=2), 1),
+                                        (dict(logits_type=2), 1), (dict(num_seqs=0), 1), (dict(num_seqs=65536), 2),
+                                        (dict(T=2 ** 30, k=8), 2)])
+def test_route_descriptions(lib, bad, status):
+    f = dict(T=4, E=16, k=4, groups=1, topk_groups=1, full_softmax=0, logits_type=1, num_seqs=1, balance_coef=0.0, z_coef=0.0)
+    f.update(bad)
+    s = _lib.Route(**f)
+    assert lib.ep_route_workspace_bytes(ctypes.byref(s)) == ctypes.c_size_t(-1).value
+    assert lib.ep_route(ctypes.byref(s), FAKE, 16, *([FAKE] * 11), 1 << 30, None, None) == status
+    assert lib.ep_last_error()
+
+
+def test_route_arguments(lib):
+    s = _lib.Route(4, 16, 4, 1, 1, 0, 1, 1, 0.0, 0.0)
+    two = _lib.Route(4, 16, 4, 1, 1, 0, 1, 2, 0.0, 0.0)
+    need = lib.ep_route_workspace_bytes(ctypes.byref(s))
+
+    def fwd(shape=s, logits=FAKE, ld=16, seq=None, idx=FAKE, w=FAKE, lse=FAKE, counts=FAKE, probs=FAKE, tokens=FAKE, losses=FAKE,
+            ws=FAKE, nb=need):
+        return lib.ep_route(ctypes.byref(shape), logits, ld, None, None, seq, idx, w, lse, counts, probs, tokens, losses, ws, nb,
+                            None, None)
+
+    for bad in (dict(logits=None), dict(logits=ODD), dict(ld=15), dict(idx=None), dict(w=None), dict(lse=None), dict(counts=None),
+                dict(probs=None), dict(tokens=None), dict(losses=None), dict(ws=None), dict(nb=need - 1), dict(ws=ODD),
+                dict(shape=two)):
+        assert fwd(**bad) == _lib.EP_ERR_INVALID_ARG, bad
+    none = _lib.Route(0, 16, 4, 1, 1, 0, 1, 1, 0.0, 0.0)
+    assert lib.ep_route(ctypes.byref(none), None, 0, *([None] * 11), 0, None, None) == 0
+
+    def bwd(shape=s, logits=FAKE, ld=16, idx=FAKE, w=FAKE, lse=FAKE, counts=FAKE, tokens=FAKE, d=FAKE):
+        return lib.ep_route_backward(ctypes.byref(shape), logits, ld, None, idx, w, lse, counts, tokens, None, None, d, None)
+
+    for bad in (dict(logits=None), dict(logits=ODD), dict(ld=15), dict(idx=None), dict(w=None), dict(lse=None), dict(counts=None),
+                dict(tokens=None), dict(d=None), dict(d=ODD), dict(shape=two)):
+        assert bwd(**bad) == _lib.EP_ERR_INVALID_ARG, bad
+    assert lib.ep_route_backward(ctypes.byref(none), None, 0, *([None] * 10)) == 0

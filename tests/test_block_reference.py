@@ -44,3 +44,39 @@ def test_block_norm_gradients(gate_kind, post, pre, block):
             assert name not in v
             continue
         np.testing.assert_allclose(v[name].reshape(x.shape), differences(loss, x), rtol=1e-6, atol=1e-7, err_msg=name)
+
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("masked", [False, True])
+def test_route_gradients(full, masked):
+    """The choice and the counts are held while the logits move."""
+    rng = np.random.default_rng(5)
+    T, E, k, bounds = 7, 6, 3, np.array([0, 3, 3, 7])
+    logits = rng.standard_normal((T, E))
+    mask = (np.arange(T) != 4) if masked else None
+    idx, live = ref.choose(logits.astype(np.float32), None, mask, k, 2, 1)
+    assert (idx[:, 2] >= 0).sum() == live.sum()
+    dw, dl = rng.standard_normal((T, k)), (1.3, 0.7)
+
+    def loss():
+        v, _ = ref.route(logits, idx, live, bounds, full, 0.5, 0.25)
+        return (v["topk_w"] * dw).sum() + (v["losses"] * dl).sum()
+
+    v, _ = ref.route(logits, idx, live, bounds, full, 0.5, 0.25, dw, dl)
+    np.testing.assert_allclose(v["d_logits"], differences(loss, logits), rtol=1e-6, atol=1e-8)
+
+
+def test_choice_by_hand():
+    logits = np.array([[1, 3, 3, 2], [0, 0, 0, 0], [-np.inf, 5, -np.inf, np.nan], [-np.inf] * 4], np.float32)
+    idx, live = ref.choose(logits, None, None, 2, 1, 1)
+    assert idx.tolist() == [[1, 2], [0, 1], [1, -1], [-1, -1]] and live.tolist() == [True, True, True, False]
+    idx, _ = ref.choose(logits, np.array([0, 0, 0, 2], np.float32), None, 2, 2, 1)
+    assert idx.tolist() == [[3, 2], [3, 2], [1, -1], [-1, -1]]
+
+
+def test_losses_by_hand():
+    """Two tokens, two experts, both choose expert 0: c = (2, 0); equal logits
+    give p = 1/2, so prob_sums = (1, 1) and the balance is E/(k n^2) * 2 = 1."""
+    idx = np.zeros((2, 1), np.int64)
+    v, _ = ref.route(np.zeros((2, 2)), idx, np.ones(2, bool), np.array([0, 2]), False, 1.0, 1.0)
+    np.testing.assert_allclose(v["losses"], [1.0, np.log(2) ** 2])
