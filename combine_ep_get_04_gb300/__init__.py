@@ -25,13 +25,13 @@ import torch
 from ._lib import (CAPACITY, ERRF_BAD_EXPERT, ERRF_BAD_SEQ, ERRF_BAD_SLOT, ERRF_CAPACITY, ERRF_TIMEOUT, EXPORTED, MAX_EXPERTS, MAX_TOPK,
                    PACKED, PAYLOAD_BF16, PAYLOAD_FP8_E4M3, PAYLOAD_FP8_E4M3_UE8M0, EPError, Shape, check, library_path, load)
 from ._tensors import _ptr, _stream
-from .block import BlockNorm, BlockNormGrads, Router, Routing
+from .block import BlockNorm, BlockNormGrads, Router, Routing, W4Weights, expert_w4
 
 __all__ = ["Plan", "Layout", "Shape", "EPError", "get_layout", "dispatch", "combine", "load", "library_path",
            "PACKED", "CAPACITY", "PAYLOAD_BF16", "PAYLOAD_FP8_E4M3", "PAYLOAD_FP8_E4M3_UE8M0", "ERRF_BAD_EXPERT", "ERRF_CAPACITY",
            "ERRF_TIMEOUT", "ERRF_BAD_SLOT", "MAX_EXPERTS", "MAX_TOPK", "EXPORTED", "make_shape", "recv_rows",
            "layout_workspace_bytes", "fused_layout_dispatch", "FUSED_MAX_N", "FUSED_MAX_T", "BlockNorm", "BlockNormGrads",
-           "Router", "Routing", "ERRF_BAD_SEQ"]
+           "Router", "Routing", "W4Weights", "expert_w4", "ERRF_BAD_SEQ"]
 
 
 # Batches the library dispatches with the layout folded into one launch

@@ -38,7 +38,8 @@ EP_ERR_CUDA = 3
 # Every symbol include/ep.h declares.
 EXPORTED = ("ep_recv_rows", "ep_layout_workspace_bytes", "ep_get_layout", "ep_get_layout_static",
             "ep_dispatch", "ep_layout_dispatch", "ep_combine", "ep_combine_fp8", "ep_combine_src_workspace_bytes",
-            "ep_combine_src", "ep_route_workspace_bytes", "ep_route", "ep_route_backward", "ep_block_norm", "ep_block_norm_workspace_bytes", "ep_block_norm_backward", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
+            "ep_combine_src", "ep_route_workspace_bytes", "ep_route", "ep_route_backward", "ep_w4_bytes", "ep_w4_pack",
+            "ep_expert_w4", "ep_block_norm", "ep_block_norm_workspace_bytes", "ep_block_norm_backward", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
 
 
 class Shape(ctypes.Structure):
@@ -56,6 +57,12 @@ class Route(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("full_softmax", ctypes.c_int32), ("logits_type", ctypes.c_int32),
                 ("num_seqs", ctypes.c_int32), ("balance_coef", ctypes.c_float), ("z_coef", ctypes.c_float)]
+
+
+class W4(ctypes.Structure):
+    """ep_w4_t."""
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("paired", ctypes.c_int32)]
 
 
 class Norm(ctypes.Structure):
@@ -119,6 +126,13 @@ def load() -> ctypes.CDLL:
     lib.ep_route.argtypes = [rp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp, vp]
     lib.ep_route_backward.restype = ctypes.c_int
     lib.ep_route_backward.argtypes = [rp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    wp = ctypes.POINTER(W4)
+    lib.ep_w4_bytes.restype = size
+    lib.ep_w4_bytes.argtypes = [wp]
+    lib.ep_w4_pack.restype = ctypes.c_int
+    lib.ep_w4_pack.argtypes = [wp, vp, vp, vp, vp]
+    lib.ep_expert_w4.restype = ctypes.c_int
+    lib.ep_expert_w4.argtypes = [wp, vp, i32, i32, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp]
     lib.ep_block_norm.restype = ctypes.c_int
     lib.ep_block_norm.argtypes = [npt, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.ep_block_norm_workspace_bytes.restype = size

@@ -3,6 +3,8 @@
     router = Router(T, E, k, balance_coef=0.01, train=True)
     r = router.route(logits)                       # r.topk_idx, r.topk_w for dispatch and combine
     d_logits = router.backward(logits, d_topk_w, d_losses)
+    w = W4Weights(codes, scales, group=128, paired=True)
+    y = expert_w4(recv, w, layout.counts, layout.offsets, x_scales=recv_scales)
     norm = BlockNorm(T, H, gate="channel", scaled=True, train=True)
     h, n = norm.forward(h, y, w_post, w_pre, gate, res_scale)
 
@@ -17,7 +19,8 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import GATE_CHANNEL, GATE_NONE, GATE_TOKEN, TYPE_BF16, TYPE_F32, Norm, Route, check, load
+from ._lib import (CAPACITY, GATE_CHANNEL, GATE_NONE, GATE_TOKEN, PACKED, PAYLOAD_BF16, PAYLOAD_FP8_E4M3,
+                   PAYLOAD_FP8_E4M3_UE8M0, TYPE_BF16, TYPE_F32, W4, Norm, Route, check, load)
 from ._tensors import _ptr, _rows_ptr, _shaped_ptr, _stream
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
@@ -108,6 +111,72 @@ class Router:
             _shaped_ptr(d_losses, torch.float32, "d_losses", (2,)), _ptr(self.d_logits), _stream(stream))
         check(st, "ep_route_backward")
         return self.d_logits
+
+
+class W4Weights:
+    """4-bit weights with group scales, laid out for expert_w4 (ep_w4_pack).
+
+    codes u8 [E, rows, K/2]: input channel 2i in the low half of byte i; code c
+    stands for (c - 8) * scale.  scales bf16 [E, rows, ceil(K / group)].
+    paired: rows are N gate rows and then N up rows of a SwiGLU.  codes and
+    scales are not needed afterwards.
+    """
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, group: int = 128, paired: bool = False,
+                 stream: torch.cuda.Stream | None = None):
+        lib = load()
+        if codes.dim() != 3:
+            raise ValueError(f"codes must be [E, rows, K/2], got {tuple(codes.shape)}")
+        E, rows, half = codes.shape
+        if paired and rows % 2:
+            raise ValueError(f"paired weights have an even number of rows, got {rows}")
+        self.E, self.N, self.K, self.group, self.paired = E, rows // 2 if paired else rows, 2 * half, group, paired
+        self.desc = W4(E, self.N, self.K, group, int(paired))
+        self._ref = ctypes.byref(self.desc)
+        nbytes = lib.ep_w4_bytes(self._ref)
+        if nbytes == ctypes.c_size_t(-1).value:
+            check(1, "ep_w4_bytes")
+        cp = _ptr(codes, torch.uint8, "codes")
+        sp = _shaped_ptr(scales, torch.bfloat16, "scales", (E, rows, -(-self.K // group)))
+        self.packed = torch.empty(int(nbytes), dtype=torch.uint8, device=codes.device)
+        check(lib.ep_w4_pack(self._ref, cp, sp, _ptr(self.packed), _stream(stream)), "ep_w4_pack")
+
+
+def expert_w4(x: torch.Tensor, weights: W4Weights, counts: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+              capacity: int | None = None, x_scales: torch.Tensor | None = None, max_rows: int | None = None,
+              out: torch.Tensor | None = None, err_flags: torch.Tensor | None = None,
+              stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Every expert's product over its rows of the receive buffer (ep_expert_w4).
+
+    x bf16 [R, K], or one-byte e4m3 with x_scales [R, K/128] (float32, or uint8
+    UE8M0 exponents), as dispatch leaves it; counts / offsets from the layout
+    (neither for a single matrix over all rows); capacity as in Plan.  max_rows:
+    rows in use at most (T * k), all of x if not given.  Returns bf16 [R, N];
+    rows without a copy are left as they were (without `out`, undefined).
+    """
+    w = weights
+    if x.dim() != 2 or x.shape[1] != w.K:
+        raise ValueError(f"x must be [R, {w.K}], got {tuple(x.shape)}")
+    R = x.shape[0]
+    if x_scales is None:
+        payload, xp, sp = PAYLOAD_BF16, _ptr(x, torch.bfloat16, "x"), None
+    else:
+        if x.element_size() != 1:
+            raise TypeError("x_scales go with one-byte e4m3 rows")
+        if x_scales.dtype not in (torch.float32, torch.uint8):
+            raise TypeError("x_scales must be float32 or uint8 (UE8M0)")
+        payload = PAYLOAD_FP8_E4M3_UE8M0 if x_scales.dtype == torch.uint8 else PAYLOAD_FP8_E4M3
+        xp, sp = _ptr(x, None, "x"), _shaped_ptr(x_scales, x_scales.dtype, "x_scales", (R, w.K // 128))
+    if counts is None and offsets is None and w.E != 1:
+        raise ValueError("several experts need the layout's counts and offsets")
+    if out is None:
+        out = torch.empty((R, w.N), dtype=torch.bfloat16, device=x.device)
+    st = load().ep_expert_w4(
+        w._ref, _ptr(w.packed), PACKED if capacity is None else CAPACITY, capacity or 0, R, R if max_rows is None else max_rows,
+        _ptr(counts, torch.int32, "counts", w.E), _ptr(offsets, torch.int32, "offsets", w.E + 1), xp, sp, payload,
+        _shaped_ptr(out, torch.bfloat16, "out", (R, w.N)), _ptr(err_flags, torch.int32, "err_flags", 1), _stream(stream))
+    check(st, "ep_expert_w4")
+    return out
 
 
 @dataclass

@@ -122,6 +122,22 @@ ep_status_t check_logits(const ep_route_t* r, const void* logits, int64_t ld) {
     return ok();
 }
 
+// -------------------------------------------------------------- expert w4
+
+ep_status_t check_w4(const ep_w4_t* w) {
+    if (w == nullptr) return fail(EP_ERR_INVALID_ARG, "w is NULL");
+    if (w->E < 1) return fail(EP_ERR_INVALID_ARG, "E = %d < 1", w->E);
+    if (w->E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, "E = %d > %d", w->E, EP_MAX_EXPERTS);
+    if (w->N <= 0 || w->N % 8 != 0) return fail(EP_ERR_INVALID_ARG, "N = %d must be a positive multiple of 8", w->N);
+    if (w->K <= 0 || w->K % 8 != 0) return fail(EP_ERR_INVALID_ARG, "K = %d must be a positive multiple of 8", w->K);
+    if (w->group != 32 && w->group != 64 && w->group != 128)
+        return fail(EP_ERR_INVALID_ARG, "group = %d must be 32, 64 or 128", w->group);
+    if (w->paired != 0 && w->paired != 1) return fail(EP_ERR_INVALID_ARG, "paired = %d must be 0 or 1", w->paired);
+    if (w->N > 1 << 24 || w->K > 1 << 24 || !ep::w4_packs({w->E, w->N, w->K, w->group, w->paired}))
+        return fail(EP_ERR_UNSUPPORTED, "weights [%d, %d, %d] are too large", w->E, w->N, w->K);
+    return ok();
+}
+
 // ------------------------------------------------------------- block norm
 
 ep_status_t check_norm(const ep_norm_t* s) {
@@ -530,6 +546,73 @@ ep_status_t ep_route_backward(const ep_route_t* route, const void* logits, int64
     p.d_logits = d_logits;
     return launched(ep::launch_route_backward(p, num_sms, reinterpret_cast<cudaStream_t>(stream)),
                     "route backward launch");
+}
+
+size_t ep_w4_bytes(const ep_w4_t* w) {
+    if (check_w4(w) != EP_OK) return (size_t)-1;
+    return ep::w4_bytes({w->E, w->N, w->K, w->group, w->paired});
+}
+
+ep_status_t ep_w4_pack(const ep_w4_t* w, const uint8_t* codes, const void* scales, void* packed, ep_stream_t stream) {
+    ep_status_t st = check_w4(w);
+    if (st != EP_OK) return st;
+    if (codes == nullptr || scales == nullptr || packed == nullptr)
+        return fail(EP_ERR_INVALID_ARG, "codes / scales / packed is NULL");
+    if ((reinterpret_cast<uintptr_t>(codes) & 3u) || (reinterpret_cast<uintptr_t>(scales) & 1u) || !aligned16(packed))
+        return fail(EP_ERR_INVALID_ARG, "codes must be 4-byte, scales 2-byte and packed 16-byte aligned");
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    return launched(ep::launch_w4_pack({w->E, w->N, w->K, w->group, w->paired}, codes, scales, packed,
+                                       reinterpret_cast<cudaStream_t>(stream)), "w4 pack launch");
+}
+
+ep_status_t ep_expert_w4(const ep_w4_t* w, const void* packed, int32_t mode, int32_t capacity, int64_t R,
+                         int64_t max_rows, const int32_t* counts, const int32_t* offsets, const void* x,
+                         const void* x_scales, int32_t payload, void* y, uint32_t* err_flags, ep_stream_t stream) {
+    ep_status_t st = check_w4(w);
+    if (st != EP_OK) return st;
+    if (payload != EP_PAYLOAD_BF16 && payload != EP_PAYLOAD_FP8_E4M3 && payload != EP_PAYLOAD_FP8_E4M3_UE8M0)
+        return fail(EP_ERR_INVALID_ARG, "payload = %d is not a payload format", payload);
+    const bool fp8 = payload != EP_PAYLOAD_BF16;
+    const bool ue8m0 = payload == EP_PAYLOAD_FP8_E4M3_UE8M0;
+    if (fp8 && w->K % 128 != 0) return fail(EP_ERR_INVALID_ARG, "fp8 rows need K %% 128 == 0 (K = %d)", w->K);
+    if (mode != EP_LAYOUT_PACKED && mode != EP_LAYOUT_CAPACITY)
+        return fail(EP_ERR_INVALID_ARG, "mode = %d is not a layout mode", mode);
+    if (R < 0 || max_rows < 0) return fail(EP_ERR_INVALID_ARG, "R and max_rows must not be negative");
+    if (R > INT32_MAX) return fail(EP_ERR_UNSUPPORTED, "R = %lld exceeds 2^31-1", (long long)R);
+    if (mode == EP_LAYOUT_CAPACITY && (capacity < 1 || R < (int64_t)w->E * capacity))
+        return fail(EP_ERR_INVALID_ARG, "capacity = %d needs at least 1 and R >= E*capacity", capacity);
+    if (max_rows > R) max_rows = R;
+    if (max_rows == 0) return ok();
+    if (mode == EP_LAYOUT_CAPACITY ? counts == nullptr : offsets == nullptr && w->E != 1)
+        return fail(EP_ERR_INVALID_ARG, "counts (capacity mode) / offsets (packed) is NULL");
+    if (packed == nullptr || x == nullptr || y == nullptr) return fail(EP_ERR_INVALID_ARG, "packed / x / y is NULL");
+    if (!aligned16(packed) || !aligned16(x) || !aligned16(y))
+        return fail(EP_ERR_INVALID_ARG, "packed, x and y must be 16-byte aligned");
+    if (fp8 && (x_scales == nullptr || (!ue8m0 && (reinterpret_cast<uintptr_t>(x_scales) & 3u))))
+        return fail(EP_ERR_INVALID_ARG, "fp8 rows need x_scales (4-byte aligned for f32 scales)");
+    ep::W4Params p{};
+    p.w = {w->E, w->N, w->K, w->group, w->paired};
+    if (!ep::w4_fits(p.w, max_rows, fp8 ? 1 : 0))
+        return fail(EP_ERR_UNSUPPORTED, "K = %d or max_rows = %lld is too large", w->K, (long long)max_rows);
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    p.packed = packed;
+    p.x = x;
+    p.x_scales = fp8 ? x_scales : nullptr;
+    p.counts = counts;
+    p.offsets = offsets;
+    p.y = y;
+    p.err_flags = err_flags;
+    p.R = R;
+    p.max_rows = max_rows;
+    p.mode = mode;
+    p.capacity = capacity;
+    p.fp8 = fp8 ? 1 : 0;
+    p.ue8m0 = ue8m0 ? 1 : 0;
+    return launched(ep::launch_expert_w4(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "expert w4 launch");
 }
 
 ep_status_t ep_block_norm(const ep_norm_t* norm, const void* h, int64_t ld_h, const void* y, int64_t ld_y,

@@ -178,6 +178,31 @@ size_t route_workspace(RouteParams* p, void* base);
 cudaError_t launch_route(const RouteParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_route_backward(const RouteParams& p, int num_sms, cudaStream_t stream);
 
+// -------------------------------------------------------------- expert w4
+
+struct W4Shape {
+    int E, N, K, group, paired;
+};
+
+struct W4Params {
+    W4Shape w;
+    const void* packed;
+    const void* x;
+    const void* x_scales;      // f32 or UE8M0 bytes (fp8)
+    const int32_t* counts;
+    const int32_t* offsets;
+    void* y;
+    uint32_t* err_flags;
+    int64_t R, max_rows;
+    int mode, capacity, fp8, ue8m0;
+};
+
+size_t w4_bytes(const W4Shape& w);
+bool w4_packs(const W4Shape& w);                                // whether one launch packs them
+bool w4_fits(const W4Shape& w, int64_t max_rows, int fp8);      // whether one launch covers the rows
+cudaError_t launch_w4_pack(const W4Shape& w, const uint8_t* codes, const void* scales, void* packed, cudaStream_t stream);
+cudaError_t launch_expert_w4(const W4Params& p, int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------------------- block norm
 
 struct NormParams {

@@ -1,0 +1,487 @@
+// expert_w4.cu -- the experts' products over the receive buffer with 4-bit
+// weights and group scales:
+//   y[r, n] = sum_k x[r, k] * (code[e, n, k] - 8) * scale[e, n, k / group]
+//
+// A decode batch gives an expert a handful of rows, so the bytes of the weights
+// decide the time.  They are laid out once so that a CTA's stream of them is
+// contiguous and every thread finds its matrix-instruction operands in one
+// 16-byte word: tiles of 16 weight rows x 128 input channels, 1024 bytes of
+// codes and then the tile's scales, eight tiles side by side for each step
+// along K.  A producer warp keeps a ring of such steps (and the matching
+// 128-channel pieces of the token rows) filled with bulk copies; eight
+// consumer warps, one tile each, widen the codes to bf16 (f16 beside fp8 rows:
+// both hold code - 8 and every e4m3 value exactly) and multiply with
+// mma.m16n8k16, the weights as the 16-row side and 8 tokens as the other.  A
+// group's products are summed unscaled and enter the fp32 accumulator through
+// one fused multiply-add with the group's scale.
+#include <algorithm>
+
+#include "ep_device.cuh"
+#include "ep_kernels.h"
+
+namespace ep {
+namespace {
+
+constexpr int kTileRows = 16;      // weight rows of one tile (the matrix instruction's)
+constexpr int kTileK = 128;        // input channels of one tile
+constexpr int kTiles = 8;          // tiles of one step, one for each consumer warp
+constexpr int kCodeBytes = kTileRows * kTileK / 2;
+constexpr int kStages = 4;
+constexpr int kThreads = (kTiles + 1) * 32;
+
+__host__ __device__ constexpr int tile_bytes(int group) { return kCodeBytes + kTileK / group * 32; }
+
+// Tiles along the output: a paired tile is 8 gate rows and the 8 up rows of
+// the same channels, so that one thread ends up with both products.
+__host__ __device__ inline int row_tiles(const W4Shape& w) { return w.paired ? (w.N + 7) / 8 : (w.N + 15) / 16; }
+__host__ __device__ inline int row_blocks(const W4Shape& w) { return (row_tiles(w) + kTiles - 1) / kTiles; }
+__host__ __device__ inline int k_blocks(const W4Shape& w) { return (w.K + kTileK - 1) / kTileK; }
+
+// Bytes between the 128-channel pieces of two token rows in a stage: 64 (32
+// for fp8) more than a piece, so that the eight rows a warp reads at once
+// fall into different banks.
+__host__ __device__ constexpr int x_pitch(bool fp8) { return fp8 ? 160 : 320; }
+
+// One word of codes: 8 input channels of one weight row, channel 2j in bits
+// 4j and channel 2j + 1 in bits 16 + 4j, so that a shift by 4j and a mask
+// leave a pair of neighbours in the two halves of a register.
+__global__ void __launch_bounds__(256) w4_pack_kernel(W4Shape w, const uint8_t* codes, const uint16_t* scales, unsigned char* packed) {
+    const int64_t tile = blockIdx.x;           // [E][row block][k block][kTiles]
+    const int nk = k_blocks(w), nb = row_blocks(w);
+    const int rt = (int)(tile % kTiles), kb = (int)(tile / kTiles % nk);
+    const int64_t blk = tile / kTiles / nk;
+    const int rb = (int)(blk % nb), e = (int)(blk / nb);
+    const int groups = (w.K + w.group - 1) / w.group, rows = w.paired ? 2 * w.N : w.N;
+    unsigned char* out = packed + tile * tile_bytes(w.group);
+    auto source_row = [&](int r) {             // weight row of row r of the tile; -1: padding
+        const int at = rb * kTiles + rt;
+        const int row = w.paired ? at * 8 + (r & 7) : at * 16 + r;
+        return row >= w.N ? -1 : w.paired && r >= 8 ? w.N + row : row;
+    };
+    {
+        const int half = threadIdx.x >> 7, lane = threadIdx.x >> 2 & 31, i = threadIdx.x & 3;
+        const int row = source_row(half * 8 + (lane >> 2)), k = kb * kTileK + 32 * i + 8 * (lane & 3);
+        uint32_t word = 0x88888888u;           // code 8: zero
+        if (row >= 0 && k < w.K) {
+            const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + (((int64_t)e * rows + row) * w.K + k) / 2);
+            word = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) word |= (c >> (8 * j) & 0xfu) << (4 * j) | (c >> (8 * j + 4) & 0xfu) << (16 + 4 * j);
+        }
+        *reinterpret_cast<uint32_t*>(out + half * 512 + lane * 16 + i * 4) = word;
+    }
+    const int per = kTileK / w.group;
+    if (threadIdx.x < 16 * per) {
+        const int r = threadIdx.x & 15, g = threadIdx.x >> 4;
+        const int row = source_row(r), at = kb * per + g;
+        const uint16_t s = row >= 0 && at < groups ? scales[((int64_t)e * rows + row) * groups + at] : (uint16_t)0;
+        *reinterpret_cast<uint16_t*>(out + kCodeBytes + g * 32 + (r & 7) * 4 + (r >> 3) * 2) = s;
+    }
+}
+
+// D += A B for one 16 x 8 x 16 step, fp32 accumulators.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Pair j of a word of codes as code - 8 in two halves: the code under an
+// exponent whose last place is 1 (bf16: 128 + c, f16: 1024 + c), less that
+// offset and 8.  Both steps are exact.
+template <bool F16>
+__device__ __forceinline__ uint32_t widen(uint32_t word, int j) {
+    const uint32_t m = (word >> (4 * j) & 0x000f000fu) | (F16 ? 0x64006400u : 0x43004300u);
+    uint32_t r;
+    if (F16)
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x64086408u));
+    else
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x43084308u));
+    return r;
+}
+
+// Two e4m3 codes -> f16x2, exact.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    return r;
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held two to a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ float silu(float x) { return x / (1.f + __expf(-x)); }
+
+struct RowTile {
+    int e;          // expert, -1: none
+    int rows;       // rows of the tile
+    int64_t first;  // its first row
+};
+
+// Rows of expert e that lie inside the buffer.
+__device__ __forceinline__ int expert_rows(const W4Params& p, int e, int64_t* first) {
+    int64_t a, n;
+    if (p.mode != 0) {
+        a = (int64_t)e * p.capacity;
+        n = min(p.counts[e], p.capacity);
+    } else if (p.offsets != nullptr) {
+        a = p.offsets[e];
+        n = p.offsets[e + 1] - a;
+    } else {
+        a = 0;
+        n = p.R;
+    }
+    const bool bad = n > 0 && (a < 0 || a + n > p.R);
+    if (bad && p.err_flags != nullptr) atomicOr(p.err_flags, kErrBadSlot);
+    *first = a;
+    return bad || n < 0 ? 0 : (int)n;
+}
+
+// Tile `at` in the order of experts and of rows within an expert.  One warp;
+// lane l counts the tiles of experts [l * per, (l + 1) * per).
+__device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_tiles) {
+    const int lane = threadIdx.x & 31;
+    const int per = (p.w.E + 31) / 32;
+    const int e0 = min(lane * per, p.w.E), e1 = min(e0 + per, p.w.E);
+    int64_t first = 0;
+    int64_t mine = 0;          // 64 bits: bad offsets may claim every row many times
+    for (int e = e0; e < e1; ++e) mine += (expert_rows(p, e, &first) + tile_rows - 1) / tile_rows;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    if (at == 0 && total > grid_tiles && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrCapacity);
+    RowTile r{-1, 0, 0};
+    if (at >= total) return r;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
+    if (lane == owner) {
+        int64_t left = at - (upto - mine);
+        for (int e = e0; e < e1; ++e) {
+            const int n = expert_rows(p, e, &first), tiles = (n + tile_rows - 1) / tile_rows;
+            if (left < tiles) {
+                r = RowTile{e, (int)min(n - left * tile_rows, (int64_t)tile_rows), first + left * tile_rows};
+                break;
+            }
+            left -= tiles;
+        }
+    }
+    r.e = __shfl_sync(0xffffffffu, r.e, owner);
+    r.rows = __shfl_sync(0xffffffffu, r.rows, owner);
+    r.first = __shfl_sync(0xffffffffu, r.first, owner);
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Reads a float of the same place in another CTA's shared memory.
+__device__ __forceinline__ float4 cluster_load(const float4* p, uint32_t rank) {
+    uint32_t a;
+    float4 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// One CTA: one row block (128 weight rows) x one tile of up to 8 NT token rows
+// x one of `splits` shares of K.  The shares of a product form a cluster and
+// add their accumulators through distributed shared memory in the order of
+// the shares.
+template <int NT, int G, bool FP8>
+__global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int splits, int grid_tiles) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ RowTile shared_tile;
+    constexpr int kWeights = kTiles * tile_bytes(G);
+    constexpr int kRows = 8 * NT;
+    constexpr int kPitch = x_pitch(FP8);
+    constexpr int kStage = kWeights + kRows * kPitch;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % splits;
+    const int blocks = row_blocks(p.w), nk = k_blocks(p.w);
+    const int rb = blockIdx.x / splits % blocks, at = blockIdx.x / splits / blocks;
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kTiles);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    if (warp == 0) {
+        const RowTile r = find_tile(p, at, kRows, grid_tiles);
+        if (lane == 0) shared_tile = r;
+    }
+    __syncthreads();
+    const RowTile tile = shared_tile;
+    if (tile.e < 0) return;              // the same in all CTAs of a cluster
+    const int kb0 = (int)((int64_t)nk * split / splits), kb1 = (int)((int64_t)nk * (split + 1) / splits);
+    const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + (((int64_t)tile.e * blocks + rb) * nk) * kWeights;
+    float* xs = reinterpret_cast<float*>(smem + kStages * kStage);          // [k block][kRows] (fp8)
+    float4* parts = reinterpret_cast<float4*>(smem + kStages * kStage + (FP8 ? (int64_t)nk * kRows * 4 : 0));   // [kTiles][NT][32]
+    if (FP8) {
+        for (int i = threadIdx.x; i < (kb1 - kb0) * kRows; i += kThreads) {
+            const int kb = kb0 + i / kRows, r = i % kRows;
+            float s = 0.f;
+            if (r < tile.rows) {
+                const int64_t from = (tile.first + r) * nk + kb;
+                s = p.ue8m0 ? __uint_as_float((uint32_t) static_cast<const uint8_t*>(p.x_scales)[from] << 23)
+                            : static_cast<const float*>(p.x_scales)[from];
+                if (p.ue8m0 && static_cast<const uint8_t*>(p.x_scales)[from] == 0) s = __uint_as_float(0x00400000u);   // 2^-127
+            }
+            xs[i] = s;
+        }
+        __syncthreads();
+    }
+    bool good = true;
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
+    if (warp == kTiles) {
+        // producer
+        const int size = FP8 ? 1 : 2;
+        const unsigned char* x = static_cast<const unsigned char*>(p.x) + tile.first * p.w.K * size;
+        int filled = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++filled) {
+            const int s = filled % kStages, round = filled / kStages;
+            if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (round - 1) & 1))) {
+                good = false;
+                break;
+            }
+            unsigned char* st = smem + s * kStage;
+            const uint32_t piece = (uint32_t)(min(p.w.K - kb * kTileK, kTileK) * size);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[s], kWeights + piece * tile.rows);
+                bulk_load(st, weights + (int64_t)kb * kWeights, kWeights, &full[s]);
+            }
+            __syncwarp();
+            for (int r = lane; r < tile.rows; r += 32)
+                bulk_load(st + kWeights + r * kPitch, x + ((int64_t)r * p.w.K + kb * kTileK) * size, piece, &full[s]);
+        }
+        if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
+        // no copy may be in flight when the CTA ends, whatever its consumers did
+        for (int i = max(0, filled - kStages); i < filled; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
+    } else {
+        const int g = lane >> 2, t = lane & 3;
+        const int live = (tile.rows + 7) / 8;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const int step = kb - kb0, s = step % kStages;
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (step / kStages) & 1))) {
+                good = false;
+                if (lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
+                break;
+            }
+            const unsigned char* st = smem + s * kStage;
+            const unsigned char* wt = st + warp * tile_bytes(G);
+            const uint4 lo = *reinterpret_cast<const uint4*>(wt + lane * 16);
+            const uint4 hi = *reinterpret_cast<const uint4*>(wt + 512 + lane * 16);
+            const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
+            const int valid = p.w.K - kb * kTileK;        // channels of this step that exist
+            float part[NT][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i * 32 % G == 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) part[n][c] = 0.f;
+                }
+                const uint32_t a0[4] = {widen<FP8>(w0[i], 0), widen<FP8>(w1[i], 0), widen<FP8>(w0[i], 1), widen<FP8>(w1[i], 1)};
+                const uint32_t a1[4] = {widen<FP8>(w0[i], 2), widen<FP8>(w1[i], 2), widen<FP8>(w0[i], 3), widen<FP8>(w1[i], 3)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (n >= live) break;
+                    const unsigned char* row = st + kWeights + (n * 8 + g) * kPitch;
+                    uint32_t b[4];
+                    if (FP8) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(row + 32 * i + 8 * t);
+                        b[0] = f16x2_of_e4m3x2(v.x);
+                        b[1] = f16x2_of_e4m3x2(v.x >> 16);
+                        b[2] = f16x2_of_e4m3x2(v.y);
+                        b[3] = f16x2_of_e4m3x2(v.y >> 16);
+                    } else {
+                        uint4 v = *reinterpret_cast<const uint4*>(row + 64 * i + 16 * t);
+                        if (32 * i + 8 * t >= valid) v = make_uint4(0, 0, 0, 0);   // past the row's end
+                        b[0] = v.x;
+                        b[1] = v.y;
+                        b[2] = v.z;
+                        b[3] = v.w;
+                    }
+                    mma16816<FP8>(part[n], a0, b[0], b[1]);
+                    mma16816<FP8>(part[n], a1, b[2], b[3]);
+                }
+                if ((i + 1) * 32 % G == 0) {
+                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(wt + kCodeBytes + i * 32 / G * 32 + g * 4);
+                    const float s0 = bf16_lo(sc), s1 = bf16_hi(sc);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (n >= live) break;
+                        if (FP8) {
+                            const float2 q = *reinterpret_cast<const float2*>(xs + step * kRows + n * 8 + 2 * t);
+                            acc[n][0] = fmaf(part[n][0], s0 * q.x, acc[n][0]);
+                            acc[n][1] = fmaf(part[n][1], s0 * q.y, acc[n][1]);
+                            acc[n][2] = fmaf(part[n][2], s1 * q.x, acc[n][2]);
+                            acc[n][3] = fmaf(part[n][3], s1 * q.y, acc[n][3]);
+                        } else {
+                            acc[n][0] = fmaf(part[n][0], s0, acc[n][0]);
+                            acc[n][1] = fmaf(part[n][1], s0, acc[n][1]);
+                            acc[n][2] = fmaf(part[n][2], s1, acc[n][2]);
+                            acc[n][3] = fmaf(part[n][3], s1, acc[n][3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+        }
+    }
+    if (splits > 1) {
+        // share i adds up the tiles i, i + splits, ...
+        if (warp < kTiles && warp % splits != split)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) parts[(warp * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        cluster_sync();
+        if (warp < kTiles && warp % splits == split) {
+            float sum[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sum[n][c] = 0.f;
+            for (int r = 0; r < splits; ++r) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float4 v = r == split ? make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3])
+                                                : cluster_load(parts + (warp * NT + n) * 32 + lane, (uint32_t)r);
+                    sum[n][0] += v.x;
+                    sum[n][1] += v.y;
+                    sum[n][2] += v.z;
+                    sum[n][3] += v.w;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[n][c] = sum[n][c];
+        } else {
+            good = false;     // another share writes this tile
+        }
+        cluster_sync();
+    }
+    if (warp == kTiles || !good) return;
+    // 8 channels x 8 tokens at a time: rounded, transposed, 4 bytes a lane
+    const int g = lane >> 2, t = lane & 3;
+    const int tile_at = rb * kTiles + warp;
+    uint16_t* y = static_cast<uint16_t*>(p.y) + tile.first * p.w.N;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int row = n * 8 + g;
+        if (p.w.paired) {
+            const uint32_t v = transpose8x8(pack_bf16x2(silu(acc[n][0]) * acc[n][2], silu(acc[n][1]) * acc[n][3]));
+            if (row < tile.rows && tile_at * 8 < p.w.N)
+                *reinterpret_cast<uint32_t*>(y + (int64_t)row * p.w.N + tile_at * 8 + 2 * t) = v;
+        } else {
+            const uint32_t v0 = transpose8x8(pack_bf16x2(acc[n][0], acc[n][1]));
+            const uint32_t v1 = transpose8x8(pack_bf16x2(acc[n][2], acc[n][3]));
+            uint16_t* to = y + (int64_t)row * p.w.N + tile_at * 16 + 2 * t;
+            if (row < tile.rows && tile_at * 16 < p.w.N) *reinterpret_cast<uint32_t*>(to) = v0;
+            if (row < tile.rows && tile_at * 16 + 8 < p.w.N) *reinterpret_cast<uint32_t*>(to + 8) = v1;
+        }
+    }
+}
+
+size_t w4_smem(const W4Shape& w, int nt, bool fp8, int splits) {
+    const size_t stage = (size_t)kTiles * tile_bytes(w.group) + 8 * nt * x_pitch(fp8);
+    return kStages * stage + (fp8 ? (size_t)k_blocks(w) * 8 * nt * 4 : 0) + (splits > 1 ? (size_t)kTiles * nt * 32 * 16 : 0);
+}
+
+constexpr size_t kMaxSmem = 227 * 1024 - 1024;
+
+template <int NT, int G, bool FP8>
+cudaError_t launch_form(const W4Params& p, int splits, int64_t tiles, cudaStream_t stream) {
+    auto kern = expert_w4_kernel<NT, G, FP8>;
+    const size_t smem = w4_smem(p.w, NT, FP8, splits);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * row_blocks(p.w) * splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, splits, (int)tiles);
+}
+
+template <int NT, bool FP8>
+cudaError_t launch_group(const W4Params& p, int splits, int64_t tiles, cudaStream_t stream) {
+    if (p.w.group == 32) return launch_form<NT, 32, FP8>(p, splits, tiles, stream);
+    if (p.w.group == 64) return launch_form<NT, 64, FP8>(p, splits, tiles, stream);
+    return launch_form<NT, 128, FP8>(p, splits, tiles, stream);
+}
+
+template <int NT>
+cudaError_t launch_rows(const W4Params& p, int num_sms, cudaStream_t stream) {
+    // every row in a tile of its expert: full tiles, and a last one for each expert in use
+    const int64_t tiles = std::min<int64_t>(p.w.E, p.max_rows) + p.max_rows / (8 * NT);
+    // few products: share K among the CTAs of a cluster until there are about two CTAs for every SM
+    int splits = 1;
+    while (splits < 8 && std::min<int64_t>(p.w.E, p.max_rows) * row_blocks(p.w) * splits < 2 * num_sms && k_blocks(p.w) >= 4 * splits)
+        splits *= 2;
+    return p.fp8 ? launch_group<NT, true>(p, splits, tiles, stream) : launch_group<NT, false>(p, splits, tiles, stream);
+}
+
+}  // namespace
+
+size_t w4_bytes(const W4Shape& w) {
+    return (size_t)w.E * row_blocks(w) * k_blocks(w) * kTiles * tile_bytes(w.group);
+}
+
+bool w4_packs(const W4Shape& w) { return (int64_t)w.E * row_blocks(w) * k_blocks(w) * kTiles <= INT32_MAX; }
+
+bool w4_fits(const W4Shape& w, int64_t max_rows, int fp8) {
+    // shared memory of the widest form, CTAs of the narrowest
+    return w4_smem(w, 8, fp8 != 0, 8) <= kMaxSmem &&
+           (std::min<int64_t>(w.E, max_rows) + max_rows / 8) * row_blocks(w) * 8 <= INT32_MAX;
+}
+
+cudaError_t launch_w4_pack(const W4Shape& w, const uint8_t* codes, const void* scales, void* packed, cudaStream_t stream) {
+    const int64_t tiles = (int64_t)w.E * row_blocks(w) * k_blocks(w) * kTiles;
+    return launch_kernel(false, w4_pack_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, w, codes,
+                         static_cast<const uint16_t*>(scales), static_cast<unsigned char*>(packed));
+}
+
+cudaError_t launch_expert_w4(const W4Params& p, int num_sms, cudaStream_t stream) {
+    if (p.max_rows == 0) return cudaSuccess;
+    // tokens of a tile: enough for about twice an expert's share of the rows
+    const int64_t share = p.max_rows / std::min<int64_t>(p.w.E, p.max_rows);
+    if (p.max_rows <= 8) return launch_rows<1>(p, num_sms, stream);
+    if (share <= 8) return launch_rows<2>(p, num_sms, stream);
+    if (share <= 16) return launch_rows<4>(p, num_sms, stream);
+    return launch_rows<8>(p, num_sms, stream);
+}
+
+}  // namespace ep

@@ -518,6 +518,66 @@ EP_API ep_status_t ep_route_backward(const ep_route_t *route, const void *logits
                      const int32_t *seq_tokens, const float *d_topk_w,
                      const float *d_losses, void *d_logits, ep_stream_t stream);
 
+typedef struct {
+    int32_t E;                /* matrices (experts), 1..EP_MAX_EXPERTS         */
+    int32_t N;                /* output channels, > 0, multiple of 8           */
+    int32_t K;                /* input channels, > 0, multiple of 8 (of 128 for
+                                 fp8 rows)                                     */
+    int32_t group;            /* input channels that share a scale: 32, 64 or
+                                 128 (the last group of a row may be shorter)  */
+    int32_t paired;           /* 1: each expert has 2N rows, N gate rows and
+                                 then N up rows, and y = silu(gate) * up       */
+} ep_w4_t;
+
+/* Bytes of the packed weights (codes and scales of all experts);
+ * (size_t)-1 if the description is invalid. */
+EP_API size_t ep_w4_bytes(const ep_w4_t *w);
+
+/*
+ * ep_w4_pack -- lay 4-bit weights out for ep_expert_w4, once per model load.
+ *
+ * In:  codes   u8 [E, rows, K/2] (rows = N, or 2N when paired): input channel
+ *              2i in the low half of byte i, 2i + 1 in the high half; a code c
+ *              of 0..15 stands for (c - 8) * scale.  4-byte aligned.
+ *      scales  bf16 [E, rows, ceil(K / group)].
+ * Out: packed  ep_w4_bytes(w) bytes, 16-byte aligned.
+ */
+EP_API ep_status_t ep_w4_pack(const ep_w4_t *w, const uint8_t *codes, const void *scales,
+                       void *packed, ep_stream_t stream);
+
+/*
+ * ep_expert_w4 -- every expert's product over its rows of the receive buffer:
+ *   y[r, n] = sum_k x[r, k] * (code[e, n, k] - 8) * scale[e, n, k / group]
+ * for the rows r of expert e (paired: silu of the gate product times the up
+ * product), accumulated in fp32 and rounded once to bf16.  Codes and fp8
+ * values enter the tensor cores exactly; scales are applied in fp32.  Made for
+ * the few rows an expert has in a decode batch, where the weights' bytes decide
+ * the time; correct for any number of rows.
+ *
+ * In:  mode, capacity  as in ep_shape_t: packed rows [offsets[e],
+ *              offsets[e+1]), or in capacity mode the first min(counts[e],
+ *              capacity) rows of [e*capacity, (e+1)*capacity).
+ *      counts  i32 [E] (capacity mode), offsets i32 [E+1] (packed), from
+ *              ep_get_layout; the other may be NULL.  With E = 1, packed and
+ *              offsets NULL all R rows belong to the one matrix.
+ *      R       rows of x and y (at least E*capacity in capacity mode).
+ *      max_rows  no more than this many rows hold a copy in all experts
+ *              together (T*k): sizes the launch.  If they hold more, the rest
+ *              is not computed and EP_ERRF_CAPACITY is flagged.
+ *      x, x_scales, payload  the receive buffer as ep_dispatch writes it:
+ *              bf16 [R, K], or e4m3 [R, K] with f32 (4-byte aligned) or u8
+ *              UE8M0 scales [R, K/128].  x 16-byte aligned.
+ * Out: y       bf16 [R, N], 16-byte aligned.  Rows that hold no copy are not
+ *              written.
+ * err_flags: EP_ERRF_BAD_SLOT (rows outside [0, R), skipped),
+ * EP_ERRF_CAPACITY, EP_ERRF_TIMEOUT.
+ */
+EP_API ep_status_t ep_expert_w4(const ep_w4_t *w, const void *packed, int32_t mode,
+                         int32_t capacity, int64_t R, int64_t max_rows,
+                         const int32_t *counts, const int32_t *offsets, const void *x,
+                         const void *x_scales, int32_t payload, void *y,
+                         uint32_t *err_flags, ep_stream_t stream);
+
 /* Static description of a status code. */
 EP_API const char *ep_status_string(ep_status_t status);
 

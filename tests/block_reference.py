@@ -140,3 +140,27 @@ def route(logits, idx, live, bounds, full, balance_coef, z_coef, d_topk_w=None, 
     v["d_logits"] = p * (g - (p * g).sum(1, keepdims=True)) + (zg * lse)[:, None] * p + extra
     z["d_logits"] = p * (g_size + (p * g_size).sum(1, keepdims=True)) + (abs(zg) * (np.abs(top) + np.abs(lse) + 1))[:, None] * p + size
     return v, z
+
+
+def expert_w4(x, codes, scales, group, paired, spans):
+    """Values and bounds' sizes of ep_expert_w4, in rows; spans: (expert, first
+    row, rows).  x in float64, scales applied already; codes u8 [E, rows, K/2].
+    Returns (rows written, value, size of an error of one 2^-24 per term)."""
+    R, K = x.shape
+    rows = codes.shape[1]
+    N = rows // 2 if paired else rows
+    q = np.empty((codes.shape[0], rows, K))
+    q[..., 0::2], q[..., 1::2] = codes & 15, codes >> 4
+    w = (q - 8) * np.repeat(scales, group, axis=2)[..., :K]
+    y, size, live = np.zeros((R, N)), np.zeros((R, N)), np.zeros(R, bool)
+    for e, a, n in spans:
+        v, z = x[a:a + n] @ w[e].T, np.abs(x[a:a + n]) @ np.abs(w[e]).T
+        if paired:
+            g, u = v[:, :N], v[:, N:]
+            s = 1 / (1 + np.exp(-g))
+            # |d silu / d g| <= 1.1
+            y[a:a + n], size[a:a + n] = g * s * u, 1.1 * z[:, :N] * np.abs(u) + np.abs(g * s) * z[:, N:] + z[:, :N] * z[:, N:] * K * EPS32
+        else:
+            y[a:a + n], size[a:a + n] = v, z
+        live[a:a + n] = True
+    return live, y, size

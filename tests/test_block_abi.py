@@ -97,3 +97,35 @@ def test_route_arguments(lib):
                 dict(tokens=None), dict(d=None), dict(d=ODD), dict(shape=two)):
         assert bwd(**bad) == _lib.EP_ERR_INVALID_ARG, bad
     assert lib.ep_route_backward(ctypes.byref(none), None, 0, *([None] * 10)) == 0
+
+
+@pytest.mark.parametrize("bad,status", [(dict(E=0), 1), (dict(E=1025), 2), (dict(N=0), 1), (dict(N=12), 1), (dict(K=0), 1),
+                                        (dict(K=12), 1), (dict(group=16), 1), (dict(group=256), 1), (dict(paired=2), 1),
+                                        (dict(E=1024, N=1 << 20, K=1 << 20), 2), (dict(N=1 << 25), 2)])
+def test_w4_descriptions(lib, bad, status):
+    f = dict(E=4, N=16, K=128, group=128, paired=0)
+    f.update(bad)
+    s = _lib.W4(**f)
+    assert lib.ep_w4_bytes(ctypes.byref(s)) == ctypes.c_size_t(-1).value
+    assert lib.ep_w4_pack(ctypes.byref(s), FAKE, FAKE, FAKE, None) == status
+    assert lib.ep_expert_w4(ctypes.byref(s), FAKE, 0, 0, 4, 4, FAKE, FAKE, FAKE, None, 0, FAKE, None, None) == status
+
+
+def test_w4_arguments(lib):
+    s = _lib.W4(4, 16, 128, 64, 0)
+    # one row block, one step of K: eight tiles of 1024 bytes of codes and two groups of 16 scales
+    assert lib.ep_w4_bytes(ctypes.byref(s)) == 4 * 8 * (1024 + 64)
+    for args in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None), (ODD, FAKE, FAKE), (FAKE, FAKE, ODD)):
+        assert lib.ep_w4_pack(ctypes.byref(s), *args, None) == _lib.EP_ERR_INVALID_ARG
+
+    def call(shape=s, packed=FAKE, mode=0, cap=0, R=8, rows=8, counts=FAKE, offsets=FAKE, x=FAKE, xs=None, payload=0, y=FAKE):
+        return lib.ep_expert_w4(ctypes.byref(shape), packed, mode, cap, R, rows, counts, offsets, x, xs, payload, y, None, None)
+
+    odd_k = _lib.W4(4, 16, 120, 64, 0)
+    for bad in (dict(packed=None), dict(packed=ODD), dict(mode=2), dict(mode=1, cap=0), dict(mode=1, cap=3), dict(R=-1), dict(rows=-1),
+                dict(offsets=None), dict(mode=1, cap=2, counts=None), dict(x=None), dict(x=ODD), dict(y=None), dict(y=ODD),
+                dict(payload=3), dict(payload=1), dict(payload=1, xs=ODD), dict(shape=odd_k, payload=1, xs=FAKE)):
+        assert call(**bad) == _lib.EP_ERR_INVALID_ARG, bad
+    assert call(R=0) == 0 and call(rows=0) == 0
+    assert call(R=2 ** 31) == _lib.EP_ERR_UNSUPPORTED
+    assert call(shape=_lib.W4(1, 16, 1 << 20, 128, 0), payload=1, xs=FAKE) == _lib.EP_ERR_UNSUPPORTED   # a row's scales do not fit

@@ -80,3 +80,14 @@ def test_losses_by_hand():
     idx = np.zeros((2, 1), np.int64)
     v, _ = ref.route(np.zeros((2, 2)), idx, np.ones(2, bool), np.array([0, 2]), False, 1.0, 1.0)
     np.testing.assert_allclose(v["losses"], [1.0, np.log(2) ** 2])
+
+
+def test_expert_w4_by_hand():
+    codes = np.array([[[0x9f, 0x08], [0x71, 0xe8]]], np.uint8)        # codes 15 9 8 0 / 1 7 8 14
+    scales = np.array([[[2.0], [0.5]]])
+    x = np.array([[1.0, 2.0, 3.0, 1.0]])
+    live, y, _ = ref.expert_w4(x, codes, scales, 32, False, [(0, 0, 1)])
+    np.testing.assert_allclose(y, [[2 * (7 + 2 - 8), 0.5 * (-7 - 2 + 6)]])
+    _, y, _ = ref.expert_w4(x, codes, scales, 32, True, [(0, 0, 1)])
+    np.testing.assert_allclose(y, [[2 / (1 + np.exp(-2)) * -1.5]])
+    assert live.all()

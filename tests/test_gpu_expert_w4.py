@@ -1,0 +1,218 @@
+"""ep_expert_w4 against a plain 64-bit implementation.
+
+Bound: K products a sum, fp32 (the matrix instructions may cut off where a
+fused multiply-add rounds, so two units of 2^-24 a term), one rounding to bf16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+import combine_ep_get_04_gb300 as ep
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    assert torch.cuda.is_available(), "the GPU tests need a CUDA device"
+    ep.load()
+
+
+def make_weights(E, N, K, group, paired, g):
+    rows = 2 * N if paired else N
+    codes = torch.randint(0, 256, (E, rows, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = ((torch.rand(E, rows, -(-K // group), generator=g, device="cuda") + 0.5) * 0.3 / K ** 0.5).bfloat16()
+    return codes, scales
+
+
+def make_rows(R, K, kind, g):
+    x = torch.randn(R, K, generator=g, device="cuda")
+    if kind == "bf16":
+        x = x.bfloat16()
+        return x, None, x.double().cpu().numpy()
+    b = x.view(R, K // 128, 128)
+    s = b.abs().amax(2).clamp_min(1e-4) / 448
+    if kind == "ue8m0":
+        e = torch.ceil(torch.log2(s))
+        q = (b * torch.exp2(-e)[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        value = q.double() * torch.exp2(e.double())[..., None]
+        s = (e + 127).to(torch.uint8)
+    else:
+        q = (b / s[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        value = q.double() * s.double()[..., None]
+    return q.view(R, K), s, value.view(R, K).cpu().numpy()
+
+
+def check(counts, N, K, group=128, paired=False, kind="bf16", capacity=None, seed=0, max_rows=None, bare=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    E = len(counts)
+    codes, scales = make_weights(E, N, K, group, paired, g)
+    w = ep.W4Weights(codes, scales, group, paired)
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    R = E * capacity if capacity else int(offsets[-1])
+    x, xs, value = make_rows(R, K, kind, g)
+    kept = [min(c, capacity) if capacity else c for c in counts]
+    spans = [(e, e * capacity if capacity else int(offsets[e]), n) for e, n in enumerate(kept)]
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dev = dict(dtype=torch.int32, device="cuda")
+    layout = {} if bare else dict(counts=torch.tensor(counts, **dev), offsets=torch.tensor(offsets, **dev))
+    got = ep.expert_w4(x, w, **layout, capacity=capacity, x_scales=xs, max_rows=max_rows, out=out, err_flags=err)
+    torch.cuda.synchronize()
+    assert got is out and int(err) == 0
+    live, y, size = ref.expert_w4(value, codes.cpu().numpy(), scales.double().cpu().numpy(), group, paired, spans)
+    got = out.double().cpu().numpy()
+    assert (got[~live] == 7.0).all(), "rows without a copy were written"
+    b = ref.bound(y, size, 2 * K, True)[live]
+    off = np.abs(got - y)[live]
+    assert (off <= b).all(), f"{(off > b).sum()} of {off.size} beyond the bound, worst {(off - b).max():.3g} past it"
+
+
+@pytest.mark.parametrize("kind,K", [("bf16", 8), ("bf16", 72), ("bf16", 128), ("bf16", 200), ("bf16", 1000), ("bf16", 4096),
+                                    ("fp8", 128), ("fp8", 640), ("ue8m0", 384), ("fp8", 7168)])
+@pytest.mark.parametrize("N", [8, 24, 128, 136, 1000])
+@pytest.mark.parametrize("paired", [False, True])
+def test_one_matrix(kind, K, N, paired):
+    for group, rows in ((32, 1), (64, 3), (128, 8)):
+        check([rows], N, K, group, paired, kind, bare=rows == 3)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 31, 33, 63, 64, 65, 130, 300])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "ue8m0"])
+def test_rows_of_one_matrix(rows, kind):
+    check([rows], 72, 512, 64, True, kind)
+    check([rows], 200, 256, 128, False, kind)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "ue8m0"])
+@pytest.mark.parametrize("capacity", [None, 12])
+def test_experts_with_few_rows(group, kind, capacity):
+    counts = [3, 0, 1, 12, 0, 0, 5, 9, 8, 2, 1, 4, 0]
+    check(counts, 136, 384, group, False, kind, capacity, max_rows=sum(counts))
+    check(counts, 72, 256, group, True, kind, capacity, max_rows=sum(counts))
+
+
+@pytest.mark.parametrize("capacity", [None, 40])
+def test_uneven_experts(capacity):
+    """Shares of 8, 16 and more rows an expert take tiles of other sizes; one expert has most rows."""
+    check([70, 0, 1, 2, 0, 3], 64, 256, capacity=capacity)
+    check([0, 0, 129, 2], 64, 256, 64, True, "fp8", capacity=capacity)
+    check([40, 40, 39, 33, 64], 64, 256, 32, capacity=capacity)
+
+
+def test_many_experts():
+    rng = np.random.default_rng(4)
+    check(rng.poisson(0.7, 1024).tolist(), 16, 128, 32)
+    check(rng.poisson(2.0, 333).tolist(), 16, 128, 128, True, "fp8")
+    check(rng.poisson(2.0, 33).tolist(), 24, 136, 64, False, capacity=3)
+
+
+def test_no_rows():
+    check([0, 0, 0], 16, 128, capacity=4, max_rows=5)
+    w = ep.W4Weights(*make_weights(3, 16, 128, 128, False, torch.Generator(device="cuda").manual_seed(0)))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    y = ep.expert_w4(torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"), w, torch.zeros(3, **i32), torch.zeros(4, **i32))
+    assert y.shape == (0, 16)
+
+
+def test_a_bad_row_stays_alone():
+    """Infinities and NaN reach the outputs of their own row only, also past
+    the end of a short last step of K."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    codes, scales = make_weights(1, 64, 200, 64, False, g)
+    w = ep.W4Weights(codes, scales, 64)
+    x = torch.randn(6, 200, generator=g, device="cuda").bfloat16()
+    clean = ep.expert_w4(x, w).clone()
+    for bad in (float("nan"), float("inf")):
+        z = x.clone()
+        z[2, 100] = bad
+        z[4, 199] = bad
+        y = ep.expert_w4(z, w)
+        rows = [0, 1, 3, 5]
+        assert torch.equal(y[rows], clean[rows])
+        for r, k in ((2, 100), (4, 199)):
+            code = (codes[0, :, k // 2] >> (4 * (k % 2))) & 15
+            finite = torch.isfinite(y[r].float())
+            # inf times a zero weight is NaN too
+            assert not finite.any(), (bad, r, code[finite])
+
+
+def test_same_bits_twice_and_on_another_stream():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for counts, N, K in (([1], 4096, 4096), ([4] * 40, 512, 1024)):
+        codes, scales = make_weights(len(counts), N, K, 128, False, g)
+        w = ep.W4Weights(codes, scales)
+        x = torch.randn(sum(counts), K, generator=g, device="cuda").bfloat16()
+        o = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+        a = ep.expert_w4(x, w, offsets=o).clone()
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        b = ep.expert_w4(x, w, offsets=o, stream=s)
+        s.synchronize()
+        assert torch.equal(a, b) and torch.equal(a, ep.expert_w4(x, w, offsets=o))
+
+
+def test_bad_layouts_are_flagged_and_skipped():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    codes, scales = make_weights(3, 16, 128, 128, False, g)
+    w = ep.W4Weights(codes, scales)
+    x = torch.randn(12, 128, generator=g, device="cuda").bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(offsets, **more):
+        out = torch.full((12, 16), 7.0, dtype=torch.bfloat16, device="cuda")
+        err.zero_()
+        ep.expert_w4(x, w, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=out, err_flags=err, **more)
+        return out, int(err)
+
+    good, flags = run([0, 4, 8, 12])
+    assert flags == 0
+    out, flags = run([0, 4, 8, 13])
+    assert flags == ep.ERRF_BAD_SLOT and torch.equal(out[:8], good[:8]) and (out[8:] == 7).all()
+    out, flags = run([-2, 4, 8, 12])
+    assert flags == ep.ERRF_BAD_SLOT and (out[:4] == 7).all() and torch.equal(out[4:], good[4:])
+    out, flags = run([0, 12, 8, 12])              # falls: expert 1 has no rows
+    assert flags == 0 and torch.equal(out[:4], good[:4])
+    _, flags = run([0, 4, 8, 12], max_rows=1)     # room for one expert's tile
+    assert flags == ep.ERRF_CAPACITY
+    x, out = x[:12], None
+
+
+def test_refusals():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    codes, scales = make_weights(2, 16, 128, 128, False, g)
+    w = ep.W4Weights(codes, scales)
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    o = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        ep.expert_w4(x, w)
+    with pytest.raises(ValueError):
+        ep.expert_w4(x[:, :64], w, offsets=o)
+    with pytest.raises(TypeError):
+        ep.expert_w4(x.float(), w, offsets=o)
+    with pytest.raises(ValueError):
+        ep.expert_w4(x, w, offsets=o[:2])
+    with pytest.raises(TypeError):
+        ep.expert_w4(x, w, offsets=o, x_scales=torch.ones(4, 1, device="cuda"))
+    with pytest.raises(TypeError):
+        ep.expert_w4(x.to(torch.float8_e4m3fn), w, offsets=o, x_scales=torch.ones(4, 1, device="cuda").half())
+    with pytest.raises(ValueError):
+        ep.expert_w4(x.to(torch.float8_e4m3fn), w, offsets=o, x_scales=torch.ones(4, 2, device="cuda"))
+    with pytest.raises(ep.EPError):
+        ep.expert_w4(x, w, counts=o[:2], capacity=3)      # needs 6 rows
+    with pytest.raises(ep.EPError):
+        ep.expert_w4(x, w, counts=o[:2])                   # packed rows need offsets
+    with pytest.raises(ValueError):
+        ep.expert_w4(x, w, offsets=o, out=torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda"))
+    for bad in (dict(group=96), dict(codes=codes[:, :, :62], scales=scales), dict(codes=codes[:, :12], scales=scales[:, :12])):
+        with pytest.raises(ep.EPError):
+            ep.W4Weights(**{**dict(codes=codes, scales=scales), **bad})
+    with pytest.raises(ValueError):
+        ep.W4Weights(codes, scales, group=64)
+    with pytest.raises(TypeError):
+        ep.W4Weights(codes, scales.float())
+    odd = ep.W4Weights(codes[:, :, :60].contiguous(), scales)   # K = 120: no fp8 rows
+    with pytest.raises(ep.EPError):
+        ep.expert_w4(x.to(torch.float8_e4m3fn)[:, :120].contiguous(), odd, offsets=o, x_scales=torch.ones(4, 0, device="cuda"))
