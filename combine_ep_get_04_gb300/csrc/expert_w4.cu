@@ -8,12 +8,12 @@
 // 16-byte word: tiles of 16 weight rows x 128 input channels, 1024 bytes of
 // codes and then the tile's scales, eight tiles side by side for each step
 // along K.  A producer warp keeps a ring of such steps (and the matching
-// 128-channel pieces of the token rows) filled with bulk copies; eight
-// consumer warps, one tile each, widen the codes to bf16 (f16 beside fp8 rows:
-// both hold code - 8 and every e4m3 value exactly) and multiply with
+// 128-channel pieces of the token rows) filled with bulk copies; four consumer
+// warps, two tiles each, widen the codes to bf16 (f16 beside fp8 rows: either
+// holds code - 8 and f16 every e4m3 value exactly) and multiply with
 // mma.m16n8k16, the weights as the 16-row side and 8 tokens as the other.  A
-// group's products are summed unscaled and enter the fp32 accumulator through
-// one fused multiply-add with the group's scale.
+// group's products are summed unscaled in fp32 and enter the accumulator
+// through one fused multiply-add with the group's scale.
 #include <algorithm>
 
 #include "ep_device.cuh"
@@ -26,8 +26,12 @@ constexpr int kTileRows = 16;      // weight rows of one tile (the matrix instru
 constexpr int kTileK = 128;        // input channels of one tile
 constexpr int kTiles = 8;          // tiles of one step, one for each consumer warp
 constexpr int kCodeBytes = kTileRows * kTileK / 2;
-constexpr int kStages = 4;
-constexpr int kThreads = (kTiles + 1) * 32;
+
+// Steps in flight; the widest form has the fewest, so that two CTAs fit an SM.
+__host__ __device__ constexpr int ring_stages(int nt) { return nt >= 8 ? 3 : 4; }
+constexpr int kWarps = 4;          // consumer warps, kOwn tiles each
+constexpr int kOwn = kTiles / kWarps;
+constexpr int kThreads = (kWarps + 1) * 32;
 
 __host__ __device__ constexpr int tile_bytes(int group) { return kCodeBytes + kTileK / group * 32; }
 
@@ -79,32 +83,45 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4Shape w, const uint8_t* 
     }
 }
 
-// D += A B for one 16 x 8 x 16 step, fp32 accumulators.
+// D = A B + C for one 16 x 8 x 16 step, fp32 accumulators.
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1, float c2,
+                                         float c3) {
     if (F16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Pair j of a word of codes as code - 8 in two halves: the code under an
-// exponent whose last place is 1 (bf16: 128 + c, f16: 1024 + c), less that
-// offset and 8.  Both steps are exact.
+// Widening a word of codes to four pairs of numbers, (code - 8) * 2^-6 in bf16
+// or (code - 8) * 2^-9 in f16.  Masked out of its half, a code in bits 0-3 or
+// 4-7 is a tiny number as it stands: subnormals and the first binade above
+// them are one linear range, so in bf16 it is code * 2^-133 or code * 2^-129,
+// in f16 code * 2^-24 or code * 2^-20.  One fused multiply-add brings it up
+// and takes 8 off; both steps are exact.  One shift, four masks and four
+// multiply-adds for eight codes: masks and shifts go through the ALU, which is
+// the busiest pipe, so nothing else is left to it.
 template <bool F16>
-__device__ __forceinline__ uint32_t widen(uint32_t word, int j) {
-    const uint32_t m = (word >> (4 * j) & 0x000f000fu) | (F16 ? 0x64006400u : 0x43004300u);
-    uint32_t r;
-    if (F16)
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x64086408u));
-    else
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x43084308u));
-    return r;
+__device__ __forceinline__ void widen(uint32_t word, uint32_t (&pair)[4]) {
+    constexpr uint32_t kLow = F16 ? 0x78007800u : 0x7f007f00u;       // 2^15, 2^127
+    constexpr uint32_t kHigh = F16 ? 0x68006800u : 0x7d007d00u;      // 2^11, 2^123
+    constexpr uint32_t kOff = F16 ? 0xa400a400u : 0xbe00be00u;       // -8 * 2^-9, -8 * 2^-6
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t m = (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
+        if (F16)
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(pair[j]) : "r"(m), "r"(j & 1 ? kHigh : kLow), "r"(kOff));
+        else
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(pair[j]) : "r"(m), "r"(j & 1 ? kHigh : kLow), "r"(kOff));
+    }
 }
+
+template <bool F16>
+constexpr float kUnit = F16 ? 512.f : 64.f;      // what the widened codes are divided by
 
 // Two e4m3 codes -> f16x2, exact.
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
@@ -119,6 +136,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
+
+__device__ __forceinline__ void clear(float (&v)[4]) { v[0] = v[1] = v[2] = v[3] = 0.f; }
 
 __device__ __forceinline__ float silu(float x) { return x / (1.f + __expf(-x)); }
 
@@ -197,6 +216,105 @@ __device__ __forceinline__ float4 cluster_load(const float4* p, uint32_t rank) {
     return v;
 }
 
+// A consumer warp's walk along K: `steps` steps of the ring, NL x 8 tokens.
+// The accumulators hold sums of scale * (code - 8) / kUnit * x.  False if a
+// wait timed out.
+template <int NT, int NL, int G, bool FP8>
+__device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigned char* smem, const float* xs, uint64_t* full,
+                                        uint64_t* empty, int steps) {
+    constexpr int kWeights = kTiles * tile_bytes(G);
+    constexpr int kRows = 8 * NT;
+    constexpr int kPitch = x_pitch(FP8);
+    constexpr int kStage = kWeights + kRows * kPitch;
+    constexpr int kRing = ring_stages(NT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const unsigned char* own = smem + warp * kOwn * tile_bytes(G);
+    const unsigned char* rows = smem + kWeights + g * kPitch + (FP8 ? 8 : 16) * t;
+    xs += 2 * t;
+    int s = 0;
+    uint32_t parity = 0;
+    for (int step = 0; step < steps; ++step) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], parity))) return false;
+        const unsigned char* wt = own + s * kStage;
+        const unsigned char* xr = rows + s * kStage;
+        uint32_t w[kOwn][2][4];                // [tile][row g, row g + 8][32 channels each]
+#pragma unroll
+        for (int u = 0; u < kOwn; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 v = *reinterpret_cast<const uint4*>(wt + u * tile_bytes(G) + h * 512 + lane * 16);
+                w[u][h][0] = v.x;
+                w[u][h][1] = v.y;
+                w[u][h][2] = v.z;
+                w[u][h][3] = v.w;
+            }
+        float part[kOwn][NL][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a[kOwn][2][4];            // [tile][16 channels each]
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t pair[4];
+                    widen<FP8>(w[u][h][i], pair);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a[u][j >> 1][(j & 1) * 2 + h] = pair[j];
+                }
+#pragma unroll
+            for (int n = 0; n < NL; ++n) {
+                uint32_t b[4];
+                if (FP8) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(xr + n * 8 * kPitch + 32 * i);
+                    b[0] = f16x2_of_e4m3x2(v.x);
+                    b[1] = f16x2_of_e4m3x2(v.x >> 16);
+                    b[2] = f16x2_of_e4m3x2(v.y);
+                    b[3] = f16x2_of_e4m3x2(v.y >> 16);
+                } else {
+                    const uint4 v = *reinterpret_cast<const uint4*>(xr + n * 8 * kPitch + 64 * i);
+                    b[0] = v.x;
+                    b[1] = v.y;
+                    b[2] = v.z;
+                    b[3] = v.w;
+                }
+#pragma unroll
+                for (int u = 0; u < kOwn; ++u) {
+                    float (&d)[4] = part[u][n];
+                    if (i * 32 % G == 0)
+                        mma16816<FP8>(d, a[u][0], b[0], b[1], 0.f, 0.f, 0.f, 0.f);
+                    else
+                        mma16816<FP8>(d, a[u][0], b[0], b[1], d[0], d[1], d[2], d[3]);
+                    mma16816<FP8>(d, a[u][1], b[2], b[3], d[0], d[1], d[2], d[3]);
+                }
+            }
+            if ((i + 1) * 32 % G == 0) {
+#pragma unroll
+                for (int u = 0; u < kOwn; ++u) {
+                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(wt + u * tile_bytes(G) + kCodeBytes + i * 32 / G * 32 + g * 4);
+                    const float s0 = bf16_lo(sc), s1 = bf16_hi(sc);
+#pragma unroll
+                    for (int n = 0; n < NL; ++n) {
+                        float2 q = make_float2(1.f, 1.f);
+                        if (FP8) q = *reinterpret_cast<const float2*>(xs + n * 8);
+                        acc[u][n][0] = fmaf(part[u][n][0], FP8 ? s0 * q.x : s0, acc[u][n][0]);
+                        acc[u][n][1] = fmaf(part[u][n][1], FP8 ? s0 * q.y : s0, acc[u][n][1]);
+                        acc[u][n][2] = fmaf(part[u][n][2], FP8 ? s1 * q.x : s1, acc[u][n][2]);
+                        acc[u][n][3] = fmaf(part[u][n][3], FP8 ? s1 * q.y : s1, acc[u][n][3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        if (++s == kRing) {
+            s = 0;
+            parity ^= 1;
+        }
+        if (FP8) xs += kRows;
+    }
+    return true;
+}
+
 // One CTA: one row block (128 weight rows) x one tile of up to 8 NT token rows
 // x one of `splits` shares of K.  The shares of a product form a cluster and
 // add their accumulators through distributed shared memory in the order of
@@ -204,7 +322,8 @@ __device__ __forceinline__ float4 cluster_load(const float4* p, uint32_t rank) {
 template <int NT, int G, bool FP8>
 __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int splits, int grid_tiles) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t full[kStages], empty[kStages];
+    constexpr int kRing = ring_stages(NT);
+    __shared__ uint64_t full[kRing], empty[kRing];
     __shared__ RowTile shared_tile;
     constexpr int kWeights = kTiles * tile_bytes(G);
     constexpr int kRows = 8 * NT;
@@ -216,9 +335,9 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
     const int rb = blockIdx.x / splits % blocks, at = blockIdx.x / splits / blocks;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < kRing; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kTiles);
+            mbar_init(&empty[s], kWarps);
         }
         fence_mbar_init();
     }
@@ -232,8 +351,8 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
     if (tile.e < 0) return;              // the same in all CTAs of a cluster
     const int kb0 = (int)((int64_t)nk * split / splits), kb1 = (int)((int64_t)nk * (split + 1) / splits);
     const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + (((int64_t)tile.e * blocks + rb) * nk) * kWeights;
-    float* xs = reinterpret_cast<float*>(smem + kStages * kStage);          // [k block][kRows] (fp8)
-    float4* parts = reinterpret_cast<float4*>(smem + kStages * kStage + (FP8 ? (int64_t)nk * kRows * 4 : 0));   // [kTiles][NT][32]
+    float* xs = reinterpret_cast<float*>(smem + kRing * kStage);          // [k block][kRows] (fp8)
+    float4* parts = reinterpret_cast<float4*>(smem + kRing * kStage + (FP8 ? (int64_t)nk * kRows * 4 : 0));   // [kTiles][NT][32]
     if (FP8) {
         for (int i = threadIdx.x; i < (kb1 - kb0) * kRows; i += kThreads) {
             const int kb = kb0 + i / kRows, r = i % kRows;
@@ -249,24 +368,31 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
         __syncthreads();
     }
     bool good = true;
-    float acc[NT][4];
+    float acc[kOwn][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int u = 0; u < kOwn; ++u)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
-    if (warp == kTiles) {
+        for (int n = 0; n < NT; ++n) clear(acc[u][n]);
+    if (warp == kWarps) {
         // producer
         const int size = FP8 ? 1 : 2;
         const unsigned char* x = static_cast<const unsigned char*>(p.x) + tile.first * p.w.K * size;
         int filled = 0;
         for (int kb = kb0; kb < kb1; ++kb, ++filled) {
-            const int s = filled % kStages, round = filled / kStages;
+            const int s = filled % kRing, round = filled / kRing;
             if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (round - 1) & 1))) {
                 good = false;
                 break;
             }
             unsigned char* st = smem + s * kStage;
             const uint32_t piece = (uint32_t)(min(p.w.K - kb * kTileK, kTileK) * size);
+            if (piece < kTileK * size) {
+                // a short last step: zeros stand in for the channels past the end
+                const uint32_t words = (kTileK * size - piece) / 16;
+                for (uint32_t i = lane; i < words * tile.rows; i += 32)
+                    *reinterpret_cast<uint4*>(st + kWeights + i / words * kPitch + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
+                __syncwarp();
+            }
             if (lane == 0) {
                 mbar_arrive_expect_tx(&full[s], kWeights + piece * tile.rows);
                 bulk_load(st, weights + (int64_t)kb * kWeights, kWeights, &full[s]);
@@ -277,138 +403,84 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
         }
         if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
         // no copy may be in flight when the CTA ends, whatever its consumers did
-        for (int i = max(0, filled - kStages); i < filled; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
+        for (int i = max(0, filled - kRing); i < filled; ++i) mbar_wait(&full[i % kRing], (i / kRing) & 1);
     } else {
-        const int g = lane >> 2, t = lane & 3;
-        const int live = (tile.rows + 7) / 8;
-        for (int kb = kb0; kb < kb1; ++kb) {
-            const int step = kb - kb0, s = step % kStages;
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (step / kStages) & 1))) {
-                good = false;
-                if (lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
-                break;
-            }
-            const unsigned char* st = smem + s * kStage;
-            const unsigned char* wt = st + warp * tile_bytes(G);
-            const uint4 lo = *reinterpret_cast<const uint4*>(wt + lane * 16);
-            const uint4 hi = *reinterpret_cast<const uint4*>(wt + 512 + lane * 16);
-            const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
-            const int valid = p.w.K - kb * kTileK;        // channels of this step that exist
-            float part[NT][4];
+        // tiles that are at most half full take the form made for that
+        constexpr int kHalf = NT > 1 ? NT / 2 : 1;
+        good = tile.rows <= 8 * kHalf ? consume<NT, kHalf, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0)
+                                      : consume<NT, NT, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0);
+        if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i * 32 % G == 0) {
+        for (int u = 0; u < kOwn; ++u)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) part[n][c] = 0.f;
-                }
-                const uint32_t a0[4] = {widen<FP8>(w0[i], 0), widen<FP8>(w1[i], 0), widen<FP8>(w0[i], 1), widen<FP8>(w1[i], 1)};
-                const uint32_t a1[4] = {widen<FP8>(w0[i], 2), widen<FP8>(w1[i], 2), widen<FP8>(w0[i], 3), widen<FP8>(w1[i], 3)};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n >= live) break;
-                    const unsigned char* row = st + kWeights + (n * 8 + g) * kPitch;
-                    uint32_t b[4];
-                    if (FP8) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(row + 32 * i + 8 * t);
-                        b[0] = f16x2_of_e4m3x2(v.x);
-                        b[1] = f16x2_of_e4m3x2(v.x >> 16);
-                        b[2] = f16x2_of_e4m3x2(v.y);
-                        b[3] = f16x2_of_e4m3x2(v.y >> 16);
-                    } else {
-                        uint4 v = *reinterpret_cast<const uint4*>(row + 64 * i + 16 * t);
-                        if (32 * i + 8 * t >= valid) v = make_uint4(0, 0, 0, 0);   // past the row's end
-                        b[0] = v.x;
-                        b[1] = v.y;
-                        b[2] = v.z;
-                        b[3] = v.w;
-                    }
-                    mma16816<FP8>(part[n], a0, b[0], b[1]);
-                    mma16816<FP8>(part[n], a1, b[2], b[3]);
-                }
-                if ((i + 1) * 32 % G == 0) {
-                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(wt + kCodeBytes + i * 32 / G * 32 + g * 4);
-                    const float s0 = bf16_lo(sc), s1 = bf16_hi(sc);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (n >= live) break;
-                        if (FP8) {
-                            const float2 q = *reinterpret_cast<const float2*>(xs + step * kRows + n * 8 + 2 * t);
-                            acc[n][0] = fmaf(part[n][0], s0 * q.x, acc[n][0]);
-                            acc[n][1] = fmaf(part[n][1], s0 * q.y, acc[n][1]);
-                            acc[n][2] = fmaf(part[n][2], s1 * q.x, acc[n][2]);
-                            acc[n][3] = fmaf(part[n][3], s1 * q.y, acc[n][3]);
-                        } else {
-                            acc[n][0] = fmaf(part[n][0], s0, acc[n][0]);
-                            acc[n][1] = fmaf(part[n][1], s0, acc[n][1]);
-                            acc[n][2] = fmaf(part[n][2], s1, acc[n][2]);
-                            acc[n][3] = fmaf(part[n][3], s1, acc[n][3]);
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-        }
+                for (int c = 0; c < 4; ++c) acc[u][n][c] *= kUnit<FP8>;      // a power of two
     }
     if (splits > 1) {
         // share i adds up the tiles i, i + splits, ...
-        if (warp < kTiles && warp % splits != split)
+        if (warp < kWarps)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) parts[(warp * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            for (int u = 0; u < kOwn; ++u)
+                if ((warp * kOwn + u) % splits != split)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        parts[((warp * kOwn + u) * NT + n) * 32 + lane] = make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3]);
+        __syncwarp();
         cluster_sync();
-        if (warp < kTiles && warp % splits == split) {
-            float sum[NT][4];
+        if (warp < kWarps)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) sum[n][c] = 0.f;
-            for (int r = 0; r < splits; ++r) {
+            for (int u = 0; u < kOwn; ++u) {
+                const int at_tile = warp * kOwn + u;
+                if (at_tile % splits != split) continue;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float4 v = r == split ? make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3])
-                                                : cluster_load(parts + (warp * NT + n) * 32 + lane, (uint32_t)r);
-                    sum[n][0] += v.x;
-                    sum[n][1] += v.y;
-                    sum[n][2] += v.z;
-                    sum[n][3] += v.w;
+                    float sum[4];
+                    clear(sum);
+                    for (int r = 0; r < splits; ++r) {
+                        const float4 v = r == split ? make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3])
+                                                    : cluster_load(parts + (at_tile * NT + n) * 32 + lane, (uint32_t)r);
+                        sum[0] += v.x;
+                        sum[1] += v.y;
+                        sum[2] += v.z;
+                        sum[3] += v.w;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[u][n][c] = sum[c];
                 }
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[n][c] = sum[n][c];
-        } else {
-            good = false;     // another share writes this tile
-        }
+        __syncwarp();
         cluster_sync();
     }
-    if (warp == kTiles || !good) return;
+    if (warp == kWarps || !good) return;
     // 8 channels x 8 tokens at a time: rounded, transposed, 4 bytes a lane
     const int g = lane >> 2, t = lane & 3;
-    const int tile_at = rb * kTiles + warp;
     uint16_t* y = static_cast<uint16_t*>(p.y) + tile.first * p.w.N;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int row = n * 8 + g;
-        if (p.w.paired) {
-            const uint32_t v = transpose8x8(pack_bf16x2(silu(acc[n][0]) * acc[n][2], silu(acc[n][1]) * acc[n][3]));
-            if (row < tile.rows && tile_at * 8 < p.w.N)
-                *reinterpret_cast<uint32_t*>(y + (int64_t)row * p.w.N + tile_at * 8 + 2 * t) = v;
-        } else {
-            const uint32_t v0 = transpose8x8(pack_bf16x2(acc[n][0], acc[n][1]));
-            const uint32_t v1 = transpose8x8(pack_bf16x2(acc[n][2], acc[n][3]));
-            uint16_t* to = y + (int64_t)row * p.w.N + tile_at * 16 + 2 * t;
-            if (row < tile.rows && tile_at * 16 < p.w.N) *reinterpret_cast<uint32_t*>(to) = v0;
-            if (row < tile.rows && tile_at * 16 + 8 < p.w.N) *reinterpret_cast<uint32_t*>(to + 8) = v1;
+    for (int u = 0; u < kOwn; ++u) {
+        const int own = warp * kOwn + u, tile_at = rb * kTiles + own;
+        if (own % splits != split) continue;          // another share writes it
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = n * 8 + g;
+            const float (&v)[4] = acc[u][n];
+            if (p.w.paired) {
+                const uint32_t o = transpose8x8(pack_bf16x2(silu(v[0]) * v[2], silu(v[1]) * v[3]));
+                if (row < tile.rows && tile_at * 8 < p.w.N)
+                    *reinterpret_cast<uint32_t*>(y + (int64_t)row * p.w.N + tile_at * 8 + 2 * t) = o;
+            } else {
+                const uint32_t o0 = transpose8x8(pack_bf16x2(v[0], v[1])), o1 = transpose8x8(pack_bf16x2(v[2], v[3]));
+                uint16_t* to = y + (int64_t)row * p.w.N + tile_at * 16 + 2 * t;
+                if (row < tile.rows && tile_at * 16 < p.w.N) *reinterpret_cast<uint32_t*>(to) = o0;
+                if (row < tile.rows && tile_at * 16 + 8 < p.w.N) *reinterpret_cast<uint32_t*>(to + 8) = o1;
+            }
         }
     }
 }
 
 size_t w4_smem(const W4Shape& w, int nt, bool fp8, int splits) {
     const size_t stage = (size_t)kTiles * tile_bytes(w.group) + 8 * nt * x_pitch(fp8);
-    return kStages * stage + (fp8 ? (size_t)k_blocks(w) * 8 * nt * 4 : 0) + (splits > 1 ? (size_t)kTiles * nt * 32 * 16 : 0);
+    return ring_stages(nt) * stage + (fp8 ? (size_t)k_blocks(w) * 8 * nt * 4 : 0) + (splits > 1 ? (size_t)kTiles * nt * 32 * 16 : 0);
 }
 
 constexpr size_t kMaxSmem = 227 * 1024 - 1024;
@@ -480,7 +552,7 @@ cudaError_t launch_expert_w4(const W4Params& p, int num_sms, cudaStream_t stream
     const int64_t share = p.max_rows / std::min<int64_t>(p.w.E, p.max_rows);
     if (p.max_rows <= 8) return launch_rows<1>(p, num_sms, stream);
     if (share <= 8) return launch_rows<2>(p, num_sms, stream);
-    if (share <= 16) return launch_rows<4>(p, num_sms, stream);
+    if (share <= 32) return launch_rows<4>(p, num_sms, stream);
     return launch_rows<8>(p, num_sms, stream);
 }
 
