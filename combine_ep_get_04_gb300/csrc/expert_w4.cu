@@ -26,9 +26,8 @@ constexpr int kTileRows = 16;      // weight rows of one tile (the matrix instru
 constexpr int kTileK = 128;        // input channels of one tile
 constexpr int kTiles = 8;          // tiles of one step, one for each consumer warp
 constexpr int kCodeBytes = kTileRows * kTileK / 2;
-
-// Steps in flight; the widest form has the fewest, so that two CTAs fit an SM.
-__host__ __device__ constexpr int ring_stages(int nt) { return nt >= 8 ? 3 : 4; }
+constexpr int kStep = 2;           // tiles along K of one stage of the ring
+constexpr int kRing = 2;           // stages
 constexpr int kWarps = 4;          // consumer warps, kOwn tiles each
 constexpr int kOwn = kTiles / kWarps;
 constexpr int kThreads = (kWarps + 1) * 32;
@@ -41,10 +40,12 @@ __host__ __device__ inline int row_tiles(const W4Shape& w) { return w.paired ? (
 __host__ __device__ inline int row_blocks(const W4Shape& w) { return (row_tiles(w) + kTiles - 1) / kTiles; }
 __host__ __device__ inline int k_blocks(const W4Shape& w) { return (w.K + kTileK - 1) / kTileK; }
 
-// Bytes between the 128-channel pieces of two token rows in a stage: 64 (32
-// for fp8) more than a piece, so that the eight rows a warp reads at once
-// fall into different banks.
-__host__ __device__ constexpr int x_pitch(bool fp8) { return fp8 ? 160 : 320; }
+// Bytes between the pieces of two token rows in a stage: 64 (32 for fp8) more
+// than a piece, so that the eight rows a warp reads at once fall into
+// different banks.
+__host__ __device__ constexpr int x_pitch(bool fp8) { return fp8 ? kStep * kTileK + 32 : kStep * kTileK * 2 + 64; }
+__host__ __device__ constexpr int weight_bytes(int group) { return kTiles * tile_bytes(group); }
+__host__ __device__ constexpr int stage_bytes(int group, int nt, bool fp8) { return kStep * weight_bytes(group) + 8 * nt * x_pitch(fp8); }
 
 // One word of codes: 8 input channels of one weight row, channel 2j in bits
 // 4j and channel 2j + 1 in bits 16 + 4j, so that a shift by 4j and a mask
@@ -97,36 +98,41 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Widening a word of codes to four pairs of numbers, (code - 8) * 2^-6 in bf16
-// or (code - 8) * 2^-9 in f16.  Masked out of its half, a code in bits 0-3 or
-// 4-7 is a tiny number as it stands: subnormals and the first binade above
-// them are one linear range, so in bf16 it is code * 2^-133 or code * 2^-129,
-// in f16 code * 2^-24 or code * 2^-20.  One fused multiply-add brings it up
-// and takes 8 off; both steps are exact.  One shift, four masks and four
-// multiply-adds for eight codes: masks and shifts go through the ALU, which is
-// the busiest pipe, so nothing else is left to it.
-template <bool F16>
-__device__ __forceinline__ void widen(uint32_t word, uint32_t (&pair)[4]) {
-    constexpr uint32_t kLow = F16 ? 0x78007800u : 0x7f007f00u;       // 2^15, 2^127
-    constexpr uint32_t kHigh = F16 ? 0x68006800u : 0x7d007d00u;      // 2^11, 2^123
-    constexpr uint32_t kOff = F16 ? 0xa400a400u : 0xbe00be00u;       // -8 * 2^-9, -8 * 2^-6
+// A code masked out of its half of a word, in bits 0-3 or 4-7, is a tiny
+// number as it stands: subnormals and the first binade above them are one
+// linear range, so as f16 it is code * 2^-24 or code * 2^-20, as bf16 code *
+// 2^-133 or code * 2^-129.  One shift and four masks leave the four pairs of
+// a word: 0 and 2 the low, 1 and 3 the high kind.
+__device__ __forceinline__ void unpack(uint32_t word, uint32_t (&pair)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t m = (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
-        if (F16)
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(pair[j]) : "r"(m), "r"(j & 1 ? kHigh : kLow), "r"(kOff));
-        else
-            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(pair[j]) : "r"(m), "r"(j & 1 ? kHigh : kLow), "r"(kOff));
-    }
+    for (int j = 0; j < 4; ++j) pair[j] = (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 
-template <bool F16>
-constexpr float kUnit = F16 ? 512.f : 64.f;      // what the widened codes are divided by
+// Beside bf16 rows one fused multiply-add brings the pairs up to (code - 8) *
+// 2^-6: products with numbers as small as theirs would underflow.  Exact.
+__device__ __forceinline__ void widen(uint32_t (&pair)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)    // by 2^127 or 2^123, less 8 * 2^-6
+        asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(pair[j]) : "r"(j & 1 ? 0x7d007d00u : 0x7f007f00u), "r"(0xbe00be00u));
+}
 
-// Two e4m3 codes -> f16x2, exact.
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
+// Beside fp8 rows the f16 pairs enter the product as they are, the low kind
+// with rows 16 times as large, so that all products are in units of 2^-20;
+// -8 in both units, for the product that takes the offset off.
+constexpr uint32_t kMinusEightLow = 0x80088008u, kMinusEightHigh = 0x80808080u;
+
+template <bool FP8>
+constexpr float kUnit = FP8 ? 1048576.f : 64.f;      // what the codes are divided by
+
+// Four e4m3 codes -> two pairs of f16, exact.
+__device__ __forceinline__ void f16x2_of_e4m3x4(uint32_t codes, uint32_t* lo, uint32_t* hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(*lo), "=r"(*hi) : "r"(codes));
+}
+
+__device__ __forceinline__ uint32_t times16(uint32_t f16x2) {
     uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f16x2), "r"(0x4c004c00u));
     return r;
 }
 
@@ -216,93 +222,119 @@ __device__ __forceinline__ float4 cluster_load(const float4* p, uint32_t rank) {
     return v;
 }
 
-// A consumer warp's walk along K: `steps` steps of the ring, NL x 8 tokens.
-// The accumulators hold sums of scale * (code - 8) / kUnit * x.  False if a
-// wait timed out.
+// One tile step along K (128 channels) of a consumer warp: adds scale * code
+// sums to the accumulators, in units of 1 / kUnit.  wt: the warp's tiles, xr:
+// the lane's place in the first token row, xs: the rows' scales (fp8).
 template <int NT, int NL, int G, bool FP8>
-__device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigned char* smem, const float* xs, uint64_t* full,
-                                        uint64_t* empty, int steps) {
-    constexpr int kWeights = kTiles * tile_bytes(G);
-    constexpr int kRows = 8 * NT;
+__device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsigned char* wt, const unsigned char* xr, const float* xs) {
     constexpr int kPitch = x_pitch(FP8);
-    constexpr int kStage = kWeights + kRows * kPitch;
-    constexpr int kRing = ring_stages(NT);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const unsigned char* own = smem + warp * kOwn * tile_bytes(G);
-    const unsigned char* rows = smem + kWeights + g * kPitch + (FP8 ? 8 : 16) * t;
-    xs += 2 * t;
-    int s = 0;
-    uint32_t parity = 0;
-    for (int step = 0; step < steps; ++step) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], parity))) return false;
-        const unsigned char* wt = own + s * kStage;
-        const unsigned char* xr = rows + s * kStage;
-        uint32_t w[kOwn][2][4];                // [tile][row g, row g + 8][32 channels each]
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    uint32_t w[kOwn][2][4];                // [tile][row g, row g + 8][32 channels each]
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 v = *reinterpret_cast<const uint4*>(wt + u * tile_bytes(G) + h * 512 + lane * 16);
+            w[u][h][0] = v.x;
+            w[u][h][1] = v.y;
+            w[u][h][2] = v.z;
+            w[u][h][3] = v.w;
+        }
+    float part[kOwn][NL][4], eights[NL][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool first = i * 32 % G == 0;
+        // operands of the low and the high pairs: channels 0 1 4 5 and 2 3 6 7 of the lane's eight
+        uint32_t a[kOwn][2][4];
 #pragma unroll
         for (int u = 0; u < kOwn; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint4 v = *reinterpret_cast<const uint4*>(wt + u * tile_bytes(G) + h * 512 + lane * 16);
-                w[u][h][0] = v.x;
-                w[u][h][1] = v.y;
-                w[u][h][2] = v.z;
-                w[u][h][3] = v.w;
+                uint32_t pair[4];
+                unpack(w[u][h][i], pair);
+                if (!FP8) widen(pair);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[u][j & 1][(j >> 1) * 2 + h] = pair[j];
             }
-        float part[kOwn][NL][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t a[kOwn][2][4];            // [tile][16 channels each]
-#pragma unroll
-            for (int u = 0; u < kOwn; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pair[4];
-                    widen<FP8>(w[u][h][i], pair);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) a[u][j >> 1][(j & 1) * 2 + h] = pair[j];
-                }
-#pragma unroll
-            for (int n = 0; n < NL; ++n) {
-                uint32_t b[4];
-                if (FP8) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(xr + n * 8 * kPitch + 32 * i);
-                    b[0] = f16x2_of_e4m3x2(v.x);
-                    b[1] = f16x2_of_e4m3x2(v.x >> 16);
-                    b[2] = f16x2_of_e4m3x2(v.y);
-                    b[3] = f16x2_of_e4m3x2(v.y >> 16);
-                } else {
-                    const uint4 v = *reinterpret_cast<const uint4*>(xr + n * 8 * kPitch + 64 * i);
-                    b[0] = v.x;
-                    b[1] = v.y;
-                    b[2] = v.z;
-                    b[3] = v.w;
-                }
-#pragma unroll
-                for (int u = 0; u < kOwn; ++u) {
-                    float (&d)[4] = part[u][n];
-                    if (i * 32 % G == 0)
-                        mma16816<FP8>(d, a[u][0], b[0], b[1], 0.f, 0.f, 0.f, 0.f);
-                    else
-                        mma16816<FP8>(d, a[u][0], b[0], b[1], d[0], d[1], d[2], d[3]);
-                    mma16816<FP8>(d, a[u][1], b[2], b[3], d[0], d[1], d[2], d[3]);
-                }
+        for (int n = 0; n < NL; ++n) {
+            uint32_t b[4];
+            if (FP8) {
+                const uint2 v = *reinterpret_cast<const uint2*>(xr + n * 8 * kPitch + 32 * i);
+                f16x2_of_e4m3x4(v.x, &b[0], &b[1]);
+                f16x2_of_e4m3x4(v.y, &b[2], &b[3]);
+                b[0] = times16(b[0]);
+                b[2] = times16(b[2]);
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4*>(xr + n * 8 * kPitch + 64 * i);
+                b[0] = v.x;
+                b[1] = v.y;
+                b[2] = v.z;
+                b[3] = v.w;
             }
-            if ((i + 1) * 32 % G == 0) {
+            auto multiply = [&](float (&d)[4], const uint32_t (&low)[4], const uint32_t (&high)[4]) {
+                if (first)
+                    mma16816<FP8>(d, low, b[0], b[2], 0.f, 0.f, 0.f, 0.f);
+                else
+                    mma16816<FP8>(d, low, b[0], b[2], d[0], d[1], d[2], d[3]);
+                mma16816<FP8>(d, high, b[1], b[3], d[0], d[1], d[2], d[3]);
+            };
 #pragma unroll
-                for (int u = 0; u < kOwn; ++u) {
-                    const uint32_t sc = *reinterpret_cast<const uint32_t*>(wt + u * tile_bytes(G) + kCodeBytes + i * 32 / G * 32 + g * 4);
-                    const float s0 = bf16_lo(sc), s1 = bf16_hi(sc);
+            for (int u = 0; u < kOwn; ++u) multiply(part[u][n], a[u][0], a[u][1]);
+            if (FP8) {
+                const uint32_t low[4] = {kMinusEightLow, kMinusEightLow, kMinusEightLow, kMinusEightLow};
+                const uint32_t high[4] = {kMinusEightHigh, kMinusEightHigh, kMinusEightHigh, kMinusEightHigh};
+                multiply(eights[n], low, high);
+            }
+        }
+        if ((i + 1) * 32 % G == 0) {
 #pragma unroll
-                    for (int n = 0; n < NL; ++n) {
-                        float2 q = make_float2(1.f, 1.f);
-                        if (FP8) q = *reinterpret_cast<const float2*>(xs + n * 8);
-                        acc[u][n][0] = fmaf(part[u][n][0], FP8 ? s0 * q.x : s0, acc[u][n][0]);
-                        acc[u][n][1] = fmaf(part[u][n][1], FP8 ? s0 * q.y : s0, acc[u][n][1]);
-                        acc[u][n][2] = fmaf(part[u][n][2], FP8 ? s1 * q.x : s1, acc[u][n][2]);
-                        acc[u][n][3] = fmaf(part[u][n][3], FP8 ? s1 * q.y : s1, acc[u][n][3]);
+            for (int u = 0; u < kOwn; ++u) {
+                const uint32_t sc = *reinterpret_cast<const uint32_t*>(wt + u * tile_bytes(G) + kCodeBytes + i * 32 / G * 32 + g * 4);
+                const float s0 = bf16_lo(sc), s1 = bf16_hi(sc);
+#pragma unroll
+                for (int n = 0; n < NL; ++n) {
+                    float (&v)[4] = acc[u][n];
+                    const float (&d)[4] = part[u][n];
+                    if (FP8) {
+                        const float2 q = *reinterpret_cast<const float2*>(xs + n * 8);
+                        v[0] = fmaf(d[0] + eights[n][0], s0 * q.x, v[0]);
+                        v[1] = fmaf(d[1] + eights[n][1], s0 * q.y, v[1]);
+                        v[2] = fmaf(d[2] + eights[n][2], s1 * q.x, v[2]);
+                        v[3] = fmaf(d[3] + eights[n][3], s1 * q.y, v[3]);
+                    } else {
+                        v[0] = fmaf(d[0], s0, v[0]);
+                        v[1] = fmaf(d[1], s0, v[1]);
+                        v[2] = fmaf(d[2], s1, v[2]);
+                        v[3] = fmaf(d[3], s1, v[3]);
                     }
                 }
             }
+        }
+    }
+}
+
+// A consumer warp's walk along K: `blocks` tile steps, kStep to a stage of the
+// ring, NL x 8 tokens.  False if a wait timed out.
+template <int NT, int NL, int G, bool FP8>
+__device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigned char* smem, const float* xs, uint64_t* full,
+                                        uint64_t* empty, int blocks) {
+    constexpr int kStage = stage_bytes(G, NT, FP8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const unsigned char* own = smem + warp * kOwn * tile_bytes(G);
+    const unsigned char* rows = smem + kStep * weight_bytes(G) + g * x_pitch(FP8) + (FP8 ? 8 : 16) * t;
+    xs += 2 * t;
+    int s = 0;
+    uint32_t parity = 0;
+    for (int left = blocks; left > 0; left -= kStep) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], parity))) return false;
+        const unsigned char* wt = own + s * kStage;
+        const unsigned char* xr = rows + s * kStage;
+#pragma unroll
+        for (int q = 0; q < kStep; ++q) {
+            if (q > 0 && q >= left) break;
+            tile_step<NT, NL, G, FP8>(acc, wt + q * weight_bytes(G), xr + q * kTileK * (FP8 ? 1 : 2), xs);
+            if (FP8) xs += 8 * NT;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
@@ -310,7 +342,6 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
             s = 0;
             parity ^= 1;
         }
-        if (FP8) xs += kRows;
     }
     return true;
 }
@@ -322,13 +353,12 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
 template <int NT, int G, bool FP8>
 __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int splits, int grid_tiles) {
     extern __shared__ __align__(128) unsigned char smem[];
-    constexpr int kRing = ring_stages(NT);
     __shared__ uint64_t full[kRing], empty[kRing];
     __shared__ RowTile shared_tile;
-    constexpr int kWeights = kTiles * tile_bytes(G);
+    constexpr int kWeights = weight_bytes(G);
     constexpr int kRows = 8 * NT;
     constexpr int kPitch = x_pitch(FP8);
-    constexpr int kStage = kWeights + kRows * kPitch;
+    constexpr int kStage = stage_bytes(G, NT, FP8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % splits;
     const int blocks = row_blocks(p.w), nk = k_blocks(p.w);
@@ -375,31 +405,38 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
         for (int n = 0; n < NT; ++n) clear(acc[u][n]);
     if (warp == kWarps) {
         // producer
-        const int size = FP8 ? 1 : 2;
-        const unsigned char* x = static_cast<const unsigned char*>(p.x) + tile.first * p.w.K * size;
+        constexpr int kSize = FP8 ? 1 : 2;
+        const int64_t row_bytes = (int64_t)p.w.K * kSize;
+        const unsigned char* x = static_cast<const unsigned char*>(p.x) + tile.first * row_bytes + (int64_t)kb0 * kTileK * kSize;
+        const unsigned char* weight = weights + (int64_t)kb0 * kWeights;
         int filled = 0;
-        for (int kb = kb0; kb < kb1; ++kb, ++filled) {
+        for (int kb = kb0; kb < kb1; kb += kStep, ++filled) {
             const int s = filled % kRing, round = filled / kRing;
             if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (round - 1) & 1))) {
                 good = false;
                 break;
             }
             unsigned char* st = smem + s * kStage;
-            const uint32_t piece = (uint32_t)(min(p.w.K - kb * kTileK, kTileK) * size);
-            if (piece < kTileK * size) {
+            unsigned char* xt = st + kStep * kWeights;
+            const int blocks_here = min(kStep, kb1 - kb);
+            const uint32_t wanted = blocks_here * kTileK * kSize;
+            const uint32_t piece = min((uint32_t)(p.w.K - kb * kTileK) * kSize, wanted);
+            if (piece < wanted) {
                 // a short last step: zeros stand in for the channels past the end
-                const uint32_t words = (kTileK * size - piece) / 16;
+                const uint32_t words = (wanted - piece) / 16;
                 for (uint32_t i = lane; i < words * tile.rows; i += 32)
-                    *reinterpret_cast<uint4*>(st + kWeights + i / words * kPitch + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(xt + i / words * kPitch + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
                 __syncwarp();
             }
             if (lane == 0) {
-                mbar_arrive_expect_tx(&full[s], kWeights + piece * tile.rows);
-                bulk_load(st, weights + (int64_t)kb * kWeights, kWeights, &full[s]);
+                mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + piece * tile.rows);
+                bulk_load(st, weight, kWeights * blocks_here, &full[s]);
+                const unsigned char* from = x;
+                for (int r = 0; r < tile.rows; ++r, xt += kPitch, from += row_bytes) bulk_load(xt, from, piece, &full[s]);
             }
             __syncwarp();
-            for (int r = lane; r < tile.rows; r += 32)
-                bulk_load(st + kWeights + r * kPitch, x + ((int64_t)r * p.w.K + kb * kTileK) * size, piece, &full[s]);
+            weight += kStep * kWeights;
+            x += kStep * kTileK * kSize;
         }
         if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
         // no copy may be in flight when the CTA ends, whatever its consumers did
@@ -479,8 +516,7 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
 }
 
 size_t w4_smem(const W4Shape& w, int nt, bool fp8, int splits) {
-    const size_t stage = (size_t)kTiles * tile_bytes(w.group) + 8 * nt * x_pitch(fp8);
-    return ring_stages(nt) * stage + (fp8 ? (size_t)k_blocks(w) * 8 * nt * 4 : 0) + (splits > 1 ? (size_t)kTiles * nt * 32 * 16 : 0);
+    return kRing * (size_t)stage_bytes(w.group, nt, fp8) + (fp8 ? (size_t)k_blocks(w) * 8 * nt * 4 : 0) + (splits > 1 ? (size_t)kTiles * nt * 32 * 16 : 0);
 }
 
 constexpr size_t kMaxSmem = 227 * 1024 - 1024;
