@@ -153,8 +153,8 @@ struct RowTile {
     int64_t first;  // its first row
 };
 
-// Rows of expert e that lie inside the buffer.
-__device__ __forceinline__ int expert_rows(const W4Params& p, int e, int64_t* first) {
+// Rows of expert e that lie inside the buffer; a claim beyond it gives none.
+__device__ __forceinline__ int expert_rows(const W4Params& p, int e, int64_t* first, bool* bad) {
     int64_t a, n;
     if (p.mode != 0) {
         a = (int64_t)e * p.capacity;
@@ -166,11 +166,17 @@ __device__ __forceinline__ int expert_rows(const W4Params& p, int e, int64_t* fi
         a = 0;
         n = p.R;
     }
-    const bool bad = n > 0 && (a < 0 || a + n > p.R);
-    if (bad && p.err_flags != nullptr) atomicOr(p.err_flags, kErrBadSlot);
     *first = a;
-    return bad || n < 0 ? 0 : (int)n;
+    *bad = n > 0 && (a < 0 || a + n > p.R);
+    return *bad || n < 0 ? 0 : (int)n;
 }
+
+// tile_rows is a power of two
+__device__ __forceinline__ int tiles_of(int rows, int tile_rows) {
+    return (rows >> (31 - __clz(tile_rows))) + ((rows & (tile_rows - 1)) != 0);
+}
+
+constexpr int kScan = 8;    // experts whose rows a lane looks up at a time: their loads are in flight together
 
 // Tile `at` in the order of experts and of rows within an expert.  One warp;
 // lane l counts the tiles of experts [l * per, (l + 1) * per).
@@ -178,9 +184,18 @@ __device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_
     const int lane = threadIdx.x & 31;
     const int per = (p.w.E + 31) / 32;
     const int e0 = min(lane * per, p.w.E), e1 = min(e0 + per, p.w.E);
-    int64_t first = 0;
     int64_t mine = 0;          // 64 bits: bad offsets may claim every row many times
-    for (int e = e0; e < e1; ++e) mine += (expert_rows(p, e, &first) + tile_rows - 1) / tile_rows;
+    bool any_bad = false;
+    for (int from = e0; from < e1; from += kScan) {
+        int64_t first;
+        bool bad;
+#pragma unroll
+        for (int j = 0; j < kScan; ++j)
+            if (from + j < e1) {
+                mine += tiles_of(expert_rows(p, from + j, &first, &bad), tile_rows);
+                any_bad |= bad;
+            }
+    }
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -188,25 +203,49 @@ __device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_
         if (lane >= d) upto += v;
     }
     const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
-    if (at == 0 && total > grid_tiles && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrCapacity);
+    if (at == 0 && p.err_flags != nullptr) {
+        if (any_bad) atomicOr(p.err_flags, kErrBadSlot);
+        if (total > grid_tiles && lane == 0) atomicOr(p.err_flags, kErrCapacity);
+    }
     RowTile r{-1, 0, 0};
     if (at >= total) return r;
     const int owner = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
     if (lane == owner) {
         int64_t left = at - (upto - mine);
-        for (int e = e0; e < e1; ++e) {
-            const int n = expert_rows(p, e, &first), tiles = (n + tile_rows - 1) / tile_rows;
-            if (left < tiles) {
-                r = RowTile{e, (int)min(n - left * tile_rows, (int64_t)tile_rows), first + left * tile_rows};
-                break;
+        for (int from = e0; from < e1 && r.e < 0; from += kScan) {
+            int64_t first[kScan];
+            int n[kScan];
+            bool bad;
+#pragma unroll
+            for (int j = 0; j < kScan; ++j) n[j] = from + j < e1 ? expert_rows(p, from + j, &first[j], &bad) : 0;
+#pragma unroll
+            for (int j = 0; j < kScan; ++j) {
+                const int tiles = tiles_of(n[j], tile_rows);
+                if (r.e < 0 && left >= 0 && left < tiles)
+                    r = RowTile{from + j, (int)min(n[j] - left * tile_rows, (int64_t)tile_rows), first[j] + left * tile_rows};
+                left -= tiles;
             }
-            left -= tiles;
         }
     }
     r.e = __shfl_sync(0xffffffffu, r.e, owner);
     r.rows = __shfl_sync(0xffffffffu, r.rows, owner);
     r.first = __shfl_sync(0xffffffffu, r.first, owner);
     return r;
+}
+
+// Starts bringing `bytes` (a multiple of 16) at a 16-byte boundary into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// 16 bytes global -> shared, and this thread's arrival on `bar` once all its
+// copies so far have landed (counted in the barrier's arrivals).
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -315,17 +354,15 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
 }
 
 // A consumer warp's walk along K: `blocks` tile steps, kStep to a stage of the
-// ring, NL x 8 tokens.  False if a wait timed out.
+// ring from stage s on, NL x 8 tokens.  False if a wait timed out.
 template <int NT, int NL, int G, bool FP8>
 __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigned char* smem, const float* xs, uint64_t* full,
-                                        uint64_t* empty, int blocks) {
+                                        uint64_t* empty, int blocks, int& s, uint32_t& parity) {
     constexpr int kStage = stage_bytes(G, NT, FP8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const unsigned char* own = smem + warp * kOwn * tile_bytes(G);
     const unsigned char* rows = smem + kStep * weight_bytes(G) + g * x_pitch(FP8) + (FP8 ? 8 : 16) * t;
     xs += 2 * t;
-    int s = 0;
-    uint32_t parity = 0;
     for (int left = blocks; left > 0; left -= kStep) {
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], parity))) return false;
         const unsigned char* wt = own + s * kStage;
@@ -346,12 +383,13 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
     return true;
 }
 
-// One CTA: one row block (128 weight rows) x one tile of up to 8 NT token rows
-// x one of `splits` shares of K.  The shares of a product form a cluster and
-// add their accumulators through distributed shared memory in the order of
-// the shares.
+// One CTA: `units` row blocks (128 weight rows each) of one tile of up to 8 NT
+// token rows, over one of `splits` shares of K.  The ring runs on from one row
+// block to the next.  The shares of a product form a cluster (of one row block
+// each) and add their accumulators through distributed shared memory in the
+// order of the shares.
 template <int NT, int G, bool FP8>
-__global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int splits, int grid_tiles) {
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : NT == 4 ? 2 : 1) expert_w4_kernel(W4Params p, int splits, int units, int grid_tiles) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kRing], empty[kRing];
     __shared__ RowTile shared_tile;
@@ -359,14 +397,20 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
     constexpr int kRows = 8 * NT;
     constexpr int kPitch = x_pitch(FP8);
     constexpr int kStage = stage_bytes(G, NT, FP8);
+    // a few rows go by one bulk copy each; many would queue up behind one another
+    constexpr bool kRowCopies = NT <= 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % splits;
-    const int blocks = row_blocks(p.w), nk = k_blocks(p.w);
-    const int rb = blockIdx.x / splits % blocks, at = blockIdx.x / splits / blocks;
+    const int blocks = row_blocks(p.w), nk = k_blocks(p.w), parts_of = (blocks + units - 1) / units;
+    const int rb0 = blockIdx.x / splits % parts_of * units, rb1 = min(rb0 + units, blocks), at = blockIdx.x / splits / parts_of;
+    const int kb0 = (int)((int64_t)nk * split / splits), kb1 = (int)((int64_t)nk * (split + 1) / splits);
+    const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + ((int64_t)rb0 * nk + kb0) * kWeights;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
+        // a single matrix: its first steps are known before the rows are
+        if (p.w.E == 1) prefetch_l2(weights, (uint32_t)min(kb1 - kb0, kRing * kStep) * kWeights);
         for (int s = 0; s < kRing; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], kRowCopies ? 1 : 33);
             mbar_init(&empty[s], kWarps);
         }
         fence_mbar_init();
@@ -379,8 +423,7 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
     __syncthreads();
     const RowTile tile = shared_tile;
     if (tile.e < 0) return;              // the same in all CTAs of a cluster
-    const int kb0 = (int)((int64_t)nk * split / splits), kb1 = (int)((int64_t)nk * (split + 1) / splits);
-    const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + (((int64_t)tile.e * blocks + rb) * nk) * kWeights;
+    weights += (int64_t)tile.e * blocks * nk * kWeights;
     float* xs = reinterpret_cast<float*>(smem + kRing * kStage);          // [k block][kRows] (fp8)
     float4* parts = reinterpret_cast<float4*>(smem + kRing * kStage + (FP8 ? (int64_t)nk * kRows * 4 : 0));   // [kTiles][NT][32]
     if (FP8) {
@@ -389,63 +432,83 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
             float s = 0.f;
             if (r < tile.rows) {
                 const int64_t from = (tile.first + r) * nk + kb;
-                s = p.ue8m0 ? __uint_as_float((uint32_t) static_cast<const uint8_t*>(p.x_scales)[from] << 23)
-                            : static_cast<const float*>(p.x_scales)[from];
-                if (p.ue8m0 && static_cast<const uint8_t*>(p.x_scales)[from] == 0) s = __uint_as_float(0x00400000u);   // 2^-127
+                if (p.ue8m0) {
+                    const uint32_t e = static_cast<const uint8_t*>(p.x_scales)[from];
+                    s = __uint_as_float(e == 0 ? 0x00400000u : e << 23);      // 0 is 2^-127, a subnormal
+                } else {
+                    s = static_cast<const float*>(p.x_scales)[from];
+                }
             }
             xs[i] = s;
         }
         __syncthreads();
     }
-    bool good = true;
-    float acc[kOwn][NT][4];
-#pragma unroll
-    for (int u = 0; u < kOwn; ++u)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) clear(acc[u][n]);
     if (warp == kWarps) {
         // producer
         constexpr int kSize = FP8 ? 1 : 2;
         const int64_t row_bytes = (int64_t)p.w.K * kSize;
-        const unsigned char* x = static_cast<const unsigned char*>(p.x) + tile.first * row_bytes + (int64_t)kb0 * kTileK * kSize;
-        const unsigned char* weight = weights + (int64_t)kb0 * kWeights;
+        const unsigned char* x = static_cast<const unsigned char*>(p.x) + tile.first * row_bytes;
+        bool good = true;
         int filled = 0;
-        for (int kb = kb0; kb < kb1; kb += kStep, ++filled) {
-            const int s = filled % kRing, round = filled / kRing;
-            if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (round - 1) & 1))) {
-                good = false;
-                break;
-            }
-            unsigned char* st = smem + s * kStage;
-            unsigned char* xt = st + kStep * kWeights;
-            const int blocks_here = min(kStep, kb1 - kb);
-            const uint32_t wanted = blocks_here * kTileK * kSize;
-            const uint32_t piece = min((uint32_t)(p.w.K - kb * kTileK) * kSize, wanted);
-            if (piece < wanted) {
-                // a short last step: zeros stand in for the channels past the end
-                const uint32_t words = (wanted - piece) / 16;
-                for (uint32_t i = lane; i < words * tile.rows; i += 32)
-                    *reinterpret_cast<uint4*>(xt + i / words * kPitch + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
+        for (int rb = rb0; rb < rb1 && good; ++rb) {
+            const unsigned char* weight = weights + (int64_t)(rb - rb0) * nk * kWeights;
+            for (int kb = kb0; kb < kb1; kb += kStep, ++filled) {
+                const int s = filled % kRing, round = filled / kRing;
+                if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (round - 1) & 1))) {
+                    good = false;
+                    break;
+                }
+                unsigned char* st = smem + s * kStage;
+                unsigned char* xt = st + kStep * kWeights;
+                const int blocks_here = min(kStep, kb1 - kb);
+                const uint32_t wanted = blocks_here * kTileK * kSize;
+                const uint32_t piece = min((uint32_t)(p.w.K - kb * kTileK) * kSize, wanted);
+                if (piece < wanted) {
+                    // a short last step: zeros stand in for the channels past the end
+                    const uint32_t words = (wanted - piece) / 16;
+                    for (uint32_t i = lane; i < words * tile.rows; i += 32)
+                        *reinterpret_cast<uint4*>(xt + i / words * kPitch + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
+                    __syncwarp();
+                }
+                const unsigned char* from = x + (int64_t)kb * kTileK * kSize;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + (kRowCopies ? piece * tile.rows : 0));
+                    bulk_load(st, weight, kWeights * blocks_here, &full[s]);
+                    if (kRowCopies)
+                        for (int r = 0; r < tile.rows; ++r, xt += kPitch, from += row_bytes) bulk_load(xt, from, piece, &full[s]);
+                }
+                if (!kRowCopies) {
+                    for (int r = 0; r < tile.rows; ++r, xt += kPitch, from += row_bytes)
+                        for (uint32_t c = lane * 16; c < piece; c += 512) copy16_async(xt + c, from + c);
+                    copies_arrive(&full[s]);
+                }
                 __syncwarp();
+                weight += kStep * kWeights;
             }
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + piece * tile.rows);
-                bulk_load(st, weight, kWeights * blocks_here, &full[s]);
-                const unsigned char* from = x;
-                for (int r = 0; r < tile.rows; ++r, xt += kPitch, from += row_bytes) bulk_load(xt, from, piece, &full[s]);
-            }
-            __syncwarp();
-            weight += kStep * kWeights;
-            x += kStep * kTileK * kSize;
         }
         if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
         // no copy may be in flight when the CTA ends, whatever its consumers did
         for (int i = max(0, filled - kRing); i < filled; ++i) mbar_wait(&full[i % kRing], (i / kRing) & 1);
-    } else {
+        __syncwarp();
+        if (splits > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
+    bool good = true;
+    int stage = 0;
+    uint32_t parity = 0;
+    for (int rb = rb0; rb < rb1 && good; ++rb) {
+        float acc[kOwn][NT][4];
+#pragma unroll
+        for (int u = 0; u < kOwn; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) clear(acc[u][n]);
         // tiles that are at most half full take the form made for that
         constexpr int kHalf = NT > 1 ? NT / 2 : 1;
-        good = tile.rows <= 8 * kHalf ? consume<NT, kHalf, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0)
-                                      : consume<NT, NT, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0);
+        good = tile.rows <= 8 * kHalf ? consume<NT, kHalf, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0, stage, parity)
+                                      : consume<NT, NT, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0, stage, parity);
         if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
 #pragma unroll
         for (int u = 0; u < kOwn; ++u)
@@ -453,63 +516,61 @@ __global__ void __launch_bounds__(kThreads) expert_w4_kernel(W4Params p, int spl
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[u][n][c] *= kUnit<FP8>;      // a power of two
-    }
-    if (splits > 1) {
-        // share i adds up the tiles i, i + splits, ...
-        if (warp < kWarps)
+        if (splits > 1) {
+            // share i adds up the tiles i, i + splits, ...
 #pragma unroll
-            for (int u = 0; u < kOwn; ++u)
-                if ((warp * kOwn + u) % splits != split)
+                for (int u = 0; u < kOwn; ++u)
+                    if ((warp * kOwn + u) % splits != split)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        parts[((warp * kOwn + u) * NT + n) * 32 + lane] = make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3]);
-        __syncwarp();
-        cluster_sync();
-        if (warp < kWarps)
+                        for (int n = 0; n < NT; ++n)
+                            parts[((warp * kOwn + u) * NT + n) * 32 + lane] = make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3]);
+            __syncwarp();
+            cluster_sync();
 #pragma unroll
-            for (int u = 0; u < kOwn; ++u) {
-                const int at_tile = warp * kOwn + u;
-                if (at_tile % splits != split) continue;
+                for (int u = 0; u < kOwn; ++u) {
+                    const int at_tile = warp * kOwn + u;
+                    if (at_tile % splits != split) continue;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float sum[4];
-                    clear(sum);
-                    for (int r = 0; r < splits; ++r) {
-                        const float4 v = r == split ? make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3])
-                                                    : cluster_load(parts + (at_tile * NT + n) * 32 + lane, (uint32_t)r);
-                        sum[0] += v.x;
-                        sum[1] += v.y;
-                        sum[2] += v.z;
-                        sum[3] += v.w;
+                    for (int n = 0; n < NT; ++n) {
+                        float sum[4];
+                        clear(sum);
+                        for (int r = 0; r < splits; ++r) {
+                            const float4 v = r == split ? make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3])
+                                                        : cluster_load(parts + (at_tile * NT + n) * 32 + lane, (uint32_t)r);
+                            sum[0] += v.x;
+                            sum[1] += v.y;
+                            sum[2] += v.z;
+                            sum[3] += v.w;
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[u][n][c] = sum[c];
                     }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[u][n][c] = sum[c];
                 }
-            }
-        __syncwarp();
-        cluster_sync();
-    }
-    if (warp == kWarps || !good) return;
-    // 8 channels x 8 tokens at a time: rounded, transposed, 4 bytes a lane
-    const int g = lane >> 2, t = lane & 3;
-    uint16_t* y = static_cast<uint16_t*>(p.y) + tile.first * p.w.N;
+            __syncwarp();
+            cluster_sync();
+        }
+        if (!good) break;
+        // 8 channels x 8 tokens at a time: rounded, transposed, 4 bytes a lane
+        const int g = lane >> 2, t = lane & 3;
+        uint16_t* y = static_cast<uint16_t*>(p.y) + tile.first * p.w.N;
 #pragma unroll
-    for (int u = 0; u < kOwn; ++u) {
-        const int own = warp * kOwn + u, tile_at = rb * kTiles + own;
-        if (own % splits != split) continue;          // another share writes it
+        for (int u = 0; u < kOwn; ++u) {
+            const int own = warp * kOwn + u, tile_at = rb * kTiles + own;
+            if (own % splits != split) continue;          // another share writes it
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int row = n * 8 + g;
-            const float (&v)[4] = acc[u][n];
-            if (p.w.paired) {
-                const uint32_t o = transpose8x8(pack_bf16x2(silu(v[0]) * v[2], silu(v[1]) * v[3]));
-                if (row < tile.rows && tile_at * 8 < p.w.N)
-                    *reinterpret_cast<uint32_t*>(y + (int64_t)row * p.w.N + tile_at * 8 + 2 * t) = o;
-            } else {
-                const uint32_t o0 = transpose8x8(pack_bf16x2(v[0], v[1])), o1 = transpose8x8(pack_bf16x2(v[2], v[3]));
-                uint16_t* to = y + (int64_t)row * p.w.N + tile_at * 16 + 2 * t;
-                if (row < tile.rows && tile_at * 16 < p.w.N) *reinterpret_cast<uint32_t*>(to) = o0;
-                if (row < tile.rows && tile_at * 16 + 8 < p.w.N) *reinterpret_cast<uint32_t*>(to + 8) = o1;
+            for (int n = 0; n < NT; ++n) {
+                const int row = n * 8 + g;
+                const float (&v)[4] = acc[u][n];
+                if (p.w.paired) {
+                    const uint32_t o = transpose8x8(pack_bf16x2(silu(v[0]) * v[2], silu(v[1]) * v[3]));
+                    if (row < tile.rows && tile_at * 8 < p.w.N)
+                        *reinterpret_cast<uint32_t*>(y + (int64_t)row * p.w.N + tile_at * 8 + 2 * t) = o;
+                } else {
+                    const uint32_t o0 = transpose8x8(pack_bf16x2(v[0], v[1])), o1 = transpose8x8(pack_bf16x2(v[2], v[3]));
+                    uint16_t* to = y + (int64_t)row * p.w.N + tile_at * 16 + 2 * t;
+                    if (row < tile.rows && tile_at * 16 < p.w.N) *reinterpret_cast<uint32_t*>(to) = o0;
+                    if (row < tile.rows && tile_at * 16 + 8 < p.w.N) *reinterpret_cast<uint32_t*>(to + 8) = o1;
+                }
             }
         }
     }
@@ -522,13 +583,13 @@ size_t w4_smem(const W4Shape& w, int nt, bool fp8, int splits) {
 constexpr size_t kMaxSmem = 227 * 1024 - 1024;
 
 template <int NT, int G, bool FP8>
-cudaError_t launch_form(const W4Params& p, int splits, int64_t tiles, cudaStream_t stream) {
+cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles, cudaStream_t stream) {
     auto kern = expert_w4_kernel<NT, G, FP8>;
     const size_t smem = w4_smem(p.w, NT, FP8, splits);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * row_blocks(p.w) * splits));
+    cfg.gridDim = dim3((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -541,25 +602,28 @@ cudaError_t launch_form(const W4Params& p, int splits, int64_t tiles, cudaStream
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, splits, (int)tiles);
+    return cudaLaunchKernelEx(&cfg, kern, p, splits, units, (int)tiles);
 }
 
 template <int NT, bool FP8>
-cudaError_t launch_group(const W4Params& p, int splits, int64_t tiles, cudaStream_t stream) {
-    if (p.w.group == 32) return launch_form<NT, 32, FP8>(p, splits, tiles, stream);
-    if (p.w.group == 64) return launch_form<NT, 64, FP8>(p, splits, tiles, stream);
-    return launch_form<NT, 128, FP8>(p, splits, tiles, stream);
+cudaError_t launch_group(const W4Params& p, int splits, int units, int64_t tiles, cudaStream_t stream) {
+    if (p.w.group == 32) return launch_form<NT, 32, FP8>(p, splits, units, tiles, stream);
+    if (p.w.group == 64) return launch_form<NT, 64, FP8>(p, splits, units, tiles, stream);
+    return launch_form<NT, 128, FP8>(p, splits, units, tiles, stream);
 }
 
 template <int NT>
 cudaError_t launch_rows(const W4Params& p, int num_sms, cudaStream_t stream) {
     // every row in a tile of its expert: full tiles, and a last one for each expert in use
     const int64_t tiles = std::min<int64_t>(p.w.E, p.max_rows) + p.max_rows / (8 * NT);
+    const int64_t products = std::min<int64_t>(p.w.E, p.max_rows) * row_blocks(p.w);
     // few products: share K among the CTAs of a cluster until there are about two CTAs for every SM
     int splits = 1;
-    while (splits < 8 && std::min<int64_t>(p.w.E, p.max_rows) * row_blocks(p.w) * splits < 2 * num_sms && k_blocks(p.w) >= 4 * splits)
-        splits *= 2;
-    return p.fp8 ? launch_group<NT, true>(p, splits, tiles, stream) : launch_group<NT, false>(p, splits, tiles, stream);
+    while (splits < 8 && products * splits < 2 * num_sms && k_blocks(p.w) >= 4 * splits) splits *= 2;
+    // many short ones: several to a CTA, for at least 64 steps of K, as long as 16 CTAs for every SM remain
+    int units = 1;
+    while (units * k_blocks(p.w) < 64 && products >= 32 * (int64_t)num_sms * units) units *= 2;
+    return p.fp8 ? launch_group<NT, true>(p, splits, units, tiles, stream) : launch_group<NT, false>(p, splits, units, tiles, stream);
 }
 
 }  // namespace
