@@ -15,6 +15,7 @@
 // group's products are summed unscaled in fp32 and enter the accumulator
 // through one fused multiply-add with the group's scale.
 #include <algorithm>
+#include <cuda.h>
 
 #include "ep_device.cuh"
 #include "ep_kernels.h"
@@ -40,12 +41,23 @@ __host__ __device__ inline int row_tiles(const W4Shape& w) { return w.paired ? (
 __host__ __device__ inline int row_blocks(const W4Shape& w) { return (row_tiles(w) + kTiles - 1) / kTiles; }
 __host__ __device__ inline int k_blocks(const W4Shape& w) { return (w.K + kTileK - 1) / kTileK; }
 
-// Bytes between the pieces of two token rows in a stage: 64 (32 for fp8) more
-// than a piece, so that the eight rows a warp reads at once fall into
-// different banks.
-__host__ __device__ constexpr int x_pitch(bool fp8) { return fp8 ? kStep * kTileK + 32 : kStep * kTileK * 2 + 64; }
+// Token rows in a stage.  A few rows come by one bulk copy each, every row's
+// piece 64 bytes (32 for fp8) longer than it is; more rows come as boxes of 32
+// channels, [channels / 32][rows][32 channels], by tensor copies, whose number
+// does not grow with the rows.  Either way the eight rows that a warp reads at
+// once fall into different banks.
+__host__ __device__ constexpr bool x_boxes(int nt) { return nt > 2; }
+__host__ __device__ constexpr int x_row(int nt, bool fp8) {       // from one row to the next
+    return x_boxes(nt) ? (fp8 ? 32 : 64) : fp8 ? kStep * kTileK + 32 : kStep * kTileK * 2 + 64;
+}
+__host__ __device__ constexpr int x_chunk(int nt, bool fp8) {     // from 32 channels to the next
+    return x_boxes(nt) ? 8 * nt * x_row(nt, fp8) : fp8 ? 32 : 64;
+}
+__host__ __device__ constexpr int x_bytes(int nt, bool fp8) {
+    return x_boxes(nt) ? kStep * kTileK / 32 * x_chunk(nt, fp8) : 8 * nt * x_row(nt, fp8);
+}
 __host__ __device__ constexpr int weight_bytes(int group) { return kTiles * tile_bytes(group); }
-__host__ __device__ constexpr int stage_bytes(int group, int nt, bool fp8) { return kStep * weight_bytes(group) + 8 * nt * x_pitch(fp8); }
+__host__ __device__ constexpr int stage_bytes(int group, int nt, bool fp8) { return kStep * weight_bytes(group) + x_bytes(nt, fp8); }
 
 // One word of codes: 8 input channels of one weight row, channel 2j in bits
 // 4j and channel 2j + 1 in bits 16 + 4j, so that a shift by 4j and a mask
@@ -186,15 +198,23 @@ __device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_
     const int e0 = min(lane * per, p.w.E), e1 = min(e0 + per, p.w.E);
     int64_t mine = 0;          // 64 bits: bad offsets may claim every row many times
     bool any_bad = false;
-    for (int from = e0; from < e1; from += kScan) {
-        int64_t first;
-        bool bad;
+    int64_t first[kScan];
+    int n[kScan];
+    auto look_up = [&](int from) {
+        bool bad[kScan];
 #pragma unroll
-        for (int j = 0; j < kScan; ++j)
-            if (from + j < e1) {
-                mine += tiles_of(expert_rows(p, from + j, &first, &bad), tile_rows);
-                any_bad |= bad;
-            }
+        for (int j = 0; j < kScan; ++j) {
+            n[j] = 0;
+            bad[j] = false;
+            if (from + j < e1) n[j] = expert_rows(p, from + j, &first[j], &bad[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kScan; ++j) any_bad |= bad[j];
+    };
+    for (int from = e0; from < e1; from += kScan) {
+        look_up(from);
+#pragma unroll
+        for (int j = 0; j < kScan; ++j) mine += tiles_of(n[j], tile_rows);
     }
     int64_t upto = mine;
 #pragma unroll
@@ -213,11 +233,7 @@ __device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_
     if (lane == owner) {
         int64_t left = at - (upto - mine);
         for (int from = e0; from < e1 && r.e < 0; from += kScan) {
-            int64_t first[kScan];
-            int n[kScan];
-            bool bad;
-#pragma unroll
-            for (int j = 0; j < kScan; ++j) n[j] = from + j < e1 ? expert_rows(p, from + j, &first[j], &bad) : 0;
+            if (per > kScan) look_up(from);       // else n still holds them all
 #pragma unroll
             for (int j = 0; j < kScan; ++j) {
                 const int tiles = tiles_of(n[j], tile_rows);
@@ -238,27 +254,22 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
-// 16 bytes global -> shared, and this thread's arrival on `bar` once all its
-// copies so far have landed (counted in the barrier's arrivals).
-__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Reads a float of the same place in another CTA's shared memory.
-__device__ __forceinline__ float4 cluster_load(const float4* p, uint32_t rank) {
+// Writes to the same place in another CTA's shared memory.
+__device__ __forceinline__ void cluster_store(const float4* p, uint32_t rank, const float (&v)[4]) {
     uint32_t a;
-    float4 v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+
+// A box of 32 channels x 8 NT rows, completion counted in bytes on `bar`.
+__device__ __forceinline__ void box_load(void* dst, const CUtensorMap* map, int channel, int row, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(map), "r"(channel), "r"(row), "r"(smem_addr(bar))
+                 : "memory");
 }
 
 // One tile step along K (128 channels) of a consumer warp: adds scale * code
@@ -266,7 +277,7 @@ __device__ __forceinline__ float4 cluster_load(const float4* p, uint32_t rank) {
 // the lane's place in the first token row, xs: the rows' scales (fp8).
 template <int NT, int NL, int G, bool FP8>
 __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsigned char* wt, const unsigned char* xr, const float* xs) {
-    constexpr int kPitch = x_pitch(FP8);
+    constexpr int kTile = 8 * x_row(NT, FP8), kChunk = x_chunk(NT, FP8);
     const int lane = threadIdx.x & 31, g = lane >> 2;
     uint32_t w[kOwn][2][4];                // [tile][row g, row g + 8][32 channels each]
 #pragma unroll
@@ -299,13 +310,13 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
         for (int n = 0; n < NL; ++n) {
             uint32_t b[4];
             if (FP8) {
-                const uint2 v = *reinterpret_cast<const uint2*>(xr + n * 8 * kPitch + 32 * i);
+                const uint2 v = *reinterpret_cast<const uint2*>(xr + n * kTile + i * kChunk);
                 f16x2_of_e4m3x4(v.x, &b[0], &b[1]);
                 f16x2_of_e4m3x4(v.y, &b[2], &b[3]);
                 b[0] = times16(b[0]);
                 b[2] = times16(b[2]);
             } else {
-                const uint4 v = *reinterpret_cast<const uint4*>(xr + n * 8 * kPitch + 64 * i);
+                const uint4 v = *reinterpret_cast<const uint4*>(xr + n * kTile + i * kChunk);
                 b[0] = v.x;
                 b[1] = v.y;
                 b[2] = v.z;
@@ -361,16 +372,18 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
     constexpr int kStage = stage_bytes(G, NT, FP8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const unsigned char* own = smem + warp * kOwn * tile_bytes(G);
-    const unsigned char* rows = smem + kStep * weight_bytes(G) + g * x_pitch(FP8) + (FP8 ? 8 : 16) * t;
+    const unsigned char* rows = smem + kStep * weight_bytes(G) + g * x_row(NT, FP8) + (FP8 ? 8 : 16) * t;
     xs += 2 * t;
     for (int left = blocks; left > 0; left -= kStep) {
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], parity))) return false;
         const unsigned char* wt = own + s * kStage;
         const unsigned char* xr = rows + s * kStage;
-#pragma unroll
-        for (int q = 0; q < kStep; ++q) {
-            if (q > 0 && q >= left) break;
-            tile_step<NT, NL, G, FP8>(acc, wt + q * weight_bytes(G), xr + q * kTileK * (FP8 ? 1 : 2), xs);
+        // not unrolled: a short product runs this code from a cold instruction cache
+#pragma unroll 1
+        for (int q = min(left, kStep); q > 0; --q) {
+            tile_step<NT, NL, G, FP8>(acc, wt, xr, xs);
+            wt += weight_bytes(G);
+            xr += kTileK / 32 * x_chunk(NT, FP8);
             if (FP8) xs += 8 * NT;
         }
         __syncwarp();
@@ -389,16 +402,14 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
 // each) and add their accumulators through distributed shared memory in the
 // order of the shares.
 template <int NT, int G, bool FP8>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : NT == 4 ? 2 : 1) expert_w4_kernel(W4Params p, int splits, int units, int grid_tiles) {
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 2) expert_w4_kernel(W4Params p, const __grid_constant__ CUtensorMap rows_map, int splits, int units,
+                                                                                    int grid_tiles) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kRing], empty[kRing];
     __shared__ RowTile shared_tile;
     constexpr int kWeights = weight_bytes(G);
     constexpr int kRows = 8 * NT;
-    constexpr int kPitch = x_pitch(FP8);
     constexpr int kStage = stage_bytes(G, NT, FP8);
-    // a few rows go by one bulk copy each; many would queue up behind one another
-    constexpr bool kRowCopies = NT <= 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % splits;
     const int blocks = row_blocks(p.w), nk = k_blocks(p.w), parts_of = (blocks + units - 1) / units;
@@ -410,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : NT == 4 ? 2 : 1) exper
         // a single matrix: its first steps are known before the rows are
         if (p.w.E == 1) prefetch_l2(weights, (uint32_t)min(kb1 - kb0, kRing * kStep) * kWeights);
         for (int s = 0; s < kRing; ++s) {
-            mbar_init(&full[s], kRowCopies ? 1 : 33);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], kWarps);
         }
         fence_mbar_init();
@@ -421,8 +432,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : NT == 4 ? 2 : 1) exper
         if (lane == 0) shared_tile = r;
     }
     __syncthreads();
+    if (splits > 1) cluster_arrive();
     const RowTile tile = shared_tile;
-    if (tile.e < 0) return;              // the same in all CTAs of a cluster
+    if (tile.e < 0) {                    // the same in all CTAs of a cluster
+        if (splits > 1) cluster_wait();
+        return;
+    }
     weights += (int64_t)tile.e * blocks * nk * kWeights;
     float* xs = reinterpret_cast<float*>(smem + kRing * kStage);          // [k block][kRows] (fp8)
     float4* parts = reinterpret_cast<float4*>(smem + kRing * kStage + (FP8 ? (int64_t)nk * kRows * 4 : 0));   // [kTiles][NT][32]
@@ -463,24 +478,31 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : NT == 4 ? 2 : 1) exper
                 const int blocks_here = min(kStep, kb1 - kb);
                 const uint32_t wanted = blocks_here * kTileK * kSize;
                 const uint32_t piece = min((uint32_t)(p.w.K - kb * kTileK) * kSize, wanted);
-                if (piece < wanted) {
-                    // a short last step: zeros stand in for the channels past the end
-                    const uint32_t words = (wanted - piece) / 16;
-                    for (uint32_t i = lane; i < words * tile.rows; i += 32)
-                        *reinterpret_cast<uint4*>(xt + i / words * kPitch + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
-                    __syncwarp();
-                }
-                const unsigned char* from = x + (int64_t)kb * kTileK * kSize;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + (kRowCopies ? piece * tile.rows : 0));
-                    bulk_load(st, weight, kWeights * blocks_here, &full[s]);
-                    if (kRowCopies)
-                        for (int r = 0; r < tile.rows; ++r, xt += kPitch, from += row_bytes) bulk_load(xt, from, piece, &full[s]);
-                }
-                if (!kRowCopies) {
-                    for (int r = 0; r < tile.rows; ++r, xt += kPitch, from += row_bytes)
-                        for (uint32_t c = lane * 16; c < piece; c += 512) copy16_async(xt + c, from + c);
-                    copies_arrive(&full[s]);
+                if (x_boxes(NT)) {
+                    // rows past the buffer and channels past the rows' end arrive as zeros
+                    if (lane == 0) {
+                        constexpr int kBox = x_chunk(NT, FP8);
+                        const int boxes = blocks_here * (kTileK / 32);
+                        mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + boxes * kBox);
+                        bulk_load(st, weight, kWeights * blocks_here, &full[s]);
+                        for (int i = 0; i < boxes; ++i)
+                            box_load(xt + i * kBox, &rows_map, kb * kTileK + i * 32, (int)tile.first, &full[s]);
+                    }
+                } else {
+                    constexpr int kRow = x_row(NT, FP8);
+                    if (piece < wanted) {
+                        // a short last step: zeros stand in for the channels past the end
+                        const uint32_t words = (wanted - piece) / 16;
+                        for (uint32_t i = lane; i < words * tile.rows; i += 32)
+                            *reinterpret_cast<uint4*>(xt + i / words * kRow + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + piece * tile.rows);
+                        bulk_load(st, weight, kWeights * blocks_here, &full[s]);
+                        const unsigned char* from = x + (int64_t)kb * kTileK * kSize;
+                        for (int r = 0; r < tile.rows; ++r, xt += kRow, from += row_bytes) bulk_load(xt, from, piece, &full[s]);
+                    }
                 }
                 __syncwarp();
                 weight += kStep * kWeights;
@@ -491,8 +513,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : NT == 4 ? 2 : 1) exper
         for (int i = max(0, filled - kRing); i < filled; ++i) mbar_wait(&full[i % kRing], (i / kRing) & 1);
         __syncwarp();
         if (splits > 1) {
-            cluster_sync();
-            cluster_sync();
+            cluster_wait();
+            cluster_arrive();
+            cluster_wait();
         }
         return;
     }
@@ -517,37 +540,37 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : NT == 4 ? 2 : 1) exper
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[u][n][c] *= kUnit<FP8>;      // a power of two
         if (splits > 1) {
-            // share i adds up the tiles i, i + splits, ...
+            // share i adds up the tiles i, i + splits, ...: the others send it theirs
+            const int owned = kTiles / splits;
+            cluster_wait();                    // all CTAs of the cluster have started
 #pragma unroll
-                for (int u = 0; u < kOwn; ++u)
-                    if ((warp * kOwn + u) % splits != split)
+            for (int u = 0; u < kOwn; ++u) {
+                const int own = warp * kOwn + u;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            parts[((warp * kOwn + u) * NT + n) * 32 + lane] = make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3]);
+                for (int n = 0; n < NT; ++n)
+                    cluster_store(parts + ((split * owned + own / splits) * NT + n) * 32 + lane, (uint32_t)(own % splits), acc[u][n]);
+            }
             __syncwarp();
-            cluster_sync();
+            cluster_arrive();
+            cluster_wait();
 #pragma unroll
-                for (int u = 0; u < kOwn; ++u) {
-                    const int at_tile = warp * kOwn + u;
-                    if (at_tile % splits != split) continue;
+            for (int u = 0; u < kOwn; ++u) {
+                const int own = warp * kOwn + u;
+                if (own % splits != split) continue;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float sum[4];
-                        clear(sum);
-                        for (int r = 0; r < splits; ++r) {
-                            const float4 v = r == split ? make_float4(acc[u][n][0], acc[u][n][1], acc[u][n][2], acc[u][n][3])
-                                                        : cluster_load(parts + (at_tile * NT + n) * 32 + lane, (uint32_t)r);
-                            sum[0] += v.x;
-                            sum[1] += v.y;
-                            sum[2] += v.z;
-                            sum[3] += v.w;
-                        }
+                for (int n = 0; n < NT; ++n) {
+                    clear(acc[u][n]);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[u][n][c] = sum[c];
+                    for (int r = 0; r < 8; ++r) {
+                        if (r >= splits) break;
+                        const float4 v = parts[((r * owned + own / splits) * NT + n) * 32 + lane];
+                        acc[u][n][0] += v.x;
+                        acc[u][n][1] += v.y;
+                        acc[u][n][2] += v.z;
+                        acc[u][n][3] += v.w;
                     }
                 }
-            __syncwarp();
-            cluster_sync();
+            }
         }
         if (!good) break;
         // 8 channels x 8 tokens at a time: rounded, transposed, 4 bytes a lane
@@ -582,12 +605,39 @@ size_t w4_smem(const W4Shape& w, int nt, bool fp8, int splits) {
 
 constexpr size_t kMaxSmem = 227 * 1024 - 1024;
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Describes x [R, K] for copies of 32 channels x `rows` rows.
+cudaError_t describe_rows(const W4Params& p, int rows, CUtensorMap* map) {
+    static const EncodeFn encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(f) : nullptr;
+    }();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t size = p.fp8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.w.K, (cuuint64_t)p.R}, strides[1] = {(cuuint64_t)p.w.K * size};
+    const cuuint32_t box[2] = {32, (cuuint32_t)rows}, steps[2] = {1, 1};
+    const CUresult r = encode(map, p.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                              const_cast<void*>(p.x), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int NT, int G, bool FP8>
 cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles, cudaStream_t stream) {
     auto kern = expert_w4_kernel<NT, G, FP8>;
     const size_t smem = w4_smem(p.w, NT, FP8, splits);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    CUtensorMap map{};
+    if (x_boxes(NT)) {
+        e = describe_rows(p, 8 * NT, &map);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits));
     cfg.blockDim = dim3(kThreads);
@@ -602,7 +652,7 @@ cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, splits, units, (int)tiles);
+    return cudaLaunchKernelEx(&cfg, kern, p, map, splits, units, (int)tiles);
 }
 
 template <int NT, bool FP8>
@@ -617,9 +667,10 @@ cudaError_t launch_rows(const W4Params& p, int num_sms, cudaStream_t stream) {
     // every row in a tile of its expert: full tiles, and a last one for each expert in use
     const int64_t tiles = std::min<int64_t>(p.w.E, p.max_rows) + p.max_rows / (8 * NT);
     const int64_t products = std::min<int64_t>(p.w.E, p.max_rows) * row_blocks(p.w);
-    // few products: share K among the CTAs of a cluster until there are about two CTAs for every SM
+    // few products: share K among the CTAs of a cluster until there are two CTAs for every SM (one with wide tiles, of
+    // which two fit an SM)
     int splits = 1;
-    while (splits < 8 && products * splits < 2 * num_sms && k_blocks(p.w) >= 4 * splits) splits *= 2;
+    while (splits < 8 && products * splits < (NT <= 2 ? 2 : 1) * num_sms && k_blocks(p.w) >= 4 * splits) splits *= 2;
     // many short ones: several to a CTA, for at least 64 steps of K, as long as 16 CTAs for every SM remain
     int units = 1;
     while (units * k_blocks(p.w) < 64 && products >= 32 * (int64_t)num_sms * units) units *= 2;
@@ -636,7 +687,7 @@ bool w4_packs(const W4Shape& w) { return (int64_t)w.E * row_blocks(w) * k_blocks
 
 bool w4_fits(const W4Shape& w, int64_t max_rows, int fp8) {
     // shared memory of the widest form, CTAs of the narrowest
-    return w4_smem(w, 8, fp8 != 0, 8) <= kMaxSmem &&
+    return w4_smem(w, 4, fp8 != 0, 8) <= kMaxSmem &&
            (std::min<int64_t>(w.E, max_rows) + max_rows / 8) * row_blocks(w) * 8 <= INT32_MAX;
 }
 
@@ -648,12 +699,11 @@ cudaError_t launch_w4_pack(const W4Shape& w, const uint8_t* codes, const void* s
 
 cudaError_t launch_expert_w4(const W4Params& p, int num_sms, cudaStream_t stream) {
     if (p.max_rows == 0) return cudaSuccess;
-    // tokens of a tile: enough for about twice an expert's share of the rows
+    // tokens of a tile: enough for about twice an expert's share of the rows, up to 32
     const int64_t share = p.max_rows / std::min<int64_t>(p.w.E, p.max_rows);
     if (p.max_rows <= 8) return launch_rows<1>(p, num_sms, stream);
     if (share <= 8) return launch_rows<2>(p, num_sms, stream);
-    if (share <= 32) return launch_rows<4>(p, num_sms, stream);
-    return launch_rows<8>(p, num_sms, stream);
+    return launch_rows<4>(p, num_sms, stream);
 }
 
 }  // namespace ep

@@ -216,3 +216,12 @@ def test_refusals():
     odd = ep.W4Weights(codes[:, :, :60].contiguous(), scales)   # K = 120: no fp8 rows
     with pytest.raises(ep.EPError):
         ep.expert_w4(x.to(torch.float8_e4m3fn)[:, :120].contiguous(), odd, offsets=o, x_scales=torch.ones(4, 0, device="cuda"))
+
+
+@pytest.mark.parametrize("K", [8, 40, 72, 200, 264, 1000])
+@pytest.mark.parametrize("rows", [33, 50, 95])
+def test_short_last_step_with_many_rows(K, rows):
+    """Rows end inside a box of channels, and the last tile past the buffer's end."""
+    check([rows], 72, K, 32, True)
+    check([rows, 3, 40], 24, K, 128, False)
+    check([rows, 0, 40], 24, K, 64, False, capacity=45)
