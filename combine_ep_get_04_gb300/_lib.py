@@ -139,7 +139,7 @@ def load() -> ctypes.CDLL:
     lib.ep_block_norm_workspace_bytes.argtypes = [npt]
     lib.ep_block_norm_backward.restype = ctypes.c_int
     lib.ep_block_norm_backward.argtypes = [npt, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
-                                           size, vp]
+                                           size, vp, vp]
     lib.ep_status_string.restype = ctypes.c_char_p
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_str.restype = ctypes.c_char_p

@@ -224,6 +224,7 @@ class BlockNorm:
         self.rstd = torch.empty((2, T), **f32) if train else None
         self.grads = None
         self.workspace = None
+        self.err_flags = torch.zeros(1, dtype=torch.int32, device=dev) if train else None    # OR-ed into; the caller clears it
         if train:
             self.workspace = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
             self.workspace_bytes = int(nbytes)
@@ -268,6 +269,6 @@ class BlockNorm:
             self._ref, *self._inputs(h, y, w_post, w_pre, gate, res_scale), _ptr(self.rstd),
             _shaped_ptr(d_h_out, self.dtype, "d_h_out", (T, H)), _shaped_ptr(d_n, torch.bfloat16, "d_n", (T, H)), _ptr(g.d_h),
             _ptr(g.d_y), _ptr(g.d_w_post), _ptr(g.d_gate), _ptr(g.d_res_scale), _ptr(g.d_w_pre), _ptr(self.workspace),
-            self.workspace_bytes, _stream(stream))
+            self.workspace_bytes, _ptr(self.err_flags), _stream(stream))
         check(st, "ep_block_norm_backward")
         return g

@@ -153,144 +153,236 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, RowShape shape
     }
 }
 
-// Backward.  Each CTA walks rows a grid apart and keeps its sums over rows
-// (d_w_post, d_w_pre, a channel gate's gradient) in registers, in fp32; they
-// go to the workspace once, and norm_columns_kernel adds the CTAs' sums in
+// ---------------------------------------------------------------- backward
+//
+// A row needs one reduction only: with e = d_h_out + r2 t (t = d_n w_pre) and
+// u = yn w_post, the gradient is d = e - hn * (r2 m2), m2 = mean(t hn), so that
+// the second norm's mean(g d u) = (sum g u e - r2 m2 sum g u hn) / H follows from
+// sums that are known before m2 is.
+//
+// A CTA owns up to kCols columns, one vector of 8 to a thread, and keeps their
+// weights and their sums over rows (d_w_post, d_w_pre, a channel gate's
+// gradient) in registers for all its rows; wider rows are shared by a cluster
+// of CTAs.  A producer warp keeps a ring of row stages filled by bulk copies.
+// Consumer warps put their share of a row's three sums into every CTA of the
+// cluster (pass 1) and take up the row again `lag` rows later (pass 2), when the
+// sums have long arrived, so that no warp stands still at a row's end.  The CTAs'
+// sums over rows go to the workspace once, and norm_columns_kernel adds them in
 // CTA order, so that nothing depends on the order in which CTAs run.
-template <int NV, bool F32, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_backward_kernel(NormParams p, RowShape shape) {
-    __shared__ float red1[32], red2[32], red3[32];
-    extern __shared__ float col[];   // [3][H] when a CTA works on several rows at once
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lanes = shape.warps * 32;
-    const int sub = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int vecs = p.H / kVec;
-    const float inv_h = 1.f / (float)p.H;
-    const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
-    Vec8 s_post[NV], s_gate[NV], s_pre[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s_post[i] = s_gate[i] = s_pre[i] = zeros();
-    float s_scale = 0.f;
-    for (int64_t t0 = (int64_t)blockIdx.x * shape.rows; t0 < p.T; t0 += (int64_t)gridDim.x * shape.rows) {
-        const int64_t t = t0 + sub;
-        const bool live = t < p.T;
-        const float r1 = live && p.w_post != nullptr ? p.rstd[t] : 1.f;
-        const float r2 = live && p.w_pre != nullptr ? p.rstd[p.T + t] : 0.f;
-        const float token_gate = live && p.gate_kind == kGateToken ? p.gate[t] : 1.f;
-        Vec8 h[NV], y[NV], dn[NV], dh[NV];
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = lane + i * lanes;
-            const bool in = live && v < vecs;
-            h[i] = in ? load_stream<F32>(p.h, t * p.ld_h + v * kVec) : zeros();
-            y[i] = in && p.y != nullptr ? load_bf16(p.y, t * p.ld_y + v * kVec) : zeros();
-            dn[i] = in && p.d_n != nullptr ? load_bf16(p.d_n, t * p.H + v * kVec) : zeros();
-            dh[i] = in && p.d_h_out != nullptr ? load_stream<F32>(p.d_h_out, t * p.H + v * kVec) : zeros();
-        }
-        // hn takes the place of nothing: it is kept beside h, whose gradient needs both
-        Vec8 hn[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = lane + i * lanes;
-            const bool in = live && v < vecs;
-            const Vec8 w = in && p.w_post != nullptr ? load_f32(p.w_post, v * kVec) : ones();
-            const Vec8 g = in && p.gate_kind == kGateChannel ? load_f32(p.gate, v * kVec) : ones();
-            const Vec8 q = in && p.w_pre != nullptr ? load_f32(p.w_pre, v * kVec) : zeros();
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                y[i].v[c] *= r1;
-                const float u = y[i].v[c] * w.v[c];
-                hn[i].v[c] = r2 * fmaf(scale, h[i].v[c], token_gate * g.v[c] * u);
-                s_pre[i].v[c] = fmaf(dn[i].v[c], hn[i].v[c], s_pre[i].v[c]);
-                dn[i].v[c] *= q.v[c];
-                dot = fmaf(dn[i].v[c], hn[i].v[c], dot);
-            }
-        }
-        const float m2 = p.w_pre != nullptr ? row_sum(dot, red1, shape.warps) * inv_h : 0.f;
-        float dot_y = 0.f, dot_g = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = lane + i * lanes;
-            const bool in = live && v < vecs;
-            const Vec8 w = in && p.w_post != nullptr ? load_f32(p.w_post, v * kVec) : ones();
-            const Vec8 g = in && p.gate_kind == kGateChannel ? load_f32(p.gate, v * kVec) : ones();
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                const float d = fmaf(r2, dn[i].v[c] - hn[i].v[c] * m2, dh[i].v[c]);
-                s_scale = fmaf(d, h[i].v[c], s_scale);
-                const float u = y[i].v[c] * w.v[c];
-                s_gate[i].v[c] = fmaf(d, u, s_gate[i].v[c]);
-                dot_g = fmaf(d, u, dot_g);
-                h[i].v[c] = scale * d;
-                const float du = token_gate * g.v[c] * d;
-                s_post[i].v[c] = fmaf(du, y[i].v[c], s_post[i].v[c]);
-                dn[i].v[c] = du * w.v[c];
-                dot_y = fmaf(dn[i].v[c], y[i].v[c], dot_y);
-            }
-            if (in) store_stream<F32>(p.d_h, t * p.H + v * kVec, h[i]);
-        }
-        const float m1 = p.w_post != nullptr ? row_sum(dot_y, red2, shape.warps) * inv_h : 0.f;
-        if (p.gate_kind == kGateToken) {
-            const float sum = row_sum(dot_g, red3, shape.warps);
-            if (live && lane == 0) p.d_gate[t] = sum;
-        }
-        if (p.d_y != nullptr) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = lane + i * lanes;
-                if (!live || v >= vecs) continue;
-                Vec8 d;
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) d.v[c] = r1 * (dn[i].v[c] - y[i].v[c] * m1);
-                store_bf16(p.d_y, t * p.H + v * kVec, d);
-            }
-        }
-        // the next row's sums reuse the arrays that this row's last readers may still read
-        if (shape.warps > 1) __syncthreads();
-    }
-    // the CTA's sums: rows worked on side by side are added in their order
-    float* out = p.partial + (int64_t)blockIdx.x * 3 * p.H;
-    for (int r = 0; r < shape.rows; ++r) {
-        if (sub == r) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = lane + i * lanes;
-                if (v >= vecs) continue;
-                float* to[3] = {col + v * kVec, col + p.H + v * kVec, col + 2 * p.H + v * kVec};
-                const Vec8* from[3] = {&s_post[i], &s_gate[i], &s_pre[i]};
-#pragma unroll
-                for (int a = 0; a < 3; ++a) {
-                    if (shape.rows == 1) {
-                        store_f32(out, (int64_t)a * p.H + v * kVec, *from[a]);
-                        continue;
-                    }
-#pragma unroll
-                    for (int c = 0; c < kVec; ++c) to[a][c] = (r == 0 ? 0.f : to[a][c]) + from[a]->v[c];
-                }
-            }
-        }
-        if (shape.rows > 1) __syncthreads();
-    }
-    if (shape.rows > 1)
-        for (int i = threadIdx.x; i < 3 * p.H; i += blockDim.x) out[i] = col[i];
-    if (p.d_res_scale != nullptr) {
-        s_scale = warp_sum(s_scale);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) red1[threadIdx.x >> 5] = s_scale;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float s = 0.f;
-            for (int i = 0; i < (int)blockDim.x / 32; ++i) s += red1[i];
-            p.partial[(int64_t)gridDim.x * 3 * p.H + blockIdx.x] = s;
-        }
+
+constexpr int kCols = 4096;
+constexpr int kMaxStages = 6;
+constexpr int kSlots = 8;          // rows whose sums may be on their way; a writer is less than 6 rows ahead of a reader
+constexpr int kMaxWarps = kCols / kVec / 32;
+
+struct BackwardShape {
+    int cluster;    // CTAs a row is shared by
+    int cols;       // columns of a CTA (the last may have fewer)
+    int warps;      // consumer warps
+    int stages;
+    int lag;
+    int clusters;   // clusters of the grid
+    int per_sm;     // CTAs an SM holds
+};
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t smem, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
+}
+
+// mbar_wait whose phase may be completed by other CTAs of the cluster.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
     }
 }
 
-// Adds `ctas` rows of column sums.  A CTA takes 32 columns; its 8 warps add
+template <bool F32>
+__global__ void __launch_bounds__(kMaxWarps * 32 + 32) norm_backward_kernel(NormParams p, BackwardShape s) {
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], summed[kSlots];
+    __shared__ float3 sums[kSlots][8 * kMaxWarps];
+    __shared__ float scale_part[kMaxWarps];
+    constexpr int kStream = F32 ? 4 : 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % s.cluster, group = blockIdx.x / s.cluster;
+    const int col0 = rank * s.cols, cols = min(s.cols, p.H - col0);
+    // a stage: h, d_h_out (stream type), y, d_n (bf16)
+    const int at_dh = s.cols * kStream, at_y = at_dh * 2, at_dn = at_y + s.cols * 2, stage_bytes = at_dn + s.cols * 2;
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], s.warps);
+        }
+        for (int i = 0; i < kSlots; ++i) mbar_init(&summed[i], s.warps * s.cluster);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (s.cluster > 1) cluster_barrier();
+    pdl_wait();
+    const int rows = group < p.T ? (p.T - 1 - group) / s.clusters + 1 : 0;
+    bool good = true;
+    if (warp == s.warps) {
+        // producer
+        int filled = 0;
+        for (; filled < rows; ++filled) {
+            const int st = filled % s.stages, round = filled / s.stages;
+            if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (round - 1) & 1))) {
+                good = false;
+                break;
+            }
+            if (lane == 0) {
+                const int64_t t = group + (int64_t)filled * s.clusters;
+                unsigned char* to = ring + st * stage_bytes;
+                const int wide = cols * kStream, narrow = cols * 2;
+                mbar_arrive_expect_tx(&full[st], wide + (p.d_h_out != nullptr ? wide : 0) + (p.y != nullptr ? narrow : 0) +
+                                                     (p.d_n != nullptr ? narrow : 0));
+                bulk_load(to, static_cast<const unsigned char*>(p.h) + (t * p.ld_h + col0) * kStream, wide, &full[st]);
+                if (p.y != nullptr)
+                    bulk_load(to + at_y, static_cast<const unsigned char*>(p.y) + (t * p.ld_y + col0) * 2, narrow, &full[st]);
+                if (p.d_n != nullptr)
+                    bulk_load(to + at_dn, static_cast<const unsigned char*>(p.d_n) + (t * p.H + col0) * 2, narrow, &full[st]);
+                if (p.d_h_out != nullptr)
+                    bulk_load(to + at_dh, static_cast<const unsigned char*>(p.d_h_out) + (t * p.H + col0) * kStream, wide, &full[st]);
+            }
+            __syncwarp();
+        }
+        // no copy may be in flight when the CTA ends, whatever its consumers did
+        for (int i = max(0, filled - s.stages); i < filled; ++i) mbar_wait(&full[i % s.stages], (i / s.stages) & 1);
+    } else {
+        const int v = warp * 32 + lane;
+        const bool in = v * kVec < cols;
+        const int c0 = in ? v * kVec : 0;                  // column within the CTA
+        const float inv_h = 1.f / (float)p.H;
+        const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
+        const Vec8 w = in && p.w_post != nullptr ? load_f32(p.w_post, col0 + c0) : ones();
+        const Vec8 g = in && p.gate_kind == kGateChannel ? load_f32(p.gate, col0 + c0) : ones();
+        const Vec8 q = in && p.w_pre != nullptr ? load_f32(p.w_pre, col0 + c0) : zeros();
+        Vec8 s_post = zeros(), s_gate = zeros(), s_pre = zeros();
+        float s_scale = 0.f;
+        for (int i = 0; i < rows + s.lag; ++i) {
+            if (i < rows) {
+                // pass 1: the row's three sums
+                const int st = i % s.stages;
+                const int64_t t = group + (int64_t)i * s.clusters;
+                const float r1 = p.w_post != nullptr ? p.rstd[t] : 1.f;
+                const float r2 = p.w_pre != nullptr ? p.rstd[p.T + t] : 0.f;
+                const float token_gate = p.gate_kind == kGateToken ? p.gate[t] : 1.f;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (i / s.stages) & 1))) good = false;
+                float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f;
+                if (in && good) {
+                    const unsigned char* from = ring + st * stage_bytes;
+                    const Vec8 h = load_stream<F32>(from, c0), dh = p.d_h_out != nullptr ? load_stream<F32>(from + at_dh, c0) : zeros();
+                    const Vec8 y = p.y != nullptr ? load_bf16(from + at_y, c0) : zeros();
+                    const Vec8 dn = p.d_n != nullptr ? load_bf16(from + at_dn, c0) : zeros();
+#pragma unroll
+                    for (int c = 0; c < kVec; ++c) {
+                        const float gu = g.v[c] * (y.v[c] * r1 * w.v[c]);
+                        const float hn = r2 * fmaf(scale, h.v[c], token_gate * gu);
+                        const float tt = dn.v[c] * q.v[c];
+                        const float e = fmaf(r2, tt, dh.v[c]);
+                        s_pre.v[c] = fmaf(dn.v[c], hn, s_pre.v[c]);
+                        sum0 = fmaf(tt, hn, sum0);
+                        sum1 = fmaf(gu, e, sum1);
+                        sum2 = fmaf(gu, hn, sum2);
+                    }
+                }
+                sum0 = warp_sum(sum0);
+                sum1 = warp_sum(sum1);
+                sum2 = warp_sum(sum2);
+                if (lane < s.cluster) {
+                    const uint32_t to = in_cta(smem_addr(&sums[i % kSlots][rank * s.warps + warp]), lane);
+                    asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0+4], %2;\n\tst.shared::cluster.f32 [%0+8], %3;"
+                                 ::"r"(to), "f"(sum0), "f"(sum1), "f"(sum2) : "memory");
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                                 ::"r"(in_cta(smem_addr(&summed[i % kSlots]), lane)) : "memory");
+                }
+            }
+            if (i >= s.lag) {
+                // pass 2: the gradients of the row `lag` rows back
+                const int j = i - s.lag, st = j % s.stages;
+                const int64_t t = group + (int64_t)j * s.clusters;
+                const float r1 = p.w_post != nullptr ? p.rstd[t] : 1.f;
+                const float r2 = p.w_pre != nullptr ? p.rstd[p.T + t] : 0.f;
+                const float token_gate = p.gate_kind == kGateToken ? p.gate[t] : 1.f;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&summed[j % kSlots], (j / kSlots) & 1))) good = false;
+                float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f;
+                for (int k = lane; k < s.warps * s.cluster; k += 32) {
+                    const float3 x = sums[j % kSlots][k];
+                    sum0 += x.x;
+                    sum1 += x.y;
+                    sum2 += x.z;
+                }
+                sum0 = warp_sum(sum0);
+                const float m2 = r2 * (sum0 * inv_h);
+                const float gu_d = warp_sum(sum1) - m2 * warp_sum(sum2);          // sum of g u d (without a token's gate)
+                const float m1 = p.w_post != nullptr ? token_gate * gu_d * inv_h : 0.f;
+                if (p.gate_kind == kGateToken && rank == 0 && threadIdx.x == 0) p.d_gate[t] = gu_d;
+                if (in && good) {
+                    const unsigned char* from = ring + st * stage_bytes;
+                    const Vec8 h = load_stream<F32>(from, c0), dh = p.d_h_out != nullptr ? load_stream<F32>(from + at_dh, c0) : zeros();
+                    const Vec8 y = p.y != nullptr ? load_bf16(from + at_y, c0) : zeros();
+                    const Vec8 dn = p.d_n != nullptr ? load_bf16(from + at_dn, c0) : zeros();
+                    Vec8 d_h, d_y;
+#pragma unroll
+                    for (int c = 0; c < kVec; ++c) {
+                        const float yn = y.v[c] * r1, u = yn * w.v[c];
+                        const float hn = r2 * fmaf(scale, h.v[c], token_gate * (g.v[c] * u));
+                        const float d = fmaf(-hn, m2, fmaf(r2, dn.v[c] * q.v[c], dh.v[c]));
+                        const float du = token_gate * (g.v[c] * d);
+                        s_scale = fmaf(d, h.v[c], s_scale);
+                        s_gate.v[c] = fmaf(d, u, s_gate.v[c]);
+                        s_post.v[c] = fmaf(du, yn, s_post.v[c]);
+                        d_h.v[c] = scale * d;
+                        d_y.v[c] = r1 * fmaf(-yn, m1, du * w.v[c]);
+                    }
+                    store_stream<F32>(p.d_h, t * p.H + col0 + c0, d_h);
+                    if (p.d_y != nullptr) store_bf16(p.d_y, t * p.H + col0 + c0, d_y);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
+            }
+            if (!good) break;
+        }
+        if (!in) s_scale = 0.f;
+        s_scale = warp_sum(s_scale);
+        if (lane == 0) scale_part[warp] = s_scale;
+        if (in) {
+            float* out = p.partial + (int64_t)group * 3 * p.H + col0 + c0;
+            store_f32(out, 0, s_post);
+            store_f32(out, p.H, s_gate);
+            store_f32(out, 2 * (int64_t)p.H, s_pre);
+        }
+    }
+    if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float sum = 0.f;
+        for (int i = 0; i < s.warps; ++i) sum += scale_part[i];
+        p.partial[(int64_t)s.clusters * 3 * p.H + blockIdx.x] = sum;
+    }
+    if (s.cluster > 1) cluster_barrier();      // no CTA ends while another may still write to it
+}
+
+// Adds `groups` rows of column sums and `ctas` sums for d_res_scale.  A CTA takes 32 columns; its 8 warps add
 // every eighth row, then the eight sums are added in order.
-__global__ void __launch_bounds__(256) norm_columns_kernel(NormParams p, int ctas) {
+__global__ void __launch_bounds__(256) norm_columns_kernel(NormParams p, int groups, int ctas) {
     __shared__ float part[8][32];
     pdl_launch_dependents();
     pdl_wait();
@@ -299,7 +391,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(NormParams p, int cta
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < width)
-        for (int r = warp; r < ctas; r += 8) s += p.partial[r * width + c];
+        for (int r = warp; r < groups; r += 8) s += p.partial[r * width + c];
     part[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < width) {
@@ -312,25 +404,36 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(NormParams p, int cta
     }
     if (blockIdx.x == 0 && warp == 1 && p.d_res_scale != nullptr) {
         s = 0.f;
-        for (int r = lane; r < ctas; r += 32) s += p.partial[ctas * width + r];
+        for (int r = lane; r < ctas; r += 32) s += p.partial[groups * width + r];
         s = warp_sum(s);
         if (lane == 0) *p.d_res_scale = s;
     }
 }
 
-// One CTA on each SM; never more than the workspace has room for.
-constexpr int kMaxBackwardCtas = 192;
+constexpr int kMaxSms = 192;                      // the workspace has room for this many
+constexpr size_t kRingBytes = 200 * 1024;         // shared memory of an SM that the rings may take
 
-int backward_ctas(int T, int rows, int num_sms) {
-    return (int)std::min<int64_t>(((int64_t)T + rows - 1) / rows, std::min(num_sms, kMaxBackwardCtas));
+// clusters: at most this many, 0 for the workspace's bound.
+BackwardShape backward_shape(int T, int H, int f32, int num_sms) {
+    BackwardShape s{};
+    s.cluster = H <= kCols ? 1 : H <= 2 * kCols ? 2 : 4;
+    s.cols = ((H / kVec + s.cluster - 1) / s.cluster) * kVec;
+    s.warps = (s.cols / kVec + 31) / 32;
+    // narrow rows: as many CTAs on an SM as keep 16 consumer warps
+    s.per_sm = std::max(1, std::min(4, 16 / s.warps));
+    const size_t stage = (size_t)s.cols * (f32 ? 12 : 8);
+    s.stages = (int)std::min<size_t>(kMaxStages, kRingBytes / s.per_sm / stage);
+    // a cluster's sums take longer to arrive
+    s.lag = std::min(s.cluster > 1 ? 2 : 1, s.stages - 2);
+    s.clusters = std::min(T, std::min(num_sms, kMaxSms) * s.per_sm / s.cluster);
+    return s;
 }
 
 }  // namespace
 
 size_t norm_workspace_bytes(int T, int H) {
-    const RowShape s = row_shape(H, 2, 8);
-    const size_t ctas = (size_t)backward_ctas(T, s.rows, kMaxBackwardCtas);
-    return (ctas * (3 * (size_t)H + 1) * sizeof(float) + 15) / 16 * 16;
+    const BackwardShape s = backward_shape(T, H, 0, kMaxSms);
+    return ((size_t)s.clusters * (3 * (size_t)H + s.cluster) * sizeof(float) + 15) / 16 * 16;
 }
 
 cudaError_t launch_block_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
@@ -342,22 +445,17 @@ cudaError_t launch_block_norm(const NormParams& p, int num_sms, cudaStream_t str
 }
 
 cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream) {
-    const RowShape s = row_shape(p.H, 2, 8);
-    const int ctas = backward_ctas(p.T, s.rows, num_sms);
-    if (ctas > 0) {
-        const size_t smem = s.rows > 1 ? 3 * (size_t)p.H * sizeof(float) : 0;
-        const dim3 grid(ctas), block(s.warps * 32 * s.rows);
-        cudaError_t e;
-        if (block.x <= 512)
-            e = p.f32 ? launch_kernel(true, norm_backward_kernel<2, true, 512>, grid, block, smem, stream, p, s)
-                      : launch_kernel(true, norm_backward_kernel<2, false, 512>, grid, block, smem, stream, p, s);
-        else
-            e = p.f32 ? launch_kernel(true, norm_backward_kernel<2, true, 1024>, grid, block, smem, stream, p, s)
-                      : launch_kernel(true, norm_backward_kernel<2, false, 1024>, grid, block, smem, stream, p, s);
+    const BackwardShape s = backward_shape(p.T, p.H, p.f32, num_sms);
+    if (s.clusters > 0) {
+        auto kern = p.f32 ? norm_backward_kernel<true> : norm_backward_kernel<false>;
+        const size_t smem = (size_t)s.stages * s.cols * (p.f32 ? 12 : 8);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+        if (e != cudaSuccess) return e;
+        e = launch_clusters(true, s.cluster, kern, dim3(s.clusters * s.cluster), dim3(s.warps * 32 + 32), smem, stream, p, s);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((3 * (int64_t)p.H + 31) / 32));
-    return launch_kernel(true, norm_columns_kernel, grid, dim3(256), 0, stream, p, ctas);
+    return launch_kernel(true, norm_columns_kernel, grid, dim3(256), 0, stream, p, s.clusters, s.clusters * s.cluster);
 }
 
 }  // namespace ep

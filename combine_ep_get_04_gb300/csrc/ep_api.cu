@@ -660,7 +660,8 @@ ep_status_t ep_block_norm_backward(const ep_norm_t* norm, const void* h, int64_t
                                    const float* w_post, const float* gate, const float* res_scale,
                                    const float* w_pre, const float* rstd, const void* d_h_out, const void* d_n,
                                    void* d_h, void* d_y, float* d_w_post, float* d_gate, float* d_res_scale,
-                                   float* d_w_pre, void* workspace, size_t workspace_bytes, ep_stream_t stream) {
+                                   float* d_w_pre, void* workspace, size_t workspace_bytes, uint32_t* err_flags,
+                                   ep_stream_t stream) {
     ep_status_t st = check_norm(norm);
     if (st != EP_OK) return st;
     if (norm->T > 0) {
@@ -704,6 +705,7 @@ ep_status_t ep_block_norm_backward(const ep_norm_t* norm, const void* h, int64_t
     p.d_res_scale = d_res_scale;
     p.d_w_pre = d_w_pre;
     p.partial = static_cast<float*>(workspace);
+    p.err_flags = err_flags;
     p.ld_h = ld_h;
     p.ld_y = ld_y;
     p.T = norm->T;

@@ -16,20 +16,36 @@ namespace ep {
 // only as an address hint for a prefetch).  Used for latency-sized grids
 // (about one unit of work per CTA), where the launch gap is a large share of
 // the time; large persistent grids launch normally.
+// With cluster > 1, that many consecutive CTAs form a cluster.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_kernel(bool pdl, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                          cudaStream_t stream, Args&&... args) {
+cudaError_t launch_clusters(bool pdl, int cluster, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t stream, Args&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel(bool pdl, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t stream, Args&&... args) {
+    return launch_clusters(pdl, 1, kern, grid, block, smem, stream, args...);
 }
 
 // Sets the text ep_last_error() returns on the calling thread.
@@ -223,7 +239,8 @@ struct NormParams {
     float* d_gate;
     float* d_res_scale;
     float* d_w_pre;
-    float* partial;            // workspace: column sums of each CTA, then its d_res_scale
+    float* partial;            // workspace: column sums of each group of CTAs, then each CTA's d_res_scale
+    uint32_t* err_flags;       // may be nullptr
     int64_t ld_h, ld_y;
     int T, H;
     int f32;                   // stream type

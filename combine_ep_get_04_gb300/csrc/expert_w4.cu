@@ -638,21 +638,8 @@ cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles,
         e = describe_rows(p, 8 * NT, &map);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, map, splits, units, (int)tiles);
+    const dim3 grid((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits));
+    return launch_clusters(true, splits, kern, grid, dim3(kThreads), smem, stream, p, map, splits, units, (int)tiles);
 }
 
 template <int NT, bool FP8>

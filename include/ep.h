@@ -419,6 +419,7 @@ EP_API size_t ep_block_norm_workspace_bytes(const ep_norm_t *norm);
  *      d_res_scale  f32 [1], NULL exactly when res_scale is.
  * workspace: ep_block_norm_workspace_bytes(norm) bytes, 16-byte aligned,
  * contents on entry ignored.  T = 0 sets the sums to zero.
+ * err_flags: EP_ERRF_TIMEOUT.
  */
 EP_API ep_status_t ep_block_norm_backward(const ep_norm_t *norm, const void *h, int64_t ld_h,
                           const void *y, int64_t ld_y, const float *w_post,
@@ -427,7 +428,7 @@ EP_API ep_status_t ep_block_norm_backward(const ep_norm_t *norm, const void *h, 
                           const void *d_h_out, const void *d_n, void *d_h, void *d_y,
                           float *d_w_post, float *d_gate, float *d_res_scale,
                           float *d_w_pre, void *workspace, size_t workspace_bytes,
-                          ep_stream_t stream);
+                          uint32_t *err_flags, ep_stream_t stream);
 
 #define EP_MAX_ROUTE_GROUPS 32
 

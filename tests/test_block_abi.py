@@ -51,7 +51,7 @@ def test_norm_arguments(lib):
     def bwd(shape=s, w_post=FAKE, gate=None, a=None, w_pre=FAKE, rstd=FAKE, dho=FAKE, dn=FAKE, dh=FAKE, dy=FAKE, dwq=FAKE,
             dg=None, da=None, dwp=FAKE, ws=FAKE, nb=need):
         return lib.ep_block_norm_backward(ctypes.byref(shape), FAKE, 64, FAKE, 64, w_post, gate, a, w_pre, rstd, dho, dn, dh, dy,
-                                          dwq, dg, da, dwp, ws, nb, None)
+                                          dwq, dg, da, dwp, ws, nb, None, None)
 
     for bad in (dict(rstd=None), dict(dh=None), dict(dy=None), dict(dn=None), dict(dwq=None), dict(dwp=None), dict(dg=FAKE),
                 dict(da=FAKE), dict(a=FAKE), dict(ws=None), dict(nb=need - 1), dict(ws=ODD), dict(dho=ODD), dict(dn=ODD),
