@@ -15,35 +15,74 @@ constexpr int kGateChannel = 1;
 constexpr int kGateToken = 2;
 constexpr int kVec = 8;   // channels a thread handles at once: 16 bytes of bf16
 
+// Eight fp32 values as four packed pairs: the products and sums below take two
+// at a time (f32x2), which halves the instructions a row costs.
 struct Vec8 {
-    float v[kVec];
+    uint64_t v[4];
 };
 
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+
+__device__ __forceinline__ float2 halves(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ float total(uint64_t p) {
+    const float2 x = halves(p);
+    return x.x + x.y;
+}
+
+__device__ __forceinline__ Vec8 bf16_vec(uint4 w) {
+    return Vec8{{pair(bf16_lo(w.x), bf16_hi(w.x)), pair(bf16_lo(w.y), bf16_hi(w.y)), pair(bf16_lo(w.z), bf16_hi(w.z)),
+                 pair(bf16_lo(w.w), bf16_hi(w.w))}};
+}
+
+__device__ __forceinline__ Vec8 f32_vec(float4 a, float4 b) { return Vec8{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}}; }
+
 __device__ __forceinline__ Vec8 load_bf16(const void* base, int64_t at) {
-    const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + at * 2);
-    return Vec8{{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w),
-                 bf16_hi(w.w)}};
+    return bf16_vec(*reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(base) + at * 2));
 }
 
 __device__ __forceinline__ Vec8 load_f32(const void* base, int64_t at) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    return f32_vec(p[0], p[1]);
 }
 
 __device__ __forceinline__ void store_bf16(void* base, int64_t at, const Vec8& x) {
-    uint4 w;
-    w.x = pack_bf16x2(x.v[0], x.v[1]);
-    w.y = pack_bf16x2(x.v[2], x.v[3]);
-    w.z = pack_bf16x2(x.v[4], x.v[5]);
-    w.w = pack_bf16x2(x.v[6], x.v[7]);
-    *reinterpret_cast<uint4*>(static_cast<unsigned char*>(base) + at * 2) = w;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = halves(x.v[i]);
+        w[i] = pack_bf16x2(f.x, f.y);
+    }
+    *reinterpret_cast<uint4*>(static_cast<unsigned char*>(base) + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ void store_f32(void* base, int64_t at, const Vec8& x) {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-    p[0] = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
-    p[1] = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
+    const float2 a = halves(x.v[0]), b = halves(x.v[1]), c = halves(x.v[2]), d = halves(x.v[3]);
+    p[0] = make_float4(a.x, a.y, b.x, b.y);
+    p[1] = make_float4(c.x, c.y, d.x, d.y);
 }
 
 template <bool F32>
@@ -59,97 +98,118 @@ __device__ __forceinline__ void store_stream(void* base, int64_t at, const Vec8&
         store_bf16(base, at, x);
 }
 
-__device__ __forceinline__ Vec8 zeros() { return Vec8{{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}}; }
-__device__ __forceinline__ Vec8 ones() { return Vec8{{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}}; }
+__device__ __forceinline__ Vec8 all(float x) { return Vec8{{both(x), both(x), both(x), both(x)}}; }
 
-// Sum over the `warps` warps of one row.  `red` holds one float for each warp
-// of the CTA; every thread of the CTA takes part.  One barrier: a caller that
-// sums twice uses two arrays in turn.
-__device__ __forceinline__ float row_sum(float x, float* red, int warps) {
+// Sum over the warps of a CTA.  `red` holds one float for each warp; one
+// barrier: a caller that sums again uses another array until the next.
+__device__ __forceinline__ float cta_sum(float x, float* red, int warps) {
     x = warp_sum(x);
     if (warps == 1) return x;
-    const int warp = threadIdx.x >> 5, first = warp - warp % warps;
-    if ((threadIdx.x & 31) == 0) red[warp] = x;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += red[first + i];
-    return s;
+    return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
-// Threads of a row hold NV vectors of 8 channels each, `lanes` threads apart.
-struct RowShape {
-    int warps;   // warps a row
-    int rows;    // rows a CTA works on at once
-};
-
-RowShape row_shape(int H, int nv, int least_warps) {
-    const int vecs = H / kVec;
-    RowShape r;
-    r.warps = (vecs + nv * 32 - 1) / (nv * 32);
-    r.rows = std::max(1, least_warps / r.warps);
-    return r;
-}
-
-// Forward.  A row's h and y stay in registers between its two norms: the mean
-// square of y, then that of h_out, one barrier each (none where a row fits a
-// warp).
-template <int NV, bool F32>
-__global__ void __launch_bounds__(1024) norm_kernel(NormParams p, RowShape shape) {
-    __shared__ float red1[32], red2[32];
+// ----------------------------------------------------------------- forward
+//
+// A CTA takes a row at a time, NV vectors of 8 channels to a thread, rows a
+// grid apart, and holds the weights of its channels in registers for all its
+// rows (NV = 1).  The next row's h and y are on their way while a row is worked
+// on; in between the row stays in registers: the mean square of y, then that of
+// h_out, one barrier each (none where a row fits a warp).
+//
+// FULL: y, both norms and h_out are there, which saves the tests for them.
+template <int NV, bool F32, bool FULL>
+__global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
+    __shared__ float red[4][32];
+    const int lanes = blockDim.x, warps = lanes >> 5, vecs = p.H / kVec;
+    const bool has_y = FULL || p.y != nullptr, has_post = FULL || p.w_post != nullptr, has_pre = FULL || p.w_pre != nullptr;
+    const float inv_h = 1.f / (float)p.H;
     pdl_launch_dependents();
     pdl_wait();
-    const int lanes = shape.warps * 32;
-    const int sub = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int64_t t = (int64_t)blockIdx.x * shape.rows + sub;
-    const bool live = t < p.T;
-    const int vecs = p.H / kVec;
-    Vec8 h[NV], y[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = lane + i * lanes;
-        const bool in = live && v < vecs;
-        h[i] = in ? load_stream<F32>(p.h, t * p.ld_h + v * kVec) : zeros();
-        y[i] = in && p.y != nullptr ? load_bf16(p.y, t * p.ld_y + v * kVec) : zeros();
-    }
     const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
-    const float token_gate = p.gate_kind == kGateToken && live ? p.gate[t] : 1.f;
-    float r1 = 1.f;
-    if (p.w_post != nullptr) {
-        float ss = 0.f;
+    bool in[NV];
+    int at[NV];
+    Vec8 w[NV], g[NV], q[NV];
+    auto load_weights = [&](int i) {
+        w[i] = in[i] && has_post ? load_f32(p.w_post, at[i]) : all(1.f);
+        g[i] = in[i] && p.gate_kind == kGateChannel ? load_f32(p.gate, at[i]) : all(1.f);
+        q[i] = in[i] && has_pre ? load_f32(p.w_pre, at[i]) : all(0.f);
+    };
+    constexpr int kRaw = F32 ? 2 : 1;
+    uint4 next_h[NV][kRaw], next_y[NV];
+    float next_gate = 1.f;
+    auto fetch = [&](int64_t t) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) ss = fmaf(y[i].v[c], y[i].v[c], ss);
-        r1 = rsqrtf(row_sum(ss, red1, shape.warps) / (float)p.H + p.eps);
-        if (live && lane == 0 && p.rstd != nullptr) p.rstd[t] = r1;
-    }
-    float ss = 0.f;
+            for (int r = 0; r < kRaw; ++r) next_h[i][r] = make_uint4(0, 0, 0, 0);
+            next_y[i] = make_uint4(0, 0, 0, 0);
+            if (in[i] && t < p.T) {
+                const uint4* h = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.h) + (t * p.ld_h + at[i]) * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = lane + i * lanes;
-        if (!live || v >= vecs) continue;
-        const Vec8 w = p.w_post != nullptr ? load_f32(p.w_post, v * kVec) : ones();
-        const Vec8 g = p.gate_kind == kGateChannel ? load_f32(p.gate, v * kVec) : ones();
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) {
-            const float u = y[i].v[c] * r1 * w.v[c];
-            h[i].v[c] = fmaf(scale, h[i].v[c], token_gate * g.v[c] * u);
-            ss = fmaf(h[i].v[c], h[i].v[c], ss);
+                for (int r = 0; r < kRaw; ++r) next_h[i][r] = h[r];
+                if (has_y) next_y[i] = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.y) + (t * p.ld_y + at[i]) * 2);
+            }
         }
-        if (p.h_out != nullptr) store_stream<F32>(p.h_out, t * p.H + v * kVec, h[i]);
-    }
-    if (p.w_pre == nullptr) return;
-    const float r2 = rsqrtf(row_sum(ss, red2, shape.warps) / (float)p.H + p.eps);
-    if (live && lane == 0 && p.rstd != nullptr) p.rstd[p.T + t] = r2;
+        if (p.gate_kind == kGateToken && t < p.T) next_gate = p.gate[t];
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int v = lane + i * lanes;
-        if (!live || v >= vecs) continue;
-        const Vec8 w = load_f32(p.w_pre, v * kVec);
-        Vec8 n;
+        const int v = threadIdx.x + i * lanes;
+        in[i] = v < vecs;
+        at[i] = v * kVec;
+        if (NV == 1) load_weights(i);
+    }
+    fetch(blockIdx.x);
+    int flip = 0;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, flip ^= 2) {
+        Vec8 h[NV], y[NV];
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) n.v[c] = h[i].v[c] * r2 * w.v[c];
-        store_bf16(p.n, t * p.H + v * kVec, n);
+        for (int i = 0; i < NV; ++i) {
+            const uint4 a = next_h[i][0], b = next_h[i][kRaw - 1];
+            h[i] = F32 ? f32_vec(make_float4(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w)),
+                                 make_float4(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)))
+                       : bf16_vec(a);
+            y[i] = bf16_vec(next_y[i]);
+        }
+        const float gate = next_gate;
+        fetch(t + gridDim.x);
+        float r1 = 1.f;
+        if (has_post) {
+            uint64_t ss = both(0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ss = fma2(y[i].v[c], y[i].v[c], ss);
+            r1 = rsqrtf(fmaf(cta_sum(total(ss), red[flip], warps), inv_h, p.eps));
+            if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[t] = r1;
+        }
+        uint64_t ss = both(0.f);
+        const uint64_t r1_gate = both(r1 * gate), a2 = both(scale);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (NV > 1) load_weights(i);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint64_t gu = mul2(g[i].v[c], mul2(mul2(y[i].v[c], r1_gate), w[i].v[c]));
+                h[i].v[c] = fma2(a2, h[i].v[c], gu);
+                ss = fma2(h[i].v[c], h[i].v[c], ss);
+            }
+            if (in[i] && (FULL || p.h_out != nullptr)) store_stream<F32>(p.h_out, t * p.H + at[i], h[i]);
+        }
+        if (!has_pre) continue;
+        const float r2 = rsqrtf(fmaf(cta_sum(total(ss), red[flip + 1], warps), inv_h, p.eps));
+        if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[p.T + t] = r2;
+        const uint64_t r2_2 = both(r2);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            Vec8 n;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) n.v[c] = mul2(mul2(h[i].v[c], r2_2), q[i].v[c]);
+            if (in[i]) store_bf16(p.n, t * p.H + at[i], n);
+        }
     }
 }
 
@@ -164,14 +224,16 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p, RowShape shape
 // weights and their sums over rows (d_w_post, d_w_pre, a channel gate's
 // gradient) in registers for all its rows; wider rows are shared by a cluster
 // of CTAs.  A producer warp keeps a ring of row stages filled by bulk copies.
-// Consumer warps put their share of a row's three sums into every CTA of the
-// cluster (pass 1) and take up the row again `lag` rows later (pass 2), when the
-// sums have long arrived, so that no warp stands still at a row's end.  The CTAs'
+// Consumer warps leave their share of a row's three sums to a warp that adds
+// them and passes them to every CTA of the cluster (pass 1), and take up the row
+// again `lag` rows later (pass 2), when the sums have long arrived, so that no
+// consumer stands still at a row's end.  The CTAs'
 // sums over rows go to the workspace once, and norm_columns_kernel adds them in
 // CTA order, so that nothing depends on the order in which CTAs run.
 
 constexpr int kCols = 4096;
 constexpr int kMaxStages = 6;
+constexpr int kMaxCluster = 4;
 constexpr int kSlots = 8;          // rows whose sums may be on their way; a writer is less than 6 rows ahead of a reader
 constexpr int kMaxWarps = kCols / kVec / 32;
 
@@ -195,9 +257,9 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t smem, int rank) {
     return a;
 }
 
-// mbar_wait whose phase may be completed by other CTAs of the cluster.
+// mbar_wait for bytes that CTAs of the cluster send.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     for (;;) {
         uint32_t done;
         asm volatile(
@@ -208,20 +270,32 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
             : "r"(smem_addr(bar)), "r"(parity)
             : "memory");
         if (done) return true;
-        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) return false;
     }
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kMaxWarps * 32 + 32) norm_backward_kernel(NormParams p, BackwardShape s) {
+// Writes a row's sums to a CTA of the cluster and arrives on its barrier.
+__device__ __forceinline__ void send(uint32_t to, float a, float b, float c, uint32_t bar) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(a), "f"(b), "f"(c), "f"(0.f) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// FULL: y, d_n and d_h_out are there, which saves the tests for them.
+template <bool F32, bool FULL>
+__global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(NormParams p, BackwardShape s) {
     extern __shared__ __align__(128) unsigned char ring[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], summed[kSlots];
-    __shared__ float3 sums[kSlots][8 * kMaxWarps];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], added[kSlots], summed[kSlots];
+    __shared__ float warp_sums[kSlots][3][kMaxWarps];
+    __shared__ float4 sums[kSlots][kMaxCluster];
+    __shared__ float4 row_values[kMaxStages];     // r1, r2, the token's gate
     __shared__ float scale_part[kMaxWarps];
     constexpr int kStream = F32 ? 4 : 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % s.cluster, group = blockIdx.x / s.cluster;
     const int col0 = rank * s.cols, cols = min(s.cols, p.H - col0);
+    const bool has_y = FULL || p.y != nullptr, has_dn = FULL || p.d_n != nullptr, has_dh = FULL || p.d_h_out != nullptr;
     // a stage: h, d_h_out (stream type), y, d_n (bf16)
     const int at_dh = s.cols * kStream, at_y = at_dh * 2, at_dn = at_y + s.cols * 2, stage_bytes = at_dn + s.cols * 2;
     pdl_launch_dependents();
@@ -230,7 +304,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 32) norm_backward_kernel(Norm
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], s.warps);
         }
-        for (int i = 0; i < kSlots; ++i) mbar_init(&summed[i], s.warps * s.cluster);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&added[i], s.warps);
+            mbar_init(&summed[i], s.cluster);
+        }
         fence_mbar_init();
     }
     __syncthreads();
@@ -240,129 +317,162 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 32) norm_backward_kernel(Norm
     bool good = true;
     if (warp == s.warps) {
         // producer
-        int filled = 0;
+        int filled = 0, st = 0;
+        uint32_t parity = 1;                      // of the stage's previous use
         for (; filled < rows; ++filled) {
-            const int st = filled % s.stages, round = filled / s.stages;
-            if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (round - 1) & 1))) {
+            if (filled >= s.stages && !__all_sync(0xffffffffu, mbar_wait(&empty[st], parity))) {
                 good = false;
                 break;
             }
+            const int64_t t = group + (int64_t)filled * s.clusters;
+            if (lane == 1)
+                row_values[st] = make_float4(p.w_post != nullptr ? p.rstd[t] : 1.f, p.w_pre != nullptr ? p.rstd[p.T + t] : 0.f,
+                                             p.gate_kind == kGateToken ? p.gate[t] : 1.f, 0.f);
             if (lane == 0) {
-                const int64_t t = group + (int64_t)filled * s.clusters;
                 unsigned char* to = ring + st * stage_bytes;
                 const int wide = cols * kStream, narrow = cols * 2;
-                mbar_arrive_expect_tx(&full[st], wide + (p.d_h_out != nullptr ? wide : 0) + (p.y != nullptr ? narrow : 0) +
-                                                     (p.d_n != nullptr ? narrow : 0));
+                mbar_expect_tx(&full[st], wide + (has_dh ? wide : 0) + (has_y ? narrow : 0) + (has_dn ? narrow : 0));
                 bulk_load(to, static_cast<const unsigned char*>(p.h) + (t * p.ld_h + col0) * kStream, wide, &full[st]);
-                if (p.y != nullptr)
-                    bulk_load(to + at_y, static_cast<const unsigned char*>(p.y) + (t * p.ld_y + col0) * 2, narrow, &full[st]);
-                if (p.d_n != nullptr)
-                    bulk_load(to + at_dn, static_cast<const unsigned char*>(p.d_n) + (t * p.H + col0) * 2, narrow, &full[st]);
-                if (p.d_h_out != nullptr)
+                if (has_y) bulk_load(to + at_y, static_cast<const unsigned char*>(p.y) + (t * p.ld_y + col0) * 2, narrow, &full[st]);
+                if (has_dn) bulk_load(to + at_dn, static_cast<const unsigned char*>(p.d_n) + (t * p.H + col0) * 2, narrow, &full[st]);
+                if (has_dh)
                     bulk_load(to + at_dh, static_cast<const unsigned char*>(p.d_h_out) + (t * p.H + col0) * kStream, wide, &full[st]);
             }
             __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);          // after the row's values are written
+            if (++st == s.stages) {
+                st = 0;
+                parity ^= 1;
+            }
         }
         // no copy may be in flight when the CTA ends, whatever its consumers did
         for (int i = max(0, filled - s.stages); i < filled; ++i) mbar_wait(&full[i % s.stages], (i / s.stages) & 1);
+    } else if (warp == s.warps + 1) {
+        // adds the warps' sums of each row and passes them on
+        const uint32_t to = in_cta(smem_addr(&sums[0][rank]), lane < s.cluster ? lane : 0);
+        const uint32_t bar = in_cta(smem_addr(&summed[0]), lane < s.cluster ? lane : 0);
+        uint32_t parity = 0;
+        for (int i = 0; i < rows; ++i) {
+            const int slot = i % kSlots;
+            if (!__all_sync(0xffffffffu, mbar_wait(&added[slot], parity))) {
+                good = false;
+                break;
+            }
+            const bool has = lane < s.warps;
+            const float x0 = warp_sum(has ? warp_sums[slot][0][lane] : 0.f), x1 = warp_sum(has ? warp_sums[slot][1][lane] : 0.f),
+                        x2 = warp_sum(has ? warp_sums[slot][2][lane] : 0.f);
+            if (s.cluster > 1) {
+                if (lane < s.cluster) send(to + slot * (uint32_t)sizeof(sums[0]), x0, x1, x2, bar + slot * 8);
+            } else if (lane == 0) {
+                sums[slot][0] = make_float4(x0, x1, x2, 0.f);
+                mbar_arrive(&summed[slot]);
+            }
+            if (slot == kSlots - 1) parity ^= 1;
+        }
+        __syncwarp();
     } else {
         const int v = warp * 32 + lane;
         const bool in = v * kVec < cols;
         const int c0 = in ? v * kVec : 0;                  // column within the CTA
         const float inv_h = 1.f / (float)p.H;
         const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
-        const Vec8 w = in && p.w_post != nullptr ? load_f32(p.w_post, col0 + c0) : ones();
-        const Vec8 g = in && p.gate_kind == kGateChannel ? load_f32(p.gate, col0 + c0) : ones();
-        const Vec8 q = in && p.w_pre != nullptr ? load_f32(p.w_pre, col0 + c0) : zeros();
-        Vec8 s_post = zeros(), s_gate = zeros(), s_pre = zeros();
-        float s_scale = 0.f;
+        const Vec8 w = in && p.w_post != nullptr ? load_f32(p.w_post, col0 + c0) : all(1.f);
+        const Vec8 g = in && p.gate_kind == kGateChannel ? load_f32(p.gate, col0 + c0) : all(1.f);
+        const Vec8 q = in && p.w_pre != nullptr ? load_f32(p.w_pre, col0 + c0) : all(0.f);
+        Vec8 s_post = all(0.f), s_gate = all(0.f), s_pre = all(0.f);
+        uint64_t s_scale = both(0.f);
+        const unsigned char* first = ring + c0 * 2;        // the thread's place in a bf16 row
+        int st1 = 0, st2 = 0;
+        uint32_t full_parity = 0, summed_parity = 0;
+        auto take = [&](int st, Vec8& h, Vec8& dh, Vec8& y, Vec8& dn) {
+            const unsigned char* from = first + st * stage_bytes;
+            const unsigned char* wide = from + (F32 ? c0 * 2 : 0);
+            h = load_stream<F32>(wide, 0);
+            dh = has_dh ? load_stream<F32>(wide + at_dh, 0) : all(0.f);
+            y = has_y ? load_bf16(from + at_y, 0) : all(0.f);
+            dn = has_dn ? load_bf16(from + at_dn, 0) : all(0.f);
+        };
         for (int i = 0; i < rows + s.lag; ++i) {
             if (i < rows) {
                 // pass 1: the row's three sums
-                const int st = i % s.stages;
-                const int64_t t = group + (int64_t)i * s.clusters;
-                const float r1 = p.w_post != nullptr ? p.rstd[t] : 1.f;
-                const float r2 = p.w_pre != nullptr ? p.rstd[p.T + t] : 0.f;
-                const float token_gate = p.gate_kind == kGateToken ? p.gate[t] : 1.f;
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (i / s.stages) & 1))) good = false;
-                float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[st1], full_parity))) good = false;
+                uint64_t sum0 = both(0.f), sum1 = sum0, sum2 = sum0;
                 if (in && good) {
-                    const unsigned char* from = ring + st * stage_bytes;
-                    const Vec8 h = load_stream<F32>(from, c0), dh = p.d_h_out != nullptr ? load_stream<F32>(from + at_dh, c0) : zeros();
-                    const Vec8 y = p.y != nullptr ? load_bf16(from + at_y, c0) : zeros();
-                    const Vec8 dn = p.d_n != nullptr ? load_bf16(from + at_dn, c0) : zeros();
+                    const float4 rv = row_values[st1];
+                    const uint64_t r1 = both(rv.x), r2 = both(rv.y), r2_scale = both(rv.y * scale), r2_gate = both(rv.y * rv.z);
+                    Vec8 h, dh, y, dn;
+                    take(st1, h, dh, y, dn);
 #pragma unroll
-                    for (int c = 0; c < kVec; ++c) {
-                        const float gu = g.v[c] * (y.v[c] * r1 * w.v[c]);
-                        const float hn = r2 * fmaf(scale, h.v[c], token_gate * gu);
-                        const float tt = dn.v[c] * q.v[c];
-                        const float e = fmaf(r2, tt, dh.v[c]);
-                        s_pre.v[c] = fmaf(dn.v[c], hn, s_pre.v[c]);
-                        sum0 = fmaf(tt, hn, sum0);
-                        sum1 = fmaf(gu, e, sum1);
-                        sum2 = fmaf(gu, hn, sum2);
+                    for (int c = 0; c < 4; ++c) {
+                        const uint64_t gu = mul2(g.v[c], mul2(mul2(y.v[c], r1), w.v[c]));
+                        const uint64_t hn = fma2(r2_scale, h.v[c], mul2(r2_gate, gu));
+                        const uint64_t t = mul2(dn.v[c], q.v[c]);
+                        const uint64_t e = fma2(r2, t, dh.v[c]);
+                        s_pre.v[c] = fma2(dn.v[c], hn, s_pre.v[c]);
+                        sum0 = fma2(t, hn, sum0);
+                        sum1 = fma2(gu, e, sum1);
+                        sum2 = fma2(gu, hn, sum2);
                     }
                 }
-                sum0 = warp_sum(sum0);
-                sum1 = warp_sum(sum1);
-                sum2 = warp_sum(sum2);
-                if (lane < s.cluster) {
-                    const uint32_t to = in_cta(smem_addr(&sums[i % kSlots][rank * s.warps + warp]), lane);
-                    asm volatile("st.shared::cluster.f32 [%0], %1;\n\tst.shared::cluster.f32 [%0+4], %2;\n\tst.shared::cluster.f32 [%0+8], %3;"
-                                 ::"r"(to), "f"(sum0), "f"(sum1), "f"(sum2) : "memory");
-                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
-                                 ::"r"(in_cta(smem_addr(&summed[i % kSlots]), lane)) : "memory");
+                const float x0 = warp_sum(total(sum0)), x1 = warp_sum(total(sum1)), x2 = warp_sum(total(sum2));
+                const int slot = i % kSlots;
+                if (lane == 0) {
+                    warp_sums[slot][0][warp] = x0;
+                    warp_sums[slot][1][warp] = x1;
+                    warp_sums[slot][2][warp] = x2;
+                    mbar_arrive(&added[slot]);
+                }
+                if (++st1 == s.stages) {
+                    st1 = 0;
+                    full_parity ^= 1;
                 }
             }
             if (i >= s.lag) {
                 // pass 2: the gradients of the row `lag` rows back
-                const int j = i - s.lag, st = j % s.stages;
-                const int64_t t = group + (int64_t)j * s.clusters;
-                const float r1 = p.w_post != nullptr ? p.rstd[t] : 1.f;
-                const float r2 = p.w_pre != nullptr ? p.rstd[p.T + t] : 0.f;
-                const float token_gate = p.gate_kind == kGateToken ? p.gate[t] : 1.f;
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&summed[j % kSlots], (j / kSlots) & 1))) good = false;
-                float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f;
-                for (int k = lane; k < s.warps * s.cluster; k += 32) {
-                    const float3 x = sums[j % kSlots][k];
-                    sum0 += x.x;
-                    sum1 += x.y;
-                    sum2 += x.z;
+                const int slot = (i - s.lag) % kSlots;
+                const int64_t t = group + (int64_t)(i - s.lag) * s.clusters;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&summed[slot], summed_parity))) good = false;
+                if (slot == kSlots - 1) summed_parity ^= 1;
+                float x0 = 0.f, x1 = 0.f, x2 = 0.f;
+                for (int k = 0; k < s.cluster; ++k) {
+                    const float4 x = sums[slot][k];
+                    x0 += x.x;
+                    x1 += x.y;
+                    x2 += x.z;
                 }
-                sum0 = warp_sum(sum0);
-                const float m2 = r2 * (sum0 * inv_h);
-                const float gu_d = warp_sum(sum1) - m2 * warp_sum(sum2);          // sum of g u d (without a token's gate)
-                const float m1 = p.w_post != nullptr ? token_gate * gu_d * inv_h : 0.f;
+                const float4 rv = row_values[st2];
+                const float m2 = rv.y * (x0 * inv_h);
+                const float gu_d = x1 - m2 * x2;          // sum of g u d (without a token's gate)
+                const float m1 = p.w_post != nullptr ? rv.z * gu_d * inv_h : 0.f;
                 if (p.gate_kind == kGateToken && rank == 0 && threadIdx.x == 0) p.d_gate[t] = gu_d;
                 if (in && good) {
-                    const unsigned char* from = ring + st * stage_bytes;
-                    const Vec8 h = load_stream<F32>(from, c0), dh = p.d_h_out != nullptr ? load_stream<F32>(from + at_dh, c0) : zeros();
-                    const Vec8 y = p.y != nullptr ? load_bf16(from + at_y, c0) : zeros();
-                    const Vec8 dn = p.d_n != nullptr ? load_bf16(from + at_dn, c0) : zeros();
-                    Vec8 d_h, d_y;
+                    const uint64_t r1 = both(rv.x), r2 = both(rv.y), r2_scale = both(rv.y * scale), r2_gate = both(rv.y * rv.z);
+                    const uint64_t gate = both(rv.z), a2 = both(scale), minus_m2 = both(-m2), r1_gate = both(rv.x * rv.z), back = both(-rv.x * m1);
+                    Vec8 h, dh, y, dn, d_h, d_y;
+                    take(st2, h, dh, y, dn);
 #pragma unroll
-                    for (int c = 0; c < kVec; ++c) {
-                        const float yn = y.v[c] * r1, u = yn * w.v[c];
-                        const float hn = r2 * fmaf(scale, h.v[c], token_gate * (g.v[c] * u));
-                        const float d = fmaf(-hn, m2, fmaf(r2, dn.v[c] * q.v[c], dh.v[c]));
-                        const float du = token_gate * (g.v[c] * d);
-                        s_scale = fmaf(d, h.v[c], s_scale);
-                        s_gate.v[c] = fmaf(d, u, s_gate.v[c]);
-                        s_post.v[c] = fmaf(du, yn, s_post.v[c]);
-                        d_h.v[c] = scale * d;
-                        d_y.v[c] = r1 * fmaf(-yn, m1, du * w.v[c]);
+                    for (int c = 0; c < 4; ++c) {
+                        const uint64_t yn = mul2(y.v[c], r1), u = mul2(yn, w.v[c]);
+                        const uint64_t hn = fma2(r2_scale, h.v[c], mul2(r2_gate, mul2(g.v[c], u)));
+                        const uint64_t e = fma2(r2, mul2(dn.v[c], q.v[c]), dh.v[c]);
+                        const uint64_t d = fma2(minus_m2, hn, e), gd = mul2(g.v[c], d);
+                        s_scale = fma2(d, h.v[c], s_scale);
+                        s_gate.v[c] = fma2(d, u, s_gate.v[c]);
+                        s_post.v[c] = fma2(gd, mul2(yn, gate), s_post.v[c]);
+                        d_h.v[c] = mul2(a2, d);
+                        d_y.v[c] = fma2(mul2(gd, w.v[c]), r1_gate, mul2(yn, back));
                     }
                     store_stream<F32>(p.d_h, t * p.H + col0 + c0, d_h);
-                    if (p.d_y != nullptr) store_bf16(p.d_y, t * p.H + col0 + c0, d_y);
+                    if (has_y) store_bf16(p.d_y, t * p.H + col0 + c0, d_y);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[st]);
+                if (lane == 0) mbar_arrive(&empty[st2]);
+                if (++st2 == s.stages) st2 = 0;
             }
             if (!good) break;
         }
-        if (!in) s_scale = 0.f;
-        s_scale = warp_sum(s_scale);
-        if (lane == 0) scale_part[warp] = s_scale;
+        const float sum = warp_sum(in ? total(s_scale) : 0.f);
+        if (lane == 0) scale_part[warp] = sum;
         if (in) {
             float* out = p.partial + (int64_t)group * 3 * p.H + col0 + c0;
             store_f32(out, 0, s_post);
@@ -429,29 +539,40 @@ BackwardShape backward_shape(int T, int H, int f32, int num_sms) {
     return s;
 }
 
-}  // namespace
-
-size_t norm_workspace_bytes(int T, int H) {
+size_t workspace_bytes(int T, int H) {
     const BackwardShape s = backward_shape(T, H, 0, kMaxSms);
     return ((size_t)s.clusters * (3 * (size_t)H + s.cluster) * sizeof(float) + 15) / 16 * 16;
 }
 
+template <int NV, bool F32>
+cudaError_t launch_forward(const NormParams& p, int num_sms, cudaStream_t stream) {
+    const int warps = (p.H / kVec + 32 * NV - 1) / (32 * NV);
+    // 32 warps on an SM, whole rows
+    const dim3 grid((unsigned)std::min<int64_t>(p.T, (int64_t)num_sms * (32 / warps))), block(warps * 32);
+    const bool full = p.y != nullptr && p.w_post != nullptr && p.w_pre != nullptr && p.h_out != nullptr;
+    return full ? launch_kernel(true, norm_kernel<NV, F32, true>, grid, block, 0, stream, p)
+                : launch_kernel(true, norm_kernel<NV, F32, false>, grid, block, 0, stream, p);
+}
+
+}  // namespace
+
+size_t norm_workspace_bytes(int T, int H) { return workspace_bytes(T, H); }
+
 cudaError_t launch_block_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    const RowShape s = row_shape(p.H, 2, 4);
-    const dim3 grid((unsigned)(((int64_t)p.T + s.rows - 1) / s.rows)), block(s.warps * 32 * s.rows);
-    return p.f32 ? launch_kernel(true, norm_kernel<2, true>, grid, block, 0, stream, p, s)
-                 : launch_kernel(true, norm_kernel<2, false>, grid, block, 0, stream, p, s);
+    if (p.H <= 32 * 32 * kVec) return p.f32 ? launch_forward<1, true>(p, num_sms, stream) : launch_forward<1, false>(p, num_sms, stream);
+    return p.f32 ? launch_forward<2, true>(p, num_sms, stream) : launch_forward<2, false>(p, num_sms, stream);
 }
 
 cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream) {
     const BackwardShape s = backward_shape(p.T, p.H, p.f32, num_sms);
     if (s.clusters > 0) {
-        auto kern = p.f32 ? norm_backward_kernel<true> : norm_backward_kernel<false>;
+        const bool full = p.y != nullptr && p.d_n != nullptr && p.d_h_out != nullptr;
+        auto kern = p.f32 ? (full ? norm_backward_kernel<true, true> : norm_backward_kernel<true, false>)
+                          : (full ? norm_backward_kernel<false, true> : norm_backward_kernel<false, false>);
         const size_t smem = (size_t)s.stages * s.cols * (p.f32 ? 12 : 8);
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
         if (e != cudaSuccess) return e;
-        e = launch_clusters(true, s.cluster, kern, dim3(s.clusters * s.cluster), dim3(s.warps * 32 + 32), smem, stream, p, s);
+        e = launch_clusters(true, s.cluster, kern, dim3(s.clusters * s.cluster), dim3(s.warps * 32 + 64), smem, stream, p, s);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((3 * (int64_t)p.H + 31) / 32));
