@@ -224,10 +224,10 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 // weights and their sums over rows (d_w_post, d_w_pre, a channel gate's
 // gradient) in registers for all its rows; wider rows are shared by a cluster
 // of CTAs.  A producer warp keeps a ring of row stages filled by bulk copies.
-// Consumer warps leave their share of a row's three sums to a warp that adds
-// them and passes them to every CTA of the cluster (pass 1), and take up the row
-// again `lag` rows later (pass 2), when the sums have long arrived, so that no
-// consumer stands still at a row's end.  The CTAs'
+// Consumer warps leave their share of a row's three sums to another warp, which
+// adds them and passes them to every CTA of the cluster (pass 1), and take up
+// the row again `lag` rows later (pass 2), when the sums have long arrived, so
+// that none stands still at a row's end.  The CTAs'
 // sums over rows go to the workspace once, and norm_columns_kernel adds them in
 // CTA order, so that nothing depends on the order in which CTAs run.
 
@@ -236,6 +236,7 @@ constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 4;
 constexpr int kSlots = 8;          // rows whose sums may be on their way; a writer is less than 6 rows ahead of a reader
 constexpr int kMaxWarps = kCols / kVec / 32;
+constexpr int kColumnWarps = 16;
 
 struct BackwardShape {
     int cluster;    // CTAs a row is shared by
@@ -282,14 +283,21 @@ __device__ __forceinline__ void send(uint32_t to, float a, float b, float c, uin
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// What a row's threads all need; gate is the token's.
+struct __align__(16) RowValues {
+    float r1, r2, r2_scale, r2_gate;
+    float gate, r1_gate, unused[2];
+};
+
 // FULL: y, d_n and d_h_out are there, which saves the tests for them.
-template <bool F32, bool FULL>
-__global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(NormParams p, BackwardShape s) {
+// WARPS: most warps of a CTA; up to 16 a thread has 128 registers, which is what it needs, with 18 it has 96.
+template <bool F32, bool FULL, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p, BackwardShape s) {
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], added[kSlots], summed[kSlots];
     __shared__ float warp_sums[kSlots][3][kMaxWarps];
     __shared__ float4 sums[kSlots][kMaxCluster];
-    __shared__ float4 row_values[kMaxStages];     // r1, r2, the token's gate
+    __shared__ RowValues row_values[kMaxStages];
     __shared__ float scale_part[kMaxWarps];
     constexpr int kStream = F32 ? 4 : 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -314,20 +322,29 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(Norm
     if (s.cluster > 1) cluster_barrier();
     pdl_wait();
     const int rows = group < p.T ? (p.T - 1 - group) / s.clusters + 1 : 0;
+    const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
     bool good = true;
     if (warp == s.warps) {
         // producer
         int filled = 0, st = 0;
         uint32_t parity = 1;                      // of the stage's previous use
+        // the next row's values are on their way while a stage is waited for
+        float r1 = 1.f, r2 = 0.f, gate = 1.f;
+        auto look_up = [&](int i) {
+            const int64_t t = group + (int64_t)i * s.clusters;
+            if (lane == 1 && i < rows) {
+                if (p.w_post != nullptr) r1 = p.rstd[t];
+                if (p.w_pre != nullptr) r2 = p.rstd[p.T + t];
+                if (p.gate_kind == kGateToken) gate = p.gate[t];
+            }
+        };
+        look_up(0);
         for (; filled < rows; ++filled) {
             if (filled >= s.stages && !__all_sync(0xffffffffu, mbar_wait(&empty[st], parity))) {
                 good = false;
                 break;
             }
             const int64_t t = group + (int64_t)filled * s.clusters;
-            if (lane == 1)
-                row_values[st] = make_float4(p.w_post != nullptr ? p.rstd[t] : 1.f, p.w_pre != nullptr ? p.rstd[p.T + t] : 0.f,
-                                             p.gate_kind == kGateToken ? p.gate[t] : 1.f, 0.f);
             if (lane == 0) {
                 unsigned char* to = ring + st * stage_bytes;
                 const int wide = cols * kStream, narrow = cols * 2;
@@ -338,8 +355,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(Norm
                 if (has_dh)
                     bulk_load(to + at_dh, static_cast<const unsigned char*>(p.d_h_out) + (t * p.H + col0) * kStream, wide, &full[st]);
             }
+            if (lane == 1) row_values[st] = RowValues{r1, r2, r2 * scale, r2 * gate, gate, r1 * gate, {0.f, 0.f}};
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);          // after the row's values are written
+            look_up(filled + 1);
             if (++st == s.stages) {
                 st = 0;
                 parity ^= 1;
@@ -354,10 +373,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(Norm
         uint32_t parity = 0;
         for (int i = 0; i < rows; ++i) {
             const int slot = i % kSlots;
-            if (!__all_sync(0xffffffffu, mbar_wait(&added[slot], parity))) {
-                good = false;
-                break;
-            }
+            good = __all_sync(0xffffffffu, mbar_wait(&added[slot], parity));
+            if (!good) break;
             const bool has = lane < s.warps;
             const float x0 = warp_sum(has ? warp_sums[slot][0][lane] : 0.f), x1 = warp_sum(has ? warp_sums[slot][1][lane] : 0.f),
                         x2 = warp_sum(has ? warp_sums[slot][2][lane] : 0.f);
@@ -372,36 +389,40 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(Norm
         __syncwarp();
     } else {
         const int v = warp * 32 + lane;
-        const bool in = v * kVec < cols;
+        const bool in = v * kVec < cols;                   // the others go through it with weights of 0 and store nothing
         const int c0 = in ? v * kVec : 0;                  // column within the CTA
         const float inv_h = 1.f / (float)p.H;
-        const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
-        const Vec8 w = in && p.w_post != nullptr ? load_f32(p.w_post, col0 + c0) : all(1.f);
-        const Vec8 g = in && p.gate_kind == kGateChannel ? load_f32(p.gate, col0 + c0) : all(1.f);
+        const Vec8 w = in ? (p.w_post != nullptr ? load_f32(p.w_post, col0 + c0) : all(1.f)) : all(0.f);
+        const Vec8 g = in ? (p.gate_kind == kGateChannel ? load_f32(p.gate, col0 + c0) : all(1.f)) : all(0.f);
         const Vec8 q = in && p.w_pre != nullptr ? load_f32(p.w_pre, col0 + c0) : all(0.f);
         Vec8 s_post = all(0.f), s_gate = all(0.f), s_pre = all(0.f);
         uint64_t s_scale = both(0.f);
         const unsigned char* first = ring + c0 * 2;        // the thread's place in a bf16 row
-        int st1 = 0, st2 = 0;
-        uint32_t full_parity = 0, summed_parity = 0;
-        auto take = [&](int st, Vec8& h, Vec8& dh, Vec8& y, Vec8& dn) {
-            const unsigned char* from = first + st * stage_bytes;
+        auto take = [&](int at, Vec8& h, Vec8& dh, Vec8& y, Vec8& dn) {
+            const unsigned char* from = first + at;
             const unsigned char* wide = from + (F32 ? c0 * 2 : 0);
             h = load_stream<F32>(wide, 0);
             dh = has_dh ? load_stream<F32>(wide + at_dh, 0) : all(0.f);
             y = has_y ? load_bf16(from + at_y, 0) : all(0.f);
             dn = has_dn ? load_bf16(from + at_dn, 0) : all(0.f);
         };
+        int st1 = 0, st2 = 0, at1 = 0, at2 = 0;
+        uint32_t full_parity = 0, summed_parity = 0;
+        const int64_t stride = (int64_t)s.clusters * p.H;
+        unsigned char* d_h_row = static_cast<unsigned char*>(p.d_h) + ((int64_t)group * p.H + col0 + c0) * kStream;
+        unsigned char* d_y_row = has_y ? static_cast<unsigned char*>(p.d_y) + ((int64_t)group * p.H + col0 + c0) * 2 : nullptr;
+        float* d_gate = p.gate_kind == kGateToken && rank == 0 && threadIdx.x == 0 ? p.d_gate + group : nullptr;
         for (int i = 0; i < rows + s.lag; ++i) {
             if (i < rows) {
                 // pass 1: the row's three sums
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[st1], full_parity))) good = false;
+                good = __all_sync(0xffffffffu, mbar_wait(&full[st1], full_parity));
+                if (!good) break;
                 uint64_t sum0 = both(0.f), sum1 = sum0, sum2 = sum0;
-                if (in && good) {
-                    const float4 rv = row_values[st1];
-                    const uint64_t r1 = both(rv.x), r2 = both(rv.y), r2_scale = both(rv.y * scale), r2_gate = both(rv.y * rv.z);
+                {
+                    const RowValues& rv = row_values[st1];
+                    const uint64_t r1 = both(rv.r1), r2 = both(rv.r2), r2_scale = both(rv.r2_scale), r2_gate = both(rv.r2_gate);
                     Vec8 h, dh, y, dn;
-                    take(st1, h, dh, y, dn);
+                    take(at1, h, dh, y, dn);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const uint64_t gu = mul2(g.v[c], mul2(mul2(y.v[c], r1), w.v[c]));
@@ -422,54 +443,61 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(Norm
                     warp_sums[slot][2][warp] = x2;
                     mbar_arrive(&added[slot]);
                 }
+                at1 += stage_bytes;
                 if (++st1 == s.stages) {
-                    st1 = 0;
+                    st1 = at1 = 0;
                     full_parity ^= 1;
                 }
             }
             if (i >= s.lag) {
                 // pass 2: the gradients of the row `lag` rows back
                 const int slot = (i - s.lag) % kSlots;
-                const int64_t t = group + (int64_t)(i - s.lag) * s.clusters;
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&summed[slot], summed_parity))) good = false;
+                good = __all_sync(0xffffffffu, mbar_wait_cluster(&summed[slot], summed_parity));
+                if (!good) break;
                 if (slot == kSlots - 1) summed_parity ^= 1;
-                float x0 = 0.f, x1 = 0.f, x2 = 0.f;
-                for (int k = 0; k < s.cluster; ++k) {
-                    const float4 x = sums[slot][k];
-                    x0 += x.x;
-                    x1 += x.y;
-                    x2 += x.z;
-                }
-                const float4 rv = row_values[st2];
-                const float m2 = rv.y * (x0 * inv_h);
-                const float gu_d = x1 - m2 * x2;          // sum of g u d (without a token's gate)
-                const float m1 = p.w_post != nullptr ? rv.z * gu_d * inv_h : 0.f;
-                if (p.gate_kind == kGateToken && rank == 0 && threadIdx.x == 0) p.d_gate[t] = gu_d;
-                if (in && good) {
-                    const uint64_t r1 = both(rv.x), r2 = both(rv.y), r2_scale = both(rv.y * scale), r2_gate = both(rv.y * rv.z);
-                    const uint64_t gate = both(rv.z), a2 = both(scale), minus_m2 = both(-m2), r1_gate = both(rv.x * rv.z), back = both(-rv.x * m1);
-                    Vec8 h, dh, y, dn, d_h, d_y;
-                    take(st2, h, dh, y, dn);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint64_t yn = mul2(y.v[c], r1), u = mul2(yn, w.v[c]);
-                        const uint64_t hn = fma2(r2_scale, h.v[c], mul2(r2_gate, mul2(g.v[c], u)));
-                        const uint64_t e = fma2(r2, mul2(dn.v[c], q.v[c]), dh.v[c]);
-                        const uint64_t d = fma2(minus_m2, hn, e), gd = mul2(g.v[c], d);
-                        s_scale = fma2(d, h.v[c], s_scale);
-                        s_gate.v[c] = fma2(d, u, s_gate.v[c]);
-                        s_post.v[c] = fma2(gd, mul2(yn, gate), s_post.v[c]);
-                        d_h.v[c] = mul2(a2, d);
-                        d_y.v[c] = fma2(mul2(gd, w.v[c]), r1_gate, mul2(yn, back));
+                float4 x = sums[slot][0];
+                if (s.cluster > 1)
+                    for (int k = 1; k < s.cluster; ++k) {
+                        const float4 more = sums[slot][k];
+                        x.x += more.x;
+                        x.y += more.y;
+                        x.z += more.z;
                     }
-                    store_stream<F32>(p.d_h, t * p.H + col0 + c0, d_h);
-                    if (has_y) store_bf16(p.d_y, t * p.H + col0 + c0, d_y);
+                const RowValues& rv = row_values[st2];
+                const float m2 = rv.r2 * (x.x * inv_h);
+                const float gu_d = x.y - m2 * x.z;          // sum of g u d (without a token's gate)
+                const float m1 = p.w_post != nullptr ? rv.gate * gu_d * inv_h : 0.f;
+                if (d_gate != nullptr) {
+                    *d_gate = gu_d;
+                    d_gate += s.clusters;
+                }
+                const uint64_t r1 = both(rv.r1), r2 = both(rv.r2), r2_scale = both(rv.r2_scale), r2_gate = both(rv.r2_gate);
+                const uint64_t gate = both(rv.gate), a2 = both(scale), minus_m2 = both(-m2), r1_gate = both(rv.r1_gate), back = both(-rv.r1 * m1);
+                Vec8 h, dh, y, dn, d_h, d_y;
+                take(at2, h, dh, y, dn);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint64_t yn = mul2(y.v[c], r1), u = mul2(yn, w.v[c]);
+                    const uint64_t hn = fma2(r2_scale, h.v[c], mul2(r2_gate, mul2(g.v[c], u)));
+                    const uint64_t e = fma2(r2, mul2(dn.v[c], q.v[c]), dh.v[c]);
+                    const uint64_t d = fma2(minus_m2, hn, e), gd = mul2(g.v[c], d);
+                    s_scale = fma2(d, h.v[c], s_scale);
+                    s_gate.v[c] = fma2(d, u, s_gate.v[c]);
+                    s_post.v[c] = fma2(gd, mul2(yn, gate), s_post.v[c]);
+                    d_h.v[c] = mul2(a2, d);
+                    d_y.v[c] = fma2(mul2(gd, w.v[c]), r1_gate, mul2(yn, back));
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st2]);
-                if (++st2 == s.stages) st2 = 0;
+                if (in) {
+                    store_stream<F32>(d_h_row, 0, d_h);
+                    if (has_y) store_bf16(d_y_row, 0, d_y);
+                }
+                d_h_row += stride * kStream;
+                if (has_y) d_y_row += stride * 2;
+                at2 += stage_bytes;
+                if (++st2 == s.stages) st2 = at2 = 0;
             }
-            if (!good) break;
         }
         const float sum = warp_sum(in ? total(s_scale) : 0.f);
         if (lane == 0) scale_part[warp] = sum;
@@ -490,10 +518,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + 64) norm_backward_kernel(Norm
     if (s.cluster > 1) cluster_barrier();      // no CTA ends while another may still write to it
 }
 
-// Adds `groups` rows of column sums and `ctas` sums for d_res_scale.  A CTA takes 32 columns; its 8 warps add
-// every eighth row, then the eight sums are added in order.
-__global__ void __launch_bounds__(256) norm_columns_kernel(NormParams p, int groups, int ctas) {
-    __shared__ float part[8][32];
+// Adds `groups` rows of column sums and `ctas` sums for d_res_scale.  A CTA takes 32 columns; each warp adds every
+// kColumnWarps-th row, then the warps' sums are added in order.
+__global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormParams p, int groups, int ctas) {
+    __shared__ float part[kColumnWarps][32];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -501,13 +529,14 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(NormParams p, int gro
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < width)
-        for (int r = warp; r < groups; r += 8) s += p.partial[r * width + c];
+#pragma unroll 4
+        for (int r = warp; r < groups; r += kColumnWarps) s += p.partial[r * width + c];
     part[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < width) {
         s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += part[i][lane];
+        for (int i = 0; i < kColumnWarps; ++i) s += part[i][lane];
         const int which = (int)(c / p.H), at = (int)(c % p.H);
         float* out = which == 0 ? p.d_w_post : which == 1 ? (p.gate_kind == kGateChannel ? p.d_gate : nullptr) : p.d_w_pre;
         if (out != nullptr) out[at] = s;
@@ -567,8 +596,13 @@ cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStr
     const BackwardShape s = backward_shape(p.T, p.H, p.f32, num_sms);
     if (s.clusters > 0) {
         const bool full = p.y != nullptr && p.d_n != nullptr && p.d_h_out != nullptr;
-        auto kern = p.f32 ? (full ? norm_backward_kernel<true, true> : norm_backward_kernel<true, false>)
-                          : (full ? norm_backward_kernel<false, true> : norm_backward_kernel<false, false>);
+        void (*kern)(NormParams, BackwardShape);
+        if (s.warps + 2 <= 16)
+            kern = p.f32 ? (full ? norm_backward_kernel<true, true, 16> : norm_backward_kernel<true, false, 16>)
+                         : (full ? norm_backward_kernel<false, true, 16> : norm_backward_kernel<false, false, 16>);
+        else
+            kern = p.f32 ? (full ? norm_backward_kernel<true, true, 18> : norm_backward_kernel<true, false, 18>)
+                         : (full ? norm_backward_kernel<false, true, 18> : norm_backward_kernel<false, false, 18>);
         const size_t smem = (size_t)s.stages * s.cols * (p.f32 ? 12 : 8);
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
         if (e != cudaSuccess) return e;
@@ -576,7 +610,7 @@ cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStr
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((3 * (int64_t)p.H + 31) / 32));
-    return launch_kernel(true, norm_columns_kernel, grid, dim3(256), 0, stream, p, s.clusters, s.clusters * s.cluster);
+    return launch_kernel(true, norm_columns_kernel, grid, dim3(kColumnWarps * 32), 0, stream, p, s.clusters, s.clusters * s.cluster);
 }
 
 }  // namespace ep
