@@ -4,6 +4,10 @@ from __future__ import annotations
 import torch
 
 
+# The raw handle of a device's current stream, without a Stream object around it.
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "tensor",
          numel: int | None = None) -> int | None:
     if t is None:
@@ -19,29 +23,34 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "
     return t.data_ptr() or None
 
 
-def _rows_ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, rows: int, cols: int) -> tuple[int | None, int]:
+def _rows_ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tuple[int, int]) -> tuple[int | None, int]:
     """Address and row stride (in elements) of a [rows, cols] tensor whose rows
     may lie further apart than their length."""
     if t is None:
         return None, 0
+    if t.dtype is dtype and t.shape == shape and t.is_cuda:
+        ld, step = t.stride()
+        if step == 1 or shape[1] <= 1:
+            return t.data_ptr() or None, ld if shape[0] > 1 else shape[1]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    if t.stride(1) != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr() or None, t.stride(0) if rows > 1 else cols
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have contiguous rows")
 
 
 def _shaped_ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tuple) -> int | None:
     """Address of a contiguous tensor of exactly this shape."""
-    if t is not None and tuple(t.shape) != shape:
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr() or None
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
     return _ptr(t, dtype, name)
 
 
 def _stream(stream: torch.cuda.Stream | None) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream or None
+    return (_raw_stream(_current_device()) if stream is None else stream.cuda_stream) or None

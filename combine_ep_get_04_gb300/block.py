@@ -73,10 +73,18 @@ class Router:
         self.workspace_bytes = int(nbytes) if train else 0
         self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev) if train else None
         self.d_logits = torch.empty((T, E), dtype=dtype, device=dev) if train else None
+        o = self.out
+        self._lib, self._shape = lib, (T, E)
+        self._outputs = (_ptr(o.topk_idx), _ptr(o.topk_w), _ptr(o.lse), _ptr(o.counts), _ptr(o.prob_sums), _ptr(o.seq_tokens),
+                         _ptr(o.losses), _ptr(self.workspace), self.workspace_bytes, _ptr(o.err_flags))
+        self._saved = (_ptr(o.topk_idx), _ptr(o.topk_w), _ptr(o.lse), _ptr(o.counts), _ptr(o.seq_tokens))
+        self._d_logits = _ptr(self.d_logits)
 
     def _seqs(self, seq_offsets):
-        if seq_offsets is None and self.train and self.num_seqs != 1:
-            raise ValueError(f"{self.num_seqs} sequences need seq_offsets")
+        if seq_offsets is None:
+            if self.train and self.num_seqs != 1:
+                raise ValueError(f"{self.num_seqs} sequences need seq_offsets")
+            return None
         return _shaped_ptr(seq_offsets, torch.int32, "seq_offsets", (self.num_seqs + 1,))
 
     def route(self, logits: torch.Tensor, select_bias: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
@@ -84,17 +92,15 @@ class Router:
         """logits [T, E]; select_bias f32 [E] shifts the choice alone;
         token_mask u8 or bool [T] leaves tokens out; seq_offsets i32
         [num_seqs + 1]."""
-        o = self.out
-        lp, ld = _rows_ptr(logits, self.dtype, "logits", self.T, self.E)
+        lp, ld = _rows_ptr(logits, self.dtype, "logits", self._shape)
         if token_mask is not None and token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)
-        st = load().ep_route(
+        st = self._lib.ep_route(
             self._ref, lp, ld, _shaped_ptr(select_bias, torch.float32, "select_bias", (self.E,)),
-            _shaped_ptr(token_mask, torch.uint8, "token_mask", (self.T,)), self._seqs(seq_offsets), _ptr(o.topk_idx),
-            _ptr(o.topk_w), _ptr(o.lse), _ptr(o.counts), _ptr(o.prob_sums), _ptr(o.seq_tokens), _ptr(o.losses),
-            _ptr(self.workspace), self.workspace_bytes, _ptr(o.err_flags), _stream(stream))
-        check(st, "ep_route")
-        return o
+            _shaped_ptr(token_mask, torch.uint8, "token_mask", (self.T,)), self._seqs(seq_offsets), *self._outputs, _stream(stream))
+        if st:
+            check(st, "ep_route")
+        return self.out
 
     def backward(self, logits: torch.Tensor, d_topk_w: torch.Tensor | None, d_losses: torch.Tensor | None,
                  seq_offsets: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
@@ -103,13 +109,13 @@ class Router:
         zero)."""
         if not self.train:
             raise ValueError("this router was made without train=True")
-        o = self.out
-        lp, ld = _rows_ptr(logits, self.dtype, "logits", self.T, self.E)
-        st = load().ep_route_backward(
-            self._ref, lp, ld, self._seqs(seq_offsets), _ptr(o.topk_idx), _ptr(o.topk_w), _ptr(o.lse), _ptr(o.counts),
-            _ptr(o.seq_tokens), _shaped_ptr(d_topk_w, torch.float32, "d_topk_w", (self.T, self.k)),
-            _shaped_ptr(d_losses, torch.float32, "d_losses", (2,)), _ptr(self.d_logits), _stream(stream))
-        check(st, "ep_route_backward")
+        lp, ld = _rows_ptr(logits, self.dtype, "logits", self._shape)
+        st = self._lib.ep_route_backward(
+            self._ref, lp, ld, self._seqs(seq_offsets), *self._saved,
+            _shaped_ptr(d_topk_w, torch.float32, "d_topk_w", (self.T, self.k)),
+            _shaped_ptr(d_losses, torch.float32, "d_losses", (2,)), self._d_logits, _stream(stream))
+        if st:
+            check(st, "ep_route_backward")
         return self.d_logits
 
 
@@ -139,7 +145,8 @@ class W4Weights:
         cp = _ptr(codes, torch.uint8, "codes")
         sp = _shaped_ptr(scales, torch.bfloat16, "scales", (E, rows, -(-self.K // group)))
         self.packed = torch.empty(int(nbytes), dtype=torch.uint8, device=codes.device)
-        check(lib.ep_w4_pack(self._ref, cp, sp, _ptr(self.packed), _stream(stream)), "ep_w4_pack")
+        self._lib, self._packed = lib, _ptr(self.packed)
+        check(lib.ep_w4_pack(self._ref, cp, sp, self._packed, _stream(stream)), "ep_w4_pack")
 
 
 def expert_w4(x: torch.Tensor, weights: W4Weights, counts: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
@@ -159,7 +166,7 @@ def expert_w4(x: torch.Tensor, weights: W4Weights, counts: torch.Tensor | None =
         raise ValueError(f"x must be [R, {w.K}], got {tuple(x.shape)}")
     R = x.shape[0]
     if x_scales is None:
-        payload, xp, sp = PAYLOAD_BF16, _ptr(x, torch.bfloat16, "x"), None
+        payload, xp, sp = PAYLOAD_BF16, _shaped_ptr(x, torch.bfloat16, "x", (R, w.K)), None
     else:
         if x.element_size() != 1:
             raise TypeError("x_scales go with one-byte e4m3 rows")
@@ -171,11 +178,12 @@ def expert_w4(x: torch.Tensor, weights: W4Weights, counts: torch.Tensor | None =
         raise ValueError("several experts need the layout's counts and offsets")
     if out is None:
         out = torch.empty((R, w.N), dtype=torch.bfloat16, device=x.device)
-    st = load().ep_expert_w4(
-        w._ref, _ptr(w.packed), PACKED if capacity is None else CAPACITY, capacity or 0, R, R if max_rows is None else max_rows,
-        _ptr(counts, torch.int32, "counts", w.E), _ptr(offsets, torch.int32, "offsets", w.E + 1), xp, sp, payload,
-        _shaped_ptr(out, torch.bfloat16, "out", (R, w.N)), _ptr(err_flags, torch.int32, "err_flags", 1), _stream(stream))
-    check(st, "ep_expert_w4")
+    st = w._lib.ep_expert_w4(
+        w._ref, w._packed, PACKED if capacity is None else CAPACITY, capacity or 0, R, R if max_rows is None else max_rows,
+        _shaped_ptr(counts, torch.int32, "counts", (w.E,)), _shaped_ptr(offsets, torch.int32, "offsets", (w.E + 1,)), xp, sp, payload,
+        _shaped_ptr(out, torch.bfloat16, "out", (R, w.N)), _shaped_ptr(err_flags, torch.int32, "err_flags", (1,)), _stream(stream))
+    if st:
+        check(st, "ep_expert_w4")
     return out
 
 
@@ -215,11 +223,13 @@ class BlockNorm:
         nbytes = lib.ep_block_norm_workspace_bytes(self._ref)
         if nbytes == ctypes.c_size_t(-1).value:
             check(1, "ep_block_norm_workspace_bytes")
-        self.T, self.H, self.dtype, self.gate, self.post, self.pre = T, H, dtype, gate, post, pre
-        self.scaled, self.block, self.train = scaled, block, train
+        self.T, self.H, self.dtype, self.gate, self.post, self.pre = T, H, dtype, gate, bool(post), bool(pre)
+        self.scaled, self.block, self.train = bool(scaled), bool(block), bool(train)
         dev = torch.device(device)
         f32 = dict(dtype=torch.float32, device=dev)
         self.h_out = torch.empty((T, H), dtype=dtype, device=dev)
+        self._lib, self._shape, self._row = lib, (T, H), (H,)
+        self._gate_shape = (H if gate == "channel" else T,)
         self.n = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if pre else None
         self.rstd = torch.empty((2, T), **f32) if train else None
         self.grads = None
@@ -234,26 +244,32 @@ class BlockNorm:
                 d_w_post=torch.empty(H, **f32) if post else None, d_w_pre=torch.empty(H, **f32) if pre else None,
                 d_gate=None if gate is None else torch.empty(H if gate == "channel" else T, **f32),
                 d_res_scale=torch.empty(1, **f32) if scaled else None)
+            g = self.grads
+            self._outputs = (_ptr(g.d_h), _ptr(g.d_y), _ptr(g.d_w_post), _ptr(g.d_gate), _ptr(g.d_res_scale), _ptr(g.d_w_pre),
+                             _ptr(self.workspace), self.workspace_bytes, _ptr(self.err_flags))
+        self._n, self._rstd = _ptr(self.n), _ptr(self.rstd)
 
     def _inputs(self, h, y, w_post, w_pre, gate, res_scale):
-        for t, wanted, name in ((y, self.block, "y"), (w_post, self.post, "w_post"), (w_pre, self.pre, "w_pre"),
-                                (gate, self.gate is not None, "gate"), (res_scale, self.scaled, "res_scale")):
-            if (t is not None) != wanted:
-                raise ValueError(f"{name} is {'missing' if wanted else 'not part of this norm'}")
-        T, H, f32 = self.T, self.H, torch.float32
-        hp, ldh = _rows_ptr(h, self.dtype, "h", T, H)
-        yp, ldy = _rows_ptr(y, torch.bfloat16, "y", T, H)
-        return (hp, ldh, yp, ldy, _shaped_ptr(w_post, f32, "w_post", (H,)),
-                _shaped_ptr(gate, f32, "gate", (H if self.gate == "channel" else T,)),
-                _shaped_ptr(res_scale, f32, "res_scale", (1,)), _shaped_ptr(w_pre, f32, "w_pre", (H,)))
+        if ((y is None) is self.block or (w_post is None) is self.post or (w_pre is None) is self.pre or
+                (gate is None) is not (self.gate is None) or (res_scale is None) is self.scaled):
+            for t, wanted, name in ((y, self.block, "y"), (w_post, self.post, "w_post"), (w_pre, self.pre, "w_pre"),
+                                    (gate, self.gate is not None, "gate"), (res_scale, self.scaled, "res_scale")):
+                if (t is not None) != wanted:
+                    raise ValueError(f"{name} is {'missing' if wanted else 'not part of this norm'}")
+        f32 = torch.float32
+        hp, ldh = _rows_ptr(h, self.dtype, "h", self._shape)
+        yp, ldy = _rows_ptr(y, torch.bfloat16, "y", self._shape)
+        return (hp, ldh, yp, ldy, _shaped_ptr(w_post, f32, "w_post", self._row), _shaped_ptr(gate, f32, "gate", self._gate_shape),
+                _shaped_ptr(res_scale, f32, "res_scale", (1,)), _shaped_ptr(w_pre, f32, "w_pre", self._row))
 
     def forward(self, h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
                 w_pre: torch.Tensor | None = None, gate: torch.Tensor | None = None,
                 res_scale: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
         """Returns (h_out, n); n is None without a norm before the next block."""
-        st = load().ep_block_norm(self._ref, *self._inputs(h, y, w_post, w_pre, gate, res_scale), _ptr(self.h_out),
-                                  _ptr(self.n), _ptr(self.rstd), _stream(stream))
-        check(st, "ep_block_norm")
+        st = self._lib.ep_block_norm(self._ref, *self._inputs(h, y, w_post, w_pre, gate, res_scale), self.h_out.data_ptr() or None,
+                                     self._n, self._rstd, _stream(stream))
+        if st:
+            check(st, "ep_block_norm")
         return self.h_out, self.n
 
     def backward(self, h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
@@ -264,11 +280,10 @@ class BlockNorm:
         of its outputs (d_h_out may be None: zero)."""
         if not self.train:
             raise ValueError("this norm was made without train=True")
-        g, T, H = self.grads, self.T, self.H
-        st = load().ep_block_norm_backward(
-            self._ref, *self._inputs(h, y, w_post, w_pre, gate, res_scale), _ptr(self.rstd),
-            _shaped_ptr(d_h_out, self.dtype, "d_h_out", (T, H)), _shaped_ptr(d_n, torch.bfloat16, "d_n", (T, H)), _ptr(g.d_h),
-            _ptr(g.d_y), _ptr(g.d_w_post), _ptr(g.d_gate), _ptr(g.d_res_scale), _ptr(g.d_w_pre), _ptr(self.workspace),
-            self.workspace_bytes, _ptr(self.err_flags), _stream(stream))
-        check(st, "ep_block_norm_backward")
-        return g
+        st = self._lib.ep_block_norm_backward(
+            self._ref, *self._inputs(h, y, w_post, w_pre, gate, res_scale), self._rstd,
+            _shaped_ptr(d_h_out, self.dtype, "d_h_out", self._shape), _shaped_ptr(d_n, torch.bfloat16, "d_n", self._shape),
+            *self._outputs, _stream(stream))
+        if st:
+            check(st, "ep_block_norm_backward")
+        return self.grads

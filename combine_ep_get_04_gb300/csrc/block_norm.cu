@@ -131,6 +131,12 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
     const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
     bool in[NV];
     int at[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * lanes;
+        in[i] = v < vecs;
+        at[i] = v * kVec;
+    }
     Vec8 w[NV], g[NV], q[NV];
     auto load_weights = [&](int i) {
         w[i] = in[i] && has_post ? load_f32(p.w_post, at[i]) : all(1.f);
@@ -155,13 +161,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
         }
         if (p.gate_kind == kGateToken && t < p.T) next_gate = p.gate[t];
     };
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * lanes;
-        in[i] = v < vecs;
-        at[i] = v * kVec;
-        if (NV == 1) load_weights(i);
-    }
+    if (NV == 1) load_weights(0);
     fetch(blockIdx.x);
     int flip = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, flip ^= 2) {

@@ -1,6 +1,7 @@
 // ep_api.cu -- the C ABI declared in include/ep.h: host-side argument checks,
 // launch-shape choice and error reporting.  Every step of the work runs in
 // the kernels of layout.cu, dispatch.cu and combine.cu on the caller's stream.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -53,10 +54,14 @@ int64_t rows_of(const ep_shape_t* s) {
 }
 
 // The current device must be an sm_103 part (the only code this library holds).
+// What a device is does not change, so each is asked once.
 ep_status_t device_info(int* num_sms) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> known[kMaxDevices];     // SMs of an sm_103 device, 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail(EP_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    if (dev >= 0 && dev < kMaxDevices && (*num_sms = known[dev].load(std::memory_order_relaxed)) > 0) return ok();
     int major = 0, minor = 0;
     e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
@@ -65,6 +70,7 @@ ep_status_t device_info(int* num_sms) {
     if (major != 10 || minor != 3)
         return fail(EP_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library holds sm_103a code only", dev, major,
                     minor);
+    if (dev >= 0 && dev < kMaxDevices) known[dev].store(*num_sms, std::memory_order_relaxed);
     return ok();
 }
 
