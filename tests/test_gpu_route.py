@@ -232,3 +232,19 @@ def test_refusals():
     for bad in (dict(E=1025), dict(k=17), dict(k=0), dict(groups=3), dict(groups=16, topk_groups=17), dict(num_seqs=0), dict(T=-1)):
         with pytest.raises((ep.EPError, RuntimeError)):
             ep.Router(**{**dict(T=8, E=16, k=2), **bad})
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("E,k", [(64, 8), (256, 8), (300, 32), (1024, 20)])
+def test_logits_that_differ_in_their_last_bits(E, k, bias):
+    """Neighbours that agree in all but their lowest bits, in stretches of a few
+    and of more than a warp can hold, in any order of the experts."""
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    for width in (2, 5, 40, E):
+        step = torch.rand(64, E, generator=g, device="cuda").argsort(1)             # a permutation in each row
+        x = 1.0 + (step // width).float() * 0.01 + (step % width).float() * 2.0 ** -23
+        b = torch.zeros(E, device="cuda") if bias else None
+        check(x, k, bias=b)
+        check(-x, k, bias=b)
+        if E % 4 == 0:
+            check(x, k, 4, 2, bias=b)
