@@ -185,7 +185,7 @@ struct RouteParams {
     uint32_t* err_flags;
     int64_t ld;
     int T, E, k, groups, topk_groups, full_softmax, f32, S;
-    int chunk;                   // set by the launchers
+    int chunk, per_group;        // set by the launchers
     float balance_coef, z_coef;
 };
 

@@ -48,8 +48,12 @@ __device__ __forceinline__ int seq_begin(const RouteParams& p, int s) {
 }
 
 __device__ __forceinline__ Run find_run(const RouteParams& p, int c) {
+    if (p.seq_offsets == nullptr) {
+        const int64_t first = (int64_t)c * p.chunk;
+        return Run{0, (int)min(first, (int64_t)p.T), (int)min(first + p.chunk, (int64_t)p.T)};
+    }
     int lo = 0, hi = p.S - 1;
-    if (p.seq_offsets != nullptr) {
+    {
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (seq_begin(p, mid) / p.chunk + mid <= c)
@@ -105,7 +109,9 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteParams& p, int per,
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             uint32_t m = key[i];
-            for (int d = min(per, 32) >> 1; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1)
+                if (d < per) m = max(m, __shfl_xor_sync(kAll, m, d));
             const int e = i * 32 + lane;
             if (e < p.E && (lane & (per - 1)) == 0) {
                 if (per <= 32 || (i * 32 & (per - 1)) == 0)
@@ -211,11 +217,11 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32) route_kernel(const __grid
     uint32_t* group_bit = reinterpret_cast<uint32_t*>(smem) + p.E;
     float* prob = reinterpret_cast<float*>(smem) + 2 * p.E;
     const bool sums = p.losses != nullptr, exact = !F32 && p.select_bias == nullptr;
-    const int per = p.E / p.groups;
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        hist[e] = 0;
-        group_bit[e] = 1u << (e / per);
-    }
+    const int per = p.per_group;
+    if (sums)
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+    if (p.groups > 1)
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) group_bit[e] = 1u << (e / per);
     pdl_launch_dependents();
     pdl_wait();
     if (sums && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
@@ -273,22 +279,33 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32) route_kernel(const __grid
         sort_down<NPL>(word);
         uint32_t mine = 0, last = 0;
         bool close = false;
-        int count = 0;
-        for (; count < 32; ++count) {
-            const uint32_t best = __reduce_max_sync(kAll, word[0]);
-            const bool same = (best ^ last) < 1024u;
-            if (best == 0 || (count >= p.k && (exact || !same))) break;
-            close |= same;
-            last = best;
-            if (lane == count) mine = best;
-            if (word[0] == best) {
+        auto pop = [&](uint32_t best) {
+            const bool own = word[0] == best;
 #pragma unroll
-                for (int i = 0; i + 1 < NPL; ++i) word[i] = word[i + 1];
-                word[NPL - 1] = 0;
+            for (int i = 0; i + 1 < NPL; ++i) word[i] = own ? word[i + 1] : word[i];
+            word[NPL - 1] = own ? 0u : word[NPL - 1];
+        };
+        int count = p.k;
+#pragma unroll 4
+        for (int j = 0; j < p.k; ++j) {
+            const uint32_t best = __reduce_max_sync(kAll, word[0]);     // 0 once nothing is left
+            close |= best != 0 && (best ^ last) < 1024u;
+            last = best;
+            mine = lane == j ? best : mine;
+            pop(best);
+        }
+        if (!exact) {
+            for (; count < 32; ++count) {
+                const uint32_t next_best = __reduce_max_sync(kAll, word[0]);
+                if (next_best == 0 || (next_best ^ last) >= 1024u) break;
+                close = true;
+                last = next_best;
+                mine = lane == count ? next_best : mine;
+                pop(next_best);
             }
         }
         int chosen = mine != 0 ? 1023 - (int)(mine & 1023u) : -1;
-        if (!exact && count == 32 && (__reduce_max_sync(kAll, word[0]) ^ last) < 1024u)
+        if (!exact && count == 32 && last != 0 && (__reduce_max_sync(kAll, word[0]) ^ last) < 1024u)
             chosen = choose_exactly<F32>(p, t, per, keep);       // the stretch goes on
         else if (!exact && close)
             chosen = reorder<F32>(p, t, chosen, count);
@@ -596,13 +613,14 @@ size_t route_workspace(RouteParams* p, void* base) {
 cudaError_t launch_route(const RouteParams& in, int num_sms, cudaStream_t stream) {
     RouteParams p = in;
     const bool sums = p.losses != nullptr;
+    p.per_group = p.E / p.groups;
     if (!sums) {
         p.seq_offsets = nullptr;
         p.S = 1;
     }
     const int warps = sums ? kRunWarps : kChoiceWarps;
-    // one token a warp until there are 16 CTAs for every SM
-    p.chunk = sums ? run_tokens(p.T) : kChoiceWarps * std::min(std::max(p.T / (kChoiceWarps * 16 * num_sms), 1), kChoiceTokens);
+    // one token a warp until there are 8 CTAs for every SM
+    p.chunk = sums ? run_tokens(p.T) : kChoiceWarps * std::min(std::max(p.T / (kChoiceWarps * 8 * num_sms), 1), kChoiceTokens);
     const dim3 grid((unsigned)std::max<int64_t>(num_runs(p.T, p.chunk, p.S), 1)), block(warps * 32);
     const size_t smem = (size_t)(2 + (sums ? kRunWarps : 0)) * p.E * 4;
     cudaError_t e = p.f32 ? launch_forward<true>(p, grid, block, smem, stream) : launch_forward<false>(p, grid, block, smem, stream);
