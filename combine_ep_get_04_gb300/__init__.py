@@ -7,7 +7,12 @@ module only checks tensors and passes their addresses.
     plan = Plan(T, H, E, k, num_partitions=P, capacity=None, fp8=False)
     plan.layout(topk_idx)           # counts, offsets, slot_of, src maps
     plan.dispatch(x, topk_w)        # recv (+ recv_scales, recv_w)
+    plan.expert_w4(weights)         # the experts' products over recv, 4-bit weights
     plan.combine(y, topk_w)         # out
+
+Around them, the ends of a mixture-of-experts block: Router (the choice of
+experts with its losses and gradients), W4Weights / expert_w4 and BlockNorm
+(the norms, gate and residual sum between two blocks, with gradients).
 
 The operations follow the DeepEP pages: per-expert counts and expert ->
 partition mapping ("Redundant atomics in internode_ll", quoted dispatch
@@ -247,6 +252,21 @@ class Plan:
             _ptr(self.layout_out.err_flags), _stream(stream))
         check(st, "ep_combine_src")
         return out
+
+    def expert_w4(self, weights: W4Weights, x: torch.Tensor | None = None, x_scales: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+        """Every expert's product with 4-bit weights over its rows of this plan's
+        last layout: x [R, K] is the receive buffer (the default) or what an
+        earlier product made of it.  Returns bf16 [R, weights.N]."""
+        s, L = self.shape, self.layout_out
+        if weights.E != s.E:
+            raise ValueError(f"the plan has {s.E} experts, the weights {weights.E}")
+        if x is None:
+            x, x_scales = self.recv, self.recv_scales
+        if x.shape[0] != self.R:
+            raise ValueError(f"x must have {self.R} rows, got {x.shape[0]}")
+        return expert_w4(x, weights, L.counts, L.offsets, capacity=s.capacity if s.mode == CAPACITY else None, x_scales=x_scales,
+                         max_rows=s.T * s.k, out=out, err_flags=L.err_flags, stream=stream)
 
 
 # ------------------------------------------------------- one-shot helpers
