@@ -16,6 +16,7 @@
 // through one fused multiply-add with the group's scale.
 #include <algorithm>
 #include <cuda.h>
+#include <type_traits>
 
 #include "ep_device.cuh"
 #include "ep_kernels.h"
@@ -120,21 +121,32 @@ __device__ __forceinline__ void unpack(uint32_t word, uint32_t (&pair)[4]) {
     for (int j = 0; j < 4; ++j) pair[j] = (j < 2 ? word : word >> 8) & (j & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 
-// Beside bf16 rows one fused multiply-add brings the pairs up to (code - 8) *
-// 2^-6: products with numbers as small as theirs would underflow.  Exact.
+// One fused multiply-add brings the pairs up to (code - 8) * 2^-6 in bf16 or
+// (code - 8) * 2^-9 in f16.  Exact.
+template <bool F16>
 __device__ __forceinline__ void widen(uint32_t (&pair)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)    // by 2^127 or 2^123, less 8 * 2^-6
-        asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(pair[j]) : "r"(j & 1 ? 0x7d007d00u : 0x7f007f00u), "r"(0xbe00be00u));
+    for (int j = 0; j < 4; ++j) {
+        if (F16)       // by 2^15 or 2^11, less 8 * 2^-9
+            asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(pair[j]) : "r"(j & 1 ? 0x68006800u : 0x78007800u), "r"(0xa400a400u));
+        else           // by 2^127 or 2^123, less 8 * 2^-6
+            asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(pair[j]) : "r"(j & 1 ? 0x7d007d00u : 0x7f007f00u), "r"(0xbe00be00u));
+    }
 }
 
-// Beside fp8 rows the f16 pairs enter the product as they are, the low kind
-// with rows 16 times as large, so that all products are in units of 2^-20;
-// -8 in both units, for the product that takes the offset off.
+// Beside fp8 rows (bf16 would underflow) the pairs can enter the product as
+// they are, the low kind with rows 16 times as large, so that all products are
+// in units of 2^-20, and a product with -8 in the same units takes the offset
+// off: with NL x 8 tokens 8 NL products for the warp's two tiles in place of 64
+// multiply-adds.  That pays while the tensor cores have time to spare, up to 16
+// tokens (256 experts, 4 rows each, gate and up: 650 against 781 us).
+template <bool FP8, int NL>
+constexpr bool kBare = FP8 && NL <= 2;
 constexpr uint32_t kMinusEightLow = 0x80088008u, kMinusEightHigh = 0x80808080u;
 
-template <bool FP8>
-constexpr float kUnit = FP8 ? 1048576.f : 64.f;      // what the codes are divided by
+// What the codes are divided by.
+template <bool FP8, int NL>
+constexpr float kUnit = kBare<FP8, NL> ? 1048576.f : FP8 ? 512.f : 64.f;
 
 // Four e4m3 codes -> two pairs of f16, exact.
 __device__ __forceinline__ void f16x2_of_e4m3x4(uint32_t codes, uint32_t* lo, uint32_t* hi) {
@@ -302,7 +314,7 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
             for (int h = 0; h < 2; ++h) {
                 uint32_t pair[4];
                 unpack(w[u][h][i], pair);
-                if (!FP8) widen(pair);
+                if (!kBare<FP8, NL>) widen<FP8>(pair);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[u][j & 1][(j >> 1) * 2 + h] = pair[j];
             }
@@ -313,8 +325,10 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
                 const uint2 v = *reinterpret_cast<const uint2*>(xr + n * kTile + i * kChunk);
                 f16x2_of_e4m3x4(v.x, &b[0], &b[1]);
                 f16x2_of_e4m3x4(v.y, &b[2], &b[3]);
-                b[0] = times16(b[0]);
-                b[2] = times16(b[2]);
+                if (kBare<FP8, NL>) {
+                    b[0] = times16(b[0]);
+                    b[2] = times16(b[2]);
+                }
             } else {
                 const uint4 v = *reinterpret_cast<const uint4*>(xr + n * kTile + i * kChunk);
                 b[0] = v.x;
@@ -331,7 +345,7 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
             };
 #pragma unroll
             for (int u = 0; u < kOwn; ++u) multiply(part[u][n], a[u][0], a[u][1]);
-            if (FP8) {
+            if (kBare<FP8, NL>) {
                 const uint32_t low[4] = {kMinusEightLow, kMinusEightLow, kMinusEightLow, kMinusEightLow};
                 const uint32_t high[4] = {kMinusEightHigh, kMinusEightHigh, kMinusEightHigh, kMinusEightHigh};
                 multiply(eights[n], low, high);
@@ -348,10 +362,11 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
                     const float (&d)[4] = part[u][n];
                     if (FP8) {
                         const float2 q = *reinterpret_cast<const float2*>(xs + n * 8);
-                        v[0] = fmaf(d[0] + eights[n][0], s0 * q.x, v[0]);
-                        v[1] = fmaf(d[1] + eights[n][1], s0 * q.y, v[1]);
-                        v[2] = fmaf(d[2] + eights[n][2], s1 * q.x, v[2]);
-                        v[3] = fmaf(d[3] + eights[n][3], s1 * q.y, v[3]);
+                        const bool bare = kBare<FP8, NL>;
+                        v[0] = fmaf(bare ? d[0] + eights[n][0] : d[0], s0 * q.x, v[0]);
+                        v[1] = fmaf(bare ? d[1] + eights[n][1] : d[1], s0 * q.y, v[1]);
+                        v[2] = fmaf(bare ? d[2] + eights[n][2] : d[2], s1 * q.x, v[2]);
+                        v[3] = fmaf(bare ? d[3] + eights[n][3] : d[3], s1 * q.y, v[3]);
                     } else {
                         v[0] = fmaf(d[0], s0, v[0]);
                         v[1] = fmaf(d[1], s0, v[1]);
@@ -402,7 +417,7 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
 // each) and add their accumulators through distributed shared memory in the
 // order of the shares.
 template <int NT, int G, bool FP8>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 2) expert_w4_kernel(W4Params p, const __grid_constant__ CUtensorMap rows_map, int splits, int units,
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4Params p, const __grid_constant__ CUtensorMap rows_map, int splits, int units,
                                                                                     int grid_tiles) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kRing], empty[kRing];
@@ -528,17 +543,26 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 2) expert_w4_kernel(W4
         for (int u = 0; u < kOwn; ++u)
 #pragma unroll
             for (int n = 0; n < NT; ++n) clear(acc[u][n]);
-        // tiles that are at most half full take the form made for that
-        constexpr int kHalf = NT > 1 ? NT / 2 : 1;
-        good = tile.rows <= 8 * kHalf ? consume<NT, kHalf, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0, stage, parity)
-                                      : consume<NT, NT, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0, stage, parity);
+        // a form for each number of 8-token columns in use
+        auto walk = [&](auto columns) {
+            constexpr int NL = decltype(columns)::value < NT ? decltype(columns)::value : NT;
+            good = consume<NT, NL, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0, stage, parity);
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u)
+#pragma unroll
+                for (int n = 0; n < NL; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[u][n][c] *= kUnit<FP8, NL>;      // a power of two
+        };
+        if (NT == 1 || (NT == 2 && tile.rows <= 8))
+            walk(std::integral_constant<int, 1>{});
+        else if (NT == 2 || tile.rows <= 16)
+            walk(std::integral_constant<int, 2>{});
+        else if (tile.rows <= 24)
+            walk(std::integral_constant<int, 3>{});
+        else
+            walk(std::integral_constant<int, 4>{});
         if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
-#pragma unroll
-        for (int u = 0; u < kOwn; ++u)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[u][n][c] *= kUnit<FP8>;      // a power of two
         if (splits > 1) {
             // share i adds up the tiles i, i + splits, ...: the others send it theirs
             const int owned = kTiles / splits;
