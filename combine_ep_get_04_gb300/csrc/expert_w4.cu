@@ -137,11 +137,12 @@ __device__ __forceinline__ void widen(uint32_t (&pair)[4]) {
 // Beside fp8 rows (bf16 would underflow) the pairs can enter the product as
 // they are, the low kind with rows 16 times as large, so that all products are
 // in units of 2^-20, and a product with -8 in the same units takes the offset
-// off: with NL x 8 tokens 8 NL products for the warp's two tiles in place of 64
-// multiply-adds.  That pays while the tensor cores have time to spare, up to 16
-// tokens (256 experts, 4 rows each, gate and up: 650 against 781 us).
+// off: 8 products for each 8 tokens of the warp's two tiles in place of 64
+// multiply-adds.  With one column of 8 tokens the instructions saved decide,
+// with more the products added (256 experts, 4 rows each, gate and up: 781 us
+// without, 626 us with one column so, 650 us with two).
 template <bool FP8, int NL>
-constexpr bool kBare = FP8 && NL <= 2;
+constexpr bool kBare = FP8 && NL == 1;
 constexpr uint32_t kMinusEightLow = 0x80088008u, kMinusEightHigh = 0x80808080u;
 
 // What the codes are divided by.
