@@ -170,7 +170,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 __device__ __forceinline__ void clear(float (&v)[4]) { v[0] = v[1] = v[2] = v[3] = 0.f; }
 
-__device__ __forceinline__ float silu(float x) { return x / (1.f + __expf(-x)); }
+// Both functions are good to a few units in the last place of fp32; the result is rounded to bf16.
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
 struct RowTile {
     int e;          // expert, -1: none
@@ -201,15 +202,17 @@ __device__ __forceinline__ int tiles_of(int rows, int tile_rows) {
     return (rows >> (31 - __clz(tile_rows))) + ((rows & (tile_rows - 1)) != 0);
 }
 
+constexpr int kMaxTiles = (1 << 26) - 1;     // 32 lanes' worth of them fit 31 bits
 constexpr int kScan = 8;    // experts whose rows a lane looks up at a time: their loads are in flight together
 
 // Tile `at` in the order of experts and of rows within an expert.  One warp;
 // lane l counts the tiles of experts [l * per, (l + 1) * per).
-__device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_tiles) {
+__device__ __forceinline__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_tiles) {
     const int lane = threadIdx.x & 31;
     const int per = (p.w.E + 31) / 32;
     const int e0 = min(lane * per, p.w.E), e1 = min(e0 + per, p.w.E);
-    int64_t mine = 0;          // 64 bits: bad offsets may claim every row many times
+    // bad offsets may claim every row many times: a lane's sum is cut off where no good layout comes to
+    int mine = 0;
     bool any_bad = false;
     int64_t first[kScan];
     int n[kScan];
@@ -227,15 +230,15 @@ __device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_
     for (int from = e0; from < e1; from += kScan) {
         look_up(from);
 #pragma unroll
-        for (int j = 0; j < kScan; ++j) mine += tiles_of(n[j], tile_rows);
+        for (int j = 0; j < kScan; ++j) mine = min(mine + tiles_of(n[j], tile_rows), kMaxTiles);
     }
-    int64_t upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+        const int v = __shfl_up_sync(0xffffffffu, upto, d);
         if (lane >= d) upto += v;
     }
-    const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+    const int total = __shfl_sync(0xffffffffu, upto, 31);
     if (at == 0 && p.err_flags != nullptr) {
         if (any_bad) atomicOr(p.err_flags, kErrBadSlot);
         if (total > grid_tiles && lane == 0) atomicOr(p.err_flags, kErrCapacity);
@@ -244,14 +247,14 @@ __device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_
     if (at >= total) return r;
     const int owner = __ffs(__ballot_sync(0xffffffffu, upto > at)) - 1;
     if (lane == owner) {
-        int64_t left = at - (upto - mine);
+        int left = at - (upto - mine);
         for (int from = e0; from < e1 && r.e < 0; from += kScan) {
             if (per > kScan) look_up(from);       // else n still holds them all
 #pragma unroll
             for (int j = 0; j < kScan; ++j) {
                 const int tiles = tiles_of(n[j], tile_rows);
                 if (r.e < 0 && left >= 0 && left < tiles)
-                    r = RowTile{from + j, (int)min(n[j] - left * tile_rows, (int64_t)tile_rows), first[j] + left * tile_rows};
+                    r = RowTile{from + j, min(n[j] - left * tile_rows, tile_rows), first[j] + (int64_t)left * tile_rows};
                 left -= tiles;
             }
         }
@@ -260,6 +263,19 @@ __device__ RowTile find_tile(const W4Params& p, int at, int tile_rows, int grid_
     r.rows = __shfl_sync(0xffffffffu, r.rows, owner);
     r.first = __shfl_sync(0xffffffffu, r.first, owner);
     return r;
+}
+
+// The same for a single matrix: every thread looks for itself.
+__device__ __forceinline__ RowTile tile_of_one(const W4Params& p, int at, int tile_rows, int grid_tiles) {
+    int64_t first;
+    bool bad;
+    const int n = expert_rows(p, 0, &first, &bad), tiles = tiles_of(n, tile_rows);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.err_flags != nullptr) {
+        if (bad) atomicOr(p.err_flags, kErrBadSlot);
+        if (tiles > grid_tiles) atomicOr(p.err_flags, kErrCapacity);
+    }
+    if (at >= tiles) return RowTile{-1, 0, 0};
+    return RowTile{0, min(n - at * tile_rows, tile_rows), first + (int64_t)at * tile_rows};
 }
 
 // Starts bringing `bytes` (a multiple of 16) at a 16-byte boundary into L2.
@@ -443,14 +459,37 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4
         fence_mbar_init();
     }
     pdl_wait();
-    if (warp == 0) {
-        const RowTile r = find_tile(p, at, kRows, grid_tiles);
-        if (lane == 0) shared_tile = r;
+    // a single matrix: the producer starts on its first stages while the rows are looked up
+    int primed = 0;
+    RowTile tile;
+    if (p.w.E == 1) {
+        __syncthreads();
+        if (warp == kWarps) {
+            for (; primed < kRing && kb0 + primed * kStep < kb1; ++primed)
+                if (lane == 0) {
+                    const uint32_t bytes = kWeights * min(kStep, kb1 - kb0 - primed * kStep);
+                    mbar_expect_tx(&full[primed], bytes);
+                    bulk_load(smem + primed * kStage, weights + (int64_t)primed * kStep * kWeights, bytes, &full[primed]);
+                }
+        }
+        tile = tile_of_one(p, at, kRows, grid_tiles);
+    } else {
+        if (warp == 0) {
+            const RowTile r = find_tile(p, at, kRows, grid_tiles);
+            if (lane == 0) shared_tile = r;
+        }
+        __syncthreads();
+        tile = shared_tile;
     }
-    __syncthreads();
     if (splits > 1) cluster_arrive();
-    const RowTile tile = shared_tile;
     if (tile.e < 0) {                    // the same in all CTAs of a cluster
+        if (warp == kWarps)
+            for (int s = 0; s < primed; ++s) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+                mbar_wait(&full[s], 0);
+            }
+        __syncwarp();
         if (splits > 1) cluster_wait();
         return;
     }
@@ -499,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4
                     if (lane == 0) {
                         constexpr int kBox = x_chunk(NT, FP8);
                         const int boxes = blocks_here * (kTileK / 32);
-                        mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + boxes * kBox);
-                        bulk_load(st, weight, kWeights * blocks_here, &full[s]);
+                        mbar_arrive_expect_tx(&full[s], (filled < primed ? 0 : kWeights * blocks_here) + boxes * kBox);
+                        if (filled >= primed) bulk_load(st, weight, kWeights * blocks_here, &full[s]);
                         for (int i = 0; i < boxes; ++i)
                             box_load(xt + i * kBox, &rows_map, kb * kTileK + i * 32, (int)tile.first, &full[s]);
                     }
@@ -514,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4
                         __syncwarp();
                     }
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&full[s], kWeights * blocks_here + piece * tile.rows);
-                        bulk_load(st, weight, kWeights * blocks_here, &full[s]);
+                        mbar_arrive_expect_tx(&full[s], (filled < primed ? 0 : kWeights * blocks_here) + piece * tile.rows);
+                        if (filled >= primed) bulk_load(st, weight, kWeights * blocks_here, &full[s]);
                         const unsigned char* from = x + (int64_t)kb * kTileK * kSize;
                         for (int r = 0; r < tile.rows; ++r, xt += kRow, from += row_bytes) bulk_load(xt, from, piece, &full[s]);
                     }
@@ -678,7 +717,8 @@ template <int NT>
 cudaError_t launch_rows(const W4Params& p, int num_sms, cudaStream_t stream) {
     // every row in a tile of its expert: full tiles, and a last one for each expert in use
     const int64_t tiles = std::min<int64_t>(p.w.E, p.max_rows) + p.max_rows / (8 * NT);
-    const int64_t products = std::min<int64_t>(p.w.E, p.max_rows) * row_blocks(p.w);
+    // tiles there will be: one for each expert in use, or full ones
+    const int64_t products = std::max<int64_t>(std::min<int64_t>(p.w.E, p.max_rows), p.max_rows / (8 * NT)) * row_blocks(p.w);
     // few products: share K among the CTAs of a cluster until there are two CTAs for every SM (one with wide tiles, of
     // which two fit an SM)
     int splits = 1;
@@ -700,7 +740,7 @@ bool w4_packs(const W4Shape& w) { return (int64_t)w.E * row_blocks(w) * k_blocks
 bool w4_fits(const W4Shape& w, int64_t max_rows, int fp8) {
     // shared memory of the widest form, CTAs of the narrowest
     return w4_smem(w, 4, fp8 != 0, 8) <= kMaxSmem &&
-           (std::min<int64_t>(w.E, max_rows) + max_rows / 8) * row_blocks(w) * 8 <= INT32_MAX;
+           (std::min<int64_t>(w.E, max_rows) + max_rows / 8) * row_blocks(w) * 8 <= INT32_MAX && max_rows <= (int64_t)1 << 29;
 }
 
 cudaError_t launch_w4_pack(const W4Shape& w, const uint8_t* codes, const void* scales, void* packed, cudaStream_t stream) {
