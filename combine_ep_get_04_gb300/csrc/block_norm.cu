@@ -216,13 +216,16 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 // ---------------------------------------------------------------- backward
 //
 // A row needs one reduction only: with e = d_h_out + r2 t (t = d_n w_pre) and
-// u = yn w_post, the gradient is d = e - hn * (r2 m2), m2 = mean(t hn), so that
-// the second norm's mean(g d u) = (sum g u e - r2 m2 sum g u hn) / H follows from
-// sums that are known before m2 is.
+// v = y w_post (times a channel's gate), the gradient is d = e - hn * (r2 m2),
+// m2 = mean(t hn), so that the second norm's mean follows from sums that are
+// known before m2 is: sum(v d) = sum(v e) - r2 m2 sum(v hn).
+//
+// Over rows there are two sums to a column: d_n hn, which is d_w_pre, and
+// r1 d y (times a token's gate), which times the gate is d_w_post and times
+// w_post the gradient of a channel's gate.
 //
 // A CTA owns up to kCols columns, one vector of 8 to a thread, and keeps their
-// weights and their sums over rows (d_w_post, d_w_pre, a channel gate's
-// gradient) in registers for all its rows; wider rows are shared by a cluster
+// weights and their sums over rows in registers for all its rows; wider rows are shared by a cluster
 // of CTAs.  A producer warp keeps a ring of row stages filled by bulk copies.
 // Consumer warps leave their share of a row's three sums to another warp, which
 // adds them and passes them to every CTA of the cluster (pass 1), and take up
@@ -285,9 +288,22 @@ __device__ __forceinline__ void send(uint32_t to, float a, float b, float c, uin
 
 // What a row's threads all need; gate is the token's.
 struct __align__(16) RowValues {
-    float r1, r2, r2_scale, r2_gate;
-    float gate, r1_gate, unused[2];
+    float r2, r2_scale, r2_r1_gate, r1_gate;
+    float r1, gate, unused[2];
 };
+
+// Sums of three values over a warp in six shuffles: lane 0 ends up with the
+// first, lane 16 with the second, lane 8 with the third.
+__device__ __forceinline__ float warp_sum3(float x0, float x1, float x2) {
+    const int lane = threadIdx.x & 31;
+    const bool high = lane & 16, third = lane & 8;
+    float y = (high ? x1 : x0) + __shfl_xor_sync(0xffffffffu, high ? x0 : x1, 16);
+    x2 += __shfl_xor_sync(0xffffffffu, x2, 16);
+    y = (third ? x2 : y) + __shfl_xor_sync(0xffffffffu, third ? y : x2, 8);
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+    return y;
+}
 
 // FULL: y, d_n and d_h_out are there, which saves the tests for them.
 // WARPS: most warps of a CTA; up to 16 a thread has 128 registers, which is what it needs, with 18 it has 96.
@@ -355,7 +371,7 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
                 if (has_dh)
                     bulk_load(to + at_dh, static_cast<const unsigned char*>(p.d_h_out) + (t * p.H + col0) * kStream, wide, &full[st]);
             }
-            if (lane == 1) row_values[st] = RowValues{r1, r2, r2 * scale, r2 * gate, gate, r1 * gate, {0.f, 0.f}};
+            if (lane == 1) row_values[st] = RowValues{r2, r2 * scale, r2 * r1 * gate, r1 * gate, r1, gate, {0.f, 0.f}};
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);          // after the row's values are written
             look_up(filled + 1);
@@ -392,10 +408,15 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
         const bool in = v * kVec < cols;                   // the others go through it with weights of 0 and store nothing
         const int c0 = in ? v * kVec : 0;                  // column within the CTA
         const float inv_h = 1.f / (float)p.H;
-        const Vec8 w = in ? (p.w_post != nullptr ? load_f32(p.w_post, col0 + c0) : all(1.f)) : all(0.f);
-        const Vec8 g = in ? (p.gate_kind == kGateChannel ? load_f32(p.gate, col0 + c0) : all(1.f)) : all(0.f);
         const Vec8 q = in && p.w_pre != nullptr ? load_f32(p.w_pre, col0 + c0) : all(0.f);
-        Vec8 s_post = all(0.f), s_gate = all(0.f), s_pre = all(0.f);
+        Vec8 wg = all(in ? 1.f : 0.f);
+        if (in && p.w_post != nullptr) wg = load_f32(p.w_post, col0 + c0);
+        if (in && p.gate_kind == kGateChannel) {
+            const Vec8 g = load_f32(p.gate, col0 + c0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wg.v[c] = mul2(wg.v[c], g.v[c]);
+        }
+        Vec8 s_dy = all(0.f), s_pre = all(0.f);
         uint64_t s_scale = both(0.f);
         const unsigned char* first = ring + c0 * 2;        // the thread's place in a bf16 row
         auto take = [&](int at, Vec8& h, Vec8& dh, Vec8& y, Vec8& dn) {
@@ -420,29 +441,26 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
                 uint64_t sum0 = both(0.f), sum1 = sum0, sum2 = sum0;
                 {
                     const RowValues& rv = row_values[st1];
-                    const uint64_t r1 = both(rv.r1), r2 = both(rv.r2), r2_scale = both(rv.r2_scale), r2_gate = both(rv.r2_gate);
+                    const uint64_t r2 = both(rv.r2), r2_scale = both(rv.r2_scale), r2_r1_gate = both(rv.r2_r1_gate);
                     Vec8 h, dh, y, dn;
                     take(at1, h, dh, y, dn);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const uint64_t gu = mul2(g.v[c], mul2(mul2(y.v[c], r1), w.v[c]));
-                        const uint64_t hn = fma2(r2_scale, h.v[c], mul2(r2_gate, gu));
+                        const uint64_t v = mul2(y.v[c], wg.v[c]);
+                        const uint64_t hn = fma2(r2_r1_gate, v, mul2(r2_scale, h.v[c]));
                         const uint64_t t = mul2(dn.v[c], q.v[c]);
                         const uint64_t e = fma2(r2, t, dh.v[c]);
                         s_pre.v[c] = fma2(dn.v[c], hn, s_pre.v[c]);
                         sum0 = fma2(t, hn, sum0);
-                        sum1 = fma2(gu, e, sum1);
-                        sum2 = fma2(gu, hn, sum2);
+                        sum1 = fma2(v, e, sum1);
+                        sum2 = fma2(v, hn, sum2);
                     }
                 }
-                const float x0 = warp_sum(total(sum0)), x1 = warp_sum(total(sum1)), x2 = warp_sum(total(sum2));
+                const float x = warp_sum3(total(sum0), total(sum1), total(sum2));
                 const int slot = i % kSlots;
-                if (lane == 0) {
-                    warp_sums[slot][0][warp] = x0;
-                    warp_sums[slot][1][warp] = x1;
-                    warp_sums[slot][2][warp] = x2;
-                    mbar_arrive(&added[slot]);
-                }
+                if ((lane & 7) == 0 && lane != 24) warp_sums[slot][lane == 0 ? 0 : lane == 16 ? 1 : 2][warp] = x;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&added[slot]);
                 at1 += stage_bytes;
                 if (++st1 == s.stages) {
                     st1 = at1 = 0;
@@ -465,27 +483,25 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
                     }
                 const RowValues& rv = row_values[st2];
                 const float m2 = rv.r2 * (x.x * inv_h);
-                const float gu_d = x.y - m2 * x.z;          // sum of g u d (without a token's gate)
-                const float m1 = p.w_post != nullptr ? rv.gate * gu_d * inv_h : 0.f;
+                const float u_d = rv.r1 * (x.y - m2 * x.z);          // sum of g u d (without a token's gate)
+                const float m1 = p.w_post != nullptr ? rv.gate * u_d * inv_h : 0.f;
                 if (d_gate != nullptr) {
-                    *d_gate = gu_d;
+                    *d_gate = u_d;
                     d_gate += s.clusters;
                 }
-                const uint64_t r1 = both(rv.r1), r2 = both(rv.r2), r2_scale = both(rv.r2_scale), r2_gate = both(rv.r2_gate);
-                const uint64_t gate = both(rv.gate), a2 = both(scale), minus_m2 = both(-m2), r1_gate = both(rv.r1_gate), back = both(-rv.r1 * m1);
+                const uint64_t r2 = both(rv.r2), r2_scale = both(rv.r2_scale), r2_r1_gate = both(rv.r2_r1_gate);
+                const uint64_t r1_gate = both(rv.r1_gate), a2 = both(scale), minus_m2 = both(-m2), back = both(-rv.r1 * rv.r1 * m1);
                 Vec8 h, dh, y, dn, d_h, d_y;
                 take(at2, h, dh, y, dn);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint64_t yn = mul2(y.v[c], r1), u = mul2(yn, w.v[c]);
-                    const uint64_t hn = fma2(r2_scale, h.v[c], mul2(r2_gate, mul2(g.v[c], u)));
+                    const uint64_t hn = fma2(r2_r1_gate, mul2(y.v[c], wg.v[c]), mul2(r2_scale, h.v[c]));
                     const uint64_t e = fma2(r2, mul2(dn.v[c], q.v[c]), dh.v[c]);
-                    const uint64_t d = fma2(minus_m2, hn, e), gd = mul2(g.v[c], d);
+                    const uint64_t d = fma2(minus_m2, hn, e), rd = mul2(r1_gate, d);
                     s_scale = fma2(d, h.v[c], s_scale);
-                    s_gate.v[c] = fma2(d, u, s_gate.v[c]);
-                    s_post.v[c] = fma2(gd, mul2(yn, gate), s_post.v[c]);
+                    s_dy.v[c] = fma2(rd, y.v[c], s_dy.v[c]);
                     d_h.v[c] = mul2(a2, d);
-                    d_y.v[c] = fma2(mul2(gd, w.v[c]), r1_gate, mul2(yn, back));
+                    d_y.v[c] = fma2(wg.v[c], rd, mul2(back, y.v[c]));
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st2]);
@@ -502,10 +518,9 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
         const float sum = warp_sum(in ? total(s_scale) : 0.f);
         if (lane == 0) scale_part[warp] = sum;
         if (in) {
-            float* out = p.partial + (int64_t)group * 3 * p.H + col0 + c0;
-            store_f32(out, 0, s_post);
-            store_f32(out, p.H, s_gate);
-            store_f32(out, 2 * (int64_t)p.H, s_pre);
+            float* out = p.partial + (int64_t)group * 2 * p.H + col0 + c0;
+            store_f32(out, 0, s_dy);
+            store_f32(out, p.H, s_pre);
         }
     }
     if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
@@ -513,7 +528,7 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
     if (threadIdx.x == 0) {
         float sum = 0.f;
         for (int i = 0; i < s.warps; ++i) sum += scale_part[i];
-        p.partial[(int64_t)s.clusters * 3 * p.H + blockIdx.x] = sum;
+        p.partial[(int64_t)s.clusters * 2 * p.H + blockIdx.x] = sum;
     }
     if (s.cluster > 1) cluster_barrier();      // no CTA ends while another may still write to it
 }
@@ -525,7 +540,7 @@ __global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormPar
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t width = 3 * (int64_t)p.H;
+    const int64_t width = 2 * (int64_t)p.H;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < width)
@@ -537,9 +552,13 @@ __global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormPar
         s = 0.f;
 #pragma unroll
         for (int i = 0; i < kColumnWarps; ++i) s += part[i][lane];
-        const int which = (int)(c / p.H), at = (int)(c % p.H);
-        float* out = which == 0 ? p.d_w_post : which == 1 ? (p.gate_kind == kGateChannel ? p.d_gate : nullptr) : p.d_w_pre;
-        if (out != nullptr) out[at] = s;
+        if (c >= p.H) {
+            if (p.d_w_pre != nullptr) p.d_w_pre[c - p.H] = s;
+        } else {
+            const bool channel = p.gate_kind == kGateChannel;
+            if (p.d_w_post != nullptr) p.d_w_post[c] = channel ? s * p.gate[c] : s;
+            if (channel) p.d_gate[c] = p.w_post != nullptr ? s * p.w_post[c] : s;
+        }
     }
     if (blockIdx.x == 0 && warp == 1 && p.d_res_scale != nullptr) {
         s = 0.f;
@@ -570,7 +589,7 @@ BackwardShape backward_shape(int T, int H, int f32, int num_sms) {
 
 size_t workspace_bytes(int T, int H) {
     const BackwardShape s = backward_shape(T, H, 0, kMaxSms);
-    return ((size_t)s.clusters * (3 * (size_t)H + s.cluster) * sizeof(float) + 15) / 16 * 16;
+    return ((size_t)s.clusters * (2 * (size_t)H + s.cluster) * sizeof(float) + 15) / 16 * 16;
 }
 
 template <int NV, bool F32>
@@ -609,7 +628,7 @@ cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStr
         e = launch_clusters(true, s.cluster, kern, dim3(s.clusters * s.cluster), dim3(s.warps * 32 + 64), smem, stream, p, s);
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)((3 * (int64_t)p.H + 31) / 32));
+    const dim3 grid((unsigned)((2 * (int64_t)p.H + 31) / 32));
     return launch_kernel(true, norm_columns_kernel, grid, dim3(kColumnWarps * 32), 0, stream, p, s.clusters, s.clusters * s.cluster);
 }
 
