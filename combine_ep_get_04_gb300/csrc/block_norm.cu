@@ -228,14 +228,14 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 // weights and their sums over rows in registers for all its rows; wider rows are shared by a cluster
 // of CTAs.  A producer warp keeps a ring of row stages filled by bulk copies.
 // Consumer warps leave their share of a row's three sums to another warp, which
-// adds them and passes them to every CTA of the cluster (pass 1), and take up
-// the row again `lag` rows later (pass 2), when the sums have long arrived, so
+// adds them and joins them with those of the cluster's other CTAs (pass 1), and
+// take up the row again `lag` rows later (pass 2), when the sums are there, so
 // that none stands still at a row's end.  The CTAs'
 // sums over rows go to the workspace once, and norm_columns_kernel adds them in
 // CTA order, so that nothing depends on the order in which CTAs run.
 
 constexpr int kCols = 4096;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 4;
 constexpr int kSlots = 8;          // rows whose sums may be on their way; a writer is less than 6 rows ahead of a reader
 constexpr int kMaxWarps = kCols / kVec / 32;
@@ -261,29 +261,29 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t smem, int rank) {
     return a;
 }
 
-// mbar_wait for bytes that CTAs of the cluster send.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
+// A sum on its way between CTAs: the value and, in the same 64-bit word, which
+// row it is of, so that no fence has to order the two.  (An arrival on the
+// receiver's barrier with release semantics waits until the SM's stores have
+// drained, and with the gradients streaming out that took longer than a row.)
+__device__ __forceinline__ void post(uint32_t to, float value, uint32_t row) {
+    const uint64_t word = (uint64_t)row << 32 | __float_as_uint(value);
+    asm volatile("st.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(word) : "memory");
+}
+
+// Waits, at most kWaitLimitNs, for the word of `row` and returns its value.
+__device__ __forceinline__ bool collect(const uint64_t* from, uint32_t row, float* value) {
     uint64_t t0 = 0;
     for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (done) return true;
+        uint64_t word;
+        asm volatile("ld.relaxed.cluster.shared::cta.b64 %0, [%1];" : "=l"(word) : "r"(smem_addr(from)) : "memory");
+        if ((uint32_t)(word >> 32) == row) {
+            *value = __uint_as_float((uint32_t)word);
+            return true;
+        }
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
         if (now - t0 > kWaitLimitNs) return false;
     }
-}
-
-// Writes a row's sums to a CTA of the cluster and arrives on its barrier.
-__device__ __forceinline__ void send(uint32_t to, float a, float b, float c, uint32_t bar) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(a), "f"(b), "f"(c), "f"(0.f) : "memory");
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // What a row's threads all need; gate is the token's.
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], added[kSlots], summed[kSlots];
     __shared__ float warp_sums[kSlots][3][kMaxWarps];
-    __shared__ float4 sums[kSlots][kMaxCluster];
+    __shared__ float4 sums[kSlots];
+    __shared__ uint64_t posted[kSlots][kMaxCluster][4];       // the three sums of each CTA of the cluster
     __shared__ RowValues row_values[kMaxStages];
     __shared__ float scale_part[kMaxWarps];
     constexpr int kStream = F32 ? 4 : 2;
@@ -330,10 +331,11 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&added[i], s.warps);
-            mbar_init(&summed[i], s.cluster);
+            mbar_init(&summed[i], 1);
         }
         fence_mbar_init();
     }
+    for (int i = threadIdx.x; i < kSlots * kMaxCluster * 4; i += blockDim.x) (&posted[0][0][0])[i] = 0;
     __syncthreads();
     if (s.cluster > 1) cluster_barrier();
     pdl_wait();
@@ -383,24 +385,50 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
         // no copy may be in flight when the CTA ends, whatever its consumers did
         for (int i = max(0, filled - s.stages); i < filled; ++i) mbar_wait(&full[i % s.stages], (i / s.stages) & 1);
     } else if (warp == s.warps + 1) {
-        // adds the warps' sums of each row and passes them on
-        const uint32_t to = in_cta(smem_addr(&sums[0][rank]), lane < s.cluster ? lane : 0);
-        const uint32_t bar = in_cta(smem_addr(&summed[0]), lane < s.cluster ? lane : 0);
+        // adds the warps' sums of each row
         uint32_t parity = 0;
-        for (int i = 0; i < rows; ++i) {
-            const int slot = i % kSlots;
+        auto add = [&](int slot, float (&x)[3]) {
             good = __all_sync(0xffffffffu, mbar_wait(&added[slot], parity));
-            if (!good) break;
-            const bool has = lane < s.warps;
-            const float x0 = warp_sum(has ? warp_sums[slot][0][lane] : 0.f), x1 = warp_sum(has ? warp_sums[slot][1][lane] : 0.f),
-                        x2 = warp_sum(has ? warp_sums[slot][2][lane] : 0.f);
-            if (s.cluster > 1) {
-                if (lane < s.cluster) send(to + slot * (uint32_t)sizeof(sums[0]), x0, x1, x2, bar + slot * 8);
-            } else if (lane == 0) {
-                sums[slot][0] = make_float4(x0, x1, x2, 0.f);
-                mbar_arrive(&summed[slot]);
-            }
             if (slot == kSlots - 1) parity ^= 1;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) x[k] = warp_sum(lane < s.warps ? warp_sums[slot][k][lane] : 0.f);
+            return good;
+        };
+        if (s.cluster == 1) {
+            for (int i = 0; i < rows; ++i) {
+                const int slot = i % kSlots;
+                float x[3];
+                if (!add(slot, x)) break;
+                if (lane == 0) {
+                    sums[slot] = make_float4(x[0], x[1], x[2], 0.f);
+                    mbar_arrive(&summed[slot]);
+                }
+            }
+        } else {
+            // posts them to every CTA and joins those of the row before, which have arrived by now: lane 4 r + k deals
+            // with sum k of CTA r
+            const int r = lane >> 2, k = lane & 3;
+            const bool part = r < s.cluster && k < 3;
+            const uint32_t to = in_cta(smem_addr(&posted[0][rank][k]), part ? r : 0);
+            for (int i = 0; i <= rows; ++i) {
+                const int slot = i % kSlots;
+                if (i < rows) {
+                    float x[3];
+                    if (!add(slot, x)) break;
+                    if (part) post(to + slot * (uint32_t)sizeof(posted[0]), k == 0 ? x[0] : k == 1 ? x[1] : x[2], (uint32_t)i + 1);
+                }
+                if (i > 0) {
+                    const int before = (i - 1) % kSlots;
+                    float x = 0.f;
+                    good = __all_sync(0xffffffffu, !part || collect(&posted[before][r][k], (uint32_t)i, &x));
+                    if (!good) break;
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    if (lane < 3) (&sums[before].x)[lane] = x;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&summed[before]);
+                }
+            }
         }
         __syncwarp();
     } else {
@@ -470,17 +498,10 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
             if (i >= s.lag) {
                 // pass 2: the gradients of the row `lag` rows back
                 const int slot = (i - s.lag) % kSlots;
-                good = __all_sync(0xffffffffu, mbar_wait_cluster(&summed[slot], summed_parity));
+                good = __all_sync(0xffffffffu, mbar_wait(&summed[slot], summed_parity));
                 if (!good) break;
                 if (slot == kSlots - 1) summed_parity ^= 1;
-                float4 x = sums[slot][0];
-                if (s.cluster > 1)
-                    for (int k = 1; k < s.cluster; ++k) {
-                        const float4 more = sums[slot][k];
-                        x.x += more.x;
-                        x.y += more.y;
-                        x.z += more.z;
-                    }
+                const float4 x = sums[slot];
                 const RowValues& rv = row_values[st2];
                 const float m2 = rv.r2 * (x.x * inv_h);
                 const float u_d = rv.r1 * (x.y - m2 * x.z);          // sum of g u d (without a token's gate)
@@ -569,7 +590,7 @@ __global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormPar
 }
 
 constexpr int kMaxSms = 192;                      // the workspace has room for this many
-constexpr size_t kRingBytes = 200 * 1024;         // shared memory of an SM that the rings may take
+constexpr size_t kRingBytes = 216 * 1024;         // shared memory of an SM that the rings may take
 
 // clusters: at most this many, 0 for the workspace's bound.
 BackwardShape backward_shape(int T, int H, int f32, int num_sms) {
@@ -577,12 +598,11 @@ BackwardShape backward_shape(int T, int H, int f32, int num_sms) {
     s.cluster = H <= kCols ? 1 : H <= 2 * kCols ? 2 : 4;
     s.cols = ((H / kVec + s.cluster - 1) / s.cluster) * kVec;
     s.warps = (s.cols / kVec + 31) / 32;
-    // narrow rows: as many CTAs on an SM as keep 16 consumer warps
-    s.per_sm = std::max(1, std::min(4, 16 / s.warps));
+    // narrow rows: as many CTAs on an SM as make 16 consumer warps and as its registers hold, 96 a thread
+    s.per_sm = std::max(1, std::min({6, 16 / s.warps, 65536 / (96 * 32 * (s.warps + 2))}));
     const size_t stage = (size_t)s.cols * (f32 ? 12 : 8);
     s.stages = (int)std::min<size_t>(kMaxStages, kRingBytes / s.per_sm / stage);
-    // a cluster's sums take longer to arrive
-    s.lag = std::min(s.cluster > 1 ? 2 : 1, s.stages - 2);
+    s.lag = std::min(s.per_sm > 1 ? 1 : 2, s.stages - 2);
     s.clusters = std::min(T, std::min(num_sms, kMaxSms) * s.per_sm / s.cluster);
     return s;
 }
@@ -616,7 +636,7 @@ cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStr
     if (s.clusters > 0) {
         const bool full = p.y != nullptr && p.d_n != nullptr && p.d_h_out != nullptr;
         void (*kern)(NormParams, BackwardShape);
-        if (s.warps + 2 <= 16)
+        if (s.warps + 2 <= 16 && s.per_sm == 1)
             kern = p.f32 ? (full ? norm_backward_kernel<true, true, 16> : norm_backward_kernel<true, false, 16>)
                          : (full ? norm_backward_kernel<false, true, 16> : norm_backward_kernel<false, false, 16>);
         else
