@@ -618,8 +618,11 @@ cudaError_t launch_forward(const NormParams& p, int num_sms, cudaStream_t stream
     // 32 warps on an SM, whole rows
     const dim3 grid((unsigned)std::min<int64_t>(p.T, (int64_t)num_sms * (32 / warps))), block(warps * 32);
     const bool full = p.y != nullptr && p.w_post != nullptr && p.w_pre != nullptr && p.h_out != nullptr;
-    return full ? launch_kernel(true, norm_kernel<NV, F32, true>, grid, block, 0, stream, p)
-                : launch_kernel(true, norm_kernel<NV, F32, false>, grid, block, 0, stream, p);
+    // started early, many rows' CTAs take the SMs from the kernel before (forward and backward of T=16384 H=4096 f32: 351
+    // against 323 us); a decode batch's, a row to an SM, gain the launch gap
+    const bool early = p.T <= num_sms;
+    return full ? launch_kernel(early, norm_kernel<NV, F32, true>, grid, block, 0, stream, p)
+                : launch_kernel(early, norm_kernel<NV, F32, false>, grid, block, 0, stream, p);
 }
 
 }  // namespace
