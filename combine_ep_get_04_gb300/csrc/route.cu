@@ -128,15 +128,15 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteParams& p, int per,
             if (i * 32 + lane < p.E) atomicMax(&best[(i * 32 + lane) / per], key[i]);
     }
     __syncwarp();
-    uint32_t mine = lane < p.groups ? best[lane] : 0u;
-    uint32_t keep = 0;
-    for (int r = 0; r < p.topk_groups; ++r) {
-        const uint32_t top = __reduce_max_sync(kAll, mine);
-        if (top <= kUnchoosable) break;
-        const int g = __ffs(__ballot_sync(kAll, mine == top)) - 1;
-        keep |= 1u << g;
-        if (lane == g) mine = 0;
+    // a group stays if fewer than topk_groups come before it
+    const uint32_t mine = lane < p.groups ? best[lane] : 0u;
+    int before = 0;
+#pragma unroll 4
+    for (int g = 0; g < p.groups; ++g) {
+        const uint32_t other = best[g];
+        before += other > mine || (other == mine && g < lane) ? 1 : 0;
     }
+    const uint32_t keep = __ballot_sync(kAll, mine > kUnchoosable && before < p.topk_groups);
     __syncwarp();
     return keep;
 }
@@ -207,7 +207,7 @@ __device__ __forceinline__ int reorder(const RouteParams& p, int t, int e, int c
 // whose keys have 16 bits) the rounds go on to the end of that stretch, and the
 // candidates are put into the order of their whole keys.
 template <int NPL, bool F32>
-__global__ void __launch_bounds__(kMaxRouteWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_kernel(const __grid_constant__ RouteParams p) {
     extern __shared__ unsigned char smem[];   // [E] copies, [E] group bits, then [warps][E] probabilities
     __shared__ uint32_t group_best[kMaxRouteWarps][32];
     __shared__ float warp_z[kMaxRouteWarps];
@@ -434,12 +434,14 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(RouteParams 
             p.seq_tokens[s] = n;
         }
     }
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    if (threadIdx.x == 0) {
+        __threadfence();       // what the CTA's threads wrote before the barrier goes before the ticket
+        last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
+        __threadfence();
+    }
     __syncthreads();
     if (!last || warp != 0) return;
-    __threadfence();
     float balance = 0.f, z = 0.f;
     int tokens = 0, seqs = 0;
     for (int q = lane; q < p.S; q += 32) {
