@@ -185,7 +185,7 @@ struct RouteParams {
     uint32_t* err_flags;
     int64_t ld;
     int T, E, k, groups, topk_groups, full_softmax, f32, S;
-    int chunk, per_group;        // set by the launchers
+    int chunk, per_group, wide;  // set by the launchers; wide: rows are read and written by wide accesses
     float balance_coef, z_coef;
 };
 

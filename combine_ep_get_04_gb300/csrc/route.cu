@@ -1,13 +1,15 @@
 // route.cu -- the choice of experts from router logits, per-expert counts,
 // the balance and z losses, and the gradient of all of it.
 //
-// One warp per token, the token's logits in registers (lane l holds experts
-// l, l + 32, ...).  The choice compares 32-bit keys whose unsigned order is
+// One warp per token, the token's logits in registers, as wide loads bring them:
+// a lane's NPL values are vectors of neighbours, up to 16 bytes, 32 vectors
+// apart, and a group of experts is in most cases a few lanes' vectors.  The choice compares 32-bit keys whose unsigned order is
 // that of the floats, so a maximum over the warp is one redux.sync.  What is
 // summed over tokens (probabilities, copies, squared log normalisers) is
 // summed per run of tokens of one sequence by one CTA and then over the runs in
 // their order, so the losses do not depend on which CTA runs first.
 #include <algorithm>
+#include <cstring>
 #include <cuda_bf16.h>
 
 #include "ep_device.cuh"
@@ -73,6 +75,109 @@ __device__ __forceinline__ float load_logit(const void* base, int64_t at) {
     return __uint_as_float((uint32_t) static_cast<const uint16_t*>(base)[at] << 16);
 }
 
+// Values of one wide access: 16 bytes of them, or all that a lane has.
+__host__ __device__ constexpr int wide_values(int npl, bool f32) { return f32 ? (npl < 4 ? npl : 4) : (npl < 8 ? npl : 8); }
+
+// Where value i of a lane lies behind its first, value lane * V of the row.
+template <int V>
+__device__ __forceinline__ constexpr int value_at(int i) { return i / V * 32 * V + i % V; }
+
+template <int WORDS> struct Wide;
+template <> struct Wide<1> { using T = uint32_t; };
+template <> struct Wide<2> { using T = uint2; };
+template <> struct Wide<4> { using T = uint4; };
+
+// A lane's NPL logits as they lie in memory, -inf beyond the row.  `row` is the
+// place of the lane's first, `left` the values from there to the row's end.
+template <int NPL, bool F32>
+struct RawLogits {
+    static constexpr int V = wide_values(NPL, F32), kWords = F32 ? V : V / 2;
+    uint32_t w[F32 ? NPL : NPL / 2];
+
+    __device__ __forceinline__ void load(const unsigned char* row, int left, bool wide) {
+#pragma unroll
+        for (int v = 0; v < NPL / V; ++v) {
+            const int first = v * 32 * V;
+            if (wide) {
+                const bool in = first < left;
+                typename Wide<kWords>::T x{};
+                if (in) x = *reinterpret_cast<const typename Wide<kWords>::T*>(row + first * (F32 ? 4 : 2));
+                uint32_t words[kWords];
+                memcpy(words, &x, sizeof(x));
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) w[v * kWords + i] = in ? words[i] : F32 ? 0xff800000u : 0xff80ff80u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    const int at = first + (F32 ? i : 2 * i);
+                    if (F32) {
+                        w[v * kWords + i] = at < left ? reinterpret_cast<const uint32_t*>(row)[at] : 0xff800000u;
+                    } else {
+                        const uint16_t* from = reinterpret_cast<const uint16_t*>(row);
+                        const uint32_t lo = at < left ? from[at] : 0xff80u, hi = at + 1 < left ? from[at + 1] : 0xff80u;
+                        w[v * kWords + i] = lo | hi << 16;
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        return F32 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
+
+// Writes a lane's NPL values.
+template <int NPL, bool F32>
+__device__ __forceinline__ void store_values(unsigned char* row, int left, bool wide, const float (&d)[NPL]) {
+    constexpr int V = wide_values(NPL, F32), kWords = F32 ? V : V / 2;
+#pragma unroll
+    for (int v = 0; v < NPL / V; ++v) {
+        const int first = v * 32 * V;
+        if (wide) {
+            uint32_t w[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const int at = v * V + (F32 ? i : 2 * i);
+                w[i] = F32 ? __float_as_uint(d[at]) : pack_bf16x2(d[at], d[F32 ? at : at + 1]);
+            }
+            typename Wide<kWords>::T x;
+            memcpy(&x, w, sizeof(x));
+            if (first < left) *reinterpret_cast<typename Wide<kWords>::T*>(row + first * (F32 ? 4 : 2)) = x;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (first + i >= left) continue;
+                if (F32)
+                    reinterpret_cast<float*>(row)[first + i] = d[v * V + i];
+                else
+                    reinterpret_cast<__nv_bfloat16*>(row)[first + i] = __float2bfloat16_rn(d[v * V + i]);
+            }
+        }
+    }
+}
+
+// A lane's NPL words of a row in shared memory, V neighbours each.
+template <int NPL, int V>
+__device__ __forceinline__ void load_shared(const uint32_t* row, uint32_t (&x)[NPL]) {
+    constexpr int kWords = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < NPL; i += kWords) {
+        const auto w = *reinterpret_cast<const typename Wide<kWords>::T*>(row + value_at<V>(i));
+        memcpy(x + i, &w, sizeof(w));
+    }
+}
+
+template <int NPL, int V>
+__device__ __forceinline__ void store_shared(uint32_t* row, const float (&x)[NPL]) {
+    constexpr int kWords = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < NPL; i += kWords) {
+        typename Wide<kWords>::T w;
+        memcpy(&w, x + i, sizeof(w));
+        *reinterpret_cast<typename Wide<kWords>::T*>(row + value_at<V>(i)) = w;
+    }
+}
+
 __device__ __forceinline__ float warp_max(float x) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
@@ -98,54 +203,49 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
                     }
 }
 
-// The largest of each group's keys -> the groups a token may choose from, as
-// a mask.  `best` is a row of 32 words of shared memory.
-template <int NPL>
-__device__ __forceinline__ uint32_t choose_groups(const RouteParams& p, int per, const uint32_t (&key)[NPL], uint32_t* best) {
+// The groups a token may choose from, as a mask.  A group is `lanes` lanes'
+// vectors, a power of two, or of any size (lanes = 0).  `best` is a row of 32
+// words of shared memory.
+template <int NPL, int V>
+__device__ __forceinline__ uint32_t choose_groups(const RouteParams& p, int lanes, const uint32_t (&key)[NPL], uint32_t* best) {
     const int lane = threadIdx.x & 31;
-    if ((per & (per - 1)) == 0) {
-        // a power of two: maxima over the lanes of a group, or over a lane's values and the warp
-        const int shift = 31 - __clz(per);
+    uint32_t mine = 0;             // the largest key of group `lane`
+    if (lanes > 0) {
+        const int shift = __ffs(lanes) - 1, from = lane << shift;       // the group's first vector
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            uint32_t m = key[i];
+        for (int v = 0; v < NPL / V; ++v) {
+            uint32_t m = key[v * V];
 #pragma unroll
-            for (int d = 16; d >= 1; d >>= 1)
-                if (d < per) m = max(m, __shfl_xor_sync(kAll, m, d));
-            const int e = i * 32 + lane;
-            if (e < p.E && (lane & (per - 1)) == 0) {
-                if (per <= 32 || (i * 32 & (per - 1)) == 0)
-                    best[e >> shift] = m;
-                else
-                    best[e >> shift] = max(best[e >> shift], m);      // the same lane, 0, writes all parts of a group
-            }
+            for (int i = 1; i < V; ++i) m = max(m, key[v * V + i]);
+            for (int d = 1; d < lanes; d <<= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+            m = __shfl_sync(kAll, m, from);
+            mine = from >> 5 == v ? m : mine;
         }
     } else {
         best[lane] = 0;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (i * 32 + lane < p.E) atomicMax(&best[(i * 32 + lane) / per], key[i]);
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane * V + value_at<V>(i);
+            if (e < p.E) atomicMax(&best[e / p.per_group], key[i]);
+        }
+        __syncwarp();
+        mine = best[lane];
+        __syncwarp();
     }
-    __syncwarp();
+    mine = lane < p.groups ? mine : 0u;
     // a group stays if fewer than topk_groups come before it
-    const uint32_t mine = lane < p.groups ? best[lane] : 0u;
     int before = 0;
-#pragma unroll 4
-    for (int g = 0; g < p.groups; ++g) {
-        const uint32_t other = best[g];
-        before += other > mine || (other == mine && g < lane) ? 1 : 0;
-    }
-    const uint32_t keep = __ballot_sync(kAll, mine > kUnchoosable && before < p.topk_groups);
-    __syncwarp();
-    return keep;
+#pragma unroll 8
+    for (int g = 0; g < p.groups; ++g) before += __shfl_sync(kAll, mine, g) + (g < lane ? 1u : 0u) > mine ? 1 : 0;
+    return __ballot_sync(kAll, mine > kUnchoosable && before < p.topk_groups);
 }
 
 // The choice by whole keys, for tokens whose best keys agree in their upper 22
 // bits: every round looks for the next pair (key, index) in memory.  Returns
 // lane j's expert, or -1.
 template <bool F32>
-__device__ __noinline__ int choose_exactly(const RouteParams& p, int t, int per, uint32_t keep) {
+__device__ __noinline__ int choose_exactly(const RouteParams& p, int t, uint32_t keep) {
     const int lane = threadIdx.x & 31;
     uint32_t last = kAll;
     int last_e = -1, chosen = -1;
@@ -153,7 +253,7 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, int t, int per,
         uint32_t top = 0;
         int top_e = 0;
         for (int e = lane; e < p.E; e += 32) {
-            if (p.groups > 1 && !(keep >> (e / per) & 1u)) continue;
+            if (!(keep >> (e / p.per_group) & 1u)) continue;
             const float x = load_logit<F32>(p.logits, t * p.ld + e);
             const uint32_t key = order_key(p.select_bias != nullptr ? __fadd_rn(x, p.select_bias[e]) : x);
             if ((key < last || (key == last && e > last_e)) && key > top) {
@@ -208,36 +308,40 @@ __device__ __forceinline__ int reorder(const RouteParams& p, int t, int e, int c
 // candidates are put into the order of their whole keys.
 template <int NPL, bool F32>
 __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_kernel(const __grid_constant__ RouteParams p) {
-    extern __shared__ unsigned char smem[];   // [E] copies, [E] group bits, then [warps][E] probabilities
+    constexpr int V = wide_values(NPL, F32), kRow = NPL * 32;      // kRow: words of a row of shared memory
+    extern __shared__ __align__(16) uint32_t smem[];   // rows: copies, selection bias, group bits, and a warp's probabilities each
     __shared__ uint32_t group_best[kMaxRouteWarps][32];
     __shared__ float warp_z[kMaxRouteWarps];
     __shared__ int warp_live[kMaxRouteWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int32_t* hist = reinterpret_cast<int32_t*>(smem);
-    uint32_t* group_bit = reinterpret_cast<uint32_t*>(smem) + p.E;
-    float* prob = reinterpret_cast<float*>(smem) + 2 * p.E;
-    const bool sums = p.losses != nullptr, exact = !F32 && p.select_bias == nullptr;
-    const int per = p.per_group;
-    if (sums)
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
-    if (p.groups > 1)
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) group_bit[e] = 1u << (e / per);
+    const int e0 = lane * V, left = p.E - e0;
+    uint32_t *hist = smem, *bias = smem + kRow, *group_bit = smem + 2 * kRow, *prob = smem + 3 * kRow;
+    const bool sums = p.losses != nullptr, has_bias = p.select_bias != nullptr, exact = !F32 && !has_bias;
+    // lanes of a group, if it is whole vectors, a power of two of them, and no more than a warp has lanes
+    const int vectors = p.per_group / V;
+    const int group_lanes = p.per_group % V == 0 && (vectors & (vectors - 1)) == 0 && vectors <= 32 ? vectors : 0;
+    for (int e = threadIdx.x; e < kRow; e += blockDim.x) {
+        if (sums) hist[e] = 0;
+        if (p.groups > 1 && group_lanes == 0) group_bit[e] = e < p.E ? 1u << (e / p.per_group) : 0u;
+    }
     pdl_launch_dependents();
     pdl_wait();
+    if (has_bias)
+        for (int e = threadIdx.x; e < kRow; e += blockDim.x) bias[e] = e < p.E ? __float_as_uint(p.select_bias[e]) : 0u;
     if (sums && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
     const Run run = find_run(p, blockIdx.x);
     __syncthreads();
-    float psum[NPL], next[NPL];
+    constexpr int kSize = F32 ? 4 : 2;
+    const unsigned char* row = static_cast<const unsigned char*>(p.logits) + ((int64_t)(run.begin + warp) * p.ld + e0) * kSize;
+    RawLogits<NPL, F32> next;
     bool next_mask = true;
     auto fetch = [&](int t) {      // a token's logits are on their way while the one before it is worked on
         if (t >= run.end) return;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = i * 32 + lane;
-            next[i] = e < p.E ? load_logit<F32>(p.logits, t * p.ld + e) : -INFINITY;
-        }
+        next.load(row, left, p.wide != 0);
         next_mask = p.token_mask == nullptr || p.token_mask[t] != 0;
+        row += warps * p.ld * kSize;
     };
+    float psum[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) psum[i] = 0.f;
     float z = 0.f;
@@ -247,7 +351,7 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
         float l[NPL], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            l[i] = next[i];
+            l[i] = next.get(i);
             top = fmaxf(top, l[i]);
         }
         const bool mask = next_mask;
@@ -263,22 +367,38 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
             continue;
         }
         uint32_t word[NPL];
+        if (has_bias) {
+            uint32_t b[NPL];
+            load_shared<NPL, V>(bias + e0, b);
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = i * 32 + lane;
-            word[i] = order_key(p.select_bias != nullptr && e < p.E ? __fadd_rn(l[i], p.select_bias[e]) : l[i]);
+            for (int i = 0; i < NPL; ++i) word[i] = order_key(__fadd_rn(l[i], __uint_as_float(b[i])));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) word[i] = order_key(l[i]);
         }
         uint32_t keep = kAll;
-        if (p.groups > 1) keep = choose_groups<NPL>(p, per, word, group_best[warp]);
+        if (p.groups > 1) {
+            keep = choose_groups<NPL, V>(p, group_lanes, word, group_best[warp]);
+            if (group_lanes > 0) {
+                const int shift = __ffs(group_lanes) - 1;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = i * 32 + lane;
-            const bool may = word[i] > kUnchoosable && (p.groups == 1 || (e < p.E && (keep & group_bit[e]) != 0));
-            word[i] = may ? (word[i] & ~1023u) | (1023u - e) : 0u;
+                for (int v = 0; v < NPL / V; ++v) {
+                    const bool kept = keep >> ((v * 32 + lane) >> shift) & 1u;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) word[v * V + i] = kept ? word[v * V + i] : 0u;
+                }
+            } else {
+                uint32_t bit[NPL];
+                load_shared<NPL, V>(group_bit + e0, bit);
+#pragma unroll
+                for (int i = 0; i < NPL; ++i) word[i] = (keep & bit[i]) != 0 ? word[i] : 0u;
+            }
         }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            word[i] = word[i] > kUnchoosable ? (word[i] & ~1023u) | (uint32_t)(1023 - e0 - value_at<V>(i)) : 0u;
         sort_down<NPL>(word);
         uint32_t mine = 0, last = 0;
-        bool close = false;
         auto pop = [&](uint32_t best) {
             const bool own = word[0] == best;
 #pragma unroll
@@ -288,29 +408,28 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
         int count = p.k;
 #pragma unroll 4
         for (int j = 0; j < p.k; ++j) {
-            const uint32_t best = __reduce_max_sync(kAll, word[0]);     // 0 once nothing is left
-            close |= best != 0 && (best ^ last) < 1024u;
-            last = best;
-            mine = lane == j ? best : mine;
-            pop(best);
+            last = __reduce_max_sync(kAll, word[0]);     // 0 once nothing is left
+            mine = lane == j ? last : mine;
+            pop(last);
         }
         if (!exact) {
             for (; count < 32; ++count) {
                 const uint32_t next_best = __reduce_max_sync(kAll, word[0]);
                 if (next_best == 0 || (next_best ^ last) >= 1024u) break;
-                close = true;
                 last = next_best;
                 mine = lane == count ? next_best : mine;
                 pop(next_best);
             }
         }
         int chosen = mine != 0 ? 1023 - (int)(mine & 1023u) : -1;
-        if (!exact && count == 32 && last != 0 && (__reduce_max_sync(kAll, word[0]) ^ last) < 1024u)
-            chosen = choose_exactly<F32>(p, t, per, keep);       // the stretch goes on
-        else if (!exact && close)
-            chosen = reorder<F32>(p, t, chosen, count);
-        else if (lane >= p.k)
-            chosen = -1;
+        if (!exact) {
+            const uint32_t before = __shfl_up_sync(kAll, mine, 1);
+            const bool close = __any_sync(kAll, lane > 0 && mine != 0 && (mine ^ before) < 1024u);
+            if (count == 32 && last != 0 && (__reduce_max_sync(kAll, word[0]) ^ last) < 1024u)
+                chosen = choose_exactly<F32>(p, t, keep);       // the stretch goes on
+            else if (close)
+                chosen = reorder<F32>(p, t, chosen, count);
+        }
         const float logit = chosen >= 0 ? load_logit<F32>(p.logits, t * p.ld + chosen) : -INFINITY;
         float lse = 0.f;
         if (sums || p.full_softmax || p.lse != nullptr) {
@@ -344,23 +463,21 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
             p.topk_idx[at + lane] = chosen;
             p.topk_w[at + lane] = w;
         }
-        if (sums && chosen >= 0) atomicAdd(&hist[chosen], 1);
+        if (sums && chosen >= 0) atomicAdd(&hist[chosen], 1u);
     }
     if (!sums) return;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-        if (i * 32 + lane < p.E) prob[warp * p.E + i * 32 + lane] = psum[i];
+    store_shared<NPL, V>(prob + warp * kRow + e0, psum);
     if (lane == 0) {
         warp_z[warp] = z;
         warp_live[warp] = n_live;
     }
     __syncthreads();
-    const int64_t row = (int64_t)blockIdx.x * p.E;
+    const int64_t part = (int64_t)blockIdx.x * p.E;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         float s = 0.f;
-        for (int w = 0; w < warps; ++w) s += prob[w * p.E + e];
-        p.part_prob[row + e] = s;
-        p.part_count[row + e] = hist[e];
+        for (int w = 0; w < warps; ++w) s += __uint_as_float(prob[w * kRow + e]);
+        p.part_prob[part + e] = s;
+        p.part_count[part + e] = (int32_t)hist[e];
     }
     if (threadIdx.x == 0) {
         float s = 0.f;
@@ -436,9 +553,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(RouteParams 
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();       // what the CTA's threads wrote before the barrier goes before the ticket
-        last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
-        __threadfence();
+        // released: what the CTA's threads wrote before the barrier goes before the ticket; acquired: the others' sums
+        uint32_t ticket;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(ticket) : "l"(p.ticket) : "memory");
+        last = ticket == gridDim.x * gridDim.y - 1;
     }
     __syncthreads();
     if (!last || warp != 0) return;
@@ -470,25 +588,29 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(RouteParams 
 // logits and lse; what the chosen experts add is scattered through a row of
 // shared memory, which stays zero between tokens.
 template <int NPL, bool F32>
-__global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(RouteParams p) {
-    extern __shared__ float extra_all[];      // [warps][E]
+__global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(const __grid_constant__ RouteParams p) {
+    constexpr int V = wide_values(NPL, F32), kRow = NPL * 32;
+    __shared__ __align__(16) uint32_t extra_all[kBackwardWarps * kRow];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* extra = extra_all + warp * p.E;
-    for (int e = lane; e < p.E; e += 32) extra[e] = 0.f;
+    const int e0 = lane * V, left = p.E - e0;
+    uint32_t* extra = extra_all + warp * kRow;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) extra[i * 32 + lane] = 0;
     __syncwarp();
     pdl_launch_dependents();
     pdl_wait();
     const Run run = find_run(p, blockIdx.x);
-    float next[NPL], next_lse = 0.f, next_w = 0.f, next_dw = 0.f;
+    constexpr int kSize = F32 ? 4 : 2;
+    const unsigned char* row = static_cast<const unsigned char*>(p.logits) + ((int64_t)(run.begin + warp) * p.ld + e0) * kSize;
+    unsigned char* d_row = static_cast<unsigned char*>(p.d_logits) + ((int64_t)(run.begin + warp) * p.E + e0) * kSize;
+    RawLogits<NPL, F32> next;
+    float next_lse = 0.f, next_w = 0.f, next_dw = 0.f;
     int next_chosen = -1;
     auto fetch = [&](int t) {      // a token's values are on their way while the one before it is worked on
         if (t >= run.end) return;
         next_lse = p.lse[t];
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = i * 32 + lane;
-            next[i] = e < p.E ? load_logit<F32>(p.logits, t * p.ld + e) : -INFINITY;
-        }
+        next.load(row, left, p.wide != 0);
+        row += kBackwardWarps * p.ld * kSize;
         if (lane < p.k && p.d_topk_w != nullptr) {
             const int64_t at = (int64_t)t * p.k + lane;
             next_chosen = p.topk_idx[at];
@@ -505,14 +627,12 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(Rou
     }
     float g[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = i * 32 + lane;
-        g[i] = e < p.E ? d_balance * (float)p.counts[(int64_t)run.s * p.E + e] : 0.f;
-    }
+    for (int i = 0; i < NPL; ++i)
+        g[i] = value_at<V>(i) < left ? d_balance * (float)p.counts[(int64_t)run.s * p.E + e0 + value_at<V>(i)] : 0.f;
     for (int t = run.begin + warp; t < run.end; t += kBackwardWarps) {
         float l[NPL];
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) l[i] = next[i];
+        for (int i = 0; i < NPL; ++i) l[i] = next.get(i);
         const float lse = next_lse;
         const int chosen = next_chosen >= 0 && next_chosen < p.E ? next_chosen : -1;
         const float w = chosen >= 0 ? next_w : 0.f;
@@ -524,14 +644,15 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(Rou
             for (int i = 0; i < NPL; ++i) d[i] = 0.f;
         } else {
             if (!p.full_softmax) dw = w * (dw - warp_sum(w * dw));
-            if (chosen >= 0) extra[chosen] = dw;
+            if (chosen >= 0) extra[chosen] = __float_as_uint(dw);
             __syncwarp();
             float pr[NPL], dot = 0.f;
+            uint32_t ex[NPL];
+            load_shared<NPL, V>(extra + e0, ex);
 #pragma unroll
             for (int i = 0; i < NPL; ++i) {
-                const int e = i * 32 + lane;
                 pr[i] = __expf(l[i] - lse);
-                d[i] = e < p.E ? extra[e] : 0.f;
+                d[i] = __uint_as_float(ex[i]);
                 dot = fmaf(pr[i], p.full_softmax ? g[i] + d[i] : g[i], dot);
             }
             dot = warp_sum(dot) - d_z * lse;
@@ -539,18 +660,11 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(Rou
             for (int i = 0; i < NPL; ++i)
                 d[i] = p.full_softmax ? pr[i] * (g[i] + d[i] - dot) : fmaf(pr[i], g[i] - dot, d[i]);
             __syncwarp();
-            if (chosen >= 0) extra[chosen] = 0.f;
+            if (chosen >= 0) extra[chosen] = 0;
             __syncwarp();
         }
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = i * 32 + lane;
-            if (e >= p.E) continue;
-            if (F32)
-                static_cast<float*>(p.d_logits)[(int64_t)t * p.E + e] = d[i];
-            else
-                static_cast<__nv_bfloat16*>(p.d_logits)[(int64_t)t * p.E + e] = __float2bfloat16_rn(d[i]);
-        }
+        store_values<NPL, F32>(d_row, left, p.wide != 0, d);
+        d_row += (int64_t)kBackwardWarps * p.E * kSize;
     }
 }
 
@@ -559,6 +673,15 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(Rou
 int run_tokens(int T) {
     const int per = (T + kRunWarps * 304 - 1) / (kRunWarps * 304);
     return kRunWarps * std::min(std::max(per, 1), 16);
+}
+
+// Experts of a lane.
+int lane_values(int E) { return E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+
+// Can the rows be read, or written, by wide accesses?
+bool wide_rows(const RouteParams& p, const void* base, int64_t ld) {
+    const int values = wide_values(lane_values(p.E), p.f32 != 0), bytes = values * (p.f32 ? 4 : 2);
+    return p.E % values == 0 && ld % values == 0 && reinterpret_cast<uintptr_t>(base) % bytes == 0;
 }
 
 int64_t num_runs(int T, int chunk, int S) { return ((int64_t)T + chunk - 1) / chunk + S - 1; }
@@ -582,13 +705,13 @@ cudaError_t launch_forward(const RouteParams& p, dim3 grid, dim3 block, size_t s
 }
 
 template <bool F32>
-cudaError_t launch_gradient(const RouteParams& p, dim3 grid, size_t smem, cudaStream_t stream) {
+cudaError_t launch_gradient(const RouteParams& p, dim3 grid, cudaStream_t stream) {
     const dim3 block(kBackwardWarps * 32);
-    if (p.E <= 64) return launch_kernel(true, route_backward_kernel<2, F32>, grid, block, smem, stream, p);
-    if (p.E <= 128) return launch_kernel(true, route_backward_kernel<4, F32>, grid, block, smem, stream, p);
-    if (p.E <= 256) return launch_kernel(true, route_backward_kernel<8, F32>, grid, block, smem, stream, p);
-    if (p.E <= 512) return launch_kernel(true, route_backward_kernel<16, F32>, grid, block, smem, stream, p);
-    return launch_kernel(true, route_backward_kernel<32, F32>, grid, block, smem, stream, p);
+    if (p.E <= 64) return launch_kernel(true, route_backward_kernel<2, F32>, grid, block, 0, stream, p);
+    if (p.E <= 128) return launch_kernel(true, route_backward_kernel<4, F32>, grid, block, 0, stream, p);
+    if (p.E <= 256) return launch_kernel(true, route_backward_kernel<8, F32>, grid, block, 0, stream, p);
+    if (p.E <= 512) return launch_kernel(true, route_backward_kernel<16, F32>, grid, block, 0, stream, p);
+    return launch_kernel(true, route_backward_kernel<32, F32>, grid, block, 0, stream, p);
 }
 
 }  // namespace
@@ -624,7 +747,8 @@ cudaError_t launch_route(const RouteParams& in, int num_sms, cudaStream_t stream
     // one token a warp until there are 8 CTAs for every SM
     p.chunk = sums ? run_tokens(p.T) : kChoiceWarps * std::min(std::max(p.T / (kChoiceWarps * 8 * num_sms), 1), kChoiceTokens);
     const dim3 grid((unsigned)std::max<int64_t>(num_runs(p.T, p.chunk, p.S), 1)), block(warps * 32);
-    const size_t smem = (size_t)(2 + (sums ? kRunWarps : 0)) * p.E * 4;
+    const size_t smem = (size_t)(3 + (sums ? kRunWarps : 0)) * lane_values(p.E) * 32 * 4;
+    p.wide = wide_rows(p, p.logits, p.ld);
     cudaError_t e = p.f32 ? launch_forward<true>(p, grid, block, smem, stream) : launch_forward<false>(p, grid, block, smem, stream);
     if (e != cudaSuccess || !sums) return e;
     return launch_kernel(true, route_sums_kernel, dim3((p.E + 31) / 32, p.S), dim3(kSumWarps * 32), 0, stream, p);
@@ -635,8 +759,8 @@ cudaError_t launch_route_backward(const RouteParams& in, int num_sms, cudaStream
     RouteParams p = in;
     p.chunk = kBackwardWarps * kBackwardTokens;
     const dim3 grid((unsigned)num_runs(p.T, p.chunk, p.S));
-    const size_t smem = (size_t)kBackwardWarps * p.E * 4;
-    return p.f32 ? launch_gradient<true>(p, grid, smem, stream) : launch_gradient<false>(p, grid, smem, stream);
+    p.wide = wide_rows(p, p.logits, p.ld) && wide_rows(p, p.d_logits, p.E);
+    return p.f32 ? launch_gradient<true>(p, grid, stream) : launch_gradient<false>(p, grid, stream);
 }
 
 }  // namespace ep

@@ -168,6 +168,16 @@ def test_rows_further_apart_and_odd_addresses(dtype):
     check(flat[1:].view(50, 64)[:, :63], 5)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (1, 0), (2, 2), (0, 1), (0, 4)])
+@pytest.mark.parametrize("E,groups,topk_groups", [(256, 1, 1), (256, 8, 4), (128, 32, 5), (160, 8, 3), (512, 8, 2), (1024, 2, 1), (56, 7, 2)])
+def test_groups_and_rows_at_any_place(E, groups, topk_groups, pad, shift, dtype):
+    """Groups of whole lanes and others, rows that wide accesses can and cannot read."""
+    flat = make(1, 40 * (E + pad) + shift, dtype, seed=E + pad)[0]
+    x = flat[shift:].view(40, E + pad)[:, :E]
+    check(x, 8, groups, topk_groups, bias=torch.linspace(-0.1, 0.1, E, device="cuda"))
+
+
 def test_gradient_parts():
     x = make(60, 48, torch.float32)
     _, d = check(x, 4, d_w=False, d_losses=None)
