@@ -25,6 +25,8 @@ constexpr int kChoiceTokens = 8;       // most tokens of its warps
 constexpr int kBackwardWarps = 8;
 constexpr int kBackwardTokens = 2;     // a warp's, in the backward pass: the second's loads overlap the first
 constexpr int kSumWarps = 32;
+constexpr int kSumRuns = 8;
+constexpr int kSumCluster = 8;         // most CTAs of a sequence
 constexpr uint32_t kAll = 0xffffffffu;
 
 // Unsigned order of the key = order of the float; -0 counts as 0, NaN comes
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
     pdl_wait();
     if (has_bias)
         for (int e = threadIdx.x; e < kRow; e += blockDim.x) bias[e] = e < p.E ? __float_as_uint(p.select_bias[e]) : 0u;
-    if (sums && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+    if (sums && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;      // of the kernel after this one
     const Run run = find_run(p, blockIdx.x);
     __syncthreads();
     constexpr int kSize = F32 ? 4 : 2;
@@ -492,13 +494,24 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
 }
 
 // Adds the runs of sequence blockIdx.y for 32 experts: each warp every
-// kSumWarps-th run, then the warps' sums in their order.  The CTA that finishes
-// last adds up the losses.
-__global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(RouteParams p) {
+// kSumWarps-th run, then the warps' sums in their order.  The losses need all
+// CTAs: those of a single sequence are a cluster if they may be one, and the
+// first is handed the others' shares; else the shares go to the workspace and
+// the CTA that finishes last adds them up.  (Forward pass of 4,096 tokens, 256
+// experts, one sequence: 9.8 us with the cluster, 11.2 without; a cluster for
+// each of 3 to 16 sequences costs 0.3 to 0.5 us more than it saves.)
+__host__ __device__ inline bool joins_in_cluster(int S, int E) { return S == 1 && E > 32 && E <= 32 * kSumCluster; }
+
+__global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(const __grid_constant__ RouteParams p) {
     __shared__ float fpart[kSumWarps][32];
     __shared__ int ipart[kSumWarps][32];
+    __shared__ float share[kSumCluster];
+    __shared__ float z_sum;
+    __shared__ int live;
     __shared__ bool last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool cluster = joins_in_cluster(p.S, p.E);
+    if (cluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     pdl_launch_dependents();
     pdl_wait();
     const int s = blockIdx.y, e = blockIdx.x * 32 + lane;
@@ -511,17 +524,30 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(RouteParams 
     float prob = 0.f;
     int count = 0;
     if (e < p.E) {
-        const float* fp = p.part_prob + (int64_t)first * p.E + e;
-        const int32_t* ip = p.part_count + (int64_t)first * p.E + e;
-#pragma unroll 8
-        for (int r = warp; r < runs; r += kSumWarps) {
-            prob += fp[(int64_t)r * p.E];
-            count += ip[(int64_t)r * p.E];
+        // kSumRuns at a time, whose loads are in flight together
+        const int64_t step = (int64_t)kSumWarps * p.E;
+        const float* fp = p.part_prob + (int64_t)(first + warp) * p.E + e;
+        const int32_t* ip = p.part_count + (int64_t)(first + warp) * p.E + e;
+        for (int r = warp; r < runs; r += kSumRuns * kSumWarps, fp += kSumRuns * step, ip += kSumRuns * step) {
+            float f[kSumRuns];
+            int n[kSumRuns];
+#pragma unroll
+            for (int j = 0; j < kSumRuns; ++j) {
+                const bool in = r + j * kSumWarps < runs;
+                f[j] = in ? fp[j * step] : 0.f;
+                n[j] = in ? ip[j * step] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kSumRuns; ++j) {
+                prob += f[j];
+                count += n[j];
+            }
         }
     }
     fpart[warp][lane] = prob;
     ipart[warp][lane] = count;
     __syncthreads();
+    float loss = 0.f;
     if (warp == 0) {
         prob = 0.f;
         count = 0;
@@ -534,8 +560,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(RouteParams 
             p.prob_sums[(int64_t)s * p.E + e] = prob;
             p.counts[(int64_t)s * p.E + e] = count;
         }
-        const float loss = warp_sum((float)count * prob);
-        if (lane == 0) p.part_loss[(int64_t)s * gridDim.x + blockIdx.x] = loss;
+        loss = warp_sum((float)count * prob);
+        if (!cluster && lane == 0) p.part_loss[(int64_t)s * gridDim.x + blockIdx.x] = loss;
     }
     if (warp == 1 && blockIdx.x == 0) {
         float z = 0.f;
@@ -547,35 +573,57 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(RouteParams 
         z = warp_sum(z);
         n = (int)__reduce_add_sync(kAll, (unsigned)n);
         if (lane == 0) {
-            p.seq_z[s] = z;
+            z_sum = z;
+            live = n;
             p.seq_tokens[s] = n;
+            if (!cluster) p.seq_z[s] = z;
         }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        // released: what the CTA's threads wrote before the barrier goes before the ticket; acquired: the others' sums
-        uint32_t ticket;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(ticket) : "l"(p.ticket) : "memory");
-        last = ticket == gridDim.x * gridDim.y - 1;
-    }
-    __syncthreads();
-    if (!last || warp != 0) return;
+    __syncwarp();
     float balance = 0.f, z = 0.f;
     int tokens = 0, seqs = 0;
-    for (int q = lane; q < p.S; q += 32) {
-        const int n = __ldcg(&p.seq_tokens[q]);
-        if (n == 0) continue;
-        float sum = 0.f;
-        for (unsigned b = 0; b < gridDim.x; ++b) sum += __ldcg(&p.part_loss[(int64_t)q * gridDim.x + b]);
-        balance += sum * ((float)p.E / ((float)p.k * (float)n * (float)n));
-        z += __ldcg(&p.seq_z[q]);
-        tokens += n;
-        ++seqs;
+    if (cluster) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");      // all have started
+        if (threadIdx.x == 0) {
+            uint32_t to;
+            asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_addr(&share[blockIdx.x])));
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(loss) : "memory");
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (blockIdx.x != 0 || warp != 0) return;
+        if (live > 0) {
+            for (unsigned b = 0; b < gridDim.x; ++b) balance += share[b];
+            balance *= (float)p.E / ((float)p.k * (float)live * (float)live);
+            z = z_sum;
+            tokens = live;
+            seqs = 1;
+        }
+    } else {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            // released: what the CTA's threads wrote before the barrier goes before the ticket; acquired: the others' sums
+            uint32_t ticket;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(ticket) : "l"(p.ticket) : "memory");
+            last = ticket == gridDim.x * gridDim.y - 1;
+        }
+        __syncthreads();
+        if (!last || warp != 0) return;
+        for (int q = lane; q < p.S; q += 32) {
+            const int n = __ldcg(&p.seq_tokens[q]);
+            if (n == 0) continue;
+            float sum = 0.f;
+            for (unsigned b = 0; b < gridDim.x; ++b) sum += __ldcg(&p.part_loss[(int64_t)q * gridDim.x + b]);
+            balance += sum * ((float)p.E / ((float)p.k * (float)n * (float)n));
+            z += __ldcg(&p.seq_z[q]);
+            tokens += n;
+            ++seqs;
+        }
+        balance = warp_sum(balance);
+        z = warp_sum(z);
+        tokens = (int)__reduce_add_sync(kAll, (unsigned)tokens);
+        seqs = (int)__reduce_add_sync(kAll, (unsigned)seqs);
     }
-    balance = warp_sum(balance);
-    z = warp_sum(z);
-    tokens = (int)__reduce_add_sync(kAll, (unsigned)tokens);
-    seqs = (int)__reduce_add_sync(kAll, (unsigned)seqs);
     if (lane == 0) {
         p.losses[0] = seqs > 0 ? p.balance_coef * balance / (float)seqs : 0.f;
         p.losses[1] = tokens > 0 ? p.z_coef * z / (float)tokens : 0.f;
@@ -751,7 +799,9 @@ cudaError_t launch_route(const RouteParams& in, int num_sms, cudaStream_t stream
     p.wide = wide_rows(p, p.logits, p.ld);
     cudaError_t e = p.f32 ? launch_forward<true>(p, grid, block, smem, stream) : launch_forward<false>(p, grid, block, smem, stream);
     if (e != cudaSuccess || !sums) return e;
-    return launch_kernel(true, route_sums_kernel, dim3((p.E + 31) / 32, p.S), dim3(kSumWarps * 32), 0, stream, p);
+    const int ctas = (p.E + 31) / 32;
+    return launch_clusters(true, joins_in_cluster(p.S, p.E) ? ctas : 1, route_sums_kernel, dim3(ctas, p.S), dim3(kSumWarps * 32), 0,
+                           stream, p);
 }
 
 cudaError_t launch_route_backward(const RouteParams& in, int num_sms, cudaStream_t stream) {
