@@ -15,37 +15,10 @@ constexpr int kGateChannel = 1;
 constexpr int kGateToken = 2;
 constexpr int kVec = 8;   // channels a thread handles at once: 16 bytes of bf16
 
-// Eight fp32 values as four packed pairs: the products and sums below take two
-// at a time (f32x2), which halves the instructions a row costs.
+// Eight fp32 values as four pairs (f32x2), which halves the instructions a row costs.
 struct Vec8 {
     uint64_t v[4];
 };
-
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
-
-__device__ __forceinline__ float2 halves(uint64_t p) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 __device__ __forceinline__ float total(uint64_t p) {
     const float2 x = halves(p);

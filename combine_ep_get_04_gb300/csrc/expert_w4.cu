@@ -372,24 +372,26 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
 #pragma unroll
             for (int u = 0; u < kOwn; ++u) {
                 const uint32_t sc = *reinterpret_cast<const uint32_t*>(wt + u * tile_bytes(G) + kCodeBytes + i * 32 / G * 32 + g * 4);
-                const float s0 = bf16_lo(sc), s1 = bf16_hi(sc);
+                const uint64_t s0 = both(bf16_lo(sc)), s1 = both(bf16_hi(sc));
 #pragma unroll
                 for (int n = 0; n < NL; ++n) {
                     float (&v)[4] = acc[u][n];
                     const float (&d)[4] = part[u][n];
+                    uint64_t d0 = pair(d[0], d[1]), d1 = pair(d[2], d[3]), t0 = s0, t1 = s1;
+                    if (kBare<FP8, NL>) {
+                        d0 = add2(d0, pair(eights[n][0], eights[n][1]));
+                        d1 = add2(d1, pair(eights[n][2], eights[n][3]));
+                    }
                     if (FP8) {
                         const float2 q = *reinterpret_cast<const float2*>(xs + n * 8);
-                        const bool bare = kBare<FP8, NL>;
-                        v[0] = fmaf(bare ? d[0] + eights[n][0] : d[0], s0 * q.x, v[0]);
-                        v[1] = fmaf(bare ? d[1] + eights[n][1] : d[1], s0 * q.y, v[1]);
-                        v[2] = fmaf(bare ? d[2] + eights[n][2] : d[2], s1 * q.x, v[2]);
-                        v[3] = fmaf(bare ? d[3] + eights[n][3] : d[3], s1 * q.y, v[3]);
-                    } else {
-                        v[0] = fmaf(d[0], s0, v[0]);
-                        v[1] = fmaf(d[1], s0, v[1]);
-                        v[2] = fmaf(d[2], s1, v[2]);
-                        v[3] = fmaf(d[3], s1, v[3]);
+                        t0 = mul2(s0, pair(q.x, q.y));
+                        t1 = mul2(s1, pair(q.x, q.y));
                     }
+                    const float2 v0 = halves(fma2(d0, t0, pair(v[0], v[1]))), v1 = halves(fma2(d1, t1, pair(v[2], v[3])));
+                    v[0] = v0.x;
+                    v[1] = v0.y;
+                    v[2] = v1.x;
+                    v[3] = v1.y;
                 }
             }
         }
