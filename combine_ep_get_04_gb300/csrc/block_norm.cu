@@ -14,6 +14,7 @@ namespace {
 constexpr int kGateChannel = 1;
 constexpr int kGateToken = 2;
 constexpr int kVec = 8;   // channels a thread handles at once: 16 bytes of bf16
+constexpr int kMaxStages = 8;
 
 // Eight fp32 values as four pairs (f32x2), which halves the instructions a row costs.
 struct Vec8 {
@@ -186,6 +187,157 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
     }
 }
 
+// Many wide rows.  As above, with two differences.  A row is taken up in two
+// turns, so that its two sums come with those of its neighbours: turn i has the
+// mean square of row i's y and, with that of row i - 1 known, row i - 1's h_out
+// and its mean square, both joined behind one barrier.  And rows come by bulk
+// copies into a ring of stages in shared memory; a producer warp joins the
+// barrier and fills the stage that it sets free.
+// The barrier of a turn, which the producer warp joins.
+__device__ __forceinline__ void rows_barrier(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory"); }
+
+// Sums of two values over a CTA: lanes 0 to 15 deal with the first, the others
+// with the second.  `red` has two rows of 32.
+__device__ __forceinline__ float2 cta_sum2(float a, float b, float (*red)[32], int warps) {
+    const int lane = threadIdx.x & 31;
+    const bool high = lane & 16;
+    float x = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    {
+        if ((lane & 15) == 0) red[lane >> 4][threadIdx.x >> 5] = x;
+        rows_barrier(warps + 1);
+        const int w = lane & 15;
+        x = (w < warps ? red[lane >> 4][w] : 0.f) + (w + 16 < warps ? red[lane >> 4][w + 16] : 0.f);
+#pragma unroll
+        for (int d = 8; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    }
+    const float other = __shfl_xor_sync(0xffffffffu, x, 16);
+    return high ? make_float2(other, x) : make_float2(x, other);
+}
+
+template <bool F32, bool FULL>
+__global__ void __launch_bounds__(1024) norm_rows_kernel(NormParams p, int stages) {
+    extern __shared__ __align__(128) unsigned char ring[];       // [stages][h, y]
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ float red[2][2][32];
+    constexpr int kStream = F32 ? 4 : 2;
+    const int warps = (blockDim.x >> 5) - 1, at_y = p.H * kStream, stage_bytes = p.H * (kStream + 2);
+    const bool has_y = FULL || p.y != nullptr, has_post = FULL || p.w_post != nullptr, has_pre = FULL || p.w_pre != nullptr;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    __syncthreads();
+    const int rows = blockIdx.x < p.T ? (p.T - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    if (threadIdx.x >> 5 == warps) {
+        // producer: fills the ring, then the stage of row i - 1 behind the barrier of turn i
+        const int lane = threadIdx.x & 31;
+        const unsigned char* h = static_cast<const unsigned char*>(p.h) + (int64_t)blockIdx.x * p.ld_h * kStream;
+        const unsigned char* y = static_cast<const unsigned char*>(p.y) + (int64_t)blockIdx.x * p.ld_y * 2;
+        auto fetch = [&](int st) {
+            if (lane == 0) {
+                unsigned char* to = ring + st * stage_bytes;
+                mbar_arrive_expect_tx(&full[st], has_y ? stage_bytes : at_y);
+                bulk_load(to, h, at_y, &full[st]);
+                if (has_y) bulk_load(to + at_y, y, p.H * 2, &full[st]);
+            }
+            h += gridDim.x * p.ld_h * kStream;
+            y += gridDim.x * p.ld_y * 2;
+        };
+        for (int i = 0; i < min(stages, rows); ++i) fetch(i);
+        int st = 0;
+        uint32_t parity = 0;
+        bool lost = false;
+        for (int i = 0; i <= rows; ++i) {
+            __syncwarp();
+            rows_barrier(warps + 1);
+            if (i == 0) continue;
+            lost |= !__all_sync(0xffffffffu, mbar_wait(&full[st], parity));        // the consumers have waited: it is there
+            if (i - 1 + stages < rows) fetch(st);
+            if (++st == stages) {
+                st = 0;
+                parity ^= 1;
+            }
+        }
+        rows_barrier(warps + 1);
+        // where a copy did not come in time: seen in what is written
+        if (lost)
+            for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x)
+                for (int at = lane * kVec; at < p.H; at += 32 * kVec) {
+                    if (p.h_out != nullptr) store_stream<F32>(p.h_out, t * p.H + at, all(NAN));
+                    if (has_pre) store_bf16(p.n, t * p.H + at, all(NAN));
+                }
+        return;
+    }
+    const float inv_h = 1.f / (float)p.H;
+    const float scale = p.res_scale != nullptr ? *p.res_scale : 1.f;
+    const bool in = threadIdx.x < p.H / kVec;
+    const int at = in ? threadIdx.x * kVec : 0;
+    const Vec8 q = in && has_pre ? load_f32(p.w_pre, at) : all(0.f);
+    Vec8 w = in && has_post ? load_f32(p.w_post, at) : all(1.f);
+    if (in && p.gate_kind == kGateChannel) {
+        const Vec8 g = load_f32(p.gate, at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w.v[c] = mul2(w.v[c], g.v[c]);
+    }
+    unsigned char* h_to = static_cast<unsigned char*>(p.h_out) + (int64_t)blockIdx.x * p.H * kStream;
+    unsigned char* n_to = static_cast<unsigned char*>(p.n) + (int64_t)blockIdx.x * p.H * 2;
+    int64_t t = blockIdx.x;                       // row of turn i
+    float r1 = 1.f, gate = 1.f, next_gate = 1.f;
+    int st = 0, before = 0;                       // stages of rows i and i - 1
+    uint32_t parity = 0;
+    for (int i = 0; i <= rows; ++i) {
+        if (p.gate_kind == kGateToken && i < rows) next_gate = p.gate[t];
+        Vec8 h;
+        uint64_t ss2 = both(0.f), ss1 = ss2;
+        if (i > 0) {
+            const uint64_t r1_gate = both(r1 * gate), a2 = both(scale);
+            const unsigned char* row = ring + before * stage_bytes;
+            const Vec8 y = in && has_y ? load_bf16(row + at_y, at) : all(0.f);
+            h = in ? load_stream<F32>(row, at) : all(0.f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                h.v[c] = fma2(a2, h.v[c], mul2(mul2(y.v[c], r1_gate), w.v[c]));
+                ss2 = fma2(h.v[c], h.v[c], ss2);
+            }
+            if (in && (FULL || p.h_out != nullptr)) store_stream<F32>(h_to, at, h);
+            h_to += (int64_t)gridDim.x * p.H * kStream;
+        }
+        if (i < rows) {
+            mbar_wait(&full[st], parity);                     // the producer sees to rows that do not come
+            const Vec8 y = in && has_y ? load_bf16(ring + st * stage_bytes + at_y, at) : all(0.f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ss1 = fma2(y.v[c], y.v[c], ss1);
+        }
+        const float2 sums = cta_sum2(total(ss1), total(ss2), red[i & 1], warps);
+        if (i > 0 && has_pre) {
+            const float r2 = rsqrtf(fmaf(sums.y, inv_h, p.eps));
+            if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[p.T + t - gridDim.x] = r2;
+            const uint64_t r2_2 = both(r2);
+            Vec8 n;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) n.v[c] = mul2(mul2(h.v[c], r2_2), q.v[c]);
+            if (in) store_bf16(n_to, at, n);
+            n_to += (int64_t)gridDim.x * p.H * 2;
+        }
+        if (has_post) {
+            r1 = rsqrtf(fmaf(sums.x, inv_h, p.eps));
+            if (threadIdx.x == 0 && p.rstd != nullptr && i < rows) p.rstd[t] = r1;
+        }
+        gate = next_gate;
+        t += gridDim.x;
+        before = st;
+        if (++st == stages) {
+            st = 0;
+            parity ^= 1;
+        }
+    }
+    rows_barrier(warps + 1);
+}
+
 // ---------------------------------------------------------------- backward
 //
 // A row needs one reduction only: with e = d_h_out + r2 t (t = d_n w_pre) and
@@ -208,7 +360,6 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 // CTA order, so that nothing depends on the order in which CTAs run.
 
 constexpr int kCols = 4096;
-constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 4;
 constexpr int kSlots = 8;          // rows whose sums may be on their way; a writer is less than 6 rows ahead of a reader
 constexpr int kMaxWarps = kCols / kVec / 32;
@@ -585,6 +736,19 @@ size_t workspace_bytes(int T, int H) {
     return ((size_t)s.clusters * (2 * (size_t)H + s.cluster) * sizeof(float) + 15) / 16 * 16;
 }
 
+template <bool F32>
+cudaError_t launch_rows(const NormParams& p, int num_sms, cudaStream_t stream) {
+    const int warps = (p.H / kVec + 31) / 32;
+    const dim3 grid((unsigned)std::min(p.T, num_sms)), block(warps * 32 + 32);
+    const bool full = p.y != nullptr && p.w_post != nullptr && p.w_pre != nullptr && p.h_out != nullptr;
+    const size_t row = (size_t)p.H * (F32 ? 6 : 4);
+    const int stages = (int)std::min<size_t>(kMaxStages, kRingBytes / row);
+    auto kern = full ? norm_rows_kernel<F32, true> : norm_rows_kernel<F32, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(false, kern, grid, block, stages * row, stream, p, stages);
+}
+
 template <int NV, bool F32>
 cudaError_t launch_forward(const NormParams& p, int num_sms, cudaStream_t stream) {
     const int warps = (p.H / kVec + 32 * NV - 1) / (32 * NV);
@@ -603,6 +767,11 @@ cudaError_t launch_forward(const NormParams& p, int num_sms, cudaStream_t stream
 size_t norm_workspace_bytes(int T, int H) { return workspace_bytes(T, H); }
 
 cudaError_t launch_block_norm(const NormParams& p, int num_sms, cudaStream_t stream) {
+    // Wide rows, where the other form has one CTA on an SM, and many of them (us, other form | this one: T=16384 H=4096 f32
+    // 135 | 128; T=8192 H=5120 bf16 65 | 58, f32 99 | 80; T=4096 H=7168 bf16 42.7 | 41.7, f32 66.5 | 59.5; T=2560 H=7168
+    // bf16 28.5 | 29.4; T=700 10.5 | 12.7; T=16384 H=4096 bf16 86 | 98).  H > 7936 leaves no warp for the producer.
+    if (p.T >= 20 * num_sms && p.H >= (p.f32 ? 4096 : 4104) && p.H <= 31 * 32 * kVec)
+        return p.f32 ? launch_rows<true>(p, num_sms, stream) : launch_rows<false>(p, num_sms, stream);
     if (p.H <= 32 * 32 * kVec) return p.f32 ? launch_forward<1, true>(p, num_sms, stream) : launch_forward<1, false>(p, num_sms, stream);
     return p.f32 ? launch_forward<2, true>(p, num_sms, stream) : launch_forward<2, false>(p, num_sms, stream);
 }

@@ -107,6 +107,47 @@ def test_more_rows_than_the_grid_holds():
     check(2051, 2048, torch.bfloat16, "token", True, True, True)
 
 
+@pytest.mark.parametrize("T,H,dtype,gate,post,pre,scaled,block,pad", [
+    (3040, 4104, torch.bfloat16, "channel", True, True, True, True, 0), (3041, 4096, torch.float32, "token", True, True, True, True, 0),
+    (6100, 4104, torch.bfloat16, "token", True, True, True, True, 24), (3200, 7936, torch.float32, "channel", True, True, False, True, 8),
+    (3333, 7168, torch.bfloat16, None, True, True, False, True, 0), (3100, 5000, torch.float32, "token", False, True, True, True, 0),
+    (3100, 5000, torch.bfloat16, "channel", True, False, True, True, 0), (3100, 4800, torch.float32, "channel", False, False, True, True, 0),
+    (3100, 6008, torch.bfloat16, None, False, True, True, False, 0), (4000, 7944, torch.bfloat16, "token", True, True, True, True, 0)])
+def test_many_wide_rows(T, H, dtype, gate, post, pre, scaled, block, pad):
+    """The first and the last rows, all of some CTAs' and some of the others'."""
+    inputs, _ = make(T, H, dtype, gate, post, pre, scaled, block, pad=pad)
+    m = ep.BlockNorm(T, H, dtype, gate=gate, post=post, pre=pre, scaled=scaled, block=block, eps=EPS, train=True)
+    m.h_out.fill_(float("nan"))
+    h_out, n = m.forward(**inputs)
+    rows = torch.tensor(sorted({t for t in range(T) if t < 4 or t >= T - 160 or t % 152 in (5, 151) or t % 53 == 0}), device="cuda")
+    r = {k: v if k in ("w_post", "w_pre", "res_scale") or (k == "gate" and gate != "token") or v is None else v[rows] for k, v in inputs.items()}
+    r = {k: f64(v) for k, v in r.items()}
+    if gate == "token":
+        r["gate"] = r["gate"][:, None]
+    r["res_scale"] = 1.0 if r["res_scale"] is None else r["res_scale"][0]
+    v, z = ref.block_norm(**r, eps=EPS)
+    for name, x in dict(h_out=h_out, n=n).items():
+        if x is None:
+            continue
+        b = ref.bound(v[name], z[name], H, x.dtype == torch.bfloat16)
+        off = np.abs(f64(x[rows]) - v[name])
+        assert (off <= b).all(), f"{name}: {(off > b).sum()} of {off.size} beyond the bound, worst {(off - b).max():.3g} past it"
+    assert torch.isfinite(h_out).all() and (n is None or torch.isfinite(n).all())
+    # a root's relative error is half its argument's
+    for i, (there, x) in enumerate(((post, r["y"]), (pre, v["h_out"]))):
+        if there:
+            want = 1 / np.sqrt((x * x).mean(1) + EPS)
+            slack = np.sqrt((z["h_out"] ** 2).mean(1) / (x * x).mean(1)) if i else 1.0
+            assert (np.abs(f64(m.rstd[i][rows]) / want - 1) <= (H + 64) * ref.EPS32 * slack).all()
+    want = [None if x is None else x.clone() for x in (h_out, n)]
+    m.forward(**inputs)
+    assert torch.equal(m.h_out, want[0]) and (n is None or torch.equal(m.n, want[1]))
+    if not pad:
+        m.h_out = inputs["h"]                        # in place
+        m.forward(**inputs)
+        assert torch.equal(inputs["h"], want[0]) and (n is None or torch.equal(m.n, want[1]))
+
+
 def test_rows_of_zeros():
     """A row of zeros has mean square 0: eps alone stands under the root."""
     def edit(i):
