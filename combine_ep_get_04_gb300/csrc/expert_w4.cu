@@ -435,6 +435,13 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
 // block to the next.  The shares of a product form a cluster (of one row block
 // each) and add their accumulators through distributed shared memory in the
 // order of the shares.
+//
+// Up to 8 rows an expert the weights' bytes decide: 256 experts with 4 rows each,
+// gate and up (7168 -> 2 x 2048, fp8 rows) 606 us, down (2048 -> 7168, bf16 rows)
+// 325 us, 6.3 and 6.1 TB/s, 93 and 90 % of the measured copy rate.  With more
+// rows the matrix instructions and the widening do: 220 to 285 TFLOP/s from 16 to
+// 32 rows.  One row through one matrix of 4096 x 7168 is latency: 6.9 us against
+// 2.2 for its bytes.
 template <int NT, int G, bool FP8>
 __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4Params p, const __grid_constant__ CUtensorMap rows_map, int splits, int units,
                                                                                     int grid_tiles) {
