@@ -15,6 +15,7 @@
 // group's products are summed unscaled in fp32 and enter the accumulator
 // through one fused multiply-add with the group's scale.
 #include <algorithm>
+#include <atomic>
 #include <cuda.h>
 #include <type_traits>
 
@@ -677,6 +678,7 @@ size_t w4_smem(const W4Shape& w, int nt, bool fp8, int splits) {
 }
 
 constexpr size_t kMaxSmem = 227 * 1024 - 1024;
+constexpr size_t kSmSmem = 228 * 1024;
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -700,10 +702,50 @@ cudaError_t describe_rows(const W4Params& p, int rows, CUtensorMap* map) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Shared memory that a CTA asks for beyond its own needs, so that clusters are
+// spread over all SMs: the scheduler fills an SM before it takes the next, and
+// with room for four CTAs on each a few clusters would sit on half of them (one
+// row, 7168 -> 2 x 2048: 9.1 us so, 6.8 spread out).  At most as many CTAs to an
+// SM as leave a place for every cluster: a second wave would cost far more.
+template <int NT, int G, bool FP8>
+size_t spread_clusters(size_t smem, int splits, int64_t ctas, dim3 block) {
+    constexpr int kMost = 3;
+    static std::atomic<int> places[4][kMost];            // + 1, of clusters of 2, 4 and 8; 0: not asked yet
+    const int which = splits == 2 ? 1 : splits == 4 ? 2 : 3;
+    for (int per_sm = 1; per_sm <= kMost; ++per_sm) {
+        const size_t spread = (size_t)kSmSmem / (per_sm + 1);        // one more does not fit
+        if (spread > kMaxSmem || spread < smem) continue;
+        std::atomic<int>& known = places[which][per_sm - 1];
+        int n = known.load(std::memory_order_relaxed);
+        if (n == 0) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)splits;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.gridDim = dim3((unsigned)splits);
+            cfg.blockDim = block;
+            cfg.dynamicSmemBytes = spread;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaFuncSetAttribute(expert_w4_kernel<NT, G, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)spread) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&n, expert_w4_kernel<NT, G, FP8>, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                return smem;
+            }
+            known.store(++n, std::memory_order_relaxed);
+        }
+        if ((int64_t)(n - 1) * splits >= ctas) return spread;
+    }
+    return smem;
+}
+
 template <int NT, int G, bool FP8>
 cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles, cudaStream_t stream) {
     auto kern = expert_w4_kernel<NT, G, FP8>;
-    const size_t smem = w4_smem(p.w, NT, FP8, splits);
+    const dim3 grid((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits)), block(kThreads);
+    size_t smem = w4_smem(p.w, NT, FP8, splits);
+    if (splits > 1) smem = spread_clusters<NT, G, FP8>(smem, splits, grid.x, block);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     CUtensorMap map{};
@@ -711,8 +753,7 @@ cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles,
         e = describe_rows(p, 8 * NT, &map);
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits));
-    return launch_clusters(true, splits, kern, grid, dim3(kThreads), smem, stream, p, map, splits, units, (int)tiles);
+    return launch_clusters(true, splits, kern, grid, block, smem, stream, p, map, splits, units, (int)tiles);
 }
 
 template <int NT, bool FP8>
@@ -728,11 +769,13 @@ cudaError_t launch_rows(const W4Params& p, int num_sms, cudaStream_t stream) {
     const int64_t tiles = std::min<int64_t>(p.w.E, p.max_rows) + p.max_rows / (8 * NT);
     // tiles there will be: one for each expert in use, or full ones
     const int64_t products = std::max<int64_t>(std::min<int64_t>(p.w.E, p.max_rows), p.max_rows / (8 * NT)) * row_blocks(p.w);
-    // few products: share K among the CTAs of a cluster until there are two CTAs for every SM (one with wide tiles, of
-    // which two fit an SM)
+    // few products: share K among the CTAs of a cluster until there are two CTAs for every SM (one with wide tiles, whose
+    // sums are larger): one row of 4096 x 7168 11.7 us without, 9.6 with one CTA an SM, 6.9 with two; 16 experts with 32 rows
+    // of 1024 -> 2 x 1000 16.0 with one, 24.2 with two
     int splits = 1;
     while (splits < 8 && products * splits < (NT <= 2 ? 2 : 1) * num_sms && k_blocks(p.w) >= 4 * splits) splits *= 2;
-    // many short ones: several to a CTA, for at least 64 steps of K, as long as 16 CTAs for every SM remain
+    // many short ones: several to a CTA, for at least 64 steps of K, as long as 16 CTAs for every SM remain (256 experts,
+    // down, 2048 -> 7168: 361 us one by one, 326 four to a CTA)
     int units = 1;
     while (units * k_blocks(p.w) < 64 && products >= 32 * (int64_t)num_sms * units) units *= 2;
     return p.fp8 ? launch_group<NT, true>(p, splits, units, tiles, stream) : launch_group<NT, false>(p, splits, units, tiles, stream);
@@ -760,7 +803,8 @@ cudaError_t launch_w4_pack(const W4Shape& w, const uint8_t* codes, const void* s
 
 cudaError_t launch_expert_w4(const W4Params& p, int num_sms, cudaStream_t stream) {
     if (p.max_rows == 0) return cudaSuccess;
-    // tokens of a tile: enough for about twice an expert's share of the rows, up to 32
+    // Tokens of a tile: enough for about twice an expert's share of the rows, up to 32 (16 rows an expert, gate and up: 282 us
+    // with 16 to a tile, 242 with 32; one row of 4096 x 7168: 11.9 with 16, 6.9 with 8).
     const int64_t share = p.max_rows / std::min<int64_t>(p.w.E, p.max_rows);
     if (p.max_rows <= 8) return launch_rows<1>(p, num_sms, stream);
     if (share <= 8) return launch_rows<2>(p, num_sms, stream);
