@@ -22,7 +22,7 @@ constexpr int kMaxRouteWarps = 16;
 constexpr int kRunWarps = 16;          // of a CTA that sums its run
 constexpr int kChoiceTokens = 8;       // most tokens of its warps
 constexpr int kBackwardWarps = 8;
-constexpr int kBackwardTokens = 2;     // a warp's, in the backward pass: the second's loads overlap the first
+constexpr int kBackwardTokens = 4;     // most tokens of a warp in the backward pass
 constexpr int kSumWarps = 32;
 constexpr int kSumRuns = 8;
 constexpr int kSumCluster = 8;         // most CTAs of a sequence
@@ -644,9 +644,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(const __grid
 
 // Gradient, one warp per token: the probabilities are recomputed from the
 // logits and lse; what the chosen experts add is scattered through a row of
-// shared memory, which stays zero between tokens.  Two tokens a warp, the
-// second's loads behind the first's work: 4,096 tokens of 256 fp32 logits 3.9 us,
-// 32,768 15.8 us (4.5 TB/s; four tokens a warp 14.9, but 5.7 at 4,096).
+// shared memory, which stays zero between tokens.  32,768 tokens of 256 fp32
+// logits 14.9 us, 4.7 TB/s; 4,096 tokens 3.1 us, latency.
 template <int NPL, bool F32>
 __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(const __grid_constant__ RouteParams p) {
     constexpr int V = wide_values(NPL, F32), kRow = NPL * 32;
@@ -729,7 +728,8 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(con
 }
 
 // Tokens of a run: one for each warp until there are two CTAs for every SM,
-// then more, so that the per-run sums stay small beside the logits.
+// then more, so that the per-run sums stay small beside the logits (forward pass
+// of 32,768 tokens, 256 experts 31.7 us; with runs of up to 64 tokens 38.7).
 int run_tokens(int T) {
     const int per = (T + kRunWarps * 304 - 1) / (kRunWarps * 304);
     return kRunWarps * std::min(std::max(per, 1), 16);
@@ -806,7 +806,7 @@ cudaError_t launch_route(const RouteParams& in, int num_sms, cudaStream_t stream
     // of a CTA that only chooses (32,768 tokens: 256 experts 23.7 us with 4, 22.0 with 8; 512 experts in groups 20.3 and 22.0)
     const int choice_warps = p.E <= 256 ? 8 : 4;
     const int warps = sums ? kRunWarps : choice_warps;
-    // one token a warp until there are 8 CTAs for every SM
+    // one token a warp until there are 8 CTAs for every SM (32,768 tokens of 256 fp32 logits: 25.3 us one by one, 22.0 so)
     p.chunk = sums ? run_tokens(p.T) : choice_warps * std::min(std::max(p.T / (choice_warps * 8 * num_sms), 1), kChoiceTokens);
     const dim3 grid((unsigned)std::max<int64_t>(num_runs(p.T, p.chunk, p.S), 1)), block(warps * 32);
     const size_t smem = (size_t)(3 + (sums ? kRunWarps : 0)) * lane_values(p.E) * 32 * 4;
@@ -819,9 +819,12 @@ cudaError_t launch_route(const RouteParams& in, int num_sms, cudaStream_t stream
 }
 
 cudaError_t launch_route_backward(const RouteParams& in, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
     RouteParams p = in;
-    p.chunk = kBackwardWarps * kBackwardTokens;
+    // A wave of CTAs, as the registers hold them, up to 4 tokens a warp: a token's loads come behind the work on the one
+    // before (us with 1, 2, 3 and 4: 4,096 tokens of 256 fp32 logits 3.1, 3.9, 4.9, 5.7; 32,768 19.4, 15.7, 15.5, 14.9;
+    // 16,384 of 128 bf16 8.9, 7.3, 6.9, 8.2; 8,192 of 512 fp32 11.8, 9.6, 10.5, 8.5).
+    const int wave = kBackwardWarps * num_sms * (p.E <= 128 ? 6 : p.E <= 256 ? 4 : p.E <= 512 ? 2 : 1);
+    p.chunk = kBackwardWarps * std::min((p.T - 1) / wave + 1, kBackwardTokens);
     const dim3 grid((unsigned)num_runs(p.T, p.chunk, p.S));
     p.wide = wide_rows(p, p.logits, p.ld) && wide_rows(p, p.d_logits, p.E);
     return p.f32 ? launch_gradient<true>(p, grid, stream) : launch_gradient<false>(p, grid, stream);
