@@ -364,13 +364,11 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormParams p, int stage
 // Consumer warps leave their share of a row's three sums to another warp, which
 // adds them and joins them with those of the cluster's other CTAs (pass 1), and
 // take up the row again `lag` rows later (pass 2), when the sums are there, so
-// that none stands still at a row's end (one row of lag where an SM has several CTAs,
-// two where it has one).  The CTAs'
-// sums over rows go to the workspace once, and norm_columns_kernel adds them in
-// CTA order, so that nothing depends on the order in which CTAs run.
+// that none stands still at a row's end.  The CTAs' sums over rows go to the
+// workspace once, and norm_columns_kernel adds them in CTA order, so that nothing depends on the order in which CTAs run.
 //
 // T=16384 H=4096 fp32 188 us, 6.4 TB/s, 95 % of the measured copy rate; T=4096 H=7168
-// fp32 83 us, 93 %; bf16 67 us, 5.2 TB/s: at two bytes a value the instructions of the
+// fp32 83 us, 93 %; bf16 66 us, 5.3 TB/s: at two bytes a value the instructions of the
 // two passes (58 % of the issue slots with 16 warps an SM) weigh as much as the bytes.
 
 constexpr int kCols = 4096;
@@ -693,7 +691,8 @@ __global__ void __launch_bounds__(WARPS * 32) norm_backward_kernel(NormParams p,
 }
 
 // Adds `groups` rows of column sums and `ctas` sums for d_res_scale.  A CTA takes 32 columns; each warp adds every
-// kColumnWarps-th row, then the warps' sums are added in order.  4.4 MB at T=4096 H=7168: latency, about 4 us.
+// kColumnWarps-th row, then the warps' sums are added in order.  4.4 MB at T=4096 H=7168, 6.5 us by itself from a cold
+// cache: latency.
 __global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormParams p, int groups, int ctas) {
     __shared__ float part[kColumnWarps][32];
     pdl_launch_dependents();
@@ -736,11 +735,14 @@ BackwardShape backward_shape(int T, int H, int f32, int num_sms) {
     s.cluster = H <= kCols ? 1 : H <= 2 * kCols ? 2 : 4;
     s.cols = ((H / kVec + s.cluster - 1) / s.cluster) * kVec;
     s.warps = (s.cols / kVec + 31) / 32;
-    // narrow rows: as many CTAs on an SM as make 16 consumer warps and as its registers hold, 96 a thread
+    // narrow rows: as many CTAs on an SM as make 16 consumer warps and as its registers hold, 96 a thread (T=8192 H=256 bf16
+    // 21 us, with one CTA an SM 48; T=9000 H=1672 fp32 47 and 53)
     s.per_sm = std::max(1, std::min({6, 16 / s.warps, 65536 / (96 * 32 * (s.warps + 2))}));
     const size_t stage = (size_t)s.cols * (f32 ? 12 : 8);
     s.stages = (int)std::min<size_t>(kMaxStages, kRingBytes / s.per_sm / stage);
-    s.lag = std::min(s.per_sm > 1 ? 1 : 2, s.stages - 2);
+    // one CTA an SM has nothing else to do until a row's sums are there (T=4096 H=7168 bf16, 7 stages: 91 us with a lag of
+    // 1, 67 with 2, 66 with 3; fp32, 5 stages: 95, 83 and 88)
+    s.lag = std::min(s.per_sm > 1 ? 1 : s.stages >= 7 ? 3 : 2, s.stages - 2);
     s.clusters = std::min(T, std::min(num_sms, kMaxSms) * s.per_sm / s.cluster);
     return s;
 }
