@@ -5,8 +5,8 @@
 // kernels read and write each tensor once and are bound by HBM.
 #include <algorithm>
 
-#include "ep_device.cuh"
-#include "ep_kernels.h"
+#include "block_device.cuh"
+#include "block_kernels.h"
 
 namespace ep {
 namespace {

@@ -7,7 +7,7 @@
 #include <string>
 
 #include "ep.h"
-#include "ep_kernels.h"
+#include "block_kernels.h"
 
 namespace {
 

@@ -19,8 +19,8 @@
 #include <cuda.h>
 #include <type_traits>
 
-#include "ep_device.cuh"
-#include "ep_kernels.h"
+#include "block_device.cuh"
+#include "block_kernels.h"
 
 namespace ep {
 namespace {

@@ -12,8 +12,8 @@
 #include <cstring>
 #include <cuda_bf16.h>
 
-#include "ep_device.cuh"
-#include "ep_kernels.h"
+#include "block_device.cuh"
+#include "block_kernels.h"
 
 namespace ep {
 namespace {
