@@ -124,8 +124,9 @@ class W4Weights:
 
     codes u8 [E, rows, K/2]: input channel 2i in the low half of byte i; code c
     stands for (c - 8) * scale.  scales bf16 [E, rows, ceil(K / group)].
-    paired: rows are N gate rows and then N up rows of a SwiGLU.  codes and
-    scales are not needed afterwards.
+    paired: rows are N gate rows and then N up rows of a SwiGLU.  They are
+    packed on `stream`: wait for it before products on another one, and before
+    codes and scales, not needed afterwards, are overwritten.
     """
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, group: int = 128, paired: bool = False,
