@@ -728,8 +728,7 @@ size_t spread_clusters(size_t smem, int splits, int64_t ctas, dim3 block) {
             cfg.dynamicSmemBytes = spread;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
-            if (cudaFuncSetAttribute(expert_w4_kernel<NT, G, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)spread) != cudaSuccess ||
-                cudaOccupancyMaxActiveClusters(&n, expert_w4_kernel<NT, G, FP8>, &cfg) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&n, expert_w4_kernel<NT, G, FP8>, &cfg) != cudaSuccess) {
                 (void)cudaGetLastError();
                 return smem;
             }
@@ -744,10 +743,11 @@ template <int NT, int G, bool FP8>
 cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles, cudaStream_t stream) {
     auto kern = expert_w4_kernel<NT, G, FP8>;
     const dim3 grid((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits)), block(kThreads);
+    // the same value whatever a call needs: another thread may be between this and its launch
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+    if (e != cudaSuccess) return e;
     size_t smem = w4_smem(p.w, NT, FP8, splits);
     if (splits > 1) smem = spread_clusters<NT, G, FP8>(smem, splits, grid.x, block);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     CUtensorMap map{};
     if (x_boxes(NT)) {
         e = describe_rows(p, 8 * NT, &map);

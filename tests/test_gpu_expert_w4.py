@@ -3,6 +3,8 @@
 Bound: K products a sum, fp32 (the matrix instructions may cut off where a
 fused multiply-add rounds, so two units of 2^-24 a term), one rounding to bf16.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -152,6 +154,35 @@ def test_same_bits_twice_and_on_another_stream():
         b = ep.expert_w4(x, w, offsets=o, stream=s)
         s.synchronize()
         assert torch.equal(a, b) and torch.equal(a, ep.expert_w4(x, w, offsets=o))
+
+
+def test_calls_of_several_threads():
+    """Forms that need little and much shared memory, from two threads at once."""
+    jobs, errors = [], []
+    for i, K in enumerate((128, 16384)):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        w = ep.W4Weights(*make_weights(1, 64, K, 128, False, g), 128, False)
+        x, xs, _ = make_rows(4, K, "fp8", g)
+        jobs.append((w, x, xs, ep.expert_w4(x, w, x_scales=xs).clone()))
+    torch.cuda.synchronize()
+
+    def run(w, x, xs, want):
+        stream, got = torch.cuda.Stream(), torch.full_like(want, 7.0)
+        torch.cuda.synchronize()
+        try:
+            for _ in range(300):
+                ep.expert_w4(x, w, x_scales=xs, out=got, stream=stream)
+            stream.synchronize()
+            assert torch.equal(got, want)
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=job) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
 
 
 def test_bad_layouts_are_flagged_and_skipped():
