@@ -31,9 +31,11 @@ constexpr int kTiles = 8;          // tiles of one step, one for each consumer w
 constexpr int kCodeBytes = kTileRows * kTileK / 2;
 constexpr int kStep = 2;           // tiles along K of one stage of the ring
 constexpr int kRing = 2;           // stages
-constexpr int kWarps = 4;          // consumer warps, kOwn tiles each
-constexpr int kOwn = kTiles / kWarps;
-constexpr int kThreads = (kWarps + 1) * 32;
+
+// OWN: tiles of a consumer warp.  Two share the rows' operands; one, with twice
+// the warps, takes half the time for a step where an SM has few warps.
+__host__ __device__ constexpr int consumer_warps(int own) { return kTiles / own; }
+__host__ __device__ constexpr int block_threads(int own) { return (consumer_warps(own) + 1) * 32; }
 
 __host__ __device__ constexpr int tile_bytes(int group) { return kCodeBytes + kTileK / group * 32; }
 
@@ -305,13 +307,13 @@ __device__ __forceinline__ void box_load(void* dst, const CUtensorMap* map, int 
 // One tile step along K (128 channels) of a consumer warp: adds scale * code
 // sums to the accumulators, in units of 1 / kUnit.  wt: the warp's tiles, xr:
 // the lane's place in the first token row, xs: the rows' scales (fp8).
-template <int NT, int NL, int G, bool FP8>
-__device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsigned char* wt, const unsigned char* xr, const float* xs) {
+template <int NT, int OWN, int NL, int G, bool FP8>
+__device__ __forceinline__ void tile_step(float (&acc)[OWN][NT][4], const unsigned char* wt, const unsigned char* xr, const float* xs) {
     constexpr int kTile = 8 * x_row(NT, FP8), kChunk = x_chunk(NT, FP8);
     const int lane = threadIdx.x & 31, g = lane >> 2;
-    uint32_t w[kOwn][2][4];                // [tile][row g, row g + 8][32 channels each]
+    uint32_t w[OWN][2][4];                // [tile][row g, row g + 8][32 channels each]
 #pragma unroll
-    for (int u = 0; u < kOwn; ++u)
+    for (int u = 0; u < OWN; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint4 v = *reinterpret_cast<const uint4*>(wt + u * tile_bytes(G) + h * 512 + lane * 16);
@@ -320,14 +322,14 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
             w[u][h][2] = v.z;
             w[u][h][3] = v.w;
         }
-    float part[kOwn][NL][4], eights[NL][4];
+    float part[OWN][NL][4], eights[NL][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const bool first = i * 32 % G == 0;
         // operands of the low and the high pairs: channels 0 1 4 5 and 2 3 6 7 of the lane's eight
-        uint32_t a[kOwn][2][4];
+        uint32_t a[OWN][2][4];
 #pragma unroll
-        for (int u = 0; u < kOwn; ++u)
+        for (int u = 0; u < OWN; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t pair[4];
@@ -362,7 +364,7 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
                 mma16816<FP8>(d, high, b[1], b[3], d[0], d[1], d[2], d[3]);
             };
 #pragma unroll
-            for (int u = 0; u < kOwn; ++u) multiply(part[u][n], a[u][0], a[u][1]);
+            for (int u = 0; u < OWN; ++u) multiply(part[u][n], a[u][0], a[u][1]);
             if (kBare<FP8, NL>) {
                 const uint32_t low[4] = {kMinusEightLow, kMinusEightLow, kMinusEightLow, kMinusEightLow};
                 const uint32_t high[4] = {kMinusEightHigh, kMinusEightHigh, kMinusEightHigh, kMinusEightHigh};
@@ -371,7 +373,7 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
         }
         if ((i + 1) * 32 % G == 0) {
 #pragma unroll
-            for (int u = 0; u < kOwn; ++u) {
+            for (int u = 0; u < OWN; ++u) {
                 const uint32_t sc = *reinterpret_cast<const uint32_t*>(wt + u * tile_bytes(G) + kCodeBytes + i * 32 / G * 32 + g * 4);
                 const uint64_t s0 = both(bf16_lo(sc)), s1 = both(bf16_hi(sc));
 #pragma unroll
@@ -401,12 +403,12 @@ __device__ __forceinline__ void tile_step(float (&acc)[kOwn][NT][4], const unsig
 
 // A consumer warp's walk along K: `blocks` tile steps, kStep to a stage of the
 // ring from stage s on, NL x 8 tokens.  False if a wait timed out.
-template <int NT, int NL, int G, bool FP8>
-__device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigned char* smem, const float* xs, uint64_t* full,
+template <int NT, int OWN, int NL, int G, bool FP8>
+__device__ __forceinline__ bool consume(float (&acc)[OWN][NT][4], const unsigned char* smem, const float* xs, uint64_t* full,
                                         uint64_t* empty, int blocks, int& s, uint32_t& parity) {
     constexpr int kStage = stage_bytes(G, NT, FP8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const unsigned char* own = smem + warp * kOwn * tile_bytes(G);
+    const unsigned char* own = smem + warp * OWN * tile_bytes(G);
     const unsigned char* rows = smem + kStep * weight_bytes(G) + g * x_row(NT, FP8) + (FP8 ? 8 : 16) * t;
     xs += 2 * t;
     for (int left = blocks; left > 0; left -= kStep) {
@@ -416,7 +418,7 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
         // not unrolled: a short product runs this code from a cold instruction cache
 #pragma unroll 1
         for (int q = min(left, kStep); q > 0; --q) {
-            tile_step<NT, NL, G, FP8>(acc, wt, xr, xs);
+            tile_step<NT, OWN, NL, G, FP8>(acc, wt, xr, xs);
             wt += weight_bytes(G);
             xr += kTileK / 32 * x_chunk(NT, FP8);
             if (FP8) xs += 8 * NT;
@@ -443,12 +445,13 @@ __device__ __forceinline__ bool consume(float (&acc)[kOwn][NT][4], const unsigne
 // rows the matrix instructions and the widening do: 220 to 285 TFLOP/s from 16 to
 // 32 rows.  One row through one matrix of 4096 x 7168 is latency: 6.9 us against
 // 2.2 for its bytes.
-template <int NT, int G, bool FP8>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4Params p, const __grid_constant__ CUtensorMap rows_map, int splits, int units,
+template <int NT, int OWN, int G, bool FP8>
+__global__ void __launch_bounds__(block_threads(OWN), NT <= 2 ? 4 : OWN == 1 ? 2 : 3) expert_w4_kernel(W4Params p, const __grid_constant__ CUtensorMap rows_map, int splits, int units,
                                                                                     int grid_tiles) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kRing], empty[kRing];
     __shared__ RowTile shared_tile;
+    constexpr int kWarps = consumer_warps(OWN), kThreads = block_threads(OWN);
     constexpr int kWeights = weight_bytes(G);
     constexpr int kRows = 8 * NT;
     constexpr int kStage = stage_bytes(G, NT, FP8);
@@ -588,17 +591,17 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4
     int stage = 0;
     uint32_t parity = 0;
     for (int rb = rb0; rb < rb1 && good; ++rb) {
-        float acc[kOwn][NT][4];
+        float acc[OWN][NT][4];
 #pragma unroll
-        for (int u = 0; u < kOwn; ++u)
+        for (int u = 0; u < OWN; ++u)
 #pragma unroll
             for (int n = 0; n < NT; ++n) clear(acc[u][n]);
         // a form for each number of 8-token columns in use
         auto walk = [&](auto columns) {
             constexpr int NL = decltype(columns)::value < NT ? decltype(columns)::value : NT;
-            good = consume<NT, NL, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0, stage, parity);
+            good = consume<NT, OWN, NL, G, FP8>(acc, smem, xs, full, empty, kb1 - kb0, stage, parity);
 #pragma unroll
-            for (int u = 0; u < kOwn; ++u)
+            for (int u = 0; u < OWN; ++u)
 #pragma unroll
                 for (int n = 0; n < NL; ++n)
 #pragma unroll
@@ -618,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4
             const int owned = kTiles / splits;
             cluster_wait();                    // all CTAs of the cluster have started
 #pragma unroll
-            for (int u = 0; u < kOwn; ++u) {
-                const int own = warp * kOwn + u;
+            for (int u = 0; u < OWN; ++u) {
+                const int own = warp * OWN + u;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     cluster_store(parts + ((split * owned + own / splits) * NT + n) * 32 + lane, (uint32_t)(own % splits), acc[u][n]);
@@ -628,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4
             cluster_arrive();
             cluster_wait();
 #pragma unroll
-            for (int u = 0; u < kOwn; ++u) {
-                const int own = warp * kOwn + u;
+            for (int u = 0; u < OWN; ++u) {
+                const int own = warp * OWN + u;
                 if (own % splits != split) continue;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -651,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 4 : 3) expert_w4_kernel(W4
         const int g = lane >> 2, t = lane & 3;
         uint16_t* y = static_cast<uint16_t*>(p.y) + tile.first * p.w.N;
 #pragma unroll
-        for (int u = 0; u < kOwn; ++u) {
-            const int own = warp * kOwn + u, tile_at = rb * kTiles + own;
+        for (int u = 0; u < OWN; ++u) {
+            const int own = warp * OWN + u, tile_at = rb * kTiles + own;
             if (own % splits != split) continue;          // another share writes it
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -707,7 +710,7 @@ cudaError_t describe_rows(const W4Params& p, int rows, CUtensorMap* map) {
 // with room for four CTAs on each a few clusters would sit on half of them (one
 // row, 7168 -> 2 x 2048: 9.1 us so, 6.8 spread out).  At most as many CTAs to an
 // SM as leave a place for every cluster: a second wave would cost far more.
-template <int NT, int G, bool FP8>
+template <int NT, int OWN, int G, bool FP8>
 size_t spread_clusters(size_t smem, int splits, int64_t ctas, dim3 block) {
     constexpr int kMost = 3;
     static std::atomic<int> places[4][kMost];            // + 1, of clusters of 2, 4 and 8; 0: not asked yet
@@ -728,7 +731,7 @@ size_t spread_clusters(size_t smem, int splits, int64_t ctas, dim3 block) {
             cfg.dynamicSmemBytes = spread;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&n, expert_w4_kernel<NT, G, FP8>, &cfg) != cudaSuccess) {
+            if (cudaOccupancyMaxActiveClusters(&n, expert_w4_kernel<NT, OWN, G, FP8>, &cfg) != cudaSuccess) {
                 (void)cudaGetLastError();
                 return smem;
             }
@@ -739,15 +742,15 @@ size_t spread_clusters(size_t smem, int splits, int64_t ctas, dim3 block) {
     return smem;
 }
 
-template <int NT, int G, bool FP8>
+template <int NT, int OWN, int G, bool FP8>
 cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles, cudaStream_t stream) {
-    auto kern = expert_w4_kernel<NT, G, FP8>;
-    const dim3 grid((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits)), block(kThreads);
+    auto kern = expert_w4_kernel<NT, OWN, G, FP8>;
+    const dim3 grid((unsigned)(tiles * ((row_blocks(p.w) + units - 1) / units) * splits)), block(block_threads(OWN));
     // the same value whatever a call needs: another thread may be between this and its launch
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e != cudaSuccess) return e;
     size_t smem = w4_smem(p.w, NT, FP8, splits);
-    if (splits > 1) smem = spread_clusters<NT, G, FP8>(smem, splits, grid.x, block);
+    if (splits > 1) smem = spread_clusters<NT, OWN, G, FP8>(smem, splits, grid.x, block);
     CUtensorMap map{};
     if (x_boxes(NT)) {
         e = describe_rows(p, 8 * NT, &map);
@@ -756,11 +759,11 @@ cudaError_t launch_form(const W4Params& p, int splits, int units, int64_t tiles,
     return launch_clusters(true, splits, kern, grid, block, smem, stream, p, map, splits, units, (int)tiles);
 }
 
-template <int NT, bool FP8>
+template <int NT, int OWN, bool FP8>
 cudaError_t launch_group(const W4Params& p, int splits, int units, int64_t tiles, cudaStream_t stream) {
-    if (p.w.group == 32) return launch_form<NT, 32, FP8>(p, splits, units, tiles, stream);
-    if (p.w.group == 64) return launch_form<NT, 64, FP8>(p, splits, units, tiles, stream);
-    return launch_form<NT, 128, FP8>(p, splits, units, tiles, stream);
+    if (p.w.group == 32) return launch_form<NT, OWN, 32, FP8>(p, splits, units, tiles, stream);
+    if (p.w.group == 64) return launch_form<NT, OWN, 64, FP8>(p, splits, units, tiles, stream);
+    return launch_form<NT, OWN, 128, FP8>(p, splits, units, tiles, stream);
 }
 
 template <int NT>
@@ -778,7 +781,14 @@ cudaError_t launch_rows(const W4Params& p, int num_sms, cudaStream_t stream) {
     // down, 2048 -> 7168: 361 us one by one, 326 four to a CTA)
     int units = 1;
     while (units * k_blocks(p.w) < 64 && products >= 32 * (int64_t)num_sms * units) units *= 2;
-    return p.fp8 ? launch_group<NT, true>(p, splits, units, tiles, stream) : launch_group<NT, false>(p, splits, units, tiles, stream);
+    // few CTAs of wide tiles: one tile a warp (16 rows of 4096 x 4096 8.4 us with two, 7.1 with one; 40 of 4096 -> 2 x 1024 9.8
+    // and 8.8; 16 experts with 32 rows of 1024 -> 2 x 1000 16.0 and 19.0, 64 with 16 of 7168 -> 2 x 2048 242 and 291)
+    if (NT > 2 && tiles * row_blocks(p.w) * splits <= 2 * num_sms) {
+        constexpr int OWN = NT > 2 ? 1 : 2;
+        return p.fp8 ? launch_group<NT, OWN, true>(p, splits, units, tiles, stream)
+                     : launch_group<NT, OWN, false>(p, splits, units, tiles, stream);
+    }
+    return p.fp8 ? launch_group<NT, 2, true>(p, splits, units, tiles, stream) : launch_group<NT, 2, false>(p, splits, units, tiles, stream);
 }
 
 }  // namespace

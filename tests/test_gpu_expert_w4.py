@@ -104,6 +104,13 @@ def test_uneven_experts(capacity):
     check([40, 40, 39, 33, 64], 64, 256, 32, capacity=capacity)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind,K", [("bf16", 264), ("bf16", 1000), ("fp8", 384), ("ue8m0", 640)])
+@pytest.mark.parametrize("paired", [False, True])
+def test_wide_tiles_in_many_ctas(group, kind, K, paired):
+    check([0, 1, 30, 33, 17, 8, 24, 64, 25, 40, 12, 9, 31, 2, 16, 50, 7, 32, 13, 21, 26, 19], 2040, K, group, paired, kind)
+
+
 def test_many_experts():
     rng = np.random.default_rng(4)
     check(rng.poisson(0.7, 1024).tolist(), 16, 128, 32)
