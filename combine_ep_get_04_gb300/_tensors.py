@@ -54,3 +54,13 @@ def _shaped_ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tu
 
 def _stream(stream: torch.cuda.Stream | None) -> int | None:
     return (_raw_stream(_current_device()) if stream is None else stream.cuda_stream) or None
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream: torch.cuda.Stream | None) -> torch.Tensor:
+    """Memory that is written on `stream`.  Of that stream's own: what the
+    allocator has for the current one may still be read there, and would go
+    back to it while `stream` writes."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)

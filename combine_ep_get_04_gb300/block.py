@@ -10,7 +10,8 @@
 
 As elsewhere in this package, objects allocate their outputs and workspace
 once, and calls only launch kernels on the given (or current) stream: a
-second call overwrites what the first returned.
+second call overwrites what the first returned.  (expert_w4 is a function: it
+allocates its result where no `out` is given.)
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ import torch
 
 from ._lib import (CAPACITY, GATE_CHANNEL, GATE_NONE, GATE_TOKEN, PACKED, PAYLOAD_BF16, PAYLOAD_FP8_E4M3,
                    PAYLOAD_FP8_E4M3_UE8M0, TYPE_BF16, TYPE_F32, W4, Norm, Route, check, load)
-from ._tensors import _ptr, _rows_ptr, _shaped_ptr, _stream
+from ._tensors import _empty, _ptr, _rows_ptr, _shaped_ptr, _stream
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
 _GATES = {None: GATE_NONE, "channel": GATE_CHANNEL, "token": GATE_TOKEN}
@@ -125,8 +126,9 @@ class W4Weights:
     codes u8 [E, rows, K/2]: input channel 2i in the low half of byte i; code c
     stands for (c - 8) * scale.  scales bf16 [E, rows, ceil(K / group)].
     paired: rows are N gate rows and then N up rows of a SwiGLU.  They are
-    packed on `stream`: wait for it before products on another one, and before
-    codes and scales, not needed afterwards, are overwritten.
+    packed on `stream`, whose memory they are: wait for it before products on
+    another one, and before codes and scales are overwritten.  Codes and scales
+    are not needed afterwards and may be dropped at once.
     """
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, group: int = 128, paired: bool = False,
@@ -145,7 +147,10 @@ class W4Weights:
             check(1, "ep_w4_bytes")
         cp = _ptr(codes, torch.uint8, "codes")
         sp = _shaped_ptr(scales, torch.bfloat16, "scales", (E, rows, -(-self.K // group)))
-        self.packed = torch.empty(int(nbytes), dtype=torch.uint8, device=codes.device)
+        self.packed = _empty(int(nbytes), torch.uint8, codes.device, stream)
+        if stream is not None:
+            for t in (codes, scales):
+                t.record_stream(stream)         # the allocator does not hand them out again before they are packed
         self._lib, self._packed = lib, _ptr(self.packed)
         check(lib.ep_w4_pack(self._ref, cp, sp, self._packed, _stream(stream)), "ep_w4_pack")
 
@@ -161,6 +166,8 @@ def expert_w4(x: torch.Tensor, weights: W4Weights, counts: torch.Tensor | None =
     (neither for a single matrix over all rows); capacity as in Plan.  max_rows:
     rows in use at most (T * k), all of x if not given.  Returns bf16 [R, N];
     rows without a copy are left as they were (without `out`, undefined).
+    Without `out` the result is allocated by this call, as memory of `stream`
+    where one is given (as under `with torch.cuda.stream(stream)`).
     """
     w = weights
     if x.dim() != 2 or x.shape[1] != w.K:
@@ -178,7 +185,7 @@ def expert_w4(x: torch.Tensor, weights: W4Weights, counts: torch.Tensor | None =
     if counts is None and offsets is None and w.E != 1:
         raise ValueError("several experts need the layout's counts and offsets")
     if out is None:
-        out = torch.empty((R, w.N), dtype=torch.bfloat16, device=x.device)
+        out = _empty((R, w.N), torch.bfloat16, x.device, stream)
     st = w._lib.ep_expert_w4(
         w._ref, w._packed, PACKED if capacity is None else CAPACITY, capacity or 0, R, R if max_rows is None else max_rows,
         _shaped_ptr(counts, torch.int32, "counts", (w.E,)), _shaped_ptr(offsets, torch.int32, "offsets", (w.E + 1,)), xp, sp, payload,

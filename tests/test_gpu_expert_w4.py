@@ -263,3 +263,54 @@ def test_short_last_step_with_many_rows(K, rows):
     check([rows], 72, K, 32, True)
     check([rows, 3, 40], 24, K, 128, False)
     check([rows, 0, 40], 24, K, 64, False, capacity=45)
+
+
+def test_memory_of_a_call_on_another_stream():
+    """What a call on a stream allocates is that stream's: it is not what other
+    work may still be reading, nor handed out while the call runs; codes and
+    scales may be dropped at once.  (Seen from the addresses: nothing here would
+    read or write memory in use even if it were not so.)"""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    codes, scales = make_weights(1, 4096, 1024, 128, False, g)
+    kept = ep.W4Weights(codes, scales)
+    x = torch.randn(256, 1024, generator=g, device="cuda").bfloat16()
+    want = ep.expert_w4(x, kept).clone()
+    s = torch.cuda.Stream()
+
+    def block(nbytes):
+        """A block of the current stream, freed: the next of its size there."""
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda").data_ptr()
+
+    freed = block(want.numel() * 2)
+    assert freed == torch.empty(want.numel() * 2, dtype=torch.uint8, device="cuda").data_ptr()
+    y = ep.expert_w4(x, kept, stream=s)
+    assert y.data_ptr() != freed
+    s.synchronize()
+    assert torch.equal(y, want)
+    y = y.data_ptr()                                    # dropped: memory of s
+    assert torch.empty(want.numel() * 2, dtype=torch.uint8, device="cuda").data_ptr() != y
+
+    freed = block(kept.packed.numel())
+    w = ep.W4Weights(codes, scales, stream=s)
+    assert w.packed.data_ptr() != freed
+    s.synchronize()
+    assert torch.equal(w.packed, kept.packed)
+
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    mine = [t.clone() for t in (codes, scales)]
+    places = [(t.data_ptr(), t.numel() * t.element_size()) for t in mine]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)                  # some 50 ms
+    w = ep.W4Weights(*mine, stream=s)
+    packed = torch.cuda.Event()
+    packed.record(s)
+    del mine
+    again = [torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr() for _, n in places]
+    assert not packed.query(), "the packing was over before the addresses were looked at"
+    assert not {p for p, _ in places} & set(again)
+    s.synchronize()
+    assert torch.equal(w.packed, kept.packed)
