@@ -563,6 +563,8 @@ __global__ void __launch_bounds__(block_threads(OWN), NT <= 2 ? 4 : OWN == 1 ? 2
                         const uint32_t words = (wanted - piece) / 16;
                         for (uint32_t i = lane; i < words * tile.rows; i += 32)
                             *reinterpret_cast<uint4*>(xt + i / words * kRow + piece + i % words * 16) = make_uint4(0, 0, 0, 0);
+                        // the next row block's copies write the same bytes: plain stores go before them
+                        fence_proxy_async_smem();
                         __syncwarp();
                     }
                     if (lane == 0) {

@@ -314,3 +314,25 @@ def test_memory_of_a_call_on_another_stream():
     assert not {p for p, _ in places} & set(again)
     s.synchronize()
     assert torch.equal(w.packed, kept.packed)
+
+
+def spread(E, few, seed=0):
+    """Rows of E experts, up to `few` each, some none."""
+    return np.random.default_rng(seed).integers(0, few + 1, E).tolist()
+
+
+@pytest.mark.parametrize("counts,N,K,group,paired,kind", [
+    (spread(240, 8), 2680, 200, 64, False, "bf16"),       # 2 steps of K, the second short: 21 row blocks, two to a CTA
+    (spread(240, 8, 1), 2680, 264, 128, False, "bf16"),   # 3 steps: a stage of two and a short one
+    (spread(240, 8, 2), 1336, 136, 32, True, "bf16"),
+    (spread(240, 14, 3), 2680, 72, 64, False, "bf16"),    # one short step; some experts with two columns of tokens
+    (spread(240, 8, 4), 2680, 384, 128, False, "fp8"),
+    (spread(240, 8, 5), 1336, 128, 64, True, "ue8m0"),
+    (spread(470, 8, 6), 2680, 136, 64, False, "bf16"),    # four to a CTA, the last CTA with one
+    ([1] * 8, 78088, 136, 128, False, "bf16"),            # no more than 8 rows in all
+    ([20, 3, 33, 9] * 20, 9752, 136, 128, False, "bf16"), # rows by tensor copies
+])
+def test_several_row_blocks_a_cta(counts, N, K, group, paired, kind):
+    """At least 32 x 152 products of 128 weight rows, so that a CTA takes several
+    and its ring runs on from one to the next, over a short last step of K too."""
+    check(counts, N, K, group, paired, kind, max_rows=sum(counts))
