@@ -14,12 +14,12 @@
 
 #include "block_device.cuh"
 #include "block_kernels.h"
+#include "route_runs.h"
 
 namespace ep {
 namespace {
 
 constexpr int kMaxRouteWarps = 16;
-constexpr int kRunWarps = 16;          // of a CTA that sums its run
 constexpr int kChoiceTokens = 8;       // most tokens of its warps
 constexpr int kBackwardWarps = 8;
 constexpr int kBackwardTokens = 4;     // most tokens of a warp in the backward pass
@@ -246,7 +246,7 @@ __device__ __forceinline__ uint32_t choose_groups(const RouteParams& p, int lane
 // bits: every round looks for the next pair (key, index) in memory.  Returns
 // lane j's expert, or -1.
 template <bool F32>
-__device__ __noinline__ int choose_exactly(const RouteParams& p, int t, uint32_t keep) {
+__device__ __noinline__ int choose_exactly(const RouteParams& p, uint32_t t, uint32_t keep) {
     const int lane = threadIdx.x & 31;
     uint32_t last = kAll;
     int last_e = -1, chosen = -1;
@@ -275,7 +275,7 @@ __device__ __noinline__ int choose_exactly(const RouteParams& p, int t, uint32_t
 // last) into the order of their whole keys: one look at each key, and every
 // lane counts the candidates before its own.  Returns lane j's expert.
 template <bool F32>
-__device__ __forceinline__ int reorder(const RouteParams& p, int t, int e, int count) {
+__device__ __forceinline__ int reorder(const RouteParams& p, uint32_t t, int e, int count) {
     const int lane = threadIdx.x & 31;
     uint32_t key = 0;
     if (e >= 0) {
@@ -342,11 +342,11 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
     const Run run = find_run(p, blockIdx.x);
     __syncthreads();
     constexpr int kSize = F32 ? 4 : 2;
-    const unsigned char* row = static_cast<const unsigned char*>(p.logits) + ((int64_t)(run.begin + warp) * p.ld + e0) * kSize;
+    const unsigned char* row = static_cast<const unsigned char*>(p.logits) + ((int64_t)first_token(run.begin, warp) * p.ld + e0) * kSize;
     RawLogits<NPL, F32> next;
     bool next_mask = true;
-    auto fetch = [&](int t) {      // a token's logits are on their way while the one before it is worked on
-        if (t >= run.end) return;
+    auto fetch = [&](uint32_t t) {      // a token's logits are on their way while the one before it is worked on
+        if (!in_run(t, run.end)) return;
         next.load(row, left, p.wide != 0);
         next_mask = p.token_mask == nullptr || p.token_mask[t] != 0;
         row += warps * p.ld * kSize;
@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
     for (int i = 0; i < NPL; ++i) psum[i] = 0.f;
     float z = 0.f;
     int n_live = 0;
-    fetch(run.begin + warp);
-    for (int t = run.begin + warp; t < run.end; t += warps) {
+    fetch(first_token(run.begin, warp));
+    for (uint32_t t = first_token(run.begin, warp); in_run(t, run.end); t = next_token(t, warps)) {
         float l[NPL], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
             top = fmaxf(top, l[i]);
         }
         const bool mask = next_mask;
-        fetch(t + warps);
+        fetch(next_token(t, warps));
         const int64_t at = (int64_t)t * p.k;
         top = warp_max(top);
         if (!mask || !(top > -INFINITY)) {
@@ -660,13 +660,13 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(con
     pdl_wait();
     const Run run = find_run(p, blockIdx.x);
     constexpr int kSize = F32 ? 4 : 2;
-    const unsigned char* row = static_cast<const unsigned char*>(p.logits) + ((int64_t)(run.begin + warp) * p.ld + e0) * kSize;
-    unsigned char* d_row = static_cast<unsigned char*>(p.d_logits) + ((int64_t)(run.begin + warp) * p.E + e0) * kSize;
+    const unsigned char* row = static_cast<const unsigned char*>(p.logits) + ((int64_t)first_token(run.begin, warp) * p.ld + e0) * kSize;
+    unsigned char* d_row = static_cast<unsigned char*>(p.d_logits) + ((int64_t)first_token(run.begin, warp) * p.E + e0) * kSize;
     RawLogits<NPL, F32> next;
     float next_lse = 0.f, next_w = 0.f, next_dw = 0.f;
     int next_chosen = -1;
-    auto fetch = [&](int t) {      // a token's values are on their way while the one before it is worked on
-        if (t >= run.end) return;
+    auto fetch = [&](uint32_t t) {      // a token's values are on their way while the one before it is worked on
+        if (!in_run(t, run.end)) return;
         next_lse = p.lse[t];
         next.load(row, left, p.wide != 0);
         row += kBackwardWarps * p.ld * kSize;
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(con
             next_dw = p.d_topk_w[at];
         }
     };
-    fetch(run.begin + warp);
+    fetch(first_token(run.begin, warp));
     const int n_s = p.seq_tokens[run.s], n = p.seq_tokens[p.S], seqs = p.seq_tokens[p.S + 1];
     float d_balance = 0.f, d_z = 0.f;
     if (p.d_losses != nullptr && n_s > 0) {
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(con
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
         g[i] = value_at<V>(i) < left ? d_balance * (float)p.counts[(int64_t)run.s * p.E + e0 + value_at<V>(i)] : 0.f;
-    for (int t = run.begin + warp; t < run.end; t += kBackwardWarps) {
+    for (uint32_t t = first_token(run.begin, warp); in_run(t, run.end); t = next_token(t, kBackwardWarps)) {
         float l[NPL];
 #pragma unroll
         for (int i = 0; i < NPL; ++i) l[i] = next.get(i);
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(con
         const int chosen = next_chosen >= 0 && next_chosen < p.E ? next_chosen : -1;
         const float w = chosen >= 0 ? next_w : 0.f;
         float dw = chosen >= 0 ? next_dw : 0.f;
-        fetch(t + kBackwardWarps);
+        fetch(next_token(t, kBackwardWarps));
         float d[NPL];
         if (lse == -INFINITY) {
 #pragma unroll
@@ -727,14 +727,6 @@ __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(con
     }
 }
 
-// Tokens of a run: one for each warp until there are two CTAs for every SM,
-// then more, so that the per-run sums stay small beside the logits (forward pass
-// of 32,768 tokens, 256 experts 31.7 us; with runs of up to 64 tokens 38.7).
-int run_tokens(int T) {
-    const int per = (T + kRunWarps * 304 - 1) / (kRunWarps * 304);
-    return kRunWarps * std::min(std::max(per, 1), 16);
-}
-
 // Experts of a lane.
 int lane_values(int E) { return E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
 
@@ -743,8 +735,6 @@ bool wide_rows(const RouteParams& p, const void* base, int64_t ld) {
     const int values = wide_values(lane_values(p.E), p.f32 != 0), bytes = values * (p.f32 ? 4 : 2);
     return p.E % values == 0 && ld % values == 0 && reinterpret_cast<uintptr_t>(base) % bytes == 0;
 }
-
-int64_t num_runs(int T, int chunk, int S) { return ((int64_t)T + chunk - 1) / chunk + S - 1; }
 
 template <int NPL, bool F32>
 cudaError_t launch_choice(const RouteParams& p, dim3 grid, dim3 block, size_t smem, cudaStream_t stream) {

@@ -258,3 +258,37 @@ def test_logits_that_differ_in_their_last_bits(E, k, bias):
         check(-x, k, bias=b)
         if E % 4 == 0:
             check(x, k, 4, 2, bias=b)
+
+
+def test_the_largest_batch():
+    """2^31 - 1 tokens of one expert: token numbers past the end of the last run
+    do not fit a signed 32-bit number.  21 GB, with the losses and gradient 35."""
+    T = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 60 * 2 ** 30:
+        pytest.skip("needs 60 GB")
+    x = torch.full((T, 1), 0.5, dtype=torch.bfloat16, device="cuda")
+
+    def everywhere(t, want):
+        flat = t.view(-1)
+        return all(bool((part == want).all()) for part in flat.split(2 ** 28))
+
+    serve = ep.Router(T, 1, 1, dtype=torch.bfloat16)
+    serve.out.topk_idx.fill_(7)
+    o = serve.route(x)
+    assert everywhere(o.topk_idx, 0) and everywhere(o.topk_w, 1.0)
+    del serve, o
+    r = ep.Router(T, 1, 1, dtype=torch.bfloat16, balance_coef=1.0, z_coef=1.0, train=True)
+    r.out.topk_idx.fill_(7)
+    r.d_logits.fill_(7)
+    o = r.route(x)
+    assert everywhere(o.topk_idx, 0) and everywhere(o.topk_w, 1.0) and everywhere(o.lse, 0.5)
+    assert o.counts.item() == T and o.seq_tokens.tolist() == [T, T, 1]
+    # sums of 2^31 terms in runs of 256: chains of 256, 2^18 (a warp's runs) and 32 additions
+    bound = (256 + 2 ** 18 + 32) * ref.EPS32
+    assert abs(o.prob_sums.item() / T - 1) <= bound
+    assert abs(o.losses[0].item() - 1) <= 2 * bound and abs(o.losses[1].item() / 0.25 - 1) <= bound
+    # the probability is 1 and counts cancel: 2 lse / n of the z loss is left
+    d = r.backward(x, None, torch.tensor([1.0, float(T)], device="cuda"))
+    assert everywhere(d, 1.0)
+    del r, o, d, x
+    torch.cuda.empty_cache()
