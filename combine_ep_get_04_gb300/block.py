@@ -25,6 +25,7 @@ from ._lib import (CAPACITY, GATE_CHANNEL, GATE_NONE, GATE_TOKEN, PACKED, PAYLOA
 from ._tensors import _empty, _ptr, _rows_ptr, _shaped_ptr, _stream
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+_E4M3_ROWS = (torch.float8_e4m3fn, torch.uint8)
 _GATES = {None: GATE_NONE, "channel": GATE_CHANNEL, "token": GATE_TOKEN}
 
 
@@ -176,8 +177,8 @@ def expert_w4(x: torch.Tensor, weights: W4Weights, counts: torch.Tensor | None =
     if x_scales is None:
         payload, xp, sp = PAYLOAD_BF16, _shaped_ptr(x, torch.bfloat16, "x", (R, w.K)), None
     else:
-        if x.element_size() != 1:
-            raise TypeError("x_scales go with one-byte e4m3 rows")
+        if x.dtype not in _E4M3_ROWS:
+            raise TypeError(f"x_scales go with rows of e4m3 (torch.float8_e4m3fn, or torch.uint8 holding its codes), got {x.dtype}")
         if x_scales.dtype not in (torch.float32, torch.uint8):
             raise TypeError("x_scales must be float32 or uint8 (UE8M0)")
         payload = PAYLOAD_FP8_E4M3_UE8M0 if x_scales.dtype == torch.uint8 else PAYLOAD_FP8_E4M3

@@ -336,3 +336,14 @@ def test_several_row_blocks_a_cta(counts, N, K, group, paired, kind):
     """At least 32 x 152 products of 128 weight rows, so that a CTA takes several
     and its ring runs on from one to the next, over a short last step of K too."""
     check(counts, N, K, group, paired, kind, max_rows=sum(counts))
+
+
+def test_one_byte_rows_of_another_type_are_refused():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = ep.W4Weights(*make_weights(1, 16, 128, 128, False, g))
+    x, xs, _ = make_rows(4, 128, "fp8", g)
+    want = ep.expert_w4(x, w, x_scales=xs)
+    assert torch.equal(ep.expert_w4(x.view(torch.uint8), w, x_scales=xs), want)       # codes as bytes
+    for other in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.int8, torch.bool):
+        with pytest.raises(TypeError):
+            ep.expert_w4(x.view(other), w, x_scales=xs)
