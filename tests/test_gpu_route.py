@@ -292,3 +292,32 @@ def test_the_largest_batch():
     assert everywhere(d, 1.0)
     del r, o, d, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("E", [48, 128, 256, 512, 1000])
+def test_small_probabilities_are_as_close_as_large_ones(E, full):
+    """One expert far above the rest, by whole numbers from 24 to 80, so that each
+    argument of an exponential is exact and the sum is 1 to within 2^-24: what
+    is left of a probability's error is that of the exponential (at most two units
+    in its last place, 4 x 2^-24) and of some roundings, at every size of the
+    argument: 16 x 2^-24 for a probability, 24 x 2^-24 for a gradient."""
+    T, k = 60, 4
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x = -torch.randint(24 + (E > 300), 81, (T, E), generator=g, device="cuda").float()
+    top = torch.randint(0, E, (T,), generator=g, device="cuda")
+    x[torch.arange(T), top] = 0.0
+    bounds = list(range(T + 1))                         # each token its own sequence: prob_sums are probabilities
+    seq = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    r = ep.Router(T, E, k, full_softmax=full, num_seqs=T, balance_coef=BALANCE, z_coef=Z, train=True)
+    dl = torch.tensor([0.7, 0.0], device="cuda")
+    o = r.route(x, seq_offsets=seq)
+    d = r.backward(x, None, dl, seq).double().cpu().numpy()
+    idx, live = ref.choose(x.cpu().numpy(), None, None, k, 1, 1)
+    np.testing.assert_array_equal(o.topk_idx.cpu().numpy(), idx)
+    v, z = ref.route(x.double().cpu().numpy(), idx, live, np.array(bounds), full, BALANCE, Z, None, dl.double().cpu().numpy())
+    p = v["prob_sums"]
+    assert (p < 1e-30).sum() > T                        # down to exp(-80)
+    for name, got, size, units in (("prob_sums", o.prob_sums.double().cpu().numpy(), p, 16), ("d_logits", d, z["d_logits"], 24)):
+        off = np.abs(got - v[name]) / (units * ref.EPS32 * size)
+        assert (off <= 1).all(), f"{name}: {(off > 1).sum()} of {off.size} beyond the bound, worst {off.max():.3g} of it"
