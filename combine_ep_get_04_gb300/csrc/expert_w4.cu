@@ -173,8 +173,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 __device__ __forceinline__ void clear(float (&v)[4]) { v[0] = v[1] = v[2] = v[3] = 0.f; }
 
-// Both functions are good to a few units in the last place of fp32; the result is rounded to bf16.
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+// x times its sigmoid, by exp(-|x|): that never overflows, so a large negative
+// x leaves what exp(x) leaves of it.  expf is good to two units in the last
+// place; the fast form's error grows with |x|.
+__device__ __forceinline__ float silu(float x) {
+    const float e = expf(-fabsf(x));
+    return x * __fdividef(x < 0.f ? e : 1.f, 1.f + e);
+}
 
 struct RowTile {
     int e;          // expert, -1: none

@@ -347,3 +347,25 @@ def test_one_byte_rows_of_another_type_are_refused():
     for other in (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.int8, torch.bool):
         with pytest.raises(TypeError):
             ep.expert_w4(x.view(other), w, x_scales=xs)
+
+
+def test_gates_of_any_size():
+    """y = silu(gate) * up for exact gates and ups (one weight of 1 each): two
+    units in the last place of an exponential, a quotient and a product, 16 x
+    2^-24 in all, beside the steps of numbers below fp32's normal range and the
+    rounding to bf16."""
+    gates = torch.linspace(-110, 110, 881, device="cuda").bfloat16()
+    ups = torch.tensor([1.0, -3.0, 1e30, 1e-6], device="cuda").bfloat16()
+    x = torch.zeros(gates.numel() * 4, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1] = gates.repeat_interleave(4), ups.repeat(gates.numel())
+    codes = torch.full((1, 16, 4), 0x88, dtype=torch.uint8, device="cuda")
+    codes[0, :8, 0], codes[0, 8:, 0] = 0x89, 0x98
+    w = ep.W4Weights(codes, torch.ones(1, 16, 1, dtype=torch.bfloat16, device="cuda"), 32, True)
+    g, u = (x[:, i].double().cpu().numpy()[:, None] for i in (0, 1))
+    want = g / (1 + np.exp(-g)) * u
+    bound = ref.HALF_ULP_BF16 * np.abs(want) + 16 * ref.EPS32 * np.abs(want) + (np.abs(g) + 1) * 2.0 ** -149 * np.abs(u) + 2.0 ** -133
+    for rows in (5, 8, 40, x.shape[0]):          # every form
+        for at in range(0, x.shape[0], rows):
+            got = ep.expert_w4(x[at:at + rows], w).double().cpu().numpy()
+            off = np.abs(got - want[at:at + rows])
+            assert (off <= bound[at:at + rows]).all(), (rows, g[at:at + rows][(off > bound[at:at + rows]).any(1)])
