@@ -798,6 +798,12 @@ cudaError_t launch_rows(const W4Params& p, int num_sms, cudaStream_t stream) {
     return p.fp8 ? launch_group<NT, 2, true>(p, splits, units, tiles, stream) : launch_group<NT, 2, false>(p, splits, units, tiles, stream);
 }
 
+// Tokens of a tile, in columns of 8: enough for about twice an expert's share of the rows, up to 32 (16 rows an expert, gate
+// and up: 282 us with 16 to a tile, 242 with 32; one row of 4096 x 7168: 11.9 with 16, 6.9 with 8).
+int token_columns(const W4Shape& w, int64_t max_rows) {
+    return max_rows <= 8 ? 1 : max_rows / std::min<int64_t>(w.E, max_rows) <= 8 ? 2 : 4;
+}
+
 }  // namespace
 
 size_t w4_bytes(const W4Shape& w) {
@@ -807,8 +813,8 @@ size_t w4_bytes(const W4Shape& w) {
 bool w4_packs(const W4Shape& w) { return (int64_t)w.E * row_blocks(w) * k_blocks(w) * kTiles <= INT32_MAX; }
 
 bool w4_fits(const W4Shape& w, int64_t max_rows, int fp8) {
-    // shared memory of the widest form, CTAs of the narrowest
-    return w4_smem(w, 4, fp8 != 0, 8) <= kMaxSmem &&
+    // shared memory of the call's form, sharing K; CTAs of the narrowest
+    return w4_smem(w, token_columns(w, max_rows), fp8 != 0, 8) <= kMaxSmem &&
            (std::min<int64_t>(w.E, max_rows) + max_rows / 8) * row_blocks(w) * 8 <= INT32_MAX && max_rows <= (int64_t)1 << 29;
 }
 
@@ -820,12 +826,8 @@ cudaError_t launch_w4_pack(const W4Shape& w, const uint8_t* codes, const void* s
 
 cudaError_t launch_expert_w4(const W4Params& p, int num_sms, cudaStream_t stream) {
     if (p.max_rows == 0) return cudaSuccess;
-    // Tokens of a tile: enough for about twice an expert's share of the rows, up to 32 (16 rows an expert, gate and up: 282 us
-    // with 16 to a tile, 242 with 32; one row of 4096 x 7168: 11.9 with 16, 6.9 with 8).
-    const int64_t share = p.max_rows / std::min<int64_t>(p.w.E, p.max_rows);
-    if (p.max_rows <= 8) return launch_rows<1>(p, num_sms, stream);
-    if (share <= 8) return launch_rows<2>(p, num_sms, stream);
-    return launch_rows<4>(p, num_sms, stream);
+    const int nt = token_columns(p.w, p.max_rows);
+    return nt == 1 ? launch_rows<1>(p, num_sms, stream) : nt == 2 ? launch_rows<2>(p, num_sms, stream) : launch_rows<4>(p, num_sms, stream);
 }
 
 }  // namespace ep

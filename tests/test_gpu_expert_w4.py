@@ -369,3 +369,15 @@ def test_gates_of_any_size():
             got = ep.expert_w4(x[at:at + rows], w).double().cpu().numpy()
             off = np.abs(got - want[at:at + rows])
             assert (off <= bound[at:at + rows]).all(), (rows, g[at:at + rows][(off > bound[at:at + rows]).any(1)])
+
+
+def test_rows_too_long_for_a_wide_tile():
+    """A call whose own form holds a row's scales is answered, whatever the
+    others could; one whose form does not is refused."""
+    check([2], 16, 2 ** 18, 128, False, "fp8", bare=True)
+    check([3, 0, 8, 7, 2], 24, 2 ** 18, 64, True, "ue8m0")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = ep.W4Weights(*make_weights(1, 16, 2 ** 18, 128, False, g))
+    x, xs, _ = make_rows(40, 2 ** 18, "fp8", g)
+    with pytest.raises(ep.EPError):
+        ep.expert_w4(x, w, x_scales=xs)
