@@ -728,23 +728,37 @@ __global__ void __launch_bounds__(kColumnWarps * 32) norm_columns_kernel(NormPar
 
 constexpr int kMaxSms = 192;                      // the workspace has room for this many
 constexpr size_t kRingBytes = 216 * 1024;         // shared memory of an SM that the rings may take
+constexpr size_t kSmBytes = 228 * 1024;           // all of it,
+constexpr size_t kBesideRing = 4608;              // and what a CTA of the backward pass takes beside its ring: 3328 of its own, 1 KB reserved
 
-// clusters: at most this many, 0 for the workspace's bound.
 BackwardShape backward_shape(int T, int H, int f32, int num_sms) {
     BackwardShape s{};
     s.cluster = H <= kCols ? 1 : H <= 2 * kCols ? 2 : 4;
     s.cols = ((H / kVec + s.cluster - 1) / s.cluster) * kVec;
     s.warps = (s.cols / kVec + 31) / 32;
-    // narrow rows: as many CTAs on an SM as make 16 consumer warps and as its registers hold, 96 a thread (T=8192 H=256 bf16
-    // 21 us, with one CTA an SM 48; T=9000 H=1672 fp32 47 and 53)
-    s.per_sm = std::max(1, std::min({6, 16 / s.warps, 65536 / (96 * 32 * (s.warps + 2))}));
+    // narrow rows: as many CTAs on an SM as make 16 consumer warps and as its registers hold, 96 a thread, five warps to each
+    // quarter of the SM (T=8192 H=256 bf16 21 us, with one CTA an SM 48; T=9000 H=1672 fp32 47 and 53)
+    s.per_sm = std::max(1, std::min({6, 16 / s.warps, 20 / (s.warps + 2)}));
     const size_t stage = (size_t)s.cols * (f32 ? 12 : 8);
-    s.stages = (int)std::min<size_t>(kMaxStages, kRingBytes / s.per_sm / stage);
+    // no more stages than leave room for per_sm CTAs, or the grid runs a second, half-empty wave
+    s.stages = (int)std::min<size_t>(kMaxStages, std::min(kRingBytes / s.per_sm, kSmBytes / s.per_sm - kBesideRing) / stage);
     // one CTA an SM has nothing else to do until a row's sums are there (T=4096 H=7168 bf16, 7 stages: 91 us with a lag of
     // 1, 67 with 2, 66 with 3; fp32, 5 stages: 95, 83 and 88)
     s.lag = std::min(s.per_sm > 1 ? 1 : s.stages >= 7 ? 3 : 2, s.stages - 2);
     s.clusters = std::min(T, std::min(num_sms, kMaxSms) * s.per_sm / s.cluster);
     return s;
+}
+
+size_t ring_bytes(const BackwardShape& s, int f32) { return (size_t)s.stages * s.cols * (f32 ? 12 : 8); }
+
+using BackwardKernel = void (*)(NormParams, BackwardShape);
+
+BackwardKernel backward_kernel(const BackwardShape& s, int f32, bool full) {
+    if (s.warps + 2 <= 16 && s.per_sm == 1)
+        return f32 ? (full ? norm_backward_kernel<true, true, 16> : norm_backward_kernel<true, false, 16>)
+                   : (full ? norm_backward_kernel<false, true, 16> : norm_backward_kernel<false, false, 16>);
+    return f32 ? (full ? norm_backward_kernel<true, true, 18> : norm_backward_kernel<true, false, 18>)
+               : (full ? norm_backward_kernel<false, true, 18> : norm_backward_kernel<false, false, 18>);
 }
 
 size_t workspace_bytes(int T, int H) {
@@ -795,15 +809,8 @@ cudaError_t launch_block_norm(const NormParams& p, int num_sms, cudaStream_t str
 cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream) {
     const BackwardShape s = backward_shape(p.T, p.H, p.f32, num_sms);
     if (s.clusters > 0) {
-        const bool full = p.y != nullptr && p.d_n != nullptr && p.d_h_out != nullptr;
-        void (*kern)(NormParams, BackwardShape);
-        if (s.warps + 2 <= 16 && s.per_sm == 1)
-            kern = p.f32 ? (full ? norm_backward_kernel<true, true, 16> : norm_backward_kernel<true, false, 16>)
-                         : (full ? norm_backward_kernel<false, true, 16> : norm_backward_kernel<false, false, 16>);
-        else
-            kern = p.f32 ? (full ? norm_backward_kernel<true, true, 18> : norm_backward_kernel<true, false, 18>)
-                         : (full ? norm_backward_kernel<false, true, 18> : norm_backward_kernel<false, false, 18>);
-        const size_t smem = (size_t)s.stages * s.cols * (p.f32 ? 12 : 8);
+        const BackwardKernel kern = backward_kernel(s, p.f32, p.y != nullptr && p.d_n != nullptr && p.d_h_out != nullptr);
+        const size_t smem = ring_bytes(s, p.f32);
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
         if (e != cudaSuccess) return e;
         e = launch_clusters(true, s.cluster, kern, dim3(s.clusters * s.cluster), dim3(s.warps * 32 + 64), smem, stream, p, s);

@@ -3,6 +3,9 @@
 The bounds come from the formulas (block_reference.bound): a row's sums have H
 terms, sums over rows T terms, each result is rounded once to its type.
 """
+import os
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -235,3 +238,13 @@ def test_refusals():
         ep.BlockNorm(4, 16392)
     with pytest.raises(ep.EPError):
         ep.BlockNorm(4, 64, eps=0.0)
+
+
+def test_an_sm_holds_the_ctas_that_the_backward_pass_plans(tmp_path):
+    from combine_ep_get_04_gb300 import build as B
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = tmp_path / "norm_occupancy"
+    subprocess.run([B.nvcc(), *B.ARCH, *B.NVCC_FLAGS, os.path.join(here, "norm_occupancy.cu"), "-o", str(exe)], check=True,
+                   capture_output=True, text=True)
+    res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert res.returncode == 0, res.stdout + res.stderr
