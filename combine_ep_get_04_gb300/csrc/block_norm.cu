@@ -191,17 +191,6 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
     }
 }
 
-// Many wide rows.  As above, with two differences.  A row is taken up in two
-// turns, so that its two sums come with those of its neighbours: turn i has the
-// mean square of row i's y and, with that of row i - 1 known, row i - 1's h_out
-// and its mean square, both joined behind one barrier.  And rows come by bulk
-// copies into a ring of stages in shared memory; a producer warp joins the
-// barrier and fills the stage that it sets free.
-//
-// T=16384 H=4096 fp32 128 us, 6.3 TB/s, 92 % of the measured copy rate; T=4096 H=7168
-// fp32 59.5 us, 87 %, bf16 41.7 us, 83 %.  (Rows copied by each thread for itself, without
-// a producer, took 150, 78 and 42 us: a 16-byte copy of fp32 fetches half a sector.  The
-// ring filled by a consumer thread took 144, 60 and 46 us: all others wait for it.)
 // The barrier of a turn, which the producer warp joins.
 __device__ __forceinline__ void rows_barrier(int warps) { asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory"); }
 
@@ -225,17 +214,44 @@ __device__ __forceinline__ float2 cta_sum2(float a, float b, float (*red)[32], i
     return high ? make_float2(other, x) : make_float2(x, other);
 }
 
+// Waits for a row's copies, at most kWaitLimitNs.  A wait that runs out sets
+// *lost, with which the others end too.
+__device__ __forceinline__ void wait_row(uint64_t* bar, uint32_t parity, volatile int* lost) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*lost != 0) return;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *lost = 1;
+            return;
+        }
+    }
+}
+
+// Many wide rows.  As above, with two differences.  A row is taken up in two
+// turns, so that its two sums come with those of its neighbours: turn i has the
+// mean square of row i's y and, with that of row i - 1 known, row i - 1's h_out
+// and its mean square, both joined behind one barrier.  And rows come by bulk
+// copies into a ring of stages in shared memory; a producer warp joins the
+// barrier and fills the stage that it sets free.
+//
+// T=16384 H=4096 fp32 128 us, 6.3 TB/s, 92 % of the measured copy rate; T=4096 H=7168
+// fp32 59.5 us, 87 %, bf16 41.7 us, 83 %.  (Rows copied by each thread for itself, without
+// a producer, took 150, 78 and 42 us: a 16-byte copy of fp32 fetches half a sector.  The
+// ring filled by a consumer thread took 144, 60 and 46 us: all others wait for it.)
 template <bool F32, bool FULL>
 __global__ void __launch_bounds__(1024) norm_rows_kernel(NormParams p, int stages) {
     extern __shared__ __align__(128) unsigned char ring[];       // [stages][h, y]
     __shared__ uint64_t full[kMaxStages];
     __shared__ float red[2][2][32];
+    __shared__ int lost;                                         // a copy did not come in time
     constexpr int kStream = F32 ? 4 : 2;
     const int warps = (blockDim.x >> 5) - 1, at_y = p.H * kStream, stage_bytes = p.H * (kStream + 2);
     const bool has_y = FULL || p.y != nullptr, has_post = FULL || p.w_post != nullptr, has_pre = FULL || p.w_pre != nullptr;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
+        lost = 0;
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -246,7 +262,10 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormParams p, int stage
         const int lane = threadIdx.x & 31;
         const unsigned char* h = static_cast<const unsigned char*>(p.h) + (int64_t)blockIdx.x * p.ld_h * kStream;
         const unsigned char* y = static_cast<const unsigned char*>(p.y) + (int64_t)blockIdx.x * p.ld_y * 2;
+        volatile int* const missing = &lost;
+        int filled = 0;
         auto fetch = [&](int st) {
+            ++filled;
             if (lane == 0) {
                 unsigned char* to = ring + st * stage_bytes;
                 mbar_arrive_expect_tx(&full[st], has_y ? stage_bytes : at_y);
@@ -258,27 +277,30 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormParams p, int stage
         };
         for (int i = 0; i < min(stages, rows); ++i) fetch(i);
         int st = 0;
-        uint32_t parity = 0;
-        bool lost = false;
         for (int i = 0; i <= rows; ++i) {
             __syncwarp();
             rows_barrier(warps + 1);
             if (i == 0) continue;
-            lost |= !__all_sync(0xffffffffu, mbar_wait(&full[st], parity));        // the consumers have waited: it is there
-            if (i - 1 + stages < rows) fetch(st);
-            if (++st == stages) {
-                st = 0;
-                parity ^= 1;
-            }
+            // all consumers have seen row i - 1 come, or one of them has set `lost`
+            if (i - 1 + stages < rows && *missing == 0) fetch(st);
+            if (++st == stages) st = 0;
         }
+        __syncwarp();
         rows_barrier(warps + 1);
-        // where a copy did not come in time: seen in what is written
-        if (lost)
-            for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x)
+        if (*missing != 0) {
+            // no copy may be in flight when the CTA ends; and the loss is seen in what is written
+            for (int i = max(0, filled - stages); i < filled; ++i) mbar_wait(&full[i % stages], (i / stages) & 1);
+            for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
                 for (int at = lane * kVec; at < p.H; at += 32 * kVec) {
                     if (p.h_out != nullptr) store_stream<F32>(p.h_out, t * p.H + at, all(NAN));
                     if (has_pre) store_bf16(p.n, t * p.H + at, all(NAN));
                 }
+                if (lane == 0 && p.rstd != nullptr) {
+                    if (has_post) p.rstd[t] = NAN;
+                    if (has_pre) p.rstd[p.T + t] = NAN;
+                }
+            }
+        }
         return;
     }
     const float inv_h = 1.f / (float)p.H;
@@ -316,7 +338,7 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(NormParams p, int stage
             h_to += (int64_t)gridDim.x * p.H * kStream;
         }
         if (i < rows) {
-            mbar_wait(&full[st], parity);                     // the producer sees to rows that do not come
+            wait_row(&full[st], parity, &lost);
             const Vec8 y = in && has_y ? load_bf16(ring + st * stage_bytes + at_y, at) : all(0.f);
 #pragma unroll
             for (int c = 0; c < 4; ++c) ss1 = fma2(y.v[c], y.v[c], ss1);

@@ -382,7 +382,7 @@ typedef struct {
  *      rstd      f32 [2, T]: r1 then r2 of every row, for the backward pass
  *                (entries of a norm that is absent are not written), or NULL.
  * There are no err_flags: should a copy inside the kernel not end within its
- * time limit, the rows of that thread block come out as NaN.
+ * time limit, the rows of that thread block come out as NaN (rstd too).
  * h and h_out may be the same buffer when ld_h = H.  16-byte alignment of h,
  * y, w_post, w_pre, h_out, n and a channel gate; ld_h and ld_y multiples of 8
  * and at least H.

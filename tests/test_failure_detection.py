@@ -35,3 +35,18 @@ def test_bounded_wait_runs_out_reports_and_leaves_the_context_usable(tmp_path):
     assert f["err1"] == f["err2"] == f["err3"] == "cudaSuccess", out
     assert int(f["delivered_flag"]) == 0 and f["delivered_ok"] == "1", out
     assert f["plain_ok"] == "1", out
+
+
+def test_a_row_that_does_not_come_is_marked_once_and_ends_all_waits(tmp_path):
+    """The block norm's ring: the waiting warp itself marks the loss, so that no
+    row can arrive between its giving up and another warp's look."""
+    from combine_ep_get_04_gb300 import build as B
+    exe = tmp_path / "row_wait_timeout"
+    subprocess.run([B.nvcc(), *B.ARCH, *B.NVCC_FLAGS, os.path.join(HERE, "row_wait_timeout.cu"), "-o", str(exe)], check=True,
+                   capture_output=True, text=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=120).stdout
+    f = dict(kv.split("=", 1) for kv in out.split())
+    assert f["err"] == "cudaSuccess" and f["lost"] == "1" and f["lost_not"] == "0", out
+    assert 900.0 <= float(f["first_ms"]) <= 1500.0, out
+    assert 400.0 <= float(f["second_ms"]) <= 900.0, out
+    assert float(f["third_ms"]) <= 100.0 and float(f["there_ms"]) <= 100.0, out
