@@ -5,7 +5,8 @@ import torch
 
 
 # The raw handle of a device's current stream, without a Stream object around it.
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (A torch without CUDA has neither: the package can be imported there all the same.)
+_raw_stream, _current_device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
 def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "tensor",

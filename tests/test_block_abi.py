@@ -1,6 +1,9 @@
 """Host-side checks of the block operators' entry points: bad calls return an
 error before any CUDA call, so this runs without a GPU."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -129,3 +132,15 @@ def test_w4_arguments(lib):
     assert call(R=0) == 0 and call(rows=0) == 0
     assert call(R=2 ** 31) == _lib.EP_ERR_UNSUPPORTED
     assert call(shape=_lib.W4(1, 16, 1 << 20, 128, 0), payload=1, xs=FAKE) == _lib.EP_ERR_UNSUPPORTED   # a row's scales do not fit
+
+
+def test_import_on_a_torch_without_cuda(lib):
+    """A CPU build of torch has no CUDA bindings; what needs no GPU works there."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(ep.__file__)))
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_get')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import combine_ep_get_04_gb300 as ep\n"
+            "assert ep.recv_rows(ep.make_shape(4, 64, 8, 2)) == 8\n")
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
