@@ -381,3 +381,11 @@ def test_rows_too_long_for_a_wide_tile():
     x, xs, _ = make_rows(40, 2 ** 18, "fp8", g)
     with pytest.raises(ep.EPError):
         ep.expert_w4(x, w, x_scales=xs)
+
+
+@pytest.mark.parametrize("counts,N,K,group,paired,kind", [
+    ([1024], 4096, 512, 128, True, "fp8"), ([700], 3000, 264, 32, False, "bf16"), ([64, 70, 100, 65] * 4, 4096, 256, 128, False, "bf16"),
+    ([128, 0, 513, 64, 96, 1], 2048, 384, 64, True, "ue8m0"), ([90] * 30, 1000, 640, 128, False, "fp8")])
+def test_prompt_batches(counts, N, K, group, paired, kind):
+    """Many tiles of rows an expert."""
+    check(counts, N, K, group, paired, kind, max_rows=sum(counts))
