@@ -125,7 +125,13 @@ __device__ __forceinline__ void unpack(uint32_t word, uint32_t (&pair)[4]) {
 }
 
 // One fused multiply-add brings the pairs up to (code - 8) * 2^-6 in bf16 or
-// (code - 8) * 2^-9 in f16.  Exact.
+// (code - 8) * 2^-9 in f16.  Exact.  (Pairs that enter the products as they are,
+// with one more product for the offset, are not an alternative: the matrix
+// instruction lines products up by their exponents, a subnormal's as 2^-14
+// whatever its value, and cuts off what lies too far below the largest.  A
+// channel at e4m3's 448 under a zero weight cost 3 to 13 % of a result of its
+// smallest values.  256 experts, 4 fp8 rows each, gate and up, by groups of 32, 64
+// and 128: 717, 645 and 609 us so, 671, 637 and 619 with the multiply-adds.)
 template <bool F16>
 __device__ __forceinline__ void widen(uint32_t (&pair)[4]) {
 #pragma unroll
@@ -137,31 +143,14 @@ __device__ __forceinline__ void widen(uint32_t (&pair)[4]) {
     }
 }
 
-// Beside fp8 rows (bf16 would underflow) the pairs can enter the product as
-// they are, the low kind with rows 16 times as large, so that all products are
-// in units of 2^-20, and a product with -8 in the same units takes the offset
-// off: 8 products for each 8 tokens of the warp's two tiles in place of 64
-// multiply-adds.  With one column of 8 tokens the instructions saved decide,
-// with more the products added (256 experts, 4 rows each, gate and up: 781 us
-// without, 626 us with one column so, 650 us with two).
-template <bool FP8, int NL>
-constexpr bool kBare = FP8 && NL == 1;
-constexpr uint32_t kMinusEightLow = 0x80088008u, kMinusEightHigh = 0x80808080u;
-
 // What the codes are divided by.
-template <bool FP8, int NL>
-constexpr float kUnit = kBare<FP8, NL> ? 1048576.f : FP8 ? 512.f : 64.f;
+template <bool FP8>
+constexpr float kUnit = FP8 ? 512.f : 64.f;
 
 // Four e4m3 codes -> two pairs of f16, exact.
 __device__ __forceinline__ void f16x2_of_e4m3x4(uint32_t codes, uint32_t* lo, uint32_t* hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
         : "=r"(*lo), "=r"(*hi) : "r"(codes));
-}
-
-__device__ __forceinline__ uint32_t times16(uint32_t f16x2) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f16x2), "r"(0x4c004c00u));
-    return r;
 }
 
 // Transposes an 8 x 8 matrix of 16-bit values held two to a lane.
@@ -327,7 +316,7 @@ __device__ __forceinline__ void tile_step(float (&acc)[OWN][NT][4], const unsign
             w[u][h][2] = v.z;
             w[u][h][3] = v.w;
         }
-    float part[OWN][NL][4], eights[NL][4];
+    float part[OWN][NL][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const bool first = i * 32 % G == 0;
@@ -339,7 +328,7 @@ __device__ __forceinline__ void tile_step(float (&acc)[OWN][NT][4], const unsign
             for (int h = 0; h < 2; ++h) {
                 uint32_t pair[4];
                 unpack(w[u][h][i], pair);
-                if (!kBare<FP8, NL>) widen<FP8>(pair);
+                widen<FP8>(pair);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[u][j & 1][(j >> 1) * 2 + h] = pair[j];
             }
@@ -350,10 +339,6 @@ __device__ __forceinline__ void tile_step(float (&acc)[OWN][NT][4], const unsign
                 const uint2 v = *reinterpret_cast<const uint2*>(xr + n * kTile + i * kChunk);
                 f16x2_of_e4m3x4(v.x, &b[0], &b[1]);
                 f16x2_of_e4m3x4(v.y, &b[2], &b[3]);
-                if (kBare<FP8, NL>) {
-                    b[0] = times16(b[0]);
-                    b[2] = times16(b[2]);
-                }
             } else {
                 const uint4 v = *reinterpret_cast<const uint4*>(xr + n * kTile + i * kChunk);
                 b[0] = v.x;
@@ -370,11 +355,6 @@ __device__ __forceinline__ void tile_step(float (&acc)[OWN][NT][4], const unsign
             };
 #pragma unroll
             for (int u = 0; u < OWN; ++u) multiply(part[u][n], a[u][0], a[u][1]);
-            if (kBare<FP8, NL>) {
-                const uint32_t low[4] = {kMinusEightLow, kMinusEightLow, kMinusEightLow, kMinusEightLow};
-                const uint32_t high[4] = {kMinusEightHigh, kMinusEightHigh, kMinusEightHigh, kMinusEightHigh};
-                multiply(eights[n], low, high);
-            }
         }
         if ((i + 1) * 32 % G == 0) {
 #pragma unroll
@@ -385,11 +365,8 @@ __device__ __forceinline__ void tile_step(float (&acc)[OWN][NT][4], const unsign
                 for (int n = 0; n < NL; ++n) {
                     float (&v)[4] = acc[u][n];
                     const float (&d)[4] = part[u][n];
-                    uint64_t d0 = pair(d[0], d[1]), d1 = pair(d[2], d[3]), t0 = s0, t1 = s1;
-                    if (kBare<FP8, NL>) {
-                        d0 = add2(d0, pair(eights[n][0], eights[n][1]));
-                        d1 = add2(d1, pair(eights[n][2], eights[n][3]));
-                    }
+                    const uint64_t d0 = pair(d[0], d[1]), d1 = pair(d[2], d[3]);
+                    uint64_t t0 = s0, t1 = s1;
                     if (FP8) {
                         const float2 q = *reinterpret_cast<const float2*>(xs + n * 8);
                         t0 = mul2(s0, pair(q.x, q.y));
@@ -445,8 +422,8 @@ __device__ __forceinline__ bool consume(float (&acc)[OWN][NT][4], const unsigned
 // order of the shares.
 //
 // Up to 8 rows an expert the weights' bytes decide: 256 experts with 4 rows each,
-// gate and up (7168 -> 2 x 2048, fp8 rows) 606 us, down (2048 -> 7168, bf16 rows)
-// 325 us, 6.3 and 6.1 TB/s, 93 and 90 % of the measured copy rate.  With more
+// gate and up (7168 -> 2 x 2048, fp8 rows) 618 us, down (2048 -> 7168, bf16 rows)
+// 326 us, 6.2 and 6.1 TB/s, 91 and 90 % of the measured copy rate.  With more
 // rows the matrix instructions and the widening do: 220 to 285 TFLOP/s from 16 to
 // 32 rows.  One row through one matrix of 4096 x 7168 is latency: 6.9 us against
 // 2.2 for its bytes.
@@ -612,7 +589,7 @@ __global__ void __launch_bounds__(block_threads(OWN), NT <= 2 ? 4 : OWN == 1 ? 2
 #pragma unroll
                 for (int n = 0; n < NL; ++n)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[u][n][c] *= kUnit<FP8, NL>;      // a power of two
+                    for (int c = 0; c < 4; ++c) acc[u][n][c] *= kUnit<FP8>;      // a power of two
         };
         if (NT == 1 || (NT == 2 && tile.rows <= 8))
             walk(std::integral_constant<int, 1>{});

@@ -389,3 +389,32 @@ def test_rows_too_long_for_a_wide_tile():
 def test_prompt_batches(counts, N, K, group, paired, kind):
     """Many tiles of rows an expert."""
     check(counts, N, K, group, paired, kind, max_rows=sum(counts))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "ue8m0"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows", [1, 5, 8, 12, 40])
+@pytest.mark.parametrize("large", [1, 4])
+def test_small_channels_beside_a_large_one(rows, group, kind, large):
+    """One or four channels of each 128 at e4m3's largest value, with zero weights,
+    the others at multiples of its smallest, 2^-9.  Every product is a multiple of
+    2^-9, and sums of them stay below 2^14 even where the codes are taken as 0 to
+    15 and 8 times the row is taken off: 24 bits hold all of them exactly."""
+    K, N = 640, 72
+    g = torch.Generator(device="cuda").manual_seed(rows + group)
+    codes, _ = make_weights(1, N, K, group, False, g)
+    at = (torch.rand(K // 128, 128, generator=g, device="cuda").argsort(1)[:, :large] + 128 * torch.arange(K // 128, device="cuda")[:, None]).view(-1)
+    for parity in (0, 1):                       # two channels of one byte one after the other
+        here = at[at % 2 == parity]
+        half = codes[0, :, here // 2]
+        codes[0, :, here // 2] = (half & 0x0f) | 0x80 if parity else (half & 0xf0) | 8
+    scales = torch.ones(1, N, K // group, dtype=torch.bfloat16, device="cuda")
+    x = torch.randint(-7, 8, (rows, K), generator=g, device="cuda") * 2.0 ** -9
+    x[:, at] = 448.0 * (1 - 2 * torch.randint(0, 2, (rows, at.numel()), generator=g, device="cuda"))
+    x = x.to(torch.float8_e4m3fn)
+    xs = torch.full((rows, K // 128), 127, dtype=torch.uint8, device="cuda") if kind == "ue8m0" else torch.ones(rows, K // 128, device="cuda")
+    got = ep.expert_w4(x, ep.W4Weights(codes, scales, group), x_scales=xs).double().cpu().numpy()
+    _, y, size = ref.expert_w4(x.double().cpu().numpy(), codes.cpu().numpy(), scales.double().cpu().numpy(), group, False, [(0, 0, rows)])
+    b = ref.bound(y, size, 0, True)
+    off = np.abs(got - y)
+    assert (off <= b).all(), f"{(off > b).sum()} of {off.size} beyond the bound, worst {np.max(off / np.abs(y).mean()):.3g} of a mean result"
