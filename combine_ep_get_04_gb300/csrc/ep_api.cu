@@ -155,7 +155,8 @@ ep_status_t check_norm(const ep_norm_t* s) {
         return fail(EP_ERR_INVALID_ARG, "stream_type = %d is not a type", s->stream_type);
     if (s->gate_kind != EP_GATE_NONE && s->gate_kind != EP_GATE_CHANNEL && s->gate_kind != EP_GATE_TOKEN)
         return fail(EP_ERR_INVALID_ARG, "gate_kind = %d is not a gate kind", s->gate_kind);
-    if (!(s->eps > 0.f) || !(s->eps <= 1e30f)) return fail(EP_ERR_INVALID_ARG, "eps = %g must be positive and finite", (double)s->eps);
+    // the backward pass multiplies two reciprocal roots, each up to eps^-1/2
+    if (!(s->eps >= 1e-30f) || !(s->eps <= 1e30f)) return fail(EP_ERR_INVALID_ARG, "eps = %g must be in [1e-30, 1e30]", (double)s->eps);
     return ok();
 }
 

@@ -357,7 +357,8 @@ typedef struct {
                                  EP_MAX_NORM_WIDTH                             */
     int32_t stream_type;      /* ep_type_t of h, h_out, d_h_out and d_h        */
     int32_t gate_kind;        /* ep_gate_kind_t                                */
-    float eps;                /* > 0, added to the mean square of both norms   */
+    float eps;                /* 1e-30..1e30, added to the mean square of both
+                                 norms                                         */
 } ep_norm_t;
 
 /*

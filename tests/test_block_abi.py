@@ -144,3 +144,11 @@ def test_import_on_a_torch_without_cuda(lib):
             "assert ep.recv_rows(ep.make_shape(4, 64, 8, 2)) == 8\n")
     res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
+
+
+@pytest.mark.parametrize("eps", [1e-45, 1e-38, 9e-31, 2e30, -1e-6, float("inf")])
+def test_norm_refuses_an_eps_whose_roots_overflow(lib, eps):
+    s = _lib.Norm(4, 64, 0, 0, eps)
+    assert lib.ep_block_norm_workspace_bytes(ctypes.byref(s)) == ctypes.c_size_t(-1).value
+    assert lib.ep_block_norm(ctypes.byref(s), FAKE, 64, FAKE, 64, FAKE, None, None, FAKE, FAKE, FAKE, None, None) == _lib.EP_ERR_INVALID_ARG
+    assert lib.ep_block_norm_workspace_bytes(ctypes.byref(_lib.Norm(4, 64, 0, 0, 1e-30))) > 0

@@ -248,3 +248,23 @@ def test_an_sm_holds_the_ctas_that_the_backward_pass_plans(tmp_path):
                    capture_output=True, text=True)
     res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert res.returncode == 0, res.stdout + res.stderr
+
+
+def test_the_smallest_eps():
+    """Rows of zeros: the reciprocal roots are as large as they get, and their
+    products stay finite."""
+    T, H = 6, 264
+    inputs, grads = make(T, H, torch.float32, "channel", True, True, True)
+    for t in (1, 4):
+        inputs["h"][t], inputs["y"][t] = 0, 0
+    m = ep.BlockNorm(T, H, torch.float32, gate="channel", scaled=True, eps=1e-30, train=True)
+    h_out, n = m.forward(**inputs)
+    grads["d_h_out"][[1, 4]] *= 1e-20            # the gradient of a row of zeros is eps^-1/2 times the one behind it
+    grads["d_n"][[1, 4]] *= 1e-20
+    d = m.backward(**inputs, **grads)
+    r = {k: f64(v) for k, v in inputs.items()}
+    r["res_scale"] = r["res_scale"][0]
+    v, z = ref.block_norm(**r, eps=1e-30, **{k: f64(x) for k, x in grads.items()})
+    for name, x in dict(h_out=h_out, n=n, d_h=d.d_h, d_y=d.d_y, d_w_post=d.d_w_post, d_w_pre=d.d_w_pre, d_gate=d.d_gate).items():
+        b = ref.bound(v[name], z[name], H + T, x.dtype == torch.bfloat16)
+        assert (np.abs(f64(x) - v[name]) <= b).all(), name
