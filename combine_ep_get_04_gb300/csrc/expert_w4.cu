@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kTileRows = 16;      // weight rows of one tile (the matrix instruction's)
 constexpr int kTileK = 128;        // input channels of one tile
-constexpr int kTiles = 8;          // tiles of one step, one for each consumer warp
+constexpr int kTiles = 8;          // tiles of one step
 constexpr int kCodeBytes = kTileRows * kTileK / 2;
 constexpr int kStep = 2;           // tiles along K of one stage of the ring
 constexpr int kRing = 2;           // stages

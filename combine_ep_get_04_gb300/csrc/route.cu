@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kMaxRouteWarps * 32, NPL <= 8 ? 2 : 1) route_k
 // CTAs: those of a single sequence are a cluster if they may be one, and the
 // first is handed the others' shares; else the shares go to the workspace and
 // the CTA that finishes last adds them up.  (Forward pass of 4,096 tokens, 256
-// experts, one sequence: 9.8 us with the cluster, 11.2 without; a cluster for
+// experts, one sequence: 10.0 us with the cluster, 11.4 without; a cluster for
 // each of 3 to 16 sequences costs 0.3 to 0.5 us more than it saves.)  Bound by
 // latency: about 3 us from the first kernel's end, of which the runs' loads, all
 // of a warp in flight at once, are one round trip.
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) route_sums_kernel(const __grid
 // Gradient, one warp per token: the probabilities are recomputed from the
 // logits and lse; what the chosen experts add is scattered through a row of
 // shared memory, which stays zero between tokens.  32,768 tokens of 256 fp32
-// logits 14.9 us, 4.7 TB/s; 4,096 tokens 3.1 us, latency.
+// logits 14.9 us, 4.7 TB/s; 4,096 tokens 3.3 us, latency.
 template <int NPL, bool F32>
 __global__ void __launch_bounds__(kBackwardWarps * 32) route_backward_kernel(const __grid_constant__ RouteParams p) {
     constexpr int V = wide_values(NPL, F32), kRow = NPL * 32;
@@ -812,8 +812,8 @@ cudaError_t launch_route(const RouteParams& in, int num_sms, cudaStream_t stream
 cudaError_t launch_route_backward(const RouteParams& in, int num_sms, cudaStream_t stream) {
     RouteParams p = in;
     // A wave of CTAs, as the registers hold them, up to 4 tokens a warp: a token's loads come behind the work on the one
-    // before (us with 1, 2, 3 and 4: 4,096 tokens of 256 fp32 logits 3.1, 3.9, 4.9, 5.7; 32,768 19.4, 15.7, 15.5, 14.9;
-    // 16,384 of 128 bf16 8.9, 7.3, 6.9, 8.2; 8,192 of 512 fp32 11.8, 9.6, 10.5, 8.5).
+    // before (us with 1, 2, 3 and 4: 4,096 tokens of 256 fp32 logits 3.3, 4.4, 5.4, 6.1; 32,768 19.8, 16.1, 15.6, 14.9;
+    // 16,384 of 128 bf16 6.6, 5.5, 5.2, 6.3; 8,192 of 512 fp32 11.8, 9.5, 10.5, 8.2).
     const int wave = kBackwardWarps * num_sms * (p.E <= 128 ? 6 : p.E <= 256 ? 4 : p.E <= 512 ? 2 : 1);
     p.chunk = kBackwardWarps * std::min((p.T - 1) / wave + 1, kBackwardTokens);
     const dim3 grid((unsigned)num_runs(p.T, p.chunk, p.S));
