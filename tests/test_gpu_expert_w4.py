@@ -304,7 +304,7 @@ def test_memory_of_a_call_on_another_stream():
     places = [(t.data_ptr(), t.numel() * t.element_size()) for t in mine]
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
-        torch.cuda._sleep(100_000_000)                  # some 50 ms
+        torch.cuda._sleep(600_000_000)                  # some 300 ms
     w = ep.W4Weights(*mine, stream=s)
     packed = torch.cuda.Event()
     packed.record(s)
