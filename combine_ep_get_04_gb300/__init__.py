@@ -12,7 +12,10 @@ module only checks tensors and passes their addresses.
 
 Around them, the ends of a mixture-of-experts block: Router (the choice of
 experts with its losses and gradients), W4Weights / expert_w4 and BlockNorm
-(the norms, gate and residual sum between two blocks, with gradients).
+(the norms, gate and residual sum between two blocks, with gradients).  For
+layer-normed networks: LayerNorm (the residual sum after dropout and the layer
+norm before the next block, with gradients) and dropout.  For 8-bit integers:
+quant_i8 (rows with a scale each) and I8Weights / expert_i8.
 
 The operations follow the DeepEP pages: per-expert counts and expert ->
 partition mapping ("Redundant atomics in internode_ll", quoted dispatch
@@ -31,12 +34,14 @@ from ._lib import (CAPACITY, ERRF_BAD_EXPERT, ERRF_BAD_SEQ, ERRF_BAD_SLOT, ERRF_
                    PACKED, PAYLOAD_BF16, PAYLOAD_FP8_E4M3, PAYLOAD_FP8_E4M3_UE8M0, EPError, Shape, check, library_path, load)
 from ._tensors import _ptr, _stream
 from .block import BlockNorm, BlockNormGrads, Router, Routing, W4Weights, expert_w4
+from .layer import I8Weights, LayerNorm, LayerNormGrads, dropout, expert_i8, quant_i8
 
 __all__ = ["Plan", "Layout", "Shape", "EPError", "get_layout", "dispatch", "combine", "load", "library_path",
            "PACKED", "CAPACITY", "PAYLOAD_BF16", "PAYLOAD_FP8_E4M3", "PAYLOAD_FP8_E4M3_UE8M0", "ERRF_BAD_EXPERT", "ERRF_CAPACITY",
            "ERRF_TIMEOUT", "ERRF_BAD_SLOT", "MAX_EXPERTS", "MAX_TOPK", "EXPORTED", "make_shape", "recv_rows",
            "layout_workspace_bytes", "fused_layout_dispatch", "FUSED_MAX_N", "FUSED_MAX_T", "BlockNorm", "BlockNormGrads",
-           "Router", "Routing", "W4Weights", "expert_w4", "ERRF_BAD_SEQ"]
+           "Router", "Routing", "W4Weights", "expert_w4", "ERRF_BAD_SEQ", "LayerNorm", "LayerNormGrads", "dropout", "I8Weights",
+           "quant_i8", "expert_i8"]
 
 
 # Batches the library dispatches with the layout folded into one launch
@@ -266,6 +271,30 @@ class Plan:
         if x.shape[0] != self.R:
             raise ValueError(f"x must have {self.R} rows, got {x.shape[0]}")
         return expert_w4(x, weights, L.counts, L.offsets, capacity=s.capacity if s.mode == CAPACITY else None, x_scales=x_scales,
+                         max_rows=s.T * s.k, out=out, err_flags=L.err_flags, stream=stream)
+
+    def quant_i8(self, x: torch.Tensor | None = None, out: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                 stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+        """quant_i8() of the rows that this plan's last layout filled: x bf16
+        [R, K] is the receive buffer (the default) or what a product made of it."""
+        s, L = self.shape, self.layout_out
+        x = self.recv if x is None else x
+        if x.shape[0] != self.R:
+            raise ValueError(f"x must have {self.R} rows, got {x.shape[0]}")
+        return quant_i8(x, L.counts, L.offsets, capacity=s.capacity if s.mode == CAPACITY else None, out=out, scales=scales,
+                        err_flags=L.err_flags, stream=stream)
+
+    def expert_i8(self, weights: I8Weights, x: torch.Tensor, x_scales: torch.Tensor, out: torch.Tensor | None = None,
+                  stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+        """Every expert's product with 8-bit weights over its rows of this plan's
+        last layout: x i8 [R, K] and x_scales f32 [R] from quant_i8().  Returns
+        bf16 [R, weights.N]."""
+        s, L = self.shape, self.layout_out
+        if weights.E != s.E:
+            raise ValueError(f"the plan has {s.E} experts, the weights {weights.E}")
+        if x.shape[0] != self.R:
+            raise ValueError(f"x must have {self.R} rows, got {x.shape[0]}")
+        return expert_i8(x, x_scales, weights, L.counts, L.offsets, capacity=s.capacity if s.mode == CAPACITY else None,
                          max_rows=s.T * s.k, out=out, err_flags=L.err_flags, stream=stream)
 
 

@@ -39,7 +39,8 @@ EP_ERR_CUDA = 3
 EXPORTED = ("ep_recv_rows", "ep_layout_workspace_bytes", "ep_get_layout", "ep_get_layout_static",
             "ep_dispatch", "ep_layout_dispatch", "ep_combine", "ep_combine_fp8", "ep_combine_src_workspace_bytes",
             "ep_combine_src", "ep_route_workspace_bytes", "ep_route", "ep_route_backward", "ep_w4_bytes", "ep_w4_pack",
-            "ep_expert_w4", "ep_block_norm", "ep_block_norm_workspace_bytes", "ep_block_norm_backward", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
+            "ep_expert_w4", "ep_block_norm", "ep_block_norm_workspace_bytes", "ep_block_norm_backward", "ep_dropout", "ep_layer_norm",
+            "ep_layer_norm_workspace_bytes", "ep_layer_norm_backward", "ep_quant_i8", "ep_i8_bytes", "ep_i8_pack", "ep_expert_i8", "ep_status_string", "ep_status_str", "ep_last_error", "ep_abi_version")
 
 
 class Shape(ctypes.Structure):
@@ -69,6 +70,17 @@ class Norm(ctypes.Structure):
     """ep_norm_t."""
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("stream_type", ctypes.c_int32),
                 ("gate_kind", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    """ep_layer_norm_t."""
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("stream_type", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("p", ctypes.c_double), ("site", ctypes.c_uint64)]
+
+
+class I8(ctypes.Structure):
+    """ep_i8_t."""
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("paired", ctypes.c_int32)]
 
 
 class EPError(RuntimeError):
@@ -140,6 +152,24 @@ def load() -> ctypes.CDLL:
     lib.ep_block_norm_backward.restype = ctypes.c_int
     lib.ep_block_norm_backward.argtypes = [npt, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                            size, vp, vp]
+    f64, u64 = ctypes.c_double, ctypes.c_uint64
+    lnp, ip = ctypes.POINTER(LayerNormDesc), ctypes.POINTER(I8)
+    lib.ep_dropout.restype = ctypes.c_int
+    lib.ep_dropout.argtypes = [i64, i64, i32, vp, i64, vp, i64, f64, vp, u64, vp, i64, vp]
+    lib.ep_layer_norm.restype = ctypes.c_int
+    lib.ep_layer_norm.argtypes = [lnp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.ep_layer_norm_workspace_bytes.restype = size
+    lib.ep_layer_norm_workspace_bytes.argtypes = [lnp]
+    lib.ep_layer_norm_backward.restype = ctypes.c_int
+    lib.ep_layer_norm_backward.argtypes = [lnp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp, vp]
+    lib.ep_quant_i8.restype = ctypes.c_int
+    lib.ep_quant_i8.argtypes = [i32, i32, i32, i32, i64, vp, vp, vp, i64, vp, vp, vp, vp]
+    lib.ep_i8_bytes.restype = size
+    lib.ep_i8_bytes.argtypes = [ip]
+    lib.ep_i8_pack.restype = ctypes.c_int
+    lib.ep_i8_pack.argtypes = [ip, vp, vp, vp, vp]
+    lib.ep_expert_i8.restype = ctypes.c_int
+    lib.ep_expert_i8.argtypes = [ip, vp, i32, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp]
     lib.ep_status_string.restype = ctypes.c_char_p
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_str.restype = ctypes.c_char_p

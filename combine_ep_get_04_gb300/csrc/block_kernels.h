@@ -125,4 +125,93 @@ size_t norm_workspace_bytes(int T, int H);
 cudaError_t launch_block_norm(const NormParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- dropout
+
+// What stays and what it is multiplied by: an element is dropped when its 16
+// random bits are below `limit`.
+struct Dropout {
+    const int64_t* rng;     // seed and step, on the device; nullptr: nothing is dropped
+    uint64_t site;          // added to the step
+    uint32_t limit;         // 0..65536
+    float scale;            // 65536 / (65536 - limit), 0 where everything is dropped
+};
+
+struct DropoutParams {
+    const void* x;             // [T, H], rows ld_x apart
+    const void* residual;      // [T, H], rows ld_res apart, or nullptr
+    void* y;                   // [T, H], rows ld_y apart
+    Dropout drop;
+    int64_t T, H, ld_x, ld_res, ld_y;
+    int f32;
+};
+
+cudaError_t launch_dropout(const DropoutParams& p, cudaStream_t stream);
+
+// ------------------------------------------------------------- layer norm
+
+struct LayerNormParams {
+    const void* h;             // stream type [T, H], rows ld_h apart (backward: h_out)
+    const void* y;             // bf16 [T, H], rows ld_y apart, or nullptr (forward)
+    const float* w;            // [H] or nullptr
+    const float* b;            // [H] or nullptr
+    void* h_out;               // stream type [T, H], nullptr without y (forward)
+    void* n;                   // bf16 [T, H] (forward)
+    float* stats;              // [2, T]: mean, 1 / deviation; written forward (may be nullptr), read backward
+    const void* d_n;           // backward from here on
+    const void* d_h_out;
+    void* d_h;
+    void* d_y;                 // or nullptr
+    float* d_w;                // or nullptr
+    float* d_b;                // or nullptr
+    float* partial;            // workspace: column sums of each CTA
+    uint32_t* err_flags;       // may be nullptr
+    Dropout drop;
+    int64_t ld_h, ld_y;
+    int T, H;
+    int f32;                   // stream type
+    float eps;
+};
+
+size_t layer_norm_workspace_bytes(int T, int H);
+cudaError_t launch_layer_norm(const LayerNormParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_layer_norm_backward(const LayerNormParams& p, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------- 8-bit integers
+
+struct QuantParams {
+    const void* x;             // bf16 [R, K], rows ld apart
+    const int32_t* counts;
+    const int32_t* offsets;
+    int8_t* q;                 // [R, K]
+    float* scales;             // [R]
+    uint32_t* err_flags;
+    int64_t R, ld;
+    int E, K, mode, capacity;
+};
+
+cudaError_t launch_quant_i8(const QuantParams& p, int num_sms, cudaStream_t stream);
+
+struct I8Shape {
+    int E, N, K, paired;
+};
+
+struct I8Params {
+    I8Shape w;
+    const void* packed;
+    const int8_t* x;           // [R, K]
+    const float* x_scales;     // [R]
+    const int32_t* counts;
+    const int32_t* offsets;
+    void* y;                   // bf16 [R, N]
+    uint32_t* err_flags;
+    int64_t R, max_rows;
+    int mode, capacity;
+};
+
+size_t i8_bytes(const I8Shape& w);
+bool i8_packs(const I8Shape& w);                        // whether one launch packs them
+bool i8_fits(const I8Shape& w, int64_t max_rows);       // whether one launch covers the rows
+cudaError_t launch_i8_pack(const I8Shape& w, const int8_t* codes, const float* scales, void* packed, cudaStream_t stream);
+cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream);
+
 }  // namespace ep

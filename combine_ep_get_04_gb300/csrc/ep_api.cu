@@ -2,6 +2,7 @@
 // launch-shape choice and error reporting.  Every step of the work runs in
 // the kernels of layout.cu, dispatch.cu and combine.cu on the caller's stream.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
@@ -174,6 +175,65 @@ ep_status_t check_norm_inputs(const ep_norm_t* s, const void* h, int64_t ld_h, c
     if (!aligned16(h) || !aligned16(y) || !aligned16(w_post) || !aligned16(w_pre) ||
         (s->gate_kind == EP_GATE_CHANNEL && !aligned16(gate)))
         return fail(EP_ERR_INVALID_ARG, "h, y, w_post, w_pre and a channel gate must be 16-byte aligned");
+    return ok();
+}
+
+// ------------------------------------------------- dropout and layer norm
+
+// Sets *d; EP_OK, or the reason why p is no probability.
+ep_status_t set_dropout(ep::Dropout* d, double p, const int64_t* rng, uint64_t site) {
+    if (!(p >= 0.0 && p <= 1.0)) return fail(EP_ERR_INVALID_ARG, "p = %g must be in [0, 1]", p);
+    if (reinterpret_cast<uintptr_t>(rng) & 7u) return fail(EP_ERR_INVALID_ARG, "rng must be 8-byte aligned");
+    *d = ep::Dropout{};
+    d->limit = (uint32_t)nearbyint(p * 65536.0);
+    d->rng = d->limit != 0 ? rng : nullptr;
+    d->site = site;
+    d->scale = d->limit < 65536u ? (float)(65536.0 / (65536.0 - d->limit)) : 0.f;
+    return ok();
+}
+
+ep_status_t check_layer_norm(const ep_layer_norm_t* s) {
+    if (s == nullptr) return fail(EP_ERR_INVALID_ARG, "norm is NULL");
+    if (s->T < 0) return fail(EP_ERR_INVALID_ARG, "T = %d < 0", s->T);
+    if (s->H <= 0 || s->H % 8 != 0) return fail(EP_ERR_INVALID_ARG, "H = %d must be a positive multiple of 8", s->H);
+    if (s->H > EP_MAX_NORM_WIDTH) return fail(EP_ERR_UNSUPPORTED, "H = %d > %d", s->H, EP_MAX_NORM_WIDTH);
+    if (s->stream_type != EP_TYPE_BF16 && s->stream_type != EP_TYPE_F32)
+        return fail(EP_ERR_INVALID_ARG, "stream_type = %d is not a type", s->stream_type);
+    if (!(s->eps >= 1e-30f) || !(s->eps <= 1e30f)) return fail(EP_ERR_INVALID_ARG, "eps = %g must be in [1e-30, 1e30]", (double)s->eps);
+    ep::Dropout d;
+    return set_dropout(&d, s->p, nullptr, s->site);
+}
+
+ep_status_t check_norm_rows(const char* name, const void* rows, int64_t ld, int H) {
+    if (ld < H || ld % 8 != 0) return fail(EP_ERR_INVALID_ARG, "ld_%s = %lld must be a multiple of 8 and at least H = %d", name, (long long)ld, H);
+    if (!aligned16(rows)) return fail(EP_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+    return ok();
+}
+
+// ---------------------------------------------------------- 8-bit integers
+
+ep_status_t check_i8(const ep_i8_t* w) {
+    if (w == nullptr) return fail(EP_ERR_INVALID_ARG, "w is NULL");
+    if (w->E < 1) return fail(EP_ERR_INVALID_ARG, "E = %d < 1", w->E);
+    if (w->E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, "E = %d > %d", w->E, EP_MAX_EXPERTS);
+    if (w->N <= 0 || w->N % 8 != 0) return fail(EP_ERR_INVALID_ARG, "N = %d must be a positive multiple of 8", w->N);
+    if (w->K <= 0 || w->K % 16 != 0) return fail(EP_ERR_INVALID_ARG, "K = %d must be a positive multiple of 16", w->K);
+    if (w->paired != 0 && w->paired != 1) return fail(EP_ERR_INVALID_ARG, "paired = %d must be 0 or 1", w->paired);
+    if (w->N > 1 << 24 || w->K > 1 << 24 || !ep::i8_packs({w->E, w->N, w->K, w->paired}))
+        return fail(EP_ERR_UNSUPPORTED, "weights [%d, %d, %d] are too large", w->E, w->N, w->K);
+    return ok();
+}
+
+// Which rows hold a copy.
+ep_status_t check_rows(int E, int32_t mode, int32_t capacity, int64_t R, const int32_t* counts, const int32_t* offsets, bool all_rows) {
+    if (mode != EP_LAYOUT_PACKED && mode != EP_LAYOUT_CAPACITY)
+        return fail(EP_ERR_INVALID_ARG, "mode = %d is not a layout mode", mode);
+    if (R < 0) return fail(EP_ERR_INVALID_ARG, "R must not be negative");
+    if (R > INT32_MAX) return fail(EP_ERR_UNSUPPORTED, "R = %lld exceeds 2^31-1", (long long)R);
+    if (mode == EP_LAYOUT_CAPACITY && (capacity < 1 || R < (int64_t)E * capacity))
+        return fail(EP_ERR_INVALID_ARG, "capacity = %d needs at least 1 and R >= E*capacity", capacity);
+    if (R > 0 && (mode == EP_LAYOUT_CAPACITY ? counts == nullptr : offsets == nullptr && !all_rows))
+        return fail(EP_ERR_INVALID_ARG, "counts (capacity mode) / offsets (packed) is NULL");
     return ok();
 }
 
@@ -722,6 +782,214 @@ ep_status_t ep_block_norm_backward(const ep_norm_t* norm, const void* h, int64_t
     p.eps = norm->eps;
     return launched(ep::launch_block_norm_backward(p, num_sms, reinterpret_cast<cudaStream_t>(stream)),
                     "block norm backward launch");
+}
+
+ep_status_t ep_dropout(int64_t T, int64_t H, int32_t type, const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                       double p, const int64_t* rng, uint64_t site, void* y, int64_t ld_y, ep_stream_t stream) {
+    ep::DropoutParams d{};
+    ep_status_t st = set_dropout(&d.drop, p, rng, site);
+    if (st != EP_OK) return st;
+    if (T < 0 || H < 1) return fail(EP_ERR_INVALID_ARG, "T = %lld must be at least 0 and H = %lld at least 1", (long long)T, (long long)H);
+    if (T > INT32_MAX || H > INT32_MAX) return fail(EP_ERR_UNSUPPORTED, "T = %lld or H = %lld exceeds 2^31-1", (long long)T, (long long)H);
+    if (type != EP_TYPE_BF16 && type != EP_TYPE_F32) return fail(EP_ERR_INVALID_ARG, "type = %d is not a type", type);
+    if (T == 0) return ok();
+    if (x == nullptr || y == nullptr) return fail(EP_ERR_INVALID_ARG, "x / y is NULL");
+    if (ld_x < H || ld_y < H || (residual != nullptr && ld_res < H)) return fail(EP_ERR_INVALID_ARG, "rows are less than H = %lld apart", (long long)H);
+    if ((x == y && ld_x != ld_y) || (residual == y && ld_res != ld_y))
+        return fail(EP_ERR_INVALID_ARG, "y in place of an input needs rows as far apart");
+    const uintptr_t mask = type == EP_TYPE_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(y)) & mask)
+        return fail(EP_ERR_INVALID_ARG, "x, residual or y is not aligned to its elements");
+    if (T * H > (int64_t)1 << 40)          // one launch's grid, at 32 vectors of 8 a block
+        return fail(EP_ERR_UNSUPPORTED, "%lld rows of %lld elements are too many", (long long)T, (long long)H);
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    d.x = x;
+    d.residual = residual;
+    d.y = y;
+    d.T = T;
+    d.H = H;
+    d.ld_x = ld_x;
+    d.ld_res = ld_res;
+    d.ld_y = ld_y;
+    d.f32 = type == EP_TYPE_F32 ? 1 : 0;
+    return launched(ep::launch_dropout(d, reinterpret_cast<cudaStream_t>(stream)), "dropout launch");
+}
+
+ep_status_t ep_layer_norm(const ep_layer_norm_t* norm, const void* h, int64_t ld_h, const void* y, int64_t ld_y, const float* w,
+                          const float* b, const int64_t* rng, void* h_out, void* n, float* stats, uint32_t* err_flags,
+                          ep_stream_t stream) {
+    ep_status_t st = check_layer_norm(norm);
+    if (st != EP_OK) return st;
+    ep::LayerNormParams p{};
+    st = set_dropout(&p.drop, norm->p, rng, norm->site);
+    if (st != EP_OK) return st;
+    if (norm->T == 0) return ok();
+    if (h == nullptr || n == nullptr) return fail(EP_ERR_INVALID_ARG, "h / n is NULL");
+    if ((h_out != nullptr) != (y != nullptr)) return fail(EP_ERR_INVALID_ARG, "h_out and y go together");
+    st = check_norm_rows("h", h, ld_h, norm->H);
+    if (st != EP_OK) return st;
+    if (y != nullptr) {
+        st = check_norm_rows("y", y, ld_y, norm->H);
+        if (st != EP_OK) return st;
+    }
+    if (!aligned16(w) || !aligned16(b) || !aligned16(h_out) || !aligned16(n))
+        return fail(EP_ERR_INVALID_ARG, "w, b, h_out and n must be 16-byte aligned");
+    if (h == h_out && ld_h != norm->H) return fail(EP_ERR_INVALID_ARG, "h_out in place of h needs ld_h = H");
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    if (y == nullptr) p.drop = ep::Dropout{};
+    p.h = h;
+    p.y = y;
+    p.w = w;
+    p.b = b;
+    p.h_out = h_out;
+    p.n = n;
+    p.stats = stats;
+    p.err_flags = err_flags;
+    p.ld_h = ld_h;
+    p.ld_y = ld_y;
+    p.T = norm->T;
+    p.H = norm->H;
+    p.f32 = norm->stream_type == EP_TYPE_F32 ? 1 : 0;
+    p.eps = norm->eps;
+    return launched(ep::launch_layer_norm(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "layer norm launch");
+}
+
+size_t ep_layer_norm_workspace_bytes(const ep_layer_norm_t* norm) {
+    if (check_layer_norm(norm) != EP_OK) return (size_t)-1;
+    return ep::layer_norm_workspace_bytes(norm->T, norm->H);
+}
+
+ep_status_t ep_layer_norm_backward(const ep_layer_norm_t* norm, const void* h_out, int64_t ld_h, const float* w, const int64_t* rng,
+                                   const float* stats, const void* d_h_out, const void* d_n, void* d_h, void* d_y, float* d_w,
+                                   float* d_b, void* workspace, size_t workspace_bytes, uint32_t* err_flags, ep_stream_t stream) {
+    ep_status_t st = check_layer_norm(norm);
+    if (st != EP_OK) return st;
+    ep::LayerNormParams p{};
+    st = set_dropout(&p.drop, norm->p, rng, norm->site);
+    if (st != EP_OK) return st;
+    if (norm->T > 0) {
+        if (h_out == nullptr || stats == nullptr || d_n == nullptr || d_h == nullptr)
+            return fail(EP_ERR_INVALID_ARG, "h_out / stats / d_n / d_h is NULL");
+        st = check_norm_rows("h", h_out, ld_h, norm->H);
+        if (st != EP_OK) return st;
+        if (!aligned16(w) || !aligned16(d_h_out) || !aligned16(d_n) || !aligned16(d_h) || !aligned16(d_y))
+            return fail(EP_ERR_INVALID_ARG, "w, d_h_out, d_n, d_h and d_y must be 16-byte aligned");
+        if (d_h == h_out && ld_h != norm->H) return fail(EP_ERR_INVALID_ARG, "d_h in place of h_out needs ld_h = H");
+        const size_t need = ep::layer_norm_workspace_bytes(norm->T, norm->H);
+        if (workspace == nullptr || workspace_bytes < need)
+            return fail(EP_ERR_INVALID_ARG, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+        if (!aligned16(workspace)) return fail(EP_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    }
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    p.h = h_out;
+    p.w = w;
+    p.stats = const_cast<float*>(stats);
+    p.d_n = d_n;
+    p.d_h_out = d_h_out;
+    p.d_h = d_h;
+    p.d_y = d_y;
+    p.d_w = d_w;
+    p.d_b = d_b;
+    p.partial = static_cast<float*>(workspace);
+    p.err_flags = err_flags;
+    p.ld_h = ld_h;
+    p.T = norm->T;
+    p.H = norm->H;
+    p.f32 = norm->stream_type == EP_TYPE_F32 ? 1 : 0;
+    p.eps = norm->eps;
+    return launched(ep::launch_layer_norm_backward(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "layer norm backward launch");
+}
+
+ep_status_t ep_quant_i8(int32_t E, int32_t K, int32_t mode, int32_t capacity, int64_t R, const int32_t* counts,
+                        const int32_t* offsets, const void* x, int64_t ld_x, int8_t* q, float* scales, uint32_t* err_flags,
+                        ep_stream_t stream) {
+    if (E < 1) return fail(EP_ERR_INVALID_ARG, "E = %d < 1", E);
+    if (E > EP_MAX_EXPERTS) return fail(EP_ERR_UNSUPPORTED, "E = %d > %d", E, EP_MAX_EXPERTS);
+    if (K <= 0 || K % 16 != 0) return fail(EP_ERR_INVALID_ARG, "K = %d must be a positive multiple of 16", K);
+    if (K > EP_MAX_QUANT_WIDTH) return fail(EP_ERR_UNSUPPORTED, "K = %d > %d", K, EP_MAX_QUANT_WIDTH);
+    ep_status_t st = check_rows(E, mode, capacity, R, counts, offsets, true);
+    if (st != EP_OK) return st;
+    if (R == 0) return ok();
+    if (x == nullptr || q == nullptr || scales == nullptr) return fail(EP_ERR_INVALID_ARG, "x / q / scales is NULL");
+    if (ld_x < K || ld_x % 8 != 0) return fail(EP_ERR_INVALID_ARG, "ld_x = %lld must be a multiple of 8 and at least K = %d", (long long)ld_x, K);
+    if (!aligned16(x) || !aligned16(q) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+        return fail(EP_ERR_INVALID_ARG, "x and q must be 16-byte, scales 4-byte aligned");
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    ep::QuantParams p{};
+    p.x = x;
+    p.counts = counts;
+    p.offsets = offsets;
+    p.q = q;
+    p.scales = scales;
+    p.err_flags = err_flags;
+    p.R = R;
+    p.ld = ld_x;
+    p.E = E;
+    p.K = K;
+    p.mode = mode;
+    p.capacity = capacity;
+    return launched(ep::launch_quant_i8(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "quant i8 launch");
+}
+
+size_t ep_i8_bytes(const ep_i8_t* w) {
+    if (check_i8(w) != EP_OK) return (size_t)-1;
+    return ep::i8_bytes({w->E, w->N, w->K, w->paired});
+}
+
+ep_status_t ep_i8_pack(const ep_i8_t* w, const int8_t* codes, const float* scales, void* packed, ep_stream_t stream) {
+    ep_status_t st = check_i8(w);
+    if (st != EP_OK) return st;
+    if (codes == nullptr || scales == nullptr || packed == nullptr)
+        return fail(EP_ERR_INVALID_ARG, "codes / scales / packed is NULL");
+    if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u) || !aligned16(packed))
+        return fail(EP_ERR_INVALID_ARG, "codes and packed must be 16-byte, scales 4-byte aligned");
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    return launched(ep::launch_i8_pack({w->E, w->N, w->K, w->paired}, codes, scales, packed, reinterpret_cast<cudaStream_t>(stream)),
+                    "i8 pack launch");
+}
+
+ep_status_t ep_expert_i8(const ep_i8_t* w, const void* packed, int32_t mode, int32_t capacity, int64_t R, int64_t max_rows,
+                         const int32_t* counts, const int32_t* offsets, const int8_t* x, const float* x_scales, void* y,
+                         uint32_t* err_flags, ep_stream_t stream) {
+    ep_status_t st = check_i8(w);
+    if (st != EP_OK) return st;
+    if (max_rows < 0) return fail(EP_ERR_INVALID_ARG, "max_rows must not be negative");
+    if (max_rows > R) max_rows = R;
+    st = check_rows(w->E, mode, capacity, R, counts, offsets, w->E == 1 || max_rows == 0);
+    if (st != EP_OK) return st;
+    if (max_rows == 0) return ok();
+    if (packed == nullptr || x == nullptr || x_scales == nullptr || y == nullptr)
+        return fail(EP_ERR_INVALID_ARG, "packed / x / x_scales / y is NULL");
+    if (!aligned16(packed) || !aligned16(x) || !aligned16(y) || (reinterpret_cast<uintptr_t>(x_scales) & 3u))
+        return fail(EP_ERR_INVALID_ARG, "packed, x and y must be 16-byte, x_scales 4-byte aligned");
+    ep::I8Params p{};
+    p.w = {w->E, w->N, w->K, w->paired};
+    if (!ep::i8_fits(p.w, max_rows)) return fail(EP_ERR_UNSUPPORTED, "max_rows = %lld is too large", (long long)max_rows);
+    int num_sms = 0;
+    st = device_info(&num_sms);
+    if (st != EP_OK) return st;
+    p.packed = packed;
+    p.x = x;
+    p.x_scales = x_scales;
+    p.counts = counts;
+    p.offsets = offsets;
+    p.y = y;
+    p.err_flags = err_flags;
+    p.R = R;
+    p.max_rows = max_rows;
+    p.mode = mode;
+    p.capacity = capacity;
+    return launched(ep::launch_expert_i8(p, num_sms, reinterpret_cast<cudaStream_t>(stream)), "expert i8 launch");
 }
 
 }  // extern "C"

@@ -582,6 +582,172 @@ EP_API ep_status_t ep_expert_w4(const ep_w4_t *w, const void *packed, int32_t mo
                          const void *x_scales, int32_t payload, void *y,
                          uint32_t *err_flags, ep_stream_t stream);
 
+#define EP_MAX_QUANT_WIDTH 16384
+
+/*
+ * Random numbers of dropout: the generator Philox4x32 with ten rounds (Salmon
+ * and others, SC11).  `rng` is two i64 on the device, a seed (the generator's
+ * key, low half first) and a step; `site` tells the dropouts of one step apart.
+ * Eight neighbours of a row share a counter: words 0 and 1 are the number of
+ * the eight, row * ceil(H / 8) + column / 8 (low half first), words 2 and 3 are
+ * step + site modulo 2^64.  Element j of the eight has the 16 bits of the low
+ * (j even) or high half of result word j / 2 and is dropped when they are below
+ * limit = round(65536 p), halves to even; what stays is multiplied by
+ * 65536 / (65536 - limit), rounded to fp32, so that the mean stays what it was.
+ * A dropped value counts as 0, whatever it is.  With p = 1 all are dropped.
+ * rng = NULL: nothing is dropped.
+ */
+
+/*
+ * ep_dropout -- y = residual + dropout(x), computed in fp32, each product and
+ * sum rounded, the result rounded once to the type.  The gradient with respect
+ * to x is the same call on the gradient of y, without the residual.
+ *
+ * In:  x         type (ep_type_t) [T, H], rows ld_x elements apart; T >= 0,
+ *                H >= 1.
+ *      residual  type [T, H], rows ld_res apart, or NULL.
+ *      p         probability of being dropped, 0..1.
+ * Out: y         type [T, H], rows ld_y apart; may be x or residual where the
+ *                rows lie the same.
+ * Rows are at least H apart.  Pointers are aligned to their elements; rows at
+ * 16-byte boundaries with H a multiple of 8 go by wide accesses.
+ */
+EP_API ep_status_t ep_dropout(int64_t T, int64_t H, int32_t type, const void *x, int64_t ld_x,
+                       const void *residual, int64_t ld_res, double p,
+                       const int64_t *rng, uint64_t site, void *y, int64_t ld_y,
+                       ep_stream_t stream);
+
+typedef struct {
+    int32_t T;                /* rows, >= 0                                    */
+    int32_t H;                /* channels, > 0, multiple of 8, at most
+                                 EP_MAX_NORM_WIDTH                             */
+    int32_t stream_type;      /* ep_type_t of h, h_out, d_h_out and d_h        */
+    float eps;                /* 1e-30..1e30, added to the variance            */
+    double p;                 /* dropout of y, 0..1                            */
+    uint64_t site;            /* which dropout of the network it is            */
+} ep_layer_norm_t;
+
+/*
+ * ep_layer_norm -- the end of one block and the start of the next in a network
+ * of layer norms, one pass over the rows:
+ *   h_out = h + dropout(y)                         (h_out = h without y)
+ *   n     = (h_out - mean) * r * w + b,   r = 1 / sqrt(variance + eps)
+ * mean and variance over a row's H channels.  In fp32; h_out is rounded once
+ * to the stream's type and the norm is taken of what is stored; n is rounded
+ * once.
+ *
+ * In:  h      stream type [T, H], rows ld_h elements apart.
+ *      y      bf16 [T, H], rows ld_y apart (the block's output, e.g. from
+ *             ep_combine), or NULL (the first norm of a network).
+ *      w, b   f32 [H], each NULL for 1 or 0.
+ *      rng    as above; NULL: nothing is dropped (as for serving).
+ * Out: h_out  stream type [T, H], NULL exactly when y is; may be h when
+ *             ld_h = H.
+ *      n      bf16 [T, H].
+ *      stats  f32 [2, T]: mean, then r of every row, or NULL.
+ * 16-byte alignment of h, y, w, b, h_out and n; ld_h and ld_y multiples of 8
+ * and at least H.
+ * err_flags: EP_ERRF_TIMEOUT.
+ */
+EP_API ep_status_t ep_layer_norm(const ep_layer_norm_t *norm, const void *h, int64_t ld_h,
+                          const void *y, int64_t ld_y, const float *w, const float *b,
+                          const int64_t *rng, void *h_out, void *n, float *stats,
+                          uint32_t *err_flags, ep_stream_t stream);
+
+/* Bytes of device workspace ep_layer_norm_backward needs (column sums in
+ * progress); (size_t)-1 if the description is invalid. */
+EP_API size_t ep_layer_norm_workspace_bytes(const ep_layer_norm_t *norm);
+
+/*
+ * ep_layer_norm_backward -- gradients of ep_layer_norm.  With
+ * xn = (h_out - mean) * r and t = d_n * w:
+ *   d   = d_h_out + r * (t - mean(t) - xn * mean(t * xn))
+ *   d_h = d          d_y = d where y stayed, times its factor, else 0
+ *   d_w = sum over rows of d_n * xn        d_b = sum over rows of d_n
+ * in fp32.  Sums over rows are taken in an order that depends on the sizes
+ * alone: a repeated call gives the same bits.
+ *
+ * In:  h_out (h where there was no y), rows ld_h apart; w, rng and the stats
+ *      of ep_layer_norm; d_h_out stream type [T, H] or NULL (zero); d_n bf16
+ *      [T, H].
+ * Out: d_h  stream type [T, H]; may be d_h_out.
+ *      d_y  bf16 [T, H], or NULL when not wanted (without dropout and with a
+ *           bf16 stream it equals d_h).
+ *      d_w, d_b  f32 [H], each NULL when not wanted.
+ * workspace: ep_layer_norm_workspace_bytes(norm) bytes, 16-byte aligned,
+ * contents on entry ignored.  T = 0 sets the sums to zero.
+ * err_flags: EP_ERRF_TIMEOUT.
+ */
+EP_API ep_status_t ep_layer_norm_backward(const ep_layer_norm_t *norm, const void *h_out, int64_t ld_h,
+                          const float *w, const int64_t *rng, const float *stats,
+                          const void *d_h_out, const void *d_n, void *d_h, void *d_y,
+                          float *d_w, float *d_b, void *workspace, size_t workspace_bytes,
+                          uint32_t *err_flags, ep_stream_t stream);
+
+/*
+ * ep_quant_i8 -- rows of the receive buffer (or of what a product made of it)
+ * to 8-bit integers with a scale each:
+ *   scale[r] = amax(|x[r]|) / 127      q[r, k] = round(127 * x[r, k] / amax)
+ * rounded to nearest, halves to even, -127..127; the codes are exactly those of
+ * the real numbers.  A row of zeros has scale 0 and codes 0, a row that holds an
+ * infinity or a NaN scale NaN and codes 0.
+ *
+ * In:  mode, capacity, counts, offsets  as in ep_expert_i8: which rows hold a
+ *      copy.  Packed with offsets NULL: all R rows.
+ *      x       bf16 [R, K], rows ld_x elements apart, 16-byte aligned; K a
+ *              multiple of 16, at most EP_MAX_QUANT_WIDTH; ld_x a multiple of 8.
+ * Out: q       i8 [R, K], 16-byte aligned;  scales  f32 [R].  Rows that hold no
+ *              copy are not written.
+ * err_flags: EP_ERRF_BAD_SLOT (offsets beyond R, cut off).
+ */
+EP_API ep_status_t ep_quant_i8(int32_t E, int32_t K, int32_t mode, int32_t capacity, int64_t R,
+                        const int32_t *counts, const int32_t *offsets, const void *x,
+                        int64_t ld_x, int8_t *q, float *scales, uint32_t *err_flags,
+                        ep_stream_t stream);
+
+typedef struct {
+    int32_t E;                /* matrices (experts), 1..EP_MAX_EXPERTS         */
+    int32_t N;                /* output channels, > 0, multiple of 8           */
+    int32_t K;                /* input channels, > 0, multiple of 16           */
+    int32_t paired;           /* 1: each expert has 2N rows, N gate rows and
+                                 then N up rows, and y = silu(gate) * up       */
+} ep_i8_t;
+
+/* Bytes of the packed weights (codes and scales of all experts);
+ * (size_t)-1 if the description is invalid. */
+EP_API size_t ep_i8_bytes(const ep_i8_t *w);
+
+/*
+ * ep_i8_pack -- lay 8-bit weights out for ep_expert_i8, once per model load.
+ *
+ * In:  codes   i8 [E, rows, K] (rows = N, or 2N when paired), 16-byte aligned.
+ *      scales  f32 [E, rows].
+ * Out: packed  ep_i8_bytes(w) bytes, 16-byte aligned.
+ */
+EP_API ep_status_t ep_i8_pack(const ep_i8_t *w, const int8_t *codes, const float *scales,
+                       void *packed, ep_stream_t stream);
+
+/*
+ * ep_expert_i8 -- every expert's product over its rows of the receive buffer:
+ *   y[r, n] = x_scale[r] * scale[e, n] * sum_k x[r, k] * code[e, n, k]
+ * for the rows r of expert e (paired: silu of the gate product times the up
+ * product).  Products of codes are exact and summed in fp32, which is exact as
+ * long as no partial sum passes 2^24; scales are applied in fp32 and the result
+ * is rounded once to bf16.
+ *
+ * In:  mode, capacity, counts, offsets, R, max_rows  as in ep_expert_w4.
+ *      x         i8 [R, K], 16-byte aligned;  x_scales  f32 [R].
+ * Out: y         bf16 [R, N], 16-byte aligned.  Rows that hold no copy are not
+ *                written.
+ * err_flags: EP_ERRF_BAD_SLOT (rows outside [0, R), skipped),
+ * EP_ERRF_CAPACITY, EP_ERRF_TIMEOUT.
+ */
+EP_API ep_status_t ep_expert_i8(const ep_i8_t *w, const void *packed, int32_t mode,
+                         int32_t capacity, int64_t R, int64_t max_rows,
+                         const int32_t *counts, const int32_t *offsets, const int8_t *x,
+                         const float *x_scales, void *y, uint32_t *err_flags,
+                         ep_stream_t stream);
+
 /* Static description of a status code. */
 EP_API const char *ep_status_string(ep_status_t status);
 
