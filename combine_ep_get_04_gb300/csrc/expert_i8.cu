@@ -4,12 +4,16 @@
 // This part multiplies 8-bit integers at 151 TOP/s (mma.sync, measured), f16 at
 // thirteen times that, so the codes go through the tensor cores as f16, which
 // holds them exactly: a product of two has 15 bits and sums stay exact below 2^24.
-// A block of 128 weight rows is the M side of tcgen05.mma, up to 128 token rows the
-// N side, 64 input channels a step.  A producer warp keeps a ring of weight codes
-// filled by bulk copies; four warps widen them into tensor memory, a row to a
-// thread, which is the instruction's A operand; four more load token codes and
-// widen them into shared memory (B); one thread issues the products.
+// Two blocks of 128 weight rows are the M side of tcgen05.mma, up to 128 token rows
+// the N side of both, 64 input channels a step.  One CTA an SM takes item after
+// item (two blocks with one tile of token rows).  A warp finds the items; a
+// producer warp keeps a ring of weight codes filled by bulk copies; eight warps
+// widen them into tensor memory, a row to a thread, which is the instruction's A
+// operand; eight more load token codes and widen them into shared memory (B), and
+// write the sums out; one thread issues the products.
 #include <algorithm>
+
+#include "ep.h"
 
 #include "block_kernels.h"
 #include "expert_rows.cuh"
@@ -18,12 +22,19 @@ namespace ep {
 namespace {
 
 constexpr int kRows = 128;         // weight rows of a block
+constexpr int kTokens = 128;       // most token rows of a tile
 constexpr int kStep = 64;          // input channels of a step
 constexpr int kStepBytes = kRows * kStep;
+constexpr int kRing = 8;           // steps of weight codes
 constexpr int kOps = 4;            // steps whose operands are widened ahead
-constexpr int kThreads = 320;      // four warps of weights, four of tokens, the producer, the issuer
-constexpr int kAColumns = kStep / 2;              // tensor memory columns of a step's A operand
-constexpr uint32_t kColumns = 256;                // tensor memory columns of a CTA: two on an SM
+constexpr int kItems = 4;          // items found ahead
+constexpr int kAhead = 3;          // steps whose token codes are on their way
+// warps: 8 of weights, 8 of tokens, the producer, the issuer, the one that finds items
+constexpr int kProducer = 16, kIssuer = 17, kFinder = 18;
+constexpr int kThreads = 19 * 32;
+constexpr int kItemReaders = 18;
+constexpr uint32_t kColumns = 512;                // tensor memory: the two blocks' sums, then kOps x 2 A operands
+constexpr int kAColumns = kStep / 2;
 
 __host__ __device__ inline int k_steps(const I8Shape& w) { return (w.K + kStep - 1) / kStep; }
 // A paired block is 64 gate rows and the 64 up rows of the same channels.
@@ -121,6 +132,13 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&v)[16]) {
         : "memory");
 }
 
+// One thread of a whole warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Four codes plus 128 -> two pairs of f16: a byte below 0x64 is 1024 + byte, and
 // 1152 less is the code.  Exact.
 __device__ __forceinline__ void widen(uint32_t biased, uint32_t* lo, uint32_t* hi) {
@@ -131,15 +149,12 @@ __device__ __forceinline__ void widen(uint32_t biased, uint32_t* lo, uint32_t* h
 
 // ------------------------------------------------------------------ kernel
 
-// A step's B operand: runs of 8 channels of NT rows, 16 bytes a row, runs
-// (NT + 2) * 16 bytes apart (the 32 bytes more keep neighbouring runs' rows in
-// different banks).
-template <int NT>
-constexpr int kRunBytes = (NT + 2) * 16;
-template <int NT>
-constexpr int kBBytes = kStep / 8 * kRunBytes<NT>;
-template <int NT, int RING>
-constexpr int kSmemBytes = RING * kStepBytes + kOps * kBBytes<NT>;
+// A step's B operand: runs of 8 channels of kTokens rows, 16 bytes a row; 32 bytes
+// more keep the runs that eight lanes write at once in different banks.
+constexpr int kRunBytes = (kTokens + 2) * 16;
+constexpr int kBBytes = kStep / 8 * kRunBytes;
+constexpr int kRingBytes = kRing * 2 * kStepBytes;
+constexpr int kSmemBytes = kRingBytes + kOps * kBBytes;
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -151,224 +166,386 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t smem, int rank) {
     return a;
 }
 
-// One CTA: a block of 128 weight rows with one tile of up to NT token rows, over
-// one of `splits` shares of K.  The shares of a product form a cluster; each
-// owns a part of the tile's token rows, whose sums the others push to it.
-template <int NT, int RING>
-__global__ void __launch_bounds__(kThreads, 2) expert_i8_kernel(I8Params p, int splits, int grid_tiles) {
+// Two blocks of weight rows (one where `two` is not set) with a tile of token rows.
+struct Item {
+    int e;            // expert, -1: no more
+    int rows;
+    int first;        // the tile's first row
+    int b;            // the first block
+    int two;
+};
+
+// Tiles of n rows: as few as hold them, each of about as many rows, in 16s (which
+// is never more than `tile` while n rows need them all).
+__device__ __forceinline__ int tile_rows_of(int n, int tile) {
+    const int tiles = (n + tile - 1) / tile;
+    return ((n + tiles - 1) / tiles + 15) & ~15;
+}
+
+// The sums of up to 16 token rows of a weight row to a lane, scaled and stored.
+struct Writer {
+    const I8Params& p;
+    uint16_t* y;             // at the lane's channel of the tile's first row
+    const float* row_scale;  // of the tile's first row
+    float scale;
+    bool stores;
+
+    __device__ __forceinline__ Writer(const I8Params& p, const Item& it, int b, int row) : p(p) {
+        bool up;
+        const int c = channel_of(p.w, b, row, &up);
+        scale = reinterpret_cast<const float*>(static_cast<const unsigned char*>(p.packed) + scales_at(p.w))[((int64_t)it.e * row_blocks(p.w) + b) * kRows + row];
+        y = static_cast<uint16_t*>(p.y) + (int64_t)it.first * p.w.N + c;
+        row_scale = p.x_scales + it.first;
+        stores = c < p.w.N && !up;
+    }
+
+    __device__ __forceinline__ void put(int n, float sum, float xs) const {
+        float f = sum * scale * xs;
+        if (p.w.paired) f = silu(f) * __shfl_xor_sync(0xffffffffu, f, 16);
+        if (stores) y[(int64_t)n * p.w.N] = (uint16_t)pack_bf16x2(f, 0.f);
+    }
+};
+
+// items: a grid of clusters of `splits` CTAs takes them a grid apart; with more
+// than one share of K (which a launch of few products has) a cluster takes one.
+__global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int splits, int tile_rows) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t ring_full[RING], ring_empty[RING], op_full[kOps], op_empty[kOps], done;
+    __shared__ uint64_t ring_full[kRing], ring_empty[kRing], op_full[kOps], op_empty[kOps], item_full[kItems], item_empty[kItems];
+    __shared__ uint64_t done, drained;
     __shared__ uint32_t tmem_at;
-    __shared__ RowTile shared_tile;
-    __shared__ float row_scale[NT];
+    __shared__ Item items[kItems];
+    __shared__ int table_first[EP_MAX_EXPERTS], table_rows[EP_MAX_EXPERTS], table_upto[EP_MAX_EXPERTS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % splits, nb = row_blocks(p.w), nk = k_steps(p.w);
-    const int b = blockIdx.x / splits % nb, at = blockIdx.x / splits / nb;
-    const int k0 = (int)((int64_t)nk * split / splits), k1 = (int)((int64_t)nk * (split + 1) / splits);
+    const int split = blockIdx.x % splits, cluster = blockIdx.x / splits, clusters = gridDim.x / splits;
+    const int nb = row_blocks(p.w), nk = k_steps(p.w);
+    const int k0 = (int)((int64_t)nk * split / splits), steps = (int)((int64_t)nk * (split + 1) / splits) - k0;
+    unsigned char* ops = smem + kRingBytes;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < RING; ++i) {
+        for (int i = 0; i < kRing; ++i) {
             mbar_init(&ring_full[i], 1);
-            mbar_init(&ring_empty[i], 4);
+            mbar_init(&ring_empty[i], 8);
         }
         for (int i = 0; i < kOps; ++i) {
-            mbar_init(&op_full[i], 8);
+            mbar_init(&op_full[i], 16);
             mbar_init(&op_empty[i], 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], kItemReaders);
+        }
         mbar_init(&done, 1);
+        mbar_init(&drained, 8);
         fence_mbar_init();
-    }
-    // a share may push to another once that runs
-    if (splits > 1) {
-        __syncwarp();
-        cluster_barrier();
     }
     pdl_wait();
     // not before the wait: a CTA that holds tensor memory must not wait for one that may need it
-    if (warp == 9) tmem_alloc(&tmem_at, kColumns);
-    if (warp == 0) {
-        const RowTile r = p.w.E == 1 ? tile_of_one(p, at, NT, grid_tiles) : find_tile(p, at, NT, grid_tiles);
-        if (lane == 0) shared_tile = r;
+    if (warp == kIssuer) tmem_alloc(&tmem_at, kColumns);
+    for (int e = threadIdx.x; e < p.w.E; e += kThreads) {
+        int64_t first;
+        bool bad;
+        table_rows[e] = expert_rows(p, e, &first, &bad);
+        table_first[e] = (int)first;
+        if (bad && blockIdx.x == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrBadSlot);
     }
     tcgen05_before();
     __syncthreads();
     tcgen05_after();
-    const RowTile tile = shared_tile;
-    const uint32_t tmem = tmem_at;
-    if (tile.e >= 0) {
-        const int rows = tile.rows, cols = (rows + 15) & ~15;      // the products' N: a multiple of 16
-        unsigned char* ring = smem;
-        unsigned char* ops = smem + RING * kStepBytes;
-        const uint32_t a_at = tmem + NT;                           // past the sums' columns
-        bool good = true;
-        if (warp == 8) {
-            const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + (((int64_t)tile.e * nb + b) * nk + k0) * kStepBytes;
-            int filled = 0;
-            for (; filled < k1 - k0; ++filled) {
-                const int s = filled % RING;
-                if (filled >= RING && !__all_sync(0xffffffffu, mbar_wait(&ring_empty[s], (filled / RING - 1) & 1))) {
+    const uint32_t tmem = tmem_at, a_at = tmem + 2 * kTokens;
+    bool good = true;
+    auto next_item = [&](int j, Item* it) {
+        const int slot = j % kItems;
+        good = __all_sync(0xffffffffu, mbar_wait(&item_full[slot], (j / kItems) & 1));
+        if (!good) return false;
+        *it = items[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[slot]);
+        return it->e >= 0;
+    };
+    Item it;
+    if (warp == kFinder) {
+        // tiles up to and with each expert: lane l adds up those of experts [l * per, (l + 1) * per)
+        const int per = (p.w.E + 31) / 32, e0 = min(lane * per, p.w.E), e1 = min(e0 + per, p.w.E);
+        int mine = 0;
+        for (int e = e0; e < e1; ++e) {
+            mine = min(mine + (table_rows[e] + tile_rows - 1) / tile_rows, 1 << 25);      // bad offsets may claim rows many times
+            table_upto[e] = mine;
+        }
+        int before = 0, total = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, total, d);
+            if (lane >= d) total += v;
+        }
+        before = total - mine;
+        total = __shfl_sync(0xffffffffu, total, 31);
+        for (int e = e0; e < e1; ++e) table_upto[e] += before;
+        __syncwarp();
+        const int pairs = (nb + 1) / 2;
+        const int64_t all_items = (int64_t)total * pairs, most = splits > 1 ? min(all_items, (int64_t)clusters) : all_items;
+        if (most < all_items && blockIdx.x == 0 && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrCapacity);
+        for (int j = 0;; ++j) {
+            const int slot = j % kItems;
+            const int64_t at = cluster + (int64_t)j * clusters;
+            if (j >= kItems && !__all_sync(0xffffffffu, mbar_wait(&item_empty[slot], (j / kItems - 1) & 1))) {
+                good = false;
+                break;
+            }
+            it.e = -1;
+            if (at < most) {
+                const int tile = (int)(at / pairs);
+                int lo = 0, hi = p.w.E - 1;                    // the first expert with upto > tile
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (table_upto[mid] > tile)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                const int n = table_rows[lo], size = tile_rows_of(n, tile_rows), from = (tile - (lo > 0 ? table_upto[lo - 1] : 0)) * size;
+                it.e = lo;
+                it.rows = min(size, n - from);
+                it.first = table_first[lo] + from;
+                it.b = (int)(at - (int64_t)tile * pairs) * 2;
+                it.two = it.b + 1 < nb;
+            }
+            if (lane == 0) {
+                items[slot] = it;
+                mbar_arrive(&item_full[slot]);
+            }
+            __syncwarp();
+            if (it.e < 0) break;
+        }
+    } else if (warp == kProducer) {
+        int filled = 0;
+        for (int j = 0; next_item(j, &it); ++j) {
+            const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + (((int64_t)it.e * nb + it.b) * nk + k0) * kStepBytes;
+            for (int i = 0; i < steps; ++i, ++filled, weights += kStepBytes) {
+                const int s = filled % kRing;
+                if (filled >= kRing && !__all_sync(0xffffffffu, mbar_wait(&ring_empty[s], (filled / kRing - 1) & 1))) {
                     good = false;
                     break;
                 }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&ring_full[s], kStepBytes);
-                    bulk_load(ring + s * kStepBytes, weights + (int64_t)filled * kStepBytes, kStepBytes, &ring_full[s]);
+                    unsigned char* to = smem + s * 2 * kStepBytes;
+                    mbar_arrive_expect_tx(&ring_full[s], it.two ? 2 * kStepBytes : kStepBytes);
+                    bulk_load(to, weights, kStepBytes, &ring_full[s]);
+                    if (it.two) bulk_load(to + kStepBytes, weights + (int64_t)nk * kStepBytes, kStepBytes, &ring_full[s]);
                 }
                 __syncwarp();
             }
-            // no copy may be in flight when the CTA ends, whatever its consumers did
-            for (int i = max(0, filled - RING); i < filled; ++i) mbar_wait(&ring_full[i % RING], (i / RING) & 1);
-        } else if (warp == 9) {
-            const uint32_t kind = 1u << 4 | (uint32_t)(cols / 8) << 17 | (kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
+            if (!good) break;
+        }
+        // no copy may be in flight when the CTA ends, whatever its consumers did
+        for (int i = max(0, filled - kRing); i < filled; ++i) mbar_wait(&ring_full[i % kRing], (i / kRing) & 1);
+    } else if (warp == kIssuer) {
+        // one thread from here to its end: the products' operands then stay in uniform registers
+        if (elect_one()) {
             // runs of 8 channels kRunBytes apart, 8 rows 128 bytes apart, no swizzle
-            const uint64_t desc = (uint64_t)(kRunBytes<NT> / 16) << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int s = i % kOps;
-                if (!__all_sync(0xffffffffu, mbar_wait(&op_full[s], (i / kOps) & 1))) {
-                    good = false;
-                    break;
-                }
-                tcgen05_after();
-                if (lane == 0) {
-                    const uint32_t from = smem_addr(ops + s * kBBytes<NT>);
+            const uint64_t desc = (uint64_t)(kRunBytes / 16) << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
+            const uint64_t first_b = desc | (smem_addr(ops) >> 4 & 0x3fff);          // in a cluster, addresses have a rank above
+            int g = 0, committed = 0;
+            for (int j = 0;; ++j) {
+                const int slot = j % kItems;
+                good = mbar_wait(&item_full[slot], (j / kItems) & 1);
+                if (!good) break;
+                const int e = items[slot].e, rows = items[slot].rows, two = items[slot].two;
+                mbar_arrive(&item_empty[slot]);
+                if (e < 0) break;
+                const uint32_t cols = (rows + 15) & ~15;           // the products' N: a multiple of 16
+                const uint32_t kind = 1u << 4 | (cols / 8) << 17 | (uint32_t)(kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
+                if (j > 0) good = mbar_wait(&drained, (j - 1) & 1);
+                for (int i = 0; i < steps && good; ++i, ++g) {
+                    const int s = g % kOps;
+                    good = mbar_wait(&op_full[s], (g / kOps) & 1);
+                    if (!good) break;
+                    tcgen05_after();
+                    const uint32_t a = a_at + s * 2 * kAColumns;
+                    const uint64_t b = first_b + (uint32_t)(s * (kBBytes / 16));
 #pragma unroll
-                    for (int j = 0; j < kStep / 16; ++j)
-                        mma_f16(tmem, a_at + s * kAColumns + j * 8, desc | ((from + j * 2 * kRunBytes<NT>) >> 4 & 0x3fff), kind, i > 0 || j > 0);
+                    for (int k = 0; k < kStep / 16; ++k) mma_f16(tmem, a + k * 8, b + k * 2 * (kRunBytes / 16), kind, i > 0 || k > 0);
+                    if (two)
+#pragma unroll
+                        for (int k = 0; k < kStep / 16; ++k)
+                            mma_f16(tmem + kTokens, a + kAColumns + k * 8, b + k * 2 * (kRunBytes / 16), kind, i > 0 || k > 0);
                     tcgen05_commit(&op_empty[s]);
                 }
-                __syncwarp();
+                tcgen05_commit(&done);
+                ++committed;
+                if (!good) break;
             }
-            if (lane == 0) tcgen05_commit(&done);
-            __syncwarp();
-            good = __all_sync(0xffffffffu, mbar_wait(&done, 0)) && good;
-        } else if (warp >= 4) {
-            // tokens: a thread has 16 channels of every 32nd row
-            const int t = threadIdx.x - 128, c = t & 3, n0 = t >> 2;
-            const int8_t* x = p.x + tile.first * p.w.K + c * 16;
-            for (int n = t; n < NT; n += 128) row_scale[n] = n < rows ? p.x_scales[tile.first + n] : 0.f;
-            uint4 raw[NT / 32];
-            auto fetch = [&](int step) {
-                const int k = (k0 + step) * kStep;
+            // every product is over before tensor memory is given back
+            if (committed > 0) good = mbar_wait(&done, (committed - 1) & 1) && good;
+        }
+        __syncwarp();
+        good = __all_sync(0xffffffffu, good);
+    } else if (warp >= 8) {
+        // tokens: a thread has 16 channels of rows n0 and n0 + 64
+        const int t = threadIdx.x - 256, c = t & 3, n0 = t >> 2, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+        uint4 raw[kAhead][2];
+        int g = 0, j = 0;
+        Item last{};
+        auto write_out = [&](int item) {
+            good = __all_sync(0xffffffffu, mbar_wait(&done, item & 1));
+            if (!good) return;
+            tcgen05_after();
+            if (half == 0 || last.two) {
+                const Writer w(p, last, last.b + half, row);
+                for (int n = 0; n < last.rows; n += 16) {
+                    uint32_t v[16];
+                    const float xs = (lane & 15) + n < last.rows ? w.row_scale[n + (lane & 15)] : 0.f;
+                    tmem_load16(tmem + half * kTokens + n + lanes, v);
 #pragma unroll
-                for (int j = 0; j < NT / 32; ++j) {
-                    raw[j] = make_uint4(0, 0, 0, 0);               // channels past the end
-                    const int n = n0 + 32 * j;
-                    if (n < rows && step < k1 - k0 && k + c * 16 < p.w.K) raw[j] = *reinterpret_cast<const uint4*>(x + (int64_t)n * p.w.K + k);
-                }
-            };
-            fetch(0);
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int s = i % kOps;
-                if (i >= kOps && !__all_sync(0xffffffffu, mbar_wait(&op_empty[s], (i / kOps - 1) & 1))) {
-                    good = false;
-                    break;
-                }
-                unsigned char* to = ops + s * kBBytes<NT> + c * kRunBytes<NT>;
-#pragma unroll
-                for (int j = 0; j < NT / 32; ++j) {
-                    const int n = n0 + 32 * j;
-                    if (n < rows) {
-                        uint4 lo, hi;
-                        widen(raw[j].x ^ 0x80808080u, &lo.x, &lo.y);
-                        widen(raw[j].y ^ 0x80808080u, &lo.z, &lo.w);
-                        widen(raw[j].z ^ 0x80808080u, &hi.x, &hi.y);
-                        widen(raw[j].w ^ 0x80808080u, &hi.z, &hi.w);
-                        *reinterpret_cast<uint4*>(to + n * 16) = lo;
-                        *reinterpret_cast<uint4*>(to + 4 * kRunBytes<NT> + n * 16) = hi;
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = __shfl_sync(0xffffffffu, xs, i);
+                        if (n + i < last.rows) w.put(n + i, __uint_as_float(v[i]), x);
                     }
                 }
-                fetch(i + 1);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&op_full[s]);
             }
-        } else {
-            // weights: a thread has one row
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int s = i % kOps, r = i % RING;
-                if (!__all_sync(0xffffffffu, mbar_wait(&ring_full[r], (i / RING) & 1))) {
+            tcgen05_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&drained);
+        };
+        for (; next_item(j, &it); ++j) {
+            const int8_t* x = p.x + (int64_t)it.first * p.w.K + (int64_t)k0 * kStep + c * 16;
+            const int left = p.w.K - k0 * kStep - c * 16;          // channels from the thread's on
+            auto fetch = [&](uint4 (&r)[2], int step) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int n = n0 + 64 * i;
+                    r[i] = make_uint4(0, 0, 0, 0);                 // channels past the end
+                    if (n < it.rows && step < steps && step * kStep < left)
+                        r[i] = *reinterpret_cast<const uint4*>(x + (int64_t)n * p.w.K + step * kStep);
+                }
+            };
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) fetch(raw[u], u);
+            for (int base = 0; base < steps && good; base += kAhead) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = base + u;
+                    if (i >= steps || !good) break;
+                    // the products can go on with the steps made so far while the sums before are written out
+                    if (i == kOps && j > 0 && splits == 1) {
+                        write_out(j - 1);
+                        if (!good) break;
+                    }
+                    const int s = g % kOps;
+                    if (g >= kOps && !__all_sync(0xffffffffu, mbar_wait(&op_empty[s], (g / kOps - 1) & 1))) {
+                        good = false;
+                        break;
+                    }
+                    unsigned char* to = ops + s * kBBytes + c * kRunBytes;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const int n = n0 + 64 * m;
+                        if (n < it.rows) {
+                            uint4 lo, hi;
+                            widen(raw[u][m].x ^ 0x80808080u, &lo.x, &lo.y);
+                            widen(raw[u][m].y ^ 0x80808080u, &lo.z, &lo.w);
+                            widen(raw[u][m].z ^ 0x80808080u, &hi.x, &hi.y);
+                            widen(raw[u][m].w ^ 0x80808080u, &hi.z, &hi.w);
+                            *reinterpret_cast<uint4*>(to + n * 16) = lo;
+                            *reinterpret_cast<uint4*>(to + 4 * kRunBytes + n * 16) = hi;
+                        }
+                    }
+                    fetch(raw[u], i + kAhead);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&op_full[s]);
+                    ++g;
+                }
+            }
+            if (!good) break;
+            if (j > 0 && splits == 1 && steps <= kOps) write_out(j - 1);
+            if (!good) break;
+            last = it;
+        }
+        if (good && j > 0 && splits == 1) write_out(j - 1);
+        it = last;
+        if (j == 0) it.e = -1;
+    } else {
+        // weights: a thread has one row of one block
+        const int half = warp >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+        int g = 0;
+        for (int j = 0; next_item(j, &it); ++j) {
+            const bool here = half == 0 || it.two;
+            for (int i = 0; i < steps; ++i, ++g) {
+                const int s = g % kOps, r = g % kRing;
+                if (!__all_sync(0xffffffffu, mbar_wait(&ring_full[r], (g / kRing) & 1))) {
                     good = false;
                     break;
                 }
                 uint32_t v[32];
-                const unsigned char* from = ring + r * kStepBytes + threadIdx.x * 16;
+                if (here) {
+                    const unsigned char* from = smem + (r * 2 + half) * kStepBytes + (threadIdx.x & 127) * 16;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 raw = *reinterpret_cast<const uint4*>(from + q * kRows * 16);
-                    widen(raw.x, &v[q * 8], &v[q * 8 + 1]);
-                    widen(raw.y, &v[q * 8 + 2], &v[q * 8 + 3]);
-                    widen(raw.z, &v[q * 8 + 4], &v[q * 8 + 5]);
-                    widen(raw.w, &v[q * 8 + 6], &v[q * 8 + 7]);
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 raw = *reinterpret_cast<const uint4*>(from + q * kRows * 16);
+                        widen(raw.x, &v[q * 8], &v[q * 8 + 1]);
+                        widen(raw.y, &v[q * 8 + 2], &v[q * 8 + 3]);
+                        widen(raw.z, &v[q * 8 + 4], &v[q * 8 + 5]);
+                        widen(raw.w, &v[q * 8 + 6], &v[q * 8 + 7]);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ring_empty[r]);
-                if (i >= kOps && !__all_sync(0xffffffffu, mbar_wait(&op_empty[s], (i / kOps - 1) & 1))) {
+                if (g >= kOps && !__all_sync(0xffffffffu, mbar_wait(&op_empty[s], (g / kOps - 1) & 1))) {
                     good = false;
                     break;
                 }
-                tcgen05_after();
-                tmem_store32(a_at + s * kAColumns + ((uint32_t)warp * 32 << 16), v);
-                tmem_store_wait();
-                tcgen05_before();
+                if (here) {
+                    tcgen05_after();
+                    tmem_store32(a_at + (s * 2 + half) * kAColumns + lanes, v);
+                    tmem_store_wait();
+                    tcgen05_before();
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&op_full[s]);
             }
-            good = __all_sync(0xffffffffu, mbar_wait(&done, 0)) && good;
+            if (!good) break;
+        }
+    }
+    __syncwarp();
+    if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
+    good = __syncthreads_and(good);
+    if (splits > 1) {
+        // the shares' sums: each CTA owns some of the tile's token rows, whose sums the others push to it
+        cluster_barrier();                       // the rings are free
+        float* parts = reinterpret_cast<float*>(smem);         // [share][own][block][weight row]
+        const int half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+        const bool writes = warp >= 8 && warp < 16 && it.e >= 0 && (half == 0 || it.two);
+        const int own = (it.rows + splits - 1) / splits;
+        if (writes && good) {
             tcgen05_after();
-        }
-        __syncwarp();
-        good = __syncthreads_and(good);
-        if (!good && threadIdx.x == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
-        // epilogue: a thread has one weight row, 16 tokens at a time
-        const int own = (rows + splits - 1) / splits;              // token rows that a share of K owns
-        float* parts = reinterpret_cast<float*>(ops + kOps * kBBytes<NT>);       // [share][own][weight row]
-        if (splits > 1) {
-            if (warp < 4 && good) {
-                for (int n0 = 0; n0 < rows; n0 += 16) {
-                    uint32_t v[16];
-                    tmem_load16(tmem + n0 + ((uint32_t)warp * 32 << 16), v);
+            for (int n = 0; n < it.rows; n += 16) {
+                uint32_t v[16];
+                tmem_load16(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (n0 + j < rows) {
-                            const int owner = (n0 + j) / own;
-                            const uint32_t to = in_cta(smem_addr(parts + ((int64_t)split * own + n0 + j - owner * own) * kRows + threadIdx.x), owner);
-                            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(v[j]) : "memory");
-                        }
-                }
-            }
-            __syncwarp();
-            cluster_barrier();
-        }
-        if (warp < 4 && good) {
-            bool up;
-            const int c = channel_of(p.w, b, threadIdx.x, &up);
-            const float scale = reinterpret_cast<const float*>(static_cast<const unsigned char*>(p.packed) + scales_at(p.w))[((int64_t)tile.e * nb + b) * kRows + threadIdx.x];
-            uint16_t* y = static_cast<uint16_t*>(p.y) + tile.first * p.w.N + c;
-            auto finish = [&](int n, float sum) {
-                float f = sum * scale * row_scale[n];
-                if (p.w.paired) f = silu(f) * __shfl_xor_sync(0xffffffffu, f, 16);
-                if (c < p.w.N && !up) y[(int64_t)n * p.w.N] = (uint16_t)pack_bf16x2(f, 0.f);
-            };
-            if (splits > 1) {
-                for (int n = split * own; n < min(rows, (split + 1) * own); ++n) {
-                    float sum = 0.f;
-                    for (int q = 0; q < splits; ++q) sum += parts[((int64_t)q * own + n - split * own) * kRows + threadIdx.x];
-                    finish(n, sum);
-                }
-            } else {
-                for (int n0 = 0; n0 < rows; n0 += 16) {
-                    uint32_t v[16];
-                    tmem_load16(tmem + n0 + ((uint32_t)warp * 32 << 16), v);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (n0 + j < rows) finish(n0 + j, __uint_as_float(v[j]));
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (n + i < it.rows) {
+                        const int owner = (n + i) / own;
+                        const uint32_t to = in_cta(smem_addr(parts + ((split * own + n + i - owner * own) * 2 + half) * kRows + row), owner);
+                        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(v[i]) : "memory");
+                    }
             }
             tcgen05_before();
         }
+        __syncwarp();
+        cluster_barrier();
+        if (writes && good) {
+            const Writer w(p, it, it.b + half, row);
+            for (int n = split * own; n < min(it.rows, (split + 1) * own); ++n) {
+                float sum = 0.f;
+                for (int q = 0; q < splits; ++q) sum += parts[((q * own + n - split * own) * 2 + half) * kRows + row];
+                w.put(n, sum, w.row_scale[n]);
+            }
+        }
     }
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssuer) {
         tcgen05_after();
         tmem_free(tmem, kColumns);
     }
@@ -380,25 +557,13 @@ int64_t most_tiles(int E, int64_t max_rows, int tile) {
     return used + (max_rows - used) / tile;
 }
 
-template <int NT, int RING>
-cudaError_t launch(const I8Params& p, int num_sms, cudaStream_t stream) {
-    const int64_t tiles = most_tiles(p.w.E, p.max_rows, NT), products = tiles * row_blocks(p.w);
-    int splits = 1;
-    while (splits < 8 && products * splits * 2 <= 2 * num_sms && k_steps(p.w) >= splits * 4) splits *= 2;
-    const size_t smem = kSmemBytes<NT, RING> + (splits > 1 ? (size_t)(NT + splits) * kRows * 4 : 0);
-    auto kern = expert_i8_kernel<NT, RING>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<NT, RING> + (NT + 8) * kRows * 4);
-    if (e != cudaSuccess) return e;
-    return launch_clusters(true, splits, kern, dim3((unsigned)(products * splits)), dim3(kThreads), smem, stream, p, splits, (int)tiles);
-}
-
 }  // namespace
 
 size_t i8_bytes(const I8Shape& w) { return (size_t)scales_at(w) + (size_t)w.E * row_blocks(w) * kRows * sizeof(float); }
 
 bool i8_packs(const I8Shape& w) { return (int64_t)w.E * row_blocks(w) * k_steps(w) <= INT32_MAX; }
 
-bool i8_fits(const I8Shape& w, int64_t max_rows) { return most_tiles(w.E, max_rows, 32) * row_blocks(w) <= INT32_MAX / 8; }
+bool i8_fits(const I8Shape& w, int64_t max_rows) { return most_tiles(w.E, max_rows, 16) * row_blocks(w) <= INT32_MAX / 8; }
 
 cudaError_t launch_i8_pack(const I8Shape& w, const int8_t* codes, const float* scales, void* packed, cudaStream_t stream) {
     const dim3 grid((unsigned)((int64_t)w.E * row_blocks(w) * k_steps(w)));
@@ -406,7 +571,15 @@ cudaError_t launch_i8_pack(const I8Shape& w, const int8_t* codes, const float* s
 }
 
 cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream) {
-    return p.max_rows <= (int64_t)24 * p.w.E ? launch<32, 10>(p, num_sms, stream) : launch<128, 5>(p, num_sms, stream);
+    const int pairs = (row_blocks(p.w) + 1) / 2;
+    int tile = kTokens, splits = 1;
+    while (tile > 32 && most_tiles(p.w.E, p.max_rows, tile) * pairs * 2 <= num_sms) tile /= 2;
+    const int64_t most = most_tiles(p.w.E, p.max_rows, tile) * pairs;
+    while (splits < 8 && most * splits * 2 <= num_sms && k_steps(p.w) >= splits * 4) splits *= 2;
+    const cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const unsigned clusters = (unsigned)std::min<int64_t>(most, num_sms / splits);
+    return launch_clusters(true, splits, expert_i8_kernel, dim3(clusters * splits), dim3(kThreads), kSmemBytes, stream, p, splits, tile);
 }
 
 }  // namespace ep
