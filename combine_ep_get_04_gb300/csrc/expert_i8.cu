@@ -5,7 +5,7 @@
 // thirteen times that, so the codes go through the tensor cores as f16, which
 // holds them exactly: a product of two has 15 bits and sums stay exact below 2^24.
 // Two blocks of 128 weight rows are the M side of tcgen05.mma, up to 128 token rows
-// the N side of both, 64 input channels a step.  One CTA an SM takes item after
+// the N side of both, 128 input channels a step.  One CTA an SM takes item after
 // item (two blocks with one tile of token rows).  A warp finds the items; a
 // producer warp keeps a ring of weight codes filled by bulk copies; eight warps
 // widen them into tensor memory, a row to a thread, which is the instruction's A
@@ -23,12 +23,12 @@ namespace {
 
 constexpr int kRows = 128;         // weight rows of a block
 constexpr int kTokens = 128;       // most token rows of a tile
-constexpr int kStep = 64;          // input channels of a step
+constexpr int kStep = 128;         // input channels of a step
 constexpr int kStepBytes = kRows * kStep;
-constexpr int kRing = 8;           // steps of weight codes
-constexpr int kOps = 4;            // steps whose operands are widened ahead
+constexpr int kRing = 4;           // steps of weight codes
+constexpr int kOps = 2;            // steps whose operands are widened ahead
 constexpr int kItems = 4;          // items found ahead
-constexpr int kAhead = 3;          // steps whose token codes are on their way
+constexpr int kAhead = 2;          // steps whose token codes are on their way
 // warps: 8 of weights, 8 of tokens, the producer, the issuer, the one that finds items
 constexpr int kProducer = 16, kIssuer = 17, kFinder = 18;
 constexpr int kThreads = 19 * 32;
@@ -49,11 +49,11 @@ __host__ __device__ inline int channel_of(const I8Shape& w, int b, int r, bool* 
     return w.paired ? b * 64 + (r >> 5) * 16 + (r & 15) : b * kRows + r;
 }
 
-// The order in which a step's 64 channels enter the products.  A thread that
+// The order in which a step's 128 channels enter the products.  A thread that
 // widens 16 neighbouring channels of a token writes two runs of 8; runs
 // 16-channel groups apart are neighbours, so that eight lanes' writes fall into
-// different banks: run h * 4 + c holds channels 16 c + 8 h and up.
-__host__ __device__ constexpr int run_channel(int run) { return (run & 3) * 16 + (run >> 2) * 8; }
+// different banks: run h * 8 + c holds channels 16 c + 8 h and up.
+__host__ __device__ constexpr int run_channel(int run) { return (run & 7) * 16 + (run >> 3) * 8; }
 
 // Packed: steps [E][row block][step][two runs][row][16 bytes], codes plus 128;
 // then the scales [E][row block][row].
@@ -149,9 +149,9 @@ __device__ __forceinline__ void widen(uint32_t biased, uint32_t* lo, uint32_t* h
 
 // ------------------------------------------------------------------ kernel
 
-// A step's B operand: runs of 8 channels of kTokens rows, 16 bytes a row; 32 bytes
+// A step's B operand: runs of 8 channels of kTokens rows, 16 bytes a row; 16 bytes
 // more keep the runs that eight lanes write at once in different banks.
-constexpr int kRunBytes = (kTokens + 2) * 16;
+constexpr int kRunBytes = (kTokens + 1) * 16;
 constexpr int kBBytes = kStep / 8 * kRunBytes;
 constexpr int kRingBytes = kRing * 2 * kStepBytes;
 constexpr int kSmemBytes = kRingBytes + kOps * kBBytes;
@@ -380,10 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         __syncwarp();
         good = __all_sync(0xffffffffu, good);
     } else if (warp >= 8) {
-        // tokens: a thread has 16 channels of rows n0 and n0 + 64
-        const int t = threadIdx.x - 256, c = t & 3, n0 = t >> 2, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+        // tokens: a thread has 16 channels of every 32nd row
+        const int t = threadIdx.x - 256, c = t & 7, n0 = t >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        uint4 raw[kAhead][2];
+        uint4 raw[kAhead][kTokens / 32];
         int g = 0, j = 0;
         Item last{};
         auto write_out = [&](int item) {
@@ -410,10 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         for (; next_item(j, &it); ++j) {
             const int8_t* x = p.x + (int64_t)it.first * p.w.K + (int64_t)k0 * kStep + c * 16;
             const int left = p.w.K - k0 * kStep - c * 16;          // channels from the thread's on
-            auto fetch = [&](uint4 (&r)[2], int step) {
+            auto fetch = [&](uint4 (&r)[kTokens / 32], int step) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int n = n0 + 64 * i;
+                for (int i = 0; i < kTokens / 32; ++i) {
+                    const int n = n0 + 32 * i;
                     r[i] = make_uint4(0, 0, 0, 0);                 // channels past the end
                     if (n < it.rows && step < steps && step * kStep < left)
                         r[i] = *reinterpret_cast<const uint4*>(x + (int64_t)n * p.w.K + step * kStep);
@@ -438,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                     }
                     unsigned char* to = ops + s * kBBytes + c * kRunBytes;
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const int n = n0 + 64 * m;
+                    for (int m = 0; m < kTokens / 32; ++m) {
+                        const int n = n0 + 32 * m;
                         if (n < it.rows) {
                             uint4 lo, hi;
                             widen(raw[u][m].x ^ 0x80808080u, &lo.x, &lo.y);
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                             widen(raw[u][m].z ^ 0x80808080u, &hi.x, &hi.y);
                             widen(raw[u][m].w ^ 0x80808080u, &hi.z, &hi.w);
                             *reinterpret_cast<uint4*>(to + n * 16) = lo;
-                            *reinterpret_cast<uint4*>(to + 4 * kRunBytes + n * 16) = hi;
+                            *reinterpret_cast<uint4*>(to + 8 * kRunBytes + n * 16) = hi;
                         }
                     }
                     fetch(raw[u], i + kAhead);
@@ -478,16 +478,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                     good = false;
                     break;
                 }
-                uint32_t v[32];
+                uint32_t v[2][32];
                 if (here) {
                     const unsigned char* from = smem + (r * 2 + half) * kStepBytes + (threadIdx.x & 127) * 16;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 8; ++q) {
                         const uint4 raw = *reinterpret_cast<const uint4*>(from + q * kRows * 16);
-                        widen(raw.x, &v[q * 8], &v[q * 8 + 1]);
-                        widen(raw.y, &v[q * 8 + 2], &v[q * 8 + 3]);
-                        widen(raw.z, &v[q * 8 + 4], &v[q * 8 + 5]);
-                        widen(raw.w, &v[q * 8 + 6], &v[q * 8 + 7]);
+                        uint32_t* to = &v[q >> 2][(q & 3) * 8];
+                        widen(raw.x, to, to + 1);
+                        widen(raw.y, to + 2, to + 3);
+                        widen(raw.z, to + 4, to + 5);
+                        widen(raw.w, to + 6, to + 7);
                     }
                 }
                 __syncwarp();
@@ -498,7 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                 }
                 if (here) {
                     tcgen05_after();
-                    tmem_store32(a_at + (s * 2 + half) * kAColumns + lanes, v);
+                    const uint32_t to = a_at + (s * 2 + half) * kAColumns + lanes;
+                    tmem_store32(to, v[0]);
+                    tmem_store32(to + 32, v[1]);
                     tmem_store_wait();
                     tcgen05_before();
                 }
