@@ -25,15 +25,17 @@ constexpr int kRows = 128;         // weight rows of a block
 constexpr int kTokens = 128;       // most token rows of a tile
 constexpr int kStep = 128;         // input channels of a step
 constexpr int kStepBytes = kRows * kStep;
-constexpr int kRing = 4;           // steps of weight codes
-constexpr int kOps = 2;            // steps whose operands are widened ahead
+constexpr int kRing = 3;           // steps of weight codes
+constexpr int kA = 2;              // steps whose weights are widened ahead
+constexpr int kB = 3;              // steps whose tokens are
+constexpr int kSteps = 6;          // barriers of steps under way: a multiple of both
 constexpr int kItems = 4;          // items found ahead
 constexpr int kAhead = 2;          // steps whose token codes are on their way
 // warps: 8 of weights, 8 of tokens, the producer, the issuer, the one that finds items
 constexpr int kProducer = 16, kIssuer = 17, kFinder = 18;
 constexpr int kThreads = 19 * 32;
 constexpr int kItemReaders = 18;
-constexpr uint32_t kColumns = 512;                // tensor memory: the two blocks' sums, then kOps x 2 A operands
+constexpr uint32_t kColumns = 512;                // tensor memory: the two blocks' sums, then kA x 2 A operands
 constexpr int kAColumns = kStep / 2;
 
 __host__ __device__ inline int k_steps(const I8Shape& w) { return (w.K + kStep - 1) / kStep; }
@@ -122,12 +124,14 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32
 
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+        "%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+          "=r"(v[30]), "=r"(v[31])
         : "r"(at)
         : "memory");
 }
@@ -154,7 +158,7 @@ __device__ __forceinline__ void widen(uint32_t biased, uint32_t* lo, uint32_t* h
 constexpr int kRunBytes = (kTokens + 1) * 16;
 constexpr int kBBytes = kStep / 8 * kRunBytes;
 constexpr int kRingBytes = kRing * 2 * kStepBytes;
-constexpr int kSmemBytes = kRingBytes + kOps * kBBytes;
+constexpr int kSmemBytes = kRingBytes + kB * kBBytes;
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -182,27 +186,42 @@ __device__ __forceinline__ int tile_rows_of(int n, int tile) {
     return ((n + tiles - 1) / tiles + 15) & ~15;
 }
 
-// The sums of up to 16 token rows of a weight row to a lane, scaled and stored.
+// The sums of a weight row to a lane, scaled, paired and stored.
 struct Writer {
-    const I8Params& p;
     uint16_t* y;             // at the lane's channel of the tile's first row
     const float* row_scale;  // of the tile's first row
     float scale;
-    bool stores;
+    int N, rows;
+    bool paired, stores;
 
-    __device__ __forceinline__ Writer(const I8Params& p, const Item& it, int b, int row) : p(p) {
+    __device__ __forceinline__ Writer(const I8Params& p, const Item& it, int b, int row) {
         bool up;
         const int c = channel_of(p.w, b, row, &up);
         scale = reinterpret_cast<const float*>(static_cast<const unsigned char*>(p.packed) + scales_at(p.w))[((int64_t)it.e * row_blocks(p.w) + b) * kRows + row];
         y = static_cast<uint16_t*>(p.y) + (int64_t)it.first * p.w.N + c;
         row_scale = p.x_scales + it.first;
-        stores = c < p.w.N && !up;
+        N = p.w.N;
+        rows = it.rows;
+        paired = p.w.paired;
+        stores = c < N;
     }
 
-    __device__ __forceinline__ void put(int n, float sum, float xs) const {
-        float f = sum * scale * xs;
-        if (p.w.paired) f = silu(f) * __shfl_xor_sync(0xffffffffu, f, 16);
-        if (stores) y[(int64_t)n * p.w.N] = (uint16_t)pack_bf16x2(f, 0.f);
+    // Token rows n and n + 1.  xs(r): the scale of row r (r = n or n + 1 in a lane).  Of a pair, the lower
+    // lanes have the gates and finish row n, the upper ones have the ups and finish row n + 1.
+    template <typename Scale>
+    __device__ __forceinline__ void put(int n, float s0, float s1, Scale xs) const {
+        const bool upper = threadIdx.x & 16;
+        const float a = s0 * scale, b = s1 * scale;
+        if (paired) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+            const int r = n + upper;
+            const float f = xs(r), gate = (upper ? other : a) * f, up = (upper ? b : other) * f;
+            if (stores && r < rows) y[(int64_t)r * N] = (uint16_t)pack_bf16x2(silu(gate) * up, 0.f);
+        } else {
+            const float f0 = xs(n), f1 = xs(n + 1);
+            if (stores) y[(int64_t)n * N] = (uint16_t)pack_bf16x2(a * f0, 0.f);
+            if (stores && n + 1 < rows) y[(int64_t)(n + 1) * N] = (uint16_t)pack_bf16x2(b * f1, 0.f);
+        }
     }
 };
 
@@ -210,7 +229,7 @@ struct Writer {
 // than one share of K (which a launch of few products has) a cluster takes one.
 __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int splits, int tile_rows) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t ring_full[kRing], ring_empty[kRing], op_full[kOps], op_empty[kOps], item_full[kItems], item_empty[kItems];
+    __shared__ uint64_t ring_full[kRing], ring_empty[kRing], op_full[kSteps], op_done[kSteps], item_full[kItems], item_empty[kItems];
     __shared__ uint64_t done, drained;
     __shared__ uint32_t tmem_at;
     __shared__ Item items[kItems];
@@ -226,9 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
             mbar_init(&ring_full[i], 1);
             mbar_init(&ring_empty[i], 8);
         }
-        for (int i = 0; i < kOps; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
             mbar_init(&op_full[i], 16);
-            mbar_init(&op_empty[i], 1);
+            mbar_init(&op_done[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&item_full[i], 1);
@@ -261,6 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[slot]);
         return it->e >= 0;
+    };
+    // Whether the products of step g are over, which sets its operands' room free.
+    auto step_done = [&](int g) {
+        good = __all_sync(0xffffffffu, mbar_wait(&op_done[g % kSteps], (g / kSteps) & 1));
+        return good;
     };
     Item it;
     if (warp == kFinder) {
@@ -356,19 +380,19 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                 const uint32_t kind = 1u << 4 | (cols / 8) << 17 | (uint32_t)(kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
                 if (j > 0) good = mbar_wait(&drained, (j - 1) & 1);
                 for (int i = 0; i < steps && good; ++i, ++g) {
-                    const int s = g % kOps;
-                    good = mbar_wait(&op_full[s], (g / kOps) & 1);
+                    const int s = g % kSteps;
+                    good = mbar_wait(&op_full[s], (g / kSteps) & 1);
                     if (!good) break;
                     tcgen05_after();
-                    const uint32_t a = a_at + s * 2 * kAColumns;
-                    const uint64_t b = first_b + (uint32_t)(s * (kBBytes / 16));
+                    const uint32_t a = a_at + s % kA * 2 * kAColumns;
+                    const uint64_t b = first_b + (uint32_t)(s % kB * (kBBytes / 16));
 #pragma unroll
                     for (int k = 0; k < kStep / 16; ++k) mma_f16(tmem, a + k * 8, b + k * 2 * (kRunBytes / 16), kind, i > 0 || k > 0);
                     if (two)
 #pragma unroll
                         for (int k = 0; k < kStep / 16; ++k)
                             mma_f16(tmem + kTokens, a + kAColumns + k * 8, b + k * 2 * (kRunBytes / 16), kind, i > 0 || k > 0);
-                    tcgen05_commit(&op_empty[s]);
+                    tcgen05_commit(&op_done[s]);
                 }
                 tcgen05_commit(&done);
                 ++committed;
@@ -392,15 +416,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
             tcgen05_after();
             if (half == 0 || last.two) {
                 const Writer w(p, last, last.b + half, row);
-                for (int n = 0; n < last.rows; n += 16) {
-                    uint32_t v[16];
-                    const float xs = (lane & 15) + n < last.rows ? w.row_scale[n + (lane & 15)] : 0.f;
-                    tmem_load16(tmem + half * kTokens + n + lanes, v);
+                for (int n = 0; n < last.rows; n += 32) {
+                    uint32_t v[32];
+                    const float mine = lane + n < last.rows ? w.row_scale[n + lane] : 0.f;
+                    tmem_load32(tmem + half * kTokens + n + lanes, v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = __shfl_sync(0xffffffffu, xs, i);
-                        if (n + i < last.rows) w.put(n + i, __uint_as_float(v[i]), x);
-                    }
+                    for (int i = 0; i < 32; i += 2)
+                        if (n + i < last.rows)
+                            w.put(n + i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                                  [&](int r) { return __shfl_sync(0xffffffffu, mine, r - n); });
                 }
             }
             tcgen05_before();
@@ -427,16 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                     const int i = base + u;
                     if (i >= steps || !good) break;
                     // the products can go on with the steps made so far while the sums before are written out
-                    if (i == kOps && j > 0 && splits == 1) {
+                    if (i == kB && j > 0 && splits == 1) {
                         write_out(j - 1);
                         if (!good) break;
                     }
-                    const int s = g % kOps;
-                    if (g >= kOps && !__all_sync(0xffffffffu, mbar_wait(&op_empty[s], (g / kOps - 1) & 1))) {
-                        good = false;
-                        break;
-                    }
-                    unsigned char* to = ops + s * kBBytes + c * kRunBytes;
+                    if (g >= kB && !step_done(g - kB)) break;
+                    unsigned char* to = ops + g % kB * kBBytes + c * kRunBytes;
 #pragma unroll
                     for (int m = 0; m < kTokens / 32; ++m) {
                         const int n = n0 + 32 * m;
@@ -453,12 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                     fetch(raw[u], i + kAhead);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&op_full[s]);
+                    if (lane == 0) mbar_arrive(&op_full[g % kSteps]);
                     ++g;
                 }
             }
             if (!good) break;
-            if (j > 0 && splits == 1 && steps <= kOps) write_out(j - 1);
+            if (j > 0 && splits == 1 && steps <= kB) write_out(j - 1);
             if (!good) break;
             last = it;
         }
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         for (int j = 0; next_item(j, &it); ++j) {
             const bool here = half == 0 || it.two;
             for (int i = 0; i < steps; ++i, ++g) {
-                const int s = g % kOps, r = g % kRing;
+                const int r = g % kRing;
                 if (!__all_sync(0xffffffffu, mbar_wait(&ring_full[r], (g / kRing) & 1))) {
                     good = false;
                     break;
@@ -493,20 +513,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ring_empty[r]);
-                if (g >= kOps && !__all_sync(0xffffffffu, mbar_wait(&op_empty[s], (g / kOps - 1) & 1))) {
-                    good = false;
-                    break;
-                }
+                if (g >= kA && !step_done(g - kA)) break;
                 if (here) {
                     tcgen05_after();
-                    const uint32_t to = a_at + (s * 2 + half) * kAColumns + lanes;
+                    const uint32_t to = a_at + (g % kA * 2 + half) * kAColumns + lanes;
                     tmem_store32(to, v[0]);
                     tmem_store32(to + 32, v[1]);
                     tmem_store_wait();
                     tcgen05_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&op_full[s]);
+                if (lane == 0) mbar_arrive(&op_full[g % kSteps]);
             }
             if (!good) break;
         }
@@ -523,11 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         const int own = (it.rows + splits - 1) / splits;
         if (writes && good) {
             tcgen05_after();
-            for (int n = 0; n < it.rows; n += 16) {
-                uint32_t v[16];
-                tmem_load16(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
+            for (int n = 0; n < it.rows; n += 32) {
+                uint32_t v[32];
+                tmem_load32(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 32; ++i)
                     if (n + i < it.rows) {
                         const int owner = (n + i) / own;
                         const uint32_t to = in_cta(smem_addr(parts + ((split * own + n + i - owner * own) * 2 + half) * kRows + row), owner);
@@ -539,11 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         __syncwarp();
         cluster_barrier();
         if (writes && good) {
-            const Writer w(p, it, it.b + half, row);
-            for (int n = split * own; n < min(it.rows, (split + 1) * own); ++n) {
-                float sum = 0.f;
-                for (int q = 0; q < splits; ++q) sum += parts[((q * own + n - split * own) * 2 + half) * kRows + row];
-                w.put(n, sum, w.row_scale[n]);
+            Writer w(p, it, it.b + half, row);
+            const int to = min(it.rows, (split + 1) * own);
+            w.rows = to;                         // the rows after them are another's
+            for (int n = split * own; n < to; n += 2) {
+                float sum[2] = {0.f, 0.f};
+                for (int q = 0; q < splits; ++q)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (n + i < to) sum[i] += parts[((q * own + n + i - split * own) * 2 + half) * kRows + row];
+                w.put(n, sum[0], sum[1], [&](int r) { return r < to ? w.row_scale[r] : 0.f; });
             }
         }
     }
