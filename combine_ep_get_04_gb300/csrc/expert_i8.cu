@@ -25,7 +25,7 @@ constexpr int kRows = 128;         // weight rows of a block
 constexpr int kTokens = 128;       // most token rows of a tile
 constexpr int kStep = 128;         // input channels of a step
 constexpr int kStepBytes = kRows * kStep;
-constexpr int kRing = 3;           // steps of weight codes
+constexpr int kMaxRing = 6;        // steps of weight codes
 constexpr int kA = 2;              // steps whose weights are widened ahead
 constexpr int kB = 3;              // steps whose tokens are
 constexpr int kSteps = 6;          // barriers of steps under way: a multiple of both
@@ -124,14 +124,12 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32
 
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
-        "%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
-          "=r"(v[30]), "=r"(v[31])
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(at)
         : "memory");
 }
@@ -153,12 +151,52 @@ __device__ __forceinline__ void widen(uint32_t biased, uint32_t* lo, uint32_t* h
 
 // ------------------------------------------------------------------ kernel
 
-// A step's B operand: runs of 8 channels of kTokens rows, 16 bytes a row; 16 bytes
-// more keep the runs that eight lanes write at once in different banks.
-constexpr int kRunBytes = (kTokens + 1) * 16;
-constexpr int kBBytes = kStep / 8 * kRunBytes;
-constexpr int kRingBytes = kRing * 2 * kStepBytes;
-constexpr int kSmemBytes = kRingBytes + kB * kBBytes;
+// A step's B operand: runs of 8 channels of up to tile_rows rows, 16 bytes a row;
+// 16 bytes more keep the runs that eight lanes write at once in different banks.
+// What shared memory is left holds the ring of weight codes.
+constexpr int kRuns = kStep / 8;
+constexpr int kSmemBytes = 208 * 1024;
+
+__host__ __device__ constexpr int run_bytes(int tile_rows) { return (tile_rows + 1) * 16; }
+__host__ __device__ constexpr int ring_steps(int tile_rows) {
+    const int fit = (kSmemBytes - kB * kRuns * run_bytes(tile_rows)) / (2 * kStepBytes);
+    return fit < kMaxRing ? fit : kMaxRing;
+}
+static_assert(ring_steps(kTokens) >= 3, "the widest tile leaves too little for the ring");
+
+// Waits for a phase, at most kWaitLimitNs and a few tries.  A try suspends the
+// thread for a while by itself, which leaves the issue slots to others; the clock
+// is looked at once in 64 of them.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1;; ++tries) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (tries % 64 == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) return false;
+        }
+    }
+}
+
+// A place in a ring and the parity of its phase.
+struct Place {
+    int at = 0;
+    uint32_t parity = 0;
+
+    __device__ __forceinline__ void next(int size) {
+        if (++at == size) {
+            at = 0;
+            parity ^= 1;
+        }
+    }
+};
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -188,7 +226,7 @@ __device__ __forceinline__ int tile_rows_of(int n, int tile) {
 
 // The sums of a weight row to a lane, scaled, paired and stored.
 struct Writer {
-    uint16_t* y;             // at the lane's channel of the tile's first row
+    uint16_t* y;             // at the lane's channel of the tile's first row (the upper lanes' of a pair: of the second)
     const float* row_scale;  // of the tile's first row
     float scale;
     int N, rows;
@@ -198,11 +236,11 @@ struct Writer {
         bool up;
         const int c = channel_of(p.w, b, row, &up);
         scale = reinterpret_cast<const float*>(static_cast<const unsigned char*>(p.packed) + scales_at(p.w))[((int64_t)it.e * row_blocks(p.w) + b) * kRows + row];
-        y = static_cast<uint16_t*>(p.y) + (int64_t)it.first * p.w.N + c;
-        row_scale = p.x_scales + it.first;
         N = p.w.N;
-        rows = it.rows;
         paired = p.w.paired;
+        y = static_cast<uint16_t*>(p.y) + (int64_t)it.first * N + c + (paired && (threadIdx.x & 16) ? N : 0);
+        row_scale = p.x_scales + it.first;
+        rows = it.rows;
         stores = c < N;
     }
 
@@ -212,15 +250,17 @@ struct Writer {
     __device__ __forceinline__ void put(int n, float s0, float s1, Scale xs) const {
         const bool upper = threadIdx.x & 16;
         const float a = s0 * scale, b = s1 * scale;
+        uint16_t* to = y + (int64_t)n * N;
         if (paired) {
             const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
             const int r = n + upper;
             const float f = xs(r), gate = (upper ? other : a) * f, up = (upper ? b : other) * f;
-            if (stores && r < rows) y[(int64_t)r * N] = (uint16_t)pack_bf16x2(silu(gate) * up, 0.f);
+            const uint16_t out = (uint16_t)pack_bf16x2(silu(gate) * up, 0.f);
+            if (stores && r < rows) *to = out;
         } else {
             const float f0 = xs(n), f1 = xs(n + 1);
-            if (stores) y[(int64_t)n * N] = (uint16_t)pack_bf16x2(a * f0, 0.f);
-            if (stores && n + 1 < rows) y[(int64_t)(n + 1) * N] = (uint16_t)pack_bf16x2(b * f1, 0.f);
+            if (stores && n < rows) *to = (uint16_t)pack_bf16x2(a * f0, 0.f);
+            if (stores && n + 1 < rows) to[N] = (uint16_t)pack_bf16x2(b * f1, 0.f);
         }
     }
 };
@@ -229,7 +269,7 @@ struct Writer {
 // than one share of K (which a launch of few products has) a cluster takes one.
 __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int splits, int tile_rows) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t ring_full[kRing], ring_empty[kRing], op_full[kSteps], op_done[kSteps], item_full[kItems], item_empty[kItems];
+    __shared__ uint64_t ring_full[kMaxRing], ring_empty[kMaxRing], op_full[kSteps], op_done[kSteps], item_full[kItems], item_empty[kItems];
     __shared__ uint64_t done, drained;
     __shared__ uint32_t tmem_at;
     __shared__ Item items[kItems];
@@ -238,10 +278,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
     const int split = blockIdx.x % splits, cluster = blockIdx.x / splits, clusters = gridDim.x / splits;
     const int nb = row_blocks(p.w), nk = k_steps(p.w);
     const int k0 = (int)((int64_t)nk * split / splits), steps = (int)((int64_t)nk * (split + 1) / splits) - k0;
-    unsigned char* ops = smem + kRingBytes;
+    const int ring = ring_steps(tile_rows), run = run_bytes(tile_rows), b_bytes = kRuns * run;
+    unsigned char* ops = smem + ring * 2 * kStepBytes;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRing; ++i) {
+        for (int i = 0; i < ring; ++i) {
             mbar_init(&ring_full[i], 1);
             mbar_init(&ring_empty[i], 8);
         }
@@ -272,19 +313,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
     tcgen05_after();
     const uint32_t tmem = tmem_at, a_at = tmem + 2 * kTokens;
     bool good = true;
+    auto await = [&](uint64_t* bar, uint32_t parity) {
+        good = __all_sync(0xffffffffu, wait_phase(bar, parity));
+        return good;
+    };
     auto next_item = [&](int j, Item* it) {
         const int slot = j % kItems;
-        good = __all_sync(0xffffffffu, mbar_wait(&item_full[slot], (j / kItems) & 1));
-        if (!good) return false;
+        if (!await(&item_full[slot], (j / kItems) & 1)) return false;
         *it = items[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[slot]);
         return it->e >= 0;
-    };
-    // Whether the products of step g are over, which sets its operands' room free.
-    auto step_done = [&](int g) {
-        good = __all_sync(0xffffffffu, mbar_wait(&op_done[g % kSteps], (g / kSteps) & 1));
-        return good;
     };
     Item it;
     if (warp == kFinder) {
@@ -311,10 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         for (int j = 0;; ++j) {
             const int slot = j % kItems;
             const int64_t at = cluster + (int64_t)j * clusters;
-            if (j >= kItems && !__all_sync(0xffffffffu, mbar_wait(&item_empty[slot], (j / kItems - 1) & 1))) {
-                good = false;
-                break;
-            }
+            if (j >= kItems && !await(&item_empty[slot], (j / kItems - 1) & 1)) break;
             it.e = -1;
             if (at < most) {
                 const int tile = (int)(at / pairs);
@@ -341,65 +377,63 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
             if (it.e < 0) break;
         }
     } else if (warp == kProducer) {
-        int filled = 0;
+        int64_t filled = 0;
+        Place r{0, 1};                           // the parity of the place's previous use
         for (int j = 0; next_item(j, &it); ++j) {
             const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + (((int64_t)it.e * nb + it.b) * nk + k0) * kStepBytes;
-            for (int i = 0; i < steps; ++i, ++filled, weights += kStepBytes) {
-                const int s = filled % kRing;
-                if (filled >= kRing && !__all_sync(0xffffffffu, mbar_wait(&ring_empty[s], (filled / kRing - 1) & 1))) {
-                    good = false;
-                    break;
-                }
+            for (int i = 0; i < steps; ++i, ++filled, weights += kStepBytes, r.next(ring)) {
+                if (filled >= ring && !await(&ring_empty[r.at], r.parity)) break;
                 if (lane == 0) {
-                    unsigned char* to = smem + s * 2 * kStepBytes;
-                    mbar_arrive_expect_tx(&ring_full[s], it.two ? 2 * kStepBytes : kStepBytes);
-                    bulk_load(to, weights, kStepBytes, &ring_full[s]);
-                    if (it.two) bulk_load(to + kStepBytes, weights + (int64_t)nk * kStepBytes, kStepBytes, &ring_full[s]);
+                    unsigned char* to = smem + r.at * 2 * kStepBytes;
+                    mbar_arrive_expect_tx(&ring_full[r.at], it.two ? 2 * kStepBytes : kStepBytes);
+                    bulk_load(to, weights, kStepBytes, &ring_full[r.at]);
+                    if (it.two) bulk_load(to + kStepBytes, weights + (int64_t)nk * kStepBytes, kStepBytes, &ring_full[r.at]);
                 }
                 __syncwarp();
             }
             if (!good) break;
         }
         // no copy may be in flight when the CTA ends, whatever its consumers did
-        for (int i = max(0, filled - kRing); i < filled; ++i) mbar_wait(&ring_full[i % kRing], (i / kRing) & 1);
+        for (int64_t i = max((int64_t)0, filled - ring); i < filled; ++i) wait_phase(&ring_full[i % ring], (i / ring) & 1);
     } else if (warp == kIssuer) {
         // one thread from here to its end: the products' operands then stay in uniform registers
         if (elect_one()) {
-            // runs of 8 channels kRunBytes apart, 8 rows 128 bytes apart, no swizzle
-            const uint64_t desc = (uint64_t)(kRunBytes / 16) << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
+            // runs of 8 channels `run` bytes apart, 8 rows 128 bytes apart, no swizzle
+            const uint32_t run16 = run / 16;
+            const uint64_t desc = (uint64_t)run16 << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
             const uint64_t first_b = desc | (smem_addr(ops) >> 4 & 0x3fff);          // in a cluster, addresses have a rank above
-            int g = 0, committed = 0;
+            int committed = 0;
+            Place g, a, b;
             for (int j = 0;; ++j) {
                 const int slot = j % kItems;
-                good = mbar_wait(&item_full[slot], (j / kItems) & 1);
+                good = wait_phase(&item_full[slot], (j / kItems) & 1);
                 if (!good) break;
                 const int e = items[slot].e, rows = items[slot].rows, two = items[slot].two;
                 mbar_arrive(&item_empty[slot]);
                 if (e < 0) break;
                 const uint32_t cols = (rows + 15) & ~15;           // the products' N: a multiple of 16
                 const uint32_t kind = 1u << 4 | (cols / 8) << 17 | (uint32_t)(kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
-                if (j > 0) good = mbar_wait(&drained, (j - 1) & 1);
-                for (int i = 0; i < steps && good; ++i, ++g) {
-                    const int s = g % kSteps;
-                    good = mbar_wait(&op_full[s], (g / kSteps) & 1);
+                if (j > 0) good = wait_phase(&drained, (j - 1) & 1);
+                for (int i = 0; i < steps && good; ++i, g.next(kSteps), a.next(kA), b.next(kB)) {
+                    good = wait_phase(&op_full[g.at], g.parity);
                     if (!good) break;
                     tcgen05_after();
-                    const uint32_t a = a_at + s % kA * 2 * kAColumns;
-                    const uint64_t b = first_b + (uint32_t)(s % kB * (kBBytes / 16));
+                    const uint32_t from_a = a_at + a.at * 2 * kAColumns;
+                    const uint64_t from_b = first_b + (uint32_t)(b.at * kRuns) * run16;
 #pragma unroll
-                    for (int k = 0; k < kStep / 16; ++k) mma_f16(tmem, a + k * 8, b + k * 2 * (kRunBytes / 16), kind, i > 0 || k > 0);
+                    for (int k = 0; k < kStep / 16; ++k) mma_f16(tmem, from_a + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
                     if (two)
 #pragma unroll
                         for (int k = 0; k < kStep / 16; ++k)
-                            mma_f16(tmem + kTokens, a + kAColumns + k * 8, b + k * 2 * (kRunBytes / 16), kind, i > 0 || k > 0);
-                    tcgen05_commit(&op_done[s]);
+                            mma_f16(tmem + kTokens, from_a + kAColumns + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
+                    tcgen05_commit(&op_done[g.at]);
                 }
                 tcgen05_commit(&done);
                 ++committed;
                 if (!good) break;
             }
             // every product is over before tensor memory is given back
-            if (committed > 0) good = mbar_wait(&done, (committed - 1) & 1) && good;
+            if (committed > 0) good = wait_phase(&done, (committed - 1) & 1) && good;
         }
         __syncwarp();
         good = __all_sync(0xffffffffu, good);
@@ -408,23 +442,22 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         const int t = threadIdx.x - 256, c = t & 7, n0 = t >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
         uint4 raw[kAhead][kTokens / 32];
-        int g = 0, j = 0;
+        int j = 0, made = 0;                     // made: steps, up to kB
+        Place g, b, before;                      // this step's barrier and room; the barrier of the room's last step
         Item last{};
         auto write_out = [&](int item) {
-            good = __all_sync(0xffffffffu, mbar_wait(&done, item & 1));
-            if (!good) return;
+            if (!await(&done, item & 1)) return;
             tcgen05_after();
             if (half == 0 || last.two) {
                 const Writer w(p, last, last.b + half, row);
-                for (int n = 0; n < last.rows; n += 32) {
-                    uint32_t v[32];
-                    const float mine = lane + n < last.rows ? w.row_scale[n + lane] : 0.f;
-                    tmem_load32(tmem + half * kTokens + n + lanes, v);
+                for (int n = 0; n < last.rows; n += 16) {
+                    uint32_t v[16];
+                    const float mine = (lane & 15) + n < last.rows ? w.row_scale[n + (lane & 15)] : 0.f;
+                    tmem_load16(tmem + half * kTokens + n + lanes, v);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        if (n + i < last.rows)
-                            w.put(n + i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]),
-                                  [&](int r) { return __shfl_sync(0xffffffffu, mine, r - n); });
+                    for (int i = 0; i < 16; i += 2)
+                        w.put(n + i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                              [&](int r) { return __shfl_sync(0xffffffffu, mine, r - n); });
                 }
             }
             tcgen05_before();
@@ -435,12 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
             const int8_t* x = p.x + (int64_t)it.first * p.w.K + (int64_t)k0 * kStep + c * 16;
             const int left = p.w.K - k0 * kStep - c * 16;          // channels from the thread's on
             auto fetch = [&](uint4 (&r)[kTokens / 32], int step) {
+                const bool in = step < steps && step * kStep < left;
 #pragma unroll
                 for (int i = 0; i < kTokens / 32; ++i) {
                     const int n = n0 + 32 * i;
                     r[i] = make_uint4(0, 0, 0, 0);                 // channels past the end
-                    if (n < it.rows && step < steps && step * kStep < left)
-                        r[i] = *reinterpret_cast<const uint4*>(x + (int64_t)n * p.w.K + step * kStep);
+                    if (n < it.rows && in) r[i] = *reinterpret_cast<const uint4*>(x + (uint32_t)n * (uint32_t)p.w.K + (uint32_t)(step * kStep));
                 }
             };
 #pragma unroll
@@ -450,13 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                 for (int u = 0; u < kAhead; ++u) {
                     const int i = base + u;
                     if (i >= steps || !good) break;
-                    // the products can go on with the steps made so far while the sums before are written out
-                    if (i == kB && j > 0 && splits == 1) {
+                    // the next item's first steps are made while the products of this one end; then its sums are written out
+                    if (i == kB - 1 && j > 0 && splits == 1) {
                         write_out(j - 1);
                         if (!good) break;
                     }
-                    if (g >= kB && !step_done(g - kB)) break;
-                    unsigned char* to = ops + g % kB * kBBytes + c * kRunBytes;
+                    if (made < kB) {
+                        ++made;
+                    } else {
+                        if (!await(&op_done[before.at], before.parity)) break;
+                        before.next(kSteps);
+                    }
+                    unsigned char* to = ops + b.at * b_bytes + c * run;
 #pragma unroll
                     for (int m = 0; m < kTokens / 32; ++m) {
                         const int n = n0 + 32 * m;
@@ -467,18 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                             widen(raw[u][m].z ^ 0x80808080u, &hi.x, &hi.y);
                             widen(raw[u][m].w ^ 0x80808080u, &hi.z, &hi.w);
                             *reinterpret_cast<uint4*>(to + n * 16) = lo;
-                            *reinterpret_cast<uint4*>(to + 8 * kRunBytes + n * 16) = hi;
+                            *reinterpret_cast<uint4*>(to + 8 * run + n * 16) = hi;
                         }
                     }
                     fetch(raw[u], i + kAhead);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&op_full[g % kSteps]);
-                    ++g;
+                    if (lane == 0) mbar_arrive(&op_full[g.at]);
+                    g.next(kSteps);
+                    b.next(kB);
                 }
             }
             if (!good) break;
-            if (j > 0 && splits == 1 && steps <= kB) write_out(j - 1);
+            if (j > 0 && splits == 1 && steps < kB) write_out(j - 1);
             if (!good) break;
             last = it;
         }
@@ -489,18 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         // weights: a thread has one row of one block
         const int half = warp >> 2;
         const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        int g = 0;
+        int made = 0;
+        Place g, a, r, before;
         for (int j = 0; next_item(j, &it); ++j) {
             const bool here = half == 0 || it.two;
-            for (int i = 0; i < steps; ++i, ++g) {
-                const int r = g % kRing;
-                if (!__all_sync(0xffffffffu, mbar_wait(&ring_full[r], (g / kRing) & 1))) {
-                    good = false;
-                    break;
-                }
+            for (int i = 0; i < steps; ++i) {
+                if (!await(&ring_full[r.at], r.parity)) break;
                 uint32_t v[2][32];
                 if (here) {
-                    const unsigned char* from = smem + (r * 2 + half) * kStepBytes + (threadIdx.x & 127) * 16;
+                    const unsigned char* from = smem + (r.at * 2 + half) * kStepBytes + (threadIdx.x & 127) * 16;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const uint4 raw = *reinterpret_cast<const uint4*>(from + q * kRows * 16);
@@ -512,18 +548,26 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ring_empty[r]);
-                if (g >= kA && !step_done(g - kA)) break;
+                if (lane == 0) mbar_arrive(&ring_empty[r.at]);
+                if (made < kA) {
+                    ++made;
+                } else {
+                    if (!await(&op_done[before.at], before.parity)) break;
+                    before.next(kSteps);
+                }
                 if (here) {
                     tcgen05_after();
-                    const uint32_t to = a_at + (g % kA * 2 + half) * kAColumns + lanes;
+                    const uint32_t to = a_at + (a.at * 2 + half) * kAColumns + lanes;
                     tmem_store32(to, v[0]);
                     tmem_store32(to + 32, v[1]);
                     tmem_store_wait();
                     tcgen05_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&op_full[g % kSteps]);
+                if (lane == 0) mbar_arrive(&op_full[g.at]);
+                g.next(kSteps);
+                a.next(kA);
+                r.next(ring);
             }
             if (!good) break;
         }
@@ -540,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int 
         const int own = (it.rows + splits - 1) / splits;
         if (writes && good) {
             tcgen05_after();
-            for (int n = 0; n < it.rows; n += 32) {
-                uint32_t v[32];
-                tmem_load32(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
+            for (int n = 0; n < it.rows; n += 16) {
+                uint32_t v[16];
+                tmem_load16(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < 16; ++i)
                     if (n + i < it.rows) {
                         const int owner = (n + i) / own;
                         const uint32_t to = in_cta(smem_addr(parts + ((split * own + n + i - owner * own) * 2 + half) * kRows + row), owner);
@@ -597,7 +641,9 @@ cudaError_t launch_i8_pack(const I8Shape& w, const int8_t* codes, const float* s
 
 cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream) {
     const int pairs = (row_blocks(p.w) + 1) / 2;
+    // Tiles of twice the mean: the smaller the tile, the longer the ring.
     int tile = kTokens, splits = 1;
+    while (tile > 32 && p.max_rows * 4 <= (int64_t)p.w.E * tile) tile /= 2;
     while (tile > 32 && most_tiles(p.w.E, p.max_rows, tile) * pairs * 2 <= num_sms) tile /= 2;
     const int64_t most = most_tiles(p.w.E, p.max_rows, tile) * pairs;
     while (splits < 8 && most * splits * 2 <= num_sms && k_steps(p.w) >= splits * 4) splits *= 2;
