@@ -9,8 +9,8 @@
 // item (two blocks with one tile of token rows).  A warp finds the items; a
 // producer warp keeps a ring of weight codes filled by bulk copies; eight warps
 // widen them into tensor memory, a row to a thread, which is the instruction's A
-// operand; eight more load token codes and widen them into shared memory (B), and
-// write the sums out; one thread issues the products.
+// operand; eight more load token codes, several steps ahead, and widen them into
+// shared memory (B), and write the sums out; one thread issues the products.
 #include <algorithm>
 
 #include "ep.h"
@@ -30,11 +30,11 @@ constexpr int kA = 2;              // steps whose weights are widened ahead
 constexpr int kB = 3;              // steps whose tokens are
 constexpr int kSteps = 6;          // barriers of steps under way: a multiple of both
 constexpr int kItems = 4;          // items found ahead
-constexpr int kAhead = 2;          // steps whose token codes are on their way
-// warps: 8 of weights, 8 of tokens, the producer, the issuer, the one that finds items
-constexpr int kProducer = 16, kIssuer = 17, kFinder = 18;
-constexpr int kThreads = 19 * 32;
-constexpr int kItemReaders = 18;
+constexpr int kPause = 2;          // steps made before the sums of the item before are written out: fewer than kB, whole rounds of loads
+constexpr int kWeightWarps = 8, kTokenWarps = 8;
+constexpr int kProducer = kWeightWarps + kTokenWarps, kIssuer = kProducer + 1, kFinder = kProducer + 2;
+constexpr int kThreads = (kFinder + 1) * 32;
+constexpr int kItemReaders = kFinder;
 constexpr uint32_t kColumns = 512;                // tensor memory: the two blocks' sums, then kA x 2 A operands
 constexpr int kAColumns = kStep / 2;
 
@@ -155,11 +155,13 @@ __device__ __forceinline__ void widen(uint32_t biased, uint32_t* lo, uint32_t* h
 // 16 bytes more keep the runs that eight lanes write at once in different banks.
 // What shared memory is left holds the ring of weight codes.
 constexpr int kRuns = kStep / 8;
-constexpr int kSmemBytes = 208 * 1024;
+constexpr int kControlBytes = 13 * 1024;         // barriers, items and the table of experts
+constexpr int kSmemBytes = 212 * 1024;           // the rest
+constexpr int kRingBytes = 2 * kStepBytes;       // of a step
 
 __host__ __device__ constexpr int run_bytes(int tile_rows) { return (tile_rows + 1) * 16; }
 __host__ __device__ constexpr int ring_steps(int tile_rows) {
-    const int fit = (kSmemBytes - kB * kRuns * run_bytes(tile_rows)) / (2 * kStepBytes);
+    const int fit = (kSmemBytes - kB * kRuns * run_bytes(tile_rows)) / kRingBytes;
     return fit < kMaxRing ? fit : kMaxRing;
 }
 static_assert(ring_steps(kTokens) >= 3, "the widest tile leaves too little for the ring");
@@ -227,9 +229,9 @@ __device__ __forceinline__ int tile_rows_of(int n, int tile) {
 // The sums of a weight row to a lane, scaled, paired and stored.
 struct Writer {
     uint16_t* y;             // at the lane's channel of the tile's first row (the upper lanes' of a pair: of the second)
-    const float* row_scale;  // of the tile's first row
     float scale;
-    int N, rows;
+    int64_t N;
+    int rows;
     bool paired, stores;
 
     __device__ __forceinline__ Writer(const I8Params& p, const Item& it, int b, int row) {
@@ -239,18 +241,16 @@ struct Writer {
         N = p.w.N;
         paired = p.w.paired;
         y = static_cast<uint16_t*>(p.y) + (int64_t)it.first * N + c + (paired && (threadIdx.x & 16) ? N : 0);
-        row_scale = p.x_scales + it.first;
         rows = it.rows;
         stores = c < N;
     }
 
-    // Token rows n and n + 1.  xs(r): the scale of row r (r = n or n + 1 in a lane).  Of a pair, the lower
-    // lanes have the gates and finish row n, the upper ones have the ups and finish row n + 1.
+    // Token rows n and n + 1 to `to` (y of row n).  xs(r): the scale of row r (r = n or n + 1 in a lane).  Of a pair, the
+    // lower lanes have the gates and finish row n, the upper ones have the ups and finish row n + 1.
     template <typename Scale>
-    __device__ __forceinline__ void put(int n, float s0, float s1, Scale xs) const {
+    __device__ __forceinline__ void put(int n, uint16_t* to, float s0, float s1, Scale xs) const {
         const bool upper = threadIdx.x & 16;
         const float a = s0 * scale, b = s1 * scale;
-        uint16_t* to = y + (int64_t)n * N;
         if (paired) {
             const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
             const int r = n + upper;
@@ -265,358 +265,433 @@ struct Writer {
     }
 };
 
-// items: a grid of clusters of `splits` CTAs takes them a grid apart; with more
-// than one share of K (which a launch of few products has) a cluster takes one.
-__global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(I8Params p, int splits, int tile_rows) {
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t ring_full[kMaxRing], ring_empty[kMaxRing], op_full[kSteps], op_done[kSteps], item_full[kItems], item_empty[kItems];
-    __shared__ uint64_t done, drained;
-    __shared__ uint32_t tmem_at;
-    __shared__ Item items[kItems];
-    __shared__ int table_first[EP_MAX_EXPERTS], table_rows[EP_MAX_EXPERTS], table_upto[EP_MAX_EXPERTS];
+// What the warps share beside the rings, at the start of shared memory.
+struct Control {
+    uint64_t ring_full[kMaxRing], ring_empty[kMaxRing], op_full[kSteps], op_done[kSteps];
+    uint64_t item_full[kItems], item_empty[kItems], done, drained;
+    Item items[kItems];
+    uint32_t tmem;
+    int first[EP_MAX_EXPERTS], rows[EP_MAX_EXPERTS], upto[EP_MAX_EXPERTS];       // of each expert; tiles up to and with it
+};
+
+static_assert(sizeof(Control) <= kControlBytes, "the shared state has outgrown its room");
+
+extern __shared__ __align__(128) unsigned char smem[];
+
+__device__ __forceinline__ Control& control() { return *reinterpret_cast<Control*>(smem); }
+__device__ __forceinline__ unsigned char* ring_base() { return smem + kControlBytes; }
+
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_phase(bar, parity)); }
+
+// Item j of the CTA, for a whole warp.  False if a wait ran out.
+__device__ __forceinline__ bool next_item(int j, Item* it) {
+    Control& c = control();
+    const int slot = j % kItems;
+    if (!await(&c.item_full[slot], (j / kItems) & 1)) return false;
+    *it = c.items[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&c.item_empty[slot]);
+    return true;
+}
+
+// The roles.  Each is a function of its own, so that what one keeps in registers
+// costs the others none: with all of shared memory in use there is next to no L1,
+// and a value that is spilled comes back from L2.  A role returns false if a wait
+// ran out.
+
+// Finds the items: item j of cluster c is number c + j * clusters in the order of
+// experts, tiles and blocks.
+__device__ __noinline__ bool find_items(int E, int nb, int tile_rows, int cluster, int clusters, bool one, uint32_t* err_flags) {
+    Control& c = control();
+    const int lane = threadIdx.x & 31;
+    // lane l adds up the tiles of experts [l * per, (l + 1) * per)
+    const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+    int mine = 0;
+    for (int e = e0; e < e1; ++e) {
+        mine = min(mine + (c.rows[e] + tile_rows - 1) / tile_rows, 1 << 25);      // bad offsets may claim rows many times
+        c.upto[e] = mine;
+    }
+    int total = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, total, d);
+        if (lane >= d) total += v;
+    }
+    const int before = total - mine;
+    total = __shfl_sync(0xffffffffu, total, 31);
+    for (int e = e0; e < e1; ++e) c.upto[e] += before;
+    __syncwarp();
+    const int pairs = (nb + 1) / 2;
+    const int64_t all = (int64_t)total * pairs, most = one ? min(all, (int64_t)clusters) : all;
+    if (most < all && cluster == 0 && lane == 0 && err_flags != nullptr) atomicOr(err_flags, kErrCapacity);
+    for (int j = 0;; ++j) {
+        const int slot = j % kItems;
+        const int64_t at = cluster + (int64_t)j * clusters;
+        if (j >= kItems && !await(&c.item_empty[slot], (j / kItems - 1) & 1)) return false;
+        Item it{-1, 0, 0, 0, 0};
+        if (at < most) {
+            const int tile = (int)(at / pairs);
+            int lo = 0, hi = E - 1;                    // the first expert with upto > tile
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (c.upto[mid] > tile)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            const int n = c.rows[lo], size = tile_rows_of(n, tile_rows), from = (tile - (lo > 0 ? c.upto[lo - 1] : 0)) * size;
+            const int b = (int)(at - (int64_t)tile * pairs) * 2;
+            it = Item{lo, min(size, n - from), c.first[lo] + from, b, b + 1 < nb};
+        }
+        if (lane == 0) {
+            c.items[slot] = it;
+            mbar_arrive(&c.item_full[slot]);
+        }
+        __syncwarp();
+        if (it.e < 0) return true;
+    }
+}
+
+// Keeps the ring of codes filled.
+__device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk, int k0, int steps, int tile_rows) {
+    Control& c = control();
+    const int lane = threadIdx.x & 31, ring = ring_steps(tile_rows);
+    int64_t filled = 0;
+    bool good = true;
+    Item it;
+    Place r{0, 1};                           // the parity of the place's previous use
+    for (int j = 0; good; ++j) {
+        good = next_item(j, &it);
+        if (!good || it.e < 0) break;
+        const unsigned char* weights = packed + (((int64_t)it.e * nb + it.b) * nk + k0) * kStepBytes;
+        for (int i = 0; i < steps; ++i, ++filled, weights += kStepBytes, r.next(ring)) {
+            if (filled >= ring) good = await(&c.ring_empty[r.at], r.parity);
+            if (!good) break;
+            if (lane == 0) {
+                unsigned char* to = ring_base() + r.at * kRingBytes;
+                uint64_t* bar = &c.ring_full[r.at];
+                mbar_arrive_expect_tx(bar, it.two ? kRingBytes : kStepBytes);
+                bulk_load(to, weights, kStepBytes, bar);
+                if (it.two) bulk_load(to + kStepBytes, weights + (int64_t)nk * kStepBytes, kStepBytes, bar);
+            }
+            __syncwarp();
+        }
+    }
+    // no copy may be in flight when the CTA ends, whatever its consumers did
+    for (int64_t i = max((int64_t)0, filled - ring); i < filled; ++i) wait_phase(&c.ring_full[i % ring], (i / ring) & 1);
+    return good;
+}
+
+// Issues the products.  One thread: their operands then stay in uniform registers.
+__device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows) {
+    Control& c = control();
+    const uint32_t a_at = tmem + 2 * kTokens, run16 = run_bytes(tile_rows) / 16;
+    // runs of 8 channels run16 * 16 bytes apart, 8 rows 128 bytes apart, no swizzle
+    const uint64_t desc = (uint64_t)run16 << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
+    const unsigned char* ops = ring_base() + ring_steps(tile_rows) * kRingBytes;
+    const uint64_t first_b = desc | (smem_addr(ops) >> 4 & 0x3fff);          // in a cluster, addresses have a rank above
+    int committed = 0;
+    bool good = true;
+    Place g, a, b;
+    for (int j = 0; good; ++j) {
+        const int slot = j % kItems;
+        good = wait_phase(&c.item_full[slot], (j / kItems) & 1);
+        if (!good) break;
+        const int e = c.items[slot].e, rows = c.items[slot].rows, two = c.items[slot].two;
+        mbar_arrive(&c.item_empty[slot]);
+        if (e < 0) break;
+        const uint32_t cols = (rows + 15) & ~15;           // the products' N: a multiple of 16
+        const uint32_t kind = 1u << 4 | (cols / 8) << 17 | (uint32_t)(kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
+        if (j > 0) good = wait_phase(&c.drained, (j - 1) & 1);
+        for (int i = 0; i < steps && good; ++i, g.next(kSteps), a.next(kA), b.next(kB)) {
+            const uint32_t from_a = a_at + a.at * 2 * kAColumns;
+            const uint64_t from_b = first_b + (uint32_t)(b.at * kRuns) * run16;
+            good = wait_phase(&c.op_full[g.at], g.parity);
+            if (!good) break;
+            tcgen05_after();
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k) mma_f16(tmem, from_a + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
+            if (two)
+#pragma unroll
+                for (int k = 0; k < kStep / 16; ++k)
+                    mma_f16(tmem + kTokens, from_a + kAColumns + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
+            tcgen05_commit(&c.op_done[g.at]);
+        }
+        tcgen05_commit(&c.done);
+        ++committed;
+    }
+    // every product is over before tensor memory is given back
+    if (committed > 0) good = wait_phase(&c.done, (committed - 1) & 1) && good;
+    return good;
+}
+
+// An item's sums, out of tensor memory: a row of a block to a lane.  A call apart:
+// it needs the registers that hold the token codes that are on their way.
+template <int CHUNKS>
+__device__ __noinline__ bool write_sums(const I8Params& p, const Item it, uint32_t sums, int half, int row, uint32_t parity) {
+    Control& c = control();
+    const int lane = threadIdx.x & 31;
+    const bool here = half == 0 || it.two;
+    const Writer w(p, it, it.b + (here ? half : 0), row);
+    float xs[CHUNKS];
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) xs[k] = lane + 32 * k < it.rows ? p.x_scales[it.first + lane + 32 * k] : 0.f;
+    if (!await(&c.done, parity)) return false;
+    tcgen05_after();
+    if (here) {
+        uint16_t* y = w.y;
+        // not unrolled further: addresses made ahead would not fit the registers
+#pragma unroll 1
+        for (int n = 0; n < it.rows; n += 16) {
+            uint32_t v[16];
+            tmem_load16(sums + n, v);
+            float mine = xs[0];
+#pragma unroll
+            for (int k = 1; k < CHUNKS; ++k) mine = n >= 32 * k ? xs[k] : mine;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2, y += 2 * w.N)
+                w.put(n + i, y, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), [&](int r) { return __shfl_sync(0xffffffffu, mine, r); });
+        }
+    }
+    tcgen05_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.drained);
+    return true;
+}
+
+// Tokens: a thread has 16 channels of every 32nd row, of up to 32 CHUNKS, and loads
+// them AHEAD steps ahead: with HBM busy an L2 hit takes some 1700 cycles, longer
+// than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).  The
+// same warps write the sums out (where `whole` is set: K is not shared).
+template <int CHUNKS, int AHEAD>
+__device__ __noinline__ bool widen_tokens(const I8Params& params, uint32_t tmem, int k0, int steps, int tile_rows, bool whole) {
+    Control& c = control();
+    const I8Params& p = params;
+    const int K = p.w.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, run = run_bytes(tile_rows);
+    const int t = threadIdx.x - kWeightWarps * 32, n0 = t >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+    const uint32_t sums = tmem + half * kTokens + ((uint32_t)(warp & 3) * 32 << 16);
+    unsigned char* ops = ring_base() + ring_steps(tile_rows) * kRingBytes + (t & 7) * run + n0 * 16;
+    const int8_t* first_x = p.x + (int64_t)k0 * kStep + (t & 7) * 16;
+    const int left = K - k0 * kStep - (t & 7) * 16;            // channels from the thread's on
+    int made = 0;                            // steps, up to kB
+    Item it, last{};
+    Place g, b, before;                      // this step's barrier and room; the barrier of the room's last step
+    uint4 raw[AHEAD][CHUNKS];
+    for (int j = 0;; ++j) {
+        if (!next_item(j, &it)) return false;
+        const int count = it.e >= 0 ? steps : 0;               // the end comes as an item without steps
+        static_assert(kPause % AHEAD == 0 && kPause < kB, "");
+        bool pending = j > 0 && whole;                         // the sums of the item before
+        const int8_t* x = first_x + ((int64_t)it.first + n0) * K;
+        auto fetch = [&](uint4 (&r)[CHUNKS], int step) {
+            const bool in = step < count && step * kStep < left;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                r[i] = make_uint4(0, 0, 0, 0);                 // channels past the end
+                if (n0 + 32 * i < it.rows && in) r[i] = *reinterpret_cast<const uint4*>(x + (uint32_t)(32 * i) * (uint32_t)K + (uint32_t)(step * kStep));
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) fetch(raw[u], u);
+        for (int base = 0;; base += AHEAD) {
+            // the item's first steps are made while the products of the one before end; then the sums of that are written out
+            if (pending && base >= min(kPause, count)) {
+                pending = false;
+                if (!write_sums<CHUNKS>(p, last, sums, half, row, (j - 1) & 1)) return false;
+            }
+            if (base >= count) break;
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int i = base + u;
+                if (i >= count) break;
+                if (made < kB) {
+                    ++made;
+                } else {
+                    if (!await(&c.op_done[before.at], before.parity)) return false;
+                    before.next(kSteps);
+                }
+                unsigned char* to = ops + b.at * kRuns * run;
+#pragma unroll
+                for (int m = 0; m < CHUNKS; ++m) {
+                    if (n0 + 32 * m < it.rows) {
+                        uint4 lo, hi;
+                        widen(raw[u][m].x ^ 0x80808080u, &lo.x, &lo.y);
+                        widen(raw[u][m].y ^ 0x80808080u, &lo.z, &lo.w);
+                        widen(raw[u][m].z ^ 0x80808080u, &hi.x, &hi.y);
+                        widen(raw[u][m].w ^ 0x80808080u, &hi.z, &hi.w);
+                        *reinterpret_cast<uint4*>(to + 32 * m * 16) = lo;
+                        *reinterpret_cast<uint4*>(to + 8 * run + 32 * m * 16) = hi;
+                    }
+                }
+                fetch(raw[u], i + AHEAD);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.op_full[g.at]);
+                g.next(kSteps);
+                b.next(kB);
+            }
+        }
+        if (it.e < 0) return true;
+        last = it;
+    }
+}
+
+// Weights: a thread has one row of one block.
+__device__ __noinline__ bool widen_weights(uint32_t tmem, int steps, int tile_rows) {
+    Control& c = control();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, ring = ring_steps(tile_rows);
+    const uint32_t to = tmem + 2 * kTokens + half * kAColumns + ((uint32_t)(warp & 3) * 32 << 16);
+    const unsigned char* from = ring_base() + half * kStepBytes + (threadIdx.x & 127) * 16;
+    int made = 0;
+    Item it;
+    Place g, a, r, before;                   // the step's barrier, its room, the ring's; the barrier of the room's last step
+    for (int j = 0;; ++j) {
+        if (!next_item(j, &it)) return false;
+        if (it.e < 0) return true;
+        const bool here = half == 0 || it.two;
+        for (int i = 0; i < steps; ++i) {
+            if (!await(&c.ring_full[r.at], r.parity)) return false;
+            uint32_t v[2][32];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(from + r.at * kRingBytes + q * kRows * 16);
+                uint32_t* w = &v[q >> 2][(q & 3) * 8];
+                widen(raw.x, w, w + 1);
+                widen(raw.y, w + 2, w + 3);
+                widen(raw.z, w + 4, w + 5);
+                widen(raw.w, w + 6, w + 7);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.ring_empty[r.at]);
+            r.next(ring);
+            if (made < kA) {
+                ++made;
+            } else {
+                if (!await(&c.op_done[before.at], before.parity)) return false;
+                before.next(kSteps);
+            }
+            tcgen05_after();
+            if (here) {
+                tmem_store32(to + a.at * 2 * kAColumns, v[0]);
+                tmem_store32(to + a.at * 2 * kAColumns + 32, v[1]);
+                tmem_store_wait();
+            }
+            tcgen05_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.op_full[g.at]);
+            g.next(kSteps);
+            a.next(kA);
+        }
+    }
+}
+
+// The sums of an item whose K a cluster shares: each CTA owns some of the tile's
+// token rows, whose sums the others push to it.  All threads of the cluster; it.e
+// is -1 where there is none.
+__device__ __noinline__ void join_shares(const I8Params& params, const Item it, uint32_t tmem, int split, int splits, bool good) {
+    cluster_barrier();                       // the rings are free
+    const I8Params p = params;
+    float* parts = reinterpret_cast<float*>(ring_base());          // [share][own][block][weight row]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+    const bool writes = good && warp >= kWeightWarps && warp < kProducer && it.e >= 0 && (half == 0 || it.two);
+    const int own = (it.rows + splits - 1) / splits;
+    if (writes) {
+        tcgen05_after();
+        for (int n = 0; n < it.rows; n += 16) {
+            uint32_t v[16];
+            tmem_load16(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (n + i < it.rows) {
+                    const int owner = (n + i) / own;
+                    const uint32_t to = in_cta(smem_addr(parts + ((split * own + n + i - owner * own) * 2 + half) * kRows + row), owner);
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(v[i]) : "memory");
+                }
+        }
+        tcgen05_before();
+    }
+    __syncwarp();
+    cluster_barrier();
+    if (writes) {
+        Writer w(p, it, it.b + half, row);
+        w.rows = min(it.rows, (split + 1) * own);              // the rows after them are another's
+        for (int n = split * own; n < w.rows; n += 2) {
+            float sum[2] = {0.f, 0.f};
+            for (int q = 0; q < splits; ++q)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (n + i < w.rows) sum[i] += parts[((q * own + n + i - split * own) * 2 + half) * kRows + row];
+            w.put(n, w.y + (int64_t)n * w.N, sum[0], sum[1], [&](int r) { return r < w.rows ? p.x_scales[it.first + r] : 0.f; });
+        }
+    }
+}
+
+// A grid of clusters of `splits` CTAs takes the items a grid apart; with more than
+// one share of K (which a launch of few products has) a cluster takes one.
+__global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_constant__ I8Params p, int splits, int tile_rows) {
+    Control& c = control();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % splits, cluster = blockIdx.x / splits, clusters = gridDim.x / splits;
-    const int nb = row_blocks(p.w), nk = k_steps(p.w);
+    const int split = blockIdx.x % splits, cluster = blockIdx.x / splits, nb = row_blocks(p.w), nk = k_steps(p.w);
     const int k0 = (int)((int64_t)nk * split / splits), steps = (int)((int64_t)nk * (split + 1) / splits) - k0;
-    const int ring = ring_steps(tile_rows), run = run_bytes(tile_rows), b_bytes = kRuns * run;
-    unsigned char* ops = smem + ring * 2 * kStepBytes;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < ring; ++i) {
-            mbar_init(&ring_full[i], 1);
-            mbar_init(&ring_empty[i], 8);
+        for (int i = 0; i < kMaxRing; ++i) {
+            mbar_init(&c.ring_full[i], 1);
+            mbar_init(&c.ring_empty[i], kWeightWarps);
         }
         for (int i = 0; i < kSteps; ++i) {
-            mbar_init(&op_full[i], 16);
-            mbar_init(&op_done[i], 1);
+            mbar_init(&c.op_full[i], kWeightWarps + kTokenWarps);
+            mbar_init(&c.op_done[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
-            mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], kItemReaders);
+            mbar_init(&c.item_full[i], 1);
+            mbar_init(&c.item_empty[i], kItemReaders);
         }
-        mbar_init(&done, 1);
-        mbar_init(&drained, 8);
+        mbar_init(&c.done, 1);
+        mbar_init(&c.drained, kTokenWarps);
         fence_mbar_init();
+    }
+    // a share may push to another once that runs
+    if (splits > 1) {
+        __syncwarp();
+        cluster_barrier();
     }
     pdl_wait();
     // not before the wait: a CTA that holds tensor memory must not wait for one that may need it
-    if (warp == kIssuer) tmem_alloc(&tmem_at, kColumns);
+    if (warp == kIssuer) tmem_alloc(&c.tmem, kColumns);
     for (int e = threadIdx.x; e < p.w.E; e += kThreads) {
         int64_t first;
         bool bad;
-        table_rows[e] = expert_rows(p, e, &first, &bad);
-        table_first[e] = (int)first;
+        c.rows[e] = expert_rows(p, e, &first, &bad);
+        c.first[e] = (int)first;
         if (bad && blockIdx.x == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrBadSlot);
     }
     tcgen05_before();
     __syncthreads();
     tcgen05_after();
-    const uint32_t tmem = tmem_at, a_at = tmem + 2 * kTokens;
     bool good = true;
-    auto await = [&](uint64_t* bar, uint32_t parity) {
-        good = __all_sync(0xffffffffu, wait_phase(bar, parity));
-        return good;
-    };
-    auto next_item = [&](int j, Item* it) {
-        const int slot = j % kItems;
-        if (!await(&item_full[slot], (j / kItems) & 1)) return false;
-        *it = items[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&item_empty[slot]);
-        return it->e >= 0;
-    };
-    Item it;
     if (warp == kFinder) {
-        // tiles up to and with each expert: lane l adds up those of experts [l * per, (l + 1) * per)
-        const int per = (p.w.E + 31) / 32, e0 = min(lane * per, p.w.E), e1 = min(e0 + per, p.w.E);
-        int mine = 0;
-        for (int e = e0; e < e1; ++e) {
-            mine = min(mine + (table_rows[e] + tile_rows - 1) / tile_rows, 1 << 25);      // bad offsets may claim rows many times
-            table_upto[e] = mine;
-        }
-        int before = 0, total = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, total, d);
-            if (lane >= d) total += v;
-        }
-        before = total - mine;
-        total = __shfl_sync(0xffffffffu, total, 31);
-        for (int e = e0; e < e1; ++e) table_upto[e] += before;
-        __syncwarp();
-        const int pairs = (nb + 1) / 2;
-        const int64_t all_items = (int64_t)total * pairs, most = splits > 1 ? min(all_items, (int64_t)clusters) : all_items;
-        if (most < all_items && blockIdx.x == 0 && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrCapacity);
-        for (int j = 0;; ++j) {
-            const int slot = j % kItems;
-            const int64_t at = cluster + (int64_t)j * clusters;
-            if (j >= kItems && !await(&item_empty[slot], (j / kItems - 1) & 1)) break;
-            it.e = -1;
-            if (at < most) {
-                const int tile = (int)(at / pairs);
-                int lo = 0, hi = p.w.E - 1;                    // the first expert with upto > tile
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (table_upto[mid] > tile)
-                        hi = mid;
-                    else
-                        lo = mid + 1;
-                }
-                const int n = table_rows[lo], size = tile_rows_of(n, tile_rows), from = (tile - (lo > 0 ? table_upto[lo - 1] : 0)) * size;
-                it.e = lo;
-                it.rows = min(size, n - from);
-                it.first = table_first[lo] + from;
-                it.b = (int)(at - (int64_t)tile * pairs) * 2;
-                it.two = it.b + 1 < nb;
-            }
-            if (lane == 0) {
-                items[slot] = it;
-                mbar_arrive(&item_full[slot]);
-            }
-            __syncwarp();
-            if (it.e < 0) break;
-        }
+        good = find_items(p.w.E, nb, tile_rows, cluster, gridDim.x / splits, splits > 1, p.err_flags);
     } else if (warp == kProducer) {
-        int64_t filled = 0;
-        Place r{0, 1};                           // the parity of the place's previous use
-        for (int j = 0; next_item(j, &it); ++j) {
-            const unsigned char* weights = static_cast<const unsigned char*>(p.packed) + (((int64_t)it.e * nb + it.b) * nk + k0) * kStepBytes;
-            for (int i = 0; i < steps; ++i, ++filled, weights += kStepBytes, r.next(ring)) {
-                if (filled >= ring && !await(&ring_empty[r.at], r.parity)) break;
-                if (lane == 0) {
-                    unsigned char* to = smem + r.at * 2 * kStepBytes;
-                    mbar_arrive_expect_tx(&ring_full[r.at], it.two ? 2 * kStepBytes : kStepBytes);
-                    bulk_load(to, weights, kStepBytes, &ring_full[r.at]);
-                    if (it.two) bulk_load(to + kStepBytes, weights + (int64_t)nk * kStepBytes, kStepBytes, &ring_full[r.at]);
-                }
-                __syncwarp();
-            }
-            if (!good) break;
-        }
-        // no copy may be in flight when the CTA ends, whatever its consumers did
-        for (int64_t i = max((int64_t)0, filled - ring); i < filled; ++i) wait_phase(&ring_full[i % ring], (i / ring) & 1);
+        good = produce(static_cast<const unsigned char*>(p.packed), nb, nk, k0, steps, tile_rows);
     } else if (warp == kIssuer) {
-        // one thread from here to its end: the products' operands then stay in uniform registers
-        if (elect_one()) {
-            // runs of 8 channels `run` bytes apart, 8 rows 128 bytes apart, no swizzle
-            const uint32_t run16 = run / 16;
-            const uint64_t desc = (uint64_t)run16 << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
-            const uint64_t first_b = desc | (smem_addr(ops) >> 4 & 0x3fff);          // in a cluster, addresses have a rank above
-            int committed = 0;
-            Place g, a, b;
-            for (int j = 0;; ++j) {
-                const int slot = j % kItems;
-                good = wait_phase(&item_full[slot], (j / kItems) & 1);
-                if (!good) break;
-                const int e = items[slot].e, rows = items[slot].rows, two = items[slot].two;
-                mbar_arrive(&item_empty[slot]);
-                if (e < 0) break;
-                const uint32_t cols = (rows + 15) & ~15;           // the products' N: a multiple of 16
-                const uint32_t kind = 1u << 4 | (cols / 8) << 17 | (uint32_t)(kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
-                if (j > 0) good = wait_phase(&drained, (j - 1) & 1);
-                for (int i = 0; i < steps && good; ++i, g.next(kSteps), a.next(kA), b.next(kB)) {
-                    good = wait_phase(&op_full[g.at], g.parity);
-                    if (!good) break;
-                    tcgen05_after();
-                    const uint32_t from_a = a_at + a.at * 2 * kAColumns;
-                    const uint64_t from_b = first_b + (uint32_t)(b.at * kRuns) * run16;
-#pragma unroll
-                    for (int k = 0; k < kStep / 16; ++k) mma_f16(tmem, from_a + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
-                    if (two)
-#pragma unroll
-                        for (int k = 0; k < kStep / 16; ++k)
-                            mma_f16(tmem + kTokens, from_a + kAColumns + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
-                    tcgen05_commit(&op_done[g.at]);
-                }
-                tcgen05_commit(&done);
-                ++committed;
-                if (!good) break;
-            }
-            // every product is over before tensor memory is given back
-            if (committed > 0) good = wait_phase(&done, (committed - 1) & 1) && good;
-        }
-        __syncwarp();
-        good = __all_sync(0xffffffffu, good);
-    } else if (warp >= 8) {
-        // tokens: a thread has 16 channels of every 32nd row
-        const int t = threadIdx.x - 256, c = t & 7, n0 = t >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        uint4 raw[kAhead][kTokens / 32];
-        int j = 0, made = 0;                     // made: steps, up to kB
-        Place g, b, before;                      // this step's barrier and room; the barrier of the room's last step
-        Item last{};
-        auto write_out = [&](int item) {
-            if (!await(&done, item & 1)) return;
-            tcgen05_after();
-            if (half == 0 || last.two) {
-                const Writer w(p, last, last.b + half, row);
-                for (int n = 0; n < last.rows; n += 16) {
-                    uint32_t v[16];
-                    const float mine = (lane & 15) + n < last.rows ? w.row_scale[n + (lane & 15)] : 0.f;
-                    tmem_load16(tmem + half * kTokens + n + lanes, v);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        w.put(n + i, __uint_as_float(v[i]), __uint_as_float(v[i + 1]),
-                              [&](int r) { return __shfl_sync(0xffffffffu, mine, r - n); });
-                }
-            }
-            tcgen05_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&drained);
-        };
-        for (; next_item(j, &it); ++j) {
-            const int8_t* x = p.x + (int64_t)it.first * p.w.K + (int64_t)k0 * kStep + c * 16;
-            const int left = p.w.K - k0 * kStep - c * 16;          // channels from the thread's on
-            auto fetch = [&](uint4 (&r)[kTokens / 32], int step) {
-                const bool in = step < steps && step * kStep < left;
-#pragma unroll
-                for (int i = 0; i < kTokens / 32; ++i) {
-                    const int n = n0 + 32 * i;
-                    r[i] = make_uint4(0, 0, 0, 0);                 // channels past the end
-                    if (n < it.rows && in) r[i] = *reinterpret_cast<const uint4*>(x + (uint32_t)n * (uint32_t)p.w.K + (uint32_t)(step * kStep));
-                }
-            };
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) fetch(raw[u], u);
-            for (int base = 0; base < steps && good; base += kAhead) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int i = base + u;
-                    if (i >= steps || !good) break;
-                    // the next item's first steps are made while the products of this one end; then its sums are written out
-                    if (i == kB - 1 && j > 0 && splits == 1) {
-                        write_out(j - 1);
-                        if (!good) break;
-                    }
-                    if (made < kB) {
-                        ++made;
-                    } else {
-                        if (!await(&op_done[before.at], before.parity)) break;
-                        before.next(kSteps);
-                    }
-                    unsigned char* to = ops + b.at * b_bytes + c * run;
-#pragma unroll
-                    for (int m = 0; m < kTokens / 32; ++m) {
-                        const int n = n0 + 32 * m;
-                        if (n < it.rows) {
-                            uint4 lo, hi;
-                            widen(raw[u][m].x ^ 0x80808080u, &lo.x, &lo.y);
-                            widen(raw[u][m].y ^ 0x80808080u, &lo.z, &lo.w);
-                            widen(raw[u][m].z ^ 0x80808080u, &hi.x, &hi.y);
-                            widen(raw[u][m].w ^ 0x80808080u, &hi.z, &hi.w);
-                            *reinterpret_cast<uint4*>(to + n * 16) = lo;
-                            *reinterpret_cast<uint4*>(to + 8 * run + n * 16) = hi;
-                        }
-                    }
-                    fetch(raw[u], i + kAhead);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&op_full[g.at]);
-                    g.next(kSteps);
-                    b.next(kB);
-                }
-            }
-            if (!good) break;
-            if (j > 0 && splits == 1 && steps < kB) write_out(j - 1);
-            if (!good) break;
-            last = it;
-        }
-        if (good && j > 0 && splits == 1) write_out(j - 1);
-        it = last;
-        if (j == 0) it.e = -1;
+        if (elect_one()) good = issue(c.tmem, steps, tile_rows);
+    } else if (warp >= kWeightWarps) {
+        good = tile_rows <= 32 ? widen_tokens<1, 2>(p, c.tmem, k0, steps, tile_rows, splits == 1)
+                               : widen_tokens<4, 2>(p, c.tmem, k0, steps, tile_rows, splits == 1);
     } else {
-        // weights: a thread has one row of one block
-        const int half = warp >> 2;
-        const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
-        int made = 0;
-        Place g, a, r, before;
-        for (int j = 0; next_item(j, &it); ++j) {
-            const bool here = half == 0 || it.two;
-            for (int i = 0; i < steps; ++i) {
-                if (!await(&ring_full[r.at], r.parity)) break;
-                uint32_t v[2][32];
-                if (here) {
-                    const unsigned char* from = smem + (r.at * 2 + half) * kStepBytes + (threadIdx.x & 127) * 16;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint4 raw = *reinterpret_cast<const uint4*>(from + q * kRows * 16);
-                        uint32_t* to = &v[q >> 2][(q & 3) * 8];
-                        widen(raw.x, to, to + 1);
-                        widen(raw.y, to + 2, to + 3);
-                        widen(raw.z, to + 4, to + 5);
-                        widen(raw.w, to + 6, to + 7);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ring_empty[r.at]);
-                if (made < kA) {
-                    ++made;
-                } else {
-                    if (!await(&op_done[before.at], before.parity)) break;
-                    before.next(kSteps);
-                }
-                if (here) {
-                    tcgen05_after();
-                    const uint32_t to = a_at + (a.at * 2 + half) * kAColumns + lanes;
-                    tmem_store32(to, v[0]);
-                    tmem_store32(to + 32, v[1]);
-                    tmem_store_wait();
-                    tcgen05_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&op_full[g.at]);
-                g.next(kSteps);
-                a.next(kA);
-                r.next(ring);
-            }
-            if (!good) break;
-        }
+        good = widen_weights(c.tmem, steps, tile_rows);
     }
     __syncwarp();
+    good = __all_sync(0xffffffffu, good);
     if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
     good = __syncthreads_and(good);
-    if (splits > 1) {
-        // the shares' sums: each CTA owns some of the tile's token rows, whose sums the others push to it
-        cluster_barrier();                       // the rings are free
-        float* parts = reinterpret_cast<float*>(smem);         // [share][own][block][weight row]
-        const int half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
-        const bool writes = warp >= 8 && warp < 16 && it.e >= 0 && (half == 0 || it.two);
-        const int own = (it.rows + splits - 1) / splits;
-        if (writes && good) {
-            tcgen05_after();
-            for (int n = 0; n < it.rows; n += 16) {
-                uint32_t v[16];
-                tmem_load16(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (n + i < it.rows) {
-                        const int owner = (n + i) / own;
-                        const uint32_t to = in_cta(smem_addr(parts + ((split * own + n + i - owner * own) * 2 + half) * kRows + row), owner);
-                        asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(v[i]) : "memory");
-                    }
-            }
-            tcgen05_before();
-        }
-        __syncwarp();
-        cluster_barrier();
-        if (writes && good) {
-            Writer w(p, it, it.b + half, row);
-            const int to = min(it.rows, (split + 1) * own);
-            w.rows = to;                         // the rows after them are another's
-            for (int n = split * own; n < to; n += 2) {
-                float sum[2] = {0.f, 0.f};
-                for (int q = 0; q < splits; ++q)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (n + i < to) sum[i] += parts[((q * own + n + i - split * own) * 2 + half) * kRows + row];
-                w.put(n, sum[0], sum[1], [&](int r) { return r < to ? w.row_scale[r] : 0.f; });
-            }
-        }
-    }
+    // the one item's slot is not used again
+    if (splits > 1) join_shares(p, c.items[0], c.tmem, split, splits, good);
     __syncthreads();
     if (warp == kIssuer) {
         tcgen05_after();
-        tmem_free(tmem, kColumns);
+        tmem_free(c.tmem, kColumns);
     }
 }
 
@@ -647,10 +722,10 @@ cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream
     while (tile > 32 && most_tiles(p.w.E, p.max_rows, tile) * pairs * 2 <= num_sms) tile /= 2;
     const int64_t most = most_tiles(p.w.E, p.max_rows, tile) * pairs;
     while (splits < 8 && most * splits * 2 <= num_sms && k_steps(p.w) >= splits * 4) splits *= 2;
-    const cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kControlBytes + kSmemBytes);
     if (e != cudaSuccess) return e;
     const unsigned clusters = (unsigned)std::min<int64_t>(most, num_sms / splits);
-    return launch_clusters(true, splits, expert_i8_kernel, dim3(clusters * splits), dim3(kThreads), kSmemBytes, stream, p, splits, tile);
+    return launch_clusters(true, splits, expert_i8_kernel, dim3(clusters * splits), dim3(kThreads), kControlBytes + kSmemBytes, stream, p, splits, tile);
 }
 
 }  // namespace ep
