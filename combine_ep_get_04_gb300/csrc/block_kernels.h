@@ -128,11 +128,11 @@ cudaError_t launch_block_norm_backward(const NormParams& p, int num_sms, cudaStr
 // ---------------------------------------------------------------- dropout
 
 // What stays and what it is multiplied by: an element is dropped when its 16
-// random bits are below `limit`.
+// random bits are below a limit of 1..65536.
 struct Dropout {
     const int64_t* rng;     // seed and step, on the device; nullptr: nothing is dropped
     uint64_t site;          // added to the step
-    uint32_t limit;         // 0..65536
+    uint32_t most;          // limit * 65536 - 1
     float scale;            // 65536 / (65536 - limit), 0 where everything is dropped
 };
 
@@ -145,7 +145,7 @@ struct DropoutParams {
     int f32;
 };
 
-cudaError_t launch_dropout(const DropoutParams& p, cudaStream_t stream);
+cudaError_t launch_dropout(const DropoutParams& p, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------- layer norm
 

@@ -185,10 +185,11 @@ ep_status_t set_dropout(ep::Dropout* d, double p, const int64_t* rng, uint64_t s
     if (!(p >= 0.0 && p <= 1.0)) return fail(EP_ERR_INVALID_ARG, "p = %g must be in [0, 1]", p);
     if (reinterpret_cast<uintptr_t>(rng) & 7u) return fail(EP_ERR_INVALID_ARG, "rng must be 8-byte aligned");
     *d = ep::Dropout{};
-    d->limit = (uint32_t)nearbyint(p * 65536.0);
-    d->rng = d->limit != 0 ? rng : nullptr;
+    const uint64_t limit = (uint64_t)nearbyint(p * 65536.0);
+    d->rng = limit != 0 ? rng : nullptr;
     d->site = site;
-    d->scale = d->limit < 65536u ? (float)(65536.0 / (65536.0 - d->limit)) : 0.f;
+    d->most = (uint32_t)((limit << 16) - 1);
+    d->scale = limit < 65536 ? (float)(65536.0 / (65536.0 - (double)limit)) : 0.f;
     return ok();
 }
 
@@ -800,8 +801,7 @@ ep_status_t ep_dropout(int64_t T, int64_t H, int32_t type, const void* x, int64_
     const uintptr_t mask = type == EP_TYPE_F32 ? 3u : 1u;
     if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(y)) & mask)
         return fail(EP_ERR_INVALID_ARG, "x, residual or y is not aligned to its elements");
-    if (T * H > (int64_t)1 << 40)          // one launch's grid, at 32 vectors of 8 a block
-        return fail(EP_ERR_UNSUPPORTED, "%lld rows of %lld elements are too many", (long long)T, (long long)H);
+    if (T * H > (int64_t)1 << 40) return fail(EP_ERR_UNSUPPORTED, "%lld rows of %lld elements are too many", (long long)T, (long long)H);
     int num_sms = 0;
     st = device_info(&num_sms);
     if (st != EP_OK) return st;
@@ -814,7 +814,7 @@ ep_status_t ep_dropout(int64_t T, int64_t H, int32_t type, const void* x, int64_
     d.ld_res = ld_res;
     d.ld_y = ld_y;
     d.f32 = type == EP_TYPE_F32 ? 1 : 0;
-    return launched(ep::launch_dropout(d, reinterpret_cast<cudaStream_t>(stream)), "dropout launch");
+    return launched(ep::launch_dropout(d, num_sms, reinterpret_cast<cudaStream_t>(stream)), "dropout launch");
 }
 
 ep_status_t ep_layer_norm(const ep_layer_norm_t* norm, const void* h, int64_t ld_h, const void* y, int64_t ld_y, const float* w,

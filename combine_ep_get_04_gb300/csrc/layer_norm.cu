@@ -37,14 +37,25 @@ RowShape row_shape(int T, int H, size_t row_bytes, int num_sms) {
 // The rows of a CTA are a grid apart.
 __device__ __forceinline__ int rows_of_cta(int T) { return (int)blockIdx.x < T ? (T - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0; }
 
-// Sums of two values over a warp in five shuffles and one more: lanes 0 to 15
-// end up with the first, the others with the second.
-__device__ __forceinline__ float warp_sum2(float a, float b) {
+// Sums of two values over a warp, in six shuffles, to all its lanes.
+__device__ __forceinline__ float2 warp_sum2(float a, float b) {
     const bool high = threadIdx.x & 16;
     float x = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
 #pragma unroll
     for (int d = 8; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
+    const float other = __shfl_xor_sync(0xffffffffu, x, 16);
+    return high ? make_float2(other, x) : make_float2(x, other);
+}
+
+// Of four values, in eight.
+__device__ __forceinline__ float4 warp_sum4(float a, float b, float c, float d) {
+    const bool high = threadIdx.x & 16, second = threadIdx.x & 8;
+    const float x = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+    const float y = (high ? d : c) + __shfl_xor_sync(0xffffffffu, high ? c : d, 16);
+    float z = (second ? y : x) + __shfl_xor_sync(0xffffffffu, second ? x : y, 8);
+#pragma unroll
+    for (int i = 4; i >= 1; i >>= 1) z += __shfl_xor_sync(0xffffffffu, z, i);
+    return make_float4(__shfl_sync(0xffffffffu, z, 0), __shfl_sync(0xffffffffu, z, 16), __shfl_sync(0xffffffffu, z, 8), __shfl_sync(0xffffffffu, z, 24));
 }
 
 // Channels of a row that belong to warp w.
@@ -71,9 +82,9 @@ __device__ __forceinline__ Vec8 round_bf16(const Vec8& x) {
 //
 // A producer warp keeps a ring of rows (h, y) filled by bulk copies.  A row is
 // taken up in two turns.  Turn i sums row i, writes its h_out and leaves each
-// warp's sum and squared deviations from the warp's own mean; then row i - 1,
-// whose warps' values are all there by now, is normed from registers, so that no
-// warp stands still at a row's end.  The warps' moments join by
+// warp's sum and squared deviations from the warp's own mean; beside that row
+// i - 1, whose warps' values are all there by now, is normed from registers, so
+// that no warp stands still at a row's end.  The warps' moments join by
 //   M2 = sum over warps of M2_w + n_w (mean_w - mean)^2,
 // which never subtracts large squares from each other.
 template <int NV, bool F32, bool DROP, int THREADS>
@@ -153,6 +164,7 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p, 
             Vec8 before[NV];
 #pragma unroll
             for (int k = 0; k < NV; ++k) before[k] = z[k];
+            uint64_t sum = both(0.f);
             if (i < rows) {
                 good = __all_sync(0xffffffffu, mbar_wait(&full[st], parity));
                 if (!good) break;
@@ -169,7 +181,6 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p, 
                     st = 0;
                     parity ^= 1;
                 }
-                uint64_t sum = both(0.f);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     if (DROP) apply(y[k], random_bits((uint64_t)t * vecs + threadIdx.x + k * lanes, ctr), p.drop);
@@ -182,33 +193,36 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p, 
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sum = add2(sum, z[k].v[c]);
                 }
-                const float s = warp_sum(total(sum));
-                const uint64_t less = both(-s * inv_mine);
-                uint64_t squares = both(0.f);
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    if (in[k])
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint64_t d = add2(z[k].v[c], less);
-                            squares = fma2(d, d, squares);
-                        }
-                const float m2 = warp_sum(total(squares));
-                if (lane == 0) {
-                    moments[i % kSlots][warp] = make_float2(s, m2);
-                    mbar_arrive(&summed[i % kSlots]);
-                }
             }
+            // row i's first sum with row i - 1's last join, whose chains of shuffles are then one
+            float2 m = make_float2(0.f, 0.f);
             if (i > 0) {
                 const int slot = (i - 1) % kSlots;
                 good = __all_sync(0xffffffffu, mbar_wait(&summed[slot], summed_parity));
                 if (!good) break;
                 if (slot == kSlots - 1) summed_parity ^= 1;
-                const float2 m = lane < warps ? moments[slot][lane] : make_float2(0.f, 0.f);
-                const float mean = warp_sum(m.x) * inv_h;
-                const float off = fmaf(-n_theirs, mean, m.x);
-                const float variance = warp_sum(fmaf(off * off, inv_theirs, m.y)) * inv_h;
-                const float r = rsqrtf(variance + p.eps);
+                if (lane < warps) m = moments[slot][lane];
+            }
+            const float2 first = warp_sum2(total(sum), m.x);
+            const float mean = first.y * inv_h, off = fmaf(-n_theirs, mean, m.x);
+            const uint64_t from_own = both(-first.x * inv_mine);
+            uint64_t squares = both(0.f);
+            if (i < rows)
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (in[k])
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint64_t d = add2(z[k].v[c], from_own);
+                            squares = fma2(d, d, squares);
+                        }
+            const float2 second = warp_sum2(total(squares), fmaf(off * off, inv_theirs, m.y));
+            if (i < rows && lane == 0) {
+                moments[i % kSlots][warp] = make_float2(first.x, second.x);
+                mbar_arrive(&summed[i % kSlots]);
+            }
+            if (i > 0) {
+                const float r = rsqrtf(fmaf(second.y, inv_h, p.eps));
                 const int64_t from = t - gridDim.x;
                 if (threadIdx.x == 0 && p.stats != nullptr) {
                     p.stats[from] = mean;
@@ -320,13 +334,13 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(LayerNormP
         int st1 = 0, st2 = 0;
         uint32_t full_parity = 0, summed_parity = 0;
         for (int i = 0; i < rows + lag; ++i) {
+            uint64_t sum0 = both(0.f), sum1 = sum0;
             if (i < rows) {
                 good = __all_sync(0xffffffffu, mbar_wait(&full[st1], full_parity));
                 if (!good) break;
                 const unsigned char* row = ring + st1 * stage_bytes;
                 const float2 rs = row_stats[st1];
                 const uint64_t less = both(-rs.x), r = both(rs.y);
-                uint64_t sum0 = both(0.f), sum1 = sum0;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     if (NV > 2) load_weights(k);
@@ -340,24 +354,43 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(LayerNormP
                         sum1 = fma2(t, xn, sum1);
                     }
                 }
-                const float s = warp_sum2(total(sum0), total(sum1));
-                const int slot = i % kSlots;
-                if ((lane & 15) == 0) (&sums[slot][warp].x)[lane >> 4] = s;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&summed[slot]);
                 if (++st1 == stages) {
                     st1 = 0;
                     full_parity ^= 1;
                 }
             }
-            if (i >= lag) {
+            // the sums of a row and of the one `lag` before, whose warps' sums are there by now, in one chain of shuffles
+            auto leave = [&](float a, float b) {
+                if (lane == 0) {
+                    sums[i % kSlots][warp] = make_float2(a, b);
+                    mbar_arrive(&summed[i % kSlots]);
+                }
+            };
+            auto others = [&]() {
                 const int slot = (i - lag) % kSlots;
                 good = __all_sync(0xffffffffu, mbar_wait(&summed[slot], summed_parity));
-                if (!good) break;
                 if (slot == kSlots - 1) summed_parity ^= 1;
-                const float2 part = lane < warps ? sums[slot][lane] : make_float2(0.f, 0.f);
-                const float s = warp_sum2(part.x, part.y), other = __shfl_xor_sync(0xffffffffu, s, 16);
-                const float m1 = (lane & 16 ? other : s) * inv_h, m2 = (lane & 16 ? s : other) * inv_h;
+                return good && lane < warps ? sums[slot][lane] : make_float2(0.f, 0.f);
+            };
+            float2 s;
+            if (lag == 0) {
+                const float2 own = warp_sum2(total(sum0), total(sum1));
+                leave(own.x, own.y);
+                const float2 part = others();
+                if (!good) break;
+                s = warp_sum2(part.x, part.y);
+            } else {
+                float2 part = make_float2(0.f, 0.f);
+                if (i > 0) {
+                    part = others();
+                    if (!good) break;
+                }
+                const float4 four = warp_sum4(total(sum0), total(sum1), part.x, part.y);
+                if (i < rows) leave(four.x, four.y);
+                s = make_float2(four.z, four.w);
+            }
+            if (i >= lag) {
+                const float m1 = s.x * inv_h, m2 = s.y * inv_h;
                 const unsigned char* row = ring + st2 * stage_bytes;
                 const float2 rs = row_stats[st2];
                 const uint64_t less = both(-rs.x), r = both(rs.y), minus_m1 = both(-m1), minus_m2 = both(-m2);

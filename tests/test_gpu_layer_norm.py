@@ -179,6 +179,15 @@ def test_everything_and_nothing_dropped():
             assert torch.equal(h_out, h + y.float()) and torch.equal(d.d_y, d.d_h.bfloat16())
 
 
+def test_dropout_where_nothing_is_dropped():
+    g = generator(3)
+    x, res = rows_of(g, 33, 1001, BF16), rows_of(g, 33, 1001, BF16)
+    for p, rng in ((0.4, None), (0.0, words(1, 2))):
+        assert torch.equal(ep.dropout(x, p, rng), x)
+        assert torch.equal(ep.dropout(x[:, :1000], p, rng, residual=res[:, :1000]), (x.float() + res.float()).bfloat16()[:, :1000])
+    assert torch.equal(ep.dropout(x, 1.0, words(1, 2), residual=res), res) and not ep.dropout(x, 1.0, words(1, 2)).any()
+
+
 def test_seed_step_and_site():
     """Each changes the mask; a step with a site is the step that many later."""
     x = torch.ones(64, 128, device="cuda")
