@@ -12,6 +12,7 @@
 // operand; eight more load token codes, several steps ahead, and widen them into
 // shared memory (B), and write the sums out; one thread issues the products.
 #include <algorithm>
+#include <atomic>
 
 #include "ep.h"
 
@@ -301,7 +302,7 @@ __device__ __forceinline__ bool next_item(int j, Item* it) {
 
 // Finds the items: item j of cluster c is number c + j * clusters in the order of
 // experts, tiles and blocks.
-__device__ __noinline__ bool find_items(int E, int nb, int tile_rows, int cluster, int clusters, bool one, uint32_t* err_flags) {
+__device__ __noinline__ bool find_items(int E, int nb, int width, int tile_rows, int cluster, int clusters, bool one, uint32_t* err_flags) {
     Control& c = control();
     const int lane = threadIdx.x & 31;
     // lane l adds up the tiles of experts [l * per, (l + 1) * per)
@@ -321,8 +322,8 @@ __device__ __noinline__ bool find_items(int E, int nb, int tile_rows, int cluste
     total = __shfl_sync(0xffffffffu, total, 31);
     for (int e = e0; e < e1; ++e) c.upto[e] += before;
     __syncwarp();
-    const int pairs = (nb + 1) / 2;
-    const int64_t all = (int64_t)total * pairs, most = one ? min(all, (int64_t)clusters) : all;
+    const int across = (nb + width - 1) / width;       // items of a tile
+    const int64_t all = (int64_t)total * across, most = one ? min(all, (int64_t)clusters) : all;
     if (most < all && cluster == 0 && lane == 0 && err_flags != nullptr) atomicOr(err_flags, kErrCapacity);
     for (int j = 0;; ++j) {
         const int slot = j % kItems;
@@ -330,7 +331,7 @@ __device__ __noinline__ bool find_items(int E, int nb, int tile_rows, int cluste
         if (j >= kItems && !await(&c.item_empty[slot], (j / kItems - 1) & 1)) return false;
         Item it{-1, 0, 0, 0, 0};
         if (at < most) {
-            const int tile = (int)(at / pairs);
+            const int tile = (int)(at / across);
             int lo = 0, hi = E - 1;                    // the first expert with upto > tile
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
@@ -340,8 +341,8 @@ __device__ __noinline__ bool find_items(int E, int nb, int tile_rows, int cluste
                     lo = mid + 1;
             }
             const int n = c.rows[lo], size = tile_rows_of(n, tile_rows), from = (tile - (lo > 0 ? c.upto[lo - 1] : 0)) * size;
-            const int b = (int)(at - (int64_t)tile * pairs) * 2;
-            it = Item{lo, min(size, n - from), c.first[lo] + from, b, b + 1 < nb};
+            const int b = (int)(at - (int64_t)tile * across) * width;
+            it = Item{lo, min(size, n - from), c.first[lo] + from, b, width > 1 && b + 1 < nb};
         }
         if (lane == 0) {
             c.items[slot] = it;
@@ -626,9 +627,10 @@ __device__ __noinline__ void join_shares(const I8Params& params, const Item it, 
     }
 }
 
-// A grid of clusters of `splits` CTAs takes the items a grid apart; with more than
-// one share of K (which a launch of few products has) a cluster takes one.
-__global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_constant__ I8Params p, int splits, int tile_rows) {
+// A grid of clusters of `splits` CTAs takes the items, of `width` blocks, a grid
+// apart; with more than one share of K (which a launch of few products has) a
+// cluster takes one.
+__global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_constant__ I8Params p, int splits, int width, int tile_rows) {
     Control& c = control();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % splits, cluster = blockIdx.x / splits, nb = row_blocks(p.w), nk = k_steps(p.w);
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
     tcgen05_after();
     bool good = true;
     if (warp == kFinder) {
-        good = find_items(p.w.E, nb, tile_rows, cluster, gridDim.x / splits, splits > 1, p.err_flags);
+        good = find_items(p.w.E, nb, width, tile_rows, cluster, gridDim.x / splits, splits > 1, p.err_flags);
     } else if (warp == kProducer) {
         good = produce(static_cast<const unsigned char*>(p.packed), nb, nk, k0, steps, tile_rows);
     } else if (warp == kIssuer) {
@@ -714,18 +716,50 @@ cudaError_t launch_i8_pack(const I8Shape& w, const int8_t* codes, const float* s
     return launch_kernel(false, i8_pack_kernel, grid, dim3(256), 0, stream, w, codes, scales, static_cast<unsigned char*>(packed));
 }
 
+namespace {
+
+// Clusters of so many CTAs that run at the same time.
+int clusters_at_once(int splits) {
+    static std::atomic<int> known[4];          // of 2, 4 and 8; 0: not asked yet
+    std::atomic<int>& n = known[splits == 2 ? 1 : splits == 4 ? 2 : 3];
+    int got = n.load(std::memory_order_relaxed);
+    if (got > 0) return got;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kControlBytes + kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&got, expert_i8_kernel, &cfg) != cudaSuccess || got < 1) {
+        (void)cudaGetLastError();
+        got = 1;
+    }
+    n.store(got, std::memory_order_relaxed);
+    return got;
+}
+
+}  // namespace
+
 cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream) {
-    const int pairs = (row_blocks(p.w) + 1) / 2;
-    // Tiles of twice the mean: the smaller the tile, the longer the ring.
-    int tile = kTokens, splits = 1;
-    while (tile > 32 && p.max_rows * 4 <= (int64_t)p.w.E * tile) tile /= 2;
-    while (tile > 32 && most_tiles(p.w.E, p.max_rows, tile) * pairs * 2 <= num_sms) tile /= 2;
-    const int64_t most = most_tiles(p.w.E, p.max_rows, tile) * pairs;
-    while (splits < 8 && most * splits * 2 <= num_sms && k_steps(p.w) >= splits * 4) splits *= 2;
-    cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kControlBytes + kSmemBytes);
+    const cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kControlBytes + kSmemBytes);
     if (e != cudaSuccess) return e;
-    const unsigned clusters = (unsigned)std::min<int64_t>(most, num_sms / splits);
-    return launch_clusters(true, splits, expert_i8_kernel, dim3(clusters * splits), dim3(kThreads), kControlBytes + kSmemBytes, stream, p, splits, tile);
+    // Tiles of twice the mean rows: the smaller the tile, the longer the ring.  Then as many items as there are SMs: by
+    // single blocks, by smaller tiles, by shares of K, of which a cluster that did not run at once would double the time
+    // (one row, 7168 -> 4096: 16 clusters of 8 23 us, of 4 16.5).
+    const int nb = row_blocks(p.w);
+    int tile = kTokens, width = 2, splits = 1;
+    while (tile > 32 && p.max_rows * 4 <= (int64_t)p.w.E * tile) tile /= 2;
+    auto items = [&]() { return most_tiles(p.w.E, p.max_rows, tile) * ((nb + width - 1) / width); };
+    if (items() * 2 <= num_sms) width = 1;
+    while (tile > 32 && items() * 2 <= num_sms) tile /= 2;
+    while (splits < 8 && items() * splits * 2 <= num_sms && k_steps(p.w) >= splits * 4 && items() <= clusters_at_once(splits * 2)) splits *= 2;
+    const unsigned clusters = (unsigned)std::min<int64_t>(items(), num_sms / splits);
+    return launch_clusters(true, splits, expert_i8_kernel, dim3(clusters * splits), dim3(kThreads), kControlBytes + kSmemBytes, stream, p, splits, width,
+                           tile);
 }
 
 }  // namespace ep
