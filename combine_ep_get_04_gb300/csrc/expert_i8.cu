@@ -166,6 +166,8 @@ __host__ __device__ constexpr int ring_steps(int tile_rows) {
     return fit < kMaxRing ? fit : kMaxRing;
 }
 static_assert(ring_steps(kTokens) >= 3, "the widest tile leaves too little for the ring");
+// Items of one block: the two groups of weight warps take turns, and so have places of their own.
+__host__ __device__ constexpr int ring_steps(int tile_rows, int width) { return width == 1 ? ring_steps(tile_rows) & ~1 : ring_steps(tile_rows); }
 
 // Waits for a phase, at most kWaitLimitNs and a few tries.  A try suspends the
 // thread for a while by itself, which leaves the issue slots to others; the clock
@@ -354,9 +356,9 @@ __device__ __noinline__ bool find_items(int E, int nb, int width, int tile_rows,
 }
 
 // Keeps the ring of codes filled.
-__device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk, int k0, int steps, int tile_rows) {
+__device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk, int k0, int steps, int ring) {
     Control& c = control();
-    const int lane = threadIdx.x & 31, ring = ring_steps(tile_rows);
+    const int lane = threadIdx.x & 31;
     int64_t filled = 0;
     bool good = true;
     Item it;
@@ -384,12 +386,12 @@ __device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk
 }
 
 // Issues the products.  One thread: their operands then stay in uniform registers.
-__device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows) {
+__device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows, int ring) {
     Control& c = control();
     const uint32_t a_at = tmem + 2 * kTokens, run16 = run_bytes(tile_rows) / 16;
     // runs of 8 channels run16 * 16 bytes apart, 8 rows 128 bytes apart, no swizzle
     const uint64_t desc = (uint64_t)run16 << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
-    const unsigned char* ops = ring_base() + ring_steps(tile_rows) * kRingBytes;
+    const unsigned char* ops = ring_base() + ring * kRingBytes;
     const uint64_t first_b = desc | (smem_addr(ops) >> 4 & 0x3fff);          // in a cluster, addresses have a rank above
     int committed = 0;
     bool good = true;
@@ -465,13 +467,13 @@ __device__ __noinline__ bool write_sums(const I8Params& p, const Item it, uint32
 // than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).  The
 // same warps write the sums out (where `whole` is set: K is not shared).
 template <int CHUNKS, int AHEAD>
-__device__ __noinline__ bool widen_tokens(const I8Params& params, uint32_t tmem, int k0, int steps, int tile_rows, bool whole) {
+__device__ __noinline__ bool widen_tokens(const I8Params& params, uint32_t tmem, int k0, int steps, int tile_rows, int ring, bool whole) {
     Control& c = control();
     const I8Params& p = params;
     const int K = p.w.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, run = run_bytes(tile_rows);
     const int t = threadIdx.x - kWeightWarps * 32, n0 = t >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
     const uint32_t sums = tmem + half * kTokens + ((uint32_t)(warp & 3) * 32 << 16);
-    unsigned char* ops = ring_base() + ring_steps(tile_rows) * kRingBytes + (t & 7) * run + n0 * 16;
+    unsigned char* ops = ring_base() + ring * kRingBytes + (t & 7) * run + n0 * 16;
     const int8_t* first_x = p.x + (int64_t)k0 * kStep + (t & 7) * 16;
     const int left = K - k0 * kStep - (t & 7) * 16;            // channels from the thread's on
     int made = 0;                            // steps, up to kB
@@ -537,13 +539,16 @@ __device__ __noinline__ bool widen_tokens(const I8Params& params, uint32_t tmem,
     }
 }
 
-// Weights: a thread has one row of one block.
-__device__ __noinline__ bool widen_weights(uint32_t tmem, int steps, int tile_rows) {
+// Weights: a thread has one row of one block, of two (a group of warps each), or
+// of one in every other step: what a step costs a group is mostly waiting, for
+// barriers, shared memory and tensor memory in turn.
+template <int TURNS>
+__device__ __noinline__ bool widen_weights(uint32_t tmem, int steps, int ring) {
     Control& c = control();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, ring = ring_steps(tile_rows);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, half = TURNS > 1 ? 0 : group;
     const uint32_t to = tmem + 2 * kTokens + half * kAColumns + ((uint32_t)(warp & 3) * 32 << 16);
     const unsigned char* from = ring_base() + half * kStepBytes + (threadIdx.x & 127) * 16;
-    int made = 0;
+    int n = 0;                               // steps so far, in turns' places
     Item it;
     Place g, a, r, before;                   // the step's barrier, its room, the ring's; the barrier of the room's last step
     for (int j = 0;; ++j) {
@@ -551,35 +556,35 @@ __device__ __noinline__ bool widen_weights(uint32_t tmem, int steps, int tile_ro
         if (it.e < 0) return true;
         const bool here = half == 0 || it.two;
         for (int i = 0; i < steps; ++i) {
-            if (!await(&c.ring_full[r.at], r.parity)) return false;
-            uint32_t v[2][32];
+            if (TURNS == 1 || (n & 1) == group) {
+                if (!await(&c.ring_full[r.at], r.parity)) return false;
+                uint32_t v[2][32];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint4 raw = *reinterpret_cast<const uint4*>(from + r.at * kRingBytes + q * kRows * 16);
-                uint32_t* w = &v[q >> 2][(q & 3) * 8];
-                widen(raw.x, w, w + 1);
-                widen(raw.y, w + 2, w + 3);
-                widen(raw.z, w + 4, w + 5);
-                widen(raw.w, w + 6, w + 7);
+                for (int q = 0; q < 8; ++q) {
+                    const uint4 raw = *reinterpret_cast<const uint4*>(from + r.at * kRingBytes + q * kRows * 16);
+                    uint32_t* w = &v[q >> 2][(q & 3) * 8];
+                    widen(raw.x, w, w + 1);
+                    widen(raw.y, w + 2, w + 3);
+                    widen(raw.z, w + 4, w + 5);
+                    widen(raw.w, w + 6, w + 7);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.ring_empty[r.at]);
+                if (n >= kA && !await(&c.op_done[before.at], before.parity)) return false;
+                tcgen05_after();
+                if (here) {
+                    tmem_store32(to + a.at * 2 * kAColumns, v[0]);
+                    tmem_store32(to + a.at * 2 * kAColumns + 32, v[1]);
+                    tmem_store_wait();
+                }
+                tcgen05_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.op_full[g.at]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c.ring_empty[r.at]);
-            r.next(ring);
-            if (made < kA) {
-                ++made;
-            } else {
-                if (!await(&c.op_done[before.at], before.parity)) return false;
+            if (n >= kA)
                 before.next(kSteps);
-            }
-            tcgen05_after();
-            if (here) {
-                tmem_store32(to + a.at * 2 * kAColumns, v[0]);
-                tmem_store32(to + a.at * 2 * kAColumns + 32, v[1]);
-                tmem_store_wait();
-            }
-            tcgen05_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c.op_full[g.at]);
+            n = n < kA + 2 ? n + 1 : n - 1;              // its parity and whether it is below kA are all that counts
+            r.next(ring);
             g.next(kSteps);
             a.next(kA);
         }
@@ -634,15 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
     Control& c = control();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % splits, cluster = blockIdx.x / splits, nb = row_blocks(p.w), nk = k_steps(p.w);
+    const int ring = ring_steps(tile_rows, width), weight_warps = width == 1 ? kWeightWarps / 2 : kWeightWarps;
     const int k0 = (int)((int64_t)nk * split / splits), steps = (int)((int64_t)nk * (split + 1) / splits) - k0;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxRing; ++i) {
             mbar_init(&c.ring_full[i], 1);
-            mbar_init(&c.ring_empty[i], kWeightWarps);
+            mbar_init(&c.ring_empty[i], weight_warps);
         }
         for (int i = 0; i < kSteps; ++i) {
-            mbar_init(&c.op_full[i], kWeightWarps + kTokenWarps);
+            mbar_init(&c.op_full[i], weight_warps + kTokenWarps);
             mbar_init(&c.op_done[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
@@ -675,14 +681,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
     if (warp == kFinder) {
         good = find_items(p.w.E, nb, width, tile_rows, cluster, gridDim.x / splits, splits > 1, p.err_flags);
     } else if (warp == kProducer) {
-        good = produce(static_cast<const unsigned char*>(p.packed), nb, nk, k0, steps, tile_rows);
+        good = produce(static_cast<const unsigned char*>(p.packed), nb, nk, k0, steps, ring);
     } else if (warp == kIssuer) {
-        if (elect_one()) good = issue(c.tmem, steps, tile_rows);
+        if (elect_one()) good = issue(c.tmem, steps, tile_rows, ring);
     } else if (warp >= kWeightWarps) {
-        good = tile_rows <= 32 ? widen_tokens<1, 2>(p, c.tmem, k0, steps, tile_rows, splits == 1)
-                               : widen_tokens<4, 2>(p, c.tmem, k0, steps, tile_rows, splits == 1);
+        good = tile_rows <= 32 ? widen_tokens<1, 2>(p, c.tmem, k0, steps, tile_rows, ring, splits == 1)
+                               : widen_tokens<4, 2>(p, c.tmem, k0, steps, tile_rows, ring, splits == 1);
     } else {
-        good = widen_weights(c.tmem, steps, tile_rows);
+        good = width == 1 ? widen_weights<2>(c.tmem, steps, ring) : widen_weights<1>(c.tmem, steps, ring);
     }
     __syncwarp();
     good = __all_sync(0xffffffffu, good);
