@@ -428,6 +428,157 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(LayerNormP
     if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
 }
 
+// ------------------------------------------------------------- narrow rows
+//
+// A warp takes a row by itself: no barrier, no join, and as many rows on their
+// way as an SM has warps.  NV vectors of 8 channels a lane; rows are dealt to the
+// CTAs first, then to their warps.  As far as the registers hold a row (backward,
+// the two sums over rows too): T=8192 bf16 forward and backward H=256 17 us, by the
+// ring 32; fp32 H=512 29 and 42; H=1024 forward 21.1 and 22.4, backward 35 and 40,
+// bf16 with dropout 80 and 52.
+
+constexpr int kNarrow = 1024, kNarrowBackward = 512;
+
+// Warps of a CTA, one CTA an SM, as many as the registers hold.
+constexpr int narrow_warps(int nv, bool backward) { return backward ? nv == 1 ? 24 : 16 : nv == 1 ? 32 : nv == 2 ? 24 : 16; }
+
+template <int NV, bool F32>
+__device__ __forceinline__ void load_row(Vec8 (&x)[NV], const unsigned char* row, int vecs, int lane) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) x[k] = lane + 32 * k < vecs ? load_stream<F32>(row, (lane + 32 * k) * kVec) : all(0.f);
+}
+
+template <int NV, bool F32, bool DROP>
+__global__ void __launch_bounds__(narrow_warps(NV, false) * 32) layer_norm_narrow_kernel(LayerNormParams p) {
+    constexpr int kStream = F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31, vecs = p.H / kVec;
+    const bool has_y = DROP || p.y != nullptr;
+    const float inv_h = 1.f / (float)p.H;
+    pdl_launch_dependents();
+    pdl_wait();
+    Counters ctr{};
+    if (DROP) ctr = counters(p.drop);
+    const int64_t apart = (int64_t)gridDim.x * (blockDim.x >> 5);
+    for (int64_t t = blockIdx.x + (int64_t)gridDim.x * (threadIdx.x >> 5); t < p.T; t += apart) {
+        Vec8 z[NV], y[NV];
+        load_row<NV, F32>(z, static_cast<const unsigned char*>(p.h) + t * p.ld_h * kStream, vecs, lane);
+        if (has_y) load_row<NV, false>(y, static_cast<const unsigned char*>(p.y) + t * p.ld_y * 2, vecs, lane);
+        uint64_t sum = both(0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = lane + 32 * k;
+            if (DROP) apply(y[k], random_bits((uint64_t)t * vecs + v, ctr), p.drop);
+            if (has_y) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) z[k].v[c] = add2(z[k].v[c], y[k].v[c]);
+                if (!F32) z[k] = round_bf16(z[k]);
+                if (v < vecs) store_stream<F32>(p.h_out, t * p.H + v * kVec, z[k]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum = add2(sum, z[k].v[c]);
+        }
+        const float mean = warp_sum(total(sum)) * inv_h;
+        const uint64_t less = both(-mean);
+        uint64_t squares = both(0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const bool in = lane + 32 * k < vecs;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                z[k].v[c] = in ? add2(z[k].v[c], less) : both(0.f);
+                squares = fma2(z[k].v[c], z[k].v[c], squares);
+            }
+        }
+        const float r = rsqrtf(fmaf(warp_sum(total(squares)), inv_h, p.eps));
+        if (lane == 0 && p.stats != nullptr) {
+            p.stats[t] = mean;
+            p.stats[p.T + t] = r;
+        }
+        const uint64_t r2 = both(r);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int at = (lane + 32 * k) * kVec;
+            if (at >= p.H) continue;
+            const Vec8 w = p.w != nullptr ? load_f32(p.w, at) : all(1.f), b = p.b != nullptr ? load_f32(p.b, at) : all(0.f);
+            Vec8 n;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) n.v[c] = fma2(mul2(z[k].v[c], r2), w.v[c], b.v[c]);
+            store_bf16(p.n, t * p.H + at, n);
+        }
+    }
+}
+
+template <int NV, bool F32, bool DROP>
+__global__ void __launch_bounds__(narrow_warps(NV, true) * 32) layer_norm_narrow_backward_kernel(LayerNormParams p) {
+    extern __shared__ __align__(128) unsigned char ring[];       // [warps][2 H] column sums
+    constexpr int kStream = F32 ? 4 : 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, vecs = p.H / kVec;
+    const float inv_h = 1.f / (float)p.H;
+    pdl_launch_dependents();
+    pdl_wait();
+    Counters ctr{};
+    if (DROP) ctr = counters(p.drop);
+    Vec8 s_w[NV], s_b[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) s_w[k] = s_b[k] = all(0.f);
+    const int64_t apart = (int64_t)gridDim.x * warps;
+    for (int64_t t = blockIdx.x + (int64_t)gridDim.x * warp; t < p.T; t += apart) {
+        Vec8 x[NV], dn[NV], dh[NV];
+        load_row<NV, F32>(x, static_cast<const unsigned char*>(p.h) + t * p.ld_h * kStream, vecs, lane);
+        load_row<NV, false>(dn, static_cast<const unsigned char*>(p.d_n) + t * p.H * 2, vecs, lane);
+        if (p.d_h_out != nullptr) {
+            load_row<NV, F32>(dh, static_cast<const unsigned char*>(p.d_h_out) + t * p.H * kStream, vecs, lane);
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) dh[k] = all(0.f);
+        }
+        const uint64_t less = both(-p.stats[t]), r = both(p.stats[p.T + t]);
+        uint64_t sum0 = both(0.f), sum1 = sum0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int at = (lane + 32 * k) * kVec;
+            const Vec8 w = at >= p.H ? all(0.f) : p.w != nullptr ? load_f32(p.w, at) : all(1.f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                x[k].v[c] = mul2(add2(x[k].v[c], less), r);
+                s_w[k].v[c] = fma2(dn[k].v[c], x[k].v[c], s_w[k].v[c]);
+                s_b[k].v[c] = add2(dn[k].v[c], s_b[k].v[c]);
+                dn[k].v[c] = mul2(dn[k].v[c], w.v[c]);
+                sum0 = add2(dn[k].v[c], sum0);
+                sum1 = fma2(dn[k].v[c], x[k].v[c], sum1);
+            }
+        }
+        const float2 s = warp_sum2(total(sum0), total(sum1));
+        const uint64_t minus_m1 = both(-s.x * inv_h), minus_m2 = both(-s.y * inv_h);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int v = lane + 32 * k;
+            if (v >= vecs) continue;
+            Vec8 d;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) d.v[c] = fma2(r, fma2(minus_m2, x[k].v[c], add2(dn[k].v[c], minus_m1)), dh[k].v[c]);
+            store_stream<F32>(p.d_h, t * p.H + v * kVec, d);
+            if (DROP) apply(d, random_bits((uint64_t)t * vecs + v, ctr), p.drop);
+            if (p.d_y != nullptr) store_bf16(p.d_y, t * p.H + v * kVec, d);
+        }
+    }
+    // the warps' sums over rows, in their order
+    float* parts = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int at = (lane + 32 * k) * kVec;
+        if (at >= p.H) continue;
+        store_f32(parts + (int64_t)warp * 2 * p.H, at, s_w[k]);
+        store_f32(parts + (int64_t)warp * 2 * p.H, p.H + at, s_b[k]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.H; c += blockDim.x) {
+        float sum = 0.f;
+        for (int i = 0; i < warps; ++i) sum += parts[i * 2 * p.H + c];
+        p.partial[(int64_t)blockIdx.x * 2 * p.H + c] = sum;
+    }
+}
+
 // Adds `groups` rows of column sums.  A CTA takes 32 columns; each warp adds
 // every kColumnWarps-th row, then the warps' sums are added in order.
 __global__ void __launch_bounds__(kColumnWarps * 32) layer_norm_columns_kernel(LayerNormParams p, int groups) {
@@ -456,6 +607,7 @@ __global__ void __launch_bounds__(kColumnWarps * 32) layer_norm_columns_kernel(L
 }
 
 using Kernel = void (*)(LayerNormParams, int, int);
+using Kernel1 = void (*)(LayerNormParams);
 
 // 16 warps with the producer's have 128 registers a thread, 17 have 96.
 template <int NV, bool F32, bool DROP>
@@ -479,24 +631,56 @@ cudaError_t launch_rows(const LayerNormParams& p, const RowShape& s, bool backwa
     return launch_kernel(true, kern, dim3(s.ctas), dim3(s.warps * 32 + 32), s.stages * row_bytes, stream, p, s.warps, s.stages);
 }
 
+template <bool F32, bool DROP>
+Kernel1 narrow_kernel(bool backward, int nv) {
+    if (backward) return nv == 1 ? layer_norm_narrow_backward_kernel<1, F32, DROP> : layer_norm_narrow_backward_kernel<2, F32, DROP>;
+    return nv == 1 ? layer_norm_narrow_kernel<1, F32, DROP> : nv == 2 ? layer_norm_narrow_kernel<2, F32, DROP> : layer_norm_narrow_kernel<4, F32, DROP>;
+}
+
+// *ctas: of the grid.
+cudaError_t launch_narrow(const LayerNormParams& p, int num_sms, bool backward, int* ctas, cudaStream_t stream) {
+    const int nv = p.H <= 256 ? 1 : p.H <= 512 ? 2 : 4, ctas_now = std::min(p.T, std::min(num_sms, kMaxSms));
+    // no more warps than rows
+    const int warps = std::min(narrow_warps(nv, backward), (p.T + ctas_now - 1) / ctas_now);
+    const bool drop = p.drop.rng != nullptr;
+    const Kernel1 kern = p.f32 ? (drop ? narrow_kernel<true, true>(backward, nv) : narrow_kernel<true, false>(backward, nv))
+                               : (drop ? narrow_kernel<false, true>(backward, nv) : narrow_kernel<false, false>(backward, nv));
+    const size_t smem = backward ? (size_t)warps * 2 * p.H * sizeof(float) : 0;
+    if (backward) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, narrow_warps(nv, true) * 2 * 256 * nv * (int)sizeof(float));
+        if (e != cudaSuccess) return e;
+    }
+    *ctas = ctas_now;
+    return launch_kernel(true, kern, dim3(ctas_now), dim3(warps * 32), smem, stream, p);
+}
+
 }  // namespace
 
 size_t layer_norm_workspace_bytes(int T, int H) { return (size_t)row_shape(T, H, 1, kMaxSms).ctas * 2 * H * sizeof(float); }
 
 cudaError_t launch_layer_norm(const LayerNormParams& p, int num_sms, cudaStream_t stream) {
+    int ctas;
+    if (p.H <= kNarrow) return launch_narrow(p, num_sms, false, &ctas, stream);
     const size_t row = (size_t)p.H * ((p.f32 ? 4 : 2) + (p.y != nullptr ? 2 : 0));
     return launch_rows(p, row_shape(p.T, p.H, row, num_sms), false, row, stream);
 }
 
 cudaError_t launch_layer_norm_backward(const LayerNormParams& p, int num_sms, cudaStream_t stream) {
-    const size_t row = (size_t)p.H * (p.f32 ? 10 : 6);
-    const RowShape s = row_shape(p.T, p.H, row, num_sms);
-    if (s.ctas > 0) {
-        const cudaError_t e = launch_rows(p, s, true, row, stream);
+    int ctas = 0;
+    if (p.T > 0) {
+        cudaError_t e;
+        if (p.H <= kNarrowBackward) {
+            e = launch_narrow(p, num_sms, true, &ctas, stream);
+        } else {
+            const size_t row = (size_t)p.H * (p.f32 ? 10 : 6);
+            const RowShape s = row_shape(p.T, p.H, row, num_sms);
+            ctas = s.ctas;
+            e = launch_rows(p, s, true, row, stream);
+        }
         if (e != cudaSuccess) return e;
     }
     if (p.d_w == nullptr && p.d_b == nullptr) return cudaSuccess;
-    return launch_kernel(true, layer_norm_columns_kernel, dim3((unsigned)((2 * (int64_t)p.H + 31) / 32)), dim3(kColumnWarps * 32), 0, stream, p, s.ctas);
+    return launch_kernel(true, layer_norm_columns_kernel, dim3((unsigned)((2 * (int64_t)p.H + 31) / 32)), dim3(kColumnWarps * 32), 0, stream, p, ctas);
 }
 
 }  // namespace ep
