@@ -735,7 +735,9 @@ EP_API ep_status_t ep_i8_pack(const ep_i8_t *w, const int8_t *codes, const float
  * long as no partial sum passes 2^24; scales are applied in fp32 and the result
  * is rounded once to bf16.
  *
- * In:  mode, capacity, counts, offsets, R, max_rows  as in ep_expert_w4.
+ * In:  mode, capacity, counts, offsets, R, max_rows  as in ep_expert_w4 (if
+ *                more than max_rows rows hold a copy, the rest is computed, or
+ *                left out and EP_ERRF_CAPACITY flagged).
  *      x         i8 [R, K], 16-byte aligned;  x_scales  f32 [R].
  * Out: y         bf16 [R, N], 16-byte aligned.  Rows that hold no copy are not
  *                written.

@@ -119,6 +119,50 @@ def test_largest_codes(K, rows):
     check([rows], 72, K, edit=edit)
 
 
+def test_long_sums():
+    """Many steps of K, shared by clusters and not."""
+    check([3], 16, 2 ** 18)
+    check([40], 24, 2 ** 16 + 16, True)
+    check([5, 0, 33, 2], 1000, 2 ** 14, max_rows=40)
+
+
+@pytest.mark.parametrize("K", [128, 4096])
+def test_more_rows_than_promised(K):
+    """All rows are computed, or what is not is left as it was and flagged."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = ep.I8Weights(*make_weights(3, 16, K, False, g))
+    x, xs = make_rows(12, K, g)
+    o, err = torch.tensor([0, 4, 8, 12], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = ep.expert_i8(x, xs, w, offsets=o)
+    out = ep.expert_i8(x, xs, w, offsets=o, max_rows=1, out=torch.full_like(want, 7.0), err_flags=err)
+    assert int(err) in (0, ep.ERRF_CAPACITY)
+    there = (out == want).all(1)
+    assert there.all() if int(err) == 0 else (there[:4].all() and (out[4:] == 7).all())
+
+
+def test_rows_past_2_to_the_31_bytes():
+    """The second expert of a capacity buffer, 2^31 bytes and more behind its start."""
+    K, N, cap = 4096, 72, 2 ** 19 + 40
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = ep.I8Weights(*make_weights(2, N, K, False, g))
+    x, xs = torch.zeros(2 * cap, K, dtype=torch.int8, device="cuda"), torch.zeros(2 * cap, device="cuda")
+    few, few_s = make_rows(2 * 30, K, g)
+    at = torch.tensor([*range(30), *range(cap, cap + 30)], device="cuda")
+    x[at], xs[at] = few, few_s
+    counts = torch.tensor([30, 30], dtype=torch.int32, device="cuda")
+    y = ep.expert_i8(x, xs, w, counts, capacity=cap, max_rows=60, out=torch.full((2 * cap, N), 7.0, dtype=torch.bfloat16, device="cuda"))
+    want = ep.expert_i8(few, few_s, w, offsets=torch.tensor([0, 30, 60], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y[at], want)
+    y[at] = 7.0
+    assert (y == 7.0).all()
+    del x
+    z = torch.zeros(2 * cap, K, dtype=torch.bfloat16, device="cuda")
+    z[at] = torch.randn(60, K, generator=g, device="cuda").bfloat16()
+    q, s = ep.quant_i8(z, counts, capacity=cap)
+    want = ep.quant_i8(z[at])
+    assert torch.equal(q[at], want[0]) and torch.equal(s[at], want[1])
+
+
 def test_no_rows():
     check([0, 0, 0], 16, 128, capacity=4, max_rows=5)
     w = ep.I8Weights(*make_weights(3, 16, 128, False, torch.Generator(device="cuda").manual_seed(0)))
