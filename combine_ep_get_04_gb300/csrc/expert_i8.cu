@@ -31,7 +31,6 @@ constexpr int kA = 2;              // steps whose weights are widened ahead
 constexpr int kB = 3;              // steps whose tokens are
 constexpr int kSteps = 6;          // barriers of steps under way: a multiple of both
 constexpr int kItems = 4;          // items found ahead
-constexpr int kPause = 2;          // steps made before the sums of the item before are written out: fewer than kB, whole rounds of loads
 constexpr int kWeightWarps = 8, kTokenWarps = 8;
 constexpr int kProducer = kWeightWarps + kTokenWarps, kIssuer = kProducer + 1, kFinder = kProducer + 2;
 constexpr int kThreads = (kFinder + 1) * 32;
@@ -428,18 +427,17 @@ __device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows, int 
     return good;
 }
 
-// An item's sums, out of tensor memory: a row of a block to a lane.  A call apart:
-// it needs the registers that hold the token codes that are on their way.
-template <int CHUNKS>
-__device__ __noinline__ bool write_sums(const I8Params& p, const Item it, uint32_t sums, int half, int row, uint32_t parity) {
+// An item's sums, out of tensor memory: a row of a block to a lane.
+__device__ __noinline__ bool write_sums(const I8Params& p, int j, uint32_t tmem) {
     Control& c = control();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 7) & 1, row = threadIdx.x & 127;
+    const Item it = c.items[j % kItems];
     const bool here = half == 0 || it.two;
     const Writer w(p, it, it.b + (here ? half : 0), row);
-    float xs[CHUNKS];
+    float xs[kTokens / 32];
 #pragma unroll
-    for (int k = 0; k < CHUNKS; ++k) xs[k] = lane + 32 * k < it.rows ? p.x_scales[it.first + lane + 32 * k] : 0.f;
-    if (!await(&c.done, parity)) return false;
+    for (int k = 0; k < kTokens / 32; ++k) xs[k] = lane + 32 * k < it.rows ? p.x_scales[it.first + lane + 32 * k] : 0.f;
+    if (!await(&c.done, j & 1)) return false;
     tcgen05_after();
     if (here) {
         uint16_t* y = w.y;
@@ -447,10 +445,10 @@ __device__ __noinline__ bool write_sums(const I8Params& p, const Item it, uint32
 #pragma unroll 1
         for (int n = 0; n < it.rows; n += 16) {
             uint32_t v[16];
-            tmem_load16(sums + n, v);
+            tmem_load16(tmem + half * kTokens + ((uint32_t)(row >> 5) * 32 << 16) + n, v);
             float mine = xs[0];
 #pragma unroll
-            for (int k = 1; k < CHUNKS; ++k) mine = n >= 32 * k ? xs[k] : mine;
+            for (int k = 1; k < kTokens / 32; ++k) mine = n >= 32 * k ? xs[k] : mine;
 #pragma unroll
             for (int i = 0; i < 16; i += 2, y += 2 * w.N)
                 w.put(n + i, y, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), [&](int r) { return __shfl_sync(0xffffffffu, mine, r); });
@@ -458,104 +456,115 @@ __device__ __noinline__ bool write_sums(const I8Params& p, const Item it, uint32
     }
     tcgen05_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&c.drained);
+    if (lane == 0) {
+        mbar_arrive(&c.drained);
+        mbar_arrive(&c.item_empty[j % kItems]);
+    }
     return true;
+}
+
+__device__ __forceinline__ void store_shared(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // Tokens: a thread has 16 channels of every 32nd row, of up to 32 CHUNKS, and loads
 // them AHEAD steps ahead: with HBM busy an L2 hit takes some 1700 cycles, longer
-// than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).  The
-// same warps write the sums out (where `whole` is set: K is not shared).
+// than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).
 template <int CHUNKS, int AHEAD>
-__device__ __noinline__ bool widen_tokens(const I8Params& params, uint32_t tmem, int k0, int steps, int tile_rows, int ring, bool whole) {
+__device__ __noinline__ bool widen_tokens(const I8Params& p, uint32_t tmem, int k0, int steps, int tile_rows, int ring, bool writes) {
+    static_assert(kSteps == 2 * kB && AHEAD <= kB, "");
     Control& c = control();
-    const I8Params& p = params;
-    const int K = p.w.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, run = run_bytes(tile_rows);
-    const int t = threadIdx.x - kWeightWarps * 32, n0 = t >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
-    const uint32_t sums = tmem + half * kTokens + ((uint32_t)(warp & 3) * 32 << 16);
-    unsigned char* ops = ring_base() + ring * kRingBytes + (t & 7) * run + n0 * 16;
-    const int8_t* first_x = p.x + (int64_t)k0 * kStep + (t & 7) * 16;
+    const int K = p.w.K, run = run_bytes(tile_rows);
+    const int t = threadIdx.x - kWeightWarps * 32, n0 = t >> 3;
+    const uint32_t ops = smem_addr(ring_base()) + ring * kRingBytes + (t & 7) * run + n0 * 16;
+    const int8_t* const first_x = p.x + (int64_t)k0 * kStep + (t & 7) * 16 + (int64_t)n0 * K;
     const int left = K - k0 * kStep - (t & 7) * 16;            // channels from the thread's on
-    int made = 0;                            // steps, up to kB
-    Item it, last{};
-    Place g, b, before;                      // this step's barrier and room; the barrier of the room's last step
+    bool full = false;                       // whether all rooms have been used
+    Place g;                                 // this step's barrier
     uint4 raw[AHEAD][CHUNKS];
     for (int j = 0;; ++j) {
-        if (!next_item(j, &it)) return false;
-        const int count = it.e >= 0 ? steps : 0;               // the end comes as an item without steps
-        static_assert(kPause % AHEAD == 0 && kPause < kB, "");
-        bool pending = j > 0 && whole;                         // the sums of the item before
-        const int8_t* x = first_x + ((int64_t)it.first + n0) * K;
+        const int slot = j % kItems;
+        if (!await(&c.item_full[slot], (j / kItems) & 1)) return false;
+        const int count = c.items[slot].e >= 0 ? steps : 0;    // the end comes as an item without steps
+        const int rows = c.items[slot].rows - n0;              // from the thread's first on
+        const int8_t* x = first_x + (int64_t)c.items[slot].first * K;
+        __syncwarp();
+        if (!writes && (threadIdx.x & 31) == 0) mbar_arrive(&c.item_empty[slot]);
         auto fetch = [&](uint4 (&r)[CHUNKS], int step) {
             const bool in = step < count && step * kStep < left;
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i) {
                 r[i] = make_uint4(0, 0, 0, 0);                 // channels past the end
-                if (n0 + 32 * i < it.rows && in) r[i] = *reinterpret_cast<const uint4*>(x + (uint32_t)(32 * i) * (uint32_t)K + (uint32_t)(step * kStep));
+                if (32 * i < rows && in) r[i] = *reinterpret_cast<const uint4*>(x + (uint32_t)(32 * i) * (uint32_t)K + (uint32_t)(step * kStep));
             }
         };
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) fetch(raw[u], u);
         for (int base = 0;; base += AHEAD) {
-            // the item's first steps are made while the products of the one before end; then the sums of that are written out
-            if (pending && base >= min(kPause, count)) {
-                pending = false;
-                if (!write_sums<CHUNKS>(p, last, sums, half, row, (j - 1) & 1)) return false;
-            }
+            if (CHUNKS == 1 && writes && j > 0 && base == min(AHEAD, (count + AHEAD - 1) / AHEAD * AHEAD))
+                if (!write_sums(p, j - 1, tmem)) return false;
             if (base >= count) break;
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 const int i = base + u;
                 if (i >= count) break;
-                if (made < kB) {
-                    ++made;
-                } else {
-                    if (!await(&c.op_done[before.at], before.parity)) return false;
-                    before.next(kSteps);
-                }
-                unsigned char* to = ops + b.at * kRuns * run;
+                const bool late = g.at >= kB;
+                const int room = late ? g.at - kB : g.at;
+                // the room's last step was kB ago
+                if ((full || late) && !await(&c.op_done[late ? room : room + kB], late ? g.parity : g.parity ^ 1)) return false;
+                const uint32_t to = ops + room * kRuns * run;
 #pragma unroll
                 for (int m = 0; m < CHUNKS; ++m) {
-                    if (n0 + 32 * m < it.rows) {
+                    if (32 * m < rows) {
                         uint4 lo, hi;
                         widen(raw[u][m].x ^ 0x80808080u, &lo.x, &lo.y);
                         widen(raw[u][m].y ^ 0x80808080u, &lo.z, &lo.w);
                         widen(raw[u][m].z ^ 0x80808080u, &hi.x, &hi.y);
                         widen(raw[u][m].w ^ 0x80808080u, &hi.z, &hi.w);
-                        *reinterpret_cast<uint4*>(to + 32 * m * 16) = lo;
-                        *reinterpret_cast<uint4*>(to + 8 * run + 32 * m * 16) = hi;
+                        store_shared(to + 32 * m * 16, lo.x, lo.y, lo.z, lo.w);
+                        store_shared(to + 8 * run + 32 * m * 16, hi.x, hi.y, hi.z, hi.w);
                     }
                 }
                 fetch(raw[u], i + AHEAD);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c.op_full[g.at]);
+                if ((threadIdx.x & 31) == 0) mbar_arrive(&c.op_full[g.at]);
                 g.next(kSteps);
-                b.next(kB);
+                full = full || g.at == 0;
             }
         }
-        if (it.e < 0) return true;
-        last = it;
+        if (count == 0) return true;
     }
 }
 
 // Weights: a thread has one row of one block, of two (a group of warps each), or
 // of one in every other step: what a step costs a group is mostly waiting, for
 // barriers, shared memory and tensor memory in turn.
+//
+// Who writes the sums out (`writes`; where K is shared, join_shares does) gives an
+// item's place back when that is done: these warps for wide tiles, where the tokens'
+// have the most to do and no registers left, else the tokens' (256 experts, 4 rows
+// each, 2048 -> 7168: 532 us so, 568 by these).
 template <int TURNS>
-__device__ __noinline__ bool widen_weights(uint32_t tmem, int steps, int ring) {
+__device__ __noinline__ bool widen_weights(const I8Params& p, uint32_t tmem, int steps, int ring, bool writes) {
     Control& c = control();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, half = TURNS > 1 ? 0 : group;
     const uint32_t to = tmem + 2 * kTokens + half * kAColumns + ((uint32_t)(warp & 3) * 32 << 16);
     const unsigned char* from = ring_base() + half * kStepBytes + (threadIdx.x & 127) * 16;
     int n = 0;                               // steps so far, in turns' places
-    Item it;
     Place g, a, r, before;                   // the step's barrier, its room, the ring's; the barrier of the room's last step
     for (int j = 0;; ++j) {
-        if (!next_item(j, &it)) return false;
-        if (it.e < 0) return true;
-        const bool here = half == 0 || it.two;
-        for (int i = 0; i < steps; ++i) {
+        const int slot = j % kItems;
+        if (!await(&c.item_full[slot], (j / kItems) & 1)) return false;
+        const int count = c.items[slot].e >= 0 ? steps : 0;        // the end comes as an item without steps
+        const bool here = half == 0 || c.items[slot].two;
+        __syncwarp();
+        if (!writes && lane == 0) mbar_arrive(&c.item_empty[slot]);
+        for (int i = 0;; ++i) {
+            // an item's first steps are made while the products of the one before end; then the sums of that are written out
+            if (writes && j > 0 && i == min(kA, count))
+                if (!write_sums(p, j - 1, tmem)) return false;
+            if (i >= count) break;
             if (TURNS == 1 || (n & 1) == group) {
                 if (!await(&c.ring_full[r.at], r.parity)) return false;
                 uint32_t v[2][32];
@@ -581,13 +590,13 @@ __device__ __noinline__ bool widen_weights(uint32_t tmem, int steps, int ring) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.op_full[g.at]);
             }
-            if (n >= kA)
-                before.next(kSteps);
+            if (n >= kA) before.next(kSteps);
             n = n < kA + 2 ? n + 1 : n - 1;              // its parity and whether it is below kA are all that counts
             r.next(ring);
             g.next(kSteps);
             a.next(kA);
         }
+        if (count == 0) return true;
     }
 }
 
@@ -656,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
             mbar_init(&c.item_empty[i], kItemReaders);
         }
         mbar_init(&c.done, 1);
-        mbar_init(&c.drained, kTokenWarps);
+        mbar_init(&c.drained, kWeightWarps);
         fence_mbar_init();
     }
     // a share may push to another once that runs
@@ -686,9 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
         if (elect_one()) good = issue(c.tmem, steps, tile_rows, ring);
     } else if (warp >= kWeightWarps) {
         good = tile_rows <= 32 ? widen_tokens<1, 2>(p, c.tmem, k0, steps, tile_rows, ring, splits == 1)
-                               : widen_tokens<4, 2>(p, c.tmem, k0, steps, tile_rows, ring, splits == 1);
+                               : widen_tokens<4, 3>(p, c.tmem, k0, steps, tile_rows, ring, false);
     } else {
-        good = width == 1 ? widen_weights<2>(c.tmem, steps, ring) : widen_weights<1>(c.tmem, steps, ring);
+        const bool writes = splits == 1 && tile_rows > 32;
+        good = width == 1 ? widen_weights<2>(p, c.tmem, steps, ring, writes) : widen_weights<1>(p, c.tmem, steps, ring, writes);
     }
     __syncwarp();
     good = __all_sync(0xffffffffu, good);
