@@ -89,7 +89,7 @@ __device__ __forceinline__ Vec8 round_bf16(const Vec8& x) {
 // which never subtracts large squares from each other.
 //
 // T=16384 H=4096 fp32 with dropout 132 us, 6.1 TB/s, 91 % of the measured copy rate;
-// T=4096 H=7168 bf16 39 us, 6.0 TB/s, with dropout 56 us, 4.2 TB/s: 310 instructions
+// T=4096 H=7168 bf16 40.5 us, 5.8 TB/s, with dropout 56 us, 4.2 TB/s: 310 instructions
 // a vector of a warp, twenty of them the generator's wide products, with 14 warps to
 // hide each other's waits.  (The two rows' sums each in chains of their own: 63 us;
 // twice the warps with half the registers 60, spilled ones among them; keys of the
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(LayerNormParams p, 
 // layer_norm_columns_kernel adds them in CTA order, so that nothing depends on
 // the order in which CTAs run.
 //
-// T=16384 H=4096 fp32 with dropout 170 us, 6.3 TB/s, 94 %; T=4096 H=7168 bf16 57 us,
+// T=16384 H=4096 fp32 with dropout 174 us, 6.2 TB/s, 92 %; T=4096 H=7168 bf16 57 us,
 // 5.1 TB/s: as above.
 template <int NV, bool F32, bool DROP, int THREADS>
 __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(LayerNormParams p, int warps, int stages) {

@@ -29,6 +29,7 @@ from ._tensors import _empty, _ptr, _rows_ptr, _shaped_ptr, _stream
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
 _MASK64 = 2 ** 64 - 1
+_PAIR = torch.Size((2,))
 
 
 def dropout(x: torch.Tensor, p: float, rng: torch.Tensor | None, site: int = 0, residual: torch.Tensor | None = None,
@@ -40,21 +41,22 @@ def dropout(x: torch.Tensor, p: float, rng: torch.Tensor | None, site: int = 0, 
     None: nothing is dropped.  site tells the dropouts of one step apart.  out
     may be x or residual.  The gradient with respect to x is dropout(d_out, p,
     rng, site)."""
-    lib = load()
-    if x.dim() != 2:
-        raise ValueError(f"x must be [T, H], got {tuple(x.shape)}")
-    if x.dtype not in _TYPES:
-        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
-    shape = (x.shape[0], x.shape[1])
-    if shape[1] == 0:
+    lib, shape, dtype = load(), x.shape, x.dtype
+    if len(shape) != 2:
+        raise ValueError(f"x must be [T, H], got {tuple(shape)}")
+    kind = _TYPES.get(dtype)
+    if kind is None:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {dtype}")
+    T, H = shape
+    if H == 0:
         raise ValueError("x has no columns")
-    xp, ld_x = _rows_ptr(x, x.dtype, "x", shape)
-    rp, ld_res = _rows_ptr(residual, x.dtype, "residual", shape)
-    gp = _shaped_ptr(rng, torch.int64, "rng", (2,))
+    xp, ld_x = _rows_ptr(x, dtype, "x", shape)
+    rp, ld_res = (None, 0) if residual is None else _rows_ptr(residual, dtype, "residual", shape)
     if out is None:
-        out = _empty(shape, x.dtype, x.device, stream)
-    op, ld_out = _rows_ptr(out, x.dtype, "out", shape)
-    st = lib.ep_dropout(shape[0], shape[1], _TYPES[x.dtype], xp, ld_x, rp, ld_res, p, gp, site & _MASK64, op, ld_out, _stream(stream))
+        out = _empty(shape, dtype, x.device, stream)
+    op, ld_out = _rows_ptr(out, dtype, "out", shape)
+    st = lib.ep_dropout(T, H, kind, xp, ld_x, rp, ld_res, p, _shaped_ptr(rng, torch.int64, "rng", _PAIR), site & _MASK64, op, ld_out,
+                        _stream(stream))
     if st:
         check(st, "ep_dropout")
     return out
@@ -99,7 +101,7 @@ class LayerNorm:
         self.stats = torch.empty((2, T), **f32) if train else None
         self.err_flags = torch.zeros(1, dtype=torch.int32, device=dev)      # OR-ed into; the caller clears it
         self.workspace = self.grads = None
-        self._lib, self._shape, self._row = lib, (T, H), (H,)
+        self._lib, self._shape, self._row = lib, torch.Size((T, H)), torch.Size((H,))
         self._n, self._stats, self._flags = _ptr(self.n), _ptr(self.stats), _ptr(self.err_flags)
         if train:
             self.workspace = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
@@ -111,23 +113,20 @@ class LayerNorm:
                                             d_w=torch.empty(H, **f32) if weight else None, d_b=torch.empty(H, **f32) if bias else None)
             self._outputs = (_ptr(d_h), _ptr(d_y), _ptr(g.d_w), _ptr(g.d_b), _ptr(self.workspace), self.workspace_bytes, self._flags)
 
-    def _wanted(self, t, wanted, name):
-        if (t is not None) != wanted:
-            raise ValueError(f"{name} is {'missing' if wanted else 'not part of this norm'}")
-
     def forward(self, h: torch.Tensor, y: torch.Tensor | None = None, w: torch.Tensor | None = None, b: torch.Tensor | None = None,
                 rng: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
         """Returns (h_out, n).  rng i64 [2] on the device (seed, step); None:
         nothing is dropped."""
-        self._wanted(y, self.block, "y")
-        self._wanted(w, self.weight, "w")
-        self._wanted(b, self.bias, "b")
+        if (y is None) is self.block or (w is None) is self.weight or (b is None) is self.bias:
+            for t, wanted, name in ((y, self.block, "y"), (w, self.weight, "w"), (b, self.bias, "b")):
+                if (t is not None) != wanted:
+                    raise ValueError(f"{name} is {'missing' if wanted else 'not part of this norm'}")
         f32 = torch.float32
         hp, ld_h = _rows_ptr(h, self.dtype, "h", self._shape)
         yp, ld_y = _rows_ptr(y, torch.bfloat16, "y", self._shape)
         st = self._lib.ep_layer_norm(
             self._ref, hp, ld_h, yp, ld_y, _shaped_ptr(w, f32, "w", self._row), _shaped_ptr(b, f32, "b", self._row),
-            _shaped_ptr(rng, torch.int64, "rng", (2,)), None if self.h_out is None else self.h_out.data_ptr() or None, self._n,
+            _shaped_ptr(rng, torch.int64, "rng", _PAIR), None if self.h_out is None else self.h_out.data_ptr() or None, self._n,
             self._stats, self._flags, _stream(stream))
         if st:
             check(st, "ep_layer_norm")
@@ -140,10 +139,11 @@ class LayerNorm:
         and rng, and the gradients of its outputs (d_h_out may be None: zero)."""
         if not self.train:
             raise ValueError("this norm was made without train=True")
-        self._wanted(w, self.weight, "w")
+        if (w is None) is self.weight:
+            raise ValueError(f"w is {'missing' if self.weight else 'not part of this norm'}")
         hp, ld_h = _rows_ptr(h_out, self.dtype, "h_out", self._shape)
         st = self._lib.ep_layer_norm_backward(
-            self._ref, hp, ld_h, _shaped_ptr(w, torch.float32, "w", self._row), _shaped_ptr(rng, torch.int64, "rng", (2,)), self._stats,
+            self._ref, hp, ld_h, _shaped_ptr(w, torch.float32, "w", self._row), _shaped_ptr(rng, torch.int64, "rng", _PAIR), self._stats,
             _shaped_ptr(d_h_out, self.dtype, "d_h_out", self._shape), _shaped_ptr(d_n, torch.bfloat16, "d_n", self._shape),
             *self._outputs, _stream(stream))
         if st:

@@ -265,18 +265,19 @@ def test_one_mask_in_all_calls():
     assert torch.equal(h_out != 0, mask) and torch.equal(d.d_y != 0, mask) and torch.equal(d.d_y, ep.dropout(one, p, rng, site))
 
 
-def test_in_place():
+@pytest.mark.parametrize("H", [256, 520, 2056, 8200])
+def test_in_place(H):
     g = generator(0)
-    h, y, d_n, dh = rows_of(g, 700, 520, F32), rows_of(g, 700, 520, BF16), rows_of(g, 700, 520, BF16), rows_of(g, 700, 520, F32)
-    m = ep.LayerNorm(700, 520, F32, p=0.1, weight=False, bias=False, train=True)
+    h, y, d_n, dh = rows_of(g, 700, H, F32), rows_of(g, 700, H, BF16), rows_of(g, 700, H, BF16), rows_of(g, 700, H, F32)
+    m = ep.LayerNorm(700, H, F32, p=0.1, weight=False, bias=False, train=True)
     rng = words(1, 2)
     h_out, n = (t.clone() for t in m.forward(h, y, rng=rng))
     d_h = m.backward(h_out, None, d_n, dh, rng).d_h.clone()
     lib, stream = ep.load(), torch.cuda.current_stream().cuda_stream
-    assert lib.ep_layer_norm(m._ref, h.data_ptr(), 520, y.data_ptr(), 520, None, None, rng.data_ptr(), h.data_ptr(), m.n.data_ptr(), None, None,
+    assert lib.ep_layer_norm(m._ref, h.data_ptr(), H, y.data_ptr(), H, None, None, rng.data_ptr(), h.data_ptr(), m.n.data_ptr(), None, None,
                              stream) == 0
     assert torch.equal(h, h_out) and torch.equal(m.n, n)
-    assert lib.ep_layer_norm_backward(m._ref, h.data_ptr(), 520, None, rng.data_ptr(), m.stats.data_ptr(), dh.data_ptr(), d_n.data_ptr(),
+    assert lib.ep_layer_norm_backward(m._ref, h.data_ptr(), H, None, rng.data_ptr(), m.stats.data_ptr(), dh.data_ptr(), d_n.data_ptr(),
                                       dh.data_ptr(), None, None, None, m.workspace.data_ptr(), m.workspace_bytes, None, stream) == 0
     assert torch.equal(dh, d_h)
 
