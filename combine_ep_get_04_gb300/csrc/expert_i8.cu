@@ -11,6 +11,9 @@
 // widen them into tensor memory, a row to a thread, which is the instruction's A
 // operand; eight more load token codes, several steps ahead, and widen them into
 // shared memory (B), and write the sums out; one thread issues the products.
+//
+// That chain of roles costs some 7 us before the first sum is out, so a batch of little
+// work goes another way (expert_i8_few_kernel).
 #include <algorithm>
 #include <atomic>
 
@@ -725,6 +728,111 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
     }
 }
 
+// ------------------------------------------------------------ little work
+//
+// No stages, no tensor memory, nothing to wait for but the weights.  A CTA has 16
+// weight rows (of a pair 8 gate rows and their up rows) and up to 8 token rows; its
+// warps take the steps of K in turn, straight from memory into the operands of
+// mma.m16n8k32 in 8-bit integers, whose rate is enough for eight tokens.  The packed
+// order suits it as it is: a thread's 16 bytes of a row are four products' operands,
+// and the tokens' side of the four is 32 channels in a row.  Codes are stored plus
+// 128; a token's sum of codes, times 128, comes off at the end.  Whole numbers of 32
+// bits throughout, so the sums are exact and their order does not matter.
+//
+// Bound by the latency of memory, a warp's 2 KB a step: 16 warps with a step on its way
+// while there are two CTAs an SM at most, else 8 warps with two (three would leave room
+// for two CTAs instead of three: one row, 7168 -> 18432, 29.6 us against 25.5).  One
+// row, 7168 -> 4096: 7.5 us, 3.9 TB/s (8 warps 9.7 us); 1024 -> 1024: 2.5 us.
+
+constexpr int kFewRows = 8;               // token rows of a tile
+constexpr int kMaxFewK = 65536;           // 255 * 128 * K fits 31 bits
+
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool PAIRED, int kWarps, int kAhead>
+__global__ void __launch_bounds__(kWarps * 32) expert_i8_few_kernel(I8Params p, int grid_tiles) {
+    constexpr int kSecond = PAIRED ? 16 : 8;                           // from a thread's first weight row to its other
+    __shared__ int sums[kWarps][16][kFewRows], token_sums[kWarps][kFewRows];
+    __shared__ RowTile shared_tile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int nb = row_blocks(p.w), nk = k_steps(p.w), b = blockIdx.x / 8, group = blockIdx.x % 8;
+    const int row0 = PAIRED ? group / 2 * 32 + group % 2 * 8 : group * 16;
+    pdl_launch_dependents();
+    pdl_wait();
+    RowTile tile;
+    if (p.w.E == 1) {
+        tile = tile_of_one(p, blockIdx.y, kFewRows, grid_tiles);
+    } else {
+        if (warp == 0) {
+            const RowTile r = find_tile(p, blockIdx.y, kFewRows, grid_tiles);
+            if (lane == 0) shared_tile = r;
+        }
+        __syncthreads();
+        tile = shared_tile;
+    }
+    if (tile.e < 0) return;
+    const unsigned char* packed = static_cast<const unsigned char*>(p.packed);
+    const unsigned char* weights = packed + ((int64_t)tile.e * nb + b) * nk * kStepBytes + (t * kRows + row0 + g) * 16;
+    const int8_t* x = p.x + (tile.first + g) * p.w.K + 32 * t;
+    uint4 a[kAhead][4], q[kAhead][2];
+    auto fetch = [&](int s, uint4 (&a)[4], uint4 (&q)[2]) {
+        q[0] = q[1] = make_uint4(0, 0, 0, 0);
+        if (s >= nk) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)            // both rows, then the same four units of 16 bytes further
+            a[i] = *reinterpret_cast<const uint4*>(weights + (int64_t)s * kStepBytes + ((i >> 1) * 4 * kRows + (i & 1) * kSecond) * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (g < tile.rows && s * kStep + 32 * t + 16 * h < p.w.K) q[h] = *reinterpret_cast<const uint4*>(x + s * kStep + 16 * h);
+    };
+    int acc[4] = {}, token = 0;
+    auto multiply = [&](const uint4 (&a)[4], const uint4 (&q)[2]) {
+        const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) token = __dp4a((int)w[i], 0x01010101, token);
+        mma_u8s8(acc, a[0].x, a[1].x, a[2].x, a[3].x, w[0], w[2]);
+        mma_u8s8(acc, a[0].y, a[1].y, a[2].y, a[3].y, w[1], w[3]);
+        mma_u8s8(acc, a[0].z, a[1].z, a[2].z, a[3].z, w[4], w[6]);
+        mma_u8s8(acc, a[0].w, a[1].w, a[2].w, a[3].w, w[5], w[7]);
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(warp + i * kWarps, a[i], q[i]);
+    for (int s = warp; s < nk; s += kAhead * kWarps) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s + i * kWarps >= nk) break;
+            multiply(a[i], q[i]);
+            fetch(s + (kAhead + i) * kWarps, a[i], q[i]);
+        }
+    }
+    token += __shfl_xor_sync(0xffffffffu, token, 1);
+    token += __shfl_xor_sync(0xffffffffu, token, 2);
+    if (t == 0) token_sums[warp][g] = token;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[warp][g + (i >> 1) * 8][2 * t + (i & 1)] = acc[i];
+    __syncthreads();
+    // a channel to a thread
+    constexpr int kChannels = PAIRED ? 8 : 16;
+    const int row = threadIdx.x % kChannels, n = threadIdx.x / kChannels, c = b * (PAIRED ? kRows / 2 : kRows) + group * kChannels + row;
+    if (n >= tile.rows || c >= p.w.N) return;
+    int less = 0, first = 0, second = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        less += token_sums[w][n];
+        first += sums[w][row][n];
+        if (PAIRED) second += sums[w][row + 8][n];
+    }
+    const float* scales = reinterpret_cast<const float*>(packed + scales_at(p.w)) + ((int64_t)tile.e * nb + b) * kRows + row0 + row;
+    const float xs = p.x_scales[tile.first + n];
+    float f = (float)(first - 128 * less) * scales[0] * xs;
+    if (PAIRED) f = silu(f) * ((float)(second - 128 * less) * scales[16] * xs);
+    static_cast<uint16_t*>(p.y)[(tile.first + n) * p.w.N + c] = (uint16_t)pack_bf16x2(f, 0.f);
+}
+
 // Tiles of up to `tile` rows that max_rows rows of E experts make at most.
 int64_t most_tiles(int E, int64_t max_rows, int tile) {
     const int64_t used = std::min<int64_t>(E, max_rows);
@@ -773,11 +881,23 @@ int clusters_at_once(int splits) {
 }  // namespace
 
 cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream) {
+    // Small CTAs where an SM gets 8 of them at most and, if they read weights more than once, 300 steps: one row of 7168 ->
+    // 4096 in 7.5 us against the tiles' 13.3, 4 experts' pairs of 7168 -> 2048 (1024 CTAs) in 26.5 against 29.5, 32 rows of
+    // 1024 -> 1024 in 2.8 against 10.7, of 7168 -> 1024 (118 steps) in 7.9 against 12.9; but 64 rows of 7168 -> 2048 (424
+    // steps) in 21.3 against 16.6, 8 experts of 2048 -> 7168 (3584 CTAs) in 36.7 against 30.1.
+    const int64_t few_tiles = most_tiles(p.w.E, p.max_rows, kFewRows), few_ctas = few_tiles * row_blocks(p.w) * 8;
+    const bool once = few_tiles == std::min<int64_t>(p.w.E, p.max_rows);
+    if (few_ctas <= 8 * num_sms && (once || few_ctas * k_steps(p.w) <= 300 * num_sms) && p.w.K <= kMaxFewK) {
+        const bool wide = few_ctas <= 2 * num_sms;
+        const auto kernel = p.w.paired ? (wide ? expert_i8_few_kernel<true, 16, 1> : expert_i8_few_kernel<true, 8, 2>)
+                                       : (wide ? expert_i8_few_kernel<false, 16, 1> : expert_i8_few_kernel<false, 8, 2>);
+        return launch_kernel(true, kernel, dim3((unsigned)(few_ctas / few_tiles), (unsigned)few_tiles), dim3(wide ? 512 : 256), 0, stream, p, (int)few_tiles);
+    }
     const cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kControlBytes + kSmemBytes);
     if (e != cudaSuccess) return e;
     // Tiles of twice the mean rows: the smaller the tile, the longer the ring.  Then as many items as there are SMs: by
     // single blocks, by smaller tiles, by shares of K, of which a cluster that did not run at once would double the time
-    // (one row, 7168 -> 4096: 16 clusters of 8 23 us, of 4 16.5).
+    // (one row, 7168 -> 4096, by this kernel: 16 clusters of 8 23 us, of 4 16.5).
     const int nb = row_blocks(p.w);
     int tile = kTokens, width = 2, splits = 1;
     while (tile > 32 && p.max_rows * 4 <= (int64_t)p.w.E * tile) tile /= 2;

@@ -731,9 +731,9 @@ EP_API ep_status_t ep_i8_pack(const ep_i8_t *w, const int8_t *codes, const float
  * ep_expert_i8 -- every expert's product over its rows of the receive buffer:
  *   y[r, n] = x_scale[r] * scale[e, n] * sum_k x[r, k] * code[e, n, k]
  * for the rows r of expert e (paired: silu of the gate product times the up
- * product).  Products of codes are exact and summed in fp32, which is exact as
- * long as no partial sum passes 2^24; scales are applied in fp32 and the result
- * is rounded once to bf16.
+ * product).  Products of codes are exact and summed in fp32 (a batch of little
+ * work: in 32-bit integers), which is exact as long as no partial sum passes
+ * 2^24; scales are applied in fp32 and the result is rounded once to bf16.
  *
  * In:  mode, capacity, counts, offsets, R, max_rows  as in ep_expert_w4 (if
  *                more than max_rows rows hold a copy, the rest is computed, or

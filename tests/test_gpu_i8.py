@@ -76,6 +76,37 @@ def test_rows_of_one_matrix(rows):
     check([rows], 200, 272)
 
 
+@pytest.mark.parametrize("K", [16, 48, 64, 112, 128, 144, 1008, 4096, 7168])
+@pytest.mark.parametrize("paired", [False, True])
+def test_wide_matrices(K, paired):
+    """As much work as goes in tiles of up to 128 rows, in shares of K too."""
+    N = 1032 if paired else 2056
+    check([100], N, K, paired, bare=K == 64)
+    check([3, 0, 60, 17], N, K, paired)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+def test_rows_of_a_wide_matrix(rows):
+    check([rows], 20008, 144)
+    check([rows], 10008, 80, True)
+
+
+@pytest.mark.parametrize("K", [2 ** 16, 2 ** 16 + 16])
+def test_largest_sums_of_integers(K):
+    """The longest sums that 32-bit integers hold, and the next, which go in fp32: all terms at an end, of either sign.
+    The integers are exact up to three roundings (2^-24 each) and bf16's."""
+    codes = torch.full((1, 16, K), -128, dtype=torch.int8, device="cuda")
+    codes[:, 8:] = 127
+    x = torch.full((4, K), -128, dtype=torch.int8, device="cuda")
+    x[1::2] = 127
+    w = ep.I8Weights(codes, torch.ones(1, 16, device="cuda"))
+    got = ep.expert_i8(x, torch.ones(4, device="cuda"), w).double().cpu()
+    want = x[:, :1].double().cpu() @ codes[0, :, :1].double().cpu().t() * K
+    # in fp32 K terms, each cut off at 2^-23 of the sum at most
+    bound = want.abs() * (2.0 ** -8 + 2.0 ** -22 + (0 if K <= 2 ** 16 else K * 2.0 ** -23))
+    assert ((got - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("capacity", [None, 12])
 def test_experts_with_few_rows(capacity):
     counts = [3, 0, 1, 12, 0, 0, 5, 9, 8, 2, 1, 4, 0]
@@ -88,6 +119,8 @@ def test_uneven_experts(capacity):
     check([70, 0, 1, 2, 0, 3], 64, 256, capacity=capacity)
     check([0, 0, 129, 2], 64, 256, True, capacity=capacity)
     check([40, 40, 39, 33, 64], 64, 256, capacity=capacity)
+    check([70, 0, 1, 2, 0, 3], 2600, 256, capacity=capacity)
+    check([0, 0, 129, 2], 1304, 256, True, capacity=capacity)
 
 
 def test_many_experts():
@@ -110,13 +143,29 @@ def test_many_row_blocks():
 
 
 @pytest.mark.parametrize("K,rows", [(128, 5), (1024, 40), (16384, 3), (16384, 200)])
-def test_largest_codes(K, rows):
+@pytest.mark.parametrize("N", [72, 2056])
+def test_largest_codes(K, rows, N):
     """All codes at an end: sums of up to 2^14 K, a power of two times a sum of powers of two, held exactly."""
     def edit(codes, x):
         codes.fill_(-128)
         x.fill_(-128)
         x[1::2] = 127
-    check([rows], 72, K, edit=edit)
+    check([rows], N, K, edit=edit)
+
+
+@pytest.mark.parametrize("N,paired", [(2056, False), (1032, True)])
+@pytest.mark.parametrize("K", [272, 7168])
+def test_a_row_is_the_same_in_every_batch(N, paired, K):
+    """Sums below 2^24 are exact in integers and in fp32, in whatever shares."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    codes, scales = make_weights(1, N, K, paired, g)
+    w = ep.I8Weights(codes, scales, paired)
+    x, xs = make_rows(700, K, g)
+    xs *= 30 / K ** 0.5                                       # gates on both sides of 0, not all far out
+    assert (x.float() @ codes[0].float().t()).abs().max() < 2 ** 24
+    whole = ep.expert_i8(x, xs, w)
+    for rows in (1, 5, 33, 100):
+        assert torch.equal(ep.expert_i8(x[:rows], xs[:rows], w), whole[:rows]), rows
 
 
 def test_long_sums():
@@ -126,11 +175,12 @@ def test_long_sums():
     check([5, 0, 33, 2], 1000, 2 ** 14, max_rows=40)
 
 
+@pytest.mark.parametrize("N", [16, 20008])
 @pytest.mark.parametrize("K", [128, 4096])
-def test_more_rows_than_promised(K):
+def test_more_rows_than_promised(K, N):
     """All rows are computed, or what is not is left as it was and flagged."""
     g = torch.Generator(device="cuda").manual_seed(0)
-    w = ep.I8Weights(*make_weights(3, 16, K, False, g))
+    w = ep.I8Weights(*make_weights(3, N, K, False, g))
     x, xs = make_rows(12, K, g)
     o, err = torch.tensor([0, 4, 8, 12], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     want = ep.expert_i8(x, xs, w, offsets=o)
@@ -140,9 +190,10 @@ def test_more_rows_than_promised(K):
     assert there.all() if int(err) == 0 else (there[:4].all() and (out[4:] == 7).all())
 
 
-def test_rows_past_2_to_the_31_bytes():
+@pytest.mark.parametrize("N", [72, 2056])
+def test_rows_past_2_to_the_31_bytes(N):
     """The second expert of a capacity buffer, 2^31 bytes and more behind its start."""
-    K, N, cap = 4096, 72, 2 ** 19 + 40
+    K, cap = 4096, 2 ** 19 + 40
     g = torch.Generator(device="cuda").manual_seed(0)
     w = ep.I8Weights(*make_weights(2, N, K, False, g))
     x, xs = torch.zeros(2 * cap, K, dtype=torch.int8, device="cuda"), torch.zeros(2 * cap, device="cuda")
@@ -171,10 +222,11 @@ def test_no_rows():
     assert y.shape == (0, 16)
 
 
-def test_a_row_without_a_scale_stays_alone():
+@pytest.mark.parametrize("N", [64, 20008])
+def test_a_row_without_a_scale_stays_alone(N):
     """What quantisation makes of a row that holds an infinity: NaN throughout, its neighbours untouched."""
     g = torch.Generator(device="cuda").manual_seed(0)
-    w = ep.I8Weights(*make_weights(1, 64, 208, False, g))
+    w = ep.I8Weights(*make_weights(1, N, 208, False, g))
     x = torch.randn(6, 208, generator=g, device="cuda").bfloat16()
     clean = ep.expert_i8(*ep.quant_i8(x), w).clone()
     x[2, 100], x[4, 207] = float("inf"), float("nan")
@@ -198,7 +250,7 @@ def test_same_bits_twice_and_on_another_stream():
 
 def test_calls_of_several_threads():
     jobs, errors = [], []
-    for i, (rows, K) in enumerate(((4, 128), (300, 4096), (1, 7168))):
+    for i, (rows, K) in enumerate(((4, 128), (600, 4096), (1, 7168))):
         g = torch.Generator(device="cuda").manual_seed(i)
         w = ep.I8Weights(*make_weights(1, 264, K, False, g))
         x, xs = make_rows(rows, K, g)
@@ -224,14 +276,15 @@ def test_calls_of_several_threads():
     assert not errors, errors
 
 
-def test_bad_layouts_are_flagged_and_skipped():
+@pytest.mark.parametrize("N", [16, 5200])
+def test_bad_layouts_are_flagged_and_skipped(N):
     g = torch.Generator(device="cuda").manual_seed(0)
-    w = ep.I8Weights(*make_weights(3, 16, 128, False, g))
+    w = ep.I8Weights(*make_weights(3, N, 128, False, g))
     x, xs = make_rows(12, 128, g)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
 
     def run(offsets, **more):
-        out = torch.full((12, 16), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = torch.full((12, N), 7.0, dtype=torch.bfloat16, device="cuda")
         err.zero_()
         ep.expert_i8(x, xs, w, offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=out, err_flags=err, **more)
         return out, int(err)
