@@ -4,7 +4,7 @@
 // This part multiplies 8-bit integers at 151 TOP/s (mma.sync, measured), f16 at
 // thirteen times that, so the codes go through the tensor cores as f16, which
 // holds them exactly: a product of two has 15 bits and sums stay exact below 2^24.
-// Two blocks of 128 weight rows are the M side of tcgen05.mma, up to 128 token rows
+// Two blocks of 128 weight rows are the M side of tcgen05.mma, up to 160 token rows
 // the N side of both, 128 input channels a step.  One CTA an SM takes item after
 // item (two blocks with one tile of token rows).  A warp finds the items; a
 // producer warp keeps a ring of weight codes filled by bulk copies; eight warps
@@ -26,20 +26,25 @@ namespace ep {
 namespace {
 
 constexpr int kRows = 128;         // weight rows of a block
-constexpr int kTokens = 128;       // most token rows of a tile
+constexpr int kTokens = 160;       // most token rows of a tile
 constexpr int kStep = 128;         // input channels of a step
 constexpr int kStepBytes = kRows * kStep;
-constexpr int kMaxRing = 6;        // steps of weight codes
-constexpr int kA = 2;              // steps whose weights are widened ahead
+constexpr int kMaxRing = 12;       // units of weight codes: a step of one block each
+constexpr int kMaxA = 6;           // units that are widened ahead
 constexpr int kB = 3;              // steps whose tokens are
-constexpr int kSteps = 6;          // barriers of steps under way: a multiple of both
 constexpr int kItems = 4;          // items found ahead
 constexpr int kWeightWarps = 8, kTokenWarps = 8;
 constexpr int kProducer = kWeightWarps + kTokenWarps, kIssuer = kProducer + 1, kFinder = kProducer + 2;
 constexpr int kThreads = (kFinder + 1) * 32;
 constexpr int kItemReaders = kFinder;
-constexpr uint32_t kColumns = 512;                // tensor memory: the two blocks' sums, then kA x 2 A operands
+constexpr uint32_t kColumns = 512;                // tensor memory: the two blocks' sums, a tile's columns each, then A operands
 constexpr int kAColumns = kStep / 2;
+
+__host__ __device__ constexpr int a_places(int tile_rows) {
+    const int fit = ((int)kColumns - 2 * tile_rows) / kAColumns;
+    return fit < kMaxA ? fit : kMaxA;
+}
+static_assert(a_places(kTokens) >= 3, "the widest tile leaves too little for the A operands");
 
 __host__ __device__ inline int k_steps(const I8Shape& w) { return (w.K + kStep - 1) / kStep; }
 // A paired block is 64 gate rows and the 64 up rows of the same channels.
@@ -160,16 +165,15 @@ __device__ __forceinline__ void widen(uint32_t biased, uint32_t* lo, uint32_t* h
 constexpr int kRuns = kStep / 8;
 constexpr int kControlBytes = 13 * 1024;         // barriers, items and the table of experts
 constexpr int kSmemBytes = 212 * 1024;           // the rest
-constexpr int kRingBytes = 2 * kStepBytes;       // of a step
 
 __host__ __device__ constexpr int run_bytes(int tile_rows) { return (tile_rows + 1) * 16; }
-__host__ __device__ constexpr int ring_steps(int tile_rows) {
-    const int fit = (kSmemBytes - kB * kRuns * run_bytes(tile_rows)) / kRingBytes;
+__host__ __device__ constexpr int ring_units(int tile_rows) {
+    const int fit = (kSmemBytes - kB * kRuns * run_bytes(tile_rows)) / kStepBytes;
     return fit < kMaxRing ? fit : kMaxRing;
 }
-static_assert(ring_steps(kTokens) >= 3, "the widest tile leaves too little for the ring");
-// Items of one block: the two groups of weight warps take turns, and so have places of their own.
-__host__ __device__ constexpr int ring_steps(int tile_rows, int width) { return width == 1 ? ring_steps(tile_rows) & ~1 : ring_steps(tile_rows); }
+// A group that waits for unit u to arrive has seen unit u - 2 - a_places multiplied, so the place's last unit has arrived.
+constexpr bool ring_is_ahead(int tile_rows) { return ring_units(tile_rows) >= a_places(tile_rows) + 2; }
+static_assert(ring_is_ahead(kTokens) && ring_is_ahead(128) && ring_is_ahead(64) && ring_is_ahead(32), "a place of the ring could be waited for a round early");
 
 // Waits for a phase, at most kWaitLimitNs and a few tries.  A try suspends the
 // thread for a while by itself, which leaves the issue slots to others; the clock
@@ -272,7 +276,7 @@ struct Writer {
 
 // What the warps share beside the rings, at the start of shared memory.
 struct Control {
-    uint64_t ring_full[kMaxRing], ring_empty[kMaxRing], op_full[kSteps], op_done[kSteps];
+    uint64_t ring_full[kMaxRing], ring_empty[kMaxRing], a_full[kMaxA], a_done[kMaxA], b_full[kB], b_done[kB];
     uint64_t item_full[kItems], item_empty[kItems], done, drained;
     Item items[kItems];
     uint32_t tmem;
@@ -357,7 +361,7 @@ __device__ __noinline__ bool find_items(int E, int nb, int width, int tile_rows,
     }
 }
 
-// Keeps the ring of codes filled.
+// Keeps the ring of codes filled, in the order of the products: a step's first block, its second, the next step.
 __device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk, int k0, int steps, int ring) {
     Control& c = control();
     const int lane = threadIdx.x & 31;
@@ -369,17 +373,17 @@ __device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk
         good = next_item(j, &it);
         if (!good || it.e < 0) break;
         const unsigned char* weights = packed + (((int64_t)it.e * nb + it.b) * nk + k0) * kStepBytes;
-        for (int i = 0; i < steps; ++i, ++filled, weights += kStepBytes, r.next(ring)) {
-            if (filled >= ring) good = await(&c.ring_empty[r.at], r.parity);
-            if (!good) break;
-            if (lane == 0) {
-                unsigned char* to = ring_base() + r.at * kRingBytes;
-                uint64_t* bar = &c.ring_full[r.at];
-                mbar_arrive_expect_tx(bar, it.two ? kRingBytes : kStepBytes);
-                bulk_load(to, weights, kStepBytes, bar);
-                if (it.two) bulk_load(to + kStepBytes, weights + (int64_t)nk * kStepBytes, kStepBytes, bar);
+        const int blocks = it.two ? 2 : 1;
+        for (int i = 0; i < steps && good; ++i, weights += kStepBytes) {
+            for (int h = 0; h < blocks; ++h, ++filled, r.next(ring)) {
+                if (filled >= ring) good = await(&c.ring_empty[r.at], r.parity);
+                if (!good) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&c.ring_full[r.at], kStepBytes);
+                    bulk_load(ring_base() + r.at * kStepBytes, weights + (int64_t)(h * nk) * kStepBytes, kStepBytes, &c.ring_full[r.at]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
     }
     // no copy may be in flight when the CTA ends, whatever its consumers did
@@ -390,14 +394,15 @@ __device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk
 // Issues the products.  One thread: their operands then stay in uniform registers.
 __device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows, int ring) {
     Control& c = control();
-    const uint32_t a_at = tmem + 2 * kTokens, run16 = run_bytes(tile_rows) / 16;
+    const int places = a_places(tile_rows);
+    const uint32_t a_at = tmem + 2 * tile_rows, run16 = run_bytes(tile_rows) / 16;
     // runs of 8 channels run16 * 16 bytes apart, 8 rows 128 bytes apart, no swizzle
     const uint64_t desc = (uint64_t)run16 << 16 | (uint64_t)(128 / 16) << 32 | (uint64_t)1 << 46;
-    const unsigned char* ops = ring_base() + ring * kRingBytes;
+    const unsigned char* ops = ring_base() + ring * kStepBytes;
     const uint64_t first_b = desc | (smem_addr(ops) >> 4 & 0x3fff);          // in a cluster, addresses have a rank above
     int committed = 0;
     bool good = true;
-    Place g, a, b;
+    Place a, b;
     for (int j = 0; good; ++j) {
         const int slot = j % kItems;
         good = wait_phase(&c.item_full[slot], (j / kItems) & 1);
@@ -408,19 +413,19 @@ __device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows, int 
         const uint32_t cols = (rows + 15) & ~15;           // the products' N: a multiple of 16
         const uint32_t kind = 1u << 4 | (cols / 8) << 17 | (uint32_t)(kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
         if (j > 0) good = wait_phase(&c.drained, (j - 1) & 1);
-        for (int i = 0; i < steps && good; ++i, g.next(kSteps), a.next(kA), b.next(kB)) {
-            const uint32_t from_a = a_at + a.at * 2 * kAColumns;
+        for (int i = 0; i < steps && good; ++i, b.next(kB)) {
             const uint64_t from_b = first_b + (uint32_t)(b.at * kRuns) * run16;
-            good = wait_phase(&c.op_full[g.at], g.parity);
-            if (!good) break;
-            tcgen05_after();
+            good = wait_phase(&c.b_full[b.at], b.parity);
+            for (int h = 0; h <= two && good; ++h, a.next(places)) {
+                const uint32_t from_a = a_at + a.at * kAColumns, to = tmem + h * tile_rows;
+                good = wait_phase(&c.a_full[a.at], a.parity);
+                if (!good) break;
+                tcgen05_after();
 #pragma unroll
-            for (int k = 0; k < kStep / 16; ++k) mma_f16(tmem, from_a + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
-            if (two)
-#pragma unroll
-                for (int k = 0; k < kStep / 16; ++k)
-                    mma_f16(tmem + kTokens, from_a + kAColumns + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
-            tcgen05_commit(&c.op_done[g.at]);
+                for (int k = 0; k < kStep / 16; ++k) mma_f16(to, from_a + k * 8, from_b + k * 2 * run16, kind, i > 0 || k > 0);
+                tcgen05_commit(&c.a_done[a.at]);
+            }
+            if (good) tcgen05_commit(&c.b_done[b.at]);
         }
         tcgen05_commit(&c.done);
         ++committed;
@@ -431,7 +436,7 @@ __device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows, int 
 }
 
 // An item's sums, out of tensor memory: a row of a block to a lane.
-__device__ __noinline__ bool write_sums(const I8Params& p, int j, uint32_t tmem) {
+__device__ __noinline__ bool write_sums(const I8Params& p, int j, uint32_t tmem, int tile_rows) {
     Control& c = control();
     const int lane = threadIdx.x & 31, half = (threadIdx.x >> 7) & 1, row = threadIdx.x & 127;
     const Item it = c.items[j % kItems];
@@ -448,7 +453,7 @@ __device__ __noinline__ bool write_sums(const I8Params& p, int j, uint32_t tmem)
 #pragma unroll 1
         for (int n = 0; n < it.rows; n += 16) {
             uint32_t v[16];
-            tmem_load16(tmem + half * kTokens + ((uint32_t)(row >> 5) * 32 << 16) + n, v);
+            tmem_load16(tmem + half * tile_rows + ((uint32_t)(row >> 5) * 32 << 16) + n, v);
             float mine = xs[0];
 #pragma unroll
             for (int k = 1; k < kTokens / 32; ++k) mine = n >= 32 * k ? xs[k] : mine;
@@ -475,15 +480,15 @@ __device__ __forceinline__ void store_shared(uint32_t to, uint32_t a, uint32_t b
 // than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).
 template <int CHUNKS, int AHEAD>
 __device__ __noinline__ bool widen_tokens(const I8Params& p, uint32_t tmem, int k0, int steps, int tile_rows, int ring, bool writes) {
-    static_assert(kSteps == 2 * kB && AHEAD <= kB, "");
+    static_assert(AHEAD <= kB, "steps that are made before an item's sums are written find rooms");
     Control& c = control();
     const int K = p.w.K, run = run_bytes(tile_rows);
     const int t = threadIdx.x - kWeightWarps * 32, n0 = t >> 3;
-    const uint32_t ops = smem_addr(ring_base()) + ring * kRingBytes + (t & 7) * run + n0 * 16;
+    const uint32_t ops = smem_addr(ring_base()) + ring * kStepBytes + (t & 7) * run + n0 * 16;
     const int8_t* const first_x = p.x + (int64_t)k0 * kStep + (t & 7) * 16 + (int64_t)n0 * K;
     const int left = K - k0 * kStep - (t & 7) * 16;            // channels from the thread's on
     bool full = false;                       // whether all rooms have been used
-    Place g;                                 // this step's barrier
+    Place b;                                 // this step's room
     uint4 raw[AHEAD][CHUNKS];
     for (int j = 0;; ++j) {
         const int slot = j % kItems;
@@ -505,17 +510,14 @@ __device__ __noinline__ bool widen_tokens(const I8Params& p, uint32_t tmem, int 
         for (int u = 0; u < AHEAD; ++u) fetch(raw[u], u);
         for (int base = 0;; base += AHEAD) {
             if (CHUNKS == 1 && writes && j > 0 && base == min(AHEAD, (count + AHEAD - 1) / AHEAD * AHEAD))
-                if (!write_sums(p, j - 1, tmem)) return false;
+                if (!write_sums(p, j - 1, tmem, tile_rows)) return false;
             if (base >= count) break;
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 const int i = base + u;
                 if (i >= count) break;
-                const bool late = g.at >= kB;
-                const int room = late ? g.at - kB : g.at;
-                // the room's last step was kB ago
-                if ((full || late) && !await(&c.op_done[late ? room : room + kB], late ? g.parity : g.parity ^ 1)) return false;
-                const uint32_t to = ops + room * kRuns * run;
+                if (full && !await(&c.b_done[b.at], b.parity ^ 1)) return false;
+                const uint32_t to = ops + b.at * kRuns * run;
 #pragma unroll
                 for (int m = 0; m < CHUNKS; ++m) {
                     if (32 * m < rows) {
@@ -531,82 +533,88 @@ __device__ __noinline__ bool widen_tokens(const I8Params& p, uint32_t tmem, int 
                 fetch(raw[u], i + AHEAD);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if ((threadIdx.x & 31) == 0) mbar_arrive(&c.op_full[g.at]);
-                g.next(kSteps);
-                full = full || g.at == 0;
+                if ((threadIdx.x & 31) == 0) mbar_arrive(&c.b_full[b.at]);
+                b.next(kB);
+                full = full || b.at == 0;
             }
         }
         if (count == 0) return true;
     }
 }
 
-// Weights: a thread has one row of one block, of two (a group of warps each), or
-// of one in every other step: what a step costs a group is mostly waiting, for
-// barriers, shared memory and tensor memory in turn.
+// Weights: two groups of warps take the units in turn, a row to a thread: what a
+// unit costs a group is mostly waiting, for barriers, shared memory and tensor
+// memory in turn.
 //
 // Who writes the sums out (`writes`; where K is shared, join_shares does) gives an
 // item's place back when that is done: these warps for wide tiles, where the tokens'
 // have the most to do and no registers left, else the tokens' (256 experts, 4 rows
 // each, 2048 -> 7168: 532 us so, 568 by these).
-template <int TURNS>
-__device__ __noinline__ bool widen_weights(const I8Params& p, uint32_t tmem, int steps, int ring, bool writes) {
+__device__ __noinline__ bool widen_weights(const I8Params& p, uint32_t tmem, int steps, int tile_rows, int ring, bool writes) {
     Control& c = control();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, half = TURNS > 1 ? 0 : group;
-    const uint32_t to = tmem + 2 * kTokens + half * kAColumns + ((uint32_t)(warp & 3) * 32 << 16);
-    const unsigned char* from = ring_base() + half * kStepBytes + (threadIdx.x & 127) * 16;
-    int n = 0;                               // steps so far, in turns' places
-    Place g, a, r, before;                   // the step's barrier, its room, the ring's; the barrier of the room's last step
+    const int places = a_places(tile_rows);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2;
+    const uint32_t to = tmem + 2 * tile_rows + ((uint32_t)(warp & 3) * 32 << 16);
+    const unsigned char* from = ring_base() + (threadIdx.x & 127) * 16;
+    int next = group;                        // the group's next unit, from the item's first on
+    bool full = false;                       // whether all of its A operands' places have been used
+    Place a, r;                              // the unit's A operand, its place in the ring
+    if (group == 1) {
+        a.next(places);
+        r.next(ring);
+    }
     for (int j = 0;; ++j) {
         const int slot = j % kItems;
         if (!await(&c.item_full[slot], (j / kItems) & 1)) return false;
-        const int count = c.items[slot].e >= 0 ? steps : 0;        // the end comes as an item without steps
-        const bool here = half == 0 || c.items[slot].two;
+        const int count = c.items[slot].e >= 0 ? steps * (c.items[slot].two ? 2 : 1) : 0;        // the end comes as an item without units
         __syncwarp();
         if (!writes && lane == 0) mbar_arrive(&c.item_empty[slot]);
-        for (int i = 0;; ++i) {
-            // an item's first steps are made while the products of the one before end; then the sums of that are written out
-            if (writes && j > 0 && i == min(kA, count))
-                if (!write_sums(p, j - 1, tmem)) return false;
-            if (i >= count) break;
-            if (TURNS == 1 || (n & 1) == group) {
-                if (!await(&c.ring_full[r.at], r.parity)) return false;
-                uint32_t v[2][32];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint4 raw = *reinterpret_cast<const uint4*>(from + r.at * kRingBytes + q * kRows * 16);
-                    uint32_t* w = &v[q >> 2][(q & 3) * 8];
-                    widen(raw.x, w, w + 1);
-                    widen(raw.y, w + 2, w + 3);
-                    widen(raw.z, w + 4, w + 5);
-                    widen(raw.w, w + 6, w + 7);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c.ring_empty[r.at]);
-                if (n >= kA && !await(&c.op_done[before.at], before.parity)) return false;
-                tcgen05_after();
-                if (here) {
-                    tmem_store32(to + a.at * 2 * kAColumns, v[0]);
-                    tmem_store32(to + a.at * 2 * kAColumns + 32, v[1]);
-                    tmem_store_wait();
-                }
-                tcgen05_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c.op_full[g.at]);
+        bool waiting = writes && j > 0;      // the sums of the item before
+        for (;; next += 2) {
+            // an item's first units are made while the products of the one before end; then the sums of that are written out
+            if (waiting && (next >= places || next >= count)) {
+                if (!write_sums(p, j - 1, tmem, tile_rows)) return false;
+                waiting = false;
             }
-            if (n >= kA) before.next(kSteps);
-            n = n < kA + 2 ? n + 1 : n - 1;              // its parity and whether it is below kA are all that counts
-            r.next(ring);
-            g.next(kSteps);
-            a.next(kA);
+            if (next >= count) break;
+            if (!await(&c.ring_full[r.at], r.parity)) return false;
+            uint32_t v[2][32];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(from + r.at * kStepBytes + q * kRows * 16);
+                uint32_t* w = &v[q >> 2][(q & 3) * 8];
+                widen(raw.x, w, w + 1);
+                widen(raw.y, w + 2, w + 3);
+                widen(raw.z, w + 4, w + 5);
+                widen(raw.w, w + 6, w + 7);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.ring_empty[r.at]);
+            if (full && !await(&c.a_done[a.at], a.parity ^ 1)) return false;
+            tcgen05_after();
+            tmem_store32(to + a.at * kAColumns, v[0]);
+            tmem_store32(to + a.at * kAColumns + 32, v[1]);
+            tmem_store_wait();
+            tcgen05_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.a_full[a.at]);
+            // two units on
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                r.next(ring);
+                a.next(places);
+                full = full || a.at == 0;
+            }
         }
         if (count == 0) return true;
+        next -= count;
     }
 }
 
 // The sums of an item whose K a cluster shares: each CTA owns some of the tile's
 // token rows, whose sums the others push to it.  All threads of the cluster; it.e
 // is -1 where there is none.
-__device__ __noinline__ void join_shares(const I8Params& params, const Item it, uint32_t tmem, int split, int splits, bool good) {
+__device__ __noinline__ void join_shares(const I8Params& params, const Item it, uint32_t tmem, int tile_rows, int split, int splits, bool good) {
     cluster_barrier();                       // the rings are free
     const I8Params p = params;
     float* parts = reinterpret_cast<float*>(ring_base());          // [share][own][block][weight row]
@@ -617,7 +625,7 @@ __device__ __noinline__ void join_shares(const I8Params& params, const Item it, 
         tcgen05_after();
         for (int n = 0; n < it.rows; n += 16) {
             uint32_t v[16];
-            tmem_load16(tmem + half * kTokens + n + ((uint32_t)(warp & 3) * 32 << 16), v);
+            tmem_load16(tmem + half * tile_rows + n + ((uint32_t)(warp & 3) * 32 << 16), v);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (n + i < it.rows) {
@@ -663,17 +671,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
     Control& c = control();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x % splits, cluster = blockIdx.x / splits, nb = row_blocks(p.w), nk = k_steps(p.w);
-    const int ring = ring_steps(tile_rows, width), weight_warps = width == 1 ? kWeightWarps / 2 : kWeightWarps;
+    const int ring = ring_units(tile_rows);
     const int k0 = (int)((int64_t)nk * split / splits), steps = (int)((int64_t)nk * (split + 1) / splits) - k0;
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxRing; ++i) {
             mbar_init(&c.ring_full[i], 1);
-            mbar_init(&c.ring_empty[i], weight_warps);
+            mbar_init(&c.ring_empty[i], kWeightWarps / 2);
         }
-        for (int i = 0; i < kSteps; ++i) {
-            mbar_init(&c.op_full[i], weight_warps + kTokenWarps);
-            mbar_init(&c.op_done[i], 1);
+        for (int i = 0; i < kMaxA; ++i) {
+            mbar_init(&c.a_full[i], kWeightWarps / 2);
+            mbar_init(&c.a_done[i], 1);
+        }
+        for (int i = 0; i < kB; ++i) {
+            mbar_init(&c.b_full[i], kTokenWarps);
+            mbar_init(&c.b_done[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&c.item_full[i], 1);
@@ -710,17 +722,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
         if (elect_one()) good = issue(c.tmem, steps, tile_rows, ring);
     } else if (warp >= kWeightWarps) {
         good = tile_rows <= 32 ? widen_tokens<1, 2>(p, c.tmem, k0, steps, tile_rows, ring, splits == 1)
-                               : widen_tokens<4, 3>(p, c.tmem, k0, steps, tile_rows, ring, false);
+                               : widen_tokens<kTokens / 32, 3>(p, c.tmem, k0, steps, tile_rows, ring, false);
     } else {
         const bool writes = splits == 1 && tile_rows > 32;
-        good = width == 1 ? widen_weights<2>(p, c.tmem, steps, ring, writes) : widen_weights<1>(p, c.tmem, steps, ring, writes);
+        good = widen_weights(p, c.tmem, steps, tile_rows, ring, writes);
     }
     __syncwarp();
     good = __all_sync(0xffffffffu, good);
     if (!good && lane == 0 && p.err_flags != nullptr) atomicOr(p.err_flags, kErrTimeout);
     good = __syncthreads_and(good);
     // the one item's slot is not used again
-    if (splits > 1) join_shares(p, c.items[0], c.tmem, split, splits, good);
+    if (splits > 1) join_shares(p, c.items[0], c.tmem, tile_rows, split, splits, good);
     __syncthreads();
     if (warp == kIssuer) {
         tcgen05_after();
@@ -900,10 +912,11 @@ cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream
     // (one row, 7168 -> 4096, by this kernel: 16 clusters of 8 23 us, of 4 16.5).
     const int nb = row_blocks(p.w);
     int tile = kTokens, width = 2, splits = 1;
-    while (tile > 32 && p.max_rows * 4 <= (int64_t)p.w.E * tile) tile /= 2;
+    auto smaller = [](int tile) { return tile > 128 ? 128 : tile / 2; };
+    while (tile > 32 && p.max_rows * (tile > 128 ? 2 : 4) <= (int64_t)p.w.E * tile) tile = smaller(tile);
     auto items = [&]() { return most_tiles(p.w.E, p.max_rows, tile) * ((nb + width - 1) / width); };
     if (items() * 2 <= num_sms) width = 1;
-    while (tile > 32 && items() * 2 <= num_sms) tile /= 2;
+    while (tile > 32 && items() * 2 <= num_sms) tile = smaller(tile);
     while (splits < 8 && items() * splits * 2 <= num_sms && k_steps(p.w) >= splits * 4 && items() <= clusters_at_once(splits * 2)) splits *= 2;
     const unsigned clusters = (unsigned)std::min<int64_t>(items(), num_sms / splits);
     return launch_clusters(true, splits, expert_i8_kernel, dim3(clusters * splits), dim3(kThreads), kControlBytes + kSmemBytes, stream, p, splits, width,
