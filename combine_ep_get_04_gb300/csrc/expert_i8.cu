@@ -477,7 +477,9 @@ __device__ __forceinline__ void store_shared(uint32_t to, uint32_t a, uint32_t b
 
 // Tokens: a thread has 16 channels of every 32nd row, of up to 32 CHUNKS, and loads
 // them AHEAD steps ahead: with HBM busy an L2 hit takes some 1700 cycles, longer
-// than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).
+// than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).  Each
+// tile has chunks of its own: with those of the next wider one, 64 rows an expert
+// take 342 us instead of 334 and 32 rows 311 instead of 305 (64 experts).
 template <int CHUNKS, int AHEAD>
 __device__ __noinline__ bool widen_tokens(const I8Params& p, uint32_t tmem, int k0, int steps, int tile_rows, int ring, bool writes) {
     static_assert(AHEAD <= kB, "steps that are made before an item's sums are written find rooms");
@@ -656,17 +658,24 @@ __device__ __noinline__ void join_shares(const I8Params& params, const Item it, 
 // apart; with more than one share of K (which a launch of few products has) a
 // cluster takes one.
 //
-// Up to some 16 rows an expert the weights' bytes decide: 256 experts with 4 rows
-// each, gate and up (7168 -> 2 x 2048) 1020 us, down (2048 -> 7168) 532 us, 7.2 and
-// 7.0 TB/s of weights.  With 128 rows each gate and up take 1956 us, 984 TFLOP/s:
-// every step passes 47 KB of codes and operands through shared memory two or
-// three times (256 cycles for the weights' copies, 256 for their loads, 184 for the
-// tokens' stores, 362 for the products' reads, of some 1600 a step), the rest is
-// waiting of the roles for one another.  One row through one matrix of 4096 x 7168 is
-// latency: 13.4 us against 4.4 for its bytes.  Measured and not kept, at 128 rows each:
+// Up to some 32 rows an expert the weights' bytes decide: 256 experts with 4 rows
+// each, gate and up (7168 -> 2 x 2048) 1026 us, down (2048 -> 7168) 532 us, 7.2 and
+// 7.0 TB/s of weights.  With 128 rows each gate and up take 1832 us, 1051 TFLOP/s, and
+// one matrix with 19456 rows 802 us, 1424 TFLOP/s: every step passes codes and operands
+// through shared memory two or three times (of tiles of 160 rows 256 cycles for the
+// weights' copies, 256 for their loads, 320 for the tokens' stores, 640 for the
+// products' reads and as many as 160 for the tokens' way in), and the rest is waiting
+// of the roles for one another; without the tokens' loads they would take 1635 and 740
+// us, without the weights' 1734 and 753.
+//
+// Tiles of up to 160 rows leave tensor memory for three A operands of one block: few
+// experts with about 128 rows then need a second tile, which reads and widens all
+// weights again (tiles of 128 rows and operands of both blocks 1990 us on the same part,
+// of one block 1952).  Measured and not kept, at 128 rows each and by tiles of 128:
 // steps of 64 channels 2797 us; token codes by tensor copies of 8 rows 2532, of 32
 // rows 2082 (one more pass through shared memory); sixteen warps for the weights
-// 2095; one lane of a warp waiting for the others 3093.
+// 2095; one lane of a warp waiting for the others 3093; of 160: tokens fetched into L2
+// three steps earlier 1970.
 __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_constant__ I8Params p, int splits, int width, int tile_rows) {
     Control& c = control();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -721,8 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_i8_kernel(const __grid_con
     } else if (warp == kIssuer) {
         if (elect_one()) good = issue(c.tmem, steps, tile_rows, ring);
     } else if (warp >= kWeightWarps) {
-        good = tile_rows <= 32 ? widen_tokens<1, 2>(p, c.tmem, k0, steps, tile_rows, ring, splits == 1)
-                               : widen_tokens<kTokens / 32, 3>(p, c.tmem, k0, steps, tile_rows, ring, false);
+        good = tile_rows <= 32    ? widen_tokens<1, 2>(p, c.tmem, k0, steps, tile_rows, ring, splits == 1)
+               : tile_rows <= 64  ? widen_tokens<2, 3>(p, c.tmem, k0, steps, tile_rows, ring, false)
+               : tile_rows <= 128 ? widen_tokens<4, 3>(p, c.tmem, k0, steps, tile_rows, ring, false)
+                                  : widen_tokens<kTokens / 32, 3>(p, c.tmem, k0, steps, tile_rows, ring, false);
     } else {
         const bool writes = splits == 1 && tile_rows > 32;
         good = widen_weights(p, c.tmem, steps, tile_rows, ring, writes);
@@ -907,9 +918,10 @@ cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream
     }
     const cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kControlBytes + kSmemBytes);
     if (e != cudaSuccess) return e;
-    // Tiles of twice the mean rows: the smaller the tile, the longer the ring.  Then as many items as there are SMs: by
-    // single blocks, by smaller tiles, by shares of K, of which a cluster that did not run at once would double the time
-    // (one row, 7168 -> 4096, by this kernel: 16 clusters of 8 23 us, of 4 16.5).
+    // Tiles of twice the mean rows, as far as they go (64 rows an expert in tiles of 160 347 us, of 128 343): the smaller the
+    // tile, the longer the ring.  Then as many items as there are SMs: by single blocks, by smaller tiles, by shares of K, of
+    // which a cluster that did not run at once would double the time (one row, 7168 -> 4096, by this kernel: 16 clusters of
+    // 8 23 us, of 4 16.5).
     const int nb = row_blocks(p.w);
     int tile = kTokens, width = 2, splits = 1;
     auto smaller = [](int tile) { return tile > 128 ? 128 : tile / 2; };

@@ -79,13 +79,13 @@ def test_rows_of_one_matrix(rows):
 @pytest.mark.parametrize("K", [16, 48, 64, 112, 128, 144, 1008, 4096, 7168])
 @pytest.mark.parametrize("paired", [False, True])
 def test_wide_matrices(K, paired):
-    """As much work as goes in tiles of up to 128 rows, in shares of K too."""
+    """As much work as goes in tiles, in shares of K too."""
     N = 1032 if paired else 2056
     check([100], N, K, paired, bare=K == 64)
     check([3, 0, 60, 17], N, K, paired)
 
 
-@pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 159, 160, 161, 255, 256, 257, 300, 320, 321])
 def test_rows_of_a_wide_matrix(rows):
     check([rows], 20008, 144)
     check([rows], 10008, 80, True)
