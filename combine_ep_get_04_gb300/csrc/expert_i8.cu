@@ -21,6 +21,7 @@
 
 #include "block_kernels.h"
 #include "expert_rows.cuh"
+#include "i8_tiles.h"
 
 namespace ep {
 namespace {
@@ -228,13 +229,6 @@ struct Item {
     int two;
 };
 
-// Tiles of n rows: as few as hold them, each of about as many rows, in 16s (which
-// is never more than `tile` while n rows need them all).
-__device__ __forceinline__ int tile_rows_of(int n, int tile) {
-    const int tiles = (n + tile - 1) / tile;
-    return ((n + tiles - 1) / tiles + 15) & ~15;
-}
-
 // The sums of a weight row to a lane, scaled, paired and stored.
 struct Writer {
     uint16_t* y;             // at the lane's channel of the tile's first row (the upper lanes' of a pair: of the second)
@@ -283,6 +277,7 @@ struct Control {
     int first[EP_MAX_EXPERTS], rows[EP_MAX_EXPERTS], upto[EP_MAX_EXPERTS];       // of each expert; tiles up to and with it
 };
 
+static_assert(kMostTiles >= (1 << 26) + EP_MAX_EXPERTS, "a good layout of tiles of 32 rows would be cut off");
 static_assert(sizeof(Control) <= kControlBytes, "the shared state has outgrown its room");
 
 extern __shared__ __align__(128) unsigned char smem[];
@@ -317,22 +312,23 @@ __device__ __noinline__ bool find_items(int E, int nb, int width, int tile_rows,
     const int per = (E + 31) / 32, e0 = min(lane * per, E), e1 = min(e0 + per, E);
     int mine = 0;
     for (int e = e0; e < e1; ++e) {
-        mine = min(mine + (c.rows[e] + tile_rows - 1) / tile_rows, 1 << 25);      // bad offsets may claim rows many times
+        mine = add_tiles(mine, tiles_needed(c.rows[e], tile_rows));
         c.upto[e] = mine;
     }
     int total = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, total, d);
-        if (lane >= d) total += v;
+        if (lane >= d) total = add_tiles(total, v);
     }
-    const int before = total - mine;
+    int before = __shfl_up_sync(0xffffffffu, total, 1);
+    if (lane == 0) before = 0;
     total = __shfl_sync(0xffffffffu, total, 31);
-    for (int e = e0; e < e1; ++e) c.upto[e] += before;
+    for (int e = e0; e < e1; ++e) c.upto[e] = add_tiles(c.upto[e], before);
     __syncwarp();
     const int across = (nb + width - 1) / width;       // items of a tile
     const int64_t all = (int64_t)total * across, most = one ? min(all, (int64_t)clusters) : all;
-    if (most < all && cluster == 0 && lane == 0 && err_flags != nullptr) atomicOr(err_flags, kErrCapacity);
+    if ((most < all || total == kMostTiles) && cluster == 0 && lane == 0 && err_flags != nullptr) atomicOr(err_flags, kErrCapacity);
     for (int j = 0;; ++j) {
         const int slot = j % kItems;
         const int64_t at = cluster + (int64_t)j * clusters;
