@@ -651,7 +651,7 @@ Kernel1 narrow_kernel(bool backward, int nv) {
 cudaError_t launch_narrow(const LayerNormParams& p, int num_sms, bool backward, int* ctas, cudaStream_t stream) {
     const int nv = p.H <= 256 ? 1 : p.H <= 512 ? 2 : 4, ctas_now = std::min(p.T, std::min(num_sms, kMaxSms));
     // no more warps than rows
-    const int warps = std::min(narrow_warps(nv, backward), (p.T + ctas_now - 1) / ctas_now);
+    const int warps = std::min(narrow_warps(nv, backward), (p.T - 1) / ctas_now + 1);
     const bool drop = p.drop.rng != nullptr;
     const Kernel1 kern = p.f32 ? (drop ? narrow_kernel<true, true>(backward, nv) : narrow_kernel<true, false>(backward, nv))
                                : (drop ? narrow_kernel<false, true>(backward, nv) : narrow_kernel<false, false>(backward, nv));

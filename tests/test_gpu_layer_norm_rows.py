@@ -1,0 +1,55 @@
+"""ep_layer_norm and its gradients over many rows, against the plain 64-bit
+implementations and the bounds of layer_reference."""
+import numpy as np
+import pytest
+import torch
+
+import combine_ep_get_04_gb300 as ep
+import layer_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    assert torch.cuda.is_available(), "the GPU tests need a CUDA device"
+    ep.load()
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def near(name, got, value, error):
+    error = ref.stored(value, error, got.dtype == BF16)
+    off = np.abs(f64(got) - value)
+    assert (off <= error).all(), f"{name}: {(~(off <= error)).sum()} of {off.size} beyond the bound, worst {np.nanmax(off - error):.3g} past it"
+
+
+def test_as_many_rows_as_there_are_numbers():
+    """2^31 - 1 rows of 8 channels: every row is written, and some all over the buffer are compared."""
+    T, H = 2 ** 31 - 1, 8
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 200 * 2 ** 30:
+        pytest.skip("the largest buffers do not fit")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    h, d_n = (torch.empty(T, H, dtype=BF16, device="cuda").normal_(generator=g) for _ in range(2))
+    w, b = 1 + 0.1 * torch.randn(H, generator=g, device="cuda"), 0.1 * torch.randn(H, generator=g, device="cuda")
+    m = ep.LayerNorm(T, H, BF16, block=False, eps=EPS, train=True)
+    m.n.fill_(float("nan"))
+    m.grads.d_h.fill_(float("nan"))
+    _, n = m.forward(h, w=w, b=b)
+    d = m.backward(h, w, d_n)
+    torch.cuda.synchronize()
+    assert int(m.err_flags) == 0
+    for a in range(0, T, 2 ** 26):
+        assert not n[a:a + 2 ** 26].isnan().any() and not d.d_h[a:a + 2 ** 26].isnan().any(), a
+    for a in (0, 2 ** 30 - 500, T - 1000):
+        at = slice(a, a + 1000)
+        n_v, n_e, s = ref.layer_norm(f64(h[at]), f64(w), f64(b), EPS)
+        near("n", n[at], n_v, n_e)
+        near("d_h", d.d_h[at], *ref.layer_norm_gradients(s, f64(d_n[at]), None, 1.0)["d_h"])
+    assert torch.isfinite(d.d_w).all() and torch.isfinite(d.d_b).all()
