@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(LayerNormP
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     if (NV > 2) load_weights(k);
-                    const Vec8 x = load_stream<F32>(row, at[k]), dn = load_bf16(row + at_dn, at[k]);
+                    // 0 where a thread has no channels: a weight of 0 alone would make NaN of an infinity
+                    const Vec8 x = load_stream<F32>(row, at[k]), dn = in[k] ? load_bf16(row + at_dn, at[k]) : all(0.f);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const uint64_t xn = mul2(add2(x.v[c], less), r), t = mul2(dn.v[c], w[k].v[c]);

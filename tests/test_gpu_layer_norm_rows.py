@@ -53,3 +53,36 @@ def test_as_many_rows_as_there_are_numbers():
         near("n", n[at], n_v, n_e)
         near("d_h", d.d_h[at], *ref.layer_norm_gradients(s, f64(d_n[at]), None, 1.0)["d_h"])
     assert torch.isfinite(d.d_w).all() and torch.isfinite(d.d_b).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H", [256, 520, 1032, 2056, 4104, 8200])
+def test_an_infinite_gradient_by_its_place(H, dtype):
+    """An infinity in d_n leaves in a row what the formula makes of it, infinities of either sign and NaN, whichever
+    channel it stands in: swapping two channels of all inputs swaps them in all results."""
+    T, place = 3, 123
+    g = torch.Generator(device="cuda").manual_seed(H)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda")     # noqa: E731
+    h, d_n, dh, w = rand(T, H).to(dtype), rand(T, H).bfloat16(), rand(T, H).to(dtype), 1 + 0.1 * rand(H)
+    h[:, 0] = 1.0                        # away from the mean, so that d_n times the normed value is an infinity too
+    d_n[1, 0], d_n[2, 0] = float("inf"), float("-inf")
+    swap = torch.arange(H, device="cuda")
+    swap[0], swap[place] = place, 0
+    m = ep.LayerNorm(T, H, dtype, bias=False, block=False, eps=EPS, train=True)
+    x = d_n.double() * w.double()
+
+    def run(at):
+        hs = h[:, at].contiguous()
+        m.forward(hs, w=w[at].contiguous())
+        return m.backward(hs, w[at].contiguous(), d_n[:, at].contiguous(), dh[:, at].contiguous()).d_h.clone()
+
+    first, other = run(torch.arange(H, device="cuda")), run(swap)[:, swap]
+    v = h.double()
+    xn = (v - v.mean(1, keepdim=True)) / (v.var(1, unbiased=False, keepdim=True) + EPS).sqrt()
+    want = x - x.mean(1, keepdim=True) - xn * (x * xn).mean(1, keepdim=True)
+    assert want[1:].isinf().any() and torch.isfinite(want[0]).all()
+    for got in (first, other):
+        assert torch.isfinite(got[0]).all()
+        for sign in (float("inf"), float("-inf")):
+            assert torch.equal(got[1:] == sign, want[1:] == sign)
+        assert torch.equal(got[1:].isnan(), want[1:].isnan())
