@@ -53,6 +53,13 @@ def _shaped_ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tu
     return _ptr(t, dtype, name)
 
 
+def _int32(n: int, name: str) -> int:
+    """A size that the C ABI takes as 32 bits, which ctypes would cut to its low ones."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} = {n} does not fit 32 bits")
+    return n
+
+
 def _stream(stream: torch.cuda.Stream | None) -> int | None:
     return (_raw_stream(_current_device()) if stream is None else stream.cuda_stream) or None
 

@@ -25,7 +25,7 @@ from dataclasses import dataclass
 import torch
 
 from ._lib import CAPACITY, I8, PACKED, TYPE_BF16, TYPE_F32, LayerNormDesc, check, load
-from ._tensors import _empty, _ptr, _rows_ptr, _shaped_ptr, _stream
+from ._tensors import _empty, _int32, _ptr, _rows_ptr, _shaped_ptr, _stream
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
 _MASK64 = 2 ** 64 - 1
@@ -87,7 +87,7 @@ class LayerNorm:
             raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
         if p and not block:
             raise ValueError("dropout needs the block's output: pass p=0 with block=False")
-        self.desc = LayerNormDesc(T, H, _TYPES[dtype], eps, p, site & _MASK64)
+        self.desc = LayerNormDesc(_int32(T, "T"), _int32(H, "H"), _TYPES[dtype], eps, p, site & _MASK64)
         self._ref = ctypes.byref(self.desc)
         nbytes = lib.ep_layer_norm_workspace_bytes(self._ref)
         if nbytes == ctypes.c_size_t(-1).value:
@@ -171,14 +171,16 @@ def quant_i8(x: torch.Tensor, counts: torch.Tensor | None = None, offsets: torch
         raise ValueError("a capacity buffer needs the layout's counts")
     if capacity is None and offsets is None and counts is not None:
         raise ValueError("packed rows need the layout's offsets")
-    E = counts.numel() if counts is not None else offsets.numel() - 1 if offsets is not None else 1
+    E = _int32(counts.numel() if counts is not None else offsets.numel() - 1 if offsets is not None else 1, "E")
+    mode, capacity = (PACKED, 0) if capacity is None else (CAPACITY, _int32(capacity, "capacity"))
+    _int32(K, "K")
     xp, ld = _rows_ptr(x, torch.bfloat16, "x", (R, K))
     held = _held(E, counts, offsets)
     if out is None:
         out = _empty((R, K), torch.int8, x.device, stream)
     if scales is None:
         scales = _empty((R,), torch.float32, x.device, stream)
-    st = lib.ep_quant_i8(E, K, PACKED if capacity is None else CAPACITY, capacity or 0, R, *held, xp, ld,
+    st = lib.ep_quant_i8(E, K, mode, capacity, R, *held, xp, ld,
                          _shaped_ptr(out, torch.int8, "out", (R, K)), _shaped_ptr(scales, torch.float32, "scales", (R,)),
                          _shaped_ptr(err_flags, torch.int32, "err_flags", (1,)), _stream(stream))
     if st:
@@ -205,7 +207,7 @@ class I8Weights:
         if paired and rows % 2:
             raise ValueError(f"paired weights have an even number of rows, got {rows}")
         self.E, self.N, self.K, self.paired = E, rows // 2 if paired else rows, K, paired
-        self.desc = I8(E, self.N, K, int(paired))
+        self.desc = I8(_int32(E, "E"), _int32(self.N, "N"), _int32(K, "K"), int(paired))
         self._ref = ctypes.byref(self.desc)
         nbytes = lib.ep_i8_bytes(self._ref)
         if nbytes == ctypes.c_size_t(-1).value:
@@ -234,6 +236,7 @@ def expert_i8(x: torch.Tensor, x_scales: torch.Tensor, weights: I8Weights, count
     if x.dim() != 2 or x.shape[1] != w.K:
         raise ValueError(f"x must be [R, {w.K}], got {tuple(x.shape)}")
     R = x.shape[0]
+    mode, capacity = (PACKED, 0) if capacity is None else (CAPACITY, _int32(capacity, "capacity"))
     xp, sp = _shaped_ptr(x, torch.int8, "x", (R, w.K)), _shaped_ptr(x_scales, torch.float32, "x_scales", (R,))
     if counts is None and offsets is None and w.E != 1:
         raise ValueError("several experts need the layout's counts and offsets")
@@ -241,7 +244,7 @@ def expert_i8(x: torch.Tensor, x_scales: torch.Tensor, weights: I8Weights, count
     if out is None:
         out = _empty((R, w.N), torch.bfloat16, x.device, stream)
     st = w._lib.ep_expert_i8(
-        w._ref, w._packed, PACKED if capacity is None else CAPACITY, capacity or 0, R, R if max_rows is None else max_rows,
+        w._ref, w._packed, mode, capacity, R, R if max_rows is None else max_rows,
         *held, xp, sp, _shaped_ptr(out, torch.bfloat16, "out", (R, w.N)),
         _shaped_ptr(err_flags, torch.int32, "err_flags", (1,)), _stream(stream))
     if st:
