@@ -235,6 +235,8 @@ def expert_i8(x: torch.Tensor, x_scales: torch.Tensor, weights: I8Weights, count
     w = weights
     if x.dim() != 2 or x.shape[1] != w.K:
         raise ValueError(f"x must be [R, {w.K}], got {tuple(x.shape)}")
+    if w.E == 1 and capacity is None and offsets is None and counts is not None:
+        raise ValueError("packed rows need the layout's offsets")
     R = x.shape[0]
     mode, capacity = (PACKED, 0) if capacity is None else (CAPACITY, _int32(capacity, "capacity"))
     xp, sp = _shaped_ptr(x, torch.int8, "x", (R, w.K)), _shaped_ptr(x_scales, torch.float32, "x_scales", (R,))
