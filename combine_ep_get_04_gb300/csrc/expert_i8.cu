@@ -15,13 +15,13 @@
 // That chain of roles costs some 7 us before the first sum is out, so a batch of little
 // work goes another way (expert_i8_few_kernel).
 #include <algorithm>
-#include <atomic>
 
 #include "ep.h"
 
 #include "block_kernels.h"
 #include "expert_rows.cuh"
 #include "i8_tiles.h"
+#include "per_device.h"
 
 namespace ep {
 namespace {
@@ -873,28 +873,26 @@ cudaError_t launch_i8_pack(const I8Shape& w, const int8_t* codes, const float* s
 
 namespace {
 
-// Clusters of so many CTAs that run at the same time.
+// Clusters of 2, 4 or 8 CTAs that the current device runs at the same time.
 int clusters_at_once(int splits) {
-    static std::atomic<int> known[4];          // of 2, 4 and 8; 0: not asked yet
-    std::atomic<int>& n = known[splits == 2 ? 1 : splits == 4 ? 2 : 3];
-    int got = n.load(std::memory_order_relaxed);
-    if (got > 0) return got;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(splits);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kControlBytes + kSmemBytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&got, expert_i8_kernel, &cfg) != cudaSuccess || got < 1) {
+    static PerDevice<3> known;
+    int device = -1;
+    if (cudaGetDevice(&device) != cudaSuccess) device = -1;
+    return known.get(device, splits == 2 ? 0 : splits == 4 ? 1 : 2, 1, [&](int* got) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(splits);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kControlBytes + kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)splits;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(got, expert_i8_kernel, &cfg) == cudaSuccess) return true;
         (void)cudaGetLastError();
-        got = 1;
-    }
-    n.store(got, std::memory_order_relaxed);
-    return got;
+        return false;
+    });
 }
 
 }  // namespace
