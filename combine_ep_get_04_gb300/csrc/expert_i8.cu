@@ -176,27 +176,6 @@ __host__ __device__ constexpr int ring_units(int tile_rows) {
 constexpr bool ring_is_ahead(int tile_rows) { return ring_units(tile_rows) >= a_places(tile_rows) + 2; }
 static_assert(ring_is_ahead(kTokens) && ring_is_ahead(128) && ring_is_ahead(64) && ring_is_ahead(32), "a place of the ring could be waited for a round early");
 
-// Waits for a phase, at most kWaitLimitNs and a few tries.  A try suspends the
-// thread for a while by itself, which leaves the issue slots to others; the clock
-// is looked at once in 64 of them.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
-    uint64_t t0 = 0;
-    for (uint32_t tries = 1;; ++tries) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if (tries % 64 == 0) {
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) return false;
-        }
-    }
-}
-
 // A place in a ring and the parity of its phase.
 struct Place {
     int at = 0;
@@ -285,7 +264,7 @@ extern __shared__ __align__(128) unsigned char smem[];
 __device__ __forceinline__ Control& control() { return *reinterpret_cast<Control*>(smem); }
 __device__ __forceinline__ unsigned char* ring_base() { return smem + kControlBytes; }
 
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_phase(bar, parity)); }
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_suspended(bar, parity)); }
 
 // Item j of the CTA, for a whole warp.  False if a wait ran out.
 __device__ __forceinline__ bool next_item(int j, Item* it) {
@@ -383,7 +362,7 @@ __device__ __noinline__ bool produce(const unsigned char* packed, int nb, int nk
         }
     }
     // no copy may be in flight when the CTA ends, whatever its consumers did
-    for (int64_t i = max((int64_t)0, filled - ring); i < filled; ++i) wait_phase(&c.ring_full[i % ring], (i / ring) & 1);
+    for (int64_t i = max((int64_t)0, filled - ring); i < filled; ++i) mbar_wait_suspended(&c.ring_full[i % ring], (i / ring) & 1);
     return good;
 }
 
@@ -401,20 +380,20 @@ __device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows, int 
     Place a, b;
     for (int j = 0; good; ++j) {
         const int slot = j % kItems;
-        good = wait_phase(&c.item_full[slot], (j / kItems) & 1);
+        good = mbar_wait_suspended(&c.item_full[slot], (j / kItems) & 1);
         if (!good) break;
         const int e = c.items[slot].e, rows = c.items[slot].rows, two = c.items[slot].two;
         mbar_arrive(&c.item_empty[slot]);
         if (e < 0) break;
         const uint32_t cols = (rows + 15) & ~15;           // the products' N: a multiple of 16
         const uint32_t kind = 1u << 4 | (cols / 8) << 17 | (uint32_t)(kRows / 16) << 24;      // fp32 sums, f16 operands, N, M
-        if (j > 0) good = wait_phase(&c.drained, (j - 1) & 1);
+        if (j > 0) good = mbar_wait_suspended(&c.drained, (j - 1) & 1);
         for (int i = 0; i < steps && good; ++i, b.next(kB)) {
             const uint64_t from_b = first_b + (uint32_t)(b.at * kRuns) * run16;
-            good = wait_phase(&c.b_full[b.at], b.parity);
+            good = mbar_wait_suspended(&c.b_full[b.at], b.parity);
             for (int h = 0; h <= two && good; ++h, a.next(places)) {
                 const uint32_t from_a = a_at + a.at * kAColumns, to = tmem + h * tile_rows;
-                good = wait_phase(&c.a_full[a.at], a.parity);
+                good = mbar_wait_suspended(&c.a_full[a.at], a.parity);
                 if (!good) break;
                 tcgen05_after();
 #pragma unroll
@@ -427,7 +406,7 @@ __device__ __noinline__ bool issue(uint32_t tmem, int steps, int tile_rows, int 
         ++committed;
     }
     // every product is over before tensor memory is given back
-    if (committed > 0) good = wait_phase(&c.done, (committed - 1) & 1) && good;
+    if (committed > 0) good = mbar_wait_suspended(&c.done, (committed - 1) & 1) && good;
     return good;
 }
 
