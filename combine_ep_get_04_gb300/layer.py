@@ -1,10 +1,11 @@
 """The ends of a layer-normed block, and expert products in 8-bit integers.
 
-    rng = torch.tensor([seed, step], device="cuda")    # the training loop counts the step up
+    rng = torch.tensor([seed, 0], device="cuda")        # seed, step
     norm = LayerNorm(T, H, p=0.1, site=3, train=True)
     h, n = norm.forward(h, y, w, b, rng)                # h + dropout(y), and its layer norm
     d = norm.backward(h, w, d_n, d_h, rng)              # d.d_h, d.d_y, d.d_w, d.d_b
     x = dropout(x, 0.1, rng, site=4)
+    rng[1] += 5                                         # the next step: by more than the largest site
     w = I8Weights(codes, scales, paired=True)
     q, q_scales = quant_i8(recv, layout.counts, layout.offsets)
     y = expert_i8(q, q_scales, w, layout.counts, layout.offsets)
@@ -13,6 +14,12 @@ Dropout keeps no mask: which elements are dropped follows from the seed, the
 step, the site and the element's place, so a backward pass is given the same.
 The seed and the step stay on the device, so that a captured step can be
 replayed with the step counted up inside it.
+
+Step and site are added: the masks of a step are its own only if the step goes
+up by more than the largest site each time (sites 0..n-1: by n), or if the sites
+lie further apart than the steps reach (site=i << 32, steps below 2**32 counted
+by 1).  Counted by 1 with sites 3 and 4, one layer would get the mask that the
+other had a step before.
 
 LayerNorm allocates its outputs and workspace once, as BlockNorm does; the
 functions allocate their results where no `out` is given.
@@ -38,9 +45,9 @@ def dropout(x: torch.Tensor, p: float, rng: torch.Tensor | None, site: int = 0, 
 
     x [T, H] bf16 or f32, and residual and out like it; their rows may lie
     further apart than their length.  rng i64 [2] on the device (seed, step);
-    None: nothing is dropped.  site tells the dropouts of one step apart.  out
-    may be x or residual.  The gradient with respect to x is dropout(d_out, p,
-    rng, site)."""
+    None: nothing is dropped.  site tells the dropouts of one step apart, and
+    the step goes up by more than the largest of them.  out may be x or
+    residual.  The gradient with respect to x is dropout(d_out, p, rng, site)."""
     lib, shape, dtype = load(), x.shape, x.dtype
     if len(shape) != 2:
         raise ValueError(f"x must be [T, H], got {tuple(shape)}")
@@ -76,7 +83,8 @@ class LayerNorm:
 
     dtype: type of the residual stream (h, h_out and their gradients), bf16 or
     f32; the block's output y and the normed n are bf16.  p, site: dropout of
-    y, and which dropout of the network it is.  weight / bias: whether the norm
+    y, and which dropout of the network it is (the step goes up by more than the
+    largest site each time).  weight / bias: whether the norm
     has them; block: False for the first norm of a network (no y, h_out is h).
     """
 

@@ -596,6 +596,12 @@ EP_API ep_status_t ep_expert_w4(const ep_w4_t *w, const void *packed, int32_t mo
  * 65536 / (65536 - limit), rounded to fp32, so that the mean stays what it was.
  * A dropped value counts as 0, whatever it is.  With p = 1 all are dropped.
  * rng = NULL: nothing is dropped.
+ *
+ * Only the sum of step and site enters: site 3 of one step has the random
+ * numbers of site 2 of the next if the step goes up by 1.  For masks that are
+ * never used twice under a seed, either the step goes up by more than the
+ * largest site each time (sites 0..n-1: by n), or the sites lie further apart
+ * than the steps reach (sites i * 2^32, steps below 2^32, counted by 1).
  */
 
 /*
