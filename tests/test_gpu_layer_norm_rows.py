@@ -86,3 +86,45 @@ def test_an_infinite_gradient_by_its_place(H, dtype):
         for sign in (float("inf"), float("-inf")):
             assert torch.equal(got[1:] == sign, want[1:] == sign)
         assert torch.equal(got[1:].isnan(), want[1:].isnan())
+
+
+def ring(T, H, row_bytes, sms):
+    """CTAs of a call whose rows come through a ring, and its stages."""
+    nv = 1 if H <= 4096 else 2 if H <= 8192 else 4
+    warps = -(-H // 8 // (32 * nv))
+    per_sm = 1 if nv > 1 else max(1, min(8, 20 // (warps + 1)))
+    return min(T, sms * per_sm), max(1, min(8, (212 * 1024 // per_sm - 2048) // row_bytes))
+
+
+@pytest.mark.parametrize("T,H,dtype", [(3 * 25 * 152, 1040, BF16), (2 * 25 * 152, 2048, BF16), (26 * 152, 7168, BF16), (27 * 152, 4096, F32),
+                                       (16 * 152 + 7, 8192, F32), (10 * 152 + 3, 16384, BF16), (25 * 152, 5000, BF16)])
+def test_many_rounds_of_the_ring(T, H, dtype):
+    """Every stage, slot and barrier is used at least three times in both directions; all rows and the sums over them
+    are compared.  The sums' bound counts the kernel's own chain of additions, the rows of a CTA, every 16th CTA and 16
+    warps, so that any lost or doubled row lies outside it."""
+    sms, size = torch.cuda.get_device_properties(0).multi_processor_count, 2 if dtype == BF16 else 4
+    for row_bytes in (H * (size + 2), H * (2 * size + 2)):
+        ctas, stages = ring(T, H, row_bytes, sms)
+        assert T // ctas >= 3 * stages
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *shape, scale=1.0: torch.randn(*shape, generator=g, device="cuda") * scale     # noqa: E731
+    h, y, d_n, dh = rand(T, H, scale=1.5).to(dtype), rand(T, H, scale=0.5).bfloat16(), rand(T, H).bfloat16(), rand(T, H).to(dtype)
+    w, b, rng = 1 + rand(H, scale=0.1), rand(H, scale=0.1), torch.tensor([5, 6], device="cuda")
+    m = ep.LayerNorm(T, H, dtype, p=0.1, site=2, eps=EPS, train=True)
+    h_out, n = m.forward(h, y, w, b, rng)
+    d = m.backward(h_out, w, d_n, dh, rng)
+    torch.cuda.synchronize()
+    assert int(m.err_flags) == 0
+    f = ref.factors(T, H, 0.1, (5, 6), 2)
+    near("h_out", h_out, *ref.dropped_sum(f64(y), f, f64(h)))
+    n_v, n_e, s = ref.layer_norm(f64(h_out), f64(w), f64(b), EPS)
+    near("n", n, n_v, n_e)
+    dn = f64(d_n)
+    grads = ref.layer_norm_gradients(s, dn, f64(dh), f)
+    near("d_h", d.d_h, *grads["d_h"])
+    near("d_y", d.d_y, *grads["d_y"])
+    chain = -(-T // ctas) + ctas // 16 + 1 + 17
+    for name, got, terms, off in (("d_w", d.d_w, np.abs(dn * s["xn"]), (np.abs(dn) * s["e_xn"]).sum(0)), ("d_b", d.d_b, np.abs(dn), 0.0)):
+        error = off + (chain + 2) * ref.U * terms.sum(0)
+        near(name, got, grads[name][0], error)
+        assert (terms > error).any(1).all(), "a lost row would not show"
