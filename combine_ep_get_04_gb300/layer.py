@@ -142,9 +142,11 @@ class LayerNorm:
 
     def backward(self, h_out: torch.Tensor, w: torch.Tensor | None, d_n: torch.Tensor, d_h_out: torch.Tensor | None = None,
                  rng: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> LayerNormGrads:
-        """Gradients, from the h_out of the last forward() (or a copy of it: the
-        next forward() overwrites it; h where the norm has no block), the same w
-        and rng, and the gradients of its outputs (d_h_out may be None: zero)."""
+        """Gradients of the last forward(), from its h_out (h where the norm has
+        no block), the same w and rng, and the gradients of its outputs (d_h_out
+        may be None: zero).  The rows' statistics are those that the last
+        forward() left in `stats`: two forward() calls before their backward()
+        calls need a LayerNorm each, a copy of h_out is not enough."""
         if not self.train:
             raise ValueError("this norm was made without train=True")
         if (w is None) is self.weight:

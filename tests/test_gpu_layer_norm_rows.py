@@ -128,3 +128,25 @@ def test_many_rounds_of_the_ring(T, H, dtype):
         error = off + (chain + 2) * ref.U * terms.sum(0)
         near(name, got, grads[name][0], error)
         assert (terms > error).any(1).all(), "a lost row would not show"
+
+
+def test_gradients_are_those_of_the_last_forward():
+    """From h_out or a copy of it; two batches on their way at once have a norm each."""
+    T, H = 40, 1040
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda: torch.randn(T, H, generator=g, device="cuda")          # noqa: E731
+    batches = [(rand() * (i + 1), rand().bfloat16(), rand().bfloat16()) for i in range(2)]
+    w, rng = 1 + 0.1 * rand()[0], torch.tensor([1, 2], device="cuda")
+    make = lambda: ep.LayerNorm(T, H, F32, p=0.1, bias=False, train=True)  # noqa: E731
+    want = []
+    for h, y, d_n in batches:
+        m = make()
+        copy = m.forward(h, y, w, rng=rng)[0].clone()
+        want.append([t.clone() for t in (m.backward(m.h_out, w, d_n, rng=rng).d_h, m.grads.d_w)])
+        d = m.backward(copy, w, d_n, rng=rng)
+        assert torch.equal(d.d_h, want[-1][0]) and torch.equal(d.d_w, want[-1][1])
+    norms = [make(), make()]
+    outs = [m.forward(h, y, w, rng=rng)[0] for m, (h, y, _) in zip(norms, batches)]
+    for m, h_out, (_, _, d_n), (d_h, d_w) in zip(norms, outs, batches, want):
+        d = m.backward(h_out, w, d_n, rng=rng)
+        assert torch.equal(d.d_h, d_h) and torch.equal(d.d_w, d_w)
