@@ -2,8 +2,6 @@
 // products takes, and the gate of a pair.  P: the parameters of a product (E in
 // w.E, mode, capacity, counts, offsets, R, err_flags).
 #pragma once
-#include <cuda.h>
-
 #include "block_device.cuh"
 
 namespace ep {
@@ -122,34 +120,6 @@ __device__ __forceinline__ RowTile tile_of_one(const P& p, int at, int tile_rows
     }
     if (at >= tiles) return RowTile{-1, 0, 0};
     return RowTile{0, min(n - at * tile_rows, tile_rows), first + (int64_t)at * tile_rows};
-}
-
-// A box of a tensor map's rows from `channel` and `row` on, completion counted in bytes on `bar`.
-__device__ __forceinline__ void box_load(void* dst, const CUtensorMap* map, int channel, int row, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                     smem_addr(dst)),
-                 "l"(map), "r"(channel), "r"(row), "r"(smem_addr(bar))
-                 : "memory");
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Describes x [R, K] for copies of `channels` x `rows`; zeros stand in for what lies past its ends.
-inline cudaError_t describe_boxes(const void* x, int64_t R, int K, CUtensorMapDataType type, int size, int channels, int rows, CUtensorMap* map) {
-    static const EncodeFn encode = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
-        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(f) : nullptr;
-    }();
-    if (encode == nullptr) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)R}, strides[1] = {(cuuint64_t)K * size};
-    const cuuint32_t box[2] = {(cuuint32_t)channels, (cuuint32_t)rows}, steps[2] = {1, 1};
-    const CUresult r = encode(map, type, 2, const_cast<void*>(x), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace ep

@@ -16,6 +16,7 @@
 // through one fused multiply-add with the group's scale.
 #include <algorithm>
 #include <atomic>
+#include <cuda.h>
 #include <type_traits>
 
 #include "block_device.cuh"
@@ -175,6 +176,14 @@ __device__ __forceinline__ void cluster_store(const float4* p, uint32_t rank, co
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+
+// A box of 32 channels x 8 NT rows, completion counted in bytes on `bar`.
+__device__ __forceinline__ void box_load(void* dst, const CUtensorMap* map, int channel, int row, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(map), "r"(channel), "r"(row), "r"(smem_addr(bar))
+                 : "memory");
 }
 
 // One tile step along K (128 channels) of a consumer warp: adds scale * code
@@ -546,9 +555,26 @@ size_t w4_smem(const W4Shape& w, int nt, bool fp8, int splits) {
 constexpr size_t kMaxSmem = 227 * 1024 - 1024;
 constexpr size_t kSmSmem = 228 * 1024;
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
 // Describes x [R, K] for copies of 32 channels x `rows` rows.
 cudaError_t describe_rows(const W4Params& p, int rows, CUtensorMap* map) {
-    return describe_boxes(p.x, p.R, p.w.K, p.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.fp8 ? 1 : 2, 32, rows, map);
+    static const EncodeFn encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeFn>(f) : nullptr;
+    }();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t size = p.fp8 ? 1 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.w.K, (cuuint64_t)p.R}, strides[1] = {(cuuint64_t)p.w.K * size};
+    const cuuint32_t box[2] = {32, (cuuint32_t)rows}, steps[2] = {1, 1};
+    const CUresult r = encode(map, p.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                              const_cast<void*>(p.x), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 // Shared memory that a CTA asks for beyond its own needs, so that clusters are

@@ -7,8 +7,8 @@
 // into [2^-64, 2^64] first, where no step that matters under- or overflows.
 #include <algorithm>
 
+#include "block_device.cuh"
 #include "block_kernels.h"
-#include "dropout.cuh"
 
 namespace ep {
 namespace {
