@@ -454,7 +454,7 @@ __device__ __forceinline__ void store_shared(uint32_t to, uint32_t a, uint32_t b
 // them AHEAD steps ahead: with HBM busy an L2 hit takes some 1700 cycles, longer
 // than a step (256 experts, 4 rows each, one step ahead 1378 us, two 1131).  Each
 // tile has chunks of its own: with those of the next wider one, 64 rows an expert
-// take 342 us instead of 334 and 32 rows 311 instead of 305 (64 experts).
+// take 342 us instead of 334 and 32 rows 311 instead of 305 (64 experts, rows on average).
 template <int CHUNKS, int AHEAD>
 __device__ __noinline__ bool widen_tokens(const I8Params& p, uint32_t tmem, int k0, int steps, int tile_rows, int ring, bool writes) {
     static_assert(AHEAD <= kB, "steps that are made before an item's sums are written find rooms");
@@ -635,18 +635,20 @@ __device__ __noinline__ void join_shares(const I8Params& params, const Item it, 
 //
 // Up to some 32 rows an expert the weights' bytes decide: 256 experts with 4 rows
 // each, gate and up (7168 -> 2 x 2048) 1026 us, down (2048 -> 7168) 532 us, 7.2 and
-// 7.0 TB/s of weights.  With 128 rows each gate and up take 1832 us, 1051 TFLOP/s, and
+// 7.0 TB/s of weights.  With 128 rows each gate and up take 1640 us, 1173 TFLOP/s, down
+// 976 us, 985 TFLOP/s; with 128 on average, as routers deal them, 1832 and 1057 us; and
 // one matrix with 19456 rows 802 us, 1424 TFLOP/s: every step passes codes and operands
 // through shared memory two or three times (of tiles of 160 rows 256 cycles for the
 // weights' copies, 256 for their loads, 320 for the tokens' stores, 640 for the
 // products' reads and as many as 160 for the tokens' way in), and the rest is waiting
-// of the roles for one another; without the tokens' loads they would take 1635 and 740
-// us, without the weights' 1734 and 753.
+// of the roles for one another; without the tokens' loads 1832 and 802 would be 1635 and
+// 740 us, without the weights' 1734 and 753.
 //
-// Tiles of up to 160 rows leave tensor memory for three A operands of one block: few
-// experts with about 128 rows then need a second tile, which reads and widens all
-// weights again (tiles of 128 rows and operands of both blocks 1990 us on the same part,
-// of one block 1952).  Measured and not kept, at 128 rows each and by tiles of 128:
+// Tiles of up to 160 rows leave tensor memory for three A operands of one block.  An
+// expert with more rows needs a second tile, which reads and widens all its weights
+// again: of 256 with 128 rows on average 46 to 54, of tiles of 128 rows many more
+// (operands of both blocks 1990 us on the same part, of one block 1952).  Measured and
+// not kept, at 128 rows on average and by tiles of 128:
 // steps of 64 channels 2797 us; token codes by tensor copies of 8 rows 2532, of 32
 // rows 2082 (one more pass through shared memory); sixteen warps for the weights
 // 2095; one lane of a warp waiting for the others 3093; of 160: tokens fetched into L2
@@ -891,7 +893,7 @@ cudaError_t launch_expert_i8(const I8Params& p, int num_sms, cudaStream_t stream
     }
     const cudaError_t e = cudaFuncSetAttribute(expert_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kControlBytes + kSmemBytes);
     if (e != cudaSuccess) return e;
-    // Tiles of twice the mean rows, as far as they go (64 rows an expert in tiles of 160 347 us, of 128 343): the smaller the
+    // Tiles of twice the mean rows, as far as they go (64 rows an expert in tiles of 160 348 us, of 128 336): the smaller the
     // tile, the longer the ring.  Then as many items as there are SMs: by single blocks, by smaller tiles, by shares of K, of
     // which a cluster that did not run at once would double the time (one row, 7168 -> 4096, by this kernel: 16 clusters of
     // 8 23 us, of 4 16.5).

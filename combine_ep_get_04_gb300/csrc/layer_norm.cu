@@ -444,9 +444,19 @@ __global__ void __launch_bounds__(THREADS) layer_norm_backward_kernel(LayerNormP
 // A warp takes a row by itself: no barrier, no join, and as many rows on their
 // way as an SM has warps.  NV vectors of 8 channels a lane; rows are dealt to the
 // CTAs first, then to their warps.  As far as the registers hold a row (backward,
-// the two sums over rows too): T=8192 bf16 forward and backward H=256 17 us, by the
-// ring 32; fp32 H=512 29 and 42; H=1024 forward 21.1 and 22.4, backward 35 and 40,
-// bf16 with dropout 80 and 52.
+// the two sums over rows too).  T=65536, us, in brackets by the ring:
+//
+//                    bf16                     fp32
+//   forward          no dropout   dropout     no dropout   dropout
+//   H=256            30  (59)     31  (70)    37  (59)     37  (69)
+//   H=512            49  (78)     54  (92)    64  (85)     65  (91)
+//   H=1024           92 (151)    102 (140)   123 (131)    125 (138)
+//   backward with the column sums
+//   H=256            44  (85)     51  (90)    55  (67)     57  (89)
+//   H=512            72  (83)    102 (136)    89  (85)    103 (140)
+//
+// H=1024 backward by a warp: 262 and 348 us bf16, 330 and 348 fp32, its sums spilled;
+// by the ring 115 and 153, 174 and 242.
 
 constexpr int kNarrow = 1024, kNarrowBackward = 512;
 

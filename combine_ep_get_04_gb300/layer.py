@@ -203,7 +203,8 @@ class I8Weights:
     expert_i8 (ep_i8_pack).
 
     codes i8 [E, rows, K]; scales f32 [E, rows].  paired: rows are N gate rows
-    and then N up rows of a SwiGLU.  They are packed on `stream`, whose memory
+    and then N up rows of a SwiGLU.  They take the codes' bytes with K, and rows
+    (N of a pair), made up to multiples of 128 (64).  They are packed on `stream`, whose memory
     they are: wait for it before products on another one, and before codes and
     scales are overwritten.  Codes and scales are not needed afterwards and may
     be dropped at once.

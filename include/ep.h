@@ -719,8 +719,9 @@ typedef struct {
                                  then N up rows, and y = silu(gate) * up       */
 } ep_i8_t;
 
-/* Bytes of the packed weights (codes and scales of all experts);
- * (size_t)-1 if the description is invalid. */
+/* Bytes of the packed weights (codes and scales of all experts, padded to whole
+ * blocks of 128 rows, or 64 gate and 64 up rows, and 128 input channels: K = 16
+ * takes eight times its codes); (size_t)-1 if the description is invalid. */
 EP_API size_t ep_i8_bytes(const ep_i8_t *w);
 
 /*
