@@ -7,6 +7,13 @@ import torch
 # The raw handle of a device's current stream, without a Stream object around it.
 # (A torch without CUDA has neither: the package can be imported there all the same.)
 _raw_stream, _current_device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+# Whether a tensor may be on another device than the current one, on which the kernels run.
+_SEVERAL = _current_device is not None and torch.cuda.device_count() > 1
+
+
+def _on_current(t: torch.Tensor, name: str) -> None:
+    if _SEVERAL and t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
 
 
 def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "tensor",
@@ -32,6 +39,8 @@ def _rows_ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tupl
     if t.dtype is dtype and t.shape == shape and t.is_cuda:
         ld, step = t.stride()
         if step == 1 or shape[1] <= 1:
+            if _SEVERAL:
+                _on_current(t, name)
             return t.data_ptr() or None, ld if shape[0] > 1 else shape[1]
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -47,6 +56,8 @@ def _shaped_ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape: tu
     if t is None:
         return None
     if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        if _SEVERAL:
+            _on_current(t, name)
         return t.data_ptr() or None
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")

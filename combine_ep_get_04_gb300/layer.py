@@ -32,7 +32,7 @@ from dataclasses import dataclass
 import torch
 
 from ._lib import CAPACITY, I8, PACKED, TYPE_BF16, TYPE_F32, LayerNormDesc, check, load
-from ._tensors import _empty, _int32, _ptr, _rows_ptr, _shaped_ptr, _stream
+from ._tensors import _empty, _int32, _on_current, _ptr, _rows_ptr, _shaped_ptr, _stream
 
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
 _MASK64 = 2 ** 64 - 1
@@ -129,6 +129,7 @@ class LayerNorm:
             for t, wanted, name in ((y, self.block, "y"), (w, self.weight, "w"), (b, self.bias, "b")):
                 if (t is not None) != wanted:
                     raise ValueError(f"{name} is {'missing' if wanted else 'not part of this norm'}")
+        _on_current(self.n, "the norm")
         f32 = torch.float32
         hp, ld_h = _rows_ptr(h, self.dtype, "h", self._shape)
         yp, ld_y = _rows_ptr(y, torch.bfloat16, "y", self._shape)
@@ -151,6 +152,7 @@ class LayerNorm:
             raise ValueError("this norm was made without train=True")
         if (w is None) is self.weight:
             raise ValueError(f"w is {'missing' if self.weight else 'not part of this norm'}")
+        _on_current(self.n, "the norm")
         hp, ld_h = _rows_ptr(h_out, self.dtype, "h_out", self._shape)
         st = self._lib.ep_layer_norm_backward(
             self._ref, hp, ld_h, _shaped_ptr(w, torch.float32, "w", self._row), _shaped_ptr(rng, torch.int64, "rng", _PAIR), self._stats,
@@ -223,7 +225,7 @@ class I8Weights:
         nbytes = lib.ep_i8_bytes(self._ref)
         if nbytes == ctypes.c_size_t(-1).value:
             check(1, "ep_i8_bytes")
-        cp = _ptr(codes, torch.int8, "codes")
+        cp = _shaped_ptr(codes, torch.int8, "codes", (E, rows, K))
         sp = _shaped_ptr(scales, torch.float32, "scales", (E, rows))
         self.packed = _empty(int(nbytes), torch.uint8, codes.device, stream)
         if stream is not None:
@@ -250,6 +252,7 @@ def expert_i8(x: torch.Tensor, x_scales: torch.Tensor, weights: I8Weights, count
         raise ValueError("packed rows need the layout's offsets")
     R = x.shape[0]
     mode, capacity = (PACKED, 0) if capacity is None else (CAPACITY, _int32(capacity, "capacity"))
+    _on_current(w.packed, "weights")
     xp, sp = _shaped_ptr(x, torch.int8, "x", (R, w.K)), _shaped_ptr(x_scales, torch.float32, "x_scales", (R,))
     if counts is None and offsets is None and w.E != 1:
         raise ValueError("several experts need the layout's counts and offsets")
